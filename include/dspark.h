@@ -90,6 +90,13 @@ typedef enum { DSPARK_BF16 = 0, DSPARK_FP32 = 1 } dspark_dtype_t;
 #define DSPARK_ROW_BAD_HISTORY 8   /* history ids outside [0, V) / not strictly ascending,
                                       or a count <= 0 */
 #define DSPARK_ROW_INTERNAL   16   /* an internal limit was hit (bounded wait expired) */
+/* Further bits of the entry points around the epilogue (see each): */
+#define DSPARK_ROW_BAD_BIAS   32   /* bias ids outside [0, V) / not strictly ascending, or a bias
+                                      that is NaN or +inf */
+#define DSPARK_ROW_BAD_MASK   64   /* a mask row outside [-1, n_rows) */
+#define DSPARK_ROW_BAD_TEACHER 128 /* a teacher id outside the target vocabulary or repeated, a
+                                      t2d entry outside [-1, V), a NaN or +inf teacher logit, a
+                                      non-finite teacher log-sum-exp */
 
 /* Largest supported sizes. */
 #define DSPARK_MAX_B          2048
@@ -97,6 +104,8 @@ typedef enum { DSPARK_BF16 = 0, DSPARK_FP32 = 1 } dspark_dtype_t;
 #define DSPARK_MAX_K          64
 #define DSPARK_MAX_TOP_LOGPROBS 20
 #define DSPARK_MAX_SPARSE_M   256  /* (id, probability) pairs per sparse draft row */
+#define DSPARK_MAX_TOP_LOGITS 256  /* entries of a top-logit record (dspark_top_logits, teacher) */
+#define DSPARK_MAX_ROWS  (1 << 24) /* rows of dspark_top_logits and dspark_distill */
 
 /* Sampling parameters of one request (24 bytes, device array of B). */
 typedef struct {
@@ -243,6 +252,161 @@ dspark_status_t dspark_verify_sample_static(const void* logits, const float* q, 
                                             const dspark_counts_t* counts, const dspark_params_t* params,
                                             const float* uniforms, int32_t* out_accept_len, int32_t* out_tokens,
                                             float* out_logprobs, int32_t* out_top_ids, float* out_top_logprobs);
+
+/* ------------------------------------------------------------------------------------------
+ * Around the epilogue: what turns a model's logits into the x of dspark_verify_sample, and what
+ * trains the drafter on the verified rows.  Each entry point is one kernel launch on
+ * params->stream: no workspace, no allocation, no state between calls, safe to capture into a
+ * CUDA graph and to call from several host threads.  Rows are V contiguous logits; consecutive
+ * rows are a stride apart (in elements, at least V), so a row may start at any multiple of the
+ * element size (rows starting on 16-byte boundaries are fastest).  Arithmetic is in fp32 or
+ * wider and rounds to the output's type once.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Logit processing of one request (16 bytes, device array of B). */
+typedef struct {
+    float   repetition_penalty; /* r > 0; 1 = off                                    */
+    float   presence_penalty;   /* p                                                 */
+    float   frequency_penalty;  /* f                                                 */
+    int32_t num_drafts;         /* K_b in [0, K_max]: positions 0..K_b are processed */
+} dspark_process_row_t;
+
+/* Logit biases of each request, CSR over requests (device pointers).  token_ids are strictly
+ * ascending within a request; a bias is finite or -inf (a banned token). */
+typedef struct {
+    const int32_t* row_offsets;   /* [B+1] */
+    const int32_t* token_ids;     /* [nnz] */
+    const float*   biases;        /* [nnz] */
+} dspark_bias_t;
+
+/* Grammar masks: bit t % 32 of word t / 32 of a mask row is 1 when token t is allowed (bits past
+ * V are ignored).  rows[b*(K_max+1) + j] is the mask row of position j of request b, -1 for
+ * a position without a grammar; rows == NULL: position (b, j) has mask row b*(K_max+1) + j. */
+typedef struct {
+    const uint32_t* words;        /* [n_rows, words_stride] */
+    int64_t words_stride;         /* words between mask rows, at least (V + 31) / 32 */
+    int32_t n_rows;
+    const int32_t* rows;          /* [B, K_max+1] or NULL */
+} dspark_mask_t;
+
+typedef struct {
+    int32_t B;                    /* requests, 1..DSPARK_MAX_B           */
+    int32_t K_max;                /* drafted tokens at most, 0..DSPARK_MAX_K */
+    int32_t V;                    /* vocabulary, 1..DSPARK_MAX_V         */
+    dspark_dtype_t logits_dtype;  /* of logits and out                   */
+    int64_t logits_stride;        /* elements between rows (b, j) of logits */
+    int64_t out_stride;           /* ... of out                          */
+    const dspark_process_row_t* rows;   /* device [B]                    */
+    void*    stream;              /* cudaStream_t                        */
+    int32_t* row_status;          /* device [B], required                */
+} dspark_process_params_t;
+
+/*
+ * Repetition, presence and frequency penalties, logit biases and grammar masks on the logits of
+ * every verify position: the x that dspark_verify_sample then takes (give it penalties of 0
+ * there when they were applied here).
+ *   logits, out   [B, K_max+1, V].  out may be logits itself (same pointer, same stride); any
+ *                 other overlap is the caller's error.  In place, logits that no rule changes are
+ *                 neither read nor written.
+ *   draft_ids     [B, K_max] int32, or NULL (no draft prefix)
+ *   history       or NULL.  As in dspark_verify_sample, but a count may be 0: a token of the
+ *                 prompt alone, which the repetition penalty acts on and the others do not.
+ *   bias, mask    or NULL
+ * Position j of request b, j <= K_b, with c the history count of token t plus its occurrences
+ * among d_0..d_{j-1}, and "seen" meaning listed in the history or among those drafts:
+ *   1. seen:   x > 0 ? x / r : x * r
+ *   2. c > 0:  x - ((f*c) + p)
+ *   3. biased: x + bias
+ *   4. not allowed by the mask: -inf (whatever x holds, NaN included).
+ * A mask that allows nothing leaves a row of -inf, which dspark_verify_sample reports as
+ * DSPARK_ROW_NONFINITE.  Positions j > K_b are neither read nor written.  row_status[b] is
+ * written by every call: 0, or DSPARK_ROW_BAD_PARAMS / _BAD_DRAFT / _BAD_HISTORY / _BAD_BIAS /
+ * _BAD_MASK, and then the request's rows of out hold unspecified values.
+ */
+dspark_status_t dspark_process_logits(const void* logits, void* out, const int32_t* draft_ids,
+                                      const dspark_counts_t* history, const dspark_bias_t* bias,
+                                      const dspark_mask_t* mask, const dspark_process_params_t* params);
+
+typedef struct {
+    int32_t n_rows;               /* R, 1..DSPARK_MAX_ROWS               */
+    int32_t V;                    /* 1..DSPARK_MAX_V                     */
+    dspark_dtype_t logits_dtype;
+    int64_t logits_stride;        /* elements between rows               */
+    int32_t n;                    /* 1..DSPARK_MAX_TOP_LOGITS            */
+    float   temperature;          /* T > 0 of the log-sum-exp            */
+    void*   stream;
+    int32_t* row_status;          /* device [R], required                */
+} dspark_top_params_t;
+
+/*
+ * The n largest logits of every row, in order (value descending, id ascending among equals),
+ * and the row's log-sum-exp: the record a drafter is trained on.
+ *   out_values  [R, n] fp32, the logits themselves; -inf past the last one above -inf
+ *   out_ids     [R, n] int32; -1 there
+ *   out_lse     [R] fp32 or NULL: log sum_t exp(x_t / T)
+ * A row holding NaN or +inf, or nothing above -inf, gets DSPARK_ROW_NONFINITE, ids of -1, values
+ * of -inf and a NaN log-sum-exp.
+ */
+dspark_status_t dspark_top_logits(const void* logits, const dspark_top_params_t* params, float* out_values,
+                                  int32_t* out_ids, float* out_lse);
+
+/* A teacher's record of each of R rows, as dspark_top_logits writes it (device pointers). */
+typedef struct {
+    const int32_t* ids;           /* [R, n] target ids, -1: no entry (distinct within a row)   */
+    const float*   logits;        /* [R, n] their logits (ignored where the id is -1)          */
+    const float*   lse;           /* [R] log sum exp(x / T) over the whole target vocabulary,
+                                     or NULL: the record is renormalised to 1                  */
+    int32_t n;                    /* 1..DSPARK_MAX_TOP_LOGITS                                  */
+    const int32_t* t2d;           /* [target_V] draft id of each target id, -1: not in the draft
+                                     vocabulary; or NULL: the vocabularies are the same        */
+    int32_t target_V;             /* length of t2d (ignored when it is NULL)                   */
+} dspark_teacher_t;
+
+typedef struct {
+    int32_t n_rows;               /* R, 1..DSPARK_MAX_ROWS                                     */
+    int32_t V;                    /* the student's (draft) vocabulary, 1..DSPARK_MAX_V         */
+    dspark_dtype_t logits_dtype;  /* of the student's logits and their gradient                */
+    int64_t student_stride;       /* elements between rows                                     */
+    int64_t grad_stride;
+    float   temperature;          /* T > 0, of teacher and student                             */
+    const float* weights;         /* [R] or NULL (all 1); a row of weight 0 is not read        */
+    void*   stream;
+    int32_t* row_status;          /* device [R], required                                      */
+} dspark_distill_params_t;
+
+/*
+ * Divergence of the student's distribution q = softmax(s / T) from a teacher known by its top
+ * logits, for each row.  S is the set of the record's entries with a draft id, z_i their
+ * logits over T:
+ *   lse given:  p_i = exp(z_i - lse), p_r = max(0, 1 - sum p_i): everything outside S is one
+ *               class, which the student gives q_r = sum of q outside S;
+ *   lse NULL:   p = softmax of z over S, p_r = 0.
+ *   L = sum_S p_i log(p_i / q_i) + p_r log(p_r / q_r)   (terms with p = 0, and the last with
+ *       q_r = 0, are 0)
+ *   out_loss[r] = w_r L
+ *   grad[r][v]  = w_r / T * (M q_v - p_v)               v in S, M = sum p_i + p_r
+ *                 w_r / T * q_v (M - p_r / q_r)         v not in S
+ * (multiply the weights by T*T for the usual scale.)  A row of weight 0 or with an empty S has
+ * loss 0 and gradient 0.  Student logits may be -inf.
+ *   out_loss    [R] fp32
+ *   out_saved   [R, 4] fp32 or NULL: what dspark_distill_backward needs (opaque)
+ *   out_grad    [R, V] or NULL: gradient of the sum of out_loss; may be student itself (same
+ *               pointer and stride)
+ * row_status[r]: 0, or DSPARK_ROW_BAD_TEACHER, or DSPARK_ROW_NONFINITE (a student row with NaN or
+ * +inf, or nothing above -inf); such a row has a NaN loss and a gradient of 0.
+ */
+dspark_status_t dspark_distill(const void* student, const dspark_teacher_t* teacher,
+                               const dspark_distill_params_t* params, float* out_loss, float* out_saved,
+                               void* out_grad);
+
+/*
+ * The gradient of sum_r grad_loss[r] * out_loss[r], from the same student, teacher and params and
+ * the out_saved of a dspark_distill call; grad_loss [R] fp32 or NULL (all 1).  row_status is not
+ * written and may be NULL.
+ */
+dspark_status_t dspark_distill_backward(const void* student, const dspark_teacher_t* teacher,
+                                        const dspark_distill_params_t* params, const float* saved,
+                                        const float* grad_loss, void* out_grad);
 
 /* Human-readable name of a status code. */
 const char* dspark_status_string(dspark_status_t status);

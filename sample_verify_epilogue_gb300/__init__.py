@@ -6,9 +6,13 @@ the library is missing: there is no CPU or PyTorch fallback.
 """
 from .build import build, LIB  # noqa: F401
 from .binding import (  # noqa: F401
+    dspark_distill,
+    dspark_distill_backward,
     dspark_host_workspace_bytes,
     dspark_launches_per_call,
+    dspark_process_logits,
     dspark_status_string,
+    dspark_top_logits,
     dspark_verify_sample,
     dspark_verify_sample_host,
     dspark_workspace_bytes,

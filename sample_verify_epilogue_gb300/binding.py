@@ -18,6 +18,7 @@ DSPARK_BF16 = 0
 DSPARK_FP32 = 1
 DSPARK_MAX_TOP_LOGPROBS = 20
 DSPARK_MAX_SPARSE_M = 256
+DSPARK_MAX_TOP_LOGITS = 256
 DSPARK_Q_DENSE, DSPARK_Q_SPARSE, DSPARK_Q_REDUCED = 0, 1, 2
 DSPARK_LOGPROBS_RAW, DSPARK_LOGPROBS_PENALISED = 0, 1
 Q_LAYOUTS = {"dense": DSPARK_Q_DENSE, "sparse": DSPARK_Q_SPARSE, "reduced": DSPARK_Q_REDUCED}
@@ -28,11 +29,20 @@ ROW_BAD_DRAFT = 2
 ROW_NONFINITE = 4
 ROW_BAD_HISTORY = 8
 ROW_INTERNAL = 16
+ROW_BAD_BIAS = 32
+ROW_BAD_MASK = 64
+ROW_BAD_TEACHER = 128
 
 # dspark_row_params_t: float, int32, float, float, float, int32 (24 bytes)
 ROW_PARAMS_DTYPE = np.dtype([
     ("temperature", np.float32), ("top_k", np.int32), ("top_p", np.float32),
     ("presence_penalty", np.float32), ("frequency_penalty", np.float32), ("num_drafts", np.int32),
+])
+
+# dspark_process_row_t: three floats and an int32 (16 bytes)
+PROCESS_ROW_DTYPE = np.dtype([
+    ("repetition_penalty", np.float32), ("presence_penalty", np.float32), ("frequency_penalty", np.float32),
+    ("num_drafts", np.int32),
 ])
 
 
@@ -58,6 +68,46 @@ class dspark_params_t(ctypes.Structure):
     ]
 
 
+class dspark_bias_t(ctypes.Structure):
+    _fields_ = [("row_offsets", ctypes.c_void_p), ("token_ids", ctypes.c_void_p), ("biases", ctypes.c_void_p)]
+
+
+class dspark_mask_t(ctypes.Structure):
+    _fields_ = [("words", ctypes.c_void_p), ("words_stride", ctypes.c_int64), ("n_rows", ctypes.c_int32),
+                ("rows", ctypes.c_void_p)]
+
+
+class dspark_process_params_t(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("K_max", ctypes.c_int32), ("V", ctypes.c_int32), ("logits_dtype", ctypes.c_int32),
+        ("logits_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64), ("rows", ctypes.c_void_p),
+        ("stream", ctypes.c_void_p), ("row_status", ctypes.c_void_p),
+    ]
+
+
+class dspark_top_params_t(ctypes.Structure):
+    _fields_ = [
+        ("n_rows", ctypes.c_int32), ("V", ctypes.c_int32), ("logits_dtype", ctypes.c_int32),
+        ("logits_stride", ctypes.c_int64), ("n", ctypes.c_int32), ("temperature", ctypes.c_float),
+        ("stream", ctypes.c_void_p), ("row_status", ctypes.c_void_p),
+    ]
+
+
+class dspark_teacher_t(ctypes.Structure):
+    _fields_ = [
+        ("ids", ctypes.c_void_p), ("logits", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("n", ctypes.c_int32),
+        ("t2d", ctypes.c_void_p), ("target_V", ctypes.c_int32),
+    ]
+
+
+class dspark_distill_params_t(ctypes.Structure):
+    _fields_ = [
+        ("n_rows", ctypes.c_int32), ("V", ctypes.c_int32), ("logits_dtype", ctypes.c_int32),
+        ("student_stride", ctypes.c_int64), ("grad_stride", ctypes.c_int64), ("temperature", ctypes.c_float),
+        ("weights", ctypes.c_void_p), ("stream", ctypes.c_void_p), ("row_status", ctypes.c_void_p),
+    ]
+
+
 def make_extras(q_layout="dense", q_row_len=0, q_ids=None, d2t=None, eos_ids=None, out_stopped=None,
                 pos_counts=None, logprob_mode="raw"):
     """A dspark_extras_t; array arguments are raw addresses (int) or None."""
@@ -74,7 +124,8 @@ _lib = None
 
 EXPORTS = ("dspark_workspace_bytes", "dspark_verify_sample", "dspark_host_workspace_bytes",
            "dspark_verify_sample_host", "dspark_verify_sample_static", "dspark_status_string",
-           "dspark_launches_per_call")
+           "dspark_launches_per_call", "dspark_process_logits", "dspark_top_logits", "dspark_distill",
+           "dspark_distill_backward")
 
 DSPARK_STATIC_WORKSPACE_BYTES = 16 << 20
 
@@ -112,6 +163,16 @@ def open_library(path: str):
     lib.dspark_status_string.restype = ctypes.c_char_p
     lib.dspark_launches_per_call.argtypes = []
     lib.dspark_launches_per_call.restype = ctypes.c_int32
+    lib.dspark_process_logits.argtypes = [vp, vp, vp, C, ctypes.POINTER(dspark_bias_t), ctypes.POINTER(dspark_mask_t),
+                                          ctypes.POINTER(dspark_process_params_t)]
+    lib.dspark_process_logits.restype = ctypes.c_int
+    lib.dspark_top_logits.argtypes = [vp, ctypes.POINTER(dspark_top_params_t), vp, vp, vp]
+    lib.dspark_top_logits.restype = ctypes.c_int
+    T, D = ctypes.POINTER(dspark_teacher_t), ctypes.POINTER(dspark_distill_params_t)
+    lib.dspark_distill.argtypes = [vp, T, D, vp, vp, vp]
+    lib.dspark_distill.restype = ctypes.c_int
+    lib.dspark_distill_backward.argtypes = [vp, T, D, vp, vp, vp]
+    lib.dspark_distill_backward.restype = ctypes.c_int
     return lib
 
 
@@ -243,3 +304,189 @@ def dspark_verify_sample_host(logits, q, draft_ids, counts, rows, uniforms, *, o
         hp(uniforms), hp(out["accept_len"]), hp(out["tokens"]), hp(out.get("logprobs")),
         hp(out.get("top_ids")), hp(out.get("top_logprobs")))
     _check(code)
+
+
+# ---------------------------------------------------------------- around the epilogue
+def _dtype_of(logits):
+    import torch
+    if logits.dtype == torch.bfloat16:
+        return DSPARK_BF16
+    if logits.dtype == torch.float32:
+        return DSPARK_FP32
+    raise TypeError(f"logits are bfloat16 or float32, not {logits.dtype}")
+
+
+def _rows_of(name, t, shape=None):
+    """(rows, V, stride) of a tensor of logits [..., V]: each row contiguous, the rows evenly spaced."""
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.dim() < 1 or t.numel() == 0:
+        raise ValueError(f"{name} is empty")
+    V = t.shape[-1]
+    if t.stride(-1) != 1 and V > 1:
+        raise ValueError(f"{name}: the logits of a row must be contiguous")
+    rows, stride = 1, V
+    for d in range(t.dim() - 2, -1, -1):
+        if t.shape[d] == 1:
+            continue
+        if rows == 1:
+            stride = t.stride(d)
+        elif t.stride(d) != rows * stride:
+            raise ValueError(f"{name}: the rows must be evenly spaced")
+        rows *= t.shape[d]
+    if stride < V:
+        raise ValueError(f"{name}: rows overlap")
+    return rows, V, stride
+
+
+def _flat(name, t, dtype, numel, device, optional=False):
+    """The address of a contiguous tensor of ``numel`` elements on ``device`` (None: NULL)."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is missing")
+    if t.dtype != dtype or (numel is not None and t.numel() != numel) or not t.is_contiguous() or t.device != device:
+        want = "" if numel is None else f" of {numel} elements"
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor{want} on {device}")
+    return t.data_ptr()
+
+
+def _stream(stream, device):
+    import torch
+    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream
+
+
+def _launch(fn, device, *args):
+    """Call ``fn`` with the tensors' device current."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args))
+
+
+def _need_cuda(t, name):
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def dspark_process_logits(logits, rows, *, out, row_status, draft_ids=None, history=None, bias=None, mask=None,
+                          mask_rows=None, stream=None):
+    """Penalties, biases and grammar masks on the logits of every verify position, on ``stream``
+    (default: torch's current stream).
+
+    logits, out [B, K_max+1, V] bf16/fp32 (``out`` may be ``logits``), rows: uint8 tensor of B packed
+    dspark_process_row_t (PROCESS_ROW_DTYPE), row_status [B] int32, draft_ids [B, K_max] int32,
+    history (offsets [B+1], ids, counts) int32, bias (offsets [B+1] int32, ids int32, values fp32),
+    mask [n, words >= ceil(V/32)] int32 bits of the allowed tokens, mask_rows [B, K_max+1] int32 rows of
+    mask (-1: no grammar) or None (row b*(K_max+1) + j) -- all CUDA tensors.
+    """
+    import torch
+    dev = _need_cuda(logits, "logits")
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B, K_max+1, V]")
+    B, W, V = logits.shape
+    _, _, stride = _rows_of("logits", logits)
+    _, _, out_stride = _rows_of("out", out, logits.shape)
+    if out.dtype != logits.dtype or out.device != dev:
+        raise ValueError("out must have the dtype and device of logits")
+    i32, f32 = torch.int32, torch.float32
+    p = dspark_process_params_t(B, W - 1, V, _dtype_of(logits), stride, out_stride,
+                                _flat("rows", rows, torch.uint8, B * PROCESS_ROW_DTYPE.itemsize, dev),
+                                _stream(stream, dev), _flat("row_status", row_status, i32, B, dev))
+    h = b = m = None
+    if history is not None:
+        nnz = history[1].numel()
+        h = ctypes.byref(dspark_counts_t(_flat("history offsets", history[0], i32, B + 1, dev),
+                                         _flat("history ids", history[1], i32, None, dev),
+                                         _flat("history counts", history[2], i32, nnz, dev)))
+    if bias is not None:
+        nnz = bias[1].numel()
+        b = ctypes.byref(dspark_bias_t(_flat("bias offsets", bias[0], i32, B + 1, dev),
+                                       _flat("bias ids", bias[1], i32, None, dev),
+                                       _flat("bias values", bias[2], f32, nnz, dev)))
+    if mask is not None:
+        if mask.dim() != 2 or mask.dtype != i32 or mask.device != dev or mask.stride(1) != 1:
+            raise ValueError(f"mask must be [n, words] int32 rows on {dev}")
+        m = ctypes.byref(dspark_mask_t(mask.data_ptr(), mask.stride(0) if mask.shape[0] > 1 else mask.shape[1],
+                                       mask.shape[0], _flat("mask_rows", mask_rows, i32, B * W, dev, optional=True)))
+        if mask.shape[1] < (V + 31) // 32:
+            raise ValueError(f"mask rows have {mask.shape[1]} words for {V} tokens")
+    elif mask_rows is not None:
+        raise ValueError("mask_rows without a mask")
+    d = _flat("draft_ids", draft_ids, i32, B * (W - 1), dev, optional=True) if W > 1 else None
+    _launch(load_library().dspark_process_logits, dev, logits.data_ptr(), out.data_ptr(), d, h, b, m, ctypes.byref(p))
+
+
+def dspark_top_logits(logits, *, values, ids, row_status, lse=None, temperature=1.0, stream=None):
+    """The n largest logits of every row and the row's log-sum-exp, on ``stream``.
+
+    logits [..., V] bf16/fp32 of R rows, values fp32 and ids int32 [..., n], lse [...] fp32 or None,
+    row_status [...] int32 -- all CUDA tensors; n is the last size of values.
+    """
+    import torch
+    dev = _need_cuda(logits, "logits")
+    R, V, stride = _rows_of("logits", logits)
+    n = values.shape[-1]
+    p = dspark_top_params_t(R, V, _dtype_of(logits), stride, n, temperature, _stream(stream, dev),
+                            _flat("row_status", row_status, torch.int32, R, dev))
+    _launch(load_library().dspark_top_logits, dev, logits.data_ptr(), ctypes.byref(p),
+            _flat("values", values, torch.float32, R * n, dev), _flat("ids", ids, torch.int32, R * n, dev),
+            _flat("lse", lse, torch.float32, R, dev, optional=True))
+
+
+def _distill_args(student, teacher_ids, teacher_logits, teacher_lse, t2d, weights, temperature, row_status, grad, stream):
+    import torch
+    dev = _need_cuda(student, "student")
+    R, V, stride = _rows_of("student", student)
+    grad_stride = V
+    if grad is not None:
+        _, _, grad_stride = _rows_of("grad", grad, student.shape)
+        if grad.dtype != student.dtype or grad.device != dev:
+            raise ValueError("grad must have the dtype and device of student")
+    i32, f32 = torch.int32, torch.float32
+    n = teacher_ids.shape[-1]
+    t = dspark_teacher_t(_flat("teacher_ids", teacher_ids, i32, R * n, dev),
+                         _flat("teacher_logits", teacher_logits, f32, R * n, dev),
+                         _flat("teacher_lse", teacher_lse, f32, R, dev, optional=True), n,
+                         _flat("t2d", t2d, i32, None, dev, optional=True), 0 if t2d is None else t2d.numel())
+    p = dspark_distill_params_t(R, V, _dtype_of(student), stride, grad_stride, temperature,
+                                _flat("weights", weights, f32, R, dev, optional=True), _stream(stream, dev),
+                                _flat("row_status", row_status, i32, R, dev, optional=True))
+    return dev, R, ctypes.byref(t), ctypes.byref(p), None if grad is None else grad.data_ptr()
+
+
+def dspark_distill(student, teacher_ids, teacher_logits, *, loss, row_status, grad=None, saved=None, teacher_lse=None,
+                   t2d=None, weights=None, temperature=1.0, stream=None):
+    """Divergence of the student's softmax from a teacher's top logits, row by row, on ``stream``; with
+    ``grad``, its gradient in the same launch.
+
+    student [..., V] bf16/fp32 of R rows, teacher_ids int32 and teacher_logits fp32 [..., n] (id -1: no
+    entry), teacher_lse [...] fp32 (the rest of the teacher's mass is one class) or None (the record
+    is renormalised), t2d [target_V] int32 draft id of each target id or None, weights [...] fp32 or
+    None; loss [...] fp32, row_status [...] int32, grad like student (may be student) or None, saved
+    [..., 4] fp32 for dspark_distill_backward or None -- all CUDA tensors.
+    """
+    import torch
+    if row_status is None:
+        raise ValueError("row_status is missing")
+    dev, R, t, p, g = _distill_args(student, teacher_ids, teacher_logits, teacher_lse, t2d, weights, temperature,
+                                    row_status, grad, stream)
+    _launch(load_library().dspark_distill, dev, student.data_ptr(), t, p, _flat("loss", loss, torch.float32, R, dev),
+            _flat("saved", saved, torch.float32, 4 * R, dev, optional=True), g)
+
+
+def dspark_distill_backward(student, teacher_ids, teacher_logits, *, saved, grad, grad_loss=None, teacher_lse=None,
+                            t2d=None, weights=None, temperature=1.0, row_status=None, stream=None):
+    """The gradient of sum(grad_loss * loss) by the student's logits, from the inputs and the ``saved`` of
+    a dspark_distill call; grad_loss [...] fp32 or None (all 1).  ``row_status`` is not written."""
+    import torch
+    if grad is None:
+        raise ValueError("grad is missing")
+    dev, R, t, p, g = _distill_args(student, teacher_ids, teacher_logits, teacher_lse, t2d, weights, temperature,
+                                    row_status, grad, stream)
+    _launch(load_library().dspark_distill_backward, dev, student.data_ptr(), t, p,
+            _flat("saved", saved, torch.float32, 4 * R, dev),
+            _flat("grad_loss", grad_loss, torch.float32, R, dev, optional=True), g)

@@ -1,0 +1,185 @@
+// What the one-launch kernels around the epilogue (logit processing, top-logit records, drafter
+// distillation) share: a vocabulary row seen as 16-byte vectors whatever its alignment, packed
+// maxima, and thread-block clusters that split one row.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "dspark_internal.cuh"
+
+namespace dspark {
+
+constexpr int kRowThreads = 256;                 // threads of a row CTA
+constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kMaxCluster = 8;                   // CTAs that share a row at most (the portable limit)
+constexpr float kLog2E = 1.4426950408889634f;
+constexpr double kLn2 = 0.6931471805599453;
+
+// A row of V logits of SX bytes at p, cut into 16-byte vectors at the address's own 16-byte
+// boundaries: vector k holds the logits k*VE - a0 .. k*VE - a0 + VE - 1, of which the first and
+// last vector may lack some.
+template <int SX>
+struct VocabRow {
+    static constexpr int VE = 16 / SX;           // logits per vector
+    const unsigned char* p;
+    int V, a0, nvec;
+
+    __device__ __forceinline__ VocabRow(const void* base, long long row, long long stride, int V_)
+        : p(static_cast<const unsigned char*>(base) + row * stride * SX), V(V_) {
+        a0 = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / SX);
+        nvec = (a0 + V + VE - 1) / VE;
+    }
+    __device__ __forceinline__ int first(int k) const { return k * VE - a0; }     // logit at lane 0 of vector k
+    __device__ __forceinline__ bool whole(int k) const { return first(k) >= 0 && first(k) + VE <= V; }
+};
+
+// Vectors a row of V logits can have at most, whatever its alignment.
+inline int max_vectors(int V, int sx) { return (V + 16 / sx - 1 + 16 / sx - 1) / (16 / sx); }
+
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_stream(void* p, const uint4& v) {
+    asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1, %2, %3, %4};"
+                 :: "l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4& w, int k) { return k == 0 ? w.x : k == 1 ? w.y : k == 2 ? w.z : w.w; }
+
+template <int SX>
+__device__ __forceinline__ float elem(const uint4& w, int q) {
+    if (SX == 2) {
+        const uint32_t x = word_of(w, q >> 1);
+        return (q & 1) ? bf16_hi(x) : bf16_lo(x);
+    }
+    return __uint_as_float(word_of(w, q));
+}
+
+// Replace lane q (a compile-time constant after unrolling) by the bits of an SX-byte value.
+template <int SX>
+__device__ __forceinline__ void put_bits(uint4& w, int q, uint32_t bits) {
+    const int k = SX == 2 ? q >> 1 : q;
+    uint32_t& x = k == 0 ? w.x : k == 1 ? w.y : k == 2 ? w.z : w.w;
+    if (SX == 2) x = (q & 1) ? ((x & 0x0000FFFFu) | (bits << 16)) : ((x & 0xFFFF0000u) | bits);
+    else x = bits;
+}
+template <int SX>
+__device__ __forceinline__ constexpr uint32_t ninf_bits() { return SX == 2 ? 0xFF80u : 0xFF800000u; }
+// A vector of -inf.
+template <int SX>
+__device__ __forceinline__ uint4 ninf_vec() {
+    constexpr uint32_t w = SX == 2 ? 0xFF80FF80u : 0xFF800000u;
+    return make_uint4(w, w, w, w);
+}
+
+// Round v to the row's type (to nearest even) and return its bits.
+template <int SX>
+__device__ __forceinline__ uint32_t to_bits(float v) {
+    if (SX == 2) return static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(v)));
+    return __float_as_uint(v);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+template <int SX>
+__device__ __forceinline__ float load_logit(const VocabRow<SX>& r, int i) {
+    if (SX == 2) return __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const unsigned short*>(r.p + 2LL * i)) << 16);
+    return *reinterpret_cast<const float*>(r.p + 4LL * i);
+}
+
+// Vector k of the row; the lanes it lacks (and all of a k past the row) read as -inf.
+template <int SX>
+__device__ __forceinline__ uint4 load_vec(const VocabRow<SX>& r, int k, int k_end) {
+    constexpr int VE = VocabRow<SX>::VE;
+    if (k >= k_end) return ninf_vec<SX>();
+    const int i0 = r.first(k);
+    if (r.whole(k)) return ld_stream(r.p + static_cast<long long>(i0) * SX);
+    uint4 w = ninf_vec<SX>();
+#pragma unroll
+    for (int q = 0; q < VE; ++q)
+        if (i0 + q >= 0 && i0 + q < r.V) put_bits<SX>(w, q, to_bits<SX>(load_logit<SX>(r, i0 + q)));
+    return w;
+}
+
+// Maximum of a vector's lanes, NaN lanes left out.
+template <int SX>
+__device__ __forceinline__ float vec_max(const uint4& w) {
+    if (SX == 2) {
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
+        const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(&m);
+        return fmaxf(bf16_lo(x), bf16_hi(x));
+    }
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+}
+
+// ---------------------------------------------------------------- sums of exponentials
+// Sum of 2^((x - m) * c): m the largest x seen (-inf while nothing above -inf was), c = log2(e)/T.
+// The difference comes before the product: near the maximum, where the sum is made, it is
+// exact or nearly so, and logits of the type's lowest value do not overflow.
+struct ExpSum {
+    float m, sum;
+};
+__device__ __forceinline__ float exp_of(float x, float m, float c) { return ex2_approx((x - m) * c); }
+__device__ __forceinline__ float rebase(float from, float to, float c) {   // 0 for an empty sum
+    return from > -INFINITY ? exp_of(from, to, c) : 0.f;
+}
+// NaN sums carry over: a NaN logit leaves m alone and makes its sum NaN, so does +inf.
+__device__ __forceinline__ ExpSum merge(const ExpSum& a, const ExpSum& b, float c) {
+    ExpSum r;
+    r.m = fmaxf(a.m, b.m);
+    r.sum = r.m > -INFINITY ? a.sum * rebase(a.m, r.m, c) + b.sum * rebase(b.m, r.m, c) : a.sum + b.sum;
+    return r;
+}
+
+// ---------------------------------------------------------------- clusters
+__device__ __forceinline__ unsigned cluster_rank() {
+    unsigned r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+// Shared-window address of the same variable in CTA `rank` of the cluster.
+__device__ __forceinline__ unsigned peer_addr(const void* smem, unsigned rank) {
+    unsigned a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(smem)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ uint32_t peer_ld32(unsigned a) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ unsigned long long peer_ld64(unsigned a) {
+    unsigned long long v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// Launch `grid` CTAs in clusters of `cluster` (1: no cluster).
+template <typename... KArgs, typename... Args2>
+inline cudaError_t launch_cluster(void (*kern)(KArgs...), unsigned grid, int cluster, size_t smem, cudaStream_t s,
+                                  Args2&&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kRowThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, std::forward<Args2>(args)...);
+}
+
+}  // namespace dspark
