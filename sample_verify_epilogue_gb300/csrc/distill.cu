@@ -1,33 +1,39 @@
 // distill_kernel: the divergence of a student's softmax from a teacher known by its top logits,
-// its gradient, or both in one launch; each row split over a cluster of CTAs.
+// its gradient, or both in one launch; each row split over a cluster of C CTAs.
 //
-// With e_v = 2^((s_v - m) log2(e)/T), Z = sum e_v, R = sum of e_v outside the record's set S:
-//   L = sum_S p_i (log p_i - s_i/T + m/T + log Z) + p_r log(p_r Z / R)
+// With e_v = exp(s_v / T) up to a factor of the row, Z = sum e_v, R = sum of e_v outside the record's
+// set S:
+//   L = sum_S p_i (log p_i - log e_i + log Z) + p_r log(p_r Z / R)
 //   dL/ds_v = (e_v a - p_v / T) in S, e_v b outside,  a = M / (Z T),  b = (M/Z - p_r/R) / T
-// so the row is needed twice: once for Z and R, once for the gradient.  R is summed without the
-// members of S rather than taken as Z less their sum, which cancels when they carry nearly
-// all mass.  A bit per 16-byte vector says whether the vector holds a member; only those vectors
-// (at most n of a row) look their lanes up in the CTA's part of the record.
+// R is summed without the members of S rather than taken as Z less their sum, which cancels when
+// they carry nearly all mass.
 //
-// Bound by bandwidth: s is read once, the gradient written once.  When both come from one call
-// the second read of a row follows the first at once and finds it in L2: the cluster's size
-// bounds the rows in flight.  Teacher probabilities are made by every CTA of the row, one thread
-// for each of the record's n entries; the sums that meet cancellation (of p, of p_i log p_i/q_i)
-// are held in 64 bits, by one warp: this GPU's 64-bit rate is 1/64 of its 32-bit one.
+// Bound by bandwidth: s is read once and the gradient written once.  A CTA's span of the row
+// comes to shared memory by bulk copies and stays there between the sum and the gradient, so that
+// a call for both does not read the row twice.  While it arrives, one warp makes the teacher's
+// probabilities from the record.  That warp then takes the span's members out: it notes their
+// logits and puts -inf in their place, so that the two loops over the span know nothing of S; the
+// members' gradients are written over afterwards.  (Longer spans go through the buffer in pieces,
+// twice when both results are wanted; the second read is then from L2.)
+//
+// Sums that meet cancellation (of p, of p_i log p_i/e_i) are held in 64 bits, by one warp: this
+// GPU's 64-bit rate is 1/64 of its 32-bit one.
 #include "vocab_rows.cuh"
 
 namespace dspark {
 
 namespace {
 
-constexpr int kDisVec = 4;
-constexpr int kDisBatch = kDisVec * kRowThreads;
-static_assert(DSPARK_MAX_TOP_LOGITS <= kRowThreads, "one record entry per thread");
+constexpr int kDisVec = 4;                                   // vectors a thread holds at a time
+constexpr int kDisSpan = 4608;                               // vectors of a span kept in one piece at most
+constexpr int kDisPiece = 2560;                              // vectors of a piece of a longer one
+constexpr int kDisEntries = DSPARK_MAX_TOP_LOGITS / 32;      // record entries per lane
 
 enum DistillPass : int { kLoss = 1, kGrad = 2 };
 
 struct DisArgs {
-    int V, n, cluster, target_V, words;                      // words: of the per-vector bitmap
+    int V, n, cluster, target_V;
+    int piece;                                               // vectors of the buffer
     float c;                                                 // log2(e) / T
     double inv_t;
     long long s_stride, g_stride;
@@ -46,30 +52,23 @@ struct DisArgs {
 };
 
 struct DisPart {                                             // what a CTA tells its cluster
-    float m, rest, in;                                       // maximum; sums of e relative to it
-    int pad;
-    double cross;                                            // sum over its members of p_i (log p_i - s_i/T)
+    float m, rest, in;                                       // maximum; sums of e outside and inside S, by it
+    int status;
+    double cross;                                            // sum over its members of p_i (log p_i - log e_i)
 };
 
 struct __align__(16) DisSmem {
     DisPart part;
-    alignas(16) int id[DSPARK_MAX_TOP_LOGITS];                     // draft ids of the row's record, -1: none
-    float p[DSPARK_MAX_TOP_LOGITS];                          // its probabilities (renormalised later where wanted)
-    int m_id[DSPARK_MAX_TOP_LOGITS];                         // members inside this CTA's span:
-    float m_p[DSPARK_MAX_TOP_LOGITS];                        //   probability, its logarithm
-    float m_lp[DSPARK_MAX_TOP_LOGITS];
-    int wmem[kRowWarps];
-    float wmax[kRowWarps];
+    uint64_t bar;
+    int id[DSPARK_MAX_TOP_LOGITS];                           // draft ids of the row's record, -1: none
+    float p[DSPARK_MAX_TOP_LOGITS];
+    float lv[DSPARK_MAX_TOP_LOGITS];                         // log p; once taken out, the student's logit
     ExpSum es[kRowWarps];
-    double psum;                                             // sum of p
+    float psum, p_r, mass;                                   // sum of p, 1 - sum, their sum
+    int status, any;
     float m, total, rest;                                    // the row's
+    int row_status;
 };
-
-__device__ __forceinline__ int find_member(const DisSmem& s, int n_mem, int i) {
-    for (int e = 0; e < n_mem; ++e)
-        if (s.m_id[e] == i) return e;
-    return -1;
-}
 
 // log(v), v > 0 normal: the exponent's part in 64 bits, logf of what is left in [0.75, 1.5).
 __device__ __forceinline__ double log_split(float v) {
@@ -77,14 +76,25 @@ __device__ __forceinline__ double log_split(float v) {
     return kLn2 * e + static_cast<double>(logf(__int_as_float(__float_as_int(v) - (e << 23))));
 }
 
+__device__ __forceinline__ unsigned long long dis_timer() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+// Wait for a copy with a 2 s bound; false when it runs out.
+__device__ __forceinline__ bool dis_wait(uint64_t* bar, unsigned parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = dis_timer();
+    while (!mbar_try_wait(bar, parity))
+        if (dis_timer() - t0 > 2000000000ull) return false;
+    return true;
+}
+
 template <int SX>
-__device__ __forceinline__ void store_vec(const VocabRow<SX>& g, int i0, const float (&v)[16 / SX], bool vec) {
+__device__ __forceinline__ void store_vec(const VocabRow<SX>& g, int k, int i0, const uint4& w, bool same_phase) {
     constexpr int VE = 16 / SX;
     unsigned char* p = const_cast<unsigned char*>(g.p);
-    if (vec) {
-        uint4 w;
-        if (SX == 2) w = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4 % VE], v[5 % VE]), pack_bf16(v[6 % VE], v[7 % VE]));
-        else w = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    if (same_phase && i0 >= 0 && i0 + VE <= g.V) {
         st_stream(p + static_cast<long long>(i0) * SX, w);
         return;
     }
@@ -92,17 +102,94 @@ __device__ __forceinline__ void store_vec(const VocabRow<SX>& g, int i0, const f
     for (int q = 0; q < VE; ++q) {
         const int i = i0 + q;
         if (i < 0 || i >= g.V) continue;
-        if (SX == 2) reinterpret_cast<unsigned short*>(p)[i] = static_cast<unsigned short>(to_bits<SX>(v[q]));
-        else reinterpret_cast<float*>(p)[i] = v[q];
+        if (SX == 2) reinterpret_cast<unsigned short*>(p)[i] = static_cast<unsigned short>(word_of(w, q >> 1) >> (16 * (q & 1)));
+        else reinterpret_cast<unsigned*>(p)[i] = word_of(w, q);
+    }
+}
+
+// The teacher's record of a row, by one warp: draft ids, probabilities and their logarithms.
+__device__ __forceinline__ void take_record(const DisArgs& a, DisSmem& s, long long row) {
+    const int lane = threadIdx.x & 31;
+    int id[kDisEntries], status = 0;
+    float t[kDisEntries], tmax = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < kDisEntries; ++q) {
+        const int e = lane + 32 * q;
+        id[q] = e < a.n ? a.ids[row * a.n + e] : -1;
+        t[q] = e < a.n ? a.tl[row * a.n + e] : 0.f;
+    }
+    const float lse = a.lse ? a.lse[row] : 0.f;
+#pragma unroll
+    for (int q = 0; q < kDisEntries; ++q) {
+        if (id[q] < -1 || id[q] >= (a.t2d ? a.target_V : a.V)) { status = DSPARK_ROW_BAD_TEACHER; id[q] = -1; }
+        if (a.t2d && id[q] >= 0) id[q] = a.t2d[id[q]];
+    }
+    bool any = false;
+#pragma unroll
+    for (int q = 0; q < kDisEntries; ++q) {
+        if (id[q] < -1 || id[q] >= a.V || (id[q] >= 0 && !(t[q] < INFINITY))) { status = DSPARK_ROW_BAD_TEACHER; id[q] = -1; }
+        if (id[q] >= 0) {
+            any = true;
+            tmax = fmaxf(tmax, t[q]);
+        }
+    }
+    any = __any_sync(0xffffffffu, any);
+    tmax = warp_max(tmax);
+    if (!isfinite(lse) || (any && !a.lse && !(tmax > -INFINITY))) status = DSPARK_ROW_BAD_TEACHER;
+    // log p: t / T is a product with 1/T in two parts, the first one exact inside the fma
+    const float ih = static_cast<float>(a.inv_t), il = static_cast<float>(a.inv_t - static_cast<double>(ih));
+    float lp[kDisEntries], p[kDisEntries];
+    double sum = 0.0;
+#pragma unroll
+    for (int q = 0; q < kDisEntries; ++q) {
+        lp[q] = -INFINITY;
+        p[q] = 0.f;
+        if (id[q] >= 0 && t[q] > -INFINITY) {
+            lp[q] = a.lse ? fmaf(t[q], il, fmaf(t[q], ih, -lse)) : (t[q] - tmax) * ih;
+            p[q] = expf(lp[q]);
+        }
+        if (32 * q < a.n) sum += p[q];
+    }
+    sum = warp_sum_d(sum);
+    if (!(sum < INFINITY)) status = DSPARK_ROW_BAD_TEACHER;  // a log-sum-exp far below its logits
+    float psum = static_cast<float>(sum), p_r = 0.f, mass = psum;
+    if (a.lse) {
+        if (sum < 1.0) { p_r = static_cast<float>(1.0 - sum); mass = 1.f; }
+    } else if (any) {
+        const float ls = logf(psum), inv = 1.f / psum;
+#pragma unroll
+        for (int q = 0; q < kDisEntries; ++q) {
+            lp[q] -= ls;
+            p[q] *= inv;
+        }
+        psum = mass = 1.f;
+    }
+#pragma unroll
+    for (int q = 0; q < kDisEntries; ++q) {
+        const int e = lane + 32 * q;
+        if (e < a.n) {
+            s.id[e] = id[q];
+            s.p[e] = p[q];
+            s.lv[e] = lp[q];
+        }
+    }
+    status = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(status));
+    if (lane == 0) {
+        s.psum = psum;
+        s.p_r = p_r;
+        s.mass = mass;
+        s.status = status;
+        s.any = any;
     }
 }
 
 template <int SX, int PASS>
-__global__ void __launch_bounds__(kRowThreads) distill_kernel(DisArgs a) {
+__global__ void __launch_bounds__(kRowThreads, 4) distill_kernel(DisArgs a) {
     constexpr int VE = VocabRow<SX>::VE;
     constexpr bool kWantLoss = (PASS & kLoss) != 0, kWantGrad = (PASS & kGrad) != 0;
     __shared__ DisSmem s;
-    extern __shared__ unsigned s_bits[];                     // [words]: bit k - k0 of vector k
+    extern __shared__ uint4 s_x[];                           // [piece] vectors, then a bit for each of their lanes
+    unsigned* const s_bits = reinterpret_cast<unsigned*>(s_x + a.piece);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = a.cluster, rank = static_cast<int>(blockIdx.x % C);
     const long long row = blockIdx.x / C;
@@ -110,15 +197,9 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DisArgs a) {
     const VocabRow<SX> g(a.g, row, a.g_stride, a.V);
     const int k0 = static_cast<int>(static_cast<long long>(x.nvec) * rank / C);
     const int k1 = static_cast<int>(static_cast<long long>(x.nvec) * (rank + 1) / C);
-    const int i_lo = max(0, x.first(k0)), i_hi = min(a.V, x.first(k1));
     const bool same_phase = x.a0 == g.a0;
 
-    // gradient of a row that has none
-    auto zero_grad = [&]() {
-        const float zero[VE] = {};
-        for (int k = k0 + tid; k < k1; k += kRowThreads) store_vec<SX>(g, x.first(k), zero, same_phase && x.whole(k));
-    };
-    // loss and status of a row that is not reduced; the same branch in every CTA of the row
+    // a row that is not reduced: loss, status and gradient; the same branch in every CTA of the row
     auto leave = [&](int status) {
         if (kWantLoss && rank == 0 && tid == 0) {
             a.loss[row] = status ? NAN : 0.f;
@@ -126,172 +207,129 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DisArgs a) {
             if (a.saved_out)
                 for (int k = 0; k < 4; ++k) a.saved_out[4 * row + k] = 0.f;
         }
-        if (kWantGrad) zero_grad();
+        if (kWantGrad)
+            for (int k = k0 + tid; k < k1; k += kRowThreads) store_vec<SX>(g, k, x.first(k), make_uint4(0, 0, 0, 0), same_phase);
     };
-
-    // ---- the teacher's record: draft ids, probabilities, the CTA's members
     const float w = a.weights ? a.weights[row] : 1.f;
-    int id = tid < a.n ? a.ids[row * a.n + tid] : -1;
-    float t = tid < a.n ? a.tl[row * a.n + tid] : 0.f;
     if (w == 0.f) {
         leave(0);
         return;
     }
-    uint4 nxt[kDisVec];
-    if (kWantLoss) {
-#pragma unroll
-        for (int u = 0; u < kDisVec; ++u) nxt[u] = load_vec<SX>(x, k0 + u * kRowThreads + tid, k1);
-    }
-    int bad = id < -1 || id >= (a.t2d ? a.target_V : a.V);
-    if (bad) id = -1;
-    if (a.t2d && id >= 0) {
-        id = a.t2d[id];
-        if (id < -1 || id >= a.V) { bad = 1; id = -1; }
-    }
-    if (id >= 0 && !(t < INFINITY)) { bad = 1; id = -1; }
-    s.id[tid] = id;
-    for (int i = tid; i < a.words; i += kRowThreads) s_bits[i] = 0u;
-    float tmax = id >= 0 ? t : -INFINITY;
-    tmax = warp_max(tmax);
-    if (lane == 0) s.wmax[warp] = tmax;
-    const int any = __syncthreads_or(id >= 0);
-#pragma unroll
-    for (int k = 0; k < kRowWarps; ++k) tmax = fmaxf(tmax, s.wmax[k]);
-    if (id >= 0) {                                           // a repeated id
-        int same = 0;
-        for (int e = 0; e < a.n; e += 4) {
-            const int4 o = *reinterpret_cast<const int4*>(&s.id[e]);
-            same += (o.x == id) + (o.y == id) + (o.z == id) + (o.w == id);
+
+    // vectors [b, e) of the row into the buffer: whole ones by a bulk copy, the row's ragged first
+    // and last by two threads of the warp that takes the members out
+    auto fetch = [&](int b, int e) {
+        const int wb = b + !x.whole(b), we = e - (e > wb && !x.whole(e - 1));
+        if (tid == 0) {
+            const unsigned bytes = we > wb ? 16u * static_cast<unsigned>(we - wb) : 0u;
+            mbar_arrive_expect_tx(&s.bar, bytes);
+            if (bytes) bulk_g2s(s_x + (wb - b), x.p + static_cast<long long>(x.first(wb)) * SX, bytes, &s.bar);
         }
-        bad |= same != 1;
+        if (tid == 1 && wb > b) s_x[0] = load_vec<SX>(x, b, e);
+        if (tid == 2 && we < e && we >= wb) s_x[we - b] = load_vec<SX>(x, we, e);
+    };
+    if (tid == 0) {
+        mbar_init(&s.bar, 1);
+        fence_mbar_init();
     }
-    // log p: the product t / T is exact inside the fma but for the rounding of 1 / T, put back
-    const float ih = static_cast<float>(a.inv_t), il = static_cast<float>(a.inv_t - static_cast<double>(ih));
-    float logp = -INFINITY;
-    if (id >= 0 && t > -INFINITY) {
-        if (a.lse) logp = fmaf(t, il, fmaf(t, ih, -a.lse[row]));
-        else logp = (t - tmax) * ih;
-    }
-    if (a.lse && !isfinite(a.lse[row])) bad = 1;
-    if (!a.lse && any && !(tmax > -INFINITY)) bad = 1;       // nothing above -inf in the record
-    float p = id >= 0 ? expf(logp) : 0.f;
-    if (!(p < INFINITY)) bad = 1;                            // a log-sum-exp far below its logits
-    s.p[tid] = p;
-    bad = __syncthreads_or(bad);
-    if (bad || !any) {
-        leave(bad ? DSPARK_ROW_BAD_TEACHER : 0);
+    int b = k0, e = min(k1, k0 + a.piece);
+    unsigned parity = 0;
+    if (k0 < k1) fetch(b, e);
+    for (int i = tid; i < (a.piece * VE + 31) / 32; i += kRowThreads) s_bits[i] = 0u;
+    if (warp == 0) take_record(a, s, row);
+    __syncthreads();
+    bool late = false;
+    if (!s.any || s.status) {
+        if (k0 < k1) late = !dis_wait(&s.bar, 0);
+        late = __syncthreads_or(late);
+        leave(s.status ? s.status : late ? DSPARK_ROW_INTERNAL : 0);
         return;
     }
-    if (warp == 0) {
-        double ps = 0.0;
-        for (int e = lane; e < a.n; e += 32) ps += s.p[e];
-        ps = warp_sum_d(ps);
-        if (lane == 0) s.psum = ps;
-    }
-    // the members of this span, in the record's order
-    const bool here = id >= i_lo && id < i_hi;
-    const unsigned vote = __ballot_sync(0xffffffffu, here);
-    if (lane == 0) s.wmem[warp] = __popc(vote);
-    if (here) {
-        const int k = (id + x.a0) / VE - k0;
-        atomicOr(&s_bits[k >> 5], 1u << (k & 31));
-    }
-    __syncthreads();
-    int mine = __popc(vote & ((1u << lane) - 1u)), n_mem = 0;
-#pragma unroll
-    for (int k = 0; k < kRowWarps; ++k) {
-        if (k < warp) mine += s.wmem[k];
-        n_mem += s.wmem[k];
-    }
-    // psum, p_r, mass = psum + p_r
-    float psum = static_cast<float>(s.psum), p_r = 0.f, mass = 1.f;
-    if (a.lse) {
-        p_r = s.psum < 1.0 ? static_cast<float>(1.0 - s.psum) : 0.f;
-        mass = s.psum < 1.0 ? 1.f : psum;
-    } else {
-        logp -= logf(psum);
-        p /= psum;
-        psum = 1.f;
-    }
-    if (here) {
-        s.m_id[mine] = id;
-        s.m_p[mine] = p;
-        s.m_lp[mine] = logp;
-    }
-    __syncthreads();
 
-    // ---- Z and R
+    ExpSum es{-INFINITY, 0.f};
+    double cross = 0.0;
+    int status = 0;
+    // the span's pieces for the sum (loss) or, alone, for the members' logits (gradient)
+    const double ln_c = kLn2 * a.c;                          // the sums' own 1/T: c rounds log2(e)/T to fp32
+    auto take_members = [&](int b, int e) {                  // by one warp
+        __syncwarp();
+        const int i_lo = max(0, x.first(b)), i_hi = min(a.V, x.first(e));
+        for (int r = lane; r < a.n; r += 32) {
+            const int id = s.id[r];
+            if (id < i_lo || id >= i_hi) continue;
+            const int at = id - x.first(b);                  // lane of the buffer
+            const unsigned bit = 1u << (at & 31);            // a repeated id (told by the saved sums to a gradient alone)
+            if (kWantLoss && atomicOr(&s_bits[at >> 5], bit) & bit) { status = DSPARK_ROW_BAD_TEACHER; continue; }
+            float v;
+            if (SX == 2) {
+                unsigned short* p = reinterpret_cast<unsigned short*>(s_x) + at;
+                v = __uint_as_float(static_cast<uint32_t>(*p) << 16);
+                *p = static_cast<unsigned short>(ninf_bits<SX>());
+            } else {
+                float* p = reinterpret_cast<float*>(s_x) + at;
+                v = *p;
+                *p = -INFINITY;
+            }
+            const float p = s.p[r];
+            if (p > 0.f) cross += p * (s.lv[r] - v * ln_c);
+            s.lv[r] = v;
+        }
+    };
     if (kWantLoss) {
-        ExpSum es{-INFINITY, 0.f};
-        uint4 cur[kDisVec];
-        for (int b0 = k0; b0 < k1; b0 += kDisBatch) {
+        while (true) {
+            if (k0 < k1) late |= !dis_wait(&s.bar, parity);
+            parity ^= 1;
+            if (warp == 0 && k0 < k1) take_members(b, e);
+            __syncthreads();
+            for (int base = b; base < e; base += kDisVec * kRowThreads) {
+                uint4 v[kDisVec];
+                float bm = -INFINITY;
 #pragma unroll
-            for (int u = 0; u < kDisVec; ++u) cur[u] = nxt[u];
-            if (b0 + kDisBatch < k1) {
-#pragma unroll
-                for (int u = 0; u < kDisVec; ++u) nxt[u] = load_vec<SX>(x, b0 + kDisBatch + u * kRowThreads + tid, k1);
-            }
-            float bm = -INFINITY;
-#pragma unroll
-            for (int u = 0; u < kDisVec; ++u) {
-                const int k = b0 + u * kRowThreads + tid, kb = k - k0;
-                if (k < k1 && ((s_bits[kb >> 5] >> (kb & 31)) & 1u)) {
-                    const int i0 = x.first(k);
-#pragma unroll
-                    for (int q = 0; q < VE; ++q)
-                        if (find_member(s, n_mem, i0 + q) >= 0) put_bits<SX>(cur[u], q, ninf_bits<SX>());
+                for (int u = 0; u < kDisVec; ++u) {
+                    const int k = base + u * kRowThreads + tid;
+                    v[u] = k < e ? s_x[k - b] : ninf_vec<SX>();
+                    bm = fmaxf(bm, vec_max<SX>(v[u]));
                 }
-                bm = fmaxf(bm, vec_max<SX>(cur[u]));
+                add_exps<SX>(es, v, bm, a.c);
             }
-            if (bm > es.m) {
-                es.sum *= rebase(es.m, bm, a.c);
-                es.m = bm;
-            }
-            const float ref = es.m > -INFINITY ? es.m : 0.f;
-#pragma unroll
-            for (int u = 0; u < kDisVec; ++u)
-#pragma unroll
-                for (int q = 0; q < VE; ++q) es.sum += exp_of(elem<SX>(cur[u], q), ref, a.c);
+            if (e >= k1) break;
+            for (int i = tid; i < (a.piece * VE + 31) / 32; i += kRowThreads) s_bits[i] = 0u;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncthreads();
+            b = e;
+            e = min(k1, b + a.piece);
+            fetch(b, e);
         }
         for (int o = 16; o; o >>= 1)
             es = merge(es, ExpSum{__shfl_xor_sync(0xffffffffu, es.m, o), __shfl_xor_sync(0xffffffffu, es.sum, o)}, a.c);
         if (lane == 0) s.es[warp] = es;
-        __syncthreads();
-        if (warp == 0) {                                     // the members, and the CTA's part
+        late = __syncthreads_or(late);
+        if (warp == 0) {                                     // the CTA's part
             es = s.es[lane & (kRowWarps - 1)];
             for (int o = kRowWarps / 2; o; o >>= 1)
                 es = merge(es, ExpSum{__shfl_xor_sync(0xffffffffu, es.m, o), __shfl_xor_sync(0xffffffffu, es.sum, o)}, a.c);
-            float v[DSPARK_MAX_TOP_LOGITS / 32], m = es.m;
-#pragma unroll
-            for (int q = 0; q < DSPARK_MAX_TOP_LOGITS / 32; ++q) {
-                const int e = lane + 32 * q;
-                v[q] = e < n_mem ? load_logit<SX>(x, s.m_id[e]) : -INFINITY;
-                m = fmaxf(m, v[q]);
-            }
+            const int i_lo = max(0, x.first(k0)), i_hi = min(a.V, x.first(k1));
+            float m = es.m;
+            for (int r = lane; r < a.n; r += 32)
+                if (s.id[r] >= i_lo && s.id[r] < i_hi) m = fmaxf(m, s.lv[r]);
             m = warp_max(m);
-            const float ref = m > -INFINITY ? m : 0.f;
+            const ExpRef ref(m > -INFINITY ? m : 0.f, a.c);
             float in = 0.f;
-            double cross = 0.0;
-#pragma unroll
-            for (int q = 0; q < DSPARK_MAX_TOP_LOGITS / 32; ++q) {
-                const int e = lane + 32 * q;
-                if (e >= n_mem) break;
-                in += exp_of(v[q], ref, a.c);                // NaN for NaN and +inf
-                const float pe = s.m_p[e];
-                // the student's exponent as the sums have it: c is log2(e)/T rounded to fp32
-                if (pe > 0.f) cross += pe * (s.m_lp[e] - static_cast<double>(v[q]) * (kLn2 * a.c));
-            }
+            for (int r = lane; r < a.n; r += 32)
+                if (s.id[r] >= i_lo && s.id[r] < i_hi) in += ref.of(s.lv[r]);   // NaN for NaN and +inf
             in = warp_sum(in);
             cross = warp_sum_d(cross);
+            status = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(status));
+            if (late) status |= DSPARK_ROW_INTERNAL;
             if (lane == 0) {
                 s.part.m = m;
                 s.part.rest = m > -INFINITY ? es.sum * rebase(es.m, m, a.c) : es.sum;
                 s.part.in = in;
+                s.part.status = status;
                 s.part.cross = cross;
             }
         }
         if (C > 1) {
-            __syncthreads();
             cluster_arrive();
             cluster_wait();
         }
@@ -304,7 +342,8 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DisArgs a) {
                     o.m = __uint_as_float(peer_ld32(from));
                     o.rest = __uint_as_float(peer_ld32(from + 4));
                     o.in = __uint_as_float(peer_ld32(from + 8));
-                    if (rank == 0) o.cross = __longlong_as_double(static_cast<long long>(peer_ld64(from + 16)));
+                    o.status = static_cast<int>(peer_ld32(from + 12));
+                    o.cross = __longlong_as_double(static_cast<long long>(peer_ld64(from + 16)));
                 }
             } else if (lane == 0) {
                 o = s.part;
@@ -312,65 +351,111 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DisArgs a) {
             const float m = warp_max(o.m);
             const float f = m > -INFINITY ? rebase(o.m, m, a.c) : 1.f;
             const float rest = warp_sum(o.rest * f), total = rest + warp_sum(o.in * f);
-            if (lane == 0) { s.m = m; s.total = total; s.rest = rest; }
+            int st = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(o.status));
+            if (!st && !(total == total && m > -INFINITY)) st = DSPARK_ROW_NONFINITE;
+            if (lane == 0) {
+                s.m = m;
+                s.total = st ? NAN : total;
+                s.rest = rest;
+            }
             if (rank == 0) {
-                const double cross = warp_sum_d(o.cross);
+                const double cr = warp_sum_d(o.cross);
                 if (lane == 0) {
-                    const bool ok = total == total && m > -INFINITY;
-                    double loss = cross + psum * (m * (kLn2 * a.c) + log_split(total));
-                    if (p_r > 0.f && rest > 0.f) loss += p_r * logf(p_r * (total / rest));
-                    a.loss[row] = ok ? static_cast<float>(w * loss) : NAN;
-                    a.row_status[row] = ok ? 0 : DSPARK_ROW_NONFINITE;
+                    double loss = cr + s.psum * (ExpRef(m, a.c).whole ? kLn2 * ExpRef(m, a.c).r : m * ln_c) + s.psum * log_split(total);
+                    if (s.p_r > 0.f && rest > 0.f) loss += s.p_r * logf(s.p_r * (total / rest));
+                    a.loss[row] = st ? NAN : static_cast<float>(w * loss);
+                    a.row_status[row] = st;
                     if (a.saved_out) {
                         a.saved_out[4 * row] = m;
-                        a.saved_out[4 * row + 1] = total;
+                        a.saved_out[4 * row + 1] = st ? NAN : total;
                         a.saved_out[4 * row + 2] = rest;
                         a.saved_out[4 * row + 3] = 0.f;
                     }
                 }
             }
         }
-        if (kWantGrad) __syncthreads();
         if (C > 1) cluster_arrive();                         // waited for at the end: peers have read this CTA's part
     }
 
     // ---- the gradient
     if (kWantGrad) {
+        __syncthreads();
         const float m = kWantLoss ? s.m : a.saved[4 * row], total = kWantLoss ? s.total : a.saved[4 * row + 1];
         const float rest = kWantLoss ? s.rest : a.saved[4 * row + 2];
-        if (total > 0.f && m > -INFINITY) {                  // total is NaN for a row that cannot be normalised
-            const float wt = (a.up ? w * a.up[row] : w) * ih;
-            const float scale_in = wt * (mass / total);
-            // (M R - p_r Z) / (Z R): the two products cancel where the student's tail is nearly right
-            float scale_out = scale_in;
-            if (p_r > 0.f && rest > 0.f) {
-                const float z = p_r * total, ze = fmaf(p_r, total, -z);
-                scale_out = wt * (((fmaf(mass, rest, -z) - ze) / rest) / total);
+        const bool ok = total > 0.f && m > -INFINITY;        // total is NaN for a row that cannot be normalised
+        const float wt = (a.up ? w * a.up[row] : w) * static_cast<float>(a.inv_t);
+        const float scale_in = wt * (s.mass / total);
+        // (M R - p_r Z) / (Z R): the two products cancel where the student's tail is nearly right
+        float scale_out = scale_in;
+        if (s.p_r > 0.f && rest > 0.f) {
+            const float z = s.p_r * total, ze = fmaf(s.p_r, total, -z);
+            scale_out = wt * (((fmaf(s.mass, rest, -z) - ze) / rest) / total);
+        }
+        const ExpRef ref(m, a.c);
+        // with a loss the last piece is in the buffer; the others, if any, come again
+        const bool kept = kWantLoss && e - b == k1 - k0;
+        if (!kept) {
+            if (kWantLoss) {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncthreads();
+                b = k0;
+                e = min(k1, k0 + a.piece);
+                if (k0 < k1) fetch(b, e);
             }
-            for (int b0 = k0; b0 < k1; b0 += kDisBatch) {
-                uint4 v[kDisVec];
-#pragma unroll
-                for (int u = 0; u < kDisVec; ++u) v[u] = load_vec<SX>(x, b0 + u * kRowThreads + tid, k1);
+        }
+        while (true) {
+            if (!kept) {
+                if (k0 < k1) late |= !dis_wait(&s.bar, parity);
+                parity ^= 1;
+                late = __syncthreads_or(late);
+                if (!kWantLoss && warp == 0 && k0 < k1) take_members(b, e);
+                if (!kWantLoss) __syncthreads();
+            }
+            for (int base = b; base < e; base += kDisVec * kRowThreads) {
 #pragma unroll
                 for (int u = 0; u < kDisVec; ++u) {
-                    const int k = b0 + u * kRowThreads + tid, kb = k - k0;
-                    if (k >= k1) break;
-                    const int i0 = x.first(k);
-                    float o[VE];
+                    const int k = base + u * kRowThreads + tid;
+                    if (k >= e) break;
+                    const uint4 v = s_x[k - b];
+                    uint4 o = make_uint4(0, 0, 0, 0);
+                    if (ok && !late) {
+                        float f[VE];
+                        if (ref.whole) {
+                            const unsigned long long c2 = pack2(a.c, a.c), r2 = pack2(-ref.r, -ref.r), s2 = pack2(scale_out, scale_out);
 #pragma unroll
-                    for (int q = 0; q < VE; ++q) o[q] = exp_of(elem<SX>(v[u], q), m, a.c) * scale_out;
-                    if ((s_bits[kb >> 5] >> (kb & 31)) & 1u) {
+                            for (int h = 0; h < VE / 2; ++h) {
+                                float lo, hi;
+                                unpack2(fma2(pair_of<SX>(v, h), c2, r2), lo, hi);
+                                unpack2(mul2(pack2(ex2_approx(lo), ex2_approx(hi)), s2), f[2 * h], f[2 * h + 1]);
+                            }
+                        } else {
 #pragma unroll
-                        for (int q = 0; q < VE; ++q) {
-                            const int e = find_member(s, n_mem, i0 + q);
-                            if (e >= 0) o[q] = fmaf(-s.m_p[e], wt, exp_of(elem<SX>(v[u], q), m, a.c) * scale_in);
+                            for (int q = 0; q < VE; ++q) f[q] = ref.of(elem<SX>(v, q)) * scale_out;
                         }
+                        if (SX == 2) o = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4 % VE], f[5 % VE]), pack_bf16(f[6 % VE], f[7 % VE]));
+                        else o = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
                     }
-                    store_vec<SX>(g, i0, o, same_phase && x.whole(k));
+                    store_vec<SX>(g, k, x.first(k), o, same_phase);
                 }
             }
-        } else {
-            zero_grad();
+            if (kept || e >= k1) break;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncthreads();
+            b = e;
+            e = min(k1, b + a.piece);
+            fetch(b, e);
+        }
+        __syncthreads();                                     // the members' gradients go over the span's
+        if (warp == 0 && ok && !late) {
+            const int i_lo = max(0, x.first(k0)), i_hi = min(a.V, x.first(k1));
+            for (int r = lane; r < a.n; r += 32) {
+                const int id = s.id[r];
+                if (id < i_lo || id >= i_hi) continue;
+                const float v = fmaf(-s.p[r], wt, ref.of(s.lv[r]) * scale_in);
+                unsigned char* p = const_cast<unsigned char*>(g.p);
+                if (SX == 2) reinterpret_cast<unsigned short*>(p)[id] = static_cast<unsigned short>(to_bits<SX>(v));
+                else reinterpret_cast<float*>(p)[id] = v;
+            }
         }
     }
     if (kWantLoss && C > 1) cluster_wait();
@@ -397,17 +482,23 @@ dspark_status_t distill_args(const void* student, const dspark_teacher_t* t, con
     a->g_stride = grad ? p->grad_stride : p->student_stride;
     a->ids = t->ids; a->tl = t->logits; a->lse = t->lse; a->t2d = t->t2d;
     a->weights = p->weights; a->row_status = p->row_status;
-    // CTAs per row: one batch of vectors each at least
+    // CTAs per row: spans of at most 72 KB (three CTAs to an SM), and smaller ones while the rows alone
+    // do not make two CTAs per SM.  2048 rows of 64 KB, loss then gradient: 114 us whole, 139 us in
+    // halves, 227 us in quarters: a CTA's latencies cost more than its share of the row.
     const int nvec = max_vectors(p->V, *sx);
     a->cluster = 1;
-    while (a->cluster < kMaxCluster && nvec >= 2 * a->cluster * kDisBatch) a->cluster *= 2;
-    a->words = (nvec / a->cluster + 1 + 31) / 32;
+    while (a->cluster < kMaxCluster && (nvec > a->cluster * kDisSpan ||
+                                        (nvec >= a->cluster * 512 && static_cast<long long>(p->n_rows) * a->cluster < 304)))
+        a->cluster *= 2;
+    // a longer span comes in pieces of 40 KB
+    a->piece = nvec / a->cluster + 1;
+    if (a->piece > kDisSpan) a->piece = kDisPiece;
     return DSPARK_OK;
 }
 
 template <int SX, int PASS>
 dspark_status_t distill_launch(const DisArgs& a, int rows, void* stream) {
-    const size_t smem = static_cast<size_t>(a.words) * sizeof(unsigned);
+    const size_t smem = static_cast<size_t>(a.piece) * 16 + static_cast<size_t>((a.piece * (16 / SX) + 31) / 32) * 4;
     if (smem > 32 * 1024 &&                                  // beyond what a launch gets unasked
         cudaFuncSetAttribute(distill_kernel<SX, PASS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return DSPARK_ERR_CUDA;

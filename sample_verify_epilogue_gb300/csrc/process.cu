@@ -168,33 +168,53 @@ __global__ void __launch_bounds__(kRowThreads) process_kernel(ProcArgs a) {
         if ((tid & 31) == 0) s_at[warp] = at;
     }
 
-    // the copy under the mask
+    // the copy under the mask, every load before the first store
     const bool same_phase = x.a0 == y.a0;
     unsigned char* const yp = const_cast<unsigned char*>(y.p);
+    constexpr unsigned kAll = (1u << VE) - 1u;
+    unsigned bits[kProcVec];
+    uint4 w[kProcVec];
 #pragma unroll
     for (int u = 0; u < kProcVec; ++u) {
         const int k = k0 + u * kRowThreads + tid;
-        if (k >= k1) break;
-        const int i0 = x.first(k);
-        const unsigned bits = m ? mask_bits<VE>(m, words, i0) : (1u << VE) - 1u;
-        if (a.in_place && bits == (1u << VE) - 1u) continue;
-        const bool whole = x.whole(k);
-        uint4 w = ninf_vec<SX>();
-        if (bits) {
-            w = load_vec<SX>(x, k, k1);
+        bits[u] = m && k < k1 ? mask_bits<VE>(m, words, x.first(k)) : kAll;
+    }
 #pragma unroll
-            for (int q = 0; q < VE; ++q)
-                if (!((bits >> q) & 1u)) put_bits<SX>(w, q, ninf_bits<SX>());
+    for (int u = 0; u < kProcVec; ++u) {
+        const int k = k0 + u * kRowThreads + tid;
+        const bool keep = a.in_place && bits[u] == kAll;
+        w[u] = bits[u] && !keep ? load_vec<SX>(x, k, k1) : ninf_vec<SX>();
+    }
+#pragma unroll
+    for (int u = 0; u < kProcVec; ++u) {
+        const int k = k0 + u * kRowThreads + tid;
+        if (k >= k1 || (a.in_place && bits[u] == kAll)) continue;
+        if (bits[u] != kAll && bits[u]) {
+            if (SX == 2) {
+                // two bits to a word's halves: 0xFFFF where the token is kept
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t& x2 = h == 0 ? w[u].x : h == 1 ? w[u].y : h == 2 ? w[u].z : w[u].w;
+                    const unsigned two = bits[u] >> (2 * h);
+                    const unsigned sel = ((two & 1u) * 0xFFFFu) | ((two & 2u) * 0x7FFF8000u);
+                    x2 = (x2 & sel) | (0xFF80FF80u & ~sel);
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < VE; ++q)
+                    if (!((bits[u] >> q) & 1u)) put_bits<SX>(w[u], q, ninf_bits<SX>());
+            }
         }
-        if (whole && same_phase) {
-            st_stream(yp + static_cast<long long>(i0) * SX, w);
+        const int i0 = x.first(k);
+        if (x.whole(k) && same_phase) {
+            st_stream(yp + static_cast<long long>(i0) * SX, w[u]);
         } else {
 #pragma unroll
             for (int q = 0; q < VE; ++q) {
                 const int i = i0 + q;
                 if (i < 0 || i >= a.V) continue;
-                if (SX == 2) reinterpret_cast<unsigned short*>(yp)[i] = static_cast<unsigned short>(word_of(w, q >> 1) >> (16 * (q & 1)));
-                else reinterpret_cast<unsigned*>(yp)[i] = word_of(w, q);
+                if (SX == 2) reinterpret_cast<unsigned short*>(yp)[i] = static_cast<unsigned short>(word_of(w[u], q >> 1) >> (16 * (q & 1)));
+                else reinterpret_cast<unsigned*>(yp)[i] = word_of(w[u], q);
             }
         }
     }

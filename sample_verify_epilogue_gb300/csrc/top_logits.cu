@@ -1,21 +1,21 @@
 // top_logits_kernel: the n largest logits of every row (value descending, id ascending among
-// equals) and log sum exp(x / T), one launch, each row split over a cluster of CTAs.
+// equals) and log sum exp(x / T), one launch, each row split over a cluster of C CTAs.
 //
-// One pass over the row, bound by bandwidth.  A CTA streams its span in batches of kTopVec
-// 16-byte vectors per thread, the next batch loading while this one is reduced:
-//   - the sum of 2^((x - m) log2(e)/T) per thread, m its running maximum, rescaled at most once
-//     per batch;
-//   - keys (value, id) of the logits that reach a threshold go to shared memory.  The first
-//     threshold is the n-th largest of the 256 threads' maxima over the first batch: n distinct
-//     logits reach it, so every one of the span's n largest does.  A batch whose keys do not
-//     fit is taken again vector by vector, the buffer cut down to its n largest keys whenever the
-//     next vectors might not fit and the threshold set above the n-th: spans are read in id
-//     order, so a later equal logit loses to those kept.  Any input is exact; rows of equal
-//     values take this path.
-// Each CTA cuts its keys to n by a radix selection over (value, id); the cluster's first CTA
-// gathers the CTAs' keys and sums through distributed shared memory, selects and ranks the row's n
-// and writes the record.
-#include "block_utils.cuh"
+// One pass over the row, bound by bandwidth: while a CTA streams its span, each thread keeps the sum
+// of its exponentials and the maxima of the groups of vectors it sees, and nothing else.
+// The row's 512 group maxima then give a threshold: their n-th largest is reached by at least n
+// logits, and by few more (G groups, n of them at or above: about -G ln(1 - n/G) logits, 69 for
+// n = 64), so
+//   1. group maxima go to shared memory; every CTA reads the row's 512 through distributed shared
+//      memory and finds their n-th largest by bisection on the upper 16 bits of its key (one warp);
+//   2. only the threads whose maximum reaches it read their vectors again (L2) and list the
+//      logits that do;
+//   3. every CTA reads the row's whole list and ranks its own entries in it: the rank is the place
+//      in the record.
+// Rows whose list would be too long (equal values, few distinct values, values bunched in one
+// group) take an exact path: bisection on the value over counts of the whole row, from that
+// threshold up to the maximum; then the logits above the n-th value, and in id order as many equal
+// to it as are wanted.
 #include "vocab_rows.cuh"
 
 namespace dspark {
@@ -24,25 +24,18 @@ namespace {
 
 constexpr int kTopVec = 4;
 constexpr int kTopBatch = kTopVec * kRowThreads;             // vectors per batch
-constexpr int kTopCap = 2560;                                // keys a CTA holds
-constexpr int kTopStep = kRowThreads * 8;                    // keys one vector per thread adds at most
-static_assert(kTopCap >= DSPARK_MAX_TOP_LOGITS + kTopStep, "a cut buffer must take one step");
-static_assert(kTopCap >= kMaxCluster * DSPARK_MAX_TOP_LOGITS, "the merge must take every CTA's keys");
-static_assert(DSPARK_MAX_TOP_LOGITS <= kRowThreads, "the first threshold ranks one maximum per thread");
+constexpr int kTopGroups = 512;                              // of a row, whatever its cluster
+constexpr int kTopOwn = 2 * DSPARK_MAX_TOP_LOGITS;           // entries a CTA lists at most
+constexpr int kTopAll = 1024;                                // entries of a row on the short path
+constexpr int kTopBuf = DSPARK_MAX_TOP_LOGITS * (kMaxCluster + 1);   // ... on the exact path: < n above, n equal per CTA
 
-// (order-preserving value key, id reversed): 32 + 24 bits.
-constexpr int kIdBits = 24;
-constexpr unsigned kIdMask = (1u << kIdBits) - 1;
-__device__ __forceinline__ unsigned long long top_key(float v, int id) {
-    return (static_cast<unsigned long long>(fkey(v)) << kIdBits) | (kIdMask - static_cast<unsigned>(id));
-}
-__device__ __forceinline__ float top_key_v(unsigned long long k) { return key_to_f(static_cast<uint32_t>(k >> kIdBits)); }
-__device__ __forceinline__ int top_key_id(unsigned long long k) { return static_cast<int>(kIdMask - (static_cast<unsigned>(k) & kIdMask)); }
+// (order-preserving value key, id reversed), ids below 2^24.
+__device__ __forceinline__ unsigned long long top_key(float v, int id) { return ckey(v, id); }
 
 struct TopArgs {
     int V, n, cluster;
     float c;                                                 // log2(e) / T
-    double inv_t;                                            // 1 / T
+    double inv_t;
     long long stride;
     const void* x;
     float* values;
@@ -52,139 +45,49 @@ struct TopArgs {
 };
 
 struct __align__(16) TopSmem {
-    unsigned long long keys[kTopCap];
-    int hist[256];
-    alignas(16) float tmax[kRowThreads];
+    unsigned long long own[kTopOwn];
+    unsigned long long all[kTopBuf];
+    unsigned short gmax[kTopGroups];                         // this CTA's 512/C group maxima: upper halves of their keys
     ExpSum es[kRowWarps];
     ExpSum part;                                             // this CTA's sum
-    int n;                                                   // keys held (passes kTopCap when a batch overflows)
-    int bcast[2];
-    float th;
-    int wtot[kRowWarps];
+    int n;                                                   // entries listed (passes kTopOwn when they do not fit)
+    int n_all;                                               // -1: the row takes the exact path
+    int cnt;                                                 // exact path: this CTA's count
+    int wcnt[kRowWarps];
+    unsigned th;                                             // threshold key
+    ExpSum row;
 };
 
-// Smallest key of the n largest of keys[0, m), 0 < n <= m: radix selection from the top byte,
-// left as soon as the digit's keys are all wanted.  The value's 32 bits, then the id's 24; a
-// bf16 value's key has its low 16 bits fixed by the sign (all ones below zero): they are not searched.
-template <int SX>
-__device__ unsigned long long select_nth(TopSmem& s, int m, int n) {
-    const int tid = threadIdx.x;
-    unsigned long long prefix = 0, pmask = 0;
-    int want = n;
-    for (int shift = 48; shift >= 0; shift -= 8) {
-        if (SX == 2 && shift == 32) {
-            if (!(prefix >> 55)) prefix |= 0xFFFFull << kIdBits;
-            pmask |= 0xFFFFull << kIdBits;
-        }
-        if (SX == 2 && (shift == 32 || shift == 24)) continue;
-        s.hist[tid] = 0;
+__device__ __forceinline__ float key_floor(unsigned k) {     // value of a key, never -inf
+    return fmaxf(key_to_f(k), -3.402823466e38f);
+}
+
+// Largest k with at least n of the warp's 32*Q keys >= k, on 16-bit keys; 0 when fewer are set.
+template <int Q>
+__device__ unsigned warp_nth_key16(const unsigned (&key)[Q], int n) {
+    unsigned lo = 0;
+    for (int bit = 15; bit >= 0; --bit) {
+        const unsigned mid = lo | (1u << bit);
+        int c = 0;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) c += key[q] >= mid;
+        if (__reduce_add_sync(0xffffffffu, c) >= n) lo = mid;
+    }
+    return lo;
+}
+
+// Barrier of the cluster, or of the block when the row has one CTA.
+__device__ __forceinline__ void row_sync(int C) {
+    if (C > 1) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
         __syncthreads();
-        for (int i = tid; i < m; i += kRowThreads) {
-            const unsigned long long k = s.keys[i];
-            if ((k & pmask) == prefix) atomicAdd(&s.hist[static_cast<unsigned>(k >> shift) & 255u], 1);
-        }
-        __syncthreads();
-        if (tid < 32) {                                      // lane l: digits 255-8l .. 248-8l
-            int c[8], t = 0;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) { c[q] = s.hist[255 - 8 * tid - q]; t += c[q]; }
-            int incl = t;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, incl, o);
-                if (tid >= o) incl += y;
-            }
-            int run = incl - t;
-            if (run < want && incl >= want) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    if (run < want && run + c[q] >= want) {
-                        s.bcast[0] = 255 - 8 * tid - q;
-                        s.bcast[1] = (want - run) | (run + c[q] == want ? 1 << 30 : 0);
-                    }
-                    run += c[q];
-                }
-            }
-        }
-        __syncthreads();
-        prefix |= static_cast<unsigned long long>(s.bcast[0]) << shift;
-        pmask |= 255ull << shift;
-        const int w = s.bcast[1];
-        want = w & ~(1 << 30);
-        if (w >> 30) break;
     }
-    return prefix;
-}
-
-// Keep the n largest of keys[0, m) (m > n) in keys[0, n), in no particular order.
-template <int SX>
-__device__ void cut_to(TopSmem& s, int m, int n) {
-    const int tid = threadIdx.x;
-    __syncthreads();
-    const unsigned long long least = select_nth<SX>(s, m, n);
-    unsigned long long mine[(kTopCap + kRowThreads - 1) / kRowThreads];
-    int cnt = 0;
-#pragma unroll
-    for (int q = 0; q < (kTopCap + kRowThreads - 1) / kRowThreads; ++q) {
-        const int i = q * kRowThreads + tid;
-        mine[q] = i < m ? s.keys[i] : 0ull;
-        if (mine[q] < least) mine[q] = 0ull;                 // no key is 0: fkey of a number is not
-        cnt += mine[q] != 0ull;
-    }
-    int incl = cnt;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if ((tid & 31) >= o) incl += y;
-    }
-    if ((tid & 31) == 31) s.wtot[tid >> 5] = incl;
-    __syncthreads();
-    int at = incl - cnt;
-    for (int w = 0; w < (tid >> 5); ++w) at += s.wtot[w];
-#pragma unroll
-    for (int q = 0; q < (kTopCap + kRowThreads - 1) / kRowThreads; ++q)
-        if (mine[q] != 0ull) s.keys[at++] = mine[q];
-    if (tid == 0) s.n = n;
-    __syncthreads();
-}
-
-// Hand the vector's logits that reach th to the buffer; *cnt counts them.  True when one found
-// the buffer full.
-template <int SX>
-__device__ __forceinline__ bool offer(TopSmem& s, const uint4& w, int i0, float th, int* cnt) {
-    constexpr int VE = VocabRow<SX>::VE;
-    bool full = false;
-#pragma unroll
-    for (int q = 0; q < VE; ++q) {
-        const float v = elem<SX>(w, q);
-        if (v >= th) {
-            const int at = atomicAdd(&s.n, 1);
-            ++*cnt;
-            if (at < kTopCap) s.keys[at] = top_key(v, i0 + q);
-            else full = true;
-        }
-    }
-    return full;
-}
-
-// The least value above the n-th largest key kept (keys[0, n)): what a later logit must reach.
-__device__ float above_least(TopSmem& s, int n) {
-    const int tid = threadIdx.x;
-    unsigned long long k = tid < n ? s.keys[tid] : ~0ull;    // n <= kRowThreads
-    for (int o = 16; o; o >>= 1) {
-        const unsigned long long y = __shfl_xor_sync(0xffffffffu, k, o);
-        k = y < k ? y : k;
-    }
-    unsigned long long* const part = reinterpret_cast<unsigned long long*>(s.tmax);   // tmax is free by now
-    if ((tid & 31) == 0) part[tid >> 5] = k;
-    __syncthreads();
-    for (int w = 0; w < kRowWarps; ++w) k = part[w] < k ? part[w] : k;
-    __syncthreads();
-    return key_to_f(static_cast<uint32_t>(k >> kIdBits) + 1u);
 }
 
 template <int SX>
-__global__ void __launch_bounds__(kRowThreads) top_logits_kernel(TopArgs a) {
+__global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
     constexpr int VE = VocabRow<SX>::VE;
     __shared__ TopSmem s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -195,132 +98,240 @@ __global__ void __launch_bounds__(kRowThreads) top_logits_kernel(TopArgs a) {
     const int k1 = static_cast<int>(static_cast<long long>(x.nvec) * (rank + 1) / C);
     if (tid == 0) s.n = 0;
 
-    uint4 cur[kTopVec], nxt[kTopVec];
-#pragma unroll
-    for (int u = 0; u < kTopVec; ++u) nxt[u] = load_vec<SX>(x, k0 + u * kRowThreads + tid, k1);
-
+    // ---- the stream
     ExpSum es{-INFINITY, 0.f};
-    float th = -INFINITY;
-    for (int base = k0; base < k1; base += kTopBatch) {
+    float g[2] = {-INFINITY, -INFINITY};                     // maxima of the thread's even and odd vectors
+    {
+        uint4 cur[kTopVec], nxt[kTopVec];
 #pragma unroll
-        for (int u = 0; u < kTopVec; ++u) cur[u] = nxt[u];
-        if (base + kTopBatch < k1) {
+        for (int u = 0; u < kTopVec; ++u) nxt[u] = load_vec<SX>(x, k0 + u * kRowThreads + tid, k1);
+        for (int base = k0; base < k1; base += kTopBatch) {
 #pragma unroll
-            for (int u = 0; u < kTopVec; ++u) nxt[u] = load_vec<SX>(x, base + kTopBatch + u * kRowThreads + tid, k1);
-        }
-        float vm[kTopVec], bm = -INFINITY;
+            for (int u = 0; u < kTopVec; ++u) cur[u] = nxt[u];
+            if (base + kTopBatch < k1) {
 #pragma unroll
-        for (int u = 0; u < kTopVec; ++u) {
-            vm[u] = vec_max<SX>(cur[u]);
-            bm = fmaxf(bm, vm[u]);
-        }
-        if (base == k0) {
-            // the n-th largest thread maximum, ties counted by thread order
-            s.tmax[tid] = bm;
-            __syncthreads();
-            int above = 0;
-            for (int i = 0; i < kRowThreads; i += 4) {
-                const float4 o = *reinterpret_cast<const float4*>(&s.tmax[i]);
-                above += (o.x > bm || (o.x == bm && i < tid)) + (o.y > bm || (o.y == bm && i + 1 < tid)) +
-                         (o.z > bm || (o.z == bm && i + 2 < tid)) + (o.w > bm || (o.w == bm && i + 3 < tid));
+                for (int u = 0; u < kTopVec; ++u) nxt[u] = load_vec<SX>(x, base + kTopBatch + u * kRowThreads + tid, k1);
             }
-            if (above == a.n - 1) s.th = bm;
-            __syncthreads();
-            th = fmaxf(s.th, -3.402823466e38f);              // -inf logits have no place in the record
-        }
-        if (bm > es.m) {
-            es.sum *= rebase(es.m, bm, a.c);
-            es.m = bm;
-        }
-        const float m = es.m > -INFINITY ? es.m : 0.f;
+            float bm[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int u = 0; u < kTopVec; ++u)
-#pragma unroll
-            for (int q = 0; q < VE; ++q) es.sum += exp_of(elem<SX>(cur[u], q), m, a.c);
-        int mine = 0;
-        bool full = false;
-#pragma unroll
-        for (int u = 0; u < kTopVec; ++u)
-            if (vm[u] >= th) full |= offer<SX>(s, cur[u], x.first(base + u * kRowThreads + tid), th, &mine);
-        if (__syncthreads_or(full)) {                        // take the batch back, then again in steps
-            if (mine) atomicSub(&s.n, mine);
-            __syncthreads();
-            int held = s.n;
-            __syncthreads();
-            for (int u = 0; u < kTopVec; ++u) {
-                if (held + kTopStep > kTopCap) {             // then more than n are held
-                    cut_to<SX>(s, held, a.n);
-                    th = above_least(s, a.n);
-                }
-                uint4 w = cur[0];
-#pragma unroll
-                for (int t = 1; t < kTopVec; ++t) if (u == t) w = cur[t];
-                if (vec_max<SX>(w) >= th) offer<SX>(s, w, x.first(base + u * kRowThreads + tid), th, &mine);
-                __syncthreads();
-                held = s.n;
-                __syncthreads();
-            }
+            for (int u = 0; u < kTopVec; ++u) bm[u & 1] = fmaxf(bm[u & 1], vec_max<SX>(cur[u]));
+            add_exps<SX>(es, cur, fmaxf(bm[0], bm[1]), a.c);
+            g[0] = fmaxf(g[0], bm[0]);
+            g[1] = fmaxf(g[1], bm[1]);
         }
     }
-    __syncthreads();
-    int held = s.n;
-    __syncthreads();
-    if (held > a.n) { cut_to<SX>(s, held, a.n); held = a.n; }
+    const float tmax = fmaxf(g[0], g[1]);
 
-    // the block's sum of exponentials, warps in order
-    for (int o = 16; o; o >>= 1) {
-        const ExpSum other{__shfl_xor_sync(0xffffffffu, es.m, o), __shfl_xor_sync(0xffffffffu, es.sum, o)};
-        es = merge(es, other, a.c);
-    }
-    if (lane == 0) s.es[warp] = es;
-    __syncthreads();
-    if (tid == 0) {
-        for (int w = 1; w < kRowWarps; ++w) es = merge(es, s.es[w], a.c);
-        s.part = es;
-    }
-    if (C > 1) {
+    // ---- group maxima: 512/C of this CTA; a group is a thread's half, a thread, or 2 or 4 threads
+    {
+        float gm = tmax;
+        if (C == 1) {
+            s.gmax[tid] = static_cast<unsigned short>(fkey(g[0]) >> 16);
+            s.gmax[tid + kRowThreads] = static_cast<unsigned short>(fkey(g[1]) >> 16);
+        } else {
+            if (C >= 4) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 1));
+            if (C >= 8) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 2));
+            const int per = C / 2;                           // threads of a group
+            if (tid % per == 0) s.gmax[tid / per] = static_cast<unsigned short>(fkey(gm) >> 16);
+        }
+        for (int o = 16; o; o >>= 1)
+            es = merge(es, ExpSum{__shfl_xor_sync(0xffffffffu, es.m, o), __shfl_xor_sync(0xffffffffu, es.sum, o)}, a.c);
+        if (lane == 0) s.es[warp] = es;
         __syncthreads();
-        cluster_arrive();
-        cluster_wait();
+        if (warp == 0) {
+            es = s.es[lane & (kRowWarps - 1)];
+            for (int o = kRowWarps / 2; o; o >>= 1)
+                es = merge(es, ExpSum{__shfl_xor_sync(0xffffffffu, es.m, o), __shfl_xor_sync(0xffffffffu, es.sum, o)}, a.c);
+            if (lane == 0) s.part = es;
+        }
+    }
+    row_sync(C);
+
+    // ---- threshold, and the row's sum
+    if (warp == 0) {
+        unsigned key[kTopGroups / 32];
+        if (C > 1) {
+            // two 16-bit maxima per word; CTA p has 256/C words
+            const int per = kTopGroups / 2 / C;
+#pragma unroll
+            for (int q = 0; q < kTopGroups / 64; ++q) {
+                const int w = q * 32 + lane;
+                const unsigned v = peer_ld32(peer_addr(reinterpret_cast<const unsigned*>(s.gmax) + w % per, w / per));
+                key[2 * q] = v & 0xFFFFu;
+                key[2 * q + 1] = v >> 16;
+            }
+            es = ExpSum{-INFINITY, 0.f};
+            if (lane < C) {
+                const unsigned from = peer_addr(&s.part, lane);
+                es = ExpSum{__uint_as_float(peer_ld32(from)), __uint_as_float(peer_ld32(from + 4))};
+            }
+            for (int o = kMaxCluster / 2; o; o >>= 1)
+                es = merge(es, ExpSum{__shfl_xor_sync(0xffffffffu, es.m, o), __shfl_xor_sync(0xffffffffu, es.sum, o)}, a.c);
+        } else {
+#pragma unroll
+            for (int q = 0; q < kTopGroups / 32; ++q) key[q] = s.gmax[q * 32 + lane];
+        }
+        const unsigned th = warp_nth_key16(key, a.n) << 16;
+        if (lane == 0) {
+            s.th = th;
+            s.row = es;
+        }
+    }
+    __syncthreads();
+    es = s.row;
+    // a row with NaN or +inf has a NaN sum, one with nothing above -inf a maximum of -inf
+    const bool ok = es.sum == es.sum && es.m > -INFINITY;
+
+    // ---- list the logits that reach the threshold: flagged threads' vectors, a warp to a thread
+    const float th = key_floor(s.th);
+    if (ok) {
+        unsigned flagged = __ballot_sync(0xffffffffu, tmax >= th);
+        while (flagged) {
+            const int t = warp * 32 + __ffs(flagged) - 1;
+            flagged &= flagged - 1;
+            for (int k = k0 + t + lane * kRowThreads; k < k1; k += 32 * kRowThreads) {
+                const uint4 w = load_vec<SX>(x, k, k1);
+                if (!(vec_max<SX>(w) >= th)) continue;
+#pragma unroll
+                for (int q = 0; q < VE; ++q) {
+                    const float v = elem<SX>(w, q);
+                    if (v >= th) {
+                        const int at = atomicAdd(&s.n, 1);
+                        if (at < kTopOwn) s.own[at] = top_key(v, x.first(k) + q);
+                    }
+                }
+            }
+            if (*reinterpret_cast<volatile int*>(&s.n) > kTopOwn) break;   // the exact path counts anew
+        }
+    }
+    row_sync(C);
+
+    // ---- the row's list
+    const long long out = row * a.n;
+    int total = 0, before = 0, mine = 0;
+    auto gather = [&](int cap) {                             // false: a CTA's entries or all of them are too many
+        const int np = C > 1 ? (lane < C ? static_cast<int>(peer_ld32(peer_addr(&s.n, lane))) : 0) : (lane == 0 ? s.n : 0);
+        int incl = np;
+#pragma unroll
+        for (int o = 1; o < kMaxCluster; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        total = __shfl_sync(0xffffffffu, incl, kMaxCluster - 1);
+        mine = __shfl_sync(0xffffffffu, np, rank);
+        before = __shfl_sync(0xffffffffu, incl, rank) - mine;
+        if (__any_sync(0xffffffffu, np > kTopOwn) || total > cap) return false;
+        for (int i0 = warp * 32; i0 < total; i0 += kRowThreads) {
+            const int i = i0 + lane;
+            int p = 0, start = 0;                            // entry i is number i - start of CTA p
+#pragma unroll
+            for (int t = 0; t < kMaxCluster - 1; ++t) {
+                const int end = __shfl_sync(0xffffffffu, incl, t);
+                if (i >= end) { p = t + 1; start = end; }
+            }
+            if (i < total) s.all[i] = C > 1 ? peer_ld64(peer_addr(&s.own[i - start], p)) : s.own[i];
+        }
+        return true;
+    };
+    if (ok && !gather(kTopAll)) {
+        // exact path (the same for every CTA of the row): v, the n-th largest value, is the largest
+        // with at least n logits at or above it
+        row_sync(C);                                         // the counts have been read
+        unsigned lo = fkey(th), hi = fkey(es.m);
+        while (lo < hi) {
+            const unsigned mid = lo + ((hi - lo) >> 1) + 1;
+            const float v = key_to_f(mid);
+            int c = 0;
+            for (int k = k0 + tid; k < k1; k += kRowThreads) {
+                const uint4 w = load_vec<SX>(x, k, k1);
+#pragma unroll
+                for (int q = 0; q < VE; ++q) c += elem<SX>(w, q) >= v;
+            }
+            c = __reduce_add_sync(0xffffffffu, c);
+            if (lane == 0) s.wcnt[warp] = c;
+            __syncthreads();
+            if (tid == 0) {
+                int t = 0;
+                for (int w = 0; w < kRowWarps; ++w) t += s.wcnt[w];
+                s.cnt = t;
+            }
+            __syncthreads();
+            row_sync(C);
+            int all = 0;
+            for (int p = 0; p < C; ++p) all += C > 1 ? static_cast<int>(peer_ld32(peer_addr(&s.cnt, p))) : s.cnt;
+            row_sync(C);
+            if (all >= a.n) lo = mid; else hi = mid - 1;
+        }
+        const float v = key_to_f(lo);
+        if (tid == 0) s.n = 0;
+        __syncthreads();
+        // above v: fewer than n in the row.  Equal: the span's first n in id order
+        for (int k = k0 + tid; k < k1; k += kRowThreads) {
+            const uint4 w = load_vec<SX>(x, k, k1);
+#pragma unroll
+            for (int q = 0; q < VE; ++q) {
+                const float e = elem<SX>(w, q);
+                if (e > v) s.own[atomicAdd(&s.n, 1)] = top_key(e, x.first(k) + q);
+            }
+        }
+        __syncthreads();
+        const int above = s.n;
+        int equal = 0;
+        for (int base = k0; base < k1 && equal < a.n; base += kRowThreads) {
+            const int k = base + tid;
+            const uint4 w = load_vec<SX>(x, k, k1);
+            int c = 0;
+#pragma unroll
+            for (int q = 0; q < VE; ++q) c += elem<SX>(w, q) == v;
+            int incl = c;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            if (lane == 31) s.wcnt[warp] = incl;
+            __syncthreads();
+            int at = equal + incl - c;
+            for (int p = 0; p < kRowWarps; ++p) {
+                if (p < warp) at += s.wcnt[p];
+                equal += s.wcnt[p];
+            }
+#pragma unroll
+            for (int q = 0; q < VE; ++q)
+                if (elem<SX>(w, q) == v) {
+                    if (at < a.n) s.own[above + at] = top_key(v, x.first(k) + q);
+                    ++at;
+                }
+            __syncthreads();
+        }
+        if (tid == 0) s.n = above + min(equal, a.n);
+        __syncthreads();
+        row_sync(C);
+        gather(kTopBuf);
+    }
+    __syncthreads();
+
+    // ---- places: an entry's rank in the row's list, a warp to an entry
+    if (ok) {
+        for (int i = warp; i < mine; i += kRowWarps) {
+            const unsigned long long k = s.all[before + i];
+            int at = 0;
+            for (int e = lane; e < total; e += 32) at += s.all[e] > k;
+            at = __reduce_add_sync(0xffffffffu, at);
+            if (lane == 0 && at < a.n) {
+                a.values[out + at] = ckey_v(k);
+                a.ids[out + at] = ckey_id(k);
+            }
+        }
     }
     if (rank == 0) {
-        int total = held;
-        if (C > 1) {
-            for (int p = 1; p < C; ++p) {
-                const int np = static_cast<int>(peer_ld32(peer_addr(&s.n, p)));
-                const unsigned from = peer_addr(s.keys, p);
-                for (int i = tid; i < np; i += kRowThreads) s.keys[total + i] = peer_ld64(from + 8u * i);
-                total += np;
-            }
-            if (tid == 0)
-                for (int p = 1; p < C; ++p) {
-                    const unsigned from = peer_addr(&s.part, p);
-                    es = merge(es, ExpSum{__uint_as_float(peer_ld32(from)), __uint_as_float(peer_ld32(from + 4))}, a.c);
-                }
-            __syncthreads();
-            if (total > a.n) { cut_to<SX>(s, total, a.n); total = a.n; }
+        for (int i = (ok ? total : 0) + tid; i < a.n; i += kRowThreads) {
+            a.values[out + i] = -INFINITY;
+            a.ids[out + i] = -1;
         }
-        if (tid == 0) s.part = es;
-        __syncthreads();
-        es = s.part;
-        // a row with NaN or +inf has a NaN sum, one with nothing above -inf a maximum of -inf
-        const bool ok = es.sum == es.sum && es.m > -INFINITY;
         if (tid == 0) {
             a.row_status[row] = ok ? 0 : DSPARK_ROW_NONFINITE;
-            if (a.lse) a.lse[row] = ok ? static_cast<float>(es.m * a.inv_t + log(static_cast<double>(es.sum))) : NAN;
-        }
-        if (tid < a.n) {                                     // n <= kRowThreads: rank one key per thread
-            const long long o = row * a.n;
-            if (ok && tid < total) {
-                const unsigned long long k = s.keys[tid];
-                int at = 0;
-                for (int i = 0; i < total; ++i) at += s.keys[i] > k;
-                a.values[o + at] = top_key_v(k);
-                a.ids[o + at] = top_key_id(k);
-            } else {
-                a.values[o + tid] = -INFINITY;
-                a.ids[o + tid] = -1;
-            }
+            if (a.lse)
+                a.lse[row] = ok ? static_cast<float>(ExpRef(es.m, a.c).log_unit(a.inv_t) + log(static_cast<double>(es.sum))) : NAN;
         }
     }
     if (C > 1) {                                             // peers' shared memory is read until here
@@ -348,9 +359,15 @@ extern "C" dspark_status_t dspark_top_logits(const void* logits, const dspark_to
     TopArgs a{};
     a.V = p->V; a.n = p->n; a.c = c; a.inv_t = 1.0 / p->temperature; a.stride = p->logits_stride;
     a.x = logits; a.values = out_values; a.ids = out_ids; a.lse = out_lse; a.row_status = p->row_status;
-    // CTAs per row: one batch of vectors each at least
+    // CTAs per row: spans of at most 256 KB, and smaller ones, down to a batch of vectors, while the
+    // rows alone do not make two CTAs per SM.  A CTA's part after the stream costs about as much as
+    // streaming 128 KB: 576 rows of 512 KB take 91 us in halves and 132 us in eighths, 9 rows of
+    // 304 KB 24 us whole and 12 us in eighths.
+    const int nvec = max_vectors(p->V, sx);
     a.cluster = 1;
-    while (a.cluster < kMaxCluster && max_vectors(p->V, sx) >= 2 * a.cluster * kTopBatch) a.cluster *= 2;
+    while (a.cluster < kMaxCluster && (nvec > a.cluster * 16384 ||
+                                       (nvec >= 2 * a.cluster * kTopBatch && static_cast<long long>(p->n_rows) * a.cluster < 304)))
+        a.cluster *= 2;
     const unsigned grid = static_cast<unsigned>(p->n_rows) * static_cast<unsigned>(a.cluster);
     cudaStream_t s = static_cast<cudaStream_t>(p->stream);
     const cudaError_t e = sx == 2 ? launch_cluster(top_logits_kernel<2>, grid, a.cluster, 0, s, a)

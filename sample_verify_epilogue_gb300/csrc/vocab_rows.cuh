@@ -118,16 +118,60 @@ __device__ __forceinline__ float vec_max(const uint4& w) {
     return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
 }
 
+// ---------------------------------------------------------------- packed fp32 pairs
+__device__ __forceinline__ unsigned long long pack2(float lo, float hi) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(unsigned long long v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// Pair k (a compile-time constant after unrolling) of a vector, as fp32.
+template <int SX>
+__device__ __forceinline__ unsigned long long pair_of(const uint4& w, int k) {
+    return pack2(elem<SX>(w, 2 * k), elem<SX>(w, 2 * k + 1));
+}
+
 // ---------------------------------------------------------------- sums of exponentials
-// Sum of 2^((x - m) * c): m the largest x seen (-inf while nothing above -inf was), c = log2(e)/T.
-// The difference comes before the product: near the maximum, where the sum is made, it is
-// exact or nearly so, and logits of the type's lowest value do not overflow.
+// exp(x / T) relative to a row's or thread's maximum m, as 2^(x c - r) with c = log2(e)/T: r is m c
+// rounded up to a whole number, so that the one fma rounds nothing but its result and sums of
+// different maxima join by powers of two.  Where m c has no such whole number (the type's lowest
+// values, infinities) the form is 2^((x - m) c).
+struct ExpRef {
+    float m, c, r;
+    bool whole;
+    __device__ __forceinline__ ExpRef(float m_, float c_) : m(m_), c(c_), r(ceilf(m_ * c_)), whole(fabsf(m_ * c_) < 4194304.f) {}
+    __device__ __forceinline__ float of(float x) const {     // m > -inf
+        return ex2_approx(whole ? fmaf(x, c, -r) : (x - m) * c);
+    }
+    // natural logarithm of what 2^0 stands for
+    __device__ __forceinline__ double log_unit(double inv_t) const { return whole ? kLn2 * r : m * inv_t; }
+};
+
+// A sum of them: m is the largest x seen (-inf while nothing above -inf was).
 struct ExpSum {
     float m, sum;
 };
-__device__ __forceinline__ float exp_of(float x, float m, float c) { return ex2_approx((x - m) * c); }
 __device__ __forceinline__ float rebase(float from, float to, float c) {   // 0 for an empty sum
-    return from > -INFINITY ? exp_of(from, to, c) : 0.f;
+    if (!(from > -INFINITY)) return 0.f;
+    const ExpRef a(from, c), b(to, c);
+    return ex2_approx(a.whole && b.whole ? a.r - b.r : (from - to) * c);
 }
 // NaN sums carry over: a NaN logit leaves m alone and makes its sum NaN, so does +inf.
 __device__ __forceinline__ ExpSum merge(const ExpSum& a, const ExpSum& b, float c) {
@@ -135,6 +179,37 @@ __device__ __forceinline__ ExpSum merge(const ExpSum& a, const ExpSum& b, float 
     r.m = fmaxf(a.m, b.m);
     r.sum = r.m > -INFINITY ? a.sum * rebase(a.m, r.m, c) + b.sum * rebase(b.m, r.m, c) : a.sum + b.sum;
     return r;
+}
+// Add the exponentials of U vectors whose maximum is bm.
+template <int SX, int U>
+__device__ __forceinline__ void add_exps(ExpSum& es, const uint4 (&v)[U], float bm, float c) {
+    constexpr int VE = 16 / SX;
+    if (bm > es.m) {
+        es.sum *= rebase(es.m, bm, c);
+        es.m = bm;
+    }
+    const ExpRef ref(es.m, c);
+    if (ref.whole) {
+        const unsigned long long c2 = pack2(c, c), r2 = pack2(-ref.r, -ref.r);
+        unsigned long long acc[2] = {0ull, 0ull};
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int k = 0; k < VE / 2; ++k) {
+                float lo, hi;
+                unpack2(fma2(pair_of<SX>(v[u], k), c2, r2), lo, hi);
+                acc[k & 1] = add2(acc[k & 1], pack2(ex2_approx(lo), ex2_approx(hi)));
+            }
+        float lo, hi;
+        unpack2(add2(acc[0], acc[1]), lo, hi);
+        es.sum += lo + hi;
+    } else {
+        const float m = es.m > -INFINITY ? es.m : 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int q = 0; q < VE; ++q) es.sum += ex2_approx((elem<SX>(v[u], q) - m) * c);
+    }
 }
 
 // ---------------------------------------------------------------- clusters
