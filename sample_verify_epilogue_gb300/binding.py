@@ -307,69 +307,72 @@ def dspark_verify_sample_host(logits, q, draft_ids, counts, rows, uniforms, *, o
 
 
 # ---------------------------------------------------------------- around the epilogue
+# These calls are a few microseconds of GPU work on small batches, so their checks are kept to
+# one cheap comparison per property; device indices stand for devices.
 def _dtype_of(logits):
     import torch
-    if logits.dtype == torch.bfloat16:
+    if logits.dtype is torch.bfloat16:
         return DSPARK_BF16
-    if logits.dtype == torch.float32:
+    if logits.dtype is torch.float32:
         return DSPARK_FP32
     raise TypeError(f"logits are bfloat16 or float32, not {logits.dtype}")
 
 
-def _rows_of(name, t, shape=None):
+def _rows_of(name, t, like=None):
     """(rows, V, stride) of a tensor of logits [..., V]: each row contiguous, the rows evenly spaced."""
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    shape = t.shape
+    if like is not None and (shape != like.shape or t.dtype is not like.dtype or t.get_device() != like.get_device()):
+        raise ValueError(f"{name} must have the shape, dtype and device of the logits")
     if t.dim() < 1 or t.numel() == 0:
         raise ValueError(f"{name} is empty")
-    V = t.shape[-1]
+    V = shape[-1]
+    if t.is_contiguous():
+        return t.numel() // V, V, V
     if t.stride(-1) != 1 and V > 1:
         raise ValueError(f"{name}: the logits of a row must be contiguous")
     rows, stride = 1, V
     for d in range(t.dim() - 2, -1, -1):
-        if t.shape[d] == 1:
+        if shape[d] == 1:
             continue
         if rows == 1:
             stride = t.stride(d)
         elif t.stride(d) != rows * stride:
             raise ValueError(f"{name}: the rows must be evenly spaced")
-        rows *= t.shape[d]
+        rows *= shape[d]
     if stride < V:
         raise ValueError(f"{name}: rows overlap")
     return rows, V, stride
 
 
-def _flat(name, t, dtype, numel, device, optional=False):
-    """The address of a contiguous tensor of ``numel`` elements on ``device`` (None: NULL)."""
-    if t is None:
-        if optional:
-            return None
-        raise ValueError(f"{name} is missing")
-    if t.dtype != dtype or (numel is not None and t.numel() != numel) or not t.is_contiguous() or t.device != device:
-        want = "" if numel is None else f" of {numel} elements"
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor{want} on {device}")
+def _flat(name, t, dtype, numel, dev):
+    """The address of a contiguous tensor of ``numel`` elements on device ``dev``."""
+    if t is None or t.dtype is not dtype or t.numel() != numel or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {numel} elements on the logits' device")
     return t.data_ptr()
 
 
-def _stream(stream, device):
-    import torch
-    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream
-
-
-def _launch(fn, device, *args):
-    """Call ``fn`` with the tensors' device current."""
-    import torch
-    if torch.cuda.current_device() == device.index:
-        _check(fn(*args))
-    else:
-        with torch.cuda.device(device):
-            _check(fn(*args))
-
-
-def _need_cuda(t, name):
-    if t.device.type != "cuda":
+def _device_of(name, t):
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+    return dev
+
+
+def _launch(fn, dev, *args):
+    """Call ``fn`` with device ``dev`` current."""
+    import torch
+    if torch._C._cuda_getDevice() == dev:
+        code = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args)
+    if code != DSPARK_OK:
+        _check(code)
+
+
+def _stream_of(stream, dev):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream
 
 
 def dspark_process_logits(logits, rows, *, out, row_status, draft_ids=None, history=None, bias=None, mask=None,
@@ -384,40 +387,40 @@ def dspark_process_logits(logits, rows, *, out, row_status, draft_ids=None, hist
     mask (-1: no grammar) or None (row b*(K_max+1) + j) -- all CUDA tensors.
     """
     import torch
-    dev = _need_cuda(logits, "logits")
+    dev = _device_of("logits", logits)
     if logits.dim() != 3:
         raise ValueError("logits must be [B, K_max+1, V]")
     B, W, V = logits.shape
-    _, _, stride = _rows_of("logits", logits)
-    _, _, out_stride = _rows_of("out", out, logits.shape)
-    if out.dtype != logits.dtype or out.device != dev:
-        raise ValueError("out must have the dtype and device of logits")
+    stride = _rows_of("logits", logits)[2]
+    out_stride = stride if out is logits else _rows_of("out", out, logits)[2]
     i32, f32 = torch.int32, torch.float32
     p = dspark_process_params_t(B, W - 1, V, _dtype_of(logits), stride, out_stride,
-                                _flat("rows", rows, torch.uint8, B * PROCESS_ROW_DTYPE.itemsize, dev),
-                                _stream(stream, dev), _flat("row_status", row_status, i32, B, dev))
-    h = b = m = None
+                                _flat("rows", rows, torch.uint8, B * 16, dev), _stream_of(stream, dev),
+                                _flat("row_status", row_status, i32, B, dev))
+    d = h = b = m = None
+    if draft_ids is not None and W > 1:
+        d = _flat("draft_ids", draft_ids, i32, B * (W - 1), dev)
     if history is not None:
-        nnz = history[1].numel()
-        h = ctypes.byref(dspark_counts_t(_flat("history offsets", history[0], i32, B + 1, dev),
-                                         _flat("history ids", history[1], i32, None, dev),
-                                         _flat("history counts", history[2], i32, nnz, dev)))
+        off, ids, counts = history
+        nnz = ids.numel()
+        h = dspark_counts_t(_flat("history offsets", off, i32, B + 1, dev), _flat("history ids", ids, i32, nnz, dev),
+                            _flat("history counts", counts, i32, nnz, dev))
     if bias is not None:
-        nnz = bias[1].numel()
-        b = ctypes.byref(dspark_bias_t(_flat("bias offsets", bias[0], i32, B + 1, dev),
-                                       _flat("bias ids", bias[1], i32, None, dev),
-                                       _flat("bias values", bias[2], f32, nnz, dev)))
+        off, ids, values = bias
+        nnz = ids.numel()
+        b = dspark_bias_t(_flat("bias offsets", off, i32, B + 1, dev), _flat("bias ids", ids, i32, nnz, dev),
+                          _flat("bias values", values, f32, nnz, dev))
     if mask is not None:
-        if mask.dim() != 2 or mask.dtype != i32 or mask.device != dev or mask.stride(1) != 1:
-            raise ValueError(f"mask must be [n, words] int32 rows on {dev}")
-        m = ctypes.byref(dspark_mask_t(mask.data_ptr(), mask.stride(0) if mask.shape[0] > 1 else mask.shape[1],
-                                       mask.shape[0], _flat("mask_rows", mask_rows, i32, B * W, dev, optional=True)))
-        if mask.shape[1] < (V + 31) // 32:
-            raise ValueError(f"mask rows have {mask.shape[1]} words for {V} tokens")
+        if mask.dim() != 2 or mask.dtype is not i32 or mask.get_device() != dev or (mask.stride(1) != 1 and mask.shape[1] > 1):
+            raise ValueError("mask must be [n, words] int32 rows on the logits' device")
+        n, words = mask.shape
+        if words < (V + 31) // 32:
+            raise ValueError(f"mask rows have {words} words for {V} tokens")
+        m = dspark_mask_t(mask.data_ptr(), mask.stride(0) if n > 1 else words, n,
+                          None if mask_rows is None else _flat("mask_rows", mask_rows, i32, B * W, dev))
     elif mask_rows is not None:
         raise ValueError("mask_rows without a mask")
-    d = _flat("draft_ids", draft_ids, i32, B * (W - 1), dev, optional=True) if W > 1 else None
-    _launch(load_library().dspark_process_logits, dev, logits.data_ptr(), out.data_ptr(), d, h, b, m, ctypes.byref(p))
+    _launch(load_library().dspark_process_logits, dev, logits.data_ptr(), out.data_ptr(), d, h, b, m, p)
 
 
 def dspark_top_logits(logits, *, values, ids, row_status, lse=None, temperature=1.0, stream=None):
@@ -427,35 +430,33 @@ def dspark_top_logits(logits, *, values, ids, row_status, lse=None, temperature=
     row_status [...] int32 -- all CUDA tensors; n is the last size of values.
     """
     import torch
-    dev = _need_cuda(logits, "logits")
+    dev = _device_of("logits", logits)
     R, V, stride = _rows_of("logits", logits)
     n = values.shape[-1]
-    p = dspark_top_params_t(R, V, _dtype_of(logits), stride, n, temperature, _stream(stream, dev),
-                            _flat("row_status", row_status, torch.int32, R, dev))
-    _launch(load_library().dspark_top_logits, dev, logits.data_ptr(), ctypes.byref(p),
-            _flat("values", values, torch.float32, R * n, dev), _flat("ids", ids, torch.int32, R * n, dev),
-            _flat("lse", lse, torch.float32, R, dev, optional=True))
+    i32, f32 = torch.int32, torch.float32
+    p = dspark_top_params_t(R, V, _dtype_of(logits), stride, n, temperature, _stream_of(stream, dev),
+                            _flat("row_status", row_status, i32, R, dev))
+    _launch(load_library().dspark_top_logits, dev, logits.data_ptr(), p, _flat("values", values, f32, R * n, dev),
+            _flat("ids", ids, i32, R * n, dev), None if lse is None else _flat("lse", lse, f32, R, dev))
 
 
 def _distill_args(student, teacher_ids, teacher_logits, teacher_lse, t2d, weights, temperature, row_status, grad, stream):
     import torch
-    dev = _need_cuda(student, "student")
+    dev = _device_of("student", student)
     R, V, stride = _rows_of("student", student)
-    grad_stride = V
-    if grad is not None:
-        _, _, grad_stride = _rows_of("grad", grad, student.shape)
-        if grad.dtype != student.dtype or grad.device != dev:
-            raise ValueError("grad must have the dtype and device of student")
+    grad_stride = V if grad is None else stride if grad is student else _rows_of("grad", grad, student)[2]
     i32, f32 = torch.int32, torch.float32
     n = teacher_ids.shape[-1]
     t = dspark_teacher_t(_flat("teacher_ids", teacher_ids, i32, R * n, dev),
                          _flat("teacher_logits", teacher_logits, f32, R * n, dev),
-                         _flat("teacher_lse", teacher_lse, f32, R, dev, optional=True), n,
-                         _flat("t2d", t2d, i32, None, dev, optional=True), 0 if t2d is None else t2d.numel())
+                         None if teacher_lse is None else _flat("teacher_lse", teacher_lse, f32, R, dev), n,
+                         None if t2d is None else _flat("t2d", t2d, i32, t2d.numel(), dev),
+                         0 if t2d is None else t2d.numel())
     p = dspark_distill_params_t(R, V, _dtype_of(student), stride, grad_stride, temperature,
-                                _flat("weights", weights, f32, R, dev, optional=True), _stream(stream, dev),
-                                _flat("row_status", row_status, i32, R, dev, optional=True))
-    return dev, R, ctypes.byref(t), ctypes.byref(p), None if grad is None else grad.data_ptr()
+                                None if weights is None else _flat("weights", weights, f32, R, dev),
+                                _stream_of(stream, dev),
+                                None if row_status is None else _flat("row_status", row_status, i32, R, dev))
+    return dev, R, t, p
 
 
 def dspark_distill(student, teacher_ids, teacher_logits, *, loss, row_status, grad=None, saved=None, teacher_lse=None,
@@ -472,10 +473,11 @@ def dspark_distill(student, teacher_ids, teacher_logits, *, loss, row_status, gr
     import torch
     if row_status is None:
         raise ValueError("row_status is missing")
-    dev, R, t, p, g = _distill_args(student, teacher_ids, teacher_logits, teacher_lse, t2d, weights, temperature,
-                                    row_status, grad, stream)
-    _launch(load_library().dspark_distill, dev, student.data_ptr(), t, p, _flat("loss", loss, torch.float32, R, dev),
-            _flat("saved", saved, torch.float32, 4 * R, dev, optional=True), g)
+    dev, R, t, p = _distill_args(student, teacher_ids, teacher_logits, teacher_lse, t2d, weights, temperature,
+                                 row_status, grad, stream)
+    f32 = torch.float32
+    _launch(load_library().dspark_distill, dev, student.data_ptr(), t, p, _flat("loss", loss, f32, R, dev),
+            None if saved is None else _flat("saved", saved, f32, 4 * R, dev), None if grad is None else grad.data_ptr())
 
 
 def dspark_distill_backward(student, teacher_ids, teacher_logits, *, saved, grad, grad_loss=None, teacher_lse=None,
@@ -485,8 +487,8 @@ def dspark_distill_backward(student, teacher_ids, teacher_logits, *, saved, grad
     import torch
     if grad is None:
         raise ValueError("grad is missing")
-    dev, R, t, p, g = _distill_args(student, teacher_ids, teacher_logits, teacher_lse, t2d, weights, temperature,
-                                    row_status, grad, stream)
-    _launch(load_library().dspark_distill_backward, dev, student.data_ptr(), t, p,
-            _flat("saved", saved, torch.float32, 4 * R, dev),
-            _flat("grad_loss", grad_loss, torch.float32, R, dev, optional=True), g)
+    dev, R, t, p = _distill_args(student, teacher_ids, teacher_logits, teacher_lse, t2d, weights, temperature,
+                                 row_status, grad, stream)
+    f32 = torch.float32
+    _launch(load_library().dspark_distill_backward, dev, student.data_ptr(), t, p, _flat("saved", saved, f32, 4 * R, dev),
+            None if grad_loss is None else _flat("grad_loss", grad_loss, f32, R, dev), grad.data_ptr())

@@ -18,6 +18,9 @@
 //
 // Sums that meet cancellation (of p, of p_i log p_i/e_i) are held in 64 bits, by one warp: this
 // GPU's 64-bit rate is 1/64 of its 32-bit one.
+#include <cstdlib>
+#include <type_traits>
+
 #include "vocab_rows.cuh"
 
 namespace dspark {
@@ -51,15 +54,17 @@ struct DisArgs {
     int* row_status;
 };
 
-struct DisPart {                                             // what a CTA tells its cluster
+struct __align__(16) DisPart {                               // what a CTA tells its cluster
     float m, rest, in;                                       // maximum; sums of e outside and inside S, by it
     int status;
     double cross;                                            // sum over its members of p_i (log p_i - log e_i)
+    double pad;
 };
+constexpr unsigned kDisPartBytes = 24;
 
 struct __align__(16) DisSmem {
-    DisPart part;
-    uint64_t bar;
+    DisPart all[kMaxCluster];                                // written by the cluster's CTAs
+    uint64_t bar, part_bar;
     int id[DSPARK_MAX_TOP_LOGITS];                           // draft ids of the row's record, -1: none
     float p[DSPARK_MAX_TOP_LOGITS];
     float lv[DSPARK_MAX_TOP_LOGITS];                         // log p; once taken out, the student's logit
@@ -67,27 +72,12 @@ struct __align__(16) DisSmem {
     float psum, p_r, mass;                                   // sum of p, 1 - sum, their sum
     int status, any;
     float m, total, rest;                                    // the row's
-    int row_status;
 };
 
 // log(v), v > 0 normal: the exponent's part in 64 bits, logf of what is left in [0.75, 1.5).
 __device__ __forceinline__ double log_split(float v) {
     const int e = (__float_as_int(v) - 0x3F400000) >> 23;
     return kLn2 * e + static_cast<double>(logf(__int_as_float(__float_as_int(v) - (e << 23))));
-}
-
-__device__ __forceinline__ unsigned long long dis_timer() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    return t;
-}
-// Wait for a copy with a 2 s bound; false when it runs out.
-__device__ __forceinline__ bool dis_wait(uint64_t* bar, unsigned parity) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = dis_timer();
-    while (!mbar_try_wait(bar, parity))
-        if (dis_timer() - t0 > 2000000000ull) return false;
-    return true;
 }
 
 template <int SX>
@@ -108,17 +98,26 @@ __device__ __forceinline__ void store_vec(const VocabRow<SX>& g, int k, int i0, 
 }
 
 // The teacher's record of a row, by one warp: draft ids, probabilities and their logarithms.
-__device__ __forceinline__ void take_record(const DisArgs& a, DisSmem& s, long long row) {
+struct Record {
+    int id[kDisEntries];
+    float t[kDisEntries], lse;
+    __device__ __forceinline__ void load(const DisArgs& a, long long row);
+    __device__ __forceinline__ void take(const DisArgs& a, DisSmem& s, long long row);
+};
+__device__ __forceinline__ void Record::load(const DisArgs& a, long long row) {
     const int lane = threadIdx.x & 31;
-    int id[kDisEntries], status = 0;
-    float t[kDisEntries], tmax = -INFINITY;
 #pragma unroll
     for (int q = 0; q < kDisEntries; ++q) {
         const int e = lane + 32 * q;
         id[q] = e < a.n ? a.ids[row * a.n + e] : -1;
         t[q] = e < a.n ? a.tl[row * a.n + e] : 0.f;
     }
-    const float lse = a.lse ? a.lse[row] : 0.f;
+    lse = a.lse ? a.lse[row] : 0.f;
+}
+__device__ __forceinline__ void Record::take(const DisArgs& a, DisSmem& s, long long row) {
+    const int lane = threadIdx.x & 31;
+    int status = 0;
+    float tmax = -INFINITY;
 #pragma unroll
     for (int q = 0; q < kDisEntries; ++q) {
         if (id[q] < -1 || id[q] >= (a.t2d ? a.target_V : a.V)) { status = DSPARK_ROW_BAD_TEACHER; id[q] = -1; }
@@ -184,12 +183,11 @@ __device__ __forceinline__ void take_record(const DisArgs& a, DisSmem& s, long l
 }
 
 template <int SX, int PASS>
-__global__ void __launch_bounds__(kRowThreads, 4) distill_kernel(DisArgs a) {
+__global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
     constexpr int VE = VocabRow<SX>::VE;
     constexpr bool kWantLoss = (PASS & kLoss) != 0, kWantGrad = (PASS & kGrad) != 0;
     __shared__ DisSmem s;
-    extern __shared__ uint4 s_x[];                           // [piece] vectors, then a bit for each of their lanes
-    unsigned* const s_bits = reinterpret_cast<unsigned*>(s_x + a.piece);
+    extern __shared__ uint4 s_x[];                           // [piece]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = a.cluster, rank = static_cast<int>(blockIdx.x % C);
     const long long row = blockIdx.x / C;
@@ -198,7 +196,16 @@ __global__ void __launch_bounds__(kRowThreads, 4) distill_kernel(DisArgs a) {
     const int k0 = static_cast<int>(static_cast<long long>(x.nvec) * rank / C);
     const int k1 = static_cast<int>(static_cast<long long>(x.nvec) * (rank + 1) / C);
     const bool same_phase = x.a0 == g.a0;
+    const float w = a.weights ? a.weights[row] : 1.f;
 
+    if (kWantLoss && C > 1) {                                // before a peer can push here
+        if (tid == 0) {
+            mbar_init(&s.part_bar, 1);
+            fence_mbar_init();
+            mbar_arrive_expect_tx(&s.part_bar, kDisPartBytes * C);
+        }
+        cluster_arrive();
+    }
     // a row that is not reduced: loss, status and gradient; the same branch in every CTA of the row
     auto leave = [&](int status) {
         if (kWantLoss && rank == 0 && tid == 0) {
@@ -209,13 +216,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) distill_kernel(DisArgs a) {
         }
         if (kWantGrad)
             for (int k = k0 + tid; k < k1; k += kRowThreads) store_vec<SX>(g, k, x.first(k), make_uint4(0, 0, 0, 0), same_phase);
+        if (kWantLoss && C > 1) cluster_wait();
     };
-    const float w = a.weights ? a.weights[row] : 1.f;
-    if (w == 0.f) {
-        leave(0);
-        return;
-    }
-
     // vectors [b, e) of the row into the buffer: whole ones by a bulk copy, the row's ragged first
     // and last by two threads of the warp that takes the members out
     auto fetch = [&](int b, int e) {
@@ -228,6 +230,12 @@ __global__ void __launch_bounds__(kRowThreads, 4) distill_kernel(DisArgs a) {
         if (tid == 1 && wb > b) s_x[0] = load_vec<SX>(x, b, e);
         if (tid == 2 && we < e && we >= wb) s_x[we - b] = load_vec<SX>(x, we, e);
     };
+    Record rec;
+    if (warp == 0) rec.load(a, row);
+    if (w == 0.f) {
+        leave(0);
+        return;
+    }
     if (tid == 0) {
         mbar_init(&s.bar, 1);
         fence_mbar_init();
@@ -235,151 +243,132 @@ __global__ void __launch_bounds__(kRowThreads, 4) distill_kernel(DisArgs a) {
     int b = k0, e = min(k1, k0 + a.piece);
     unsigned parity = 0;
     if (k0 < k1) fetch(b, e);
-    for (int i = tid; i < (a.piece * VE + 31) / 32; i += kRowThreads) s_bits[i] = 0u;
-    if (warp == 0) take_record(a, s, row);
+    if (warp == 0) rec.take(a, s, row);
     __syncthreads();
     bool late = false;
     if (!s.any || s.status) {
-        if (k0 < k1) late = !dis_wait(&s.bar, 0);
+        if (k0 < k1) late = !bar_wait(&s.bar, 0);
         late = __syncthreads_or(late);
         leave(s.status ? s.status : late ? DSPARK_ROW_INTERNAL : 0);
         return;
     }
 
+    if (kWantLoss && C > 1) cluster_wait();                  // the peers' barriers stand
+
     ExpSum es{-INFINITY, 0.f};
     double cross = 0.0;
     int status = 0;
-    // the span's pieces for the sum (loss) or, alone, for the members' logits (gradient)
     const double ln_c = kLn2 * a.c;                          // the sums' own 1/T: c rounds log2(e)/T to fp32
-    auto take_members = [&](int b, int e) {                  // by one warp
+    // One warp notes the logits of the members among the buffer's vectors [b, e) and puts -inf in
+    // their place.  A repeated id finds the mark of the first (a NaN that is cleared at the end).
+    auto take_members = [&](int b, int e) {
         __syncwarp();
-        const int i_lo = max(0, x.first(b)), i_hi = min(a.V, x.first(e));
+        constexpr uint32_t kMark = SX == 2 ? 0x7FD5u : 0x7FD5AB31u;
+        using Bits = std::conditional_t<SX == 2, unsigned short, unsigned>;
+        Bits* const buf = reinterpret_cast<Bits*>(s_x);
+        const int i0 = x.first(b), i_lo = max(0, i0), i_hi = min(a.V, x.first(e));
+        for (int r0 = 0; r0 < a.n; r0 += 32) {
+            const int r = r0 + lane, id = r < a.n ? s.id[r] : -1;
+            const bool in = id >= i_lo && id < i_hi;
+            if (!__any_sync(0xffffffffu, in)) continue;
+            if (__popc(__match_any_sync(0xffffffffu, in ? id : -2 - lane)) > 1) status = DSPARK_ROW_BAD_TEACHER;
+            if (in) {
+                const uint32_t bits = buf[id - i0];
+                if (bits == kMark) status = DSPARK_ROW_BAD_TEACHER;
+                const float v = __uint_as_float(SX == 2 ? bits << 16 : bits), p = s.p[r];
+                if (p > 0.f) cross += p * (s.lv[r] - v * ln_c);
+                s.lv[r] = v;
+            }
+            __syncwarp();
+            if (in) buf[id - i0] = static_cast<Bits>(kMark);
+            __syncwarp();
+        }
         for (int r = lane; r < a.n; r += 32) {
             const int id = s.id[r];
-            if (id < i_lo || id >= i_hi) continue;
-            const int at = id - x.first(b);                  // lane of the buffer
-            const unsigned bit = 1u << (at & 31);            // a repeated id (told by the saved sums to a gradient alone)
-            if (kWantLoss && atomicOr(&s_bits[at >> 5], bit) & bit) { status = DSPARK_ROW_BAD_TEACHER; continue; }
-            float v;
-            if (SX == 2) {
-                unsigned short* p = reinterpret_cast<unsigned short*>(s_x) + at;
-                v = __uint_as_float(static_cast<uint32_t>(*p) << 16);
-                *p = static_cast<unsigned short>(ninf_bits<SX>());
-            } else {
-                float* p = reinterpret_cast<float*>(s_x) + at;
-                v = *p;
-                *p = -INFINITY;
-            }
-            const float p = s.p[r];
-            if (p > 0.f) cross += p * (s.lv[r] - v * ln_c);
-            s.lv[r] = v;
+            if (id >= i_lo && id < i_hi) buf[id - i0] = static_cast<Bits>(ninf_bits<SX>());
         }
     };
+    double row_cross = 0.0;
+    int row_status = 0;
     if (kWantLoss) {
         while (true) {
-            if (k0 < k1) late |= !dis_wait(&s.bar, parity);
+            if (k0 < k1) late |= !bar_wait(&s.bar, parity);
             parity ^= 1;
             if (warp == 0 && k0 < k1) take_members(b, e);
             __syncthreads();
-            for (int base = b; base < e; base += kDisVec * kRowThreads) {
+            int k = tid;
+            for (; k + (kDisVec - 1) * kRowThreads < e - b; k += kDisVec * kRowThreads) {
                 uint4 v[kDisVec];
                 float bm = -INFINITY;
 #pragma unroll
                 for (int u = 0; u < kDisVec; ++u) {
-                    const int k = base + u * kRowThreads + tid;
-                    v[u] = k < e ? s_x[k - b] : ninf_vec<SX>();
+                    v[u] = s_x[k + u * kRowThreads];
                     bm = fmaxf(bm, vec_max<SX>(v[u]));
                 }
                 add_exps<SX>(es, v, bm, a.c);
             }
+            for (; k < e - b; k += kRowThreads) {
+                const uint4 v[1] = {s_x[k]};
+                add_exps<SX>(es, v, vec_max<SX>(v[0]), a.c);
+            }
             if (e >= k1) break;
-            for (int i = tid; i < (a.piece * VE + 31) / 32; i += kRowThreads) s_bits[i] = 0u;
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncthreads();
             b = e;
             e = min(k1, b + a.piece);
             fetch(b, e);
         }
-        for (int o = 16; o; o >>= 1)
-            es = merge(es, ExpSum{__shfl_xor_sync(0xffffffffu, es.m, o), __shfl_xor_sync(0xffffffffu, es.sum, o)}, a.c);
+        es = warp_merge(es, a.c);
         if (lane == 0) s.es[warp] = es;
         late = __syncthreads_or(late);
-        if (warp == 0) {                                     // the CTA's part
-            es = s.es[lane & (kRowWarps - 1)];
-            for (int o = kRowWarps / 2; o; o >>= 1)
-                es = merge(es, ExpSum{__shfl_xor_sync(0xffffffffu, es.m, o), __shfl_xor_sync(0xffffffffu, es.sum, o)}, a.c);
+        if (warp == 0) {                                     // the CTA's part, to every CTA of the row
+            es = lane < kRowWarps ? s.es[lane] : ExpSum{-INFINITY, 0.f};
             const int i_lo = max(0, x.first(k0)), i_hi = min(a.V, x.first(k1));
             float m = es.m;
             for (int r = lane; r < a.n; r += 32)
                 if (s.id[r] >= i_lo && s.id[r] < i_hi) m = fmaxf(m, s.lv[r]);
-            m = warp_max(m);
+            m = key_to_f(__reduce_max_sync(0xffffffffu, fkey(m)));
             const ExpRef ref(m > -INFINITY ? m : 0.f, a.c);
             float in = 0.f;
             for (int r = lane; r < a.n; r += 32)
                 if (s.id[r] >= i_lo && s.id[r] < i_hi) in += ref.of(s.lv[r]);   // NaN for NaN and +inf
             in = warp_sum(in);
+            const float rest = warp_sum(m > -INFINITY ? es.sum * rebase(es.m, m, a.c) : es.sum);
             cross = warp_sum_d(cross);
             status = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(status));
             if (late) status |= DSPARK_ROW_INTERNAL;
-            if (lane == 0) {
-                s.part.m = m;
-                s.part.rest = m > -INFINITY ? es.sum * rebase(es.m, m, a.c) : es.sum;
-                s.part.in = in;
-                s.part.status = status;
-                s.part.cross = cross;
-            }
-        }
-        if (C > 1) {
-            cluster_arrive();
-            cluster_wait();
-        }
-        if (warp == 0) {                                     // the row: every CTA joins the C parts alike
-            __syncwarp();
-            DisPart o{-INFINITY, 0.f, 0.f, 0, 0.0};
             if (C > 1) {
                 if (lane < C) {
-                    const unsigned from = peer_addr(&s.part, lane);
-                    o.m = __uint_as_float(peer_ld32(from));
-                    o.rest = __uint_as_float(peer_ld32(from + 4));
-                    o.in = __uint_as_float(peer_ld32(from + 8));
-                    o.status = static_cast<int>(peer_ld32(from + 12));
-                    o.cross = __longlong_as_double(static_cast<long long>(peer_ld64(from + 16)));
+                    const unsigned to = peer_addr(&s.all[rank], lane), bar = peer_addr(&s.part_bar, lane);
+                    peer_push128(to, bar, __float_as_uint(m), __float_as_uint(rest), __float_as_uint(in), static_cast<uint32_t>(status));
+                    peer_push64(to + 16, bar, static_cast<unsigned long long>(__double_as_longlong(cross)));
                 }
+                late = !bar_wait(&s.part_bar, 0);
             } else if (lane == 0) {
-                o = s.part;
+                s.all[0] = DisPart{m, rest, in, status, cross, 0.0};
             }
-            const float m = warp_max(o.m);
+            __syncwarp();
+            // the row: every CTA joins the C parts alike
+            DisPart o{-INFINITY, 0.f, 0.f, 0, 0.0, 0.0};
+            if (lane < C) o = s.all[lane];
+            m = key_to_f(__reduce_max_sync(0xffffffffu, fkey(o.m)));
             const float f = m > -INFINITY ? rebase(o.m, m, a.c) : 1.f;
-            const float rest = warp_sum(o.rest * f), total = rest + warp_sum(o.in * f);
-            int st = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(o.status));
-            if (!st && !(total == total && m > -INFINITY)) st = DSPARK_ROW_NONFINITE;
+            const float rest_r = warp_sum(lane < C ? o.rest * f : 0.f), total = rest_r + warp_sum(lane < C ? o.in * f : 0.f);
+            row_status = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(o.status));
+            if (late) row_status |= DSPARK_ROW_INTERNAL;
+            if (!row_status && !(total == total && m > -INFINITY)) row_status = DSPARK_ROW_NONFINITE;
+            row_cross = o.cross;
             if (lane == 0) {
                 s.m = m;
-                s.total = st ? NAN : total;
-                s.rest = rest;
-            }
-            if (rank == 0) {
-                const double cr = warp_sum_d(o.cross);
-                if (lane == 0) {
-                    double loss = cr + s.psum * (ExpRef(m, a.c).whole ? kLn2 * ExpRef(m, a.c).r : m * ln_c) + s.psum * log_split(total);
-                    if (s.p_r > 0.f && rest > 0.f) loss += s.p_r * logf(s.p_r * (total / rest));
-                    a.loss[row] = st ? NAN : static_cast<float>(w * loss);
-                    a.row_status[row] = st;
-                    if (a.saved_out) {
-                        a.saved_out[4 * row] = m;
-                        a.saved_out[4 * row + 1] = st ? NAN : total;
-                        a.saved_out[4 * row + 2] = rest;
-                        a.saved_out[4 * row + 3] = 0.f;
-                    }
-                }
+                s.total = row_status ? NAN : total;
+                s.rest = rest_r;
             }
         }
-        if (C > 1) cluster_arrive();                         // waited for at the end: peers have read this CTA's part
+        __syncthreads();
     }
 
     // ---- the gradient
     if (kWantGrad) {
-        __syncthreads();
         const float m = kWantLoss ? s.m : a.saved[4 * row], total = kWantLoss ? s.total : a.saved[4 * row + 1];
         const float rest = kWantLoss ? s.rest : a.saved[4 * row + 2];
         const bool ok = total > 0.f && m > -INFINITY;        // total is NaN for a row that cannot be normalised
@@ -394,49 +383,43 @@ __global__ void __launch_bounds__(kRowThreads, 4) distill_kernel(DisArgs a) {
         const ExpRef ref(m, a.c);
         // with a loss the last piece is in the buffer; the others, if any, come again
         const bool kept = kWantLoss && e - b == k1 - k0;
-        if (!kept) {
-            if (kWantLoss) {
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncthreads();
-                b = k0;
-                e = min(k1, k0 + a.piece);
-                if (k0 < k1) fetch(b, e);
-            }
+        if (kWantLoss && !kept) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncthreads();
+            b = k0;
+            e = min(k1, k0 + a.piece);
+            if (k0 < k1) fetch(b, e);
         }
+        bool lost = false;
         while (true) {
             if (!kept) {
-                if (k0 < k1) late |= !dis_wait(&s.bar, parity);
+                if (k0 < k1) lost |= !bar_wait(&s.bar, parity);
                 parity ^= 1;
-                late = __syncthreads_or(late);
+                lost = __syncthreads_or(lost);
                 if (!kWantLoss && warp == 0 && k0 < k1) take_members(b, e);
                 if (!kWantLoss) __syncthreads();
             }
-            for (int base = b; base < e; base += kDisVec * kRowThreads) {
+            for (int k = b + tid; k < e; k += kRowThreads) {
+                const uint4 v = s_x[k - b];
+                uint4 o = make_uint4(0, 0, 0, 0);
+                if (ok && !lost) {
+                    float f[VE];
+                    if (ref.whole) {
+                        const unsigned long long c2 = pack2(a.c, a.c), r2 = pack2(-ref.r, -ref.r), s2 = pack2(scale_out, scale_out);
 #pragma unroll
-                for (int u = 0; u < kDisVec; ++u) {
-                    const int k = base + u * kRowThreads + tid;
-                    if (k >= e) break;
-                    const uint4 v = s_x[k - b];
-                    uint4 o = make_uint4(0, 0, 0, 0);
-                    if (ok && !late) {
-                        float f[VE];
-                        if (ref.whole) {
-                            const unsigned long long c2 = pack2(a.c, a.c), r2 = pack2(-ref.r, -ref.r), s2 = pack2(scale_out, scale_out);
-#pragma unroll
-                            for (int h = 0; h < VE / 2; ++h) {
-                                float lo, hi;
-                                unpack2(fma2(pair_of<SX>(v, h), c2, r2), lo, hi);
-                                unpack2(mul2(pack2(ex2_approx(lo), ex2_approx(hi)), s2), f[2 * h], f[2 * h + 1]);
-                            }
-                        } else {
-#pragma unroll
-                            for (int q = 0; q < VE; ++q) f[q] = ref.of(elem<SX>(v, q)) * scale_out;
+                        for (int h = 0; h < VE / 2; ++h) {
+                            float lo, hi;
+                            unpack2(fma2(pair_of<SX>(v, h), c2, r2), lo, hi);
+                            unpack2(mul2(pack2(ex2_approx(lo), ex2_approx(hi)), s2), f[2 * h], f[2 * h + 1]);
                         }
-                        if (SX == 2) o = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4 % VE], f[5 % VE]), pack_bf16(f[6 % VE], f[7 % VE]));
-                        else o = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < VE; ++q) f[q] = ref.of(elem<SX>(v, q)) * scale_out;
                     }
-                    store_vec<SX>(g, k, x.first(k), o, same_phase);
+                    if (SX == 2) o = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4 % VE], f[5 % VE]), pack_bf16(f[6 % VE], f[7 % VE]));
+                    else o = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
                 }
+                store_vec<SX>(g, k, x.first(k), o, same_phase);
             }
             if (kept || e >= k1) break;
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -446,7 +429,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) distill_kernel(DisArgs a) {
             fetch(b, e);
         }
         __syncthreads();                                     // the members' gradients go over the span's
-        if (warp == 0 && ok && !late) {
+        if (warp == 0 && ok && !lost) {
             const int i_lo = max(0, x.first(k0)), i_hi = min(a.V, x.first(k1));
             for (int r = lane; r < a.n; r += 32) {
                 const int id = s.id[r];
@@ -458,7 +441,23 @@ __global__ void __launch_bounds__(kRowThreads, 4) distill_kernel(DisArgs a) {
             }
         }
     }
-    if (kWantLoss && C > 1) cluster_wait();
+    if (kWantLoss && rank == 0 && warp == 0) {               // the loss, off the gradient's path
+        row_cross = warp_sum_d(lane < C ? row_cross : 0.0);
+        if (lane == 0) {
+            const float m = s.m, total = s.total, rest = s.rest;
+            const ExpRef ref(m, a.c);
+            double loss = row_cross + s.psum * ((ref.whole ? kLn2 * ref.r : m * ln_c) + log_split(total));
+            if (s.p_r > 0.f && rest > 0.f) loss += s.p_r * logf(s.p_r * (total / rest));
+            a.loss[row] = row_status ? NAN : static_cast<float>(w * loss);
+            a.row_status[row] = row_status;
+            if (a.saved_out) {
+                a.saved_out[4 * row] = m;
+                a.saved_out[4 * row + 1] = total;
+                a.saved_out[4 * row + 2] = rest;
+                a.saved_out[4 * row + 3] = 0.f;
+            }
+        }
+    }
 }
 
 // Checks shared by the two entry points; on success *a and *sx are set.
@@ -487,7 +486,9 @@ dspark_status_t distill_args(const void* student, const dspark_teacher_t* t, con
     // halves, 227 us in quarters: a CTA's latencies cost more than its share of the row.
     const int nvec = max_vectors(p->V, *sx);
     a->cluster = 1;
-    while (a->cluster < kMaxCluster && (nvec > a->cluster * kDisSpan ||
+    int span = kDisSpan;
+    if (const char* e = getenv("DISPAN")) span = atoi(e);
+    while (a->cluster < kMaxCluster && (nvec > a->cluster * span ||
                                         (nvec >= a->cluster * 512 && static_cast<long long>(p->n_rows) * a->cluster < 304)))
         a->cluster *= 2;
     // a longer span comes in pieces of 40 KB
@@ -498,7 +499,7 @@ dspark_status_t distill_args(const void* student, const dspark_teacher_t* t, con
 
 template <int SX, int PASS>
 dspark_status_t distill_launch(const DisArgs& a, int rows, void* stream) {
-    const size_t smem = static_cast<size_t>(a.piece) * 16 + static_cast<size_t>((a.piece * (16 / SX) + 31) / 32) * 4;
+    const size_t smem = static_cast<size_t>(a.piece) * 16;
     if (smem > 32 * 1024 &&                                  // beyond what a launch gets unasked
         cudaFuncSetAttribute(distill_kernel<SX, PASS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return DSPARK_ERR_CUDA;

@@ -180,6 +180,13 @@ __device__ __forceinline__ ExpSum merge(const ExpSum& a, const ExpSum& b, float 
     r.sum = r.m > -INFINITY ? a.sum * rebase(a.m, r.m, c) + b.sum * rebase(b.m, r.m, c) : a.sum + b.sum;
     return r;
 }
+// The warp's sum, in every lane: one rescaling to the warp's maximum, then plain additions.
+__device__ __forceinline__ ExpSum warp_merge(ExpSum a, float c) {
+    const float m = key_to_f(__reduce_max_sync(0xffffffffu, fkey(a.m)));
+    a.sum = warp_sum(m > -INFINITY ? a.sum * rebase(a.m, m, c) : a.sum);
+    a.m = m;
+    return a;
+}
 // Add the exponentials of U vectors whose maximum is bm.
 template <int SX, int U>
 __device__ __forceinline__ void add_exps(ExpSum& es, const uint4 (&v)[U], float bm, float c) {
@@ -236,6 +243,38 @@ __device__ __forceinline__ unsigned long long peer_ld64(unsigned a) {
     unsigned long long v;
     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
     return v;
+}
+
+// Write 16 or 8 bytes into a cluster CTA's shared memory; the bytes count on the mbarrier there.
+__device__ __forceinline__ void peer_push128(unsigned a, unsigned bar, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];"
+                 :: "r"(a), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void peer_push64(unsigned a, unsigned bar, unsigned long long v) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];"
+                 :: "r"(a), "l"(v), "r"(bar) : "memory");
+}
+__device__ __forceinline__ unsigned long long global_timer() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+// Wait for an mbarrier's phase with a 2 s bound, false when it runs out; data pushed by the
+// cluster's CTAs is visible afterwards.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, unsigned parity) {
+    unsigned long long t0 = 0;
+    for (unsigned i = 0;; ++i) {
+        unsigned ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+        if (ok) return true;
+        const unsigned long long t = global_timer();
+        if (i == 0) t0 = t;
+        else if (t - t0 > 2000000000ull) return false;
+    }
 }
 
 // Launch `grid` CTAs in clusters of `cluster` (1: no cluster).

@@ -110,11 +110,12 @@ def test_binding_refuses(bd):
             bd._rows_of("x", bad)
     with pytest.raises(TypeError):
         bd._dtype_of(torch.zeros(1, dtype=torch.float16))
-    cpu = torch.device("cpu")
-    assert bd._flat("t", torch.zeros(4), torch.float32, 4, cpu) and bd._flat("t", None, torch.float32, 4, cpu, True) is None
+    assert bd._flat("t", torch.zeros(4), torch.float32, 4, -1)
     for bad in (None, torch.zeros(5), torch.zeros(4, dtype=torch.int32), torch.zeros(8)[::2]):
         with pytest.raises(ValueError):
-            bd._flat("t", bad, torch.float32, 4, cpu)
+            bd._flat("t", bad, torch.float32, 4, -1)
+    with pytest.raises(ValueError):
+        bd._flat("t", torch.zeros(4), torch.float32, 4, 0)
 
 
 def test_oracle_gradient_by_differences():
