@@ -18,7 +18,6 @@
 //
 // Sums that meet cancellation (of p, of p_i log p_i/e_i) are held in 64 bits, by one warp: this
 // GPU's 64-bit rate is 1/64 of its 32-bit one.
-#include <cstdlib>
 #include <type_traits>
 
 #include "vocab_rows.cuh"
@@ -35,7 +34,7 @@ constexpr int kDisEntries = DSPARK_MAX_TOP_LOGITS / 32;      // record entries p
 enum DistillPass : int { kLoss = 1, kGrad = 2 };
 
 struct DisArgs {
-    int V, n, cluster, target_V;
+    int V, n, log_c, target_V;                               // log_c: of the cluster's size
     int piece;                                               // vectors of the buffer
     float c;                                                 // log2(e) / T
     double inv_t;
@@ -189,12 +188,11 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
     __shared__ DisSmem s;
     extern __shared__ uint4 s_x[];                           // [piece]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int C = a.cluster, rank = static_cast<int>(blockIdx.x % C);
-    const long long row = blockIdx.x / C;
+    const int C = 1 << a.log_c, rank = static_cast<int>(blockIdx.x & (C - 1));
+    const long long row = blockIdx.x >> a.log_c;
     const VocabRow<SX> x(a.s, row, a.s_stride, a.V);
     const VocabRow<SX> g(a.g, row, a.g_stride, a.V);
-    const int k0 = static_cast<int>(static_cast<long long>(x.nvec) * rank / C);
-    const int k1 = static_cast<int>(static_cast<long long>(x.nvec) * (rank + 1) / C);
+    const int k0 = x.nvec * rank >> a.log_c, k1 = x.nvec * (rank + 1) >> a.log_c;   // nvec * C < 2^31
     const bool same_phase = x.a0 == g.a0;
     const float w = a.weights ? a.weights[row] : 1.f;
 
@@ -247,7 +245,7 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
     __syncthreads();
     bool late = false;
     if (!s.any || s.status) {
-        if (k0 < k1) late = !bar_wait(&s.bar, 0);
+        if (warp == 0 && k0 < k1) late = !bar_wait(&s.bar, 0);
         late = __syncthreads_or(late);
         leave(s.status ? s.status : late ? DSPARK_ROW_INTERNAL : 0);
         return;
@@ -292,24 +290,22 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
     int row_status = 0;
     if (kWantLoss) {
         while (true) {
-            if (k0 < k1) late |= !bar_wait(&s.bar, parity);
+            if (warp == 0 && k0 < k1) {                      // the others sleep at the barrier
+                late |= !bar_wait(&s.bar, parity);
+                take_members(b, e);
+            }
             parity ^= 1;
-            if (warp == 0 && k0 < k1) take_members(b, e);
             __syncthreads();
             int k = tid;
             for (; k + (kDisVec - 1) * kRowThreads < e - b; k += kDisVec * kRowThreads) {
                 uint4 v[kDisVec];
-                float bm = -INFINITY;
 #pragma unroll
-                for (int u = 0; u < kDisVec; ++u) {
-                    v[u] = s_x[k + u * kRowThreads];
-                    bm = fmaxf(bm, vec_max<SX>(v[u]));
-                }
-                add_exps<SX>(es, v, bm, a.c);
+                for (int u = 0; u < kDisVec; ++u) v[u] = s_x[k + u * kRowThreads];
+                add_exps<SX>(es, v, vecs_max<SX>(v), a.c);
             }
             for (; k < e - b; k += kRowThreads) {
                 const uint4 v[1] = {s_x[k]};
-                add_exps<SX>(es, v, vec_max<SX>(v[0]), a.c);
+                add_exps<SX>(es, v, vecs_max<SX>(v), a.c);
             }
             if (e >= k1) break;
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -320,7 +316,7 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
         }
         es = warp_merge(es, a.c);
         if (lane == 0) s.es[warp] = es;
-        late = __syncthreads_or(late);
+        __syncthreads();
         if (warp == 0) {                                     // the CTA's part, to every CTA of the row
             es = lane < kRowWarps ? s.es[lane] : ExpSum{-INFINITY, 0.f};
             const int i_lo = max(0, x.first(k0)), i_hi = min(a.V, x.first(k1));
@@ -393,11 +389,12 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
         bool lost = false;
         while (true) {
             if (!kept) {
-                if (k0 < k1) lost |= !bar_wait(&s.bar, parity);
+                if (warp == 0 && k0 < k1) {
+                    lost |= !bar_wait(&s.bar, parity);
+                    if (!kWantLoss) take_members(b, e);
+                }
                 parity ^= 1;
                 lost = __syncthreads_or(lost);
-                if (!kWantLoss && warp == 0 && k0 < k1) take_members(b, e);
-                if (!kWantLoss) __syncthreads();
             }
             for (int k = b + tid; k < e; k += kRowThreads) {
                 const uint4 v = s_x[k - b];
@@ -485,14 +482,13 @@ dspark_status_t distill_args(const void* student, const dspark_teacher_t* t, con
     // do not make two CTAs per SM.  2048 rows of 64 KB, loss then gradient: 114 us whole, 139 us in
     // halves, 227 us in quarters: a CTA's latencies cost more than its share of the row.
     const int nvec = max_vectors(p->V, *sx);
-    a->cluster = 1;
-    int span = kDisSpan;
-    if (const char* e = getenv("DISPAN")) span = atoi(e);
-    while (a->cluster < kMaxCluster && (nvec > a->cluster * span ||
-                                        (nvec >= a->cluster * 512 && static_cast<long long>(p->n_rows) * a->cluster < 304)))
-        a->cluster *= 2;
+    int cluster = 1;
+    while (cluster < kMaxCluster && (nvec > cluster * kDisSpan ||
+                                        (nvec >= cluster * 512 && static_cast<long long>(p->n_rows) * cluster < 304)))
+        cluster *= 2;
+    for (a->log_c = 0; (1 << a->log_c) < cluster;) ++a->log_c;
     // a longer span comes in pieces of 40 KB
-    a->piece = nvec / a->cluster + 1;
+    a->piece = nvec / cluster + 1;
     if (a->piece > kDisSpan) a->piece = kDisPiece;
     return DSPARK_OK;
 }
@@ -503,8 +499,8 @@ dspark_status_t distill_launch(const DisArgs& a, int rows, void* stream) {
     if (smem > 32 * 1024 &&                                  // beyond what a launch gets unasked
         cudaFuncSetAttribute(distill_kernel<SX, PASS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return DSPARK_ERR_CUDA;
-    const unsigned grid = static_cast<unsigned>(rows) * static_cast<unsigned>(a.cluster);
-    const cudaError_t e = launch_cluster(distill_kernel<SX, PASS>, grid, a.cluster, smem, static_cast<cudaStream_t>(stream), a);
+    const unsigned grid = static_cast<unsigned>(rows) << a.log_c;
+    const cudaError_t e = launch_cluster(distill_kernel<SX, PASS>, grid, 1 << a.log_c, smem, static_cast<cudaStream_t>(stream), a);
     return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 

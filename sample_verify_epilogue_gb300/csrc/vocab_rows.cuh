@@ -118,6 +118,24 @@ __device__ __forceinline__ float vec_max(const uint4& w) {
     return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
 }
 
+// The same over U vectors.
+template <int SX, int U>
+__device__ __forceinline__ float vecs_max(const uint4 (&w)[U]) {
+    if (SX == 2) {
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(w);
+        __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+#pragma unroll
+        for (int u = 1; u < U; ++u)
+            m = __hmax2(m, __hmax2(__hmax2(h[4 * u], h[4 * u + 1]), __hmax2(h[4 * u + 2], h[4 * u + 3])));
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(&m);
+        return fmaxf(bf16_lo(x), bf16_hi(x));
+    }
+    float m = vec_max<SX>(w[0]);
+#pragma unroll
+    for (int u = 1; u < U; ++u) m = fmaxf(m, vec_max<SX>(w[u]));
+    return m;
+}
+
 // ---------------------------------------------------------------- packed fp32 pairs
 __device__ __forceinline__ unsigned long long pack2(float lo, float hi) {
     unsigned long long r;
