@@ -10,14 +10,17 @@
 //
 // Bound by bandwidth: s is read once and the gradient written once.  A CTA's span of the row
 // comes to shared memory by bulk copies and stays there between the sum and the gradient, so that
-// a call for both does not read the row twice.  While it arrives, one warp makes the teacher's
-// probabilities from the record.  That warp then takes the span's members out: it notes their
-// logits and puts -inf in their place, so that the two loops over the span know nothing of S; the
-// members' gradients are written over afterwards.  (Longer spans go through the buffer in pieces,
-// twice when both results are wanted; the second read is then from L2.)
+// a call for both does not read the row twice.  Five CTAs to an SM hold 190 KB of rows: what bounds
+// the rate is how long a CTA lives, so everything between copy and store is kept short and wide.  The
+// record is one thread's work per entry; while the span arrives they make the teacher's
+// probabilities, then take the members out: each notes its logit and leaves -inf in its place, so
+// that the two loops over the span know nothing of S, and writes its member's gradient over at the
+// end.  (One warp for the record took 6000 of a CTA's 24600 cycles, taking the members out 2800.)
+// Longer spans go through the buffer in pieces, twice when both results are wanted; the second
+// read is then from L2.
 //
-// Sums that meet cancellation (of p, of p_i log p_i/e_i) are held in 64 bits, by one warp: this
-// GPU's 64-bit rate is 1/64 of its 32-bit one.
+// Sums that meet cancellation (p_i log p_i/e_i) are held in 64 bits, off the path to the gradient:
+// this GPU's 64-bit rate is 1/64 of its 32-bit one.
 #include <type_traits>
 
 #include "vocab_rows.cuh"
@@ -28,14 +31,14 @@ namespace {
 
 constexpr int kDisVec = 4;                                   // vectors a thread holds at a time
 constexpr int kDisSpan = 4608;                               // vectors of a span kept in one piece at most
-constexpr int kDisPiece = 2560;                              // vectors of a piece of a longer one
-constexpr int kDisEntries = DSPARK_MAX_TOP_LOGITS / 32;      // record entries per lane
+constexpr int kDisPiece = 1024;                              // vectors of a piece of a longer one
+static_assert(DSPARK_MAX_TOP_LOGITS <= kRowThreads, "a thread per record entry");
 
 enum DistillPass : int { kLoss = 1, kGrad = 2 };
 
 struct DisArgs {
     int V, n, log_c, target_V;                               // log_c: of the cluster's size
-    int piece;                                               // vectors of the buffer
+    int piece, log_slots;                                    // vectors of a piece; buffers for one (1 or 2)
     float c;                                                 // log2(e) / T
     double inv_t;
     long long s_stride, g_stride;
@@ -53,25 +56,25 @@ struct DisArgs {
     int* row_status;
 };
 
-struct __align__(16) DisPart {                               // what a CTA tells its cluster
+struct __align__(16) DisPart {                               // what a warp tells its CTA, a CTA its cluster
     float m, rest, in;                                       // maximum; sums of e outside and inside S, by it
     int status;
-    double cross;                                            // sum over its members of p_i (log p_i - log e_i)
-    double pad;
 };
-constexpr unsigned kDisPartBytes = 24;
 
 struct __align__(16) DisSmem {
     DisPart all[kMaxCluster];                                // written by the cluster's CTAs
-    uint64_t bar, part_bar;
-    int id[DSPARK_MAX_TOP_LOGITS];                           // draft ids of the row's record, -1: none
-    float p[DSPARK_MAX_TOP_LOGITS];
-    float lv[DSPARK_MAX_TOP_LOGITS];                         // log p; once taken out, the student's logit
-    ExpSum es[kRowWarps];
-    float psum, p_r, mass;                                   // sum of p, 1 - sum, their sum
-    int status, any;
+    DisPart warp[kRowWarps];
+    double cross_all[kMaxCluster];                           // (in the row's first CTA) written by the cluster's
+    double cross[kRowWarps];
+    uint64_t bar[2], part_bar, cross_bar;
+    alignas(16) unsigned wkey[kRowWarps];                    // largest key of the warp's record logits
+    alignas(16) float wsum[kRowWarps];                       // sum of its probabilities
     float m, total, rest;                                    // the row's
+    int status;
+    int id[DSPARK_MAX_TOP_LOGITS];                           // draft ids of the record, -1: none
+    unsigned seen[kRowThreads];                              // 8192 bits: hashes of the ids met
 };
+constexpr unsigned kSeenBits = 32 * kRowThreads;
 
 // log(v), v > 0 normal: the exponent's part in 64 bits, logf of what is left in [0.75, 1.5).
 __device__ __forceinline__ double log_split(float v) {
@@ -80,7 +83,7 @@ __device__ __forceinline__ double log_split(float v) {
 }
 
 template <int SX>
-__device__ __forceinline__ void store_vec(const VocabRow<SX>& g, int k, int i0, const uint4& w, bool same_phase) {
+__device__ __forceinline__ void store_vec(const VocabRow<SX>& g, int i0, const uint4& w, bool same_phase) {
     constexpr int VE = 16 / SX;
     unsigned char* p = const_cast<unsigned char*>(g.p);
     if (same_phase && i0 >= 0 && i0 + VE <= g.V) {
@@ -96,97 +99,12 @@ __device__ __forceinline__ void store_vec(const VocabRow<SX>& g, int k, int i0, 
     }
 }
 
-// The teacher's record of a row, by one warp: draft ids, probabilities and their logarithms.
-struct Record {
-    int id[kDisEntries];
-    float t[kDisEntries], lse;
-    __device__ __forceinline__ void load(const DisArgs& a, long long row);
-    __device__ __forceinline__ void take(const DisArgs& a, DisSmem& s, long long row);
-};
-__device__ __forceinline__ void Record::load(const DisArgs& a, long long row) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int q = 0; q < kDisEntries; ++q) {
-        const int e = lane + 32 * q;
-        id[q] = e < a.n ? a.ids[row * a.n + e] : -1;
-        t[q] = e < a.n ? a.tl[row * a.n + e] : 0.f;
-    }
-    lse = a.lse ? a.lse[row] : 0.f;
-}
-__device__ __forceinline__ void Record::take(const DisArgs& a, DisSmem& s, long long row) {
-    const int lane = threadIdx.x & 31;
-    int status = 0;
-    float tmax = -INFINITY;
-#pragma unroll
-    for (int q = 0; q < kDisEntries; ++q) {
-        if (id[q] < -1 || id[q] >= (a.t2d ? a.target_V : a.V)) { status = DSPARK_ROW_BAD_TEACHER; id[q] = -1; }
-        if (a.t2d && id[q] >= 0) id[q] = a.t2d[id[q]];
-    }
-    bool any = false;
-#pragma unroll
-    for (int q = 0; q < kDisEntries; ++q) {
-        if (id[q] < -1 || id[q] >= a.V || (id[q] >= 0 && !(t[q] < INFINITY))) { status = DSPARK_ROW_BAD_TEACHER; id[q] = -1; }
-        if (id[q] >= 0) {
-            any = true;
-            tmax = fmaxf(tmax, t[q]);
-        }
-    }
-    any = __any_sync(0xffffffffu, any);
-    tmax = warp_max(tmax);
-    if (!isfinite(lse) || (any && !a.lse && !(tmax > -INFINITY))) status = DSPARK_ROW_BAD_TEACHER;
-    // log p: t / T is a product with 1/T in two parts, the first one exact inside the fma
-    const float ih = static_cast<float>(a.inv_t), il = static_cast<float>(a.inv_t - static_cast<double>(ih));
-    float lp[kDisEntries], p[kDisEntries];
-    double sum = 0.0;
-#pragma unroll
-    for (int q = 0; q < kDisEntries; ++q) {
-        lp[q] = -INFINITY;
-        p[q] = 0.f;
-        if (id[q] >= 0 && t[q] > -INFINITY) {
-            lp[q] = a.lse ? fmaf(t[q], il, fmaf(t[q], ih, -lse)) : (t[q] - tmax) * ih;
-            p[q] = expf(lp[q]);
-        }
-        if (32 * q < a.n) sum += p[q];
-    }
-    sum = warp_sum_d(sum);
-    if (!(sum < INFINITY)) status = DSPARK_ROW_BAD_TEACHER;  // a log-sum-exp far below its logits
-    float psum = static_cast<float>(sum), p_r = 0.f, mass = psum;
-    if (a.lse) {
-        if (sum < 1.0) { p_r = static_cast<float>(1.0 - sum); mass = 1.f; }
-    } else if (any) {
-        const float ls = logf(psum), inv = 1.f / psum;
-#pragma unroll
-        for (int q = 0; q < kDisEntries; ++q) {
-            lp[q] -= ls;
-            p[q] *= inv;
-        }
-        psum = mass = 1.f;
-    }
-#pragma unroll
-    for (int q = 0; q < kDisEntries; ++q) {
-        const int e = lane + 32 * q;
-        if (e < a.n) {
-            s.id[e] = id[q];
-            s.p[e] = p[q];
-            s.lv[e] = lp[q];
-        }
-    }
-    status = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(status));
-    if (lane == 0) {
-        s.psum = psum;
-        s.p_r = p_r;
-        s.mass = mass;
-        s.status = status;
-        s.any = any;
-    }
-}
-
 template <int SX, int PASS>
 __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
     constexpr int VE = VocabRow<SX>::VE;
     constexpr bool kWantLoss = (PASS & kLoss) != 0, kWantGrad = (PASS & kGrad) != 0;
     __shared__ DisSmem s;
-    extern __shared__ uint4 s_x[];                           // [piece]
+    extern __shared__ uint4 s_x[];                           // [slots][piece]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = 1 << a.log_c, rank = static_cast<int>(blockIdx.x & (C - 1));
     const long long row = blockIdx.x >> a.log_c;
@@ -194,16 +112,27 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
     const VocabRow<SX> g(a.g, row, a.g_stride, a.V);
     const int k0 = x.nvec * rank >> a.log_c, k1 = x.nvec * (rank + 1) >> a.log_c;   // nvec * C < 2^31
     const bool same_phase = x.a0 == g.a0;
-    const float w = a.weights ? a.weights[row] : 1.f;
 
-    if (kWantLoss && C > 1) {                                // before a peer can push here
-        if (tid == 0) {
+    const float w = a.weights ? a.weights[row] : 1.f;
+    int id = tid < a.n ? a.ids[row * a.n + tid] : -1;
+    const float t = tid < a.n ? a.tl[row * a.n + tid] : 0.f;
+    const float lse = a.lse ? a.lse[row] : 0.f;
+    if (tid == 0) {
+        mbar_init(&s.bar[0], 1);
+        mbar_init(&s.bar[1], 1);
+        if (kWantLoss && C > 1) {
             mbar_init(&s.part_bar, 1);
-            fence_mbar_init();
-            mbar_arrive_expect_tx(&s.part_bar, kDisPartBytes * C);
+            mbar_init(&s.cross_bar, 1);
         }
-        cluster_arrive();
+        fence_mbar_init();
+        if (kWantLoss && C > 1) {
+            mbar_arrive_expect_tx(&s.part_bar, sizeof(DisPart) * C);
+            mbar_arrive_expect_tx(&s.cross_bar, sizeof(double) * C);
+        }
     }
+    s.seen[tid] = 0u;
+    if (kWantLoss && C > 1) cluster_arrive();                // before a peer can push here
+
     // a row that is not reduced: loss, status and gradient; the same branch in every CTA of the row
     auto leave = [&](int status) {
         if (kWantLoss && rank == 0 && tid == 0) {
@@ -213,154 +142,202 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
                 for (int k = 0; k < 4; ++k) a.saved_out[4 * row + k] = 0.f;
         }
         if (kWantGrad)
-            for (int k = k0 + tid; k < k1; k += kRowThreads) store_vec<SX>(g, k, x.first(k), make_uint4(0, 0, 0, 0), same_phase);
+            for (int k = k0 + tid; k < k1; k += kRowThreads) store_vec<SX>(g, x.first(k), make_uint4(0, 0, 0, 0), same_phase);
         if (kWantLoss && C > 1) cluster_wait();
     };
-    // vectors [b, e) of the row into the buffer: whole ones by a bulk copy, the row's ragged first
-    // and last by two threads of the warp that takes the members out
-    auto fetch = [&](int b, int e) {
+    // The span in np pieces; copy number f (the pieces in turn, then again for a second pass) goes to
+    // buffer f mod slots: whole vectors by a bulk copy, the row's ragged first and last by two threads.
+    const int np = (k1 - k0 + a.piece - 1) / a.piece, slots = 1 << a.log_slots;
+    auto lo = [&](int j) { return k0 + j * a.piece; };
+    auto hi = [&](int j) { return min(k1, k0 + (j + 1) * a.piece); };
+    auto buffer = [&](int f) { return s_x + (f & (slots - 1)) * a.piece; };
+    auto fetch = [&](int f) {
+        const int j = f < np ? f : f - np, b = lo(j), e = hi(j);
         const int wb = b + !x.whole(b), we = e - (e > wb && !x.whole(e - 1));
         if (tid == 0) {
+            uint64_t* const bar = &s.bar[f & (slots - 1)];
             const unsigned bytes = we > wb ? 16u * static_cast<unsigned>(we - wb) : 0u;
-            mbar_arrive_expect_tx(&s.bar, bytes);
-            if (bytes) bulk_g2s(s_x + (wb - b), x.p + static_cast<long long>(x.first(wb)) * SX, bytes, &s.bar);
+            mbar_arrive_expect_tx(bar, bytes);
+            if (bytes) bulk_g2s(buffer(f) + (wb - b), x.p + static_cast<long long>(x.first(wb)) * SX, bytes, bar);
         }
-        if (tid == 1 && wb > b) s_x[0] = load_vec<SX>(x, b, e);
-        if (tid == 2 && we < e && we >= wb) s_x[we - b] = load_vec<SX>(x, we, e);
+        if (tid == 32 && wb > b) buffer(f)[0] = load_vec<SX>(x, b, e);
+        if (tid == 64 && we < e && we >= wb) buffer(f)[we - b] = load_vec<SX>(x, we, e);
     };
-    Record rec;
-    if (warp == 0) rec.load(a, row);
     if (w == 0.f) {
         leave(0);
         return;
     }
-    if (tid == 0) {
-        mbar_init(&s.bar, 1);
-        fence_mbar_init();
+    for (int f = 0; f < min(np, slots); ++f) fetch(f);
+
+    // ---- the record, a thread to an entry
+    bool bad = id < -1 || id >= (a.t2d ? a.target_V : a.V);
+    if (bad) id = -1;
+    if (a.t2d && id >= 0) {
+        id = a.t2d[id];
+        if (id < -1 || id >= a.V) { bad = true; id = -1; }
     }
-    int b = k0, e = min(k1, k0 + a.piece);
-    unsigned parity = 0;
-    if (k0 < k1) fetch(b, e);
-    if (warp == 0) rec.take(a, s, row);
+    if (id >= 0 && !(t < INFINITY)) { bad = true; id = -1; }
+    s.id[tid] = id;
+    const unsigned key = __reduce_max_sync(0xffffffffu, id >= 0 ? fkey(t) : 0u);   // 0: no entry
+    if (lane == 0) s.wkey[warp] = key;
     __syncthreads();
+    unsigned top = 0u;
+#pragma unroll
+    for (int k = 0; k < kRowWarps; ++k) top = max(top, s.wkey[k]);
+    const float tmax = key_to_f(top);
+    float lp = -INFINITY, p = 0.f;
+    if (id >= 0) {
+        if (t > -INFINITY) {
+            // log p: t / T is a product with 1/T in two parts, the first one exact inside the fma
+            const float ih = static_cast<float>(a.inv_t), il = static_cast<float>(a.inv_t - static_cast<double>(ih));
+            lp = a.lse ? fmaf(t, il, fmaf(t, ih, -lse)) : (t - tmax) * ih;
+            p = expf(lp);
+        }
+        // a repeated id: entries whose hash was met before look for it
+        const unsigned h = (static_cast<unsigned>(id) * 2654435761u) >> 19;
+        static_assert(kSeenBits == 1u << 13, "the hash has 13 bits");
+        if (atomicOr(&s.seen[h >> 5], 1u << (h & 31)) >> (h & 31) & 1u)
+            for (int k = 0; k < a.n; ++k) bad = bad || (k != tid && s.id[k] == id);
+    }
+    // not finite, only -inf in the record, a log-sum-exp far below its logits
+    bad = bad || !isfinite(lse) || (top != 0u && !a.lse && !(tmax > -INFINITY)) || !(p < INFINITY);
+    const float ws = warp_sum(p);
+    if (lane == 0) s.wsum[warp] = ws;
+    const int status0 = __syncthreads_or(bad) ? DSPARK_ROW_BAD_TEACHER : 0;
+    float psum = 0.f, p_r = 0.f;
+#pragma unroll
+    for (int k = 0; k < kRowWarps; ++k) psum += s.wsum[k];
+    float mass = psum;                                       // sum of p, 1 - sum, their sum
+    if (a.lse) {
+        if (psum < 1.f) { p_r = 1.f - psum; mass = 1.f; }
+    } else {
+        lp -= logf(psum);
+        p *= 1.f / psum;
+        psum = mass = 1.f;
+    }
     bool late = false;
-    if (!s.any || s.status) {
-        if (warp == 0 && k0 < k1) late = !bar_wait(&s.bar, 0);
+    if (status0 || top == 0u) {
+        if (warp == 0)
+            for (int f = 0; f < min(np, slots); ++f) late = late || !bar_wait(&s.bar[f], 0);
         late = __syncthreads_or(late);
-        leave(s.status ? s.status : late ? DSPARK_ROW_INTERNAL : 0);
+        leave(status0 ? status0 : late ? DSPARK_ROW_INTERNAL : 0);
         return;
     }
-
     if (kWantLoss && C > 1) cluster_wait();                  // the peers' barriers stand
 
-    ExpSum es{-INFINITY, 0.f};
-    double cross = 0.0;
-    int status = 0;
     const double ln_c = kLn2 * a.c;                          // the sums' own 1/T: c rounds log2(e)/T to fp32
-    // One warp notes the logits of the members among the buffer's vectors [b, e) and puts -inf in
-    // their place.  A repeated id finds the mark of the first (a NaN that is cleared at the end).
-    auto take_members = [&](int b, int e) {
-        __syncwarp();
-        constexpr uint32_t kMark = SX == 2 ? 0x7FD5u : 0x7FD5AB31u;
-        using Bits = std::conditional_t<SX == 2, unsigned short, unsigned>;
-        Bits* const buf = reinterpret_cast<Bits*>(s_x);
-        const int i0 = x.first(b), i_lo = max(0, i0), i_hi = min(a.V, x.first(e));
-        for (int r0 = 0; r0 < a.n; r0 += 32) {
-            const int r = r0 + lane, id = r < a.n ? s.id[r] : -1;
-            const bool in = id >= i_lo && id < i_hi;
-            if (!__any_sync(0xffffffffu, in)) continue;
-            if (__popc(__match_any_sync(0xffffffffu, in ? id : -2 - lane)) > 1) status = DSPARK_ROW_BAD_TEACHER;
-            if (in) {
-                const uint32_t bits = buf[id - i0];
-                if (bits == kMark) status = DSPARK_ROW_BAD_TEACHER;
-                const float v = __uint_as_float(SX == 2 ? bits << 16 : bits), p = s.p[r];
-                if (p > 0.f) cross += p * (s.lv[r] - v * ln_c);
-                s.lv[r] = v;
-            }
-            __syncwarp();
-            if (in) buf[id - i0] = static_cast<Bits>(kMark);
-            __syncwarp();
+    float v = -INFINITY;                                     // this thread's member: its logit
+    bool here = false;                                       // ... is in this span
+    // Wait for copy f of piece j; its members are noted and replaced by -inf.  Ends with a barrier.
+    auto arrive = [&](int f, int j, bool note) {
+        const int i0 = x.first(lo(j));
+        const bool in = id >= max(0, i0) && id < min(a.V, x.first(hi(j)));
+        if (warp == 0 || __any_sync(0xffffffffu, in)) late = late || !bar_wait(&s.bar[f & (slots - 1)], static_cast<unsigned>(f >> a.log_slots) & 1u);
+        if (in && note) {
+            using Bits = std::conditional_t<SX == 2, unsigned short, unsigned>;
+            Bits* const at = reinterpret_cast<Bits*>(buffer(f)) + (id - i0);
+            v = __uint_as_float(static_cast<uint32_t>(*at) << (SX == 2 ? 16 : 0));
+            *at = static_cast<Bits>(ninf_bits<SX>());
+            here = true;
         }
-        for (int r = lane; r < a.n; r += 32) {
-            const int id = s.id[r];
-            if (id >= i_lo && id < i_hi) buf[id - i0] = static_cast<Bits>(ninf_bits<SX>());
-        }
+        __syncthreads();
     };
-    double row_cross = 0.0;
-    int row_status = 0;
+    // The buffer of copy f - slots is free for copy f.
+    auto refill = [&](int f) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();
+        fetch(f);
+        if (slots == 1) __syncthreads();                     // the ragged vectors are read before the next barrier
+    };
+
+    // ---- Z and R
     if (kWantLoss) {
-        while (true) {
-            if (warp == 0 && k0 < k1) {                      // the others sleep at the barrier
-                late |= !bar_wait(&s.bar, parity);
-                take_members(b, e);
-            }
-            parity ^= 1;
-            __syncthreads();
+        ExpSum es{-INFINITY, 0.f};
+        const bool twice = kWantGrad && np > 1;              // the pieces come again for the gradient
+        for (int j = 0; j < np; ++j) {
+            arrive(j, j, true);
+            const uint4* const q0 = buffer(j);
+            const int cnt = hi(j) - lo(j);
             int k = tid;
-            for (; k + (kDisVec - 1) * kRowThreads < e - b; k += kDisVec * kRowThreads) {
-                uint4 v[kDisVec];
+            for (; k + (kDisVec - 1) * kRowThreads < cnt; k += kDisVec * kRowThreads) {
+                uint4 q[kDisVec];
 #pragma unroll
-                for (int u = 0; u < kDisVec; ++u) v[u] = s_x[k + u * kRowThreads];
-                add_exps<SX>(es, v, vecs_max<SX>(v), a.c);
+                for (int u = 0; u < kDisVec; ++u) q[u] = q0[k + u * kRowThreads];
+                add_exps<SX>(es, q, vecs_max<SX>(q), a.c);
             }
-            for (; k < e - b; k += kRowThreads) {
-                const uint4 v[1] = {s_x[k]};
-                add_exps<SX>(es, v, vecs_max<SX>(v), a.c);
+            for (; k < cnt; k += kRowThreads) {
+                const uint4 q[1] = {q0[k]};
+                add_exps<SX>(es, q, vecs_max<SX>(q), a.c);
             }
-            if (e >= k1) break;
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncthreads();
-            b = e;
-            e = min(k1, b + a.piece);
-            fetch(b, e);
+            if (j + slots < (twice ? 2 * np : np)) refill(j + slots);
         }
-        es = warp_merge(es, a.c);
-        if (lane == 0) s.es[warp] = es;
-        __syncthreads();
-        if (warp == 0) {                                     // the CTA's part, to every CTA of the row
-            es = lane < kRowWarps ? s.es[lane] : ExpSum{-INFINITY, 0.f};
-            const int i_lo = max(0, x.first(k0)), i_hi = min(a.V, x.first(k1));
-            float m = es.m;
-            for (int r = lane; r < a.n; r += 32)
-                if (s.id[r] >= i_lo && s.id[r] < i_hi) m = fmaxf(m, s.lv[r]);
-            m = key_to_f(__reduce_max_sync(0xffffffffu, fkey(m)));
-            const ExpRef ref(m > -INFINITY ? m : 0.f, a.c);
-            float in = 0.f;
-            for (int r = lane; r < a.n; r += 32)
-                if (s.id[r] >= i_lo && s.id[r] < i_hi) in += ref.of(s.lv[r]);   // NaN for NaN and +inf
-            in = warp_sum(in);
+        // the warp's part, then the CTA's to every CTA of the row, then the row's
+        const bool mine = __any_sync(0xffffffffu, here);
+        {
+            // a member that is NaN is left out of the maximum and shows in the sum
+            const float m = key_to_f(__reduce_max_sync(0xffffffffu, max(fkey(es.m), v == v ? fkey(v) : 0u)));
             const float rest = warp_sum(m > -INFINITY ? es.sum * rebase(es.m, m, a.c) : es.sum);
-            cross = warp_sum_d(cross);
-            status = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(status));
-            if (late) status |= DSPARK_ROW_INTERNAL;
-            if (C > 1) {
-                if (lane < C) {
-                    const unsigned to = peer_addr(&s.all[rank], lane), bar = peer_addr(&s.part_bar, lane);
-                    peer_push128(to, bar, __float_as_uint(m), __float_as_uint(rest), __float_as_uint(in), static_cast<uint32_t>(status));
-                    peer_push64(to + 16, bar, static_cast<unsigned long long>(__double_as_longlong(cross)));
-                }
-                late = !bar_wait(&s.part_bar, 0);
-            } else if (lane == 0) {
-                s.all[0] = DisPart{m, rest, in, status, cross, 0.0};
-            }
-            __syncwarp();
-            // the row: every CTA joins the C parts alike
-            DisPart o{-INFINITY, 0.f, 0.f, 0, 0.0, 0.0};
-            if (lane < C) o = s.all[lane];
-            m = key_to_f(__reduce_max_sync(0xffffffffu, fkey(o.m)));
+            float in = 0.f;
+            if (mine) in = warp_sum(here ? ExpRef(m > -INFINITY ? m : 0.f, a.c).of(v) : 0.f);   // NaN for NaN and +inf
+            if (lane == 0) s.warp[warp] = DisPart{m, rest, in, late ? DSPARK_ROW_INTERNAL : 0};
+        }
+        __syncthreads();
+        auto join = [&](const DisPart* parts, int count) {   // by one warp, in lane order
+            DisPart o{-INFINITY, 0.f, 0.f, 0};
+            if (lane < count) o = parts[lane];
+            const float m = key_to_f(__reduce_max_sync(0xffffffffu, fkey(o.m)));
             const float f = m > -INFINITY ? rebase(o.m, m, a.c) : 1.f;
-            const float rest_r = warp_sum(lane < C ? o.rest * f : 0.f), total = rest_r + warp_sum(lane < C ? o.in * f : 0.f);
-            row_status = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(o.status));
-            if (late) row_status |= DSPARK_ROW_INTERNAL;
-            if (!row_status && !(total == total && m > -INFINITY)) row_status = DSPARK_ROW_NONFINITE;
-            row_cross = o.cross;
+            o.rest = lane < count ? o.rest * f : 0.f;
+            o.in = lane < count ? o.in * f : 0.f;
+#pragma unroll
+            for (int i = kMaxCluster / 2; i; i >>= 1) {
+                o.rest += __shfl_xor_sync(0xffffffffu, o.rest, i);
+                o.in += __shfl_xor_sync(0xffffffffu, o.in, i);
+            }
+            o.m = m;
+            o.status = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(o.status));
+            return o;
+        };
+        static_assert(kRowWarps <= kMaxCluster, "join adds over kMaxCluster lanes");
+        DisPart o;
+        if (warp == 0) {
+            o = join(s.warp, kRowWarps);
+            if (C > 1 && lane < C)
+                peer_push128(peer_addr(&s.all[rank], lane), peer_addr(&s.part_bar, lane), __float_as_uint(o.m), __float_as_uint(o.rest),
+                             __float_as_uint(o.in), static_cast<uint32_t>(o.status));
+        }
+        // meanwhile sum p_i (log p_i - log e_i)
+        double cross = 0.0;
+        if (mine) {
+            if (here && p > 0.f) cross = p * (lp - v * ln_c);
+            cross = warp_sum_d(cross);
+        }
+        if (lane == 0) s.cross[warp] = cross;
+        if (warp == 0) {
+            if (C > 1) {
+                late = !bar_wait(&s.part_bar, 0);
+                o = join(s.all, C);
+            }
+            int status = o.status | (late ? DSPARK_ROW_INTERNAL : 0);
+            const float total = o.rest + o.in;
+            if (!status && !(total == total && o.m > -INFINITY)) status = DSPARK_ROW_NONFINITE;
             if (lane == 0) {
-                s.m = m;
-                s.total = row_status ? NAN : total;
-                s.rest = rest_r;
+                s.m = o.m;
+                s.total = status ? NAN : total;
+                s.rest = o.rest;
+                s.status = status;
             }
         }
         __syncthreads();
+        if (warp == 0) {                                     // the CTA's part of the sum to the row's first
+            cross = lane < kRowWarps ? s.cross[lane] : 0.0;
+#pragma unroll
+            for (int i = kRowWarps / 2; i; i >>= 1) cross += __shfl_xor_sync(0xffffffffu, cross, i);
+            if (lane == 0) {
+                if (C > 1) peer_push64(peer_addr(&s.cross_all[rank], 0), peer_addr(&s.cross_bar, 0), static_cast<unsigned long long>(__double_as_longlong(cross)));
+                else s.cross_all[0] = cross;
+            }
+        }
     }
 
     // ---- the gradient
@@ -369,84 +346,61 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
         const float rest = kWantLoss ? s.rest : a.saved[4 * row + 2];
         const bool ok = total > 0.f && m > -INFINITY;        // total is NaN for a row that cannot be normalised
         const float wt = (a.up ? w * a.up[row] : w) * static_cast<float>(a.inv_t);
-        const float scale_in = wt * (s.mass / total);
+        const float scale_in = wt * (mass / total);
         // (M R - p_r Z) / (Z R): the two products cancel where the student's tail is nearly right
-        float scale_out = scale_in;
-        if (s.p_r > 0.f && rest > 0.f) {
-            const float z = s.p_r * total, ze = fmaf(s.p_r, total, -z);
-            scale_out = wt * (((fmaf(s.mass, rest, -z) - ze) / rest) / total);
+        float scale = scale_in;
+        if (p_r > 0.f && rest > 0.f) {
+            const float z = p_r * total, ze = fmaf(p_r, total, -z);
+            scale = wt * (((fmaf(mass, rest, -z) - ze) / rest) / total);
         }
         const ExpRef ref(m, a.c);
-        // with a loss the last piece is in the buffer; the others, if any, come again
-        const bool kept = kWantLoss && e - b == k1 - k0;
-        if (kWantLoss && !kept) {
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncthreads();
-            b = k0;
-            e = min(k1, k0 + a.piece);
-            if (k0 < k1) fetch(b, e);
-        }
-        bool lost = false;
-        while (true) {
-            if (!kept) {
-                if (warp == 0 && k0 < k1) {
-                    lost |= !bar_wait(&s.bar, parity);
-                    if (!kWantLoss) take_members(b, e);
-                }
-                parity ^= 1;
-                lost = __syncthreads_or(lost);
-            }
-            for (int k = b + tid; k < e; k += kRowThreads) {
-                const uint4 v = s_x[k - b];
-                uint4 o = make_uint4(0, 0, 0, 0);
-                if (ok && !lost) {
-                    float f[VE];
-                    if (ref.whole) {
-                        const unsigned long long c2 = pack2(a.c, a.c), r2 = pack2(-ref.r, -ref.r), s2 = pack2(scale_out, scale_out);
+        const unsigned long long c2 = pack2(a.c, a.c), r2 = pack2(-ref.r, -ref.r), s2 = pack2(scale, scale);
+        auto grad_of = [&](const uint4& q) {
+            float f[VE];
+            if (ref.whole) {
 #pragma unroll
-                        for (int h = 0; h < VE / 2; ++h) {
-                            float lo, hi;
-                            unpack2(fma2(pair_of<SX>(v, h), c2, r2), lo, hi);
-                            unpack2(mul2(pack2(ex2_approx(lo), ex2_approx(hi)), s2), f[2 * h], f[2 * h + 1]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < VE; ++q) f[q] = ref.of(elem<SX>(v, q)) * scale_out;
-                    }
-                    if (SX == 2) o = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4 % VE], f[5 % VE]), pack_bf16(f[6 % VE], f[7 % VE]));
-                    else o = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+                for (int h = 0; h < VE / 2; ++h) {
+                    float lo, hi;
+                    unpack2(fma2(pair_of<SX>(q, h), c2, r2), lo, hi);
+                    unpack2(mul2(pack2(ex2_approx(lo), ex2_approx(hi)), s2), f[2 * h], f[2 * h + 1]);
                 }
-                store_vec<SX>(g, k, x.first(k), o, same_phase);
+            } else {
+#pragma unroll
+                for (int h = 0; h < VE; ++h) f[h] = ref.of(elem<SX>(q, h)) * scale;
             }
-            if (kept || e >= k1) break;
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncthreads();
-            b = e;
-            e = min(k1, b + a.piece);
-            fetch(b, e);
+            if (SX == 2) return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4 % VE], f[5 % VE]), pack_bf16(f[6 % VE], f[7 % VE]));
+            return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+        };
+        // one piece is still in its buffer from the sum
+        for (int j = 0; j < np; ++j) {
+            const int f = kWantLoss ? np + j : j;
+            if (!kWantLoss || np > 1) arrive(f, j, !kWantLoss);
+            const uint4* const q0 = buffer(kWantLoss && np == 1 ? 0 : f);
+            const int b = lo(j), cnt = hi(j) - b;
+            for (int k = tid; k < cnt; k += kRowThreads)
+                store_vec<SX>(g, x.first(b + k), ok ? grad_of(q0[k]) : make_uint4(0, 0, 0, 0), same_phase);
+            if (j + slots < np) refill(f + slots);
         }
         __syncthreads();                                     // the members' gradients go over the span's
-        if (warp == 0 && ok && !lost) {
-            const int i_lo = max(0, x.first(k0)), i_hi = min(a.V, x.first(k1));
-            for (int r = lane; r < a.n; r += 32) {
-                const int id = s.id[r];
-                if (id < i_lo || id >= i_hi) continue;
-                const float v = fmaf(-s.p[r], wt, ref.of(s.lv[r]) * scale_in);
-                unsigned char* p = const_cast<unsigned char*>(g.p);
-                if (SX == 2) reinterpret_cast<unsigned short*>(p)[id] = static_cast<unsigned short>(to_bits<SX>(v));
-                else reinterpret_cast<float*>(p)[id] = v;
-            }
+        if (here && ok) {
+            const float d = fmaf(-p, wt, ref.of(v) * scale_in);
+            unsigned char* const gp = const_cast<unsigned char*>(g.p);
+            if (SX == 2) reinterpret_cast<unsigned short*>(gp)[id] = static_cast<unsigned short>(to_bits<SX>(d));
+            else reinterpret_cast<float*>(gp)[id] = d;
         }
     }
-    if (kWantLoss && rank == 0 && warp == 0) {               // the loss, off the gradient's path
-        row_cross = warp_sum_d(lane < C ? row_cross : 0.0);
+    if (kWantLoss && rank == 0 && warp == 0) {               // the loss
+        if (C > 1) late = late || !bar_wait(&s.cross_bar, 0);
+        __syncwarp();
         if (lane == 0) {
             const float m = s.m, total = s.total, rest = s.rest;
+            const int status = s.status | (late ? DSPARK_ROW_INTERNAL : 0);
             const ExpRef ref(m, a.c);
-            double loss = row_cross + s.psum * ((ref.whole ? kLn2 * ref.r : m * ln_c) + log_split(total));
-            if (s.p_r > 0.f && rest > 0.f) loss += s.p_r * logf(s.p_r * (total / rest));
-            a.loss[row] = row_status ? NAN : static_cast<float>(w * loss);
-            a.row_status[row] = row_status;
+            double loss = psum * ((ref.whole ? kLn2 * ref.r : m * ln_c) + log_split(total));
+            for (int k = 0; k < C; ++k) loss += s.cross_all[k];
+            if (p_r > 0.f && rest > 0.f) loss += p_r * logf(p_r * (total / rest));
+            a.loss[row] = status ? NAN : static_cast<float>(w * loss);
+            a.row_status[row] = status;
             if (a.saved_out) {
                 a.saved_out[4 * row] = m;
                 a.saved_out[4 * row + 1] = total;
@@ -459,7 +413,7 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
 
 // Checks shared by the two entry points; on success *a and *sx are set.
 dspark_status_t distill_args(const void* student, const dspark_teacher_t* t, const dspark_distill_params_t* p, const void* grad,
-                             DisArgs* a, int* sx) {
+                             bool both, DisArgs* a, int* sx) {
     if (!student || !t || !p || !t->ids || !t->logits) return DSPARK_ERR_INVALID_ARG;
     if (p->n_rows < 1 || p->n_rows > DSPARK_MAX_ROWS || p->V < 1 || p->V > DSPARK_MAX_V) return DSPARK_ERR_INVALID_ARG;
     if (t->n < 1 || t->n > DSPARK_MAX_TOP_LOGITS) return DSPARK_ERR_INVALID_ARG;
@@ -478,29 +432,32 @@ dspark_status_t distill_args(const void* student, const dspark_teacher_t* t, con
     a->g_stride = grad ? p->grad_stride : p->student_stride;
     a->ids = t->ids; a->tl = t->logits; a->lse = t->lse; a->t2d = t->t2d;
     a->weights = p->weights; a->row_status = p->row_status;
-    // CTAs per row: spans of at most 72 KB (three CTAs to an SM), and smaller ones while the rows alone
-    // do not make two CTAs per SM.  2048 rows of 64 KB, loss then gradient: 114 us whole, 139 us in
-    // halves, 227 us in quarters: a CTA's latencies cost more than its share of the row.
+    // CTAs per row.  For both results at once spans of at most 72 KB, each kept in one piece; for one of
+    // them a span streams through two buffers and may be as long as the row: a CTA's latencies cost
+    // about what 40 KB do (2048 rows of 304 KB, loss alone: 101 us whole, 138 us in quarters, 198 us
+    // in eighths).  Smaller spans while the rows alone do not make two CTAs per SM.
     const int nvec = max_vectors(p->V, *sx);
     int cluster = 1;
-    while (cluster < kMaxCluster && (nvec > cluster * kDisSpan ||
-                                        (nvec >= cluster * 512 && static_cast<long long>(p->n_rows) * cluster < 304)))
+    while (cluster < kMaxCluster && ((both && nvec > cluster * kDisSpan) ||
+                                     (nvec >= cluster * 512 && static_cast<long long>(p->n_rows) * cluster < 304)))
         cluster *= 2;
     for (a->log_c = 0; (1 << a->log_c) < cluster;) ++a->log_c;
-    // a longer span comes in pieces of 40 KB
     a->piece = nvec / cluster + 1;
-    if (a->piece > kDisSpan) a->piece = kDisPiece;
+    if (a->piece > (both ? kDisSpan : kDisPiece)) {
+        a->piece = kDisPiece;
+        a->log_slots = 1;
+    }
     return DSPARK_OK;
 }
 
 template <int SX, int PASS>
 dspark_status_t distill_launch(const DisArgs& a, int rows, void* stream) {
-    const size_t smem = static_cast<size_t>(a.piece) * 16;
+    const size_t smem = static_cast<size_t>(a.piece) * 16 << a.log_slots;
     if (smem > 32 * 1024 &&                                  // beyond what a launch gets unasked
         cudaFuncSetAttribute(distill_kernel<SX, PASS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return DSPARK_ERR_CUDA;
     const unsigned grid = static_cast<unsigned>(rows) << a.log_c;
-    const cudaError_t e = launch_cluster(distill_kernel<SX, PASS>, grid, 1 << a.log_c, smem, static_cast<cudaStream_t>(stream), a);
+    const cudaError_t e = launch_cluster(distill_kernel<SX, PASS>, grid, kRowThreads, 1 << a.log_c, smem, static_cast<cudaStream_t>(stream), a);
     return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
@@ -515,7 +472,7 @@ dspark_status_t dspark_distill(const void* student, const dspark_teacher_t* teac
                                float* out_loss, float* out_saved, void* out_grad) {
     DisArgs a{};
     int sx = 0;
-    if (const dspark_status_t st = distill_args(student, teacher, params, out_grad, &a, &sx); st != DSPARK_OK) return st;
+    if (const dspark_status_t st = distill_args(student, teacher, params, out_grad, out_grad != nullptr, &a, &sx); st != DSPARK_OK) return st;
     if (!out_loss || !params->row_status) return DSPARK_ERR_INVALID_ARG;
     a.loss = out_loss;
     a.saved_out = out_saved;
@@ -532,7 +489,7 @@ dspark_status_t dspark_distill_backward(const void* student, const dspark_teache
     DisArgs a{};
     int sx = 0;
     if (!out_grad || !saved) return DSPARK_ERR_INVALID_ARG;
-    if (const dspark_status_t st = distill_args(student, teacher, params, out_grad, &a, &sx); st != DSPARK_OK) return st;
+    if (const dspark_status_t st = distill_args(student, teacher, params, out_grad, false, &a, &sx); st != DSPARK_OK) return st;
     a.saved = saved;
     a.up = grad_loss;
     return sx == 2 ? distill_launch<2, kGrad>(a, params->n_rows, params->stream)

@@ -370,7 +370,7 @@ extern "C" dspark_status_t dspark_top_logits(const void* logits, const dspark_to
         a.cluster *= 2;
     const unsigned grid = static_cast<unsigned>(p->n_rows) * static_cast<unsigned>(a.cluster);
     cudaStream_t s = static_cast<cudaStream_t>(p->stream);
-    const cudaError_t e = sx == 2 ? launch_cluster(top_logits_kernel<2>, grid, a.cluster, 0, s, a)
-                                  : launch_cluster(top_logits_kernel<4>, grid, a.cluster, 0, s, a);
+    const cudaError_t e = sx == 2 ? launch_cluster(top_logits_kernel<2>, grid, kRowThreads, a.cluster, 0, s, a)
+                                  : launch_cluster(top_logits_kernel<4>, grid, kRowThreads, a.cluster, 0, s, a);
     return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }

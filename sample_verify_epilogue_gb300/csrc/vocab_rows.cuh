@@ -277,17 +277,28 @@ __device__ __forceinline__ unsigned long long global_timer() {
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
     return t;
 }
+// Whether an mbarrier's phase is over; what the cluster's CTAs pushed is visible then.
+__device__ __forceinline__ bool bar_test(uint64_t* bar, unsigned parity) {
+    unsigned ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
 // Wait for an mbarrier's phase with a 2 s bound, false when it runs out; data pushed by the
-// cluster's CTAs is visible afterwards.
+// cluster's CTAs is visible afterwards.  The thread sleeps up to 1 ms at a time: without the
+// hint a waiting warp polls, and takes issue slots from those that work.
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, unsigned parity) {
     unsigned long long t0 = 0;
     for (unsigned i = 0;; ++i) {
         unsigned ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+            : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u) : "memory");
         if (ok) return true;
         const unsigned long long t = global_timer();
         if (i == 0) t0 = t;
@@ -295,13 +306,13 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, unsigned parity) {
     }
 }
 
-// Launch `grid` CTAs in clusters of `cluster` (1: no cluster).
+// Launch `grid` CTAs of `threads` threads in clusters of `cluster`.
 template <typename... KArgs, typename... Args2>
-inline cudaError_t launch_cluster(void (*kern)(KArgs...), unsigned grid, int cluster, size_t smem, cudaStream_t s,
+inline cudaError_t launch_cluster(void (*kern)(KArgs...), unsigned grid, int threads, int cluster, size_t smem, cudaStream_t s,
                                   Args2&&... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kRowThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -312,6 +323,24 @@ inline cudaError_t launch_cluster(void (*kern)(KArgs...), unsigned grid, int clu
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, std::forward<Args2>(args)...);
+}
+
+// Clusters of such CTAs the device holds at a time, 0 on an error.
+template <typename... KArgs>
+inline int resident_clusters(void (*kern)(KArgs...), int threads, int cluster, size_t smem) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(64u * static_cast<unsigned>(cluster));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess ? n : 0;
 }
 
 }  // namespace dspark
