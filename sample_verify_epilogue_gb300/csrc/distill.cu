@@ -38,7 +38,7 @@ enum DistillPass : int { kLoss = 1, kGrad = 2 };
 
 struct DisArgs {
     int V, n, log_c, target_V;                               // log_c: of the cluster's size
-    int piece, log_slots;                                    // vectors of a piece; buffers for one (1 or 2)
+    int piece, np, log_slots;                                // vectors of a piece, pieces of a span; buffers (1 or 2)
     float c;                                                 // log2(e) / T
     double inv_t;
     long long s_stride, g_stride;
@@ -70,6 +70,7 @@ struct __align__(16) DisSmem {
     alignas(16) unsigned wkey[kRowWarps];                    // largest key of the warp's record logits
     alignas(16) float wsum[kRowWarps];                       // sum of its probabilities
     float m, total, rest;                                    // the row's
+    float wt, scale_in, scale_out;
     int status;
     int id[DSPARK_MAX_TOP_LOGITS];                           // draft ids of the record, -1: none
     unsigned seen[kRowThreads];                              // 8192 bits: hashes of the ids met
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
         }
     }
     s.seen[tid] = 0u;
-    if (kWantLoss && C > 1) cluster_arrive();                // before a peer can push here
+    if (kWantLoss && C > 1) cluster_arrive_relaxed();        // before a peer can push here (the fence above orders it)
 
     // a row that is not reduced: loss, status and gradient; the same branch in every CTA of the row
     auto leave = [&](int status) {
@@ -145,74 +146,82 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
             for (int k = k0 + tid; k < k1; k += kRowThreads) store_vec<SX>(g, x.first(k), make_uint4(0, 0, 0, 0), same_phase);
         if (kWantLoss && C > 1) cluster_wait();
     };
-    // The span in np pieces; copy number f (the pieces in turn, then again for a second pass) goes to
-    // buffer f mod slots: whole vectors by a bulk copy, the row's ragged first and last by two threads.
-    const int np = (k1 - k0 + a.piece - 1) / a.piece, slots = 1 << a.log_slots;
-    auto lo = [&](int j) { return k0 + j * a.piece; };
+    // The span in np pieces (the last may be short, or empty); copy number f (the pieces in turn, then
+    // again for a second pass) goes to buffer f mod slots.  Warp 0 fetches: whole vectors by a bulk
+    // copy, the row's ragged first and last by two lanes.
+    const int np = a.np, slots = 1 << a.log_slots;
+    auto lo = [&](int j) { return min(k1, k0 + j * a.piece); };
     auto hi = [&](int j) { return min(k1, k0 + (j + 1) * a.piece); };
     auto buffer = [&](int f) { return s_x + (f & (slots - 1)) * a.piece; };
     auto fetch = [&](int f) {
         const int j = f < np ? f : f - np, b = lo(j), e = hi(j);
-        const int wb = b + !x.whole(b), we = e - (e > wb && !x.whole(e - 1));
-        if (tid == 0) {
+        const int wb = b + (e > b && !x.whole(b)), we = e - (e > wb && !x.whole(e - 1));
+        if (lane == 0) {
             uint64_t* const bar = &s.bar[f & (slots - 1)];
             const unsigned bytes = we > wb ? 16u * static_cast<unsigned>(we - wb) : 0u;
             mbar_arrive_expect_tx(bar, bytes);
             if (bytes) bulk_g2s(buffer(f) + (wb - b), x.p + static_cast<long long>(x.first(wb)) * SX, bytes, bar);
         }
-        if (tid == 32 && wb > b) buffer(f)[0] = load_vec<SX>(x, b, e);
-        if (tid == 64 && we < e && we >= wb) buffer(f)[we - b] = load_vec<SX>(x, we, e);
+        if (lane == 1 && wb > b) buffer(f)[0] = load_vec<SX>(x, b, e);
+        if (lane == 2 && we < e && we >= wb) buffer(f)[we - b] = load_vec<SX>(x, we, e);
     };
     if (w == 0.f) {
         leave(0);
         return;
     }
-    for (int f = 0; f < min(np, slots); ++f) fetch(f);
+    if (warp == 0)
+        for (int f = 0; f < min(np, slots); ++f) fetch(f);
 
-    // ---- the record, a thread to an entry
-    bool bad = id < -1 || id >= (a.t2d ? a.target_V : a.V);
-    if (bad) id = -1;
-    if (a.t2d && id >= 0) {
-        id = a.t2d[id];
-        if (id < -1 || id >= a.V) { bad = true; id = -1; }
+    // ---- the record, a thread to an entry; warps past it have nothing to do
+    const bool entries = 32 * warp < a.n;
+    const int n_warps = (a.n + 31) >> 5;
+    bool bad = !isfinite(lse);
+    if (entries) {
+        if (id < -1 || id >= (a.t2d ? a.target_V : a.V)) { bad = true; id = -1; }
+        if (a.t2d && id >= 0) {
+            id = a.t2d[id];
+            if (id < -1 || id >= a.V) { bad = true; id = -1; }
+        }
+        if (id >= 0 && !(t < INFINITY)) { bad = true; id = -1; }
+        s.id[tid] = id;
+        const unsigned key = __reduce_max_sync(0xffffffffu, id >= 0 ? fkey(t) : 0u);   // 0: no entry
+        if (lane == 0) s.wkey[warp] = key;
     }
-    if (id >= 0 && !(t < INFINITY)) { bad = true; id = -1; }
-    s.id[tid] = id;
-    const unsigned key = __reduce_max_sync(0xffffffffu, id >= 0 ? fkey(t) : 0u);   // 0: no entry
-    if (lane == 0) s.wkey[warp] = key;
     __syncthreads();
     unsigned top = 0u;
-#pragma unroll
-    for (int k = 0; k < kRowWarps; ++k) top = max(top, s.wkey[k]);
-    const float tmax = key_to_f(top);
+    for (int k = 0; k < n_warps; ++k) top = max(top, s.wkey[k]);
     float lp = -INFINITY, p = 0.f;
-    if (id >= 0) {
-        if (t > -INFINITY) {
-            // log p: t / T is a product with 1/T in two parts, the first one exact inside the fma
-            const float ih = static_cast<float>(a.inv_t), il = static_cast<float>(a.inv_t - static_cast<double>(ih));
-            lp = a.lse ? fmaf(t, il, fmaf(t, ih, -lse)) : (t - tmax) * ih;
-            p = expf(lp);
+    if (entries) {
+        const float tmax = key_to_f(top);
+        if (id >= 0) {
+            if (t > -INFINITY) {
+                // log p: t / T is a product with 1/T in two parts, the first one exact inside the fma
+                const float ih = static_cast<float>(a.inv_t), il = static_cast<float>(a.inv_t - static_cast<double>(ih));
+                lp = a.lse ? fmaf(t, il, fmaf(t, ih, -lse)) : (t - tmax) * ih;
+                p = expf(lp);
+            }
+            // a repeated id: entries whose hash was met before look for it
+            const unsigned h = (static_cast<unsigned>(id) * 2654435761u) >> 19;
+            static_assert(kSeenBits == 1u << 13, "the hash has 13 bits");
+            if (atomicOr(&s.seen[h >> 5], 1u << (h & 31)) >> (h & 31) & 1u)
+                for (int k = 0; k < a.n; ++k) bad = bad || (k != tid && s.id[k] == id);
         }
-        // a repeated id: entries whose hash was met before look for it
-        const unsigned h = (static_cast<unsigned>(id) * 2654435761u) >> 19;
-        static_assert(kSeenBits == 1u << 13, "the hash has 13 bits");
-        if (atomicOr(&s.seen[h >> 5], 1u << (h & 31)) >> (h & 31) & 1u)
-            for (int k = 0; k < a.n; ++k) bad = bad || (k != tid && s.id[k] == id);
+        // only -inf in the record, a log-sum-exp far below its logits
+        bad = bad || (top != 0u && !a.lse && !(tmax > -INFINITY)) || !(p < INFINITY);
+        const float ws = warp_sum(p);
+        if (lane == 0) s.wsum[warp] = ws;
     }
-    // not finite, only -inf in the record, a log-sum-exp far below its logits
-    bad = bad || !isfinite(lse) || (top != 0u && !a.lse && !(tmax > -INFINITY)) || !(p < INFINITY);
-    const float ws = warp_sum(p);
-    if (lane == 0) s.wsum[warp] = ws;
     const int status0 = __syncthreads_or(bad) ? DSPARK_ROW_BAD_TEACHER : 0;
     float psum = 0.f, p_r = 0.f;
-#pragma unroll
-    for (int k = 0; k < kRowWarps; ++k) psum += s.wsum[k];
+    for (int k = 0; k < n_warps; ++k) psum += s.wsum[k];
     float mass = psum;                                       // sum of p, 1 - sum, their sum
     if (a.lse) {
         if (psum < 1.f) { p_r = 1.f - psum; mass = 1.f; }
     } else {
-        lp -= logf(psum);
-        p *= 1.f / psum;
+        if (entries) {
+            lp -= logf(psum);
+            p *= 1.f / psum;
+        }
         psum = mass = 1.f;
     }
     bool late = false;
@@ -230,29 +239,43 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
     bool here = false;                                       // ... is in this span
     // Wait for copy f of piece j; its members are noted and replaced by -inf.  Ends with a barrier.
     auto arrive = [&](int f, int j, bool note) {
-        const int i0 = x.first(lo(j));
-        const bool in = id >= max(0, i0) && id < min(a.V, x.first(hi(j)));
-        if (warp == 0 || __any_sync(0xffffffffu, in)) late = late || !bar_wait(&s.bar[f & (slots - 1)], static_cast<unsigned>(f >> a.log_slots) & 1u);
-        if (in && note) {
-            using Bits = std::conditional_t<SX == 2, unsigned short, unsigned>;
-            Bits* const at = reinterpret_cast<Bits*>(buffer(f)) + (id - i0);
-            v = __uint_as_float(static_cast<uint32_t>(*at) << (SX == 2 ? 16 : 0));
-            *at = static_cast<Bits>(ninf_bits<SX>());
-            here = true;
+        if (entries) {
+            const int i0 = x.first(lo(j));
+            const bool in = id >= max(0, i0) && id < min(a.V, x.first(hi(j)));
+            if (warp == 0 || __any_sync(0xffffffffu, in)) late = late || !bar_wait(&s.bar[f & (slots - 1)], static_cast<unsigned>(f >> a.log_slots) & 1u);
+            if (in && note) {
+                using Bits = std::conditional_t<SX == 2, unsigned short, unsigned>;
+                Bits* const at = reinterpret_cast<Bits*>(buffer(f)) + (id - i0);
+                v = __uint_as_float(static_cast<uint32_t>(*at) << (SX == 2 ? 16 : 0));
+                *at = static_cast<Bits>(ninf_bits<SX>());
+                here = true;
+            }
         }
         __syncthreads();
     };
-    // The buffer of copy f - slots is free for copy f.
+    // The buffer of copy f - slots is free for copy f (entry warps have written to it).
     auto refill = [&](int f) {
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (entries) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncthreads();
-        fetch(f);
+        if (warp == 0) fetch(f);
         if (slots == 1) __syncthreads();                     // the ragged vectors are read before the next barrier
+    };
+
+    // what the gradient is made with, by one thread
+    auto scales = [&](float total, float rest) {
+        const float wt = (a.up ? w * a.up[row] : w) * static_cast<float>(a.inv_t), in = wt * (mass / total);
+        s.wt = wt;
+        s.scale_in = s.scale_out = in;
+        // (M R - p_r Z) / (Z R): the two products cancel where the student's tail is nearly right
+        if (p_r > 0.f && rest > 0.f) {
+            const float z = p_r * total, ze = fmaf(p_r, total, -z);
+            s.scale_out = wt * (((fmaf(mass, rest, -z) - ze) / rest) / total);
+        }
     };
 
     // ---- Z and R
     if (kWantLoss) {
-        ExpSum es{-INFINITY, 0.f};
+        RunSum run;
         const bool twice = kWantGrad && np > 1;              // the pieces come again for the gradient
         for (int j = 0; j < np; ++j) {
             arrive(j, j, true);
@@ -263,16 +286,17 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
                 uint4 q[kDisVec];
 #pragma unroll
                 for (int u = 0; u < kDisVec; ++u) q[u] = q0[k + u * kRowThreads];
-                add_exps<SX>(es, q, vecs_max<SX>(q), a.c);
+                add_exps<SX>(run, q, vecs_max<SX>(q), a.c);
             }
             for (; k < cnt; k += kRowThreads) {
                 const uint4 q[1] = {q0[k]};
-                add_exps<SX>(es, q, vecs_max<SX>(q), a.c);
+                add_exps<SX>(run, q, vecs_max<SX>(q), a.c);
             }
             if (j + slots < (twice ? 2 * np : np)) refill(j + slots);
         }
+        const ExpSum es = run.get();
         // the warp's part, then the CTA's to every CTA of the row, then the row's
-        const bool mine = __any_sync(0xffffffffu, here);
+        const bool mine = entries && __any_sync(0xffffffffu, here);
         {
             // a member that is NaN is left out of the maximum and shows in the sum
             const float m = key_to_f(__reduce_max_sync(0xffffffffu, max(fkey(es.m), v == v ? fkey(v) : 0u)));
@@ -326,6 +350,7 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
                 s.total = status ? NAN : total;
                 s.rest = o.rest;
                 s.status = status;
+                if (kWantGrad) scales(total, o.rest);
             }
         }
         __syncthreads();
@@ -343,33 +368,33 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
     // ---- the gradient
     if (kWantGrad) {
         const float m = kWantLoss ? s.m : a.saved[4 * row], total = kWantLoss ? s.total : a.saved[4 * row + 1];
-        const float rest = kWantLoss ? s.rest : a.saved[4 * row + 2];
         const bool ok = total > 0.f && m > -INFINITY;        // total is NaN for a row that cannot be normalised
-        const float wt = (a.up ? w * a.up[row] : w) * static_cast<float>(a.inv_t);
-        const float scale_in = wt * (mass / total);
-        // (M R - p_r Z) / (Z R): the two products cancel where the student's tail is nearly right
-        float scale = scale_in;
-        if (p_r > 0.f && rest > 0.f) {
-            const float z = p_r * total, ze = fmaf(p_r, total, -z);
-            scale = wt * (((fmaf(mass, rest, -z) - ze) / rest) / total);
+        if (!kWantLoss) {
+            if (tid == 0) scales(total, a.saved[4 * row + 2]);
+            __syncthreads();
         }
+        const float scale = s.scale_out;
         const ExpRef ref(m, a.c);
         const unsigned long long c2 = pack2(a.c, a.c), r2 = pack2(-ref.r, -ref.r), s2 = pack2(scale, scale);
-        auto grad_of = [&](const uint4& q) {
-            float f[VE];
-            if (ref.whole) {
-#pragma unroll
-                for (int h = 0; h < VE / 2; ++h) {
-                    float lo, hi;
-                    unpack2(fma2(pair_of<SX>(q, h), c2, r2), lo, hi);
-                    unpack2(mul2(pack2(ex2_approx(lo), ex2_approx(hi)), s2), f[2 * h], f[2 * h + 1]);
-                }
-            } else {
-#pragma unroll
-                for (int h = 0; h < VE; ++h) f[h] = ref.of(elem<SX>(q, h)) * scale;
-            }
+        auto pack = [&](const float (&f)[VE]) {
             if (SX == 2) return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4 % VE], f[5 % VE]), pack_bf16(f[6 % VE], f[7 % VE]));
             return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+        };
+        auto grad_whole = [&](const uint4& q) {
+            float f[VE];
+#pragma unroll
+            for (int h = 0; h < VE / 2; ++h) {
+                float lo, hi;
+                unpack2(fma2(pair_of<SX>(q, h), c2, r2), lo, hi);
+                unpack2(mul2(pack2(ex2_approx(lo), ex2_approx(hi)), s2), f[2 * h], f[2 * h + 1]);
+            }
+            return pack(f);
+        };
+        auto grad_far = [&](const uint4& q) {                // logits of the type's lowest values
+            float f[VE];
+#pragma unroll
+            for (int h = 0; h < VE; ++h) f[h] = ref.of(elem<SX>(q, h)) * scale;
+            return pack(f);
         };
         // one piece is still in its buffer from the sum
         for (int j = 0; j < np; ++j) {
@@ -377,13 +402,31 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
             if (!kWantLoss || np > 1) arrive(f, j, !kWantLoss);
             const uint4* const q0 = buffer(kWantLoss && np == 1 ? 0 : f);
             const int b = lo(j), cnt = hi(j) - b;
-            for (int k = tid; k < cnt; k += kRowThreads)
-                store_vec<SX>(g, x.first(b + k), ok ? grad_of(q0[k]) : make_uint4(0, 0, 0, 0), same_phase);
+            // whole vectors of rows that lie alike go straight through
+            int w0 = 0, w1 = 0;
+            if (ok && ref.whole && same_phase) {
+                w0 = !x.whole(b);
+                w1 = cnt - (cnt > w0 && !x.whole(b + cnt - 1));   // both 0 or 1 from the ends
+                unsigned char* gp = const_cast<unsigned char*>(g.p) + static_cast<long long>(x.first(b + w0 + tid)) * SX;
+                const uint4* const end = q0 + w1;
+#pragma unroll 2
+                for (const uint4* q = q0 + w0 + tid; q < end; q += kRowThreads, gp += 16 * kRowThreads) st_stream(gp, grad_whole(*q));
+            }
+            // the ragged ones, or all of them
+            auto one = [&](int k) {
+                store_vec<SX>(g, x.first(b + k), !ok ? make_uint4(0, 0, 0, 0) : ref.whole ? grad_whole(q0[k]) : grad_far(q0[k]), same_phase);
+            };
+            if (w1 > w0) {
+                if (tid < w0) one(0);
+                if (tid < cnt - w1) one(cnt - 1);
+            } else {
+                for (int k = tid; k < cnt; k += kRowThreads) one(k);
+            }
             if (j + slots < np) refill(f + slots);
         }
         __syncthreads();                                     // the members' gradients go over the span's
         if (here && ok) {
-            const float d = fmaf(-p, wt, ref.of(v) * scale_in);
+            const float d = fmaf(-p, s.wt, ref.of(v) * s.scale_in);
             unsigned char* const gp = const_cast<unsigned char*>(g.p);
             if (SX == 2) reinterpret_cast<unsigned short*>(gp)[id] = static_cast<unsigned short>(to_bits<SX>(d));
             else reinterpret_cast<float*>(gp)[id] = d;
@@ -443,7 +486,9 @@ dspark_status_t distill_args(const void* student, const dspark_teacher_t* t, con
         cluster *= 2;
     for (a->log_c = 0; (1 << a->log_c) < cluster;) ++a->log_c;
     a->piece = nvec / cluster + 1;
+    a->np = 1;
     if (a->piece > (both ? kDisSpan : kDisPiece)) {
+        a->np = (a->piece + kDisPiece - 1) / kDisPiece;
         a->piece = kDisPiece;
         a->log_slots = 1;
     }

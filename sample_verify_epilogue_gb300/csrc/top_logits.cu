@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
     if (tid == 0) s.n = 0;
 
     // ---- the stream
-    ExpSum es{-INFINITY, 0.f};
+    RunSum run;
     float g[2] = {-INFINITY, -INFINITY};                     // maxima of the thread's even and odd vectors
     {
         uint4 cur[kTopVec], nxt[kTopVec];
@@ -115,12 +115,13 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
             float bm[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int u = 0; u < kTopVec; ++u) bm[u & 1] = fmaxf(bm[u & 1], vec_max<SX>(cur[u]));
-            add_exps<SX>(es, cur, fmaxf(bm[0], bm[1]), a.c);
+            add_exps<SX>(run, cur, fmaxf(bm[0], bm[1]), a.c);
             g[0] = fmaxf(g[0], bm[0]);
             g[1] = fmaxf(g[1], bm[1]);
         }
     }
     const float tmax = fmaxf(g[0], g[1]);
+    ExpSum es = run.get();
 
     // ---- group maxima: 512/C of this CTA; a group is a thread's half, a thread, or 2 or 4 threads
     {

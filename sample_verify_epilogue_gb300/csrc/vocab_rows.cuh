@@ -205,18 +205,20 @@ __device__ __forceinline__ ExpSum warp_merge(ExpSum a, float c) {
     a.m = m;
     return a;
 }
+// A thread's sum while it streams: the maximum, its whole exponent r, the sum.
+struct RunSum {
+    float m = -INFINITY, r = -INFINITY, sum = 0.f;
+    __device__ __forceinline__ ExpSum get() const { return ExpSum{m, sum}; }
+};
 // Add the exponentials of U vectors whose maximum is bm.
 template <int SX, int U>
-__device__ __forceinline__ void add_exps(ExpSum& es, const uint4 (&v)[U], float bm, float c) {
+__device__ __forceinline__ void add_exps(RunSum& es, const uint4 (&v)[U], float bm, float c) {
     constexpr int VE = 16 / SX;
-    if (bm > es.m) {
-        es.sum *= rebase(es.m, bm, c);
-        es.m = bm;
-    }
-    const ExpRef ref(es.m, c);
-    if (ref.whole) {
-        const unsigned long long c2 = pack2(c, c), r2 = pack2(-ref.r, -ref.r);
-        unsigned long long acc[2] = {0ull, 0ull};
+    const float m = fmaxf(es.m, bm), t = m * c, r = ceilf(t);
+    if (fabsf(t) < 4194304.f) {
+        // what came before scales by a power of two: 0 for nothing (r = -inf) and for the lowest values
+        const unsigned long long c2 = pack2(c, c), r2 = pack2(-r, -r);
+        unsigned long long acc[2] = {pack2(es.sum * ex2_approx(es.r - r), 0.f), 0ull};
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -227,14 +229,17 @@ __device__ __forceinline__ void add_exps(ExpSum& es, const uint4 (&v)[U], float 
             }
         float lo, hi;
         unpack2(add2(acc[0], acc[1]), lo, hi);
-        es.sum += lo + hi;
+        es.sum = lo + hi;
     } else {
-        const float m = es.m > -INFINITY ? es.m : 0.f;
+        es.sum = rebase(es.m, m, c) * es.sum;
+        const float ref = m > -INFINITY ? m : 0.f;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int q = 0; q < VE; ++q) es.sum += ex2_approx((elem<SX>(v[u], q) - m) * c);
+            for (int q = 0; q < VE; ++q) es.sum += ex2_approx((elem<SX>(v[u], q) - ref) * c);
     }
+    es.m = m;
+    es.r = r;
 }
 
 // ---------------------------------------------------------------- clusters
@@ -244,6 +249,7 @@ __device__ __forceinline__ unsigned cluster_rank() {
     return r;
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // Shared-window address of the same variable in CTA `rank` of the cluster.
