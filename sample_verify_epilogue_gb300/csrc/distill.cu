@@ -100,7 +100,8 @@ __device__ __forceinline__ void store_vec(const VocabRow<SX>& g, int i0, const u
     }
 }
 
-template <int SX, int PASS>
+// ONE: the span is one piece.
+template <int SX, int PASS, bool ONE>
 __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
     constexpr int VE = VocabRow<SX>::VE;
     constexpr bool kWantLoss = (PASS & kLoss) != 0, kWantGrad = (PASS & kGrad) != 0;
@@ -147,23 +148,14 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
         if (kWantLoss && C > 1) cluster_wait();
     };
     // The span in np pieces (the last may be short, or empty); copy number f (the pieces in turn, then
-    // again for a second pass) goes to buffer f mod slots.  Warp 0 fetches: whole vectors by a bulk
-    // copy, the row's ragged first and last by two lanes.
-    const int np = a.np, slots = 1 << a.log_slots;
+    // again for a second pass) goes to buffer f mod slots; warp 0 fetches.
+    const int np = ONE ? 1 : a.np, log_slots = ONE ? 0 : a.log_slots, slots = 1 << log_slots;
     auto lo = [&](int j) { return min(k1, k0 + j * a.piece); };
     auto hi = [&](int j) { return min(k1, k0 + (j + 1) * a.piece); };
     auto buffer = [&](int f) { return s_x + (f & (slots - 1)) * a.piece; };
     auto fetch = [&](int f) {
-        const int j = f < np ? f : f - np, b = lo(j), e = hi(j);
-        const int wb = b + (e > b && !x.whole(b)), we = e - (e > wb && !x.whole(e - 1));
-        if (lane == 0) {
-            uint64_t* const bar = &s.bar[f & (slots - 1)];
-            const unsigned bytes = we > wb ? 16u * static_cast<unsigned>(we - wb) : 0u;
-            mbar_arrive_expect_tx(bar, bytes);
-            if (bytes) bulk_g2s(buffer(f) + (wb - b), x.p + static_cast<long long>(x.first(wb)) * SX, bytes, bar);
-        }
-        if (lane == 1 && wb > b) buffer(f)[0] = load_vec<SX>(x, b, e);
-        if (lane == 2 && we < e && we >= wb) buffer(f)[we - b] = load_vec<SX>(x, we, e);
+        const int j = f < np ? f : f - np;
+        fetch_piece<SX>(x, lo(j), hi(j), buffer(f), &s.bar[f & (slots - 1)]);
     };
     if (w == 0.f) {
         leave(0);
@@ -242,7 +234,7 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
         if (entries) {
             const int i0 = x.first(lo(j));
             const bool in = id >= max(0, i0) && id < min(a.V, x.first(hi(j)));
-            if (warp == 0 || __any_sync(0xffffffffu, in)) late = late || !bar_wait(&s.bar[f & (slots - 1)], static_cast<unsigned>(f >> a.log_slots) & 1u);
+            if (warp == 0 || __any_sync(0xffffffffu, in)) late = late || !bar_wait(&s.bar[f & (slots - 1)], static_cast<unsigned>(f >> log_slots) & 1u);
             if (in && note) {
                 using Bits = std::conditional_t<SX == 2, unsigned short, unsigned>;
                 Bits* const at = reinterpret_cast<Bits*>(buffer(f)) + (id - i0);
@@ -258,7 +250,6 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
         if (entries) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncthreads();
         if (warp == 0) fetch(f);
-        if (slots == 1) __syncthreads();                     // the ragged vectors are read before the next barrier
     };
 
     // what the gradient is made with, by one thread
@@ -276,7 +267,7 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
     // ---- Z and R
     if (kWantLoss) {
         RunSum run;
-        const bool twice = kWantGrad && np > 1;              // the pieces come again for the gradient
+        const bool twice = kWantGrad && !ONE;                // the pieces come again for the gradient
         for (int j = 0; j < np; ++j) {
             arrive(j, j, true);
             const uint4* const q0 = buffer(j);
@@ -292,7 +283,7 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
                 const uint4 q[1] = {q0[k]};
                 add_exps<SX>(run, q, vecs_max<SX>(q), a.c);
             }
-            if (j + slots < (twice ? 2 * np : np)) refill(j + slots);
+            if (!ONE && j + slots < (twice ? 2 * np : np)) refill(j + slots);
         }
         const ExpSum es = run.get();
         // the warp's part, then the CTA's to every CTA of the row, then the row's
@@ -399,8 +390,8 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
         // one piece is still in its buffer from the sum
         for (int j = 0; j < np; ++j) {
             const int f = kWantLoss ? np + j : j;
-            if (!kWantLoss || np > 1) arrive(f, j, !kWantLoss);
-            const uint4* const q0 = buffer(kWantLoss && np == 1 ? 0 : f);
+            if (!kWantLoss || !ONE) arrive(f, j, !kWantLoss);
+            const uint4* const q0 = buffer(f);
             const int b = lo(j), cnt = hi(j) - b;
             // whole vectors of rows that lie alike go straight through
             int w0 = 0, w1 = 0;
@@ -422,7 +413,7 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
             } else {
                 for (int k = tid; k < cnt; k += kRowThreads) one(k);
             }
-            if (j + slots < np) refill(f + slots);
+            if (!ONE && j + slots < np) refill(f + slots);
         }
         __syncthreads();                                     // the members' gradients go over the span's
         if (here && ok) {
@@ -498,11 +489,12 @@ dspark_status_t distill_args(const void* student, const dspark_teacher_t* t, con
 template <int SX, int PASS>
 dspark_status_t distill_launch(const DisArgs& a, int rows, void* stream) {
     const size_t smem = static_cast<size_t>(a.piece) * 16 << a.log_slots;
+    auto kern = a.np == 1 ? distill_kernel<SX, PASS, true> : distill_kernel<SX, PASS, false>;
     if (smem > 32 * 1024 &&                                  // beyond what a launch gets unasked
-        cudaFuncSetAttribute(distill_kernel<SX, PASS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return DSPARK_ERR_CUDA;
     const unsigned grid = static_cast<unsigned>(rows) << a.log_c;
-    const cudaError_t e = launch_cluster(distill_kernel<SX, PASS>, grid, kRowThreads, 1 << a.log_c, smem, static_cast<cudaStream_t>(stream), a);
+    const cudaError_t e = launch_cluster(kern, grid, kRowThreads, 1 << a.log_c, smem, static_cast<cudaStream_t>(stream), a);
     return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 

@@ -1,15 +1,15 @@
 // top_logits_kernel: the n largest logits of every row (value descending, id ascending among
 // equals) and log sum exp(x / T), one launch, each row split over a cluster of C CTAs.
 //
-// One pass over the row, bound by bandwidth: while a CTA streams its span, each thread keeps the sum
-// of its exponentials and the maxima of the groups of vectors it sees, and nothing else.
-// The row's 512 group maxima then give a threshold: their n-th largest is reached by at least n
-// logits, and by few more (G groups, n of them at or above: about -G ln(1 - n/G) logits, 69 for
-// n = 64), so
-//   1. group maxima go to shared memory; every CTA reads the row's 512 through distributed shared
-//      memory and finds their n-th largest by bisection on the upper 16 bits of its key (one warp);
-//   2. only the threads whose maximum reaches it read their vectors again (L2) and list the
-//      logits that do;
+// One pass over the row, bound by bandwidth: a CTA streams its span through three 16 KB buffers filled
+// by bulk copies, a batch of four 16-byte vectors per thread at a time, and each thread keeps the sum of
+// its exponentials and its two largest batch maxima (where they were, and the third), nothing
+// else.  The row's 512 largest such maxima then give a threshold: their n-th largest is reached by at
+// least n logits, and by few more (of 512 groups about -512 ln(1 - n/512) logits: 69 for n = 64), so
+//   1. maxima go to shared memory; every CTA reads the row's 512 through distributed shared memory
+//      and finds their n-th largest by bisection on the upper 16 bits of its key (one warp);
+//   2. a thread whose maximum reaches it reads that batch again (L2), or both, or all of its vectors
+//      where the third maximum reaches it too, and lists the logits that do;
 //   3. every CTA reads the row's whole list and ranks its own entries in it: the rank is the place
 //      in the record.
 // Rows whose list would be too long (equal values, few distinct values, values bunched in one
@@ -23,17 +23,17 @@ namespace dspark {
 namespace {
 
 constexpr int kTopVec = 4;
-constexpr int kTopBatch = kTopVec * kRowThreads;             // vectors per batch
+constexpr int kTopBatch = kTopVec * kRowThreads;             // vectors per piece: a batch per thread
+constexpr int kTopSlots = 3;                                 // buffers
 constexpr int kTopGroups = 512;                              // of a row, whatever its cluster
 constexpr int kTopOwn = 2 * DSPARK_MAX_TOP_LOGITS;           // entries a CTA lists at most
 constexpr int kTopAll = 1024;                                // entries of a row on the short path
 constexpr int kTopBuf = DSPARK_MAX_TOP_LOGITS * (kMaxCluster + 1);   // ... on the exact path: < n above, n equal per CTA
-
-// (order-preserving value key, id reversed), ids below 2^24.
-__device__ __forceinline__ unsigned long long top_key(float v, int id) { return ckey(v, id); }
+constexpr size_t kTopSmem = sizeof(uint4) * kTopSlots * kTopBatch;
+static_assert(sizeof(unsigned long long) * (kTopOwn + kTopBuf) <= kTopSmem, "the lists take the buffers' place");
 
 struct TopArgs {
-    int V, n, cluster;
+    int V, n, log_c;                                         // log_c: of the cluster's size
     float c;                                                 // log2(e) / T
     double inv_t;
     long long stride;
@@ -45,33 +45,39 @@ struct TopArgs {
 };
 
 struct __align__(16) TopSmem {
-    unsigned long long own[kTopOwn];
-    unsigned long long all[kTopBuf];
     unsigned short gmax[kTopGroups];                         // this CTA's 512/C group maxima: upper halves of their keys
+    uint64_t full[kTopSlots], empty[kTopSlots];
     ExpSum es[kRowWarps];
     ExpSum part;                                             // this CTA's sum
+    int late;                                                // a copy did not come in time
     int n;                                                   // entries listed (passes kTopOwn when they do not fit)
-    int n_all;                                               // -1: the row takes the exact path
     int cnt;                                                 // exact path: this CTA's count
     int wcnt[kRowWarps];
     unsigned th;                                             // threshold key
     ExpSum row;
+    int row_late;
 };
 
 __device__ __forceinline__ float key_floor(unsigned k) {     // value of a key, never -inf
     return fmaxf(key_to_f(k), -3.402823466e38f);
 }
 
-// Largest k with at least n of the warp's 32*Q keys >= k, on 16-bit keys; 0 when fewer are set.
+// Largest k with at least n of the warp's 32*Q 16-bit keys >= k (n <= 32*Q), or a smaller one with
+// exactly n.
 template <int Q>
 __device__ unsigned warp_nth_key16(const unsigned (&key)[Q], int n) {
-    unsigned lo = 0;
-    for (int bit = 15; bit >= 0; --bit) {
-        const unsigned mid = lo | (1u << bit);
+    unsigned lo = key[0], hi = key[0];
+#pragma unroll
+    for (int q = 1; q < Q; ++q) { lo = min(lo, key[q]); hi = max(hi, key[q]); }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    while (lo < hi) {
+        const unsigned mid = (lo + hi + 1) >> 1;
         int c = 0;
 #pragma unroll
-        for (int q = 0; q < Q; ++q) c += key[q] >= mid;
-        if (__reduce_add_sync(0xffffffffu, c) >= n) lo = mid;
+        for (int q = 0; q < Q; ++q) c += __popc(__ballot_sync(0xffffffffu, key[q] >= mid));
+        if (c >= n) lo = mid; else hi = mid - 1;
+        if (c == n) break;
     }
     return lo;
 }
@@ -90,60 +96,84 @@ template <int SX>
 __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
     constexpr int VE = VocabRow<SX>::VE;
     __shared__ TopSmem s;
+    extern __shared__ uint4 s_ring[];                        // [kTopSlots][kTopBatch]; after the stream the two lists:
+    unsigned long long* const own = reinterpret_cast<unsigned long long*>(s_ring);   // this CTA's entries
+    unsigned long long* const all = own + kTopOwn;           // the row's
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int C = a.cluster, rank = static_cast<int>(blockIdx.x % C);
-    const long long row = blockIdx.x / C;
+    const int C = 1 << a.log_c, rank = static_cast<int>(blockIdx.x & (C - 1));
+    const long long row = blockIdx.x >> a.log_c;
     const VocabRow<SX> x(a.x, row, a.stride, a.V);
-    const int k0 = static_cast<int>(static_cast<long long>(x.nvec) * rank / C);
-    const int k1 = static_cast<int>(static_cast<long long>(x.nvec) * (rank + 1) / C);
-    if (tid == 0) s.n = 0;
+    const int k0 = x.nvec * rank >> a.log_c, k1 = x.nvec * (rank + 1) >> a.log_c;   // nvec * C < 2^31
+    const int np = (k1 - k0 + kTopBatch - 1) / kTopBatch;
+    if (tid == 0) {
+        for (int k = 0; k < kTopSlots; ++k) {
+            mbar_init(&s.full[k], 1);
+            mbar_init(&s.empty[k], kRowWarps);
+        }
+        fence_mbar_init();
+        s.n = 0;
+        s.late = 0;
+    }
+    __syncthreads();
 
     // ---- the stream
     RunSum run;
-    float g[2] = {-INFINITY, -INFINITY};                     // maxima of the thread's even and odd vectors
+    float m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;    // the thread's largest batch maxima
+    int b1 = 0, b2 = 0;                                      // where the first two were
     {
-        uint4 cur[kTopVec], nxt[kTopVec];
-#pragma unroll
-        for (int u = 0; u < kTopVec; ++u) nxt[u] = load_vec<SX>(x, k0 + u * kRowThreads + tid, k1);
-        for (int base = k0; base < k1; base += kTopBatch) {
-#pragma unroll
-            for (int u = 0; u < kTopVec; ++u) cur[u] = nxt[u];
-            if (base + kTopBatch < k1) {
-#pragma unroll
-                for (int u = 0; u < kTopVec; ++u) nxt[u] = load_vec<SX>(x, base + kTopBatch + u * kRowThreads + tid, k1);
+        bool late = false;
+        if (warp == 0)
+            for (int j = 0; j < min(np, kTopSlots); ++j)
+                fetch_piece<SX>(x, k0 + j * kTopBatch, min(k1, k0 + (j + 1) * kTopBatch), s_ring + j * kTopBatch, &s.full[j]);
+        int slot = 0, before = kTopSlots - 1;                // of piece j and of piece j - 1
+        unsigned parity = 0, parity_before = 0;
+        for (int j = 0; j < np; ++j) {
+            if (warp == 0 && j > 0 && j + kTopSlots - 1 < np) {   // the piece before this one leaves its buffer
+                const int f = j + kTopSlots - 1;
+                late = late || !bar_wait(&s.empty[before], parity_before);
+                fetch_piece<SX>(x, k0 + f * kTopBatch, min(k1, k0 + (f + 1) * kTopBatch), s_ring + before * kTopBatch, &s.full[before]);
             }
-            float bm[2] = {-INFINITY, -INFINITY};
+            late = late || !bar_wait(&s.full[slot], parity);
+            const uint4* const q0 = s_ring + slot * kTopBatch;
+            const int cnt = min(kTopBatch, k1 - k0 - j * kTopBatch);
+            uint4 v[kTopVec];
 #pragma unroll
-            for (int u = 0; u < kTopVec; ++u) bm[u & 1] = fmaxf(bm[u & 1], vec_max<SX>(cur[u]));
-            add_exps<SX>(run, cur, fmaxf(bm[0], bm[1]), a.c);
-            g[0] = fmaxf(g[0], bm[0]);
-            g[1] = fmaxf(g[1], bm[1]);
+            for (int u = 0; u < kTopVec; ++u) v[u] = u * kRowThreads + tid < cnt ? q0[u * kRowThreads + tid] : ninf_vec<SX>();
+            const float bm = vecs_max<SX>(v);
+            add_exps<SX>(run, v, bm, a.c);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.empty[slot]);
+            m3 = fmaxf(m3, fminf(m2, bm));
+            const bool first = bm > m1, second = bm > m2;
+            m2 = first ? m1 : fmaxf(m2, bm);
+            b2 = first ? b1 : second ? j : b2;
+            m1 = fmaxf(m1, bm);
+            b1 = first ? j : b1;
+            before = slot;
+            parity_before = parity;
+            if (++slot == kTopSlots) { slot = 0; parity ^= 1u; }
         }
+        if (late) s.late = 1;
     }
-    const float tmax = fmaxf(g[0], g[1]);
-    ExpSum es = run.get();
 
-    // ---- group maxima: 512/C of this CTA; a group is a thread's half, a thread, or 2 or 4 threads
+    // ---- group maxima: 512/C of this CTA; a group is a batch, a thread, or 2 or 4 threads
     {
-        float gm = tmax;
+        float gm = m1;
         if (C == 1) {
-            s.gmax[tid] = static_cast<unsigned short>(fkey(g[0]) >> 16);
-            s.gmax[tid + kRowThreads] = static_cast<unsigned short>(fkey(g[1]) >> 16);
+            s.gmax[tid] = static_cast<unsigned short>(fkey(m1) >> 16);
+            s.gmax[tid + kRowThreads] = static_cast<unsigned short>(fkey(m2) >> 16);
         } else {
             if (C >= 4) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 1));
             if (C >= 8) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 2));
-            const int per = C / 2;                           // threads of a group
-            if (tid % per == 0) s.gmax[tid / per] = static_cast<unsigned short>(fkey(gm) >> 16);
+            const int per = C / 2;                           // threads of a group, a power of two
+            if ((tid & (per - 1)) == 0) s.gmax[tid >> (a.log_c - 1)] = static_cast<unsigned short>(fkey(gm) >> 16);
         }
-        for (int o = 16; o; o >>= 1)
-            es = merge(es, ExpSum{__shfl_xor_sync(0xffffffffu, es.m, o), __shfl_xor_sync(0xffffffffu, es.sum, o)}, a.c);
+        const ExpSum es = warp_merge(run.get(), a.c);
         if (lane == 0) s.es[warp] = es;
         __syncthreads();
         if (warp == 0) {
-            es = s.es[lane & (kRowWarps - 1)];
-            for (int o = kRowWarps / 2; o; o >>= 1)
-                es = merge(es, ExpSum{__shfl_xor_sync(0xffffffffu, es.m, o), __shfl_xor_sync(0xffffffffu, es.sum, o)}, a.c);
-            if (lane == 0) s.part = es;
+            const ExpSum part = warp_merge(lane < kRowWarps ? s.es[lane] : ExpSum{-INFINITY, 0.f}, a.c);
+            if (lane == 0) s.part = part;
         }
     }
     row_sync(C);
@@ -153,55 +183,73 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
         unsigned key[kTopGroups / 32];
         if (C > 1) {
             // two 16-bit maxima per word; CTA p has 256/C words
-            const int per = kTopGroups / 2 / C;
+            const int log_per = 8 - a.log_c;
 #pragma unroll
             for (int q = 0; q < kTopGroups / 64; ++q) {
                 const int w = q * 32 + lane;
-                const unsigned v = peer_ld32(peer_addr(reinterpret_cast<const unsigned*>(s.gmax) + w % per, w / per));
+                const unsigned v = peer_ld32(peer_addr(reinterpret_cast<const unsigned*>(s.gmax) + (w & ((1 << log_per) - 1)), w >> log_per));
                 key[2 * q] = v & 0xFFFFu;
                 key[2 * q + 1] = v >> 16;
             }
-            es = ExpSum{-INFINITY, 0.f};
-            if (lane < C) {
-                const unsigned from = peer_addr(&s.part, lane);
-                es = ExpSum{__uint_as_float(peer_ld32(from)), __uint_as_float(peer_ld32(from + 4))};
-            }
-            for (int o = kMaxCluster / 2; o; o >>= 1)
-                es = merge(es, ExpSum{__shfl_xor_sync(0xffffffffu, es.m, o), __shfl_xor_sync(0xffffffffu, es.sum, o)}, a.c);
         } else {
 #pragma unroll
             for (int q = 0; q < kTopGroups / 32; ++q) key[q] = s.gmax[q * 32 + lane];
         }
         const unsigned th = warp_nth_key16(key, a.n) << 16;
+        if (lane == 0) s.th = th;
+    } else if (warp == 1) {
+        ExpSum es{-INFINITY, 0.f};
+        int late = 0;
+        if (lane < C) {
+            const unsigned from = peer_addr(&s.part, lane);
+            es = ExpSum{__uint_as_float(peer_ld32(from)), __uint_as_float(peer_ld32(from + 4))};
+            late = static_cast<int>(peer_ld32(peer_addr(&s.late, lane)));
+        }
+        es = warp_merge(es, a.c);
+        late = __any_sync(0xffffffffu, late);
         if (lane == 0) {
-            s.th = th;
             s.row = es;
+            s.row_late = late;
         }
     }
     __syncthreads();
-    es = s.row;
+    const float top = s.row.m;
     // a row with NaN or +inf has a NaN sum, one with nothing above -inf a maximum of -inf
-    const bool ok = es.sum == es.sum && es.m > -INFINITY;
+    const bool ok = s.row.sum == s.row.sum && top > -INFINITY && !s.row_late;
 
-    // ---- list the logits that reach the threshold: flagged threads' vectors, a warp to a thread
+    // ---- list the logits that reach the threshold
     const float th = key_floor(s.th);
-    if (ok) {
-        unsigned flagged = __ballot_sync(0xffffffffu, tmax >= th);
-        while (flagged) {
-            const int t = warp * 32 + __ffs(flagged) - 1;
-            flagged &= flagged - 1;
-            for (int k = k0 + t + lane * kRowThreads; k < k1; k += 32 * kRowThreads) {
-                const uint4 w = load_vec<SX>(x, k, k1);
-                if (!(vec_max<SX>(w) >= th)) continue;
+    auto offer = [&](const uint4& w, int k) {
+        if (!(vec_max<SX>(w) >= th)) return;
 #pragma unroll
-                for (int q = 0; q < VE; ++q) {
-                    const float v = elem<SX>(w, q);
-                    if (v >= th) {
-                        const int at = atomicAdd(&s.n, 1);
-                        if (at < kTopOwn) s.own[at] = top_key(v, x.first(k) + q);
-                    }
-                }
+        for (int q = 0; q < VE; ++q) {
+            const float v = elem<SX>(w, q);
+            if (v >= th) {
+                const int at = atomicAdd(&s.n, 1);
+                if (at < kTopOwn) own[at] = ckey(v, x.first(k) + q);
             }
+        }
+    };
+    if (ok) {
+        if (m1 >= th && !(m3 >= th)) {                       // one or two batches, by the thread itself
+            uint4 w[2][kTopVec];
+            const int at[2] = {k0 + b1 * kTopBatch + tid, k0 + b2 * kTopBatch + tid};
+            const bool both = m2 >= th;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int u = 0; u < kTopVec; ++u)
+                    w[h][u] = h == 0 || both ? load_vec<SX>(x, at[h] + u * kRowThreads, k1) : ninf_vec<SX>();
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int u = 0; u < kTopVec; ++u) offer(w[h][u], at[h] + u * kRowThreads);
+        }
+        unsigned many = __ballot_sync(0xffffffffu, m3 >= th);   // all its vectors, by the warp
+        while (many) {
+            const int t = warp * 32 + __ffs(many) - 1;
+            many &= many - 1;
+            for (int k = k0 + t + lane * kRowThreads; k < k1; k += 32 * kRowThreads) offer(load_vec<SX>(x, k, k1), k);
             if (*reinterpret_cast<volatile int*>(&s.n) > kTopOwn) break;   // the exact path counts anew
         }
     }
@@ -230,7 +278,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
                 const int end = __shfl_sync(0xffffffffu, incl, t);
                 if (i >= end) { p = t + 1; start = end; }
             }
-            if (i < total) s.all[i] = C > 1 ? peer_ld64(peer_addr(&s.own[i - start], p)) : s.own[i];
+            if (i < total) all[i] = C > 1 ? peer_ld64(peer_addr(&own[i - start], p)) : own[i];
         }
         return true;
     };
@@ -238,7 +286,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
         // exact path (the same for every CTA of the row): v, the n-th largest value, is the largest
         // with at least n logits at or above it
         row_sync(C);                                         // the counts have been read
-        unsigned lo = fkey(th), hi = fkey(es.m);
+        unsigned lo = fkey(th), hi = fkey(top);
         while (lo < hi) {
             const unsigned mid = lo + ((hi - lo) >> 1) + 1;
             const float v = key_to_f(mid);
@@ -258,10 +306,10 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
             }
             __syncthreads();
             row_sync(C);
-            int all = 0;
-            for (int p = 0; p < C; ++p) all += C > 1 ? static_cast<int>(peer_ld32(peer_addr(&s.cnt, p))) : s.cnt;
+            int count = 0;
+            for (int p = 0; p < C; ++p) count += C > 1 ? static_cast<int>(peer_ld32(peer_addr(&s.cnt, p))) : s.cnt;
             row_sync(C);
-            if (all >= a.n) lo = mid; else hi = mid - 1;
+            if (count >= a.n) lo = mid; else hi = mid - 1;
         }
         const float v = key_to_f(lo);
         if (tid == 0) s.n = 0;
@@ -272,7 +320,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
 #pragma unroll
             for (int q = 0; q < VE; ++q) {
                 const float e = elem<SX>(w, q);
-                if (e > v) s.own[atomicAdd(&s.n, 1)] = top_key(e, x.first(k) + q);
+                if (e > v) own[atomicAdd(&s.n, 1)] = ckey(e, x.first(k) + q);
             }
         }
         __syncthreads();
@@ -299,7 +347,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
 #pragma unroll
             for (int q = 0; q < VE; ++q)
                 if (elem<SX>(w, q) == v) {
-                    if (at < a.n) s.own[above + at] = top_key(v, x.first(k) + q);
+                    if (at < a.n) own[above + at] = ckey(v, x.first(k) + q);
                     ++at;
                 }
             __syncthreads();
@@ -311,14 +359,14 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
     }
     __syncthreads();
 
-    // ---- places: an entry's rank in the row's list, a warp to an entry
+    // ---- places: an entry's rank in the row's list
     if (ok) {
-        for (int i = warp; i < mine; i += kRowWarps) {
-            const unsigned long long k = s.all[before + i];
-            int at = 0;
-            for (int e = lane; e < total; e += 32) at += s.all[e] > k;
-            at = __reduce_add_sync(0xffffffffu, at);
-            if (lane == 0 && at < a.n) {
+        for (int i = tid; i < mine; i += kRowThreads) {
+            const unsigned long long k = all[before + i];
+            int at = 0, e = 0;
+            for (; e + 4 <= total; e += 4) at += (all[e] > k) + (all[e + 1] > k) + (all[e + 2] > k) + (all[e + 3] > k);
+            for (; e < total; ++e) at += all[e] > k;
+            if (at < a.n) {
                 a.values[out + at] = ckey_v(k);
                 a.ids[out + at] = ckey_id(k);
             }
@@ -329,10 +377,10 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
             a.values[out + i] = -INFINITY;
             a.ids[out + i] = -1;
         }
-        if (tid == 0) {
-            a.row_status[row] = ok ? 0 : DSPARK_ROW_NONFINITE;
+        if (tid == kRowThreads - 1) {                        // (a warp that ranks little)
+            a.row_status[row] = s.row_late ? DSPARK_ROW_INTERNAL : ok ? 0 : DSPARK_ROW_NONFINITE;
             if (a.lse)
-                a.lse[row] = ok ? static_cast<float>(ExpRef(es.m, a.c).log_unit(a.inv_t) + log(static_cast<double>(es.sum))) : NAN;
+                a.lse[row] = ok ? static_cast<float>(ExpRef(top, a.c).log_unit(a.inv_t) + log(static_cast<double>(s.row.sum))) : NAN;
         }
     }
     if (C > 1) {                                             // peers' shared memory is read until here
@@ -360,18 +408,19 @@ extern "C" dspark_status_t dspark_top_logits(const void* logits, const dspark_to
     TopArgs a{};
     a.V = p->V; a.n = p->n; a.c = c; a.inv_t = 1.0 / p->temperature; a.stride = p->logits_stride;
     a.x = logits; a.values = out_values; a.ids = out_ids; a.lse = out_lse; a.row_status = p->row_status;
-    // CTAs per row: spans of at most 256 KB, and smaller ones, down to a batch of vectors, while the
-    // rows alone do not make two CTAs per SM.  A CTA's part after the stream costs about as much as
-    // streaming 128 KB: 576 rows of 512 KB take 91 us in halves and 132 us in eighths, 9 rows of
-    // 304 KB 24 us whole and 12 us in eighths.
+    // CTAs per row: one, or more, down to a piece of the row each, while the rows alone do not make two
+    // CTAs per SM: what follows the stream costs a CTA about what 100 KB do.  576 rows of 512 KB take
+    // 65 us whole, 81 us in halves and 109 us in quarters; 9 rows of 304 KB are fastest in eighths.
     const int nvec = max_vectors(p->V, sx);
-    a.cluster = 1;
-    while (a.cluster < kMaxCluster && (nvec > a.cluster * 16384 ||
-                                       (nvec >= 2 * a.cluster * kTopBatch && static_cast<long long>(p->n_rows) * a.cluster < 304)))
-        a.cluster *= 2;
-    const unsigned grid = static_cast<unsigned>(p->n_rows) * static_cast<unsigned>(a.cluster);
+    int cluster = 1;
+    while (cluster < kMaxCluster && nvec >= 2 * cluster * kTopBatch && static_cast<long long>(p->n_rows) * cluster < 304)
+        cluster *= 2;
+    while ((1 << a.log_c) < cluster) ++a.log_c;
+    const unsigned grid = static_cast<unsigned>(p->n_rows) << a.log_c;
     cudaStream_t s = static_cast<cudaStream_t>(p->stream);
-    const cudaError_t e = sx == 2 ? launch_cluster(top_logits_kernel<2>, grid, kRowThreads, a.cluster, 0, s, a)
-                                  : launch_cluster(top_logits_kernel<4>, grid, kRowThreads, a.cluster, 0, s, a);
+    auto kern = sx == 2 ? top_logits_kernel<2> : top_logits_kernel<4>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kTopSmem)) != cudaSuccess)
+        return DSPARK_ERR_CUDA;
+    const cudaError_t e = launch_cluster(kern, grid, kRowThreads, cluster, kTopSmem, s, a);
     return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }

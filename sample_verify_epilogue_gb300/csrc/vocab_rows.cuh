@@ -106,6 +106,27 @@ __device__ __forceinline__ uint4 load_vec(const VocabRow<SX>& r, int k, int k_en
     return w;
 }
 
+// One warp copies vectors [b, e) of a row to shared memory: whole ones by a bulk copy, the row's
+// ragged first and last by two lanes.  The mbarrier takes one arrival per phase.
+template <int SX>
+__device__ __forceinline__ void fetch_piece(const VocabRow<SX>& r, int b, int e, uint4* dst, uint64_t* bar) {
+    const int lane = threadIdx.x & 31;
+    const int wb = b + (e > b && !r.whole(b)), we = e - (e > wb && !r.whole(e - 1));
+    const bool ragged = wb > b || we < e;
+    if (lane == 0) {
+        const unsigned bytes = we > wb ? 16u * static_cast<unsigned>(we - wb) : 0u;
+        if (ragged) asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" :: "r"(smem_u32(bar)), "r"(bytes) : "memory");
+        else mbar_arrive_expect_tx(bar, bytes);
+        if (bytes) bulk_g2s(dst + (wb - b), r.p + static_cast<long long>(r.first(wb)) * SX, bytes, bar);
+    }
+    if (ragged) {
+        if (lane == 1 && wb > b) dst[0] = load_vec<SX>(r, b, e);
+        if (lane == 2 && we < e && we >= wb) dst[we - b] = load_vec<SX>(r, we, e);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    }
+}
+
 // Maximum of a vector's lanes, NaN lanes left out.
 template <int SX>
 __device__ __forceinline__ float vec_max(const uint4& w) {
