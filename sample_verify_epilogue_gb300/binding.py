@@ -309,13 +309,33 @@ def dspark_verify_sample_host(logits, q, draft_ids, counts, rows, uniforms, *, o
 # ---------------------------------------------------------------- around the epilogue
 # These calls are a few microseconds of GPU work on small batches, so their checks are kept to
 # one cheap comparison per property; device indices stand for devices.
+class _Torch:
+    """What the calls below use of torch, looked up once (this module is importable without it)."""
+
+    def __init__(self):
+        import torch
+        self.i32, self.f32, self.u8 = torch.int32, torch.float32, torch.uint8
+        self.dtypes = {torch.bfloat16: DSPARK_BF16, torch.float32: DSPARK_FP32}
+        self.stream = torch._C._cuda_getCurrentRawStream
+        self.device = torch._C._cuda_getDevice
+        self.guard = torch.cuda.device
+
+
+_torch = None
+
+
+def _t():
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    return _torch
+
+
 def _dtype_of(logits):
-    import torch
-    if logits.dtype is torch.bfloat16:
-        return DSPARK_BF16
-    if logits.dtype is torch.float32:
-        return DSPARK_FP32
-    raise TypeError(f"logits are bfloat16 or float32, not {logits.dtype}")
+    d = _t().dtypes.get(logits.dtype)
+    if d is None:
+        raise TypeError(f"logits are bfloat16 or float32, not {logits.dtype}")
+    return d
 
 
 def _rows_of(name, t, like=None):
@@ -360,19 +380,13 @@ def _device_of(name, t):
 
 def _launch(fn, dev, *args):
     """Call ``fn`` with device ``dev`` current."""
-    import torch
-    if torch._C._cuda_getDevice() == dev:
+    if _torch.device() == dev:
         code = fn(*args)
     else:
-        with torch.cuda.device(dev):
+        with _torch.guard(dev):
             code = fn(*args)
     if code != DSPARK_OK:
         _check(code)
-
-
-def _stream_of(stream, dev):
-    import torch
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream
 
 
 def dspark_process_logits(logits, rows, *, out, row_status, draft_ids=None, history=None, bias=None, mask=None,
@@ -386,16 +400,16 @@ def dspark_process_logits(logits, rows, *, out, row_status, draft_ids=None, hist
     mask [n, words >= ceil(V/32)] int32 bits of the allowed tokens, mask_rows [B, K_max+1] int32 rows of
     mask (-1: no grammar) or None (row b*(K_max+1) + j) -- all CUDA tensors.
     """
-    import torch
+    T = _t()
     dev = _device_of("logits", logits)
     if logits.dim() != 3:
         raise ValueError("logits must be [B, K_max+1, V]")
     B, W, V = logits.shape
     stride = _rows_of("logits", logits)[2]
     out_stride = stride if out is logits else _rows_of("out", out, logits)[2]
-    i32, f32 = torch.int32, torch.float32
+    i32, f32 = T.i32, T.f32
     p = dspark_process_params_t(B, W - 1, V, _dtype_of(logits), stride, out_stride,
-                                _flat("rows", rows, torch.uint8, B * 16, dev), _stream_of(stream, dev),
+                                _flat("rows", rows, T.u8, B * 16, dev), T.stream(dev) if stream is None else stream,
                                 _flat("row_status", row_status, i32, B, dev))
     d = h = b = m = None
     if draft_ids is not None and W > 1:
@@ -429,23 +443,23 @@ def dspark_top_logits(logits, *, values, ids, row_status, lse=None, temperature=
     logits [..., V] bf16/fp32 of R rows, values fp32 and ids int32 [..., n], lse [...] fp32 or None,
     row_status [...] int32 -- all CUDA tensors; n is the last size of values.
     """
-    import torch
+    T = _t()
     dev = _device_of("logits", logits)
     R, V, stride = _rows_of("logits", logits)
     n = values.shape[-1]
-    i32, f32 = torch.int32, torch.float32
-    p = dspark_top_params_t(R, V, _dtype_of(logits), stride, n, temperature, _stream_of(stream, dev),
+    i32, f32 = T.i32, T.f32
+    p = dspark_top_params_t(R, V, _dtype_of(logits), stride, n, temperature, T.stream(dev) if stream is None else stream,
                             _flat("row_status", row_status, i32, R, dev))
     _launch(load_library().dspark_top_logits, dev, logits.data_ptr(), p, _flat("values", values, f32, R * n, dev),
             _flat("ids", ids, i32, R * n, dev), None if lse is None else _flat("lse", lse, f32, R, dev))
 
 
 def _distill_args(student, teacher_ids, teacher_logits, teacher_lse, t2d, weights, temperature, row_status, grad, stream):
-    import torch
+    T = _t()
     dev = _device_of("student", student)
     R, V, stride = _rows_of("student", student)
     grad_stride = V if grad is None else stride if grad is student else _rows_of("grad", grad, student)[2]
-    i32, f32 = torch.int32, torch.float32
+    i32, f32 = T.i32, T.f32
     n = teacher_ids.shape[-1]
     t = dspark_teacher_t(_flat("teacher_ids", teacher_ids, i32, R * n, dev),
                          _flat("teacher_logits", teacher_logits, f32, R * n, dev),
@@ -454,7 +468,7 @@ def _distill_args(student, teacher_ids, teacher_logits, teacher_lse, t2d, weight
                          0 if t2d is None else t2d.numel())
     p = dspark_distill_params_t(R, V, _dtype_of(student), stride, grad_stride, temperature,
                                 None if weights is None else _flat("weights", weights, f32, R, dev),
-                                _stream_of(stream, dev),
+                                T.stream(dev) if stream is None else stream,
                                 None if row_status is None else _flat("row_status", row_status, i32, R, dev))
     return dev, R, t, p
 
@@ -470,12 +484,11 @@ def dspark_distill(student, teacher_ids, teacher_logits, *, loss, row_status, gr
     None; loss [...] fp32, row_status [...] int32, grad like student (may be student) or None, saved
     [..., 4] fp32 for dspark_distill_backward or None -- all CUDA tensors.
     """
-    import torch
     if row_status is None:
         raise ValueError("row_status is missing")
     dev, R, t, p = _distill_args(student, teacher_ids, teacher_logits, teacher_lse, t2d, weights, temperature,
                                  row_status, grad, stream)
-    f32 = torch.float32
+    f32 = _torch.f32
     _launch(load_library().dspark_distill, dev, student.data_ptr(), t, p, _flat("loss", loss, f32, R, dev),
             None if saved is None else _flat("saved", saved, f32, 4 * R, dev), None if grad is None else grad.data_ptr())
 
@@ -484,11 +497,10 @@ def dspark_distill_backward(student, teacher_ids, teacher_logits, *, saved, grad
                             t2d=None, weights=None, temperature=1.0, row_status=None, stream=None):
     """The gradient of sum(grad_loss * loss) by the student's logits, from the inputs and the ``saved`` of
     a dspark_distill call; grad_loss [...] fp32 or None (all 1).  ``row_status`` is not written."""
-    import torch
     if grad is None:
         raise ValueError("grad is missing")
     dev, R, t, p = _distill_args(student, teacher_ids, teacher_logits, teacher_lse, t2d, weights, temperature,
                                  row_status, grad, stream)
-    f32 = torch.float32
+    f32 = _torch.f32
     _launch(load_library().dspark_distill_backward, dev, student.data_ptr(), t, p, _flat("saved", saved, f32, 4 * R, dev),
             None if grad_loss is None else _flat("grad_loss", grad_loss, f32, R, dev), grad.data_ptr())

@@ -56,6 +56,15 @@ struct DisArgs {
     int* row_status;
 };
 
+// A value as the sum of two floats; two_sum's is exact.
+struct TwoFloat {
+    float hi, lo;
+};
+__device__ __forceinline__ TwoFloat two_sum(float a, float b) {
+    const float s = a + b, t = s - a;
+    return TwoFloat{s, (a - (s - t)) + (b - t)};
+}
+
 struct __align__(16) DisPart {                               // what a warp tells its CTA, a CTA its cluster
     float m, rest, in;                                       // maximum; sums of e outside and inside S, by it
     int status;
@@ -68,8 +77,8 @@ struct __align__(16) DisSmem {
     double cross[kRowWarps];
     uint64_t bar[2], part_bar, cross_bar;
     alignas(16) unsigned wkey[kRowWarps];                    // largest key of the warp's record logits
-    alignas(16) float wsum[kRowWarps];                       // sum of its probabilities
-    float m, total, rest;                                    // the row's
+    alignas(16) TwoFloat wsum[kRowWarps];                    // sum of its probabilities
+    float m, total, rest, in;                                // the row's: Z = total = rest + in
     float wt, scale_in, scale_out;
     int status;
     int id[DSPARK_MAX_TOP_LOGITS];                           // draft ids of the record, -1: none
@@ -182,15 +191,25 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
     __syncthreads();
     unsigned top = 0u;
     for (int k = 0; k < n_warps; ++k) top = max(top, s.wkey[k]);
-    float lp = -INFINITY, p = 0.f;
+    float lp = -INFINITY, lp_low = 0.f, p = 0.f;             // log p in two parts
     if (entries) {
         const float tmax = key_to_f(top);
         if (id >= 0) {
             if (t > -INFINITY) {
-                // log p: t / T is a product with 1/T in two parts, the first one exact inside the fma
                 const float ih = static_cast<float>(a.inv_t), il = static_cast<float>(a.inv_t - static_cast<double>(ih));
-                lp = a.lse ? fmaf(t, il, fmaf(t, ih, -lse)) : (t - tmax) * ih;
-                p = expf(lp);
+                if (a.lse) {                                 // 1 - sum p is what is left of the mass: p to its last bits
+                    const float prod = t * ih, rest = fmaf(t, ih, -prod);
+                    const TwoFloat d = two_sum(prod, -lse);
+                    lp = d.hi;
+                    lp_low = d.lo + fmaf(t, il, rest);
+                    p = expf(lp);
+                    p = fmaf(p, lp_low, p);
+                } else {
+                    const float d = t - tmax;
+                    lp = d * ih;
+                    lp_low = fmaf(d, il, fmaf(d, ih, -lp));
+                    p = expf(lp);
+                }
             }
             // a repeated id: entries whose hash was met before look for it
             const unsigned h = (static_cast<unsigned>(id) * 2654435761u) >> 19;
@@ -200,22 +219,33 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
         }
         // only -inf in the record, a log-sum-exp far below its logits
         bad = bad || (top != 0u && !a.lse && !(tmax > -INFINITY)) || !(p < INFINITY);
-        const float ws = warp_sum(p);
+        TwoFloat ws{p, 0.f};
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const float hi = __shfl_xor_sync(0xffffffffu, ws.hi, o), lo = __shfl_xor_sync(0xffffffffu, ws.lo, o);
+            const TwoFloat d = two_sum(ws.hi, hi);
+            ws = TwoFloat{d.hi, d.lo + (ws.lo + lo)};
+        }
         if (lane == 0) s.wsum[warp] = ws;
     }
     const int status0 = __syncthreads_or(bad) ? DSPARK_ROW_BAD_TEACHER : 0;
-    float psum = 0.f, p_r = 0.f;
-    for (int k = 0; k < n_warps; ++k) psum += s.wsum[k];
-    float mass = psum;                                       // sum of p, 1 - sum, their sum
-    if (a.lse) {
-        if (psum < 1.f) { p_r = 1.f - psum; mass = 1.f; }
-    } else {
-        if (entries) {
-            lp -= logf(psum);
-            p *= 1.f / psum;
-        }
-        psum = mass = 1.f;
+    TwoFloat sum{0.f, 0.f};
+    for (int k = 0; k < n_warps; ++k) {
+        const TwoFloat d = two_sum(sum.hi, s.wsum[k].hi);
+        sum = TwoFloat{d.hi, d.lo + (sum.lo + s.wsum[k].lo)};
     }
+    // the entries' p stand as they are; with a log-sum-exp the rest of the mass is p_r, without one
+    // their sum is what they are relative to
+    float mass = sum.hi, p_r = 0.f;                          // M = sum of p + p_r
+    if (a.lse) {
+        p_r = fmaxf((1.f - sum.hi) - sum.lo, 0.f);
+        if (p_r > 0.f) mass = 1.f;
+    }
+    // p_r Z / R - 1 for Z = R + in, p_r = 1 - sum: without the difference of the two near ones
+    auto tail_excess = [&](float rest, float in) {
+        const float z = sum.hi * rest;
+        return ((fmaf(p_r, in, -z) - fmaf(sum.hi, rest, -z)) - sum.lo * rest) / rest;
+    };
     bool late = false;
     if (status0 || top == 0u) {
         if (warp == 0)
@@ -253,15 +283,12 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
     };
 
     // what the gradient is made with, by one thread
-    auto scales = [&](float total, float rest) {
-        const float wt = (a.up ? w * a.up[row] : w) * static_cast<float>(a.inv_t), in = wt * (mass / total);
+    auto scales = [&](float total, float rest, float in) {
+        float wt = (a.up ? w * a.up[row] : w) * static_cast<float>(a.inv_t);
+        if (!a.lse) wt /= sum.hi;
         s.wt = wt;
-        s.scale_in = s.scale_out = in;
-        // (M R - p_r Z) / (Z R): the two products cancel where the student's tail is nearly right
-        if (p_r > 0.f && rest > 0.f) {
-            const float z = p_r * total, ze = fmaf(p_r, total, -z);
-            s.scale_out = wt * (((fmaf(mass, rest, -z) - ze) / rest) / total);
-        }
+        s.scale_in = s.scale_out = wt * (mass / total);
+        if (p_r > 0.f && rest > 0.f) s.scale_out = -wt * (tail_excess(rest, in) / total);   // M/Z - p_r/R, M = 1
     };
 
     // ---- Z and R
@@ -324,7 +351,7 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
         // meanwhile sum p_i (log p_i - log e_i)
         double cross = 0.0;
         if (mine) {
-            if (here && p > 0.f) cross = p * (lp - v * ln_c);
+            if (here && p > 0.f) cross = p * (static_cast<double>(lp) + lp_low - v * ln_c);
             cross = warp_sum_d(cross);
         }
         if (lane == 0) s.cross[warp] = cross;
@@ -340,8 +367,9 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
                 s.m = o.m;
                 s.total = status ? NAN : total;
                 s.rest = o.rest;
+                s.in = o.in;
                 s.status = status;
-                if (kWantGrad) scales(total, o.rest);
+                if (kWantGrad) scales(total, o.rest, o.in);
             }
         }
         __syncthreads();
@@ -361,7 +389,7 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
         const float m = kWantLoss ? s.m : a.saved[4 * row], total = kWantLoss ? s.total : a.saved[4 * row + 1];
         const bool ok = total > 0.f && m > -INFINITY;        // total is NaN for a row that cannot be normalised
         if (!kWantLoss) {
-            if (tid == 0) scales(total, a.saved[4 * row + 2]);
+            if (tid == 0) scales(total, a.saved[4 * row + 2], a.saved[4 * row + 3]);
             __syncthreads();
         }
         const float scale = s.scale_out;
@@ -430,16 +458,21 @@ __global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
             const float m = s.m, total = s.total, rest = s.rest;
             const int status = s.status | (late ? DSPARK_ROW_INTERNAL : 0);
             const ExpRef ref(m, a.c);
+            const double psum = static_cast<double>(sum.hi) + sum.lo;
             double loss = psum * ((ref.whole ? kLn2 * ref.r : m * ln_c) + log_split(total));
             for (int k = 0; k < C; ++k) loss += s.cross_all[k];
-            if (p_r > 0.f && rest > 0.f) loss += p_r * logf(p_r * (total / rest));
+            if (!a.lse) loss = loss / psum - log_split(sum.hi);
+            if (p_r > 0.f && rest > 0.f) {
+                const float d = tail_excess(rest, s.in);
+                loss += p_r * (fabsf(d) < 0.5f ? log1pf(d) : logf(p_r * (total / rest)));
+            }
             a.loss[row] = status ? NAN : static_cast<float>(w * loss);
             a.row_status[row] = status;
             if (a.saved_out) {
                 a.saved_out[4 * row] = m;
                 a.saved_out[4 * row + 1] = total;
                 a.saved_out[4 * row + 2] = rest;
-                a.saved_out[4 * row + 3] = 0.f;
+                a.saved_out[4 * row + 3] = s.in;
             }
         }
     }
