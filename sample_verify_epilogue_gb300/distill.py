@@ -37,7 +37,7 @@ class _DistillLoss(torch.autograd.Function):
         return grad, None, None, None, None, None, None
 
 
-def distill_loss(student, teacher_ids, teacher_logits, *, teacher_lse=None, t2d=None, weights=None, temperature=1.0):
+def distill_loss(student, teacher_ids, teacher_logits, teacher_lse=None, *, t2d=None, weights=None, temperature=1.0):
     """(loss, status) of every row of student [..., V]: see dspark_distill for the arguments.
 
     The teacher's record, ``teacher_lse`` and ``weights`` are constants: no gradient reaches them.

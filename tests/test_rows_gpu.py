@@ -543,3 +543,11 @@ def test_chain_with_the_epilogue(bd):
     tokens = tokens[tokens >= 0]
     assert len(tokens) and ((tokens >= 100) & (tokens < 200)).all()
     assert math.isfinite(float(call.x[0, 0, 150]))
+
+
+def test_example_round_trip(bd):
+    """The example's rounds: the drafter's loss falls, and no emitted token breaks its grammar or its ban."""
+    from examples.constrained_verify_distill import run
+    losses, accepted, legal = run(rounds=20, B=16, K=3, V=5003, draft_V=1201, hidden=16, n=32, say=lambda *_: None)
+    # (a round's 48 rows are other rows than the last one's: means over five rounds)
+    assert legal and all(np.isfinite(losses)) and np.mean(losses[-5:]) < 0.9 * np.mean(losses[:5])
