@@ -10,10 +10,10 @@
 // empties is not read; in place, a vector that the mask leaves whole is neither read nor written.
 //
 // Without lists the copy runs at 0.95 of the measured bandwidth (64x9 rows of 262144 bf16, no
-// masks: 93 us); 1000 listed tokens a row add 20 us of scattered two-byte stores.  Taking the tokens
-// through shared memory into the vectors before they are stored costs more than that, in barriers
-// for every tile or in what the first store waits for (115 to 130 us where this takes 99), and so does
-// a warp to a span without barriers (117 us).
+// masks: 93 us); 1000 listed tokens a row add some 15 us of scattered two-byte stores (30 with loads
+// and stores that pass the L1 cache by).  Taking the tokens through shared memory into the vectors
+// before they are stored costs more than that, in barriers for every tile or in what the first store
+// waits for (104 to 130 us where this takes 89), and so does a warp to a span without barriers (117 us).
 //
 // The first B CTAs check one request each (parameters, list order and ranges, draft ids, mask
 // rows) and write its status; they run beside the copying CTAs, whose own range checks keep every
@@ -377,8 +377,8 @@ extern "C" dspark_status_t dspark_process_logits(const void* logits, void* out, 
     a.in_place = out == logits;
     a.row_status = p->row_status;
     // Tiles per CTA: a CTA's chain of list and mask look-ups is worth a few tiles, so more than one where
-    // that leaves CTAs enough.  18432 tiles: 128 us one by one, 109 in twos, 99 in fours; 1520 tiles:
-    // 12.4, 10.8, 11.7 us; 684 tiles: 7.3, 7.8, 9.1 us.
+    // that leaves CTAs enough.  18432 tiles: 94 us in twos, 89 in fours, 94 in sixes; 1520 tiles:
+    // 12.4 us one by one, 11.2 in twos, 12.6 in fours; 684 tiles: 7.1, 7.7, 8.0 us.
     const bool aligned = reinterpret_cast<uintptr_t>(logits) % 16 == 0 && p->logits_stride * sx % 16 == 0;
     const int nvec = aligned ? (p->V + 16 / sx - 1) / (16 / sx) : max_vectors(p->V, sx);
     const int tiles = (nvec + kProcTile - 1) / kProcTile;
