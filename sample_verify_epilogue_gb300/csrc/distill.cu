@@ -111,7 +111,7 @@ __device__ __forceinline__ void store_vec(const VocabRow<SX>& g, int i0, const u
 
 // ONE: the span is one piece.
 template <int SX, int PASS, bool ONE>
-__global__ void __launch_bounds__(kRowThreads, 5) distill_kernel(DisArgs a) {
+__global__ void __launch_bounds__(kRowThreads, ONE ? 5 : 6) distill_kernel(DisArgs a) {
     constexpr int VE = VocabRow<SX>::VE;
     constexpr bool kWantLoss = (PASS & kLoss) != 0, kWantGrad = (PASS & kGrad) != 0;
     __shared__ DisSmem s;
