@@ -3,13 +3,13 @@
 //
 // One pass over the row, bound by bandwidth: a CTA streams its span through three 16 KB buffers filled
 // by bulk copies, a batch of four 16-byte vectors per thread at a time, and each thread keeps the sum of
-// its exponentials and its two largest batch maxima (where they were, and the third), nothing
-// else.  The row's 512 largest such maxima then give a threshold: their n-th largest is reached by at
-// least n logits, and by few more (of 512 groups about -512 ln(1 - n/512) logits: 69 for n = 64), so
+// its exponentials and its three largest batch maxima (where they were, and the fourth), nothing
+// else.  512 of the row's largest such maxima then give a threshold: their n-th largest is reached by
+// at least n logits, and by few more (of 512 groups about -512 ln(1 - n/512) logits: 69 for n = 64), so
 //   1. maxima go to shared memory; every CTA reads the row's 512 through distributed shared memory
-//      and finds their n-th largest by bisection on the upper 16 bits of its key (one warp);
-//   2. a thread whose maximum reaches it reads that batch again (L2), or both, or all of its vectors
-//      where the third maximum reaches it too, and lists the logits that do;
+//      and finds their n-th largest by bisection on the upper 16 bits of its key;
+//   2. a thread whose maximum reaches it reads that batch again (L2), or two, or three, or all of its
+//      vectors where the fourth maximum reaches it too, and lists the logits that do;
 //   3. every CTA reads the row's whole list and ranks its own entries in it: the rank is the place
 //      in the record.
 // Rows whose list would be too long (equal values, few distinct values, values bunched in one
@@ -50,9 +50,12 @@ struct __align__(16) TopSmem {
     ExpSum es[kRowWarps];
     ExpSum part;                                             // this CTA's sum
     int late;                                                // a copy did not come in time
+    int todo[kRowWarps][3 * 32];                             // a warp's (batch << 5 | lane) to look at again
     int n;                                                   // entries listed (passes kTopOwn when they do not fit)
     int cnt;                                                 // exact path: this CTA's count
     int wcnt[kRowWarps];
+    uint2 range[kRowWarps];                                  // smallest and largest maxima of a warp's
+    alignas(16) int reach[2][kRowWarps];                     // a warp's maxima that reach a step's key
     unsigned th;                                             // threshold key
     ExpSum row;
     int row_late;
@@ -60,26 +63,6 @@ struct __align__(16) TopSmem {
 
 __device__ __forceinline__ float key_floor(unsigned k) {     // value of a key, never -inf
     return fmaxf(key_to_f(k), -3.402823466e38f);
-}
-
-// Largest k with at least n of the warp's 32*Q 16-bit keys >= k (n <= 32*Q), or a smaller one with
-// exactly n.
-template <int Q>
-__device__ unsigned warp_nth_key16(const unsigned (&key)[Q], int n) {
-    unsigned lo = key[0], hi = key[0];
-#pragma unroll
-    for (int q = 1; q < Q; ++q) { lo = min(lo, key[q]); hi = max(hi, key[q]); }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    while (lo < hi) {
-        const unsigned mid = (lo + hi + 1) >> 1;
-        int c = 0;
-#pragma unroll
-        for (int q = 0; q < Q; ++q) c += __popc(__ballot_sync(0xffffffffu, key[q] >= mid));
-        if (c >= n) lo = mid; else hi = mid - 1;
-        if (c == n) break;
-    }
-    return lo;
 }
 
 // Barrier of the cluster, or of the block when the row has one CTA.
@@ -118,8 +101,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
 
     // ---- the stream
     RunSum run;
-    float m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;    // the thread's largest batch maxima
-    int b1 = 0, b2 = 0;                                      // where the first two were
+    float m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY, m4 = -INFINITY;   // the thread's largest batch maxima
+    int b1 = 0, b2 = 0, b3 = 0;                              // where the first three were
     {
         bool late = false;
         if (warp == 0)
@@ -143,8 +126,10 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
             add_exps<SX>(run, v, bm, a.c);
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.empty[slot]);
-            m3 = fmaxf(m3, fminf(m2, bm));
-            const bool first = bm > m1, second = bm > m2;
+            const bool first = bm > m1, second = bm > m2, third = bm > m3;
+            m4 = fmaxf(m4, fminf(m3, bm));
+            m3 = second ? m2 : fmaxf(m3, bm);
+            b3 = second ? b2 : third ? j : b3;
             m2 = first ? m1 : fmaxf(m2, bm);
             b2 = first ? b1 : second ? j : b2;
             m1 = fmaxf(m1, bm);
@@ -179,37 +164,47 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
     row_sync(C);
 
     // ---- threshold, and the row's sum
-    if (warp == 0) {
-        unsigned key[kTopGroups / 32];
-        if (C > 1) {
-            // two 16-bit maxima per word; CTA p has 256/C words
-            const int log_per = 8 - a.log_c;
-#pragma unroll
-            for (int q = 0; q < kTopGroups / 64; ++q) {
-                const int w = q * 32 + lane;
-                const unsigned v = peer_ld32(peer_addr(reinterpret_cast<const unsigned*>(s.gmax) + (w & ((1 << log_per) - 1)), w >> log_per));
-                key[2 * q] = v & 0xFFFFu;
-                key[2 * q + 1] = v >> 16;
-            }
-        } else {
-#pragma unroll
-            for (int q = 0; q < kTopGroups / 32; ++q) key[q] = s.gmax[q * 32 + lane];
-        }
-        const unsigned th = warp_nth_key16(key, a.n) << 16;
-        if (lane == 0) s.th = th;
-    } else if (warp == 1) {
-        ExpSum es{-INFINITY, 0.f};
+    {
+        // two of the row's 512 maxima to a thread; CTA p has 256/C words of two
+        const int log_per = 8 - a.log_c;
+        const unsigned* const word = reinterpret_cast<const unsigned*>(s.gmax) + (tid & ((1 << log_per) - 1));
+        const unsigned two = C > 1 ? peer_ld32(peer_addr(word, tid >> log_per)) : *word;
+        const unsigned x0 = two & 0xFFFFu, x1 = two >> 16;
+        ExpSum es{-INFINITY, 0.f};                           // (warp 1: the CTAs' sums, joined below)
         int late = 0;
-        if (lane < C) {
+        if (warp == 1 && lane < C) {
             const unsigned from = peer_addr(&s.part, lane);
             es = ExpSum{__uint_as_float(peer_ld32(from)), __uint_as_float(peer_ld32(from + 4))};
             late = static_cast<int>(peer_ld32(peer_addr(&s.late, lane)));
         }
-        es = warp_merge(es, a.c);
-        late = __any_sync(0xffffffffu, late);
-        if (lane == 0) {
-            s.row = es;
-            s.row_late = late;
+        // the largest key that n maxima reach, or a smaller one that exactly n do
+        unsigned lo = __reduce_min_sync(0xffffffffu, min(x0, x1)), hi = __reduce_max_sync(0xffffffffu, max(x0, x1));
+        if (lane == 0) s.range[warp] = make_uint2(lo, hi);
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kRowWarps; ++w) {
+            lo = min(lo, s.range[w].x);
+            hi = max(hi, s.range[w].y);
+        }
+        for (int step = 0; lo < hi; ++step) {
+            const unsigned mid = (lo + hi + 1) >> 1;
+            const int c = __popc(__ballot_sync(0xffffffffu, x0 >= mid)) + __popc(__ballot_sync(0xffffffffu, x1 >= mid));
+            if (lane == 0) s.reach[step & 1][warp] = c;
+            __syncthreads();
+            int all_c = 0;
+#pragma unroll
+            for (int w = 0; w < kRowWarps; ++w) all_c += s.reach[step & 1][w];
+            if (all_c >= a.n) lo = mid; else hi = mid - 1;
+            if (all_c == a.n) break;
+        }
+        if (tid == 0) s.th = lo << 16;
+        if (warp == 1) {
+            es = warp_merge(es, a.c);
+            late = __any_sync(0xffffffffu, late);
+            if (lane == 0) {
+                s.row = es;
+                s.row_late = late;
+            }
         }
     }
     __syncthreads();
@@ -219,38 +214,55 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
 
     // ---- list the logits that reach the threshold
     const float th = key_floor(s.th);
+    // A warp's vectors, one per lane (k, or nothing for a vector of -inf): one place for all of it.
     auto offer = [&](const uint4& w, int k) {
-        if (!(vec_max<SX>(w) >= th)) return;
+        unsigned hits = 0u;
 #pragma unroll
-        for (int q = 0; q < VE; ++q) {
-            const float v = elem<SX>(w, q);
-            if (v >= th) {
-                const int at = atomicAdd(&s.n, 1);
-                if (at < kTopOwn) own[at] = ckey(v, x.first(k) + q);
-            }
+        for (int q = 0; q < VE; ++q) hits |= static_cast<unsigned>(elem<SX>(w, q) >= th) << q;
+        if (!__any_sync(0xffffffffu, hits != 0u)) return;
+        const int c = __popc(hits);
+        int incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
         }
+        int at = 0;
+        if (lane == 31) at = atomicAdd(&s.n, incl);
+        at = __shfl_sync(0xffffffffu, at, 31) + incl - c;
+#pragma unroll
+        for (int q = 0; q < VE; ++q)
+            if (hits >> q & 1u) {
+                if (at < kTopOwn) own[at] = ckey(elem<SX>(w, q), x.first(k) + q);
+                ++at;
+            }
     };
     if (ok) {
-        if (m1 >= th && !(m3 >= th)) {                       // one or two batches, by the thread itself
-            uint4 w[2][kTopVec];
-            const int at[2] = {k0 + b1 * kTopBatch + tid, k0 + b2 * kTopBatch + tid};
-            const bool both = m2 >= th;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int u = 0; u < kTopVec; ++u)
-                    w[h][u] = h == 0 || both ? load_vec<SX>(x, at[h] + u * kRowThreads, k1) : ninf_vec<SX>();
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int u = 0; u < kTopVec; ++u) offer(w[h][u], at[h] + u * kRowThreads);
+        // the batches to look at again, a lane to a vector: (lane, batch) pairs of the warp's threads
+        const bool whole = m4 >= th;                         // or all its vectors
+        const unsigned f1 = __ballot_sync(0xffffffffu, m1 >= th && !whole), f2 = __ballot_sync(0xffffffffu, m2 >= th && !whole);
+        const unsigned f3 = __ballot_sync(0xffffffffu, m3 >= th && !whole), below = (1u << lane) - 1u;
+        const int n1 = __popc(f1), n2 = n1 + __popc(f2), n3 = n2 + __popc(f3);
+        int* const todo = s.todo[warp];
+        if (f1 >> lane & 1u) todo[__popc(f1 & below)] = b1 << 5 | lane;
+        if (f2 >> lane & 1u) todo[n1 + __popc(f2 & below)] = b2 << 5 | lane;
+        if (f3 >> lane & 1u) todo[n2 + __popc(f3 & below)] = b3 << 5 | lane;
+        __syncwarp();
+        for (int i0 = 0; i0 < n3; i0 += 32 / kTopVec) {
+            const int i = i0 + lane / kTopVec, what = i < n3 ? todo[i] : 0;
+            const int k = k0 + (what >> 5) * kTopBatch + (lane % kTopVec) * kRowThreads + warp * 32 + (what & 31);
+            offer(i < n3 ? load_vec<SX>(x, k, k1) : ninf_vec<SX>(), k);
         }
-        unsigned many = __ballot_sync(0xffffffffu, m3 >= th);   // all its vectors, by the warp
+        unsigned many = __ballot_sync(0xffffffffu, whole);
         while (many) {
             const int t = warp * 32 + __ffs(many) - 1;
             many &= many - 1;
-            for (int k = k0 + t + lane * kRowThreads; k < k1; k += 32 * kRowThreads) offer(load_vec<SX>(x, k, k1), k);
-            if (*reinterpret_cast<volatile int*>(&s.n) > kTopOwn) break;   // the exact path counts anew
+            for (int base = k0 + t; base < k1; base += 32 * kRowThreads) {
+                const int k = base + lane * kRowThreads;
+                offer(load_vec<SX>(x, k, k1), k);
+            }
+            // the exact path counts anew (a lane's view of the count is as good as another's)
+            if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s.n) > kTopOwn)) break;
         }
     }
     row_sync(C);
@@ -361,12 +373,18 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
 
     // ---- places: an entry's rank in the row's list
     if (ok) {
-        for (int i = tid; i < mine; i += kRowThreads) {
-            const unsigned long long k = all[before + i];
-            int at = 0, e = 0;
-            for (; e + 4 <= total; e += 4) at += (all[e] > k) + (all[e + 1] > k) + (all[e + 2] > k) + (all[e + 3] > k);
-            for (; e < total; ++e) at += all[e] > k;
-            if (at < a.n) {
+        const int sub = tid & 3;                             // four lanes to an entry, a quarter of the list each
+        for (int i0 = 0; i0 < mine; i0 += kRowThreads / 4) {
+            const int i = i0 + (tid >> 2);
+            const unsigned long long k = i < mine ? all[before + i] : ~0ull;
+            int at = 0;
+            for (int e = 2 * sub; e < total; e += 8) {
+                const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(all + e);
+                at += (two.x > k) + (e + 1 < total && two.y > k);
+            }
+            at += __shfl_xor_sync(0xffffffffu, at, 1);
+            at += __shfl_xor_sync(0xffffffffu, at, 2);
+            if (sub == 0 && i < mine && at < a.n) {
                 a.values[out + at] = ckey_v(k);
                 a.ids[out + at] = ckey_id(k);
             }
