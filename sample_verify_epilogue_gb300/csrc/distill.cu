@@ -502,11 +502,12 @@ dspark_status_t distill_args(const void* student, const dspark_teacher_t* t, con
     // CTAs per row.  For both results at once spans of at most 72 KB, each kept in one piece; for one of
     // them a span streams through two buffers and may be as long as the row: a CTA's latencies cost
     // about what 40 KB do (2048 rows of 304 KB, loss alone: 101 us whole, 138 us in quarters, 198 us
-    // in eighths).  Smaller spans while the rows alone do not make two CTAs per SM.
+    // in eighths).  Smaller spans while that makes no more than four CTAs per SM (loss alone, 150 rows of
+    // 304 KB: 25.7 us whole, 18.7 in halves, 16.2 in quarters, 21.7 in eighths), or two where they are kept.
     const int nvec = max_vectors(p->V, *sx);
     int cluster = 1;
     while (cluster < kMaxCluster && ((both && nvec > cluster * kDisSpan) ||
-                                     (nvec >= cluster * 512 && static_cast<long long>(p->n_rows) * cluster < 304)))
+                                     (nvec >= cluster * 512 && static_cast<long long>(p->n_rows) * 2 * cluster <= (both ? 320 : 640))))
         cluster *= 2;
     for (a->log_c = 0; (1 << a->log_c) < cluster;) ++a->log_c;
     a->piece = nvec / cluster + 1;

@@ -426,12 +426,13 @@ extern "C" dspark_status_t dspark_top_logits(const void* logits, const dspark_to
     TopArgs a{};
     a.V = p->V; a.n = p->n; a.c = c; a.inv_t = 1.0 / p->temperature; a.stride = p->logits_stride;
     a.x = logits; a.values = out_values; a.ids = out_ids; a.lse = out_lse; a.row_status = p->row_status;
-    // CTAs per row: one, or more, down to a piece of the row each, while the rows alone do not make two
-    // CTAs per SM: what follows the stream costs a CTA about what 100 KB do.  576 rows of 512 KB take
-    // 65 us whole, 81 us in halves and 109 us in quarters; 9 rows of 304 KB are fastest in eighths.
+    // CTAs per row: one, or more, down to three quarters of a piece of the row each, while that makes no more
+    // than two CTAs per SM or so: what follows the stream costs a CTA about what 100 KB do, and more
+    // CTAs only stand in line.  Rows of 304 KB: 250 of them 25.0 us whole, 24.5 in halves, 31.5 in
+    // quarters; 80 of them 20.3, 15.5, 13.5 us and 18.6 in eighths; 16 of them 19.3, 13.8, 10.3, 9.6.
     const int nvec = max_vectors(p->V, sx);
     int cluster = 1;
-    while (cluster < kMaxCluster && nvec >= 2 * cluster * kTopBatch && static_cast<long long>(p->n_rows) * cluster < 304)
+    while (cluster < kMaxCluster && nvec >= 2 * cluster * (kTopBatch * 3 / 4) && static_cast<long long>(p->n_rows) * 2 * cluster <= 330)
         cluster *= 2;
     while ((1 << a.log_c) < cluster) ++a.log_c;
     const unsigned grid = static_cast<unsigned>(p->n_rows) << a.log_c;
