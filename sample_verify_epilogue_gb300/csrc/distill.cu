@@ -211,11 +211,15 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? 5 : 6) distill_kernel(DisAr
                     p = expf(lp);
                 }
             }
-            // a repeated id: entries whose hash was met before look for it
-            const unsigned h = (static_cast<unsigned>(id) * 2654435761u) >> 19;
-            static_assert(kSeenBits == 1u << 13, "the hash has 13 bits");
-            if (atomicOr(&s.seen[h >> 5], 1u << (h & 31)) >> (h & 31) & 1u)
-                for (int k = 0; k < a.n; ++k) bad = bad || (k != tid && s.id[k] == id);
+        }
+        // a repeated id: the warp looks for the entries whose hash was met before, one after the other
+        // (an entry by itself through the record: 65 us where this takes 44, 2048 rows of 32000, n = 256)
+        const unsigned h = (static_cast<unsigned>(id) * 2654435761u) >> 19;
+        static_assert(kSeenBits == 1u << 13, "the hash has 13 bits");
+        unsigned met = __ballot_sync(0xffffffffu, id >= 0 && (atomicOr(&s.seen[h >> 5], 1u << (h & 31)) >> (h & 31) & 1u));
+        for (; met; met &= met - 1) {
+            const int from = __ffs(met) - 1, other = __shfl_sync(0xffffffffu, id, from);
+            for (int k = lane; k < a.n; k += 32) bad = bad || (s.id[k] == other && k != 32 * warp + from);
         }
         // only -inf in the record, a log-sum-exp far below its logits
         bad = bad || (top != 0u && !a.lse && !(tmax > -INFINITY)) || !(p < INFINITY);

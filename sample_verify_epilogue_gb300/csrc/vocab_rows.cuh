@@ -264,11 +264,6 @@ __device__ __forceinline__ void add_exps(RunSum& es, const uint4 (&v)[U], float 
 }
 
 // ---------------------------------------------------------------- clusters
-__device__ __forceinline__ unsigned cluster_rank() {
-    unsigned r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
@@ -303,16 +298,6 @@ __device__ __forceinline__ unsigned long long global_timer() {
     unsigned long long t;
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
     return t;
-}
-// Whether an mbarrier's phase is over; what the cluster's CTAs pushed is visible then.
-__device__ __forceinline__ bool bar_test(uint64_t* bar, unsigned parity) {
-    unsigned ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-    return ok != 0;
 }
 // Wait for an mbarrier's phase with a 2 s bound, false when it runs out; data pushed by the
 // cluster's CTAs is visible afterwards.  The thread sleeps up to 1 ms at a time: without the
@@ -350,24 +335,6 @@ inline cudaError_t launch_cluster(void (*kern)(KArgs...), unsigned grid, int thr
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, std::forward<Args2>(args)...);
-}
-
-// Clusters of such CTAs the device holds at a time, 0 on an error.
-template <typename... KArgs>
-inline int resident_clusters(void (*kern)(KArgs...), int threads, int cluster, size_t smem) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(64u * static_cast<unsigned>(cluster));
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    return cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess ? n : 0;
 }
 
 }  // namespace dspark
