@@ -3,15 +3,17 @@
 //
 // One pass over the row, bound by bandwidth: a CTA streams its span through three 16 KB buffers filled
 // by bulk copies, a batch of four 16-byte vectors per thread at a time, and each thread keeps the sum of
-// its exponentials and its three largest batch maxima (where they were, and the fourth), nothing
+// its exponentials and its four largest batch maxima (where they were, and the fifth), nothing
 // else.  512 of the row's largest such maxima then give a threshold: their n-th largest is reached by
 // at least n logits, and by few more (of 512 groups about -512 ln(1 - n/512) logits: 69 for n = 64), so
 //   1. maxima go to shared memory; every CTA reads the row's 512 through distributed shared memory
 //      and finds their n-th largest by bisection on the upper 16 bits of its key;
-//   2. a thread whose maximum reaches it reads that batch again (L2), or two, or three, or all of its
-//      vectors where the fourth maximum reaches it too, and lists the logits that do;
-//   3. every CTA reads the row's whole list and ranks its own entries in it: the rank is the place
-//      in the record.
+//   2. a thread whose maximum reaches it reads that batch again (L2), or up to four, or all of its
+//      vectors where the fifth maximum reaches it too, and lists the logits that do (576 rows of 262144,
+//      n = 256: 90 us with three noted, 76 with four; n = 64: 57 both ways);
+//   3. every CTA reads the row's whole list, sorts it into 256 buckets by value and ranks its own entries in
+//      theirs: the rank is the place in the record (against the whole list: 96 us where buckets take 90,
+//      same rows, three noted; 333 rows of 50001 fp32, n = 256: 36 and 29).
 // Rows whose list would be too long (equal values, few distinct values, values bunched in one
 // group) take an exact path: bisection on the value over counts of the whole row, from that
 // threshold up to the maximum; then the logits above the n-th value, and in id order as many equal
@@ -30,7 +32,9 @@ constexpr int kTopOwn = 2 * DSPARK_MAX_TOP_LOGITS;           // entries a CTA li
 constexpr int kTopAll = 1024;                                // entries of a row on the short path
 constexpr int kTopBuf = DSPARK_MAX_TOP_LOGITS * (kMaxCluster + 1);   // ... on the exact path: < n above, n equal per CTA
 constexpr size_t kTopSmem = sizeof(uint4) * kTopSlots * kTopBatch;
-static_assert(sizeof(unsigned long long) * (kTopOwn + kTopBuf) <= kTopSmem, "the lists take the buffers' place");
+constexpr unsigned kTopBuckets = kRowThreads;                // a thread to a bucket
+static_assert(kTopBuckets == 256, "the bucket is 8 bits of the key");
+static_assert(sizeof(unsigned long long) * (kTopOwn + 2 * kTopBuf) <= kTopSmem, "the lists take the buffers' place");
 
 struct TopArgs {
     int V, n, log_c;                                         // log_c: of the cluster's size
@@ -50,10 +54,11 @@ struct __align__(16) TopSmem {
     ExpSum es[kRowWarps];
     ExpSum part;                                             // this CTA's sum
     int late;                                                // a copy did not come in time
-    int todo[kRowWarps][3 * 32];                             // a warp's (batch << 5 | lane) to look at again
+    int todo[kRowWarps][4 * 32];                             // a warp's (batch << 5 | lane) to look at again
     int n;                                                   // entries listed (passes kTopOwn when they do not fit)
     int cnt;                                                 // exact path: this CTA's count
     int wcnt[kRowWarps];
+    int bucket[kTopBuckets];                                 // entries of a bucket, then where it ends
     uint2 range[kRowWarps];                                  // smallest and largest maxima of a warp's
     alignas(16) int reach[2][kRowWarps];                     // a warp's maxima that reach a step's key
     unsigned th;                                             // threshold key
@@ -79,9 +84,10 @@ template <int SX>
 __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
     constexpr int VE = VocabRow<SX>::VE;
     __shared__ TopSmem s;
-    extern __shared__ uint4 s_ring[];                        // [kTopSlots][kTopBatch]; after the stream the two lists:
+    extern __shared__ uint4 s_ring[];                        // [kTopSlots][kTopBatch]; after the stream the lists:
     unsigned long long* const own = reinterpret_cast<unsigned long long*>(s_ring);   // this CTA's entries
     unsigned long long* const all = own + kTopOwn;           // the row's
+    unsigned long long* const sorted = all + kTopBuf;        // the row's by buckets
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = 1 << a.log_c, rank = static_cast<int>(blockIdx.x & (C - 1));
     const long long row = blockIdx.x >> a.log_c;
@@ -97,12 +103,13 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
         s.n = 0;
         s.late = 0;
     }
+    s.bucket[tid] = 0;
     __syncthreads();
 
     // ---- the stream
     RunSum run;
-    float m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY, m4 = -INFINITY;   // the thread's largest batch maxima
-    int b1 = 0, b2 = 0, b3 = 0;                              // where the first three were
+    float m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY, m4 = -INFINITY, m5 = -INFINITY;   // the thread's largest batch maxima
+    int b1 = 0, b2 = 0, b3 = 0, b4 = 0;                              // where the first four were
     {
         bool late = false;
         if (warp == 0)
@@ -126,8 +133,10 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
             add_exps<SX>(run, v, bm, a.c);
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.empty[slot]);
-            const bool first = bm > m1, second = bm > m2, third = bm > m3;
-            m4 = fmaxf(m4, fminf(m3, bm));
+            const bool first = bm > m1, second = bm > m2, third = bm > m3, fourth = bm > m4;
+            m5 = fmaxf(m5, fminf(m4, bm));
+            m4 = third ? m3 : fmaxf(m4, bm);
+            b4 = third ? b3 : fourth ? j : b4;
             m3 = second ? m2 : fmaxf(m3, bm);
             b3 = second ? b2 : third ? j : b3;
             m2 = first ? m1 : fmaxf(m2, bm);
@@ -239,19 +248,20 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
     };
     if (ok) {
         // the batches to look at again, a lane to a vector: (lane, batch) pairs of the warp's threads
-        const bool whole = m4 >= th;                         // or all its vectors
+        const bool whole = m5 >= th;                         // or all its vectors
         const unsigned f1 = __ballot_sync(0xffffffffu, m1 >= th && !whole), f2 = __ballot_sync(0xffffffffu, m2 >= th && !whole);
-        const unsigned f3 = __ballot_sync(0xffffffffu, m3 >= th && !whole), below = (1u << lane) - 1u;
-        const int n1 = __popc(f1), n2 = n1 + __popc(f2), n3 = n2 + __popc(f3);
+        const unsigned f3 = __ballot_sync(0xffffffffu, m3 >= th && !whole), f4 = __ballot_sync(0xffffffffu, m4 >= th && !whole), below = (1u << lane) - 1u;
+        const int n1 = __popc(f1), n2 = n1 + __popc(f2), n3 = n2 + __popc(f3), n4 = n3 + __popc(f4);
         int* const todo = s.todo[warp];
         if (f1 >> lane & 1u) todo[__popc(f1 & below)] = b1 << 5 | lane;
         if (f2 >> lane & 1u) todo[n1 + __popc(f2 & below)] = b2 << 5 | lane;
         if (f3 >> lane & 1u) todo[n2 + __popc(f3 & below)] = b3 << 5 | lane;
+        if (f4 >> lane & 1u) todo[n3 + __popc(f4 & below)] = b4 << 5 | lane;
         __syncwarp();
-        for (int i0 = 0; i0 < n3; i0 += 32 / kTopVec) {
-            const int i = i0 + lane / kTopVec, what = i < n3 ? todo[i] : 0;
+        for (int i0 = 0; i0 < n4; i0 += 32 / kTopVec) {
+            const int i = i0 + lane / kTopVec, what = i < n4 ? todo[i] : 0;
             const int k = k0 + (what >> 5) * kTopBatch + (lane % kTopVec) * kRowThreads + warp * 32 + (what & 31);
-            offer(i < n3 ? load_vec<SX>(x, k, k1) : ninf_vec<SX>(), k);
+            offer(i < n4 ? load_vec<SX>(x, k, k1) : ninf_vec<SX>(), k);
         }
         unsigned many = __ballot_sync(0xffffffffu, whole);
         while (many) {
@@ -267,8 +277,14 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
     }
     row_sync(C);
 
-    // ---- the row's list
+    // ---- the row's list, counted by buckets of the value's key between the maximum (bucket 0) and the threshold
     const long long out = row * a.n;
+    const unsigned key_lo = fkey(th), key_hi = fkey(top);
+    const int shift = max(0, 32 - __clz(key_hi - key_lo) - 8);
+    auto bucket = [&](unsigned long long k) {
+        const unsigned key = static_cast<unsigned>(k >> 32);
+        return min(kTopBuckets - 1u, (key_hi - min(key, key_hi)) >> shift);
+    };
     int total = 0, before = 0, mine = 0;
     auto gather = [&](int cap) {                             // false: a CTA's entries or all of them are too many
         const int np = C > 1 ? (lane < C ? static_cast<int>(peer_ld32(peer_addr(&s.n, lane))) : 0) : (lane == 0 ? s.n : 0);
@@ -290,7 +306,11 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
                 const int end = __shfl_sync(0xffffffffu, incl, t);
                 if (i >= end) { p = t + 1; start = end; }
             }
-            if (i < total) all[i] = C > 1 ? peer_ld64(peer_addr(&own[i - start], p)) : own[i];
+            if (i < total) {
+                const unsigned long long k = C > 1 ? peer_ld64(peer_addr(&own[i - start], p)) : own[i];
+                all[i] = k;
+                atomicAdd(&s.bucket[bucket(k)], 1);
+            }
         }
         return true;
     };
@@ -373,17 +393,40 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
 
     // ---- places: an entry's rank in the row's list
     if (ok) {
-        const int sub = tid & 3;                             // four lanes to an entry, a quarter of the list each
+        int incl = s.bucket[tid];
+        const int c = incl;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) s.wcnt[warp] = incl;
+        __syncthreads();
+        incl -= c;
+#pragma unroll
+        for (int w = 0; w < kRowWarps; ++w) incl += w < warp ? s.wcnt[w] : 0;
+        s.bucket[tid] = incl;                                // where a bucket begins; then, entry by entry, where it ends
+        __syncthreads();
+        for (int i = tid; i < total; i += kRowThreads) {
+            const unsigned long long k = all[i];
+            sorted[atomicAdd(&s.bucket[bucket(k)], 1)] = k;
+        }
+        __syncthreads();
+        const int sub = tid & 3;                             // four lanes to an entry, a quarter of its bucket each
         for (int i0 = 0; i0 < mine; i0 += kRowThreads / 4) {
             const int i = i0 + (tid >> 2);
-            const unsigned long long k = i < mine ? all[before + i] : ~0ull;
-            int at = 0;
-            for (int e = 2 * sub; e < total; e += 8) {
-                const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(all + e);
-                at += (two.x > k) + (e + 1 < total && two.y > k);
+            int at = 0, begin = 0;
+            unsigned long long k = 0;
+            if (i < mine) {
+                k = all[before + i];
+                const unsigned b = bucket(k);
+                begin = b ? s.bucket[b - 1] : 0;
+                const int end = begin < a.n ? s.bucket[b] : begin;   // (past the record)
+                for (int e = begin + sub; e < end; e += 4) at += sorted[e] > k;
             }
             at += __shfl_xor_sync(0xffffffffu, at, 1);
             at += __shfl_xor_sync(0xffffffffu, at, 2);
+            at += begin;
             if (sub == 0 && i < mine && at < a.n) {
                 a.values[out + at] = ckey_v(k);
                 a.ids[out + at] = ckey_id(k);
