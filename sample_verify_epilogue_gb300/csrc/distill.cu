@@ -124,10 +124,6 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? 5 : 6) distill_kernel(DisAr
     const int k0 = x.nvec * rank >> a.log_c, k1 = x.nvec * (rank + 1) >> a.log_c;   // nvec * C < 2^31
     const bool same_phase = x.a0 == g.a0;
 
-    const float w = a.weights ? a.weights[row] : 1.f;
-    int id = tid < a.n ? a.ids[row * a.n + tid] : -1;
-    const float t = tid < a.n ? a.tl[row * a.n + tid] : 0.f;
-    const float lse = a.lse ? a.lse[row] : 0.f;
     if (tid == 0) {
         mbar_init(&s.bar[0], 1);
         mbar_init(&s.bar[1], 1);
@@ -143,6 +139,11 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? 5 : 6) distill_kernel(DisAr
     }
     s.seen[tid] = 0u;
     if (kWantLoss && C > 1) cluster_arrive_relaxed();        // before a peer can push here (the fence above orders it)
+    pdl_wait();                                              // what came before in the stream
+    const float w = a.weights ? a.weights[row] : 1.f;
+    int id = tid < a.n ? a.ids[row * a.n + tid] : -1;
+    const float t = tid < a.n ? a.tl[row * a.n + tid] : 0.f;
+    const float lse = a.lse ? a.lse[row] : 0.f;
 
     // a row that is not reduced: loss, status and gradient; the same branch in every CTA of the row
     auto leave = [&](int status) {

@@ -151,6 +151,7 @@ __device__ __forceinline__ void mask_vec(uint4& w, unsigned bits) {
 template <int SX>
 __global__ void __launch_bounds__(kRowThreads, 6) process_kernel(ProcArgs a) {
     constexpr int VE = VocabRow<SX>::VE;
+    pdl_wait();                                              // what came before in the stream
     if (blockIdx.x < static_cast<unsigned>(a.B)) {
         check_request(a, static_cast<int>(blockIdx.x));
         return;
@@ -390,7 +391,7 @@ extern "C" dspark_status_t dspark_process_logits(const void* logits, void* out, 
     if (grid > 0x7fffffffLL) return DSPARK_ERR_UNSUPPORTED;
     cudaStream_t s = static_cast<cudaStream_t>(p->stream);
     const dim3 g(static_cast<unsigned>(grid)), t(kRowThreads);
-    const cudaError_t e = sx == 2 ? launch_k(process_kernel<2>, g, t, 0, s, false, a)
-                                  : launch_k(process_kernel<4>, g, t, 0, s, false, a);
+    const cudaError_t e = sx == 2 ? launch_k(process_kernel<2>, g, t, 0, s, true, a)
+                                  : launch_k(process_kernel<4>, g, t, 0, s, true, a);
     return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }

@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
     }
     s.bucket[tid] = 0;
     __syncthreads();
+    pdl_wait();                                              // what came before in the stream
 
     // ---- the stream
     RunSum run;

@@ -318,7 +318,10 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, unsigned parity) {
     }
 }
 
-// Launch `grid` CTAs of `threads` threads in clusters of `cluster`.
+// Launch `grid` CTAs of `threads` threads in clusters of `cluster`, as a programmatic dependent of the
+// previous kernel in s: the CTAs are placed while that one's last end, and wait for it (0.1 to 0.6 us a
+// call).  The kernels do not let their own successors in before they end: its CTAs took the places
+// that even out a grid of a few per SM (333 top-logit rows of 50001: 24.7 us, 21.8 without).
 template <typename... KArgs, typename... Args2>
 inline cudaError_t launch_cluster(void (*kern)(KArgs...), unsigned grid, int threads, int cluster, size_t smem, cudaStream_t s,
                                   Args2&&... args) {
@@ -327,13 +330,15 @@ inline cudaError_t launch_cluster(void (*kern)(KArgs...), unsigned grid, int thr
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, std::forward<Args2>(args)...);
 }
 

@@ -515,6 +515,64 @@ def test_streams_and_graph(bd):
         assert all(torch.equal(a, b) for a, b in zip(first, (y, v, i, lse, loss, g)))
 
 
+def test_between_copies_and_fills(bd):
+    """A launch waits for whatever its stream holds before it, and what follows waits for it: copies from and
+    to the host, fills, a fork to another stream and back; eagerly and in a graph."""
+    R_, V, n = 24, 30011, 16
+    host = (torch.randn(3, R_, V) * 3).pin_memory()
+    x, y, g = (torch.zeros(R_, V, device="cuda") for _ in range(3))
+    v, i = torch.empty(R_, n, device="cuda"), torch.empty(R_, n, dtype=torch.int32, device="cuda")
+    st, status = torch.empty(R_, dtype=torch.int32, device="cuda"), torch.empty(R_, dtype=torch.int32, device="cuda")
+    lse, loss, loss2 = (torch.empty(R_, device="cuda") for _ in range(3))
+    back = torch.empty(R_, V).pin_memory()
+    rows = torch.from_numpy(np.array([(1.2, 0.1, 0.2, 0)] * R_, "f4,f4,f4,i4").view(np.uint8).copy()).cuda()
+    bias = (torch.arange(R_ + 1, dtype=torch.int32).cuda(), torch.arange(R_, dtype=torch.int32).cuda() * 7,
+            torch.full((R_,), -math.inf, device="cuda"))
+    side = torch.cuda.Stream()
+
+    def step():
+        x.copy_(host[0], non_blocking=True)
+        bd.dspark_process_logits(x.view(R_, 1, V), rows, out=y.view(R_, 1, V), row_status=status, bias=bias)
+        x.zero_()
+        bd.dspark_top_logits(y, values=v, ids=i, lse=lse, row_status=st)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            bd.dspark_distill(y, i, v, loss=loss2, row_status=status, teacher_lse=lse)
+        x.copy_(host[1], non_blocking=True)
+        bd.dspark_distill(x, i, v, loss=loss, row_status=st, grad=g, teacher_lse=lse)
+        back.copy_(g, non_blocking=True)
+        torch.cuda.current_stream().wait_stream(side)
+        y.zero_()
+        g.zero_()
+
+    def check():
+        torch.cuda.synchronize()
+        want = host[0].clone()
+        want[torch.arange(R_), torch.arange(R_) * 7] = -math.inf
+        top = torch.topk(want, n)
+        assert torch.equal(v.cpu(), top.values) and torch.equal(i.cpu().long(), top.indices)
+        # the record of y against y itself has no divergence, against x some
+        assert loss2.abs().max() < 1e-5 and loss.min() > 0.1
+        q = torch.softmax(host[1].double(), -1)
+        p = torch.exp(top.values.double() - torch.logsumexp(want.double(), -1, keepdim=True))
+        inside = torch.zeros(R_, V, dtype=torch.bool).scatter_(1, top.indices, True)
+        left, q_left = 1 - p.sum(-1, keepdim=True), torch.where(inside, 0.0, q).sum(-1, keepdim=True)
+        grad = (q * (1 - left / q_left)).scatter(1, top.indices, q.gather(1, top.indices) - p)
+        assert (back.double() - grad).abs().max() < 2e-6   # a dozen roundings of values below 1, 2^-24 each
+        assert not y.any() and not g.any()
+
+    step()
+    check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        for a in (v, lse, loss, back):
+            a.zero_()
+        graph.replay()
+        check()
+
+
 def test_chain_with_the_epilogue(bd):
     """Processed logits go through dspark_verify_sample, greedily: with the same penalties the
     epilogue's own path gives the same tokens, and a mask keeps every token inside it."""
