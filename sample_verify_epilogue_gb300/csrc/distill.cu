@@ -8,16 +8,19 @@
 // R is summed without the members of S rather than taken as Z less their sum, which cancels when
 // they carry nearly all mass.
 //
-// Bound by bandwidth: s is read once and the gradient written once.  A CTA's span of the row
-// comes to shared memory by bulk copies and stays there between the sum and the gradient, so that
-// a call for both does not read the row twice.  Five CTAs to an SM hold 190 KB of rows: what bounds
-// the rate is how long a CTA lives, so everything between copy and store is kept short and wide.  The
-// record is one thread's work per entry; while the span arrives they make the teacher's
-// probabilities, then take the members out: each notes its logit and leaves -inf in its place, so
-// that the two loops over the span know nothing of S, and writes its member's gradient over at the
-// end.  (One warp for the record took 6000 of a CTA's 24600 cycles, taking the members out 2800.)
-// Longer spans go through the buffer in pieces, twice when both results are wanted; the second
-// read is then from L2.
+// Bound by bandwidth: s is read once and the gradient written once (4096 rows of 151936 bf16, a tenth
+// of weight 0: 369 us, 0.94 of what the copy bandwidth takes for the same bytes).  For both results a CTA's
+// span of the row comes to shared memory by bulk copies and stays there between the sum and the gradient,
+// so that the row is not read twice; an SM holds some 200 KB of rows.  What bounds the rate is how long a
+// CTA lives, so everything between copy and store is kept short and wide.  The record is one thread's
+// work per entry; while the span arrives they make the teacher's probabilities, then take the members out:
+// each notes its logit and leaves -inf in its place, so that the two loops over the span know nothing of
+// S, and writes its member's gradient over at the end.  (The record by one warp: 6000 cycles of a CTA's
+// 24600; the members looked up from inside the loops: 2800.)
+// For one result a CTA streams its span through two 16 KB buffers, six CTAs to an SM (2048 rows of 151936,
+// loss alone: 97 us, 0.85 of the bandwidth; of 32000: 34 us, 0.57, and the gradient alone 43 us, 0.90:
+// there a CTA waits for its row's ids, first pieces and joins about as long as it reads).  Spans too
+// long to keep go through the buffers twice; the second read is then from L2.
 //
 // Sums that meet cancellation (p_i log p_i/e_i) are held in 64 bits, off the path to the gradient:
 // this GPU's 64-bit rate is 1/64 of its 32-bit one.
@@ -32,12 +35,14 @@ namespace {
 constexpr int kDisVec = 4;                                   // vectors a thread holds at a time
 constexpr int kDisSpan = 4608;                               // vectors of a span kept in one piece at most
 constexpr int kDisPiece = 1024;                              // vectors of a piece of a longer one
+constexpr int kDisCtas = 5;                                  // CTAs of one-piece spans an SM takes at most
+constexpr int kSmSmem = 228 * 1024, kCtaSmem = 4 * 1024;     // an SM's shared memory; what a CTA takes beside its span
 static_assert(DSPARK_MAX_TOP_LOGITS <= kRowThreads, "a thread per record entry");
 
 enum DistillPass : int { kLoss = 1, kGrad = 2 };
 
 struct DisArgs {
-    int V, n, log_c, target_V;                               // log_c: of the cluster's size
+    int V, n, log_c, target_V;                               // log_c: log2 of C, rounded up
     int piece, np, log_slots;                                // vectors of a piece, pieces of a span; buffers (1 or 2)
     float c;                                                 // log2(e) / T
     double inv_t;
@@ -54,6 +59,7 @@ struct DisArgs {
     float* saved_out;
     const float* saved;
     int* row_status;
+    int C, span;                                             // CTAs of a row, vectors of each
 };
 
 // A value as the sum of two floats; two_sum's is exact.
@@ -84,6 +90,7 @@ struct __align__(16) DisSmem {
     int id[DSPARK_MAX_TOP_LOGITS];                           // draft ids of the record, -1: none
     unsigned seen[kRowThreads];                              // 8192 bits: hashes of the ids met
 };
+static_assert(sizeof(DisSmem) + 1024 <= kCtaSmem, "the system takes 1 KB of a CTA's");
 constexpr unsigned kSeenBits = 32 * kRowThreads;
 
 // log(v), v > 0 normal: the exponent's part in 64 bits, logf of what is left in [0.75, 1.5).
@@ -111,17 +118,22 @@ __device__ __forceinline__ void store_vec(const VocabRow<SX>& g, int i0, const u
 
 // ONE: the span is one piece.
 template <int SX, int PASS, bool ONE>
-__global__ void __launch_bounds__(kRowThreads, ONE ? 5 : 6) distill_kernel(DisArgs a) {
+__global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kernel(DisArgs a) {
     constexpr int VE = VocabRow<SX>::VE;
     constexpr bool kWantLoss = (PASS & kLoss) != 0, kWantGrad = (PASS & kGrad) != 0;
     __shared__ DisSmem s;
     extern __shared__ uint4 s_x[];                           // [slots][piece]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int C = 1 << a.log_c, rank = static_cast<int>(blockIdx.x & (C - 1));
-    const long long row = blockIdx.x >> a.log_c;
+    // only spans kept whole come in other numbers than a power of two: the streaming forms have no registers
+    // to spare at six CTAs to an SM (backward of 2048 rows of 32000: 1.5 us for two spilled)
+    constexpr bool kAnyC = ONE && kWantLoss && kWantGrad;
+    const int C = kAnyC ? a.C : 1 << a.log_c;
+    const int rank = kAnyC ? static_cast<int>(cluster_rank()) : static_cast<int>(blockIdx.x & (C - 1));
+    const long long row = kAnyC ? cluster_id() : blockIdx.x >> a.log_c;
     const VocabRow<SX> x(a.s, row, a.s_stride, a.V);
     const VocabRow<SX> g(a.g, row, a.g_stride, a.V);
-    const int k0 = x.nvec * rank >> a.log_c, k1 = x.nvec * (rank + 1) >> a.log_c;   // nvec * C < 2^31
+    const int k0 = kAnyC ? min(x.nvec, rank * a.span) : x.nvec * rank >> a.log_c;   // nvec * C < 2^31
+    const int k1 = kAnyC ? min(x.nvec, k0 + a.span) : x.nvec * (rank + 1) >> a.log_c;
     const bool same_phase = x.a0 == g.a0;
 
     if (tid == 0) {
@@ -504,21 +516,33 @@ dspark_status_t distill_args(const void* student, const dspark_teacher_t* t, con
     a->g_stride = grad ? p->grad_stride : p->student_stride;
     a->ids = t->ids; a->tl = t->logits; a->lse = t->lse; a->t2d = t->t2d;
     a->weights = p->weights; a->row_status = p->row_status;
-    // CTAs per row.  For both results at once spans of at most 72 KB, each kept in one piece; for one of
-    // them a span streams through two buffers and may be as long as the row: a CTA's latencies cost
-    // about what 40 KB do (2048 rows of 304 KB, loss alone: 101 us whole, 138 us in quarters, 198 us
-    // in eighths).  Smaller spans while that makes no more than four CTAs per SM (loss alone, 150 rows of
-    // 304 KB: 25.7 us whole, 18.7 in halves, 16.2 in quarters, 21.7 in eighths), or two where they are kept.
+    // CTAs per row.  For one result a span streams through two buffers and may be as long as the row: a
+    // CTA's latencies cost about what 40 KB do (2048 rows of 304 KB, loss alone: 101 us whole, 138 us in
+    // quarters, 198 us in eighths).  Smaller spans while that makes no more than four CTAs per SM (150 such
+    // rows: 25.7 us whole, 18.7 in halves, 16.2 in quarters, 21.7 in eighths), or two for both results.
     const int nvec = max_vectors(p->V, *sx);
-    int cluster = 1;
-    while (cluster < kMaxCluster && ((both && nvec > cluster * kDisSpan) ||
-                                     (nvec >= cluster * 512 && static_cast<long long>(p->n_rows) * 2 * cluster <= (both ? 320 : 640))))
-        cluster *= 2;
-    for (a->log_c = 0; (1 << a->log_c) < cluster;) ++a->log_c;
-    a->piece = nvec / cluster + 1;
+    int C = 1;
+    while (C < kMaxCluster && nvec >= C * 512 && static_cast<long long>(p->n_rows) * 2 * C <= (both ? 320 : 640)) C *= 2;
+    // Both results: spans kept in one piece, of which an SM holds the more bytes the better (1024 rows
+    // of 128256 bf16 in 4, 5, 6, 7, 8: 90, 85, 83, 88, 94 us for 188, 200, 209, 180, 157 KB; of 151936 in
+    // 5 to 8: 108, 100, 108, 102 us for 178, 198, 170, 186).
+    if (both)
+        for (int c = C, most = 0; c <= kMaxCluster; ++c) {
+            const int span = (nvec + c - 1) / c;
+            if (c > C && span < 512) break;
+            if (span > kDisSpan && c < kMaxCluster) continue;
+            const int held = span * min(kDisCtas, kSmSmem / (16 * span + kCtaSmem));
+            if (held >= most) {
+                most = held;
+                C = c;
+            }
+        }
+    a->C = C;
+    while ((1 << a->log_c) < C) ++a->log_c;
+    a->span = a->piece = (nvec + C - 1) / C;
     a->np = 1;
-    if (a->piece > (both ? kDisSpan : kDisPiece)) {
-        a->np = (a->piece + kDisPiece - 1) / kDisPiece;
+    if (a->span > (both ? kDisSpan : kDisPiece)) {
+        a->np = (a->span + kDisPiece - 1) / kDisPiece;
         a->piece = kDisPiece;
         a->log_slots = 1;
     }
@@ -532,8 +556,8 @@ dspark_status_t distill_launch(const DisArgs& a, int rows, void* stream) {
     if (smem > 32 * 1024 &&                                  // beyond what a launch gets unasked
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return DSPARK_ERR_CUDA;
-    const unsigned grid = static_cast<unsigned>(rows) << a.log_c;
-    const cudaError_t e = launch_cluster(kern, grid, kRowThreads, 1 << a.log_c, smem, static_cast<cudaStream_t>(stream), a);
+    const unsigned grid = static_cast<unsigned>(rows) * a.C;
+    const cudaError_t e = launch_cluster(kern, grid, kRowThreads, a.C, smem, static_cast<cudaStream_t>(stream), a);
     return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 

@@ -381,6 +381,16 @@ def test_distill(bd, rows, V, n, T, tail, form, dtype):
     check_distill(c, distill_call(bd, c, dtype, form, up=up), dtype, up=up)
 
 
+@pytest.mark.parametrize("V,dtype,shift", [(32003, "fp32", 1), (50001, "fp32", 3), (75968, "fp32", 0), (74530, "fp32", 1),
+                                           (100003, "bf16", 5)])
+def test_distill_rows_enough_to_fill(bd, V, dtype, shift):
+    """More rows than the GPU has SMs: a row goes to 3, 5, 6, 7 and 5 CTAs."""
+    rng = np.random.default_rng(V)
+    c = distill_batch(rng, 161, V, 50, dtype, 1.0, True)
+    c["w"][rng.permutation(161)[:140]] = 0
+    check_distill(c, distill_call(bd, c, dtype, "fused", 1, shift), dtype)
+
+
 @pytest.mark.parametrize("tail", [True, False])
 @pytest.mark.parametrize("form", ["fused", "two_call"])
 def test_distill_reduced_vocabulary(bd, form, tail):
