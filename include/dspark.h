@@ -341,11 +341,11 @@ typedef struct {
 /*
  * The n largest logits of every row, in order (value descending, id ascending among equals),
  * and the row's log-sum-exp: the record a drafter is trained on.
- *   out_values  [R, n] fp32, the logits themselves; -inf past the last one above -inf
+ *   out_values  [R, n] fp32, the logits themselves (-0 as 0); -inf past the last one above -inf
  *   out_ids     [R, n] int32; -1 there
  *   out_lse     [R] fp32 or NULL: log sum_t exp(x_t / T)
- * A row holding NaN or +inf, or nothing above -inf, gets DSPARK_ROW_NONFINITE, ids of -1, values
- * of -inf and a NaN log-sum-exp.
+ * row_status[r]: 0, or DSPARK_ROW_NONFINITE for a row holding NaN or +inf, or nothing above -inf, or
+ * DSPARK_ROW_INTERNAL; such a row gets ids of -1, values of -inf and a NaN log-sum-exp.
  */
 dspark_status_t dspark_top_logits(const void* logits, const dspark_top_params_t* params, float* out_values,
                                   int32_t* out_ids, float* out_lse);
@@ -393,7 +393,7 @@ typedef struct {
  *   out_grad    [R, V] or NULL: gradient of the sum of out_loss; may be student itself (same
  *               pointer and stride)
  * row_status[r]: 0, or DSPARK_ROW_BAD_TEACHER, or DSPARK_ROW_NONFINITE (a student row with NaN or
- * +inf, or nothing above -inf); such a row has a NaN loss and a gradient of 0.
+ * +inf, or nothing above -inf), or DSPARK_ROW_INTERNAL; such a row has a NaN loss and a gradient of 0.
  */
 dspark_status_t dspark_distill(const void* student, const dspark_teacher_t* teacher,
                                const dspark_distill_params_t* params, float* out_loss, float* out_saved,

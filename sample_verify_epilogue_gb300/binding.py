@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -338,6 +339,42 @@ def _dtype_of(logits):
     return d
 
 
+def _packer(cls):
+    """pack(*fields) -> the bytes of a structure: a quarter of the time that ctypes takes to make one (0 for a
+    null pointer)."""
+    kinds = {ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_float: "f", ctypes.c_void_p: "P"}
+    layout = struct.Struct("@" + "".join(kinds[t] for _, t in cls._fields_) + "0P")
+    assert layout.size == ctypes.sizeof(cls)
+    return layout.pack
+
+
+_counts, _bias, _mask, _process_params, _top_params, _teacher, _distill_params = map(_packer, (
+    dspark_counts_t, dspark_bias_t, dspark_mask_t, dspark_process_params_t, dspark_top_params_t, dspark_teacher_t,
+    dspark_distill_params_t))
+
+
+class _Calls:
+    """The entry points around the epilogue, taking packed structures."""
+
+    def __init__(self, lib):
+        for name, n in (("dspark_process_logits", 7), ("dspark_top_logits", 5), ("dspark_distill", 6),
+                        ("dspark_distill_backward", 6)):
+            fn = lib[name]
+            fn.argtypes = [ctypes.c_void_p] * n
+            fn.restype = ctypes.c_int
+            setattr(self, name, fn)
+
+
+_calls_of = None
+
+
+def _calls():
+    global _calls_of
+    if _calls_of is None:
+        _calls_of = _Calls(load_library())
+    return _calls_of
+
+
 def _rows_of(name, t, like=None):
     """(rows, V, stride) of a tensor of logits [..., V]: each row contiguous, the rows evenly spaced."""
     shape = t.shape
@@ -408,33 +445,32 @@ def dspark_process_logits(logits, rows, *, out, row_status, draft_ids=None, hist
     stride = _rows_of("logits", logits)[2]
     out_stride = stride if out is logits else _rows_of("out", out, logits)[2]
     i32, f32 = T.i32, T.f32
-    p = dspark_process_params_t(B, W - 1, V, _dtype_of(logits), stride, out_stride,
-                                _flat("rows", rows, T.u8, B * 16, dev), T.stream(dev) if stream is None else stream,
-                                _flat("row_status", row_status, i32, B, dev))
+    p = _process_params(B, W - 1, V, _dtype_of(logits), stride, out_stride, _flat("rows", rows, T.u8, B * 16, dev),
+                        T.stream(dev) if stream is None else stream, _flat("row_status", row_status, i32, B, dev))
     d = h = b = m = None
     if draft_ids is not None and W > 1:
         d = _flat("draft_ids", draft_ids, i32, B * (W - 1), dev)
     if history is not None:
         off, ids, counts = history
         nnz = ids.numel()
-        h = dspark_counts_t(_flat("history offsets", off, i32, B + 1, dev), _flat("history ids", ids, i32, nnz, dev),
-                            _flat("history counts", counts, i32, nnz, dev))
+        h = _counts(_flat("history offsets", off, i32, B + 1, dev), _flat("history ids", ids, i32, nnz, dev),
+                    _flat("history counts", counts, i32, nnz, dev))
     if bias is not None:
         off, ids, values = bias
         nnz = ids.numel()
-        b = dspark_bias_t(_flat("bias offsets", off, i32, B + 1, dev), _flat("bias ids", ids, i32, nnz, dev),
-                          _flat("bias values", values, f32, nnz, dev))
+        b = _bias(_flat("bias offsets", off, i32, B + 1, dev), _flat("bias ids", ids, i32, nnz, dev),
+                  _flat("bias values", values, f32, nnz, dev))
     if mask is not None:
         if mask.dim() != 2 or mask.dtype is not i32 or mask.get_device() != dev or (mask.stride(1) != 1 and mask.shape[1] > 1):
             raise ValueError("mask must be [n, words] int32 rows on the logits' device")
         n, words = mask.shape
         if words < (V + 31) // 32:
             raise ValueError(f"mask rows have {words} words for {V} tokens")
-        m = dspark_mask_t(mask.data_ptr(), mask.stride(0) if n > 1 else words, n,
-                          None if mask_rows is None else _flat("mask_rows", mask_rows, i32, B * W, dev))
+        m = _mask(mask.data_ptr(), mask.stride(0) if n > 1 else words, n,
+                  0 if mask_rows is None else _flat("mask_rows", mask_rows, i32, B * W, dev))
     elif mask_rows is not None:
         raise ValueError("mask_rows without a mask")
-    _launch(load_library().dspark_process_logits, dev, logits.data_ptr(), out.data_ptr(), d, h, b, m, p)
+    _launch(_calls().dspark_process_logits, dev, logits.data_ptr(), out.data_ptr(), d, h, b, m, p)
 
 
 def dspark_top_logits(logits, *, values, ids, row_status, lse=None, temperature=1.0, stream=None):
@@ -448,9 +484,9 @@ def dspark_top_logits(logits, *, values, ids, row_status, lse=None, temperature=
     R, V, stride = _rows_of("logits", logits)
     n = values.shape[-1]
     i32, f32 = T.i32, T.f32
-    p = dspark_top_params_t(R, V, _dtype_of(logits), stride, n, temperature, T.stream(dev) if stream is None else stream,
-                            _flat("row_status", row_status, i32, R, dev))
-    _launch(load_library().dspark_top_logits, dev, logits.data_ptr(), p, _flat("values", values, f32, R * n, dev),
+    p = _top_params(R, V, _dtype_of(logits), stride, n, temperature, T.stream(dev) if stream is None else stream,
+                    _flat("row_status", row_status, i32, R, dev))
+    _launch(_calls().dspark_top_logits, dev, logits.data_ptr(), p, _flat("values", values, f32, R * n, dev),
             _flat("ids", ids, i32, R * n, dev), None if lse is None else _flat("lse", lse, f32, R, dev))
 
 
@@ -461,15 +497,13 @@ def _distill_args(student, teacher_ids, teacher_logits, teacher_lse, t2d, weight
     grad_stride = V if grad is None else stride if grad is student else _rows_of("grad", grad, student)[2]
     i32, f32 = T.i32, T.f32
     n = teacher_ids.shape[-1]
-    t = dspark_teacher_t(_flat("teacher_ids", teacher_ids, i32, R * n, dev),
-                         _flat("teacher_logits", teacher_logits, f32, R * n, dev),
-                         None if teacher_lse is None else _flat("teacher_lse", teacher_lse, f32, R, dev), n,
-                         None if t2d is None else _flat("t2d", t2d, i32, t2d.numel(), dev),
-                         0 if t2d is None else t2d.numel())
-    p = dspark_distill_params_t(R, V, _dtype_of(student), stride, grad_stride, temperature,
-                                None if weights is None else _flat("weights", weights, f32, R, dev),
-                                T.stream(dev) if stream is None else stream,
-                                None if row_status is None else _flat("row_status", row_status, i32, R, dev))
+    t = _teacher(_flat("teacher_ids", teacher_ids, i32, R * n, dev), _flat("teacher_logits", teacher_logits, f32, R * n, dev),
+                 0 if teacher_lse is None else _flat("teacher_lse", teacher_lse, f32, R, dev), n,
+                 0 if t2d is None else _flat("t2d", t2d, i32, t2d.numel(), dev), 0 if t2d is None else t2d.numel())
+    p = _distill_params(R, V, _dtype_of(student), stride, grad_stride, temperature,
+                        0 if weights is None else _flat("weights", weights, f32, R, dev),
+                        T.stream(dev) if stream is None else stream,
+                        0 if row_status is None else _flat("row_status", row_status, i32, R, dev))
     return dev, R, t, p
 
 
@@ -489,7 +523,7 @@ def dspark_distill(student, teacher_ids, teacher_logits, *, loss, row_status, gr
     dev, R, t, p = _distill_args(student, teacher_ids, teacher_logits, teacher_lse, t2d, weights, temperature,
                                  row_status, grad, stream)
     f32 = _torch.f32
-    _launch(load_library().dspark_distill, dev, student.data_ptr(), t, p, _flat("loss", loss, f32, R, dev),
+    _launch(_calls().dspark_distill, dev, student.data_ptr(), t, p, _flat("loss", loss, f32, R, dev),
             None if saved is None else _flat("saved", saved, f32, 4 * R, dev), None if grad is None else grad.data_ptr())
 
 
@@ -502,5 +536,5 @@ def dspark_distill_backward(student, teacher_ids, teacher_logits, *, saved, grad
     dev, R, t, p = _distill_args(student, teacher_ids, teacher_logits, teacher_lse, t2d, weights, temperature,
                                  row_status, grad, stream)
     f32 = _torch.f32
-    _launch(load_library().dspark_distill_backward, dev, student.data_ptr(), t, p, _flat("saved", saved, f32, 4 * R, dev),
+    _launch(_calls().dspark_distill_backward, dev, student.data_ptr(), t, p, _flat("saved", saved, f32, 4 * R, dev),
             None if grad_loss is None else _flat("grad_loss", grad_loss, f32, R, dev), grad.data_ptr())

@@ -9,8 +9,8 @@
 // the other lists say about it looked up, so that it is rounded once.  A vector that the mask
 // empties is not read; in place, a vector that the mask leaves whole is neither read nor written.
 //
-// Without lists the copy runs at 0.95 of the measured bandwidth (64x9 rows of 262144 bf16, no
-// masks: 93 us); 1000 listed tokens a row add some 15 us of scattered two-byte stores (30 with loads
+// Without lists the copy runs at 0.99 of the measured bandwidth (64x9 rows of 262144 bf16, no
+// masks: 90 us); 1000 listed tokens a row add some 11 us of scattered two-byte stores (30 with loads
 // and stores that pass the L1 cache by).  Taking the tokens through shared memory into the vectors
 // before they are stored costs more than that, in barriers for every tile or in what the first store
 // waits for (104 to 130 us where this takes 89), and so does a warp to a span without barriers (117 us).
