@@ -9,7 +9,7 @@
 // they carry nearly all mass.
 //
 // Bound by bandwidth: s is read once and the gradient written once (4096 rows of 151936 bf16, a tenth
-// of weight 0: 369 us, 0.94 of what the copy bandwidth takes for the same bytes).  For both results a CTA's
+// of weight 0: 361 us, 0.97 of what the copy bandwidth takes for the same bytes).  For both results a CTA's
 // span of the row comes to shared memory by bulk copies and stays there between the sum and the gradient,
 // so that the row is not read twice; an SM holds some 200 KB of rows.  What bounds the rate is how long a
 // CTA lives, so everything between copy and store is kept short and wide.  The record is one thread's
@@ -18,12 +18,14 @@
 // S, and writes its member's gradient over at the end.  (The record by one warp: 6000 cycles of a CTA's
 // 24600; the members looked up from inside the loops: 2800.)
 // For one result a CTA streams its span through two 16 KB buffers, six CTAs to an SM (2048 rows of 151936,
-// loss alone: 97 us, 0.85 of the bandwidth; of 32000: 34 us, 0.57, and the gradient alone 43 us, 0.90:
+// loss alone: 95 us, 0.87 of the bandwidth; of 32000: 31 us, 0.62, and the gradient alone 43 us, 0.90:
 // there a CTA waits for its row's ids, first pieces and joins about as long as it reads).  Spans too
 // long to keep go through the buffers twice; the second read is then from L2.
 //
-// Sums that meet cancellation (p_i log p_i/e_i) are held in 64 bits, off the path to the gradient:
-// this GPU's 64-bit rate is 1/64 of its 32-bit one.
+// Sums that meet cancellation (p_i log p_i/e_i) are held as pairs of floats, and by 2^-k so that logits of
+// the types' lowest values do not pass fp32's range on the way.
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "vocab_rows.cuh"
@@ -45,7 +47,9 @@ struct DisArgs {
     int V, n, log_c, target_V;                               // log_c: log2 of C, rounded up
     int piece, np, log_slots;                                // vectors of a piece, pieces of a span; buffers (1 or 2)
     float c;                                                 // log2(e) / T
-    double inv_t;
+    float inv_t, inv_t_low;                                  // 1 / T in two parts
+    float down, up_again;                                    // 2^-k, 2^k
+    float unit2, unit2_low;                                  // 2 ln 2 times c, by 2^-k: the sums' own 1/T (c is rounded)
     long long s_stride, g_stride;
     const void* s;
     void* g;
@@ -62,42 +66,29 @@ struct DisArgs {
     int C, span;                                             // CTAs of a row, vectors of each
 };
 
-// A value as the sum of two floats; two_sum's is exact.
-struct TwoFloat {
-    float hi, lo;
-};
-__device__ __forceinline__ TwoFloat two_sum(float a, float b) {
-    const float s = a + b, t = s - a;
-    return TwoFloat{s, (a - (s - t)) + (b - t)};
-}
-
 struct __align__(16) DisPart {                               // what a warp tells its CTA, a CTA its cluster
     float m, rest, in;                                       // maximum; sums of e outside and inside S, by it
-    int status;
+    int status;                                              // of the row, or kDisInf
 };
+constexpr int kDisInf = 1 << 30;                             // a member with p > 0 has a logit of -inf
 
 struct __align__(16) DisSmem {
     DisPart all[kMaxCluster];                                // written by the cluster's CTAs
     DisPart warp[kRowWarps];
-    double cross_all[kMaxCluster];                           // (in the row's first CTA) written by the cluster's
-    double cross[kRowWarps];
+    alignas(16) TwoFloat cross_all[kMaxCluster];             // (in the row's first CTA) written by the cluster's
+    TwoFloat cross[kRowWarps];
     uint64_t bar[2], part_bar, cross_bar;
     alignas(16) unsigned wkey[kRowWarps];                    // largest key of the warp's record logits
     alignas(16) TwoFloat wsum[kRowWarps];                    // sum of its probabilities
     float m, total, rest, in;                                // the row's: Z = total = rest + in
     float wt, scale_in, scale_out;
     int status;
+    bool infinite;                                           // its loss
     int id[DSPARK_MAX_TOP_LOGITS];                           // draft ids of the record, -1: none
     unsigned seen[kRowThreads];                              // 8192 bits: hashes of the ids met
 };
 static_assert(sizeof(DisSmem) + 1024 <= kCtaSmem, "the system takes 1 KB of a CTA's");
 constexpr unsigned kSeenBits = 32 * kRowThreads;
-
-// log(v), v > 0 normal: the exponent's part in 64 bits, logf of what is left in [0.75, 1.5).
-__device__ __forceinline__ double log_split(float v) {
-    const int e = (__float_as_int(v) - 0x3F400000) >> 23;
-    return kLn2 * e + static_cast<double>(logf(__int_as_float(__float_as_int(v) - (e << 23))));
-}
 
 template <int SX>
 __device__ __forceinline__ void store_vec(const VocabRow<SX>& g, int i0, const uint4& w, bool same_phase) {
@@ -146,7 +137,7 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
         fence_mbar_init();
         if (kWantLoss && C > 1) {
             mbar_arrive_expect_tx(&s.part_bar, sizeof(DisPart) * C);
-            mbar_arrive_expect_tx(&s.cross_bar, sizeof(double) * C);
+            mbar_arrive_expect_tx(&s.cross_bar, sizeof(TwoFloat) * C);
         }
     }
     s.seen[tid] = 0u;
@@ -209,7 +200,7 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
         const float tmax = key_to_f(top);
         if (id >= 0) {
             if (t > -INFINITY) {
-                const float ih = static_cast<float>(a.inv_t), il = static_cast<float>(a.inv_t - static_cast<double>(ih));
+                const float ih = a.inv_t, il = a.inv_t_low;
                 if (a.lse) {                                 // 1 - sum p is what is left of the mass: p to its last bits
                     const float prod = t * ih, rest = fmaf(t, ih, -prod);
                     const TwoFloat d = two_sum(prod, -lse);
@@ -273,7 +264,6 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
     }
     if (kWantLoss && C > 1) cluster_wait();                  // the peers' barriers stand
 
-    const double ln_c = kLn2 * a.c;                          // the sums' own 1/T: c rounds log2(e)/T to fp32
     float v = -INFINITY;                                     // this thread's member: its logit
     bool here = false;                                       // ... is in this span
     // Wait for copy f of piece j; its members are noted and replaced by -inf.  Ends with a barrier.
@@ -301,7 +291,7 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
 
     // what the gradient is made with, by one thread
     auto scales = [&](float total, float rest, float in) {
-        float wt = (a.up ? w * a.up[row] : w) * static_cast<float>(a.inv_t);
+        float wt = (a.up ? w * a.up[row] : w) * a.inv_t;
         if (!a.lse) wt /= sum.hi;
         s.wt = wt;
         s.scale_in = s.scale_out = wt * (mass / total);
@@ -338,7 +328,8 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
             const float rest = warp_sum(m > -INFINITY ? es.sum * rebase(es.m, m, a.c) : es.sum);
             float in = 0.f;
             if (mine) in = warp_sum(here ? ExpRef(m > -INFINITY ? m : 0.f, a.c).of(v) : 0.f);   // NaN for NaN and +inf
-            if (lane == 0) s.warp[warp] = DisPart{m, rest, in, late ? DSPARK_ROW_INTERNAL : 0};
+            const bool infinite = mine && __any_sync(0xffffffffu, here && p > 0.f && v == -INFINITY);
+            if (lane == 0) s.warp[warp] = DisPart{m, rest, in, (late ? DSPARK_ROW_INTERNAL : 0) | (infinite ? kDisInf : 0)};
         }
         __syncthreads();
         auto join = [&](const DisPart* parts, int count) {   // by one warp, in lane order
@@ -365,19 +356,28 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
                 peer_push128(peer_addr(&s.all[rank], lane), peer_addr(&s.part_bar, lane), __float_as_uint(o.m), __float_as_uint(o.rest),
                              __float_as_uint(o.in), static_cast<uint32_t>(o.status));
         }
-        // meanwhile sum p_i (log p_i - log e_i)
-        double cross = 0.0;
-        if (mine) {
-            if (here && p > 0.f) cross = p * (static_cast<double>(lp) + lp_low - v * ln_c);
-            cross = warp_sum_d(cross);
-        }
-        if (lane == 0) s.cross[warp] = cross;
+        // sum p_i (log p_i - (v_i - from) / T) of the warp's members
+        auto cross_from = [&](float from) {
+            TwoFloat cross{0.f, 0.f};
+            if (mine) {
+                if (here && p > 0.f && v > -INFINITY) {
+                    const TwoFloat to = two_prod(p, lp * a.down);
+                    cross = TwoFloat{to.hi, fmaf(p, lp_low * a.down, to.lo)} +
+                            -(two_prod(p, v * 0.5f - from * 0.5f) * TwoFloat{a.unit2, a.unit2_low});   // halves: in range
+                }
+#pragma unroll
+                for (int o = 16; o; o >>= 1)
+                    cross = cross + TwoFloat{__shfl_xor_sync(0xffffffffu, cross.hi, o), __shfl_xor_sync(0xffffffffu, cross.lo, o)};
+            }
+            if (lane == 0) s.cross[warp] = cross;
+        };
+        cross_from(0.f);                                     // while the parts are on their way
         if (warp == 0) {
             if (C > 1) {
                 late = !bar_wait(&s.part_bar, 0);
                 o = join(s.all, C);
             }
-            int status = o.status | (late ? DSPARK_ROW_INTERNAL : 0);
+            int status = (o.status & ~kDisInf) | (late ? DSPARK_ROW_INTERNAL : 0);
             const float total = o.rest + o.in;
             if (!status && !(total == total && o.m > -INFINITY)) status = DSPARK_ROW_NONFINITE;
             if (lane == 0) {
@@ -386,16 +386,22 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
                 s.rest = o.rest;
                 s.in = o.in;
                 s.status = status;
+                s.infinite = (o.status & kDisInf) != 0;
                 if (kWantGrad) scales(total, o.rest, o.in);
             }
         }
         __syncthreads();
+        if (!ExpRef(s.m, a.c).whole) {                       // logits of the lowest values: what is left of them counts
+            cross_from(s.m);
+            __syncthreads();
+        }
         if (warp == 0) {                                     // the CTA's part of the sum to the row's first
-            cross = lane < kRowWarps ? s.cross[lane] : 0.0;
+            TwoFloat cross = lane < kRowWarps ? s.cross[lane] : TwoFloat{0.f, 0.f};
 #pragma unroll
-            for (int i = kRowWarps / 2; i; i >>= 1) cross += __shfl_xor_sync(0xffffffffu, cross, i);
+            for (int i = kRowWarps / 2; i; i >>= 1)
+                cross = cross + TwoFloat{__shfl_xor_sync(0xffffffffu, cross.hi, i), __shfl_xor_sync(0xffffffffu, cross.lo, i)};
             if (lane == 0) {
-                if (C > 1) peer_push64(peer_addr(&s.cross_all[rank], 0), peer_addr(&s.cross_bar, 0), static_cast<unsigned long long>(__double_as_longlong(cross)));
+                if (C > 1) peer_push64(peer_addr(&s.cross_all[rank], 0), peer_addr(&s.cross_bar, 0), pack2(cross.hi, cross.lo));
                 else s.cross_all[0] = cross;
             }
         }
@@ -475,15 +481,17 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
             const float m = s.m, total = s.total, rest = s.rest;
             const int status = s.status | (late ? DSPARK_ROW_INTERNAL : 0);
             const ExpRef ref(m, a.c);
-            const double psum = static_cast<double>(sum.hi) + sum.lo;
-            double loss = psum * ((ref.whole ? kLn2 * ref.r : m * ln_c) + log_split(total));
-            for (int k = 0; k < C; ++k) loss += s.cross_all[k];
-            if (!a.lse) loss = loss / psum - log_split(sum.hi);
+            auto scaled = [&](const TwoFloat& l) { return TwoFloat{l.hi * a.down, l.lo * a.down}; };
+            const TwoFloat unit = ref.whole ? TwoFloat{ref.r * a.down, 0.f} * ln2_two() : TwoFloat{0.f, 0.f};
+            TwoFloat loss = sum * (unit + scaled(log_two(total)));
+            for (int k = 0; k < C; ++k) loss = loss + s.cross_all[k];
+            if (!a.lse) loss = loss / sum + -scaled(log_two(sum.hi));
             if (p_r > 0.f && rest > 0.f) {
                 const float d = tail_excess(rest, s.in);
-                loss += p_r * (fabsf(d) < 0.5f ? log1pf(d) : logf(p_r * (total / rest)));
+                loss = loss + TwoFloat{p_r * (fabsf(d) < 0.5f ? log1pf(d) : logf(p_r * (total / rest))) * a.down, 0.f};
             }
-            a.loss[row] = status ? NAN : static_cast<float>(w * loss);
+            loss = loss * TwoFloat{w, 0.f};
+            a.loss[row] = status ? NAN : s.infinite ? w * INFINITY : fabsf(loss.hi) < INFINITY ? (loss.hi + loss.lo) * a.up_again : loss.hi;
             a.row_status[row] = status;
             if (a.saved_out) {
                 a.saved_out[4 * row] = m;
@@ -510,7 +518,16 @@ dspark_status_t distill_args(const void* student, const dspark_teacher_t* t, con
     if (grad && (p->grad_stride < p->V || reinterpret_cast<uintptr_t>(grad) % *sx)) return DSPARK_ERR_INVALID_ARG;
     if (grad == student && p->grad_stride != p->student_stride) return DSPARK_ERR_INVALID_ARG;
     a->V = p->V; a->n = t->n; a->target_V = t->target_V;
-    a->c = c; a->inv_t = 1.0 / p->temperature;
+    a->c = c;
+    const double inv_t = 1.0 / p->temperature, unit = 0.69314718055994530942 * c;
+    a->inv_t = static_cast<float>(inv_t);
+    a->inv_t_low = static_cast<float>(inv_t - static_cast<double>(a->inv_t));
+    // logits of up to 2^128 over T, p of up to 256 in sum
+    const int k = std::min(126, std::max(10, std::ilogb(unit) + 11));
+    a->down = std::ldexp(1.f, -k);
+    a->up_again = std::ldexp(1.f, k);
+    a->unit2 = static_cast<float>(std::ldexp(unit, 1 - k));
+    a->unit2_low = static_cast<float>(std::ldexp(unit, 1 - k) - static_cast<double>(a->unit2));
     a->s = student; a->s_stride = p->student_stride;
     a->g = const_cast<void*>(grad ? grad : student);         // the row's phase alone is read without a gradient
     a->g_stride = grad ? p->grad_stride : p->student_stride;

@@ -39,7 +39,7 @@ static_assert(sizeof(unsigned long long) * (kTopOwn + 2 * kTopBuf) <= kTopSmem, 
 struct TopArgs {
     int V, n, log_c;                                         // log_c: of the cluster's size
     float c;                                                 // log2(e) / T
-    double inv_t;
+    float inv_t, inv_t_low;                                  // 1 / T in two parts
     long long stride;
     const void* x;
     float* values;
@@ -441,8 +441,12 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
         }
         if (tid == kRowThreads - 1) {                        // (a warp that ranks little)
             a.row_status[row] = s.row_late ? DSPARK_ROW_INTERNAL : ok ? 0 : DSPARK_ROW_NONFINITE;
-            if (a.lse)
-                a.lse[row] = ok ? static_cast<float>(ExpRef(top, a.c).log_unit(a.inv_t) + log(static_cast<double>(s.row.sum))) : NAN;
+            if (a.lse) {
+                const ExpRef ref(top, a.c);
+                const TwoFloat unit = ref.whole ? TwoFloat{ref.r, 0.f} * ln2_two() : TwoFloat{top, 0.f} * TwoFloat{a.inv_t, a.inv_t_low};
+                const TwoFloat l = unit + log_two(s.row.sum);
+                a.lse[row] = !ok ? NAN : fabsf(unit.hi) < INFINITY ? l.hi + l.lo : unit.hi;
+            }
         }
     }
     if (C > 1) {                                             // peers' shared memory is read until here
@@ -468,7 +472,9 @@ extern "C" dspark_status_t dspark_top_logits(const void* logits, const dspark_to
     if (p->logits_stride < p->V || reinterpret_cast<uintptr_t>(logits) % sx) return DSPARK_ERR_INVALID_ARG;
 
     TopArgs a{};
-    a.V = p->V; a.n = p->n; a.c = c; a.inv_t = 1.0 / p->temperature; a.stride = p->logits_stride;
+    a.V = p->V; a.n = p->n; a.c = c; a.stride = p->logits_stride;
+    a.inv_t = static_cast<float>(1.0 / p->temperature);
+    a.inv_t_low = static_cast<float>(1.0 / p->temperature - static_cast<double>(a.inv_t));
     a.x = logits; a.values = out_values; a.ids = out_ids; a.lse = out_lse; a.row_status = p->row_status;
     // CTAs per row: one, or more, down to three quarters of a piece of the row each, while that makes no more
     // than two CTAs per SM or so: what follows the stream costs a CTA about what 100 KB do, and more

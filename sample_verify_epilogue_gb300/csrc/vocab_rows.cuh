@@ -13,7 +13,6 @@ constexpr int kRowThreads = 256;                 // threads of a row CTA
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kMaxCluster = 8;                   // CTAs that share a row at most (the portable limit)
 constexpr float kLog2E = 1.4426950408889634f;
-constexpr double kLn2 = 0.6931471805599453;
 
 // A row of V logits of SX bytes at p, cut into 16-byte vectors at the address's own 16-byte
 // boundaries: vector k holds the logits k*VE - a0 .. k*VE - a0 + VE - 1, of which the first and
@@ -187,6 +186,40 @@ __device__ __forceinline__ unsigned long long pair_of(const uint4& w, int k) {
     return pack2(elem<SX>(w, 2 * k), elem<SX>(w, 2 * k + 1));
 }
 
+// ---------------------------------------------------------------- values as the sum of two floats
+// For what meets cancellation at a row's end: some 2^-45 relative, in a few dozen cycles a step (the
+// 64-bit unit takes as long for one addition, and a thread's chain of them kept its CTA).
+struct TwoFloat {
+    float hi, lo;
+};
+__device__ __forceinline__ TwoFloat two_sum(float a, float b) {   // exact
+    const float s = a + b, t = s - a;
+    return TwoFloat{s, (a - (s - t)) + (b - t)};
+}
+__device__ __forceinline__ TwoFloat two_prod(float a, float b) {   // exact, underflow aside
+    const float p = a * b;
+    return TwoFloat{p, fmaf(a, b, -p)};
+}
+__device__ __forceinline__ TwoFloat operator+(const TwoFloat& a, const TwoFloat& b) {
+    const TwoFloat s = two_sum(a.hi, b.hi);
+    return TwoFloat{s.hi, s.lo + (a.lo + b.lo)};
+}
+__device__ __forceinline__ TwoFloat operator-(const TwoFloat& a) { return TwoFloat{-a.hi, -a.lo}; }
+__device__ __forceinline__ TwoFloat operator*(const TwoFloat& a, const TwoFloat& b) {
+    const TwoFloat p = two_prod(a.hi, b.hi);
+    return TwoFloat{p.hi, p.lo + fmaf(a.hi, b.lo, a.lo * b.hi)};
+}
+__device__ __forceinline__ TwoFloat operator/(const TwoFloat& a, const TwoFloat& b) {
+    const float q = a.hi / b.hi;
+    return TwoFloat{q, (fmaf(-q, b.hi, a.hi) + fmaf(-q, b.lo, a.lo)) / b.hi};
+}
+__device__ __forceinline__ TwoFloat ln2_two() { return TwoFloat{0.693147182464599609375f, -1.90465429995777e-9f}; }
+// log(v), v > 0 normal: the exponent's part, and logf of what is left in [0.75, 1.5).
+__device__ __forceinline__ TwoFloat log_two(float v) {
+    const int e = (__float_as_int(v) - 0x3F400000) >> 23;
+    return TwoFloat{static_cast<float>(e), 0.f} * ln2_two() + TwoFloat{logf(__int_as_float(__float_as_int(v) - (e << 23))), 0.f};
+}
+
 // ---------------------------------------------------------------- sums of exponentials
 // exp(x / T) relative to a row's or thread's maximum m, as 2^(x c - r) with c = log2(e)/T: r is m c
 // rounded up to a whole number, so that the one fma rounds nothing but its result and sums of
@@ -199,8 +232,6 @@ struct ExpRef {
     __device__ __forceinline__ float of(float x) const {     // m > -inf
         return ex2_approx(whole ? fmaf(x, c, -r) : (x - m) * c);
     }
-    // natural logarithm of what 2^0 stands for
-    __device__ __forceinline__ double log_unit(double inv_t) const { return whole ? kLn2 * r : m * inv_t; }
 };
 
 // A sum of them: m is the largest x seen (-inf while nothing above -inf was).

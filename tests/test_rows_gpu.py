@@ -359,10 +359,12 @@ def check_distill(c, got, dtype, up=None, bad=()):
         lse = None if c["lse"] is None else float(c["lse"][r])
         want, wgrad, d = O.distill_row(c["s"][r], ids, c["logits"][r], lse, c["T"], w)
         assert st[r] == (4 if np.isnan(want) else 0), r
-        if np.isfinite(want):
+        with np.errstate(over="ignore"):
+            out = np.float32(want)                           # a loss past fp32's range is infinite
+        if np.isfinite(out):
             assert abs(loss[r] - want) <= R.loss_bound(d, V, w, lse, c["T"]) + R.U * abs(want), (r, loss[r], want)
         else:
-            assert np.array_equal(loss[r], np.float32(want), equal_nan=True), (r, loss[r], want)
+            assert np.array_equal(loss[r], out, equal_nan=True), (r, loss[r], want)
         if grad is not None:
             g = 1.0 if up is None else float(up[r])
             tol = R.grad_bound(d, V, w * g, c["T"], lse, c["s"][r], dtype, wgrad * g)
@@ -432,6 +434,28 @@ def test_distill_edge_rows(bd, form, tail):
     assert got[2][1] == 0 and got[0][1] > 1e37
     d = O.distill_row(c["s"][7], c["ids"][7], c["logits"][7], None if not tail else float(c["lse"][7]), 1.0, 1.0)
     assert np.isfinite(got[1][7]).all() and np.abs(got[1][7] - d[1]).max() < 1e-5
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T", [1.0, 0.5, 3.0])
+@pytest.mark.parametrize("tail", [True, False])
+def test_distill_rows_of_the_lowest_value(bd, tail, T, dtype):
+    """Masks that write the type's lowest value: a row that is nothing else, one with all but its members at
+    it, one with all but a single other logit at it."""
+    V, n = 9001, 12
+    c = distill_batch(np.random.default_rng(16), 4, V, n, dtype, T, tail)
+    c["w"] = None
+    c["ids"][2:] = c["ids"][0]
+    c["logits"][2:] = c["logits"][0]
+    c["s"][0, :] = LOWEST[dtype]
+    members = c["ids"][1][c["ids"][1] >= 0]
+    kept = c["s"][1, members]
+    c["s"][1, :] = LOWEST[dtype]
+    c["s"][1, members] = kept
+    c["s"][2, :] = LOWEST[dtype]
+    c["s"][2, 77] = LOWEST[dtype] * 0.5
+    got = distill_call(bd, c, dtype, "fused")
+    check_distill(c, got, dtype)                             # row 1 with a tail: q_r = 0; row 2: a loss of some 1e37
 
 
 def test_distill_status(bd):
