@@ -15,7 +15,7 @@
 //      theirs: the rank is the place in the record (against the whole list: 96 us where buckets take 90,
 //      same rows, three noted; 333 rows of 50001 fp32, n = 256: 36 and 29).
 // Rows whose list would be too long (equal values, few distinct values, values bunched in one
-// group) take an exact path: bisection on the value over counts of the whole row, from that
+// group, more than a tenth of a row of 1000 to 2500 wanted) take an exact path: bisection on the value over counts of the whole row, from that
 // threshold up to the maximum; then the logits above the n-th value, and in id order as many equal
 // to it as are wanted.
 #include "vocab_rows.cuh"
@@ -28,16 +28,18 @@ constexpr int kTopVec = 4;
 constexpr int kTopBatch = kTopVec * kRowThreads;             // vectors per piece: a batch per thread
 constexpr int kTopSlots = 3;                                 // buffers
 constexpr int kTopGroups = 512;                              // of a row, whatever its cluster
-constexpr int kTopOwn = 2 * DSPARK_MAX_TOP_LOGITS;           // entries a CTA lists at most
+constexpr int kTopOwn = 1024;                                // entries a CTA lists at most
 constexpr int kTopAll = 1024;                                // entries of a row on the short path
 constexpr int kTopBuf = DSPARK_MAX_TOP_LOGITS * (kMaxCluster + 1);   // ... on the exact path: < n above, n equal per CTA
 constexpr size_t kTopSmem = sizeof(uint4) * kTopSlots * kTopBatch;
 constexpr unsigned kTopBuckets = kRowThreads;                // a thread to a bucket
 static_assert(kTopBuckets == 256, "the bucket is 8 bits of the key");
-static_assert(sizeof(unsigned long long) * (kTopOwn + 2 * kTopBuf) <= kTopSmem, "the lists take the buffers' place");
+constexpr size_t kTopLists = sizeof(unsigned long long) * (kTopOwn + 2 * kTopBuf);
+static_assert(kTopLists <= kTopSmem, "the lists take the buffers' place");
 
 struct TopArgs {
     int V, n, log_c;                                         // log_c: of the cluster's size
+    int keep;                                                // the span stays in its buffers
     float c;                                                 // log2(e) / T
     float inv_t, inv_t_low;                                  // 1 / T in two parts
     long long stride;
@@ -52,7 +54,6 @@ struct __align__(16) TopSmem {
     unsigned short gmax[kTopGroups];                         // this CTA's 512/C group maxima: upper halves of their keys
     uint64_t full[kTopSlots], empty[kTopSlots];
     ExpSum es[kRowWarps];
-    ExpSum part;                                             // this CTA's sum
     int late;                                                // a copy did not come in time
     int todo[kRowWarps][4 * 32];                             // a warp's (batch << 5 | lane) to look at again
     int n;                                                   // entries listed (passes kTopOwn when they do not fit)
@@ -84,8 +85,8 @@ template <int SX>
 __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
     constexpr int VE = VocabRow<SX>::VE;
     __shared__ TopSmem s;
-    extern __shared__ uint4 s_ring[];                        // [kTopSlots][kTopBatch]; after the stream the lists:
-    unsigned long long* const own = reinterpret_cast<unsigned long long*>(s_ring);   // this CTA's entries
+    extern __shared__ uint4 s_ring[];                        // [kTopSlots][kTopBatch]; after the stream, or behind it, the lists:
+    unsigned long long* const own = reinterpret_cast<unsigned long long*>(s_ring + (a.keep ? kTopSlots * kTopBatch : 0));   // this CTA's entries
     unsigned long long* const all = own + kTopOwn;           // the row's
     unsigned long long* const sorted = all + kTopBuf;        // the row's by buckets
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -111,6 +112,18 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
     RunSum run;
     float m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY, m4 = -INFINITY, m5 = -INFINITY;   // the thread's largest batch maxima
     int b1 = 0, b2 = 0, b3 = 0, b4 = 0;                              // where the first four were
+    auto note = [&](float bm, int j) {
+        const bool first = bm > m1, second = bm > m2, third = bm > m3, fourth = bm > m4;
+        m5 = fmaxf(m5, fminf(m4, bm));
+        m4 = third ? m3 : fmaxf(m4, bm);
+        b4 = third ? b3 : fourth ? j : b4;
+        m3 = second ? m2 : fmaxf(m3, bm);
+        b3 = second ? b2 : third ? j : b3;
+        m2 = first ? m1 : fmaxf(m2, bm);
+        b2 = first ? b1 : second ? j : b2;
+        m1 = fmaxf(m1, bm);
+        b1 = first ? j : b1;
+    };
     {
         bool late = false;
         if (warp == 0)
@@ -134,21 +147,24 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
             add_exps<SX>(run, v, bm, a.c);
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.empty[slot]);
-            const bool first = bm > m1, second = bm > m2, third = bm > m3, fourth = bm > m4;
-            m5 = fmaxf(m5, fminf(m4, bm));
-            m4 = third ? m3 : fmaxf(m4, bm);
-            b4 = third ? b3 : fourth ? j : b4;
-            m3 = second ? m2 : fmaxf(m3, bm);
-            b3 = second ? b2 : third ? j : b3;
-            m2 = first ? m1 : fmaxf(m2, bm);
-            b2 = first ? b1 : second ? j : b2;
-            m1 = fmaxf(m1, bm);
-            b1 = first ? j : b1;
+            note(bm, j);
             before = slot;
             parity_before = parity;
             if (++slot == kTopSlots) { slot = 0; parity ^= 1u; }
         }
         if (late) s.late = 1;
+    }
+    // a span of one piece: every vector is a batch of its own, or a short row had no more batches than a long
+    // record has entries (333 rows of 4096, n = 256: 44 us with batches of four, on the exact path, 12 so;
+    // n = 20: 7.9 and 8.2)
+    const bool fine = np == 1;
+    if (fine) {
+        m1 = m2 = m3 = m4 = m5 = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kTopVec; ++u) {
+            const int k = u * kRowThreads + tid;
+            note(k < k1 - k0 ? vec_max<SX>(s_ring[k]) : -INFINITY, u);
+        }
     }
 
     // ---- group maxima: 512/C of this CTA; a group is a batch, a thread, or 2 or 4 threads
@@ -165,11 +181,6 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
         }
         const ExpSum es = warp_merge(run.get(), a.c);
         if (lane == 0) s.es[warp] = es;
-        __syncthreads();
-        if (warp == 0) {
-            const ExpSum part = warp_merge(lane < kRowWarps ? s.es[lane] : ExpSum{-INFINITY, 0.f}, a.c);
-            if (lane == 0) s.part = part;
-        }
     }
     row_sync(C);
 
@@ -180,12 +191,17 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
         const unsigned* const word = reinterpret_cast<const unsigned*>(s.gmax) + (tid & ((1 << log_per) - 1));
         const unsigned two = C > 1 ? peer_ld32(peer_addr(word, tid >> log_per)) : *word;
         const unsigned x0 = two & 0xFFFFu, x1 = two >> 16;
-        ExpSum es{-INFINITY, 0.f};                           // (warp 1: the CTAs' sums, joined below)
+        ExpSum es{-INFINITY, 0.f};                           // (warp 1: the row's warps' sums, joined below)
         int late = 0;
-        if (warp == 1 && lane < C) {
-            const unsigned from = peer_addr(&s.part, lane);
-            es = ExpSum{__uint_as_float(peer_ld32(from)), __uint_as_float(peer_ld32(from + 4))};
-            late = static_cast<int>(peer_ld32(peer_addr(&s.late, lane)));
+        if (warp == 1) {
+            auto sum_of = [&](int w) {                       // of warp w mod 8 of CTA w / 8
+                if (w >= kRowWarps * C) return ExpSum{-INFINITY, 0.f};
+                const unsigned from = peer_addr(&s.es[w % kRowWarps], w / kRowWarps);
+                return ExpSum{__uint_as_float(peer_ld32(from)), __uint_as_float(peer_ld32(from + 4))};
+            };
+            static_assert(kRowWarps * kMaxCluster == 64, "two sums to a lane");
+            es = merge(sum_of(lane), sum_of(lane + 32), a.c);
+            if (lane < C) late = static_cast<int>(peer_ld32(peer_addr(&s.late, lane)));
         }
         // the largest key that n maxima reach, or a smaller one that exactly n do
         unsigned lo = __reduce_min_sync(0xffffffffu, min(x0, x1)), hi = __reduce_max_sync(0xffffffffu, max(x0, x1));
@@ -247,6 +263,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
                 ++at;
             }
     };
+    auto again = [&](int k) { return !a.keep ? load_vec<SX>(x, k, k1) : k < k1 ? s_ring[k - k0] : ninf_vec<SX>(); };
     if (ok) {
         // the batches to look at again, a lane to a vector: (lane, batch) pairs of the warp's threads
         const bool whole = m5 >= th;                         // or all its vectors
@@ -259,10 +276,12 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
         if (f3 >> lane & 1u) todo[n2 + __popc(f3 & below)] = b3 << 5 | lane;
         if (f4 >> lane & 1u) todo[n3 + __popc(f4 & below)] = b4 << 5 | lane;
         __syncwarp();
-        for (int i0 = 0; i0 < n4; i0 += 32 / kTopVec) {
-            const int i = i0 + lane / kTopVec, what = i < n4 ? todo[i] : 0;
-            const int k = k0 + (what >> 5) * kTopBatch + (lane % kTopVec) * kRowThreads + warp * 32 + (what & 31);
-            offer(i < n4 ? load_vec<SX>(x, k, k1) : ninf_vec<SX>(), k);
+        const int log_vec = fine ? 0 : 2;                    // vectors of a batch
+        static_assert(kTopVec == 4, "log_vec");
+        for (int i0 = 0; i0 < n4; i0 += 32 >> log_vec) {
+            const int i = i0 + (lane >> log_vec), what = i < n4 ? todo[i] : 0;
+            const int k = k0 + ((what >> 5 << log_vec) + (lane & ((1 << log_vec) - 1))) * kRowThreads + warp * 32 + (what & 31);
+            offer(i < n4 ? again(k) : ninf_vec<SX>(), k);
         }
         unsigned many = __ballot_sync(0xffffffffu, whole);
         while (many) {
@@ -270,7 +289,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
             many &= many - 1;
             for (int base = k0 + t; base < k1; base += 32 * kRowThreads) {
                 const int k = base + lane * kRowThreads;
-                offer(load_vec<SX>(x, k, k1), k);
+                offer(again(k), k);
             }
             // the exact path counts anew (a lane's view of the count is as good as another's)
             if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s.n) > kTopOwn)) break;
@@ -325,7 +344,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
             const float v = key_to_f(mid);
             int c = 0;
             for (int k = k0 + tid; k < k1; k += kRowThreads) {
-                const uint4 w = load_vec<SX>(x, k, k1);
+                const uint4 w = again(k);
 #pragma unroll
                 for (int q = 0; q < VE; ++q) c += elem<SX>(w, q) >= v;
             }
@@ -349,7 +368,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
         __syncthreads();
         // above v: fewer than n in the row.  Equal: the span's first n in id order
         for (int k = k0 + tid; k < k1; k += kRowThreads) {
-            const uint4 w = load_vec<SX>(x, k, k1);
+            const uint4 w = again(k);
 #pragma unroll
             for (int q = 0; q < VE; ++q) {
                 const float e = elem<SX>(w, q);
@@ -361,7 +380,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
         int equal = 0;
         for (int base = k0; base < k1 && equal < a.n; base += kRowThreads) {
             const int k = base + tid;
-            const uint4 w = load_vec<SX>(x, k, k1);
+            const uint4 w = again(k);
             int c = 0;
 #pragma unroll
             for (int q = 0; q < VE; ++q) c += elem<SX>(w, q) == v;
@@ -479,17 +498,23 @@ extern "C" dspark_status_t dspark_top_logits(const void* logits, const dspark_to
     // CTAs per row: one, or more, down to three quarters of a piece of the row each, while that makes no more
     // than two CTAs per SM or so: what follows the stream costs a CTA about what 100 KB do, and more
     // CTAs only stand in line.  Rows of 304 KB: 250 of them 25.0 us whole, 24.5 in halves, 31.5 in
-    // quarters; 80 of them 20.3, 15.5, 13.5 us and 18.6 in eighths; 16 of them 19.3, 13.8, 10.3, 9.6.
+    // quarters; 80 of them 20.3, 15.5, 13.5 us and 18.6 in eighths; 16 of them 19.3, 13.8, 10.3, 9.6 (before
+    // a row's end was shortened by 1 us).
     const int nvec = max_vectors(p->V, sx);
     int cluster = 1;
     while (cluster < kMaxCluster && nvec >= 2 * cluster * (kTopBatch * 3 / 4) && static_cast<long long>(p->n_rows) * 2 * cluster <= 330)
         cluster *= 2;
     while ((1 << a.log_c) < cluster) ++a.log_c;
     const unsigned grid = static_cast<unsigned>(p->n_rows) << a.log_c;
+    // A span that fits the buffers stays there where two CTAs to an SM are enough, and is looked at again there
+    // instead of in L2, with the lists behind it (200 rows of 20000, n = 256: 14.5 us, 13.2 so; 9 of 151936:
+    // 9.0, 8.8).
+    a.keep = (nvec + cluster - 1) / cluster <= kTopSlots * kTopBatch && grid <= 300;
+    const size_t smem = kTopSmem + (a.keep ? kTopLists : 0);
     cudaStream_t s = static_cast<cudaStream_t>(p->stream);
     auto kern = sx == 2 ? top_logits_kernel<2> : top_logits_kernel<4>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kTopSmem)) != cudaSuccess)
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kTopSmem + kTopLists)) != cudaSuccess)
         return DSPARK_ERR_CUDA;
-    const cudaError_t e = launch_cluster(kern, grid, kRowThreads, cluster, kTopSmem, s, a);
+    const cudaError_t e = launch_cluster(kern, grid, kRowThreads, cluster, smem, s, a);
     return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
