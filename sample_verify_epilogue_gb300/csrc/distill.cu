@@ -9,7 +9,7 @@
 // they carry nearly all mass.
 //
 // Bound by bandwidth: s is read once and the gradient written once (4096 rows of 151936 bf16, a tenth
-// of weight 0: 361 us, 0.97 of what the copy bandwidth takes for the same bytes).  For both results a CTA's
+// of weight 0: 359 us, 0.97 of what the copy bandwidth takes for the same bytes).  For both results a CTA's
 // span of the row comes to shared memory by bulk copies and stays there between the sum and the gradient,
 // so that the row is not read twice; an SM holds some 200 KB of rows.  What bounds the rate is how long a
 // CTA lives, so everything between copy and store is kept short and wide.  The record is one thread's
@@ -18,7 +18,7 @@
 // S, and writes its member's gradient over at the end.  (The record by one warp: 6000 cycles of a CTA's
 // 24600; the members looked up from inside the loops: 2800.)
 // For one result a CTA streams its span through two 16 KB buffers, six CTAs to an SM (2048 rows of 151936,
-// loss alone: 95 us, 0.87 of the bandwidth; of 32000: 31 us, 0.62, and the gradient alone 43 us, 0.90:
+// loss alone: 96 us, 0.86 of the bandwidth; of 32000: 31 us, 0.62, and the gradient alone 43 us, 0.90:
 // there a CTA waits for its row's ids, first pieces and joins about as long as it reads).  Spans too
 // long to keep go through the buffers twice; the second read is then from L2.
 //
