@@ -9,7 +9,7 @@
 // they carry nearly all mass.
 //
 // Bound by bandwidth: s is read once and the gradient written once (4096 rows of 151936 bf16, a tenth
-// of weight 0: 359 us, 0.97 of what the copy bandwidth takes for the same bytes).  For both results a CTA's
+// of weight 0: 356 us, 0.98 of what the copy bandwidth takes for the same bytes).  For both results a CTA's
 // span of the row comes to shared memory by bulk copies and stays there between the sum and the gradient,
 // so that the row is not read twice; an SM holds some 200 KB of rows.  What bounds the rate is how long a
 // CTA lives, so everything between copy and store is kept short and wide.  The record is one thread's
@@ -18,7 +18,7 @@
 // S, and writes its member's gradient over at the end.  (The record by one warp: 6000 cycles of a CTA's
 // 24600; the members looked up from inside the loops: 2800.)
 // For one result a CTA streams its span through two 16 KB buffers, six CTAs to an SM (2048 rows of 151936,
-// loss alone: 96 us, 0.86 of the bandwidth; of 32000: 31 us, 0.62, and the gradient alone 43 us, 0.90:
+// loss alone: 95 us, 0.87 of the bandwidth; of 32000: 31 us, 0.62, and the gradient alone 43 us, 0.90:
 // there a CTA waits for its row's ids, first pieces and joins about as long as it reads).  Spans too
 // long to keep go through the buffers twice; the second read is then from L2.
 //
@@ -78,10 +78,12 @@ struct __align__(16) DisSmem {
     alignas(16) TwoFloat cross_all[kMaxCluster];             // (in the row's first CTA) written by the cluster's
     TwoFloat cross[kRowWarps];
     uint64_t bar[2], part_bar, cross_bar;
-    alignas(16) unsigned wkey[kRowWarps];                    // largest key of the warp's record logits
-    alignas(16) TwoFloat wsum[kRowWarps];                    // sum of its probabilities
+    alignas(16) unsigned wkey[kRowWarps];                    // largest key of 32 entries' logits
+    alignas(16) TwoFloat wsum[kRowWarps];                    // sum of their probabilities
     float m, total, rest, in;                                // the row's: Z = total = rest + in
     float wt, scale_in, scale_out;
+    TwoFloat log_z, log_sum;                                 // the loss's parts by 2^-k: log Z, log of the record's sum,
+    float last;                                              // the last class's term
     int status;
     bool infinite;                                           // its loss
     int id[DSPARK_MAX_TOP_LOGITS];                           // draft ids of the record, -1: none
@@ -144,8 +146,11 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
     if (kWantLoss && C > 1) cluster_arrive_relaxed();        // before a peer can push here (the fence above orders it)
     pdl_wait();                                              // what came before in the stream
     const float w = a.weights ? a.weights[row] : 1.f;
-    int id = tid < a.n ? a.ids[row * a.n + tid] : -1;
-    const float t = tid < a.n ? a.tl[row * a.n + tid] : 0.f;
+    // the record's entries go to the last warp first, so that the first one fetches and joins meanwhile (0.3 to
+    // 0.6 us a call, but 0.5 more for n = 256); the gradient alone has no joins, and no registers to spare
+    const int ent = kWantLoss ? tid ^ (kRowThreads - 32) : tid, part = ent >> 5;
+    int id = ent < a.n ? a.ids[row * a.n + ent] : -1;
+    const float t = ent < a.n ? a.tl[row * a.n + ent] : 0.f;
     const float lse = a.lse ? a.lse[row] : 0.f;
 
     // a row that is not reduced: loss, status and gradient; the same branch in every CTA of the row
@@ -178,7 +183,7 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
         for (int f = 0; f < min(np, slots); ++f) fetch(f);
 
     // ---- the record, a thread to an entry; warps past it have nothing to do
-    const bool entries = 32 * warp < a.n;
+    const bool entries = 32 * part < a.n;
     const int n_warps = (a.n + 31) >> 5;
     bool bad = !isfinite(lse);
     if (entries) {
@@ -188,9 +193,9 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
             if (id < -1 || id >= a.V) { bad = true; id = -1; }
         }
         if (id >= 0 && !(t < INFINITY)) { bad = true; id = -1; }
-        s.id[tid] = id;
+        s.id[ent] = id;
         const unsigned key = __reduce_max_sync(0xffffffffu, id >= 0 ? fkey(t) : 0u);   // 0: no entry
-        if (lane == 0) s.wkey[warp] = key;
+        if (lane == 0) s.wkey[part] = key;
     }
     __syncthreads();
     unsigned top = 0u;
@@ -223,7 +228,7 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
         unsigned met = __ballot_sync(0xffffffffu, id >= 0 && (atomicOr(&s.seen[h >> 5], 1u << (h & 31)) >> (h & 31) & 1u));
         for (; met; met &= met - 1) {
             const int from = __ffs(met) - 1, other = __shfl_sync(0xffffffffu, id, from);
-            for (int k = lane; k < a.n; k += 32) bad = bad || (s.id[k] == other && k != 32 * warp + from);
+            for (int k = lane; k < a.n; k += 32) bad = bad || (s.id[k] == other && k != 32 * part + from);
         }
         // only -inf in the record, a log-sum-exp far below its logits
         bad = bad || (top != 0u && !a.lse && !(tmax > -INFINITY)) || !(p < INFINITY);
@@ -234,7 +239,7 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
             const TwoFloat d = two_sum(ws.hi, hi);
             ws = TwoFloat{d.hi, d.lo + (ws.lo + lo)};
         }
-        if (lane == 0) s.wsum[warp] = ws;
+        if (lane == 0) s.wsum[part] = ws;
     }
     const int status0 = __syncthreads_or(bad) ? DSPARK_ROW_BAD_TEACHER : 0;
     TwoFloat sum{0.f, 0.f};
@@ -268,10 +273,12 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
     bool here = false;                                       // ... is in this span
     // Wait for copy f of piece j; its members are noted and replaced by -inf.  Ends with a barrier.
     auto arrive = [&](int f, int j, bool note) {
+        auto wait = [&]() { late = late || !bar_wait(&s.bar[f & (slots - 1)], static_cast<unsigned>(f >> log_slots) & 1u); };
+        if (kWantLoss && warp == 0) wait();
         if (entries) {
             const int i0 = x.first(lo(j));
             const bool in = id >= max(0, i0) && id < min(a.V, x.first(hi(j)));
-            if (warp == 0 || __any_sync(0xffffffffu, in)) late = late || !bar_wait(&s.bar[f & (slots - 1)], static_cast<unsigned>(f >> log_slots) & 1u);
+            if (kWantLoss ? warp != 0 && __any_sync(0xffffffffu, in) : part == 0 || __any_sync(0xffffffffu, in)) wait();
             if (in && note) {
                 using Bits = std::conditional_t<SX == 2, unsigned short, unsigned>;
                 Bits* const at = reinterpret_cast<Bits*>(buffer(f)) + (id - i0);
@@ -296,6 +303,21 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
         s.wt = wt;
         s.scale_in = s.scale_out = wt * (mass / total);
         if (p_r > 0.f && rest > 0.f) s.scale_out = -wt * (tail_excess(rest, in) / total);   // M/Z - p_r/R, M = 1
+    };
+
+    // what the loss is made of, by one thread
+    auto logs = [&](float m, float total, float rest, float in) {
+        auto scaled = [&](const TwoFloat& l) { return TwoFloat{l.hi * a.down, l.lo * a.down}; };
+        const ExpRef ref(m, a.c);
+        const TwoFloat log_z = scaled(log_two(total));
+        s.log_z = ref.whole ? TwoFloat{ref.r * a.down, 0.f} * ln2_two() + log_z : log_z;
+        if (!a.lse) s.log_sum = scaled(log_two(sum.hi));
+        float last = 0.f;
+        if (p_r > 0.f && rest > 0.f) {
+            const float d = tail_excess(rest, in);
+            last = p_r * (fabsf(d) < 0.5f ? log1pf(d) : logf(p_r * (total / rest))) * a.down;
+        }
+        s.last = last;
     };
 
     // ---- Z and R
@@ -388,6 +410,7 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
                 s.status = status;
                 s.infinite = (o.status & kDisInf) != 0;
                 if (kWantGrad) scales(total, o.rest, o.in);
+                else logs(o.m, total, o.rest, o.in);
             }
         }
         __syncthreads();
@@ -480,16 +503,11 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
         if (lane == 0) {
             const float m = s.m, total = s.total, rest = s.rest;
             const int status = s.status | (late ? DSPARK_ROW_INTERNAL : 0);
-            const ExpRef ref(m, a.c);
-            auto scaled = [&](const TwoFloat& l) { return TwoFloat{l.hi * a.down, l.lo * a.down}; };
-            const TwoFloat unit = ref.whole ? TwoFloat{ref.r * a.down, 0.f} * ln2_two() : TwoFloat{0.f, 0.f};
-            TwoFloat loss = sum * (unit + scaled(log_two(total)));
+            if (kWantGrad) logs(m, total, rest, s.in);
+            TwoFloat loss = sum * s.log_z;
             for (int k = 0; k < C; ++k) loss = loss + s.cross_all[k];
-            if (!a.lse) loss = loss / sum + -scaled(log_two(sum.hi));
-            if (p_r > 0.f && rest > 0.f) {
-                const float d = tail_excess(rest, s.in);
-                loss = loss + TwoFloat{p_r * (fabsf(d) < 0.5f ? log1pf(d) : logf(p_r * (total / rest))) * a.down, 0.f};
-            }
+            if (!a.lse) loss = loss / sum + -s.log_sum;
+            loss = loss + TwoFloat{s.last, 0.f};
             loss = loss * TwoFloat{w, 0.f};
             a.loss[row] = status ? NAN : s.infinite ? w * INFINITY : fabsf(loss.hi) < INFINITY ? (loss.hi + loss.lo) * a.up_again : loss.hi;
             a.row_status[row] = status;
