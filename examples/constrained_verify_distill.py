@@ -78,7 +78,7 @@ def run(rounds=30, B=32, K=4, V=32000, draft_V=8000, hidden=16, n=64, seed=0, sa
         drafts = torch.multinomial(q.view(-1, draft_V), 1, generator=g).view(B, K)
         drafts = subset[drafts].to(torch.int32)
 
-        # the grammar of this round: one position in two is free, the others allow nine tokens in ten
+        # the grammar of the moment: one position in two is free, the others allow nine tokens in ten
         allowed = torch.rand(B * W, (V + 31) // 32, 32, generator=g, device=dev) < 0.9
         words = (allowed * bit).sum(-1)
         mask = torch.where(words >= 1 << 31, words - (1 << 32), words).to(torch.int32)

@@ -65,7 +65,7 @@ def sum_bound(V):
 
 def loss_bound(d, V, weight, lse, temperature):
     """Bound of the loss of one row from its float64 parts: the normaliser's logarithm, each p's
-    rounding (its logarithm's terms are u relative each; expf 2u; joining n of them in 64 bits)
+    rounding (its logarithm's terms are u relative each; expf 2u; joining n of them in pairs of floats)
     against the ratio it multiplies, the tail's likewise."""
     if d is None:
         return 0.0

@@ -229,6 +229,23 @@ def test_top(bd, rows, V, n, T, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows", [7, 301])
+@pytest.mark.parametrize("V", [255, 1024, 1030, 2049, 4096, 8185, 8193, 24600])
+def test_top_short_rows(bd, V, rows, dtype):
+    """Records that take much of a row, where a row has few vectors to a thread: few rows (spread over CTAs,
+    looked at again in shared memory) and many; grammars that leave less than the record wants; ties."""
+    rng = np.random.default_rng(V)
+    x = rng.normal(0, 3, (rows, V))
+    x[1, rng.permutation(V)[:V - 100]] = -np.inf
+    x[2] = np.round(x[2])
+    x[3, : V // 2] = -np.inf
+    x[4] = np.sort(x[4])
+    for n in (1, 200, 256):
+        y = R.rounded(x, dtype)
+        check_top(y, n, 1.3, top_call(bd, y, dtype, n, 1.3, 1, 3 if n == 200 else 0))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("kind", ["equal", "ascending", "descending", "two_values", "zeros", "mostly_masked", "lowest", "negative"])
 @pytest.mark.parametrize("n", [1, 50, 256])
 def test_top_hard_rows(bd, kind, n, dtype):
