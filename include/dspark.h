@@ -382,7 +382,8 @@ typedef struct {
  *               class, which the student gives q_r = sum of q outside S;
  *   lse NULL:   p = softmax of z over S, p_r = 0.
  *   L = sum_S p_i log(p_i / q_i) + p_r log(p_r / q_r)   (terms with p = 0, and the last with
- *       q_r = 0, are 0)
+ *       q_r = 0, are 0; a q_r below 2^-4194304, as masks of the type's lowest value leave it,
+ *       counts as 0)
  *   out_loss[r] = w_r L
  *   grad[r][v]  = w_r / T * (M q_v - p_v)               v in S, M = sum p_i + p_r
  *                 w_r / T * q_v (M - p_r / q_r)         v not in S

@@ -6,7 +6,9 @@
 //   L = sum_S p_i (log p_i - log e_i + log Z) + p_r log(p_r Z / R)
 //   dL/ds_v = (e_v a - p_v / T) in S, e_v b outside,  a = M / (Z T),  b = (M/Z - p_r/R) / T
 // R is summed without the members of S rather than taken as Z less their sum, which cancels when
-// they carry nearly all mass.
+// they carry nearly all mass, and both sums have a maximum of their own: by the row's, R would vanish where a
+// member lies 87 T above everything outside S, with p_r log(p_r Z / R) and the gradient there, which then is
+// -p_r e_v / R.  Only where R / Z is below 2^-kDisApart (masks of the type's lowest value) does it count as 0.
 //
 // Bound by bandwidth: s is read once and the gradient written once (4096 rows of 151936 bf16, a tenth
 // of weight 0: 356 us, 0.98 of what the copy bandwidth takes for the same bytes).  For both results a CTA's
@@ -66,26 +68,34 @@ struct DisArgs {
     int C, span;                                             // CTAs of a row, vectors of each
 };
 
-struct __align__(16) DisPart {                               // what a warp tells its CTA, a CTA its cluster
-    float m, rest, in;                                       // maximum; sums of e outside and inside S, by it
-    int status;                                              // of the row, or kDisInf
+struct __align__(16) DisCross {                              // a CTA's part of the loss
+    TwoFloat sum;
+    int flags, unused;                                       // status bits, or kDisInf
 };
 constexpr int kDisInf = 1 << 30;                             // a member with p > 0 has a logit of -inf
+// powers of two between the units of Z and R: from here on R is nothing beside Z; up to here fp32 holds R by Z's
+constexpr float kDisApart = 4194304.f, kDisNear = 96.f;
+
+struct DisRow {                                              // a row's sums
+    ExpSum out;                                              // outside S, by the maximum there
+    float m, apart;                                          // the row's maximum; powers of two by which its unit is larger than out's
+    float in_m, out_m, total;                                // the sums by m; Z by m, NaN when there is none
+};
 
 struct __align__(16) DisSmem {
-    DisPart all[kMaxCluster];                                // written by the cluster's CTAs
-    DisPart warp[kRowWarps];
-    alignas(16) TwoFloat cross_all[kMaxCluster];             // (in the row's first CTA) written by the cluster's
+    alignas(16) ExpSum all[2 * kMaxCluster];                 // sums in S, then outside: written by the cluster's CTAs
+    alignas(16) ExpSum warp[2 * kRowWarps];
+    DisCross cross_all[kMaxCluster];                         // (in the row's first CTA) written by the cluster's
     TwoFloat cross[kRowWarps];
     uint64_t bar[2], part_bar, cross_bar;
     alignas(16) unsigned wkey[kRowWarps];                    // largest key of 32 entries' logits
     alignas(16) TwoFloat wsum[kRowWarps];                    // sum of their probabilities
-    float m, total, rest, in;                                // the row's: Z = total = rest + in
+    DisRow row;
     float wt, scale_in, scale_out;
+    float by, out;                                           // outside S: maximum that its exponentials are by, their factor
     TwoFloat log_z, log_sum;                                 // the loss's parts by 2^-k: log Z, log of the record's sum,
     float last;                                              // the last class's term
-    int status;
-    bool infinite;                                           // its loss
+    int flags;                                               // of this CTA
     int id[DSPARK_MAX_TOP_LOGITS];                           // draft ids of the record, -1: none
     unsigned seen[kRowThreads];                              // 8192 bits: hashes of the ids met
 };
@@ -130,6 +140,7 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
     const bool same_phase = x.a0 == g.a0;
 
     if (tid == 0) {
+        s.flags = 0;
         mbar_init(&s.bar[0], 1);
         mbar_init(&s.bar[1], 1);
         if (kWantLoss && C > 1) {
@@ -138,8 +149,8 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
         }
         fence_mbar_init();
         if (kWantLoss && C > 1) {
-            mbar_arrive_expect_tx(&s.part_bar, sizeof(DisPart) * C);
-            mbar_arrive_expect_tx(&s.cross_bar, sizeof(TwoFloat) * C);
+            mbar_arrive_expect_tx(&s.part_bar, sizeof(ExpSum) * 2 * C);
+            mbar_arrive_expect_tx(&s.cross_bar, sizeof(DisCross) * C);
         }
     }
     s.seen[tid] = 0u;
@@ -254,7 +265,7 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
         p_r = fmaxf((1.f - sum.hi) - sum.lo, 0.f);
         if (p_r > 0.f) mass = 1.f;
     }
-    // p_r Z / R - 1 for Z = R + in, p_r = 1 - sum: without the difference of the two near ones
+    // p_r Z / R - 1 for Z = R + in (both by one maximum), p_r = 1 - sum: without the difference of the two near ones
     auto tail_excess = [&](float rest, float in) {
         const float z = sum.hi * rest;
         return ((fmaf(p_r, in, -z) - fmaf(sum.hi, rest, -z)) - sum.lo * rest) / rest;
@@ -273,7 +284,11 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
     bool here = false;                                       // ... is in this span
     // Wait for copy f of piece j; its members are noted and replaced by -inf.  Ends with a barrier.
     auto arrive = [&](int f, int j, bool note) {
-        auto wait = [&]() { late = late || !bar_wait(&s.bar[f & (slots - 1)], static_cast<unsigned>(f >> log_slots) & 1u); };
+        auto wait = [&]() {
+            if (late || bar_wait(&s.bar[f & (slots - 1)], static_cast<unsigned>(f >> log_slots) & 1u)) return;
+            late = true;
+            if (kWantLoss) atomicOr(&s.flags, DSPARK_ROW_INTERNAL);
+        };
         if (kWantLoss && warp == 0) wait();
         if (entries) {
             const int i0 = x.first(lo(j));
@@ -296,26 +311,37 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
         if (warp == 0) fetch(f);
     };
 
+    auto has_tail = [&](const DisRow& r) { return p_r > 0.f && r.out.sum > 0.f && r.apart < kDisApart; };
+
+    // the gradient's factor outside S, b T, by one thread
+    auto outside = [&](const DisRow& r) {
+        const bool tail = has_tail(r);                       // M/Z - p_r/R, M = 1
+        s.by = tail ? r.out.m : r.m;
+        if (tail && r.apart >= kDisNear) return s.out = -p_r / r.out.sum;
+        return s.out = !tail ? mass / r.total : -(tail_excess(r.out_m, r.in_m) / r.total) * ex2_approx(-r.apart);
+    };
     // what the gradient is made with, by one thread
-    auto scales = [&](float total, float rest, float in) {
+    auto scales = [&](float total, float out) {
         float wt = (a.up ? w * a.up[row] : w) * a.inv_t;
         if (!a.lse) wt /= sum.hi;
         s.wt = wt;
-        s.scale_in = s.scale_out = wt * (mass / total);
-        if (p_r > 0.f && rest > 0.f) s.scale_out = -wt * (tail_excess(rest, in) / total);   // M/Z - p_r/R, M = 1
+        s.scale_in = wt * (mass / total);
+        s.scale_out = wt * out;
     };
 
     // what the loss is made of, by one thread
-    auto logs = [&](float m, float total, float rest, float in) {
+    auto logs = [&](const DisRow& r) {
         auto scaled = [&](const TwoFloat& l) { return TwoFloat{l.hi * a.down, l.lo * a.down}; };
-        const ExpRef ref(m, a.c);
-        const TwoFloat log_z = scaled(log_two(total));
+        const ExpRef ref(r.m, a.c);
+        const TwoFloat log_z = scaled(log_two(r.total));
         s.log_z = ref.whole ? TwoFloat{ref.r * a.down, 0.f} * ln2_two() + log_z : log_z;
         if (!a.lse) s.log_sum = scaled(log_two(sum.hi));
         float last = 0.f;
-        if (p_r > 0.f && rest > 0.f) {
-            const float d = tail_excess(rest, in);
-            last = p_r * (fabsf(d) < 0.5f ? log1pf(d) : logf(p_r * (total / rest))) * a.down;
+        if (has_tail(r)) {
+            const bool near = r.apart < kDisNear;
+            const float x = near ? tail_excess(r.out_m, r.in_m) : 1.f;
+            last = fabsf(x) < 0.5f ? log1pf(x) : fmaf(near ? 0.f : r.apart, ln2_two().hi, logf(p_r * (r.total / (near ? r.out_m : r.out.sum))));
+            last *= p_r * a.down;
         }
         s.last = last;
     };
@@ -345,44 +371,58 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
         // the warp's part, then the CTA's to every CTA of the row, then the row's
         const bool mine = entries && __any_sync(0xffffffffu, here);
         {
-            // a member that is NaN is left out of the maximum and shows in the sum
-            const float m = key_to_f(__reduce_max_sync(0xffffffffu, max(fkey(es.m), v == v ? fkey(v) : 0u)));
-            const float rest = warp_sum(m > -INFINITY ? es.sum * rebase(es.m, m, a.c) : es.sum);
-            float in = 0.f;
-            if (mine) in = warp_sum(here ? ExpRef(m > -INFINITY ? m : 0.f, a.c).of(v) : 0.f);   // NaN for NaN and +inf
-            const bool infinite = mine && __any_sync(0xffffffffu, here && p > 0.f && v == -INFINITY);
-            if (lane == 0) s.warp[warp] = DisPart{m, rest, in, (late ? DSPARK_ROW_INTERNAL : 0) | (infinite ? kDisInf : 0)};
+            const float m_out = key_to_f(__reduce_max_sync(0xffffffffu, fkey(es.m)));
+            const float rest = warp_sum(m_out > -INFINITY ? es.sum * rebase(es.m, m_out, a.c) : es.sum);
+            ExpSum in{-INFINITY, 0.f};
+            if (mine) {
+                in.m = key_to_f(__reduce_max_sync(0xffffffffu, fkey(v)));
+                in.sum = warp_sum(here ? ExpRef(in.m > -INFINITY ? in.m : 0.f, a.c).of(v) : 0.f);   // NaN for NaN and +inf
+            }
+            if (lane == 0) {
+                s.warp[warp] = in;
+                s.warp[kRowWarps + warp] = ExpSum{m_out, rest};
+            }
         }
         __syncthreads();
-        auto join = [&](const DisPart* parts, int count) {   // by one warp, in lane order
-            DisPart o{-INFINITY, 0.f, 0.f, 0};
-            if (lane < count) o = parts[lane];
-            const float m = key_to_f(__reduce_max_sync(0xffffffffu, fkey(o.m)));
-            const float f = m > -INFINITY ? rebase(o.m, m, a.c) : 1.f;
-            o.rest = lane < count ? o.rest * f : 0.f;
-            o.in = lane < count ? o.in * f : 0.f;
+        // by one warp, in lane order: the sums in S in lanes 0 to 7, outside in 8 to 15; every lane has both maxima
+        static_assert(kRowWarps == 8 && kMaxCluster == 8, "eight lanes to a join");
+        float m_in = -INFINITY, m_out = -INFINITY;
+        auto join = [&](const ExpSum* parts, int count) {
+            const bool used = lane < 16 && (lane & 7) < count;
+            ExpSum o{-INFINITY, 0.f};
+            if (used) o = parts[lane];
+            const unsigned key = fkey(o.m);
+            m_in = key_to_f(__reduce_max_sync(0xffffffffu, lane < 8 ? key : 0u));
+            m_out = key_to_f(__reduce_max_sync(0xffffffffu, lane < 8 ? 0u : key));
+            const float m = lane < 8 ? m_in : m_out;
+            if (m > -INFINITY) o.sum *= rebase(o.m, m, a.c);
 #pragma unroll
-            for (int i = kMaxCluster / 2; i; i >>= 1) {
-                o.rest += __shfl_xor_sync(0xffffffffu, o.rest, i);
-                o.in += __shfl_xor_sync(0xffffffffu, o.in, i);
-            }
+            for (int i = 4; i; i >>= 1) o.sum += __shfl_xor_sync(0xffffffffu, o.sum, i);
             o.m = m;
-            o.status = __reduce_or_sync(0xffffffffu, static_cast<unsigned>(o.status));
             return o;
         };
-        static_assert(kRowWarps <= kMaxCluster, "join adds over kMaxCluster lanes");
-        DisPart o;
+        // the row's sums of what join gives, in lane 0
+        auto row_of = [&](float joined) {
+            const ExpRef i(m_in, a.c), o(m_out, a.c);
+            const float x = i.whole && o.whole ? i.r - o.r : (m_in - m_out) * a.c;   // NaN for a row of -inf
+            const float by_m = joined * ex2_approx(fminf(lane < 8 ? x : -x, 0.f));
+            const float out = __shfl_sync(0xffffffffu, joined, 8), out_m = __shfl_sync(0xffffffffu, by_m, 8);
+            return DisRow{ExpSum{m_out, out}, fmaxf(m_in, m_out), fmaxf(x, 0.f), by_m, out_m, x == x ? by_m + out_m : NAN};
+        };
+        ExpSum o;
         if (warp == 0) {
             o = join(s.warp, kRowWarps);
-            if (C > 1 && lane < C)
-                peer_push128(peer_addr(&s.all[rank], lane), peer_addr(&s.part_bar, lane), __float_as_uint(o.m), __float_as_uint(o.rest),
-                             __float_as_uint(o.in), static_cast<uint32_t>(o.status));
+            if (s.flags & DSPARK_ROW_INTERNAL) o.sum = NAN;  // no gradient from any CTA
+            if (C > 1 && lane < 16 && (lane & 7) < C)
+                peer_push64(peer_addr(&s.all[(lane & 8) + rank], lane & 7), peer_addr(&s.part_bar, lane & 7), pack2(o.m, o.sum));
         }
         // sum p_i (log p_i - (v_i - from) / T) of the warp's members
         auto cross_from = [&](float from) {
             TwoFloat cross{0.f, 0.f};
             if (mine) {
-                if (here && p > 0.f && v > -INFINITY) {
+                if (here && p > 0.f && !(v > -INFINITY)) {
+                    atomicOr(&s.flags, kDisInf);             // (or NaN, which no loss comes of either)
+                } else if (here && p > 0.f) {
                     const TwoFloat to = two_prod(p, lp * a.down);
                     cross = TwoFloat{to.hi, fmaf(p, lp_low * a.down, to.lo)} +
                             -(two_prod(p, v * 0.5f - from * 0.5f) * TwoFloat{a.unit2, a.unit2_low});   // halves: in range
@@ -399,23 +439,20 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
                 late = !bar_wait(&s.part_bar, 0);
                 o = join(s.all, C);
             }
-            int status = (o.status & ~kDisInf) | (late ? DSPARK_ROW_INTERNAL : 0);
-            const float total = o.rest + o.in;
-            if (!status && !(total == total && o.m > -INFINITY)) status = DSPARK_ROW_NONFINITE;
+            DisRow r = row_of(o.sum);
             if (lane == 0) {
-                s.m = o.m;
-                s.total = status ? NAN : total;
-                s.rest = o.rest;
-                s.in = o.in;
-                s.status = status;
-                s.infinite = (o.status & kDisInf) != 0;
-                if (kWantGrad) scales(total, o.rest, o.in);
-                else logs(o.m, total, o.rest, o.in);
+                if (late) {
+                    atomicOr(&s.flags, DSPARK_ROW_INTERNAL);
+                    r.total = NAN;
+                }
+                s.row = r;
+                if (kWantGrad) scales(r.total, outside(r));
+                else logs(r);
             }
         }
         __syncthreads();
-        if (!ExpRef(s.m, a.c).whole) {                       // logits of the lowest values: what is left of them counts
-            cross_from(s.m);
+        if (!ExpRef(s.row.m, a.c).whole) {                   // logits of the lowest values: what is left of them counts
+            cross_from(s.row.m);
             __syncthreads();
         }
         if (warp == 0) {                                     // the CTA's part of the sum to the row's first
@@ -424,22 +461,28 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
             for (int i = kRowWarps / 2; i; i >>= 1)
                 cross = cross + TwoFloat{__shfl_xor_sync(0xffffffffu, cross.hi, i), __shfl_xor_sync(0xffffffffu, cross.lo, i)};
             if (lane == 0) {
-                if (C > 1) peer_push64(peer_addr(&s.cross_all[rank], 0), peer_addr(&s.cross_bar, 0), pack2(cross.hi, cross.lo));
-                else s.cross_all[0] = cross;
+                if (C > 1)
+                    peer_push128(peer_addr(&s.cross_all[rank], 0), peer_addr(&s.cross_bar, 0), __float_as_uint(cross.hi),
+                                 __float_as_uint(cross.lo), static_cast<uint32_t>(s.flags), 0u);
+                else s.cross_all[0] = DisCross{cross, s.flags, 0};
             }
         }
     }
 
     // ---- the gradient
     if (kWantGrad) {
-        const float m = kWantLoss ? s.m : a.saved[4 * row], total = kWantLoss ? s.total : a.saved[4 * row + 1];
-        const bool ok = total > 0.f && m > -INFINITY;        // total is NaN for a row that cannot be normalised
+        const float* const saved = kWantLoss ? nullptr : a.saved + 4 * row;
+        const float total = kWantLoss ? s.row.total : saved[1], by = kWantLoss ? s.by : saved[2];
+        const bool ok = total > 0.f;                         // NaN for a row that cannot be normalised
         if (!kWantLoss) {
-            if (tid == 0) scales(total, a.saved[4 * row + 2], a.saved[4 * row + 3]);
+            if (tid == 0) {
+                s.row.m = saved[0];
+                scales(total, saved[3]);
+            }
             __syncthreads();
         }
         const float scale = s.scale_out;
-        const ExpRef ref(m, a.c);
+        const ExpRef ref(by, a.c);                           // of what lies outside S
         const unsigned long long c2 = pack2(a.c, a.c), r2 = pack2(-ref.r, -ref.r), s2 = pack2(scale, scale);
         auto pack = [&](const float (&f)[VE]) {
             if (SX == 2) return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4 % VE], f[5 % VE]), pack_bf16(f[6 % VE], f[7 % VE]));
@@ -491,7 +534,7 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
         }
         __syncthreads();                                     // the members' gradients go over the span's
         if (here && ok) {
-            const float d = fmaf(-p, s.wt, ref.of(v) * s.scale_in);
+            const float d = fmaf(-p, s.wt, ExpRef(s.row.m, a.c).of(v) * s.scale_in);
             unsigned char* const gp = const_cast<unsigned char*>(g.p);
             if (SX == 2) reinterpret_cast<unsigned short*>(gp)[id] = static_cast<unsigned short>(to_bits<SX>(d));
             else reinterpret_cast<float*>(gp)[id] = d;
@@ -501,21 +544,26 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
         if (C > 1) late = late || !bar_wait(&s.cross_bar, 0);
         __syncwarp();
         if (lane == 0) {
-            const float m = s.m, total = s.total, rest = s.rest;
-            const int status = s.status | (late ? DSPARK_ROW_INTERNAL : 0);
-            if (kWantGrad) logs(m, total, rest, s.in);
+            if (kWantGrad) logs(s.row);
             TwoFloat loss = sum * s.log_z;
-            for (int k = 0; k < C; ++k) loss = loss + s.cross_all[k];
+            int flags = late ? DSPARK_ROW_INTERNAL : 0;
+            for (int k = 0; k < C; ++k) {
+                loss = loss + s.cross_all[k].sum;
+                flags |= s.cross_all[k].flags;
+            }
+            const bool none = !(s.row.total == s.row.total);
+            const int status = flags & DSPARK_ROW_INTERNAL ? DSPARK_ROW_INTERNAL : none ? DSPARK_ROW_NONFINITE : 0;
             if (!a.lse) loss = loss / sum + -s.log_sum;
             loss = loss + TwoFloat{s.last, 0.f};
             loss = loss * TwoFloat{w, 0.f};
-            a.loss[row] = status ? NAN : s.infinite ? w * INFINITY : fabsf(loss.hi) < INFINITY ? (loss.hi + loss.lo) * a.up_again : loss.hi;
+            a.loss[row] = status ? NAN : flags & kDisInf ? w * INFINITY : fabsf(loss.hi) < INFINITY ? (loss.hi + loss.lo) * a.up_again : loss.hi;
             a.row_status[row] = status;
             if (a.saved_out) {
-                a.saved_out[4 * row] = m;
-                a.saved_out[4 * row + 1] = total;
-                a.saved_out[4 * row + 2] = rest;
-                a.saved_out[4 * row + 3] = s.in;
+                if (!kWantGrad) outside(s.row);
+                a.saved_out[4 * row + 3] = s.out;
+                a.saved_out[4 * row] = s.row.m;
+                a.saved_out[4 * row + 1] = status ? NAN : s.row.total;
+                a.saved_out[4 * row + 2] = s.by;
             }
         }
     }
