@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
                     const float prod = t * ih, rest = fmaf(t, ih, -prod);
                     const TwoFloat d = two_sum(prod, -lse);
                     lp = d.hi;
-                    lp_low = d.lo + fmaf(t, il, rest);
+                    lp_low = lp > -INFINITY ? d.lo + fmaf(t, il, rest) : 0.f;   // (the lowest value over T below 1)
                     p = expf(lp);
                     p = fmaf(p, lp_low, p);
                 } else {
