@@ -636,8 +636,8 @@ template <int SX, int PASS>
 dspark_status_t distill_launch(const DisArgs& a, int rows, void* stream) {
     const size_t smem = static_cast<size_t>(a.piece) * 16 << a.log_slots;
     auto kern = a.np == 1 ? distill_kernel<SX, PASS, true> : distill_kernel<SX, PASS, false>;
-    if (smem > 32 * 1024 &&                                  // beyond what a launch gets unasked
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    // beyond what a launch gets unasked; the same for every call, as another thread's may come between
+    if (smem > 32 * 1024 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 16 * kDisSpan) != cudaSuccess)
         return DSPARK_ERR_CUDA;
     const unsigned grid = static_cast<unsigned>(rows) * a.C;
     const cudaError_t e = launch_cluster(kern, grid, kRowThreads, a.C, smem, static_cast<cudaStream_t>(stream), a);

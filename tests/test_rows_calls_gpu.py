@@ -21,3 +21,36 @@ def test_teacher_logit_of_the_lowest_value(bd, form, T, lowest):
     c["logits"][[0, 1, 4], 7] = float(torch.finfo(R.TORCH[lowest]).min)
     c["logits"][1, 10:] = float(torch.finfo(R.TORCH[lowest]).min)
     check_distill(c, distill_call(bd, c, "fp32", form), "fp32")
+
+
+def test_calls_from_two_threads(bd):
+    """Loss and gradient of rows of two lengths from two host threads at once, whose CTAs keep spans of 36 and
+    of 72 KB: a launch needs its own limit whatever the other thread does at the time."""
+    import ctypes
+    import threading
+    lib, calls = bd.load_library(), []
+    for V in (72000, 144000):
+        c = distill_batch(np.random.default_rng(V), 2, V, 16, "fp32", 1.0, True)
+        t = [R.f32(c["s"]), R.i32(c["ids"]), R.f32(c["logits"]), R.f32(c["lse"]), R.f32(c["w"]), torch.zeros(2, device="cuda"),
+             R.i32([-1, -1]), torch.zeros(2, V, device="cuda")]
+        s, ids, logits, lse, w, loss, st, grad = (ctypes.c_void_p(a.data_ptr()) for a in t)
+        stream = torch.cuda.Stream()
+        teacher = bd.dspark_teacher_t(ids, logits, lse, c["ids"].shape[1], None, 0)
+        p = bd.dspark_distill_params_t(2, V, bd.DSPARK_FP32, V, V, 1.0, w, ctypes.c_void_p(stream.cuda_stream), st)
+        calls.append((c, t, stream, (s, ctypes.byref(teacher), ctypes.byref(p), loss, None, grad)))
+    torch.cuda.synchronize()
+    failed, barrier = [], threading.Barrier(2)
+
+    def work(args):
+        barrier.wait()
+        failed.append(sum(lib.dspark_distill(*args) != 0 for _ in range(20000)))
+
+    threads = [threading.Thread(target=work, args=(a[3],)) for a in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert failed == [0, 0]
+    for c, t, _, _ in calls:
+        check_distill(c, (t[5].cpu().numpy(), t[7].double().cpu().numpy(), t[6].cpu().numpy()), "fp32")
