@@ -453,13 +453,15 @@ def dspark_process_logits(logits, rows, *, out, row_status, draft_ids=None, hist
     if history is not None:
         off, ids, counts = history
         nnz = ids.numel()
-        h = _counts(_flat("history offsets", off, i32, B + 1, dev), _flat("history ids", ids, i32, nnz, dev),
-                    _flat("history counts", counts, i32, nnz, dev))
+        cols = (_flat("history offsets", off, i32, B + 1, dev), _flat("history ids", ids, i32, nnz, dev),
+                _flat("history counts", counts, i32, nnz, dev))
+        h = _counts(*cols) if nnz else None                  # (columns of no elements have no address)
     if bias is not None:
         off, ids, values = bias
         nnz = ids.numel()
-        b = _bias(_flat("bias offsets", off, i32, B + 1, dev), _flat("bias ids", ids, i32, nnz, dev),
-                  _flat("bias values", values, f32, nnz, dev))
+        cols = (_flat("bias offsets", off, i32, B + 1, dev), _flat("bias ids", ids, i32, nnz, dev),
+                _flat("bias values", values, f32, nnz, dev))
+        b = _bias(*cols) if nnz else None
     if mask is not None:
         if mask.dim() != 2 or mask.dtype is not i32 or mask.get_device() != dev or (mask.stride(1) != 1 and mask.shape[1] > 1):
             raise ValueError("mask must be [n, words] int32 rows on the logits' device")

@@ -54,3 +54,26 @@ def test_calls_from_two_threads(bd):
     assert failed == [0, 0]
     for c, t, _, _ in calls:
         check_distill(c, (t[5].cpu().numpy(), t[7].double().cpu().numpy(), t[6].cpu().numpy()), "fp32")
+
+
+@pytest.mark.parametrize("which", ["history", "bias", "both"])
+def test_process_empty_lists(bd, which):
+    """Lists without an entry in the whole batch (a first decoding step, no biases): offsets of zeros, columns
+    of no elements."""
+    B, K, V = 3, 2, 1003
+    c = process_batch(np.random.default_rng(31), B, K, V, "fp32")
+    if which in ("history", "both"):
+        c["hist"] = [[]] * B
+    if which in ("bias", "both"):
+        c["bias"] = [[]] * B
+
+    def columns(rows, *dtypes):
+        full = R.csr(rows, *dtypes)
+        return full if any(rows) else (full[0], *(a[:0] for a in full[1:]))
+
+    x, out, status = R.on_gpu(c["x"], "fp32"), R.on_gpu(np.full(c["x"].shape, 77.0), "fp32"), R.i32(np.full(B, -1))
+    bd.dspark_process_logits(
+        x, torch.from_numpy(c["rows"].view(np.uint8).copy()).cuda(), out=out, row_status=status, draft_ids=R.i32(c["drafts"]),
+        history=columns(c["hist"], np.int32, np.int32), bias=columns(c["bias"], np.int32, np.float32),
+        mask=R.pack_mask(c["allowed"]), mask_rows=R.i32(c["mask_rows"]))
+    check_process(c, out.double().cpu().numpy(), status.cpu().numpy(), "fp32", np.full(c["x"].shape, 77.0))
