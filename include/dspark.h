@@ -281,7 +281,8 @@ typedef struct {
 
 /* Grammar masks: bit t % 32 of word t / 32 of a mask row is 1 when token t is allowed (bits past
  * V are ignored).  rows[b*(K_max+1) + j] is the mask row of position j of request b, -1 for
- * a position without a grammar; rows == NULL: position (b, j) has mask row b*(K_max+1) + j. */
+ * a position without a grammar; rows == NULL: position (b, j) has mask row b*(K_max+1) + j.
+ * words == NULL takes n_rows == 0: no mask row exists, and rows, if given, has to hold -1 alone. */
 typedef struct {
     const uint32_t* words;        /* [n_rows, words_stride] */
     int64_t words_stride;         /* words between mask rows, at least (V + 31) / 32 */

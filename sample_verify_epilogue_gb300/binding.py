@@ -434,8 +434,8 @@ def dspark_process_logits(logits, rows, *, out, row_status, draft_ids=None, hist
     logits, out [B, K_max+1, V] bf16/fp32 (``out`` may be ``logits``), rows: uint8 tensor of B packed
     dspark_process_row_t (PROCESS_ROW_DTYPE), row_status [B] int32, draft_ids [B, K_max] int32,
     history (offsets [B+1], ids, counts) int32, bias (offsets [B+1] int32, ids int32, values fp32),
-    mask [n, words >= ceil(V/32)] int32 bits of the allowed tokens, mask_rows [B, K_max+1] int32 rows of
-    mask (-1: no grammar) or None (row b*(K_max+1) + j) -- all CUDA tensors.
+    mask [n, words >= ceil(V/32)] int32 bits of the allowed tokens (n may be 0 beside mask_rows), mask_rows
+    [B, K_max+1] int32 rows of mask (-1: no grammar) or None (row b*(K_max+1) + j) -- all CUDA tensors.
     """
     T = _t()
     dev = _device_of("logits", logits)
@@ -468,6 +468,8 @@ def dspark_process_logits(logits, rows, *, out, row_status, draft_ids=None, hist
         n, words = mask.shape
         if words < (V + 31) // 32:
             raise ValueError(f"mask rows have {words} words for {V} tokens")
+        if n == 0 and mask_rows is None:
+            raise ValueError("mask has no rows")
         m = _mask(mask.data_ptr(), mask.stride(0) if n > 1 else words, n,
                   0 if mask_rows is None else _flat("mask_rows", mask_rows, i32, B * W, dev))
     elif mask_rows is not None:

@@ -104,7 +104,7 @@ __device__ void check_request(const ProcArgs& a, int b) {
                 const int t = a.d[static_cast<long long>(b) * a.Km + i];
                 if (t < 0 || t >= a.V) st |= DSPARK_ROW_BAD_DRAFT;
             }
-        if (a.mask)
+        if (a.mask || a.mask_rows)                           // (mask rows of no mask: all have to be -1)
             for (int j = tid; j <= r.num_drafts; j += kRowThreads) {
                 const int row = b * (a.Km + 1) + j, k = a.mask_rows ? a.mask_rows[row] : row;
                 if (k < -1 || k >= a.n_mask) st |= DSPARK_ROW_BAD_MASK;
@@ -364,6 +364,8 @@ extern "C" dspark_status_t dspark_process_logits(const void* logits, void* out, 
         if (mask->n_rows < 1 || mask->words_stride < (p->V + 31) / 32) return DSPARK_ERR_INVALID_ARG;
         if (reinterpret_cast<uintptr_t>(mask->words) % 4) return DSPARK_ERR_INVALID_ARG;
         if (!mask->rows && mask->n_rows < p->B * (p->K_max + 1)) return DSPARK_ERR_INVALID_ARG;
+    } else if (mask && mask->n_rows != 0) {
+        return DSPARK_ERR_INVALID_ARG;
     }
 
     ProcArgs a{};
@@ -372,9 +374,7 @@ extern "C" dspark_status_t dspark_process_logits(const void* logits, void* out, 
     a.x = logits; a.y = out; a.rows = p->rows; a.d = draft_ids;
     if (history && history->row_offsets) { a.h_off = history->row_offsets; a.h_ids = history->token_ids; a.h_cnt = history->counts; }
     if (bias && bias->row_offsets) { a.b_off = bias->row_offsets; a.b_ids = bias->token_ids; a.b_val = bias->biases; }
-    if (mask && mask->words) {
-        a.mask = mask->words; a.mask_stride = mask->words_stride; a.mask_rows = mask->rows; a.n_mask = mask->n_rows;
-    }
+    if (mask) { a.mask = mask->words; a.mask_stride = mask->words_stride; a.mask_rows = mask->rows; a.n_mask = mask->n_rows; }
     a.in_place = out == logits;
     a.row_status = p->row_status;
     // Tiles per CTA: a CTA's chain of list and mask look-ups is worth a few tiles, so more than one where

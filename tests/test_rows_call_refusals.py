@@ -1,0 +1,7 @@
+"""More of what the operators around the epilogue refuse before any CUDA call (CPU only)."""
+from tests.test_rows_refusals import bd, process  # noqa: F401
+
+
+def test_process_refuses_mask_rows_without_words(bd):  # noqa: F811
+    assert process(bd, mask=bd.dspark_mask_t(None, 4, 4, 64)) == 1
+    assert process(bd, mask=bd.dspark_mask_t(None, 4, 4, None)) == 1

@@ -77,3 +77,28 @@ def test_process_empty_lists(bd, which):
         history=columns(c["hist"], np.int32, np.int32), bias=columns(c["bias"], np.int32, np.float32),
         mask=R.pack_mask(c["allowed"]), mask_rows=R.i32(c["mask_rows"]))
     check_process(c, out.double().cpu().numpy(), status.cpu().numpy(), "fp32", np.full(c["x"].shape, 77.0))
+
+
+def test_process_mask_without_rows(bd):
+    """No mask row at all: right where no position names one, an error of the request whose position does, and
+    refused where every position has its own."""
+    from sample_verify_epilogue_gb300 import binding as b_
+    B, K, V = 3, 2, 1003
+    c = process_batch(np.random.default_rng(32), B, K, V, "fp32", masks=False)
+    c["rows"]["k"] = K
+    x, rows = R.on_gpu(c["x"], "fp32"), torch.from_numpy(c["rows"].view(np.uint8).copy()).cuda()
+    none = torch.empty(0, (V + 31) // 32, dtype=torch.int32, device="cuda")
+    c["mask_rows"] = np.full((B, K + 1), -1)
+    for bad in (False, True):
+        out, status = R.on_gpu(np.full(c["x"].shape, 77.0), "fp32"), R.i32(np.full(B, -1))
+        if bad:
+            c["mask_rows"][0, 1] = 0
+        bd.dspark_process_logits(
+            x, rows, out=out, row_status=status, draft_ids=R.i32(c["drafts"]), history=R.csr(c["hist"], np.int32, np.int32),
+            bias=R.csr(c["bias"], np.int32, np.float32), mask=none, mask_rows=R.i32(c["mask_rows"]))
+        got, st = out.double().cpu().numpy(), status.cpu().numpy()
+        assert np.array_equal(st, [b_.ROW_BAD_MASK if bad else 0, 0, 0])
+        part = {k: v[int(bad):] for k, v in c.items() if k not in ("allowed", "mask_rows")}
+        check_process(part | dict(allowed=None), got[int(bad):], st[int(bad):], "fp32", np.full(c["x"].shape, 77.0)[int(bad):])
+    with pytest.raises(ValueError):
+        bd.dspark_process_logits(x, rows, out=out, row_status=status, mask=none)
