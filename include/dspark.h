@@ -300,6 +300,8 @@ typedef struct {
     const dspark_process_row_t* rows;   /* device [B]                    */
     void*    stream;              /* cudaStream_t                        */
     int32_t* row_status;          /* device [B], required                */
+    int32_t history_nnz;          /* entries of history's and of bias's columns: */
+    int32_t bias_nnz;             /* a request whose offsets pass them is bad    */
 } dspark_process_params_t;
 
 /*

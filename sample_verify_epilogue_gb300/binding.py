@@ -82,7 +82,8 @@ class dspark_process_params_t(ctypes.Structure):
     _fields_ = [
         ("B", ctypes.c_int32), ("K_max", ctypes.c_int32), ("V", ctypes.c_int32), ("logits_dtype", ctypes.c_int32),
         ("logits_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64), ("rows", ctypes.c_void_p),
-        ("stream", ctypes.c_void_p), ("row_status", ctypes.c_void_p),
+        ("stream", ctypes.c_void_p), ("row_status", ctypes.c_void_p), ("history_nnz", ctypes.c_int32),
+        ("bias_nnz", ctypes.c_int32),
     ]
 
 
@@ -445,23 +446,22 @@ def dspark_process_logits(logits, rows, *, out, row_status, draft_ids=None, hist
     stride = _rows_of("logits", logits)[2]
     out_stride = stride if out is logits else _rows_of("out", out, logits)[2]
     i32, f32 = T.i32, T.f32
-    p = _process_params(B, W - 1, V, _dtype_of(logits), stride, out_stride, _flat("rows", rows, T.u8, B * 16, dev),
-                        T.stream(dev) if stream is None else stream, _flat("row_status", row_status, i32, B, dev))
     d = h = b = m = None
+    n_history = n_bias = 0
     if draft_ids is not None and W > 1:
         d = _flat("draft_ids", draft_ids, i32, B * (W - 1), dev)
     if history is not None:
         off, ids, counts = history
-        nnz = ids.numel()
-        cols = (_flat("history offsets", off, i32, B + 1, dev), _flat("history ids", ids, i32, nnz, dev),
-                _flat("history counts", counts, i32, nnz, dev))
-        h = _counts(*cols) if nnz else None                  # (columns of no elements have no address)
+        n_history = ids.numel()
+        at = _flat("history offsets", off, i32, B + 1, dev)
+        # (columns of no elements have no address, and none of them is read)
+        h = _counts(at, _flat("history ids", ids, i32, n_history, dev) or at,
+                    _flat("history counts", counts, i32, n_history, dev) or at)
     if bias is not None:
         off, ids, values = bias
-        nnz = ids.numel()
-        cols = (_flat("bias offsets", off, i32, B + 1, dev), _flat("bias ids", ids, i32, nnz, dev),
-                _flat("bias values", values, f32, nnz, dev))
-        b = _bias(*cols) if nnz else None
+        n_bias = ids.numel()
+        at = _flat("bias offsets", off, i32, B + 1, dev)
+        b = _bias(at, _flat("bias ids", ids, i32, n_bias, dev) or at, _flat("bias values", values, f32, n_bias, dev) or at)
     if mask is not None:
         if mask.dim() != 2 or mask.dtype is not i32 or mask.get_device() != dev or (mask.stride(1) != 1 and mask.shape[1] > 1):
             raise ValueError("mask must be [n, words] int32 rows on the logits' device")
@@ -474,6 +474,9 @@ def dspark_process_logits(logits, rows, *, out, row_status, draft_ids=None, hist
                   0 if mask_rows is None else _flat("mask_rows", mask_rows, i32, B * W, dev))
     elif mask_rows is not None:
         raise ValueError("mask_rows without a mask")
+    p = _process_params(B, W - 1, V, _dtype_of(logits), stride, out_stride, _flat("rows", rows, T.u8, B * 16, dev),
+                        T.stream(dev) if stream is None else stream, _flat("row_status", row_status, i32, B, dev), n_history,
+                        n_bias)
     _launch(_calls().dspark_process_logits, dev, logits.data_ptr(), out.data_ptr(), d, h, b, m, p)
 
 

@@ -17,7 +17,7 @@
 //
 // The first B CTAs check one request each (parameters, list order and ranges, draft ids, mask
 // rows) and write its status; they run beside the copying CTAs, whose own range checks keep every
-// access in bounds whatever the lists hold.
+// access in bounds whatever the offsets and lists hold.
 #include "vocab_rows.cuh"
 
 namespace dspark {
@@ -40,7 +40,7 @@ struct ProcArgs {
     const float* b_val;
     const unsigned* mask;
     const int* mask_rows;
-    int n_mask;
+    int n_mask, h_nnz, b_nnz;
     int in_place;
     int* row_status;
 };
@@ -82,7 +82,7 @@ __device__ void check_request(const ProcArgs& a, int b) {
     int st = ok ? 0 : DSPARK_ROW_BAD_PARAMS;
     if (a.h_off) {
         const int lo = a.h_off[b], hi = a.h_off[b + 1];
-        if (lo < 0 || hi < lo) st |= DSPARK_ROW_BAD_HISTORY;
+        if (lo < 0 || hi < lo || hi > a.h_nnz) st |= DSPARK_ROW_BAD_HISTORY;
         else
             for (int e = lo + tid; e < hi; e += kRowThreads) {
                 const int t = a.h_ids[e];
@@ -91,7 +91,7 @@ __device__ void check_request(const ProcArgs& a, int b) {
     }
     if (a.b_off) {
         const int lo = a.b_off[b], hi = a.b_off[b + 1];
-        if (lo < 0 || hi < lo) st |= DSPARK_ROW_BAD_BIAS;
+        if (lo < 0 || hi < lo || hi > a.b_nnz) st |= DSPARK_ROW_BAD_BIAS;
         else
             for (int e = lo + tid; e < hi; e += kRowThreads) {
                 const int t = a.b_ids[e];
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kRowThreads, 6) process_kernel(ProcArgs a) {
         int at = 0;
         if (off) {
             const int lo = off[b], hi = off[b + 1];
-            if (lo >= 0 && hi > lo) at = warp_lower_bound(ids, lo, hi, (warp & 1) ? i_hi : i_lo);
+            if (lo >= 0 && hi > lo && hi <= (warp < 2 ? a.h_nnz : a.b_nnz)) at = warp_lower_bound(ids, lo, hi, (warp & 1) ? i_hi : i_lo);
         }
         if ((tid & 31) == 0) s_at[warp] = at;
     };
@@ -360,6 +360,7 @@ extern "C" dspark_status_t dspark_process_logits(const void* logits, void* out, 
     if (out == logits && p->out_stride != p->logits_stride) return DSPARK_ERR_INVALID_ARG;
     if (history && history->row_offsets && (!history->token_ids || !history->counts)) return DSPARK_ERR_INVALID_ARG;
     if (bias && bias->row_offsets && (!bias->token_ids || !bias->biases)) return DSPARK_ERR_INVALID_ARG;
+    if (p->history_nnz < 0 || p->bias_nnz < 0) return DSPARK_ERR_INVALID_ARG;
     if (mask && mask->words) {
         if (mask->n_rows < 1 || mask->words_stride < (p->V + 31) / 32) return DSPARK_ERR_INVALID_ARG;
         if (reinterpret_cast<uintptr_t>(mask->words) % 4) return DSPARK_ERR_INVALID_ARG;
@@ -372,6 +373,7 @@ extern "C" dspark_status_t dspark_process_logits(const void* logits, void* out, 
     a.B = p->B; a.Km = p->K_max; a.V = p->V;
     a.x_stride = p->logits_stride; a.y_stride = p->out_stride;
     a.x = logits; a.y = out; a.rows = p->rows; a.d = draft_ids;
+    a.h_nnz = p->history_nnz; a.b_nnz = p->bias_nnz;
     if (history && history->row_offsets) { a.h_off = history->row_offsets; a.h_ids = history->token_ids; a.h_cnt = history->counts; }
     if (bias && bias->row_offsets) { a.b_off = bias->row_offsets; a.b_ids = bias->token_ids; a.b_val = bias->biases; }
     if (mask) { a.mask = mask->words; a.mask_stride = mask->words_stride; a.mask_rows = mask->rows; a.n_mask = mask->n_rows; }

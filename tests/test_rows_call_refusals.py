@@ -5,3 +5,8 @@ from tests.test_rows_refusals import bd, process  # noqa: F401
 def test_process_refuses_mask_rows_without_words(bd):  # noqa: F811
     assert process(bd, mask=bd.dspark_mask_t(None, 4, 4, 64)) == 1
     assert process(bd, mask=bd.dspark_mask_t(None, 4, 4, None)) == 1
+
+
+def test_process_refuses_list_lengths(bd):  # noqa: F811
+    assert process(bd, history_nnz=-1) == 1
+    assert process(bd, bias_nnz=-1) == 1

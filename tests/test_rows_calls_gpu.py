@@ -102,3 +102,34 @@ def test_process_mask_without_rows(bd):
         check_process(part | dict(allowed=None), got[int(bad):], st[int(bad):], "fp32", np.full(c["x"].shape, 77.0)[int(bad):])
     with pytest.raises(ValueError):
         bd.dspark_process_logits(x, rows, out=out, row_status=status, mask=none)
+
+
+@pytest.mark.parametrize("short", ["history", "bias", "no_history", "no_bias"])
+def test_process_offsets_past_the_lists(bd, short):
+    """Offsets that pass their columns are an error of their request: nothing past the columns is read, and
+    the requests before it are right."""
+    from sample_verify_epilogue_gb300 import binding as b_
+    B, K, V = 4, 2, 1003
+    c = process_batch(np.random.default_rng(33), B, K, V, "fp32")
+    c["hist"][B - 1] = c["bias"][B - 1] = [(3, 1.0), (5, 2.0), (900, 1.0)]
+    hist, bias = R.csr(c["hist"], np.int32, np.int32), R.csr(c["bias"], np.int32, np.float32)
+
+    def cut(lists, n):
+        return (lists[0], *(a[:n].clone() for a in lists[1:]))
+
+    n = 0 if short.startswith("no") else len(hist[1] if short == "history" else bias[1]) - 1
+    if short in ("history", "no_history"):
+        hist = cut(hist, n)
+        want = np.where(hist[0].cpu().numpy()[1:] > n, b_.ROW_BAD_HISTORY, 0)
+    else:
+        bias = cut(bias, n)
+        want = np.where(bias[0].cpu().numpy()[1:] > n, b_.ROW_BAD_BIAS, 0)
+    x, out, status = R.on_gpu(c["x"], "fp32"), R.on_gpu(np.full(c["x"].shape, 77.0), "fp32"), R.i32(np.full(B, -1))
+    bd.dspark_process_logits(
+        x, torch.from_numpy(c["rows"].view(np.uint8).copy()).cuda(), out=out, row_status=status, draft_ids=R.i32(c["drafts"]),
+        history=hist, bias=bias, mask=R.pack_mask(c["allowed"]), mask_rows=R.i32(c["mask_rows"]))
+    got, st = out.double().cpu().numpy(), status.cpu().numpy()
+    assert np.array_equal(st, want)
+    for b in np.nonzero(want == 0)[0]:
+        one = {k: v[b:b + 1] for k, v in c.items() if k != "allowed"} | dict(allowed=c["allowed"])
+        check_process(one, got[b:b + 1], st[b:b + 1], "fp32", np.full((1, K + 1, V), 77.0))
