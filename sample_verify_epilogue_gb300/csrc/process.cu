@@ -357,6 +357,7 @@ extern "C" dspark_status_t dspark_process_logits(const void* logits, void* out, 
     const int sx = p->logits_dtype == DSPARK_BF16 ? 2 : 4;
     if (p->logits_stride < p->V || p->out_stride < p->V) return DSPARK_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(logits) % sx || reinterpret_cast<uintptr_t>(out) % sx) return DSPARK_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(p->rows) % 4) return DSPARK_ERR_INVALID_ARG;   // (bytes, in the binding)
     if (out == logits && p->out_stride != p->logits_stride) return DSPARK_ERR_INVALID_ARG;
     if (history && history->row_offsets && (!history->token_ids || !history->counts)) return DSPARK_ERR_INVALID_ARG;
     if (bias && bias->row_offsets && (!bias->token_ids || !bias->biases)) return DSPARK_ERR_INVALID_ARG;
