@@ -106,7 +106,8 @@ __device__ __forceinline__ uint4 load_vec(const VocabRow<SX>& r, int k, int k_en
 }
 
 // One warp copies vectors [b, e) of a row to shared memory: whole ones by a bulk copy, the row's
-// ragged first and last by two lanes.  The mbarrier takes one arrival per phase.
+// ragged first and last by two lanes, whose fence puts a later bulk copy into the same buffer behind their
+// stores.  The mbarrier takes one arrival per phase.
 template <int SX>
 __device__ __forceinline__ void fetch_piece(const VocabRow<SX>& r, int b, int e, uint4* dst, uint64_t* bar) {
     const int lane = threadIdx.x & 31;
@@ -121,6 +122,7 @@ __device__ __forceinline__ void fetch_piece(const VocabRow<SX>& r, int b, int e,
     if (ragged) {
         if (lane == 1 && wb > b) dst[0] = load_vec<SX>(r, b, e);
         if (lane == 2 && we < e && we >= wb) dst[we - b] = load_vec<SX>(r, we, e);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
     }

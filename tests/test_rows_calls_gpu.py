@@ -7,7 +7,8 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 from tests import _rows as R  # noqa: E402
-from tests.test_rows_gpu import bd, check_distill, check_process, distill_batch, distill_call, process_batch  # noqa: E402,F401
+from tests.test_rows_gpu import (  # noqa: E402,F401
+    bd, check_distill, check_process, check_top, distill_batch, distill_call, process_batch, top_call)
 
 
 @pytest.mark.parametrize("lowest", ["bf16", "fp32"])
@@ -133,3 +134,25 @@ def test_process_offsets_past_the_lists(bd, short):
     for b in np.nonzero(want == 0)[0]:
         one = {k: v[b:b + 1] for k, v in c.items() if k != "allowed"} | dict(allowed=c["allowed"])
         check_process(one, got[b:b + 1], st[b:b + 1], "fp32", np.full((1, K + 1, V), 77.0))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("shift", [1, 3])
+def test_rows_that_start_inside_a_vector(bd, shift, dtype):
+    """Rows whose first and last vectors are ragged, streamed through buffers that are filled several times:
+    what was stored there for a ragged vector never shows in a later piece."""
+    rows, V, n = 200, 70001, 40
+    rng = np.random.default_rng(shift)
+    c = distill_batch(rng, rows, V, n, dtype, 1.0, True)
+    c["s"][:, 0] = R.rounded(rng.normal(30, 3, rows), dtype)     # what a stale first or last vector would show most
+    c["s"][:, V - 1] = R.rounded(rng.normal(40, 3, rows), dtype)
+    live = set(range(0, rows, 9))
+    c["w"][[r for r in range(rows) if r not in live]] = 0.0
+    up = rng.uniform(0.5, 2, rows).astype(np.float32)
+    for form in ("forward", "two_call"):
+        check_distill(c, distill_call(bd, c, dtype, form, 3, shift, up=up), dtype, up=up)
+    x = R.rounded(np.concatenate([c["s"][:24], c["s"][:24]], 1), dtype)
+    for rows_ in (24, 3):
+        check_top(x[:rows_], n, 1.0, top_call(bd, x[:rows_], dtype, n, 1.0, 3, shift))
+    many = np.repeat(x[:8], 25, 0)                               # a CTA to a row
+    check_top(many, n, 1.0, top_call(bd, many, dtype, n, 1.0, 3, shift))
