@@ -397,7 +397,8 @@ typedef struct {
  *   out_grad    [R, V] or NULL: gradient of the sum of out_loss; may be student itself (same
  *               pointer and stride)
  * row_status[r]: 0, or DSPARK_ROW_BAD_TEACHER, or DSPARK_ROW_NONFINITE (a student row with NaN or
- * +inf, or nothing above -inf), or DSPARK_ROW_INTERNAL; such a row has a NaN loss and a gradient of 0.
+ * +inf, or nothing above -inf), or DSPARK_ROW_INTERNAL; such a row has a NaN loss and a gradient of 0
+ * (after DSPARK_ROW_INTERNAL in what was late at least).
  */
 dspark_status_t dspark_distill(const void* student, const dspark_teacher_t* teacher,
                                const dspark_distill_params_t* params, float* out_loss, float* out_saved,
@@ -405,8 +406,9 @@ dspark_status_t dspark_distill(const void* student, const dspark_teacher_t* teac
 
 /*
  * The gradient of sum_r grad_loss[r] * out_loss[r], from the same student, teacher and params and
- * the out_saved of a dspark_distill call; grad_loss [R] fp32 or NULL (all 1).  row_status is not
- * written and may be NULL.
+ * the out_saved of a dspark_distill call; grad_loss [R] fp32 or NULL (all 1).  row_status may be
+ * NULL and keeps what it holds but for rows that end with DSPARK_ROW_INTERNAL here, whose gradient is 0
+ * in what was late.
  */
 dspark_status_t dspark_distill_backward(const void* student, const dspark_teacher_t* teacher,
                                         const dspark_distill_params_t* params, const float* saved,

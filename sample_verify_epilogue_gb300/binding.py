@@ -537,7 +537,8 @@ def dspark_distill(student, teacher_ids, teacher_logits, *, loss, row_status, gr
 def dspark_distill_backward(student, teacher_ids, teacher_logits, *, saved, grad, grad_loss=None, teacher_lse=None,
                             t2d=None, weights=None, temperature=1.0, row_status=None, stream=None):
     """The gradient of sum(grad_loss * loss) by the student's logits, from the inputs and the ``saved`` of
-    a dspark_distill call; grad_loss [...] fp32 or None (all 1).  ``row_status`` is not written."""
+    a dspark_distill call; grad_loss [...] fp32 or None (all 1).  ``row_status``, if given, is written for rows
+    alone that end with DSPARK_ROW_INTERNAL here."""
     if grad is None:
         raise ValueError("grad is missing")
     dev, R, t, p = _distill_args(student, teacher_ids, teacher_logits, teacher_lse, t2d, weights, temperature,

@@ -73,6 +73,7 @@ struct __align__(16) DisCross {                              // a CTA's part of 
     int flags, unused;                                       // status bits, or kDisInf
 };
 constexpr int kDisInf = 1 << 30;                             // a member with p > 0 has a logit of -inf
+constexpr int kDisStopped = 1 << 29;                         // a copy was late: no further one is asked for
 // powers of two between the units of Z and R: from here on R is nothing beside Z; up to here fp32 holds R by Z's
 constexpr float kDisApart = 4194304.f, kDisNear = 96.f;
 
@@ -164,6 +165,9 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
     const float t = ent < a.n ? a.tl[row * a.n + ent] : 0.f;
     const float lse = a.lse ? a.lse[row] : 0.f;
 
+    auto zeros = [&]() {
+        for (int k = k0 + tid; k < k1; k += kRowThreads) store_vec<SX>(g, x.first(k), make_uint4(0, 0, 0, 0), same_phase);
+    };
     // a row that is not reduced: loss, status and gradient; the same branch in every CTA of the row
     auto leave = [&](int status) {
         if (kWantLoss && rank == 0 && tid == 0) {
@@ -172,8 +176,7 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
             if (a.saved_out)
                 for (int k = 0; k < 4; ++k) a.saved_out[4 * row + k] = 0.f;
         }
-        if (kWantGrad)
-            for (int k = k0 + tid; k < k1; k += kRowThreads) store_vec<SX>(g, x.first(k), make_uint4(0, 0, 0, 0), same_phase);
+        if (kWantGrad) zeros();
         if (kWantLoss && C > 1) cluster_wait();
     };
     // The span in np pieces (the last may be short, or empty); copy number f (the pieces in turn, then
@@ -270,10 +273,14 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
         const float z = sum.hi * rest;
         return ((fmaf(p_r, in, -z) - fmaf(sum.hi, rest, -z)) - sum.lo * rest) / rest;
     };
-    bool late = false;
     if (status0 || top == 0u) {
+        bool late = false;
         if (warp == 0)
-            for (int f = 0; f < min(np, slots); ++f) late = late || !bar_wait(&s.bar[f], 0);
+            for (int f = 0; f < min(np, slots); ++f)
+                if (!bar_wait(&s.bar[f], 0)) {
+                    late = true;
+                    bar_wait(&s.bar[f], 0);                  // once more: it is in flight
+                }
         late = __syncthreads_or(late);
         leave(status0 ? status0 : late ? DSPARK_ROW_INTERNAL : 0);
         return;
@@ -282,35 +289,37 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
 
     float v = -INFINITY;                                     // this thread's member: its logit
     bool here = false;                                       // ... is in this span
+    constexpr bool kTwice = kWantLoss && kWantGrad && !ONE;  // the pieces come again for the gradient
     // Wait for copy f of piece j; its members are noted and replaced by -inf.  Ends with a barrier.
     auto arrive = [&](int f, int j, bool note) {
-        auto wait = [&]() {
-            if (late || bar_wait(&s.bar[f & (slots - 1)], static_cast<unsigned>(f >> log_slots) & 1u)) return;
-            late = true;
-            if (kWantLoss) atomicOr(&s.flags, DSPARK_ROW_INTERNAL);
-        };
-        if (kWantLoss && warp == 0) wait();
-        if (entries) {
-            const int i0 = x.first(lo(j));
-            const bool in = id >= max(0, i0) && id < min(a.V, x.first(hi(j)));
-            if (kWantLoss ? warp != 0 && __any_sync(0xffffffffu, in) : part == 0 || __any_sync(0xffffffffu, in)) wait();
-            if (in && note) {
-                using Bits = std::conditional_t<SX == 2, unsigned short, unsigned>;
-                Bits* const at = reinterpret_cast<Bits*>(buffer(f)) + (id - i0);
-                v = __uint_as_float(static_cast<uint32_t>(*at) << (SX == 2 ? 16 : 0));
-                *at = static_cast<Bits>(ninf_bits<SX>());
-                here = true;
+        const int i0 = x.first(lo(j));
+        const bool in = entries && id >= max(0, i0) && id < min(a.V, x.first(hi(j)));
+        auto parity = [&](int k) { return static_cast<unsigned>(k >> log_slots) & 1u; };
+        if ((warp == 0 || (entries && __any_sync(0xffffffffu, in))) &&
+            !copy_wait(&s.bar[f & (slots - 1)], parity(f), ONE ? nullptr : &s.flags)) {
+            if (warp == 0 && !(s.flags & kDisStopped)) {     // those in flight arrive before the CTA ends
+                for (int k = f; k < min(f + slots, kTwice ? 2 * np : np); ++k) bar_wait(&s.bar[k & (slots - 1)], parity(k));
+                atomicOr(&s.flags, kDisStopped);
             }
+            atomicOr(&s.flags, DSPARK_ROW_INTERNAL);
+        }
+        if (in && note) {
+            using Bits = std::conditional_t<SX == 2, unsigned short, unsigned>;
+            Bits* const at = reinterpret_cast<Bits*>(buffer(f)) + (id - i0);
+            v = __uint_as_float(static_cast<uint32_t>(*at) << (SX == 2 ? 16 : 0));
+            *at = static_cast<Bits>(ninf_bits<SX>());
+            here = true;
         }
         __syncthreads();
     };
     // The buffer of copy f - slots is free for copy f (entry warps have written to it).
     auto refill = [&](int f) {
         if (entries) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        const bool late = (s.flags & kDisStopped) != 0;
         __syncthreads();
-        if (warp == 0) fetch(f);
+        if (warp != 0) return;
+        if (!late) fetch(f);
     };
-
     auto has_tail = [&](const DisRow& r) { return p_r > 0.f && r.out.sum > 0.f && r.apart < kDisApart; };
 
     // the gradient's factor outside S, b T, by one thread
@@ -346,10 +355,23 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
         s.last = last;
     };
 
+    // the CTA's part of the loss to the row's first, by one warp
+    auto push_cross = [&]() {
+        if (warp != 0) return;
+        TwoFloat cross = lane < kRowWarps ? s.cross[lane] : TwoFloat{0.f, 0.f};
+#pragma unroll
+        for (int i = kRowWarps / 2; i; i >>= 1)
+            cross = cross + TwoFloat{__shfl_xor_sync(0xffffffffu, cross.hi, i), __shfl_xor_sync(0xffffffffu, cross.lo, i)};
+        if (lane != 0) return;
+        if (C > 1)
+            peer_push128(peer_addr(&s.cross_all[rank], 0), peer_addr(&s.cross_bar, 0), __float_as_uint(cross.hi),
+                         __float_as_uint(cross.lo), static_cast<uint32_t>(s.flags), 0u);
+        else s.cross_all[0] = DisCross{cross, s.flags, 0};
+    };
+
     // ---- Z and R
     if (kWantLoss) {
         RunSum run;
-        const bool twice = kWantGrad && !ONE;                // the pieces come again for the gradient
         for (int j = 0; j < np; ++j) {
             arrive(j, j, true);
             const uint4* const q0 = buffer(j);
@@ -365,7 +387,7 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
                 const uint4 q[1] = {q0[k]};
                 add_exps<SX>(run, q, vecs_max<SX>(q), a.c);
             }
-            if (!ONE && j + slots < (twice ? 2 * np : np)) refill(j + slots);
+            if (!ONE && j + slots < (kTwice ? 2 * np : np)) refill(j + slots);
         }
         const ExpSum es = run.get();
         // the warp's part, then the CTA's to every CTA of the row, then the row's
@@ -435,13 +457,14 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
         };
         cross_from(0.f);                                     // while the parts are on their way
         if (warp == 0) {
+            bool none = false;
             if (C > 1) {
-                late = !bar_wait(&s.part_bar, 0);
+                none = !bar_wait(&s.part_bar, 0, kPeerMs);
                 o = join(s.all, C);
             }
             DisRow r = row_of(o.sum);
             if (lane == 0) {
-                if (late) {
+                if (none) {
                     atomicOr(&s.flags, DSPARK_ROW_INTERNAL);
                     r.total = NAN;
                 }
@@ -455,18 +478,7 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
             cross_from(s.row.m);
             __syncthreads();
         }
-        if (warp == 0) {                                     // the CTA's part of the sum to the row's first
-            TwoFloat cross = lane < kRowWarps ? s.cross[lane] : TwoFloat{0.f, 0.f};
-#pragma unroll
-            for (int i = kRowWarps / 2; i; i >>= 1)
-                cross = cross + TwoFloat{__shfl_xor_sync(0xffffffffu, cross.hi, i), __shfl_xor_sync(0xffffffffu, cross.lo, i)};
-            if (lane == 0) {
-                if (C > 1)
-                    peer_push128(peer_addr(&s.cross_all[rank], 0), peer_addr(&s.cross_bar, 0), __float_as_uint(cross.hi),
-                                 __float_as_uint(cross.lo), static_cast<uint32_t>(s.flags), 0u);
-                else s.cross_all[0] = DisCross{cross, s.flags, 0};
-            }
-        }
+        if (!kTwice) push_cross();
     }
 
     // ---- the gradient
@@ -533,26 +545,30 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
             if (!ONE && j + slots < np) refill(f + slots);
         }
         __syncthreads();                                     // the members' gradients go over the span's
-        if (here && ok) {
+        // a piece that did not come in time leaves no gradient
+        const bool in_time = (kWantLoss && ONE) || !(s.flags & DSPARK_ROW_INTERNAL);
+        if (!in_time) zeros();
+        else if (here && ok) {
             const float d = fmaf(-p, s.wt, ExpRef(s.row.m, a.c).of(v) * s.scale_in);
             unsigned char* const gp = const_cast<unsigned char*>(g.p);
             if (SX == 2) reinterpret_cast<unsigned short*>(gp)[id] = static_cast<unsigned short>(to_bits<SX>(d));
             else reinterpret_cast<float*>(gp)[id] = d;
         }
+        if (kTwice) push_cross();                            // with what the second look at the pieces met
+        if (!kWantLoss && tid == 0 && !in_time && a.row_status) a.row_status[row] = DSPARK_ROW_INTERNAL;
     }
     if (kWantLoss && rank == 0 && warp == 0) {               // the loss
-        if (C > 1) late = late || !bar_wait(&s.cross_bar, 0);
+        const bool none = C > 1 && !bar_wait(&s.cross_bar, 0, kPeerMs);
         __syncwarp();
         if (lane == 0) {
             if (kWantGrad) logs(s.row);
             TwoFloat loss = sum * s.log_z;
-            int flags = late ? DSPARK_ROW_INTERNAL : 0;
+            int flags = none ? DSPARK_ROW_INTERNAL : 0;
             for (int k = 0; k < C; ++k) {
                 loss = loss + s.cross_all[k].sum;
                 flags |= s.cross_all[k].flags;
             }
-            const bool none = !(s.row.total == s.row.total);
-            const int status = flags & DSPARK_ROW_INTERNAL ? DSPARK_ROW_INTERNAL : none ? DSPARK_ROW_NONFINITE : 0;
+            const int status = flags & DSPARK_ROW_INTERNAL ? DSPARK_ROW_INTERNAL : s.row.total == s.row.total ? 0 : DSPARK_ROW_NONFINITE;
             if (!a.lse) loss = loss / sum + -s.log_sum;
             loss = loss + TwoFloat{s.last, 0.f};
             loss = loss * TwoFloat{w, 0.f};

@@ -54,7 +54,7 @@ struct __align__(16) TopSmem {
     unsigned short gmax[kTopGroups];                         // this CTA's 512/C group maxima: upper halves of their keys
     uint64_t full[kTopSlots], empty[kTopSlots];
     ExpSum es[kRowWarps];
-    int late;                                                // a copy did not come in time
+    int late, issued;                                        // a copy did not come in time; copies asked for until then
     int todo[kRowWarps][4 * 32];                             // a warp's (batch << 5 | lane) to look at again
     int n;                                                   // entries listed (passes kTopOwn when they do not fit)
     int cnt;                                                 // exact path: this CTA's count
@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
         fence_mbar_init();
         s.n = 0;
         s.late = 0;
+        s.issued = np;
     }
     s.bucket[tid] = 0;
     __syncthreads();
@@ -134,10 +135,11 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
         for (int j = 0; j < np; ++j) {
             if (warp == 0 && j > 0 && j + kTopSlots - 1 < np) {   // the piece before this one leaves its buffer
                 const int f = j + kTopSlots - 1;
-                late = late || !bar_wait(&s.empty[before], parity_before);
-                fetch_piece<SX>(x, k0 + f * kTopBatch, min(k1, k0 + (f + 1) * kTopBatch), s_ring + before * kTopBatch, &s.full[before]);
+                late = late || !copy_wait(&s.empty[before], parity_before);
+                if (__any_sync(0xffffffffu, late)) s.issued = min(s.issued, f);
+                else fetch_piece<SX>(x, k0 + f * kTopBatch, min(k1, k0 + (f + 1) * kTopBatch), s_ring + before * kTopBatch, &s.full[before]);
             }
-            late = late || !bar_wait(&s.full[slot], parity);
+            late = late || !copy_wait(&s.full[slot], parity);
             const uint4* const q0 = s_ring + slot * kTopBatch;
             const int cnt = min(kTopBatch, k1 - k0 - j * kTopBatch);
             uint4 v[kTopVec];
@@ -468,6 +470,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) top_logits_kernel(TopArgs a) {
             }
         }
     }
+    if (!ok && warp == 0 && s.late)                          // the last copies in flight
+        for (int f = max(0, s.issued - kTopSlots); f < s.issued; ++f) bar_wait(&s.full[f % kTopSlots], f / kTopSlots & 1);
     if (C > 1) {                                             // peers' shared memory is read until here
         cluster_arrive();
         cluster_wait();

@@ -337,16 +337,18 @@ __device__ __forceinline__ void peer_push64(unsigned a, unsigned bar, unsigned l
     asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];"
                  :: "r"(a), "l"(v), "r"(bar) : "memory");
 }
-__device__ __forceinline__ unsigned long long global_timer() {
+__device__ __forceinline__ unsigned global_ms() {            // 2^20 ns to the unit
     unsigned long long t;
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    return t;
+    return static_cast<unsigned>(t >> 20);
 }
-// Wait for an mbarrier's phase with a 2 s bound, false when it runs out; data pushed by the
+// Wait for an mbarrier's phase with a bound, false when it runs out; data pushed by the
 // cluster's CTAs is visible afterwards.  The thread sleeps up to 1 ms at a time: without the
-// hint a waiting warp polls, and takes issue slots from those that work.
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, unsigned parity) {
-    unsigned long long t0 = 0;
+// hint a waiting warp polls, and takes issue slots from those that work.  For a peer the bound is longer than what the
+// peer may wait for its copies: it pushes late rather than not at all, and to a CTA that is still there.
+constexpr unsigned kCopyMs = 2000, kPeerMs = 10 * kCopyMs;
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, unsigned parity, unsigned limit = kCopyMs, const volatile int* given_up = nullptr) {
+    unsigned t0 = 0;
     for (unsigned i = 0;; ++i) {
         unsigned ok;
         asm volatile(
@@ -355,10 +357,21 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, unsigned parity) {
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u) : "memory");
         if (ok) return true;
-        const unsigned long long t = global_timer();
+        if (given_up && (*given_up & DSPARK_ROW_INTERNAL)) return false;   // another wait of the CTA has run out
+        const unsigned t = global_ms();
         if (i == 0) t0 = t;
-        else if (t - t0 > 2000000000ull) return false;
+        else if (t - t0 > limit) return false;
     }
+}
+// The same for a copy's arrival, or for a buffer to be free for one.  After an expired one no further copy is
+// asked for, and the CTA waits once more, for those in flight, before it ends.
+#ifdef DSPARK_TEST_EXPIRED_WAITS
+constexpr bool kExpireAtOnce = true;                         // test build: every one of them
+#else
+constexpr bool kExpireAtOnce = false;
+#endif
+__device__ __forceinline__ bool copy_wait(uint64_t* bar, unsigned parity, const volatile int* given_up = nullptr) {
+    return !kExpireAtOnce && bar_wait(bar, parity, kCopyMs, given_up);
 }
 
 // Launch `grid` CTAs of `threads` threads in clusters of `cluster`, as a programmatic dependent of the

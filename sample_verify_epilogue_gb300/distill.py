@@ -23,7 +23,7 @@ class _DistillLoss(torch.autograd.Function):
         binding.dspark_distill(student, teacher_ids, teacher_logits, loss=loss, row_status=status, saved=saved,
                                teacher_lse=teacher_lse, t2d=t2d, weights=weights, temperature=temperature)
         ctx.save_for_backward(student, teacher_ids, teacher_logits, teacher_lse, t2d, weights, saved)
-        ctx.temperature = temperature
+        ctx.temperature, ctx.status = temperature, status
         ctx.mark_non_differentiable(status)
         return loss, status
 
@@ -33,13 +33,15 @@ class _DistillLoss(torch.autograd.Function):
         student, ids, logits, lse, t2d, weights, saved = ctx.saved_tensors
         grad = torch.empty(student.shape, dtype=student.dtype, device=student.device)
         binding.dspark_distill_backward(student, ids, logits, saved=saved, grad=grad, grad_loss=grad_loss.contiguous(),
-                                        teacher_lse=lse, t2d=t2d, weights=weights, temperature=ctx.temperature)
+                                        teacher_lse=lse, t2d=t2d, weights=weights, temperature=ctx.temperature,
+                                        row_status=ctx.status)
         return grad, None, None, None, None, None, None
 
 
 def distill_loss(student, teacher_ids, teacher_logits, teacher_lse=None, *, t2d=None, weights=None, temperature=1.0):
     """(loss, status) of every row of student [..., V]: see dspark_distill for the arguments.
 
-    The teacher's record, ``teacher_lse`` and ``weights`` are constants: no gradient reaches them.
+    The teacher's record, ``teacher_lse`` and ``weights`` are constants: no gradient reaches them.  The
+    backward pass adds to status, where a row's copies did not come in time (DSPARK_ROW_INTERNAL).
     """
     return _DistillLoss.apply(student, teacher_ids, teacher_logits, teacher_lse, t2d, weights, temperature)

@@ -156,3 +156,52 @@ def test_rows_that_start_inside_a_vector(bd, shift, dtype):
         check_top(x[:rows_], n, 1.0, top_call(bd, x[:rows_], dtype, n, 1.0, 3, shift))
     many = np.repeat(x[:8], 25, 0)                               # a CTA to a row
     check_top(many, n, 1.0, top_call(bd, many, dtype, n, 1.0, 3, shift))
+
+
+def test_expired_waits(bd, monkeypatch):
+    """A test build in which every wait for a copy counts as expired at once (the CTA still waits for what is in
+    flight before it ends): rows that were to be read report DSPARK_ROW_INTERNAL and give no result, backward's
+    included; rows that are not read are as ever, and so are the calls after it."""
+    from sample_verify_epilogue_gb300 import binding as b_
+    from sample_verify_epilogue_gb300.build import build_variant
+    lib = b_.open_library(build_variant("expired_copies", ["-DDSPARK_TEST_EXPIRED_WAITS"], ["top_logits.cu", "distill.cu"]))
+    expired = b_._Calls(lib)
+    rng = np.random.default_rng(41)
+    # a span in one piece, spans that stream, two CTAs and more to a row, ragged rows, both passes over long rows
+    for rows, V, dtype, shift in ((6, 5003, "bf16", 1), (200, 30001, "fp32", 3), (5, 151936, "fp32", 0)):
+        c = distill_batch(rng, rows, V, 20, dtype, 1.0, True)
+        c["ids"][1, 1] = c["ids"][1, 0]                          # a bad record
+        up = np.ones(rows, np.float32)
+        read = np.ones(rows, bool)
+        read[[1, 2, 3]] = False                                  # bad, empty, weight 0
+        normal = distill_call(bd, c, dtype, "two_call", 1, shift, up=up)
+        for form in ("forward", "fused"):
+            with monkeypatch.context() as m:
+                m.setattr(b_, "_calls_of", expired)
+                loss, grad, st = distill_call(bd, c, dtype, form, 1, shift)
+            assert (st[read] == b_.ROW_INTERNAL).all() and st[1] == b_.ROW_BAD_TEACHER and not st[2:4].any()
+            assert np.isnan(loss[read]).all() and not loss[2:4].any()
+            assert grad is None or not grad.any()
+        # backward alone, from the sums of a good call
+        s, ids, logits, w, lse = R.on_gpu(c["s"], dtype, 1, shift), R.i32(c["ids"]), R.f32(c["logits"]), R.f32(c["w"]), R.f32(c["lse"])
+        loss, saved, status = torch.empty(rows, device="cuda"), torch.empty(rows, 4, device="cuda"), R.i32(np.full(rows, -1))
+        bd.dspark_distill(s, ids, logits, loss=loss, saved=saved, row_status=status, weights=w, teacher_lse=lse)
+        grad = R.on_gpu(np.full(c["s"].shape, 9.0), dtype, 1, shift)
+        before = status.cpu().numpy()
+        with monkeypatch.context() as m:
+            m.setattr(b_, "_calls_of", expired)
+            bd.dspark_distill_backward(s, ids, logits, saved=saved, grad=grad, row_status=status, weights=w, teacher_lse=lse)
+        assert np.array_equal(status.cpu().numpy(), np.where(read, b_.ROW_INTERNAL, before))
+        assert not grad.any()
+        # records
+        n = 30
+        v, i, st = torch.zeros(rows, n, device="cuda"), R.i32(np.zeros((rows, n))), R.i32(np.full(rows, -1))
+        lse = torch.zeros(rows, device="cuda")
+        with monkeypatch.context() as m:
+            m.setattr(b_, "_calls_of", expired)
+            bd.dspark_top_logits(s, values=v, ids=i, lse=lse, row_status=st)
+        assert (st == b_.ROW_INTERNAL).all() and torch.isneginf(v).all() and (i == -1).all() and torch.isnan(lse).all()
+        check_top(c["s"], n, 1.0, top_call(bd, c["s"], dtype, n, 1.0, 1, shift))
+        again = distill_call(bd, c, dtype, "two_call", 1, shift, up=up)
+        assert all(np.array_equal(a, b, equal_nan=True) for a, b in zip(normal, again))
+        check_distill(c, again, dtype, bad=(1,))
