@@ -8,7 +8,7 @@ pytestmark = pytest.mark.gpu
 
 from tests import _rows as R  # noqa: E402
 from tests.test_rows_gpu import (  # noqa: E402,F401
-    bd, check_distill, check_process, check_top, distill_batch, distill_call, process_batch, top_call)
+    bd, check_distill, check_process, check_top, distill_batch, distill_call, process_batch, process_call, top_call)
 
 
 @pytest.mark.parametrize("lowest", ["bf16", "fp32"])
@@ -205,3 +205,80 @@ def test_expired_waits(bd, monkeypatch):
         again = distill_call(bd, c, dtype, "two_call", 1, shift, up=up)
         assert all(np.array_equal(a, b, equal_nan=True) for a, b in zip(normal, again))
         check_distill(c, again, dtype, bad=(1,))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,K,V", [(3, 9, 2003), (2, 33, 901), (5, 64, 260)])
+def test_process_long_prefixes(bd, B, K, V, dtype):
+    """Many drafts before a position, among them repeats and tokens of the lists."""
+    c = process_batch(np.random.default_rng(K), B, K, V, dtype, history=120, bias=30)
+    got, status = process_call(bd, c, dtype, 1, 3)
+    check_process(c, got, status, dtype, np.full(c["x"].shape, 77.0))
+
+
+def test_explicit_streams(bd):
+    """Calls on a stream that is not the current one: what the other stream holds before them comes before them."""
+    side = torch.cuda.Stream()
+    on = side.cuda_stream
+    rng = np.random.default_rng(51)
+    c = process_batch(rng, 3, 2, 30001, "fp32")
+    x, out, late = R.on_gpu(c["x"], "fp32"), R.on_gpu(np.full(c["x"].shape, 77.0), "fp32"), R.on_gpu(np.zeros(c["x"].shape), "fp32")
+    status, rows = R.i32(np.full(3, -1)), torch.from_numpy(c["rows"].view(np.uint8).copy()).cuda()
+    given = dict(draft_ids=R.i32(c["drafts"]), history=R.csr(c["hist"], np.int32, np.int32), bias=R.csr(c["bias"], np.int32, np.float32),
+                 mask=R.pack_mask(c["allowed"]), mask_rows=R.i32(c["mask_rows"]))
+    d = distill_batch(rng, 6, 30001, 20, "fp32", 1.0, True)
+    s, ids, logits, lse, w = R.f32(d["s"]), R.i32(d["ids"]), R.f32(d["logits"]), R.f32(d["lse"]), R.f32(d["w"])
+    student, loss, st = torch.zeros_like(s), torch.full((6,), 5.0, device="cuda"), R.i32(np.full(6, -1))
+    saved, grad, up = torch.zeros(6, 4, device="cuda"), torch.zeros_like(s), torch.ones(6, device="cuda")
+    n = 20
+    v, i, tl, ts = torch.zeros(6, n, device="cuda"), R.i32(np.zeros((6, n))), torch.zeros(6, device="cuda"), R.i32(np.full(6, -1))
+    busy = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            busy = torch.tanh(busy @ busy)                       # some time before the inputs are there
+        late.copy_(x)
+        student.copy_(s)
+    bd.dspark_process_logits(late, rows, out=out, row_status=status, stream=on, **given)
+    bd.dspark_top_logits(student, values=v, ids=i, lse=tl, row_status=ts, stream=on)
+    bd.dspark_distill(student, ids, logits, loss=loss, saved=saved, row_status=st, teacher_lse=lse, weights=w, stream=on)
+    bd.dspark_distill_backward(student, ids, logits, saved=saved, grad=grad, grad_loss=up, teacher_lse=lse, weights=w, stream=on)
+    side.synchronize()
+    check_process(c, out.double().cpu().numpy(), status.cpu().numpy(), "fp32", np.full(c["x"].shape, 77.0))
+    check_distill(d, (loss.cpu().numpy(), grad.double().cpu().numpy(), st.cpu().numpy()), "fp32")
+    check_top(d["s"], n, 1.0, [a.cpu().numpy() for a in (v, i, tl, ts)])
+
+
+def test_distill_loss_in_a_graph(bd):
+    """A training step's loss and its gradient captured together and replayed on new inputs."""
+    from sample_verify_epilogue_gb300.distill import distill_loss
+    rng = np.random.default_rng(52)
+    batches = [distill_batch(rng, 5, 4001, 16, "fp32", 1.0, True) for _ in range(3)]
+    student = torch.zeros(5, 4001, device="cuda", requires_grad=True)
+    ids, logits, lse, w = (torch.zeros_like(a) for a in (R.i32(batches[0]["ids"]), R.f32(batches[0]["logits"]),
+                                                         R.f32(batches[0]["lse"]), R.f32(batches[0]["w"])))
+
+    def load(c):
+        with torch.no_grad():
+            for a, b in ((student, R.f32(c["s"])), (ids, R.i32(c["ids"])), (logits, R.f32(c["logits"])), (lse, R.f32(c["lse"])),
+                         (w, R.f32(c["w"]))):
+                a.copy_(b)
+
+    def step():
+        loss, status = distill_loss(student, ids, logits, lse, weights=w)
+        grad, = torch.autograd.grad(loss.sum(), student)
+        return loss.detach(), grad, status
+
+    load(batches[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss, grad, status = step()
+    for c in batches:
+        load(c)
+        graph.replay()
+        check_distill(c, (loss.cpu().numpy(), grad.double().cpu().numpy(), status.cpu().numpy()), "fp32")
