@@ -11,7 +11,7 @@
 // -p_r e_v / R.  Only where R / Z is below 2^-kDisApart (masks of the type's lowest value) does it count as 0.
 //
 // Bound by bandwidth: s is read once and the gradient written once (4096 rows of 151936 bf16, a tenth
-// of weight 0: 356 us, 0.98 of what the copy bandwidth takes for the same bytes).  For both results a CTA's
+// of weight 0: 358 us, 0.98 of what the copy bandwidth takes for the same bytes).  For both results a CTA's
 // span of the row comes to shared memory by bulk copies and stays there between the sum and the gradient,
 // so that the row is not read twice; an SM holds some 200 KB of rows.  What bounds the rate is how long a
 // CTA lives, so everything between copy and store is kept short and wide.  The record is one thread's
@@ -20,7 +20,7 @@
 // S, and writes its member's gradient over at the end.  (The record by one warp: 6000 cycles of a CTA's
 // 24600; the members looked up from inside the loops: 2800.)
 // For one result a CTA streams its span through two 16 KB buffers, six CTAs to an SM (2048 rows of 151936,
-// loss alone: 95 us, 0.87 of the bandwidth; of 32000: 31 us, 0.62, and the gradient alone 43 us, 0.90:
+// loss alone: 96 us, 0.86 of the bandwidth; of 32000: 30 us, 0.65, and the gradient alone 43 us, 0.89:
 // there a CTA waits for its row's ids, first pieces and joins about as long as it reads).  Spans too
 // long to keep go through the buffers twice; the second read is then from L2.
 //
@@ -108,7 +108,7 @@ __device__ __forceinline__ void store_vec(const VocabRow<SX>& g, int i0, const u
     constexpr int VE = 16 / SX;
     unsigned char* p = const_cast<unsigned char*>(g.p);
     if (same_phase && i0 >= 0 && i0 + VE <= g.V) {
-        st_stream(p + static_cast<long long>(i0) * SX, w);
+        st_vec16(p + static_cast<long long>(i0) * SX, w);
         return;
     }
 #pragma unroll
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kRowThreads, ONE ? kDisCtas : 6) distill_kerne
                 unsigned char* gp = const_cast<unsigned char*>(g.p) + static_cast<long long>(x.first(b + w0 + tid)) * SX;
                 const uint4* const end = q0 + w1;
 #pragma unroll 2
-                for (const uint4* q = q0 + w0 + tid; q < end; q += kRowThreads, gp += 16 * kRowThreads) st_stream(gp, grad_whole(*q));
+                for (const uint4* q = q0 + w0 + tid; q < end; q += kRowThreads, gp += 16 * kRowThreads) st_vec16(gp, grad_whole(*q));
             }
             // the ragged ones, or all of them
             auto one = [&](int k) {
@@ -624,7 +624,8 @@ dspark_status_t distill_args(const void* student, const dspark_teacher_t* t, con
     while (C < kMaxCluster && nvec >= C * 512 && static_cast<long long>(p->n_rows) * 2 * C <= (both ? 320 : 640)) C *= 2;
     // Both results: spans kept in one piece, of which an SM holds the more bytes the better (1024 rows
     // of 128256 bf16 in 4, 5, 6, 7, 8: 90, 85, 83, 88, 94 us for 188, 200, 209, 180, 157 KB; of 151936 in
-    // 5 to 8: 108, 100, 108, 102 us for 178, 198, 170, 186).
+    // 5 to 8: 108, 100, 108, 102 us for 178, 198, 170, 186).  kCtaSmem is a few hundred bytes more than a CTA takes now:
+    // five sixths of 128256 would just fit an SM, and the rule, which counts four, goes in fifths.
     if (both)
         for (int c = C, most = 0; c <= kMaxCluster; ++c) {
             const int span = (nvec + c - 1) / c;

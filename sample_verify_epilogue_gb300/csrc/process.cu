@@ -10,10 +10,11 @@
 // empties is not read; in place, a vector that the mask leaves whole is neither read nor written.
 //
 // Without lists the copy runs at 0.99 of the measured bandwidth (64x9 rows of 262144 bf16, no
-// masks: 90 us); 1000 listed tokens a row add some 11 us of scattered two-byte stores (30 with loads
-// and stores that pass the L1 cache by).  Taking the tokens through shared memory into the vectors
-// before they are stored costs more than that, in barriers for every tile or in what the first store
-// waits for (104 to 130 us where this takes 89), and so does a warp to a span without barriers (117 us).
+// masks: 90 us); the 1700 listed tokens of a row add 10 us of scattered two-byte stores, 13 us where masks
+// shorten the copy (30 with loads and stores that pass the L1 cache by).  Taking the tokens through shared
+// memory into the vectors before they are stored costs more than that, in barriers for every tile or in what
+// the first store waits for (104 to 130 us where this takes 89), and so does a warp to a span without
+// barriers (117 us).
 //
 // The first B CTAs check one request each (parameters, list order and ranges, draft ids, mask
 // rows) and write its status; they run beside the copying CTAs, whose own range checks keep every
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(kRowThreads, 6) process_kernel(ProcArgs a) {
             if (bits != kAll) mask_vec<SX>(w, bits);
         }
         if (x.whole(k) && same_phase) {
-            st_stream(yp + static_cast<long long>(i0) * SX, w);
+            st_vec16(yp + static_cast<long long>(i0) * SX, w);
             return;
         }
 #pragma unroll
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(kRowThreads, 6) process_kernel(ProcArgs a) {
 #pragma unroll
             for (int u = 0; u < kProcVec; ++u) {
                 w[u] = ninf_vec<SX>();
-                if (bits[u] && !(in_place && bits[u] == kAll)) w[u] = ld_stream(xp + u * (16 * kRowThreads));
+                if (bits[u] && !(in_place && bits[u] == kAll)) w[u] = ld_vec16(xp + u * (16 * kRowThreads));
             }
             if (!searched) search();
             searched = true;
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(kRowThreads, 6) process_kernel(ProcArgs a) {
             for (int u = 0; u < kProcVec; ++u) {
                 if (u * kRowThreads >= left || (in_place && bits[u] == kAll)) continue;
                 if (bits[u] != kAll) mask_vec<SX>(w[u], bits[u]);
-                st_stream(dp + u * (16 * kRowThreads), w[u]);
+                st_vec16(dp + u * (16 * kRowThreads), w[u]);
             }
             xp += 16 * kProcTile;
             dp += 16 * kProcTile;

@@ -35,13 +35,13 @@ struct VocabRow {
 // Vectors a row of V logits can have at most, whatever its alignment.
 inline int max_vectors(int V, int sx) { return (V + 16 / sx - 1 + 16 / sx - 1) / (16 / sx); }
 
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
+__device__ __forceinline__ uint4 ld_vec16(const void* p) {
     uint4 v;
     asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
     return v;
 }
-__device__ __forceinline__ void st_stream(void* p, const uint4& v) {
+__device__ __forceinline__ void st_vec16(void* p, const uint4& v) {
     asm volatile("st.global.v4.u32 [%0], {%1, %2, %3, %4};"
                  :: "l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -97,7 +97,7 @@ __device__ __forceinline__ uint4 load_vec(const VocabRow<SX>& r, int k, int k_en
     constexpr int VE = VocabRow<SX>::VE;
     if (k >= k_end) return ninf_vec<SX>();
     const int i0 = r.first(k);
-    if (r.whole(k)) return ld_stream(r.p + static_cast<long long>(i0) * SX);
+    if (r.whole(k)) return ld_vec16(r.p + static_cast<long long>(i0) * SX);
     uint4 w = ninf_vec<SX>();
 #pragma unroll
     for (int q = 0; q < VE; ++q)
@@ -190,7 +190,8 @@ __device__ __forceinline__ unsigned long long pair_of(const uint4& w, int k) {
 
 // ---------------------------------------------------------------- values as the sum of two floats
 // For what meets cancellation at a row's end: some 2^-45 relative, in a few dozen cycles a step (the
-// 64-bit unit takes as long for one addition, and a thread's chain of them kept its CTA).
+// 64-bit unit takes as long for one addition, and a thread's chain of them kept its CTA).  The exact sum is
+// Knuth's, the exact product Dekker's with a fused multiply-add for its splitting.
 struct TwoFloat {
     float hi, lo;
 };
@@ -226,7 +227,8 @@ __device__ __forceinline__ TwoFloat log_two(float v) {
 // exp(x / T) relative to a row's or thread's maximum m, as 2^(x c - r) with c = log2(e)/T: r is m c
 // rounded up to a whole number, so that the one fma rounds nothing but its result and sums of
 // different maxima join by powers of two.  Where m c has no such whole number (the type's lowest
-// values, infinities) the form is 2^((x - m) c).
+// values, infinities) the form is 2^((x - m) c); where sums of both forms meet (logits of 2.9 million T, on
+// either side of it) the join is off by up to one power of two.
 struct ExpRef {
     float m, c, r;
     bool whole;
