@@ -97,6 +97,7 @@ typedef enum { DSPARK_BF16 = 0, DSPARK_FP32 = 1 } dspark_dtype_t;
 #define DSPARK_ROW_BAD_TEACHER 128 /* a teacher id outside the target vocabulary or repeated, a
                                       t2d entry outside [-1, V), a NaN or +inf teacher logit, a
                                       non-finite teacher log-sum-exp */
+#define DSPARK_ROW_BAD_TOKEN 256 /* a row's token outside [-1, V) */
 
 /* Largest supported sizes. */
 #define DSPARK_MAX_B          2048
@@ -105,7 +106,9 @@ typedef enum { DSPARK_BF16 = 0, DSPARK_FP32 = 1 } dspark_dtype_t;
 #define DSPARK_MAX_TOP_LOGPROBS 20
 #define DSPARK_MAX_SPARSE_M   256  /* (id, probability) pairs per sparse draft row */
 #define DSPARK_MAX_TOP_LOGITS 256  /* entries of a top-logit record (dspark_top_logits, teacher) */
-#define DSPARK_MAX_ROWS  (1 << 24) /* rows of dspark_top_logits and dspark_distill */
+#define DSPARK_MAX_ROWS  (1 << 24) /* rows of the entry points around the epilogue that take rows */
+#define DSPARK_MAX_PAIRS (1 << 16) /* pairs of dspark_preference_loss */
+#define DSPARK_SAVED_FLOATS 8      /* floats a row that dspark_token_logprobs and the losses made of it save */
 
 /* Sampling parameters of one request (24 bytes, device array of B). */
 typedef struct {
@@ -413,6 +416,145 @@ dspark_status_t dspark_distill(const void* student, const dspark_teacher_t* teac
 dspark_status_t dspark_distill_backward(const void* student, const dspark_teacher_t* teacher,
                                         const dspark_distill_params_t* params, const float* saved,
                                         const float* grad_loss, void* out_grad);
+
+/* ------------------------------------------------------------------------------------------
+ * Training on decoded tokens: the log-probability of one token of every row, the losses made of it
+ * (of a policy from the advantages of its own tokens, of a preference between two answers) and the
+ * clipping of the gradients that come of them.  As above: no allocation, no state between calls, safe to
+ * capture and to call from several host threads.  Each call is one launch, the gradient of a loss one
+ * more, dspark_preference_loss one more, dspark_clip_grads two.
+ * ------------------------------------------------------------------------------------------ */
+
+typedef struct {
+    int32_t n_rows;               /* R, 1..DSPARK_MAX_ROWS               */
+    int32_t V;                    /* 1..DSPARK_MAX_V                     */
+    dspark_dtype_t logits_dtype;  /* of the logits and their gradient    */
+    int64_t logits_stride;        /* elements between rows               */
+    int64_t grad_stride;          /* (calls that write a gradient)       */
+    float   temperature;          /* T > 0                               */
+    const int32_t* tokens;        /* device [R]: the token of each row, -1: none (prompt, padding) */
+    void*   stream;
+    int32_t* row_status;          /* device [R]; backward calls ignore it */
+} dspark_token_params_t;
+
+/*
+ * log p(y) of each row's token y under p = softmax(x / T), and the entropy H = -sum p log p.
+ *   out_logprobs  [R] fp32.  A masked token (logit -inf) has -inf.
+ *   out_entropy   [R] fp32 or NULL
+ *   out_saved     [R, DSPARK_SAVED_FLOATS] fp32, 16-byte aligned, or NULL: what the backward call needs (opaque)
+ * A row without a token is not read and gets 0 in each.  row_status[r]: 0, or DSPARK_ROW_BAD_TOKEN (the row is
+ * not read), or DSPARK_ROW_NONFINITE (NaN or +inf in the row, or nothing above -inf); such a row gets NaN,
+ * and a gradient of 0.
+ */
+dspark_status_t dspark_token_logprobs(const void* logits, const dspark_token_params_t* params, float* out_logprobs,
+                                      float* out_entropy, float* out_saved);
+
+/*
+ * The gradient of sum_r (grad_logprobs[r] log p_r(y_r) + grad_entropy[r] H_r) by the logits, from the logits and
+ * params of a dspark_token_logprobs call and its out_saved.  Either may be NULL (all 0), not both; grad_entropy needs
+ * a call that asked for the entropy (else the gradient is NaN).
+ *   out_grad  [R, V] of logits_dtype; may be logits itself (same pointer and stride)
+ *   out_grad[r][v] = (g (1[v = y] - p_v) - e p_v (log p_v + H)) / T, g and e the upstream gradients
+ */
+dspark_status_t dspark_token_logprobs_backward(const void* logits, const dspark_token_params_t* params, const float* saved,
+                                               const float* grad_logprobs, const float* grad_entropy, void* out_grad);
+
+/* What a row's policy loss is made with (device arrays). */
+typedef struct {
+    const float* old_logprobs;    /* [R] of the policy that drew the tokens (dspark_verify_sample's out_logprobs)  */
+    const float* ref_logprobs;    /* [R] of the reference policy, or NULL                                          */
+    const float* advantages;      /* [R]                                                                           */
+    const float* weights;         /* [R] or NULL (all 1); a row of weight 0 is not read                            */
+    float clip_low, clip_high;    /* in [0, 1]; >= 0: the ratio is clipped to [1 - clip_low, 1 + clip_high]         */
+    float kl_coef;                /* of the KL term; 0, or ref_logprobs is given                                   */
+    float entropy_coef;           /* of the entropy bonus                                                          */
+} dspark_policy_t;
+
+/*
+ * The clipped policy loss of each row, with l = log p(y), rho = exp(l - old), D = ref - l:
+ *   L = -min(rho A, clip(rho) A) + kl_coef (exp(D) - D - 1) - entropy_coef H
+ *   out_loss[r] = w_r L
+ *   out_logprobs, out_entropy, out_kl   [R] fp32 or NULL: l, H, exp(D) - D - 1 (out_kl needs ref_logprobs)
+ *   out_saved   [R, DSPARK_SAVED_FLOATS] fp32, 16-byte aligned, or NULL
+ *   out_grad    [R, V] or NULL: gradient of the sum of out_loss; may be logits itself (same pointer and
+ *               stride).  It needs out_saved.
+ * Where clipping binds, rho A gives no gradient; at its border rho counts as not clipped.  A = 0 leaves the
+ * first term out, whatever rho is.  Rows without a token or of weight 0 are not read and have 0 everywhere.
+ * row_status[r] as above, and DSPARK_ROW_NONFINITE for a row whose loss or derivative is not finite as well (a
+ * masked token under a KL term, log-probabilities that are NaN): loss NaN, gradient 0.
+ */
+dspark_status_t dspark_policy_loss(const void* logits, const dspark_policy_t* policy, const dspark_token_params_t* params,
+                                   float* out_loss, float* out_logprobs, float* out_entropy, float* out_kl, float* out_saved,
+                                   void* out_grad);
+
+/* The gradient of sum_r grad_loss[r] * out_loss[r], from the same logits, policy and params and the out_saved
+ * of a dspark_policy_loss call; grad_loss [R] fp32 or NULL (all 1). */
+dspark_status_t dspark_policy_loss_backward(const void* logits, const dspark_policy_t* policy, const dspark_token_params_t* params,
+                                            const float* saved, const float* grad_loss, void* out_grad);
+
+/* Pairs of answers, packed row after row: sequence 2i is the chosen one of pair i, 2i + 1 the rejected one. */
+typedef struct {
+    int32_t n_pairs;              /* P, 1..DSPARK_MAX_PAIRS                                                  */
+    const int32_t* row_offsets;   /* device [2P + 1]: sequence k is rows row_offsets[k] .. row_offsets[k+1] - 1 */
+    const float* ref_logprobs;    /* device [R] of the reference policy, or NULL: no reference                */
+    const float* weights;         /* device [P] or NULL (all 1)                                              */
+    float beta;                   /* > 0                                                                     */
+    float margin;
+    float label_smoothing;        /* in [0, 1)                                                               */
+    int32_t mean;                 /* non-zero: log ratios are averaged over a sequence's tokens, else summed  */
+} dspark_preference_t;
+
+/*
+ * The preference loss of each pair: with S_k the sum (or mean; 0 for none) of log p(y) - ref over the rows of sequence k
+ * that have a token,
+ *   z = beta (S_2i - S_2i+1) - margin,  L = -(1 - e) log sigma(z) - e log sigma(-z),  e = label_smoothing
+ *   out_loss      [P] fp32: w_i L
+ *   out_rewards   [P, 2] fp32 or NULL: beta S_2i, beta S_2i+1
+ *   pair_status   [P] int32: 0, the bits of its rows' statuses, DSPARK_ROW_NONFINITE (z is NaN), or
+ *                 DSPARK_ROW_BAD_PARAMS (row_offsets up to the pair's last descend somewhere or leave [0, R]); such a pair
+ *                 has a loss and rewards of NaN and gradients of 0
+ *   out_logprobs  [R] fp32 or NULL
+ *   out_saved     [R, DSPARK_SAVED_FLOATS] fp32, 16-byte aligned, required: the rows' results on their way to the pairs
+ *   out_grad      [R, V] or NULL: gradient of the sum of out_loss; may be logits itself (same pointer and
+ *                 stride).  Rows without a token and rows that belong to no pair get 0.
+ */
+dspark_status_t dspark_preference_loss(const void* logits, const dspark_preference_t* pref, const dspark_token_params_t* params,
+                                       float* out_loss, float* out_rewards, int32_t* pair_status, float* out_logprobs,
+                                       float* out_saved, void* out_grad);
+
+/* The gradient of sum_i grad_loss[i] * out_loss[i], from the same logits and params and the out_saved of a
+ * dspark_preference_loss call of n_pairs pairs; grad_loss [P] fp32 or NULL (all 1). */
+dspark_status_t dspark_preference_loss_backward(const void* logits, const dspark_token_params_t* params, int32_t n_pairs,
+                                                const float* saved, const float* grad_loss, void* out_grad);
+
+/* One gradient of a list (host struct, device pointers); its elements are contiguous. */
+typedef struct {
+    const void* grad;
+    void* out;                    /* grad itself, or memory that overlaps no gradient of the list   */
+    int64_t numel;                /* >= 0                                                          */
+    dspark_dtype_t dtype;         /* of grad                                                       */
+    dspark_dtype_t out_dtype;     /* dtype, or DSPARK_FP32                                         */
+} dspark_grad_t;
+
+#define DSPARK_MAX_GRADS (1 << 16)  /* gradients of a list */
+
+/* Scratch bytes dspark_clip_grads needs for a list of n_grads gradients; 0 if there are too many. */
+size_t dspark_clip_workspace_bytes(int32_t n_grads);
+
+/*
+ * The norm of a list of gradients taken together, N = sqrt(sum of the squares of all elements), and the
+ * gradients times max_norm / N where N is larger than max_norm, as they are otherwise.
+ *   grads      host array of n_grads; a gradient appears once
+ *   max_norm   >= 0; infinity: the norm alone is wanted
+ *   out_norm   device [1] fp32: N before clipping
+ *   out_status device [1] int32: 0, or DSPARK_ROW_NONFINITE when N is not finite; the gradients are then as they were
+ *   workspace  device, 256-byte aligned, at least dspark_clip_workspace_bytes(n_grads); calls that share one
+ *              must not overlap on the GPU
+ * A gradient that is clipped in place is not written when nothing changes.  Sums are in a fixed order: the same list
+ * gives the same bits.  Squares neither overflow nor vanish: any finite gradients whose norm fits fp32 have it.
+ */
+dspark_status_t dspark_clip_grads(const dspark_grad_t* grads, int32_t n_grads, float max_norm, float* out_norm,
+                                  int32_t* out_status, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Human-readable name of a status code. */
 const char* dspark_status_string(dspark_status_t status);

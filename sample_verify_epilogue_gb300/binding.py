@@ -20,6 +20,7 @@ DSPARK_FP32 = 1
 DSPARK_MAX_TOP_LOGPROBS = 20
 DSPARK_MAX_SPARSE_M = 256
 DSPARK_MAX_TOP_LOGITS = 256
+DSPARK_MAX_GRADS = 1 << 16
 DSPARK_Q_DENSE, DSPARK_Q_SPARSE, DSPARK_Q_REDUCED = 0, 1, 2
 DSPARK_LOGPROBS_RAW, DSPARK_LOGPROBS_PENALISED = 0, 1
 Q_LAYOUTS = {"dense": DSPARK_Q_DENSE, "sparse": DSPARK_Q_SPARSE, "reduced": DSPARK_Q_REDUCED}
@@ -33,6 +34,8 @@ ROW_INTERNAL = 16
 ROW_BAD_BIAS = 32
 ROW_BAD_MASK = 64
 ROW_BAD_TEACHER = 128
+ROW_BAD_TOKEN = 256
+DSPARK_SAVED_FLOATS = 8
 
 # dspark_row_params_t: float, int32, float, float, float, int32 (24 bytes)
 ROW_PARAMS_DTYPE = np.dtype([
@@ -110,6 +113,35 @@ class dspark_distill_params_t(ctypes.Structure):
     ]
 
 
+class dspark_token_params_t(ctypes.Structure):
+    _fields_ = [
+        ("n_rows", ctypes.c_int32), ("V", ctypes.c_int32), ("logits_dtype", ctypes.c_int32),
+        ("logits_stride", ctypes.c_int64), ("grad_stride", ctypes.c_int64), ("temperature", ctypes.c_float),
+        ("tokens", ctypes.c_void_p), ("stream", ctypes.c_void_p), ("row_status", ctypes.c_void_p),
+    ]
+
+
+class dspark_policy_t(ctypes.Structure):
+    _fields_ = [
+        ("old_logprobs", ctypes.c_void_p), ("ref_logprobs", ctypes.c_void_p), ("advantages", ctypes.c_void_p),
+        ("weights", ctypes.c_void_p), ("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float),
+        ("kl_coef", ctypes.c_float), ("entropy_coef", ctypes.c_float),
+    ]
+
+
+class dspark_preference_t(ctypes.Structure):
+    _fields_ = [
+        ("n_pairs", ctypes.c_int32), ("row_offsets", ctypes.c_void_p), ("ref_logprobs", ctypes.c_void_p),
+        ("weights", ctypes.c_void_p), ("beta", ctypes.c_float), ("margin", ctypes.c_float),
+        ("label_smoothing", ctypes.c_float), ("mean", ctypes.c_int32),
+    ]
+
+
+class dspark_grad_t(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32)]
+
+
 def make_extras(q_layout="dense", q_row_len=0, q_ids=None, d2t=None, eos_ids=None, out_stopped=None,
                 pos_counts=None, logprob_mode="raw"):
     """A dspark_extras_t; array arguments are raw addresses (int) or None."""
@@ -127,7 +159,9 @@ _lib = None
 EXPORTS = ("dspark_workspace_bytes", "dspark_verify_sample", "dspark_host_workspace_bytes",
            "dspark_verify_sample_host", "dspark_verify_sample_static", "dspark_status_string",
            "dspark_launches_per_call", "dspark_process_logits", "dspark_top_logits", "dspark_distill",
-           "dspark_distill_backward")
+           "dspark_distill_backward", "dspark_token_logprobs", "dspark_token_logprobs_backward", "dspark_policy_loss",
+           "dspark_policy_loss_backward", "dspark_preference_loss", "dspark_preference_loss_backward",
+           "dspark_clip_workspace_bytes", "dspark_clip_grads")
 
 DSPARK_STATIC_WORKSPACE_BYTES = 16 << 20
 
@@ -161,6 +195,8 @@ def open_library(path: str):
     lib.dspark_verify_sample_host.restype = ctypes.c_int
     lib.dspark_verify_sample_static.argtypes = sig
     lib.dspark_verify_sample_static.restype = ctypes.c_int
+    lib.dspark_clip_workspace_bytes.argtypes = [ctypes.c_int32]
+    lib.dspark_clip_workspace_bytes.restype = ctypes.c_size_t
     lib.dspark_status_string.argtypes = [ctypes.c_int]
     lib.dspark_status_string.restype = ctypes.c_char_p
     lib.dspark_launches_per_call.argtypes = []
@@ -352,16 +388,23 @@ def _packer(cls):
 _counts, _bias, _mask, _process_params, _top_params, _teacher, _distill_params = map(_packer, (
     dspark_counts_t, dspark_bias_t, dspark_mask_t, dspark_process_params_t, dspark_top_params_t, dspark_teacher_t,
     dspark_distill_params_t))
+_token_params, _policy, _preference, _grad = map(_packer, (dspark_token_params_t, dspark_policy_t, dspark_preference_t,
+                                                           dspark_grad_t))
 
 
 class _Calls:
     """The entry points around the epilogue, taking packed structures."""
 
     def __init__(self, lib):
-        for name, n in (("dspark_process_logits", 7), ("dspark_top_logits", 5), ("dspark_distill", 6),
-                        ("dspark_distill_backward", 6)):
+        P, i32 = ctypes.c_void_p, ctypes.c_int32
+        for name, args in (("dspark_process_logits", [P] * 7), ("dspark_top_logits", [P] * 5), ("dspark_distill", [P] * 6),
+                           ("dspark_distill_backward", [P] * 6), ("dspark_token_logprobs", [P] * 5),
+                           ("dspark_token_logprobs_backward", [P] * 6), ("dspark_policy_loss", [P] * 9),
+                           ("dspark_policy_loss_backward", [P] * 6), ("dspark_preference_loss", [P] * 9),
+                           ("dspark_preference_loss_backward", [P, P, i32, P, P, P]),
+                           ("dspark_clip_grads", [P, i32, ctypes.c_float, P, P, P, ctypes.c_size_t, P])):
             fn = lib[name]
-            fn.argtypes = [ctypes.c_void_p] * n
+            fn.argtypes = args
             fn.restype = ctypes.c_int
             setattr(self, name, fn)
 
@@ -546,3 +589,189 @@ def dspark_distill_backward(student, teacher_ids, teacher_logits, *, saved, grad
     f32 = _torch.f32
     _launch(_calls().dspark_distill_backward, dev, student.data_ptr(), t, p, _flat("saved", saved, f32, 4 * R, dev),
             None if grad_loss is None else _flat("grad_loss", grad_loss, f32, R, dev), grad.data_ptr())
+
+
+# ---------------------------------------------------------------- training on decoded tokens
+def _token_args(logits, tokens, temperature, row_status, grad, stream):
+    T = _t()
+    dev = _device_of("logits", logits)
+    R, V, stride = _rows_of("logits", logits)
+    grad_stride = V if grad is None else stride if grad is logits else _rows_of("grad", grad, logits)[2]
+    p = _token_params(R, V, _dtype_of(logits), stride, grad_stride, temperature, _flat("tokens", tokens, T.i32, R, dev),
+                      T.stream(dev) if stream is None else stream,
+                      0 if row_status is None else _flat("row_status", row_status, T.i32, R, dev))
+    return dev, R, p
+
+
+def _saved(saved, R, dev):
+    return _flat("saved", saved, _torch.f32, DSPARK_SAVED_FLOATS * R, dev)
+
+
+def dspark_token_logprobs(logits, tokens, *, logprobs, row_status, entropy=None, saved=None, temperature=1.0, stream=None):
+    """The log-probability of one token of every row, and the entropy of the row's distribution, on ``stream``
+    (default: torch's current stream).
+
+    logits [..., V] bf16/fp32 of R rows, tokens [...] int32 (-1: no token, the row is not read and gets 0),
+    logprobs [...] fp32, row_status [...] int32, entropy [...] fp32 or None, saved [..., 8] fp32 for
+    dspark_token_logprobs_backward or None -- all CUDA tensors.
+    """
+    dev, R, p = _token_args(logits, tokens, temperature, row_status, None, stream)
+    f32 = _torch.f32
+    _launch(_calls().dspark_token_logprobs, dev, logits.data_ptr(), p, _flat("logprobs", logprobs, f32, R, dev),
+            None if entropy is None else _flat("entropy", entropy, f32, R, dev), None if saved is None else _saved(saved, R, dev))
+
+
+def dspark_token_logprobs_backward(logits, tokens, *, saved, grad, grad_logprobs=None, grad_entropy=None, temperature=1.0,
+                                   stream=None):
+    """The gradient of sum(grad_logprobs * logprobs + grad_entropy * entropy) by the logits, from the inputs and the
+    ``saved`` of a dspark_token_logprobs call; either of the two [...] fp32 may be None (all 0).  grad_entropy needs a call
+    that asked for the entropy.  ``grad`` is like logits and may be logits."""
+    if grad is None:
+        raise ValueError("grad is missing")
+    dev, R, p = _token_args(logits, tokens, temperature, None, grad, stream)
+    f32 = _torch.f32
+    _launch(_calls().dspark_token_logprobs_backward, dev, logits.data_ptr(), p, _saved(saved, R, dev),
+            None if grad_logprobs is None else _flat("grad_logprobs", grad_logprobs, f32, R, dev),
+            None if grad_entropy is None else _flat("grad_entropy", grad_entropy, f32, R, dev), grad.data_ptr())
+
+
+def _policy_of(R, dev, old_logprobs, advantages, ref_logprobs, weights, clip_low, clip_high, kl_coef, entropy_coef):
+    f32 = _torch.f32
+    return _policy(_flat("old_logprobs", old_logprobs, f32, R, dev),
+                   0 if ref_logprobs is None else _flat("ref_logprobs", ref_logprobs, f32, R, dev),
+                   _flat("advantages", advantages, f32, R, dev),
+                   0 if weights is None else _flat("weights", weights, f32, R, dev), clip_low, clip_high, kl_coef, entropy_coef)
+
+
+def dspark_policy_loss(logits, tokens, old_logprobs, advantages, *, loss, row_status, ref_logprobs=None, weights=None,
+                       logprobs=None, entropy=None, kl=None, saved=None, grad=None, clip_low=0.2, clip_high=0.2, kl_coef=0.0,
+                       entropy_coef=0.0, temperature=1.0, stream=None):
+    """The clipped policy loss of every row, with a KL term and an entropy bonus, on ``stream``; with ``grad``, its
+    gradient as well.
+
+    logits [..., V] bf16/fp32 of R rows, tokens [...] int32 (-1: no token), old_logprobs, advantages, ref_logprobs (or
+    None), weights (or None) [...] fp32; loss [...] fp32, row_status [...] int32, logprobs, entropy, kl [...] fp32 or None,
+    saved [..., 8] fp32 (needed with grad and for dspark_policy_loss_backward) or None, grad like logits (may be
+    logits) or None -- all CUDA tensors.
+    """
+    if row_status is None:
+        raise ValueError("row_status is missing")
+    if grad is not None and saved is None:
+        raise ValueError("grad needs saved")
+    dev, R, p = _token_args(logits, tokens, temperature, row_status, grad, stream)
+    o = _policy_of(R, dev, old_logprobs, advantages, ref_logprobs, weights, clip_low, clip_high, kl_coef, entropy_coef)
+    f32 = _torch.f32
+    _launch(_calls().dspark_policy_loss, dev, logits.data_ptr(), o, p, _flat("loss", loss, f32, R, dev),
+            None if logprobs is None else _flat("logprobs", logprobs, f32, R, dev),
+            None if entropy is None else _flat("entropy", entropy, f32, R, dev),
+            None if kl is None else _flat("kl", kl, f32, R, dev), None if saved is None else _saved(saved, R, dev),
+            None if grad is None else grad.data_ptr())
+
+
+def dspark_policy_loss_backward(logits, tokens, old_logprobs, advantages, *, saved, grad, grad_loss=None, ref_logprobs=None,
+                                weights=None, clip_low=0.2, clip_high=0.2, kl_coef=0.0, entropy_coef=0.0, temperature=1.0,
+                                stream=None):
+    """The gradient of sum(grad_loss * loss) by the logits, from the inputs and the ``saved`` of a dspark_policy_loss
+    call; grad_loss [...] fp32 or None (all 1)."""
+    if grad is None:
+        raise ValueError("grad is missing")
+    dev, R, p = _token_args(logits, tokens, temperature, None, grad, stream)
+    o = _policy_of(R, dev, old_logprobs, advantages, ref_logprobs, weights, clip_low, clip_high, kl_coef, entropy_coef)
+    _launch(_calls().dspark_policy_loss_backward, dev, logits.data_ptr(), o, p, _saved(saved, R, dev),
+            None if grad_loss is None else _flat("grad_loss", grad_loss, _torch.f32, R, dev), grad.data_ptr())
+
+
+def dspark_preference_loss(logits, tokens, row_offsets, *, loss, saved, row_status, pair_status, rewards=None,
+                           logprobs=None, ref_logprobs=None, weights=None, grad=None, beta=0.1, margin=0.0, label_smoothing=0.0,
+                           mean=False, temperature=1.0, stream=None):
+    """The preference loss of P pairs of sequences, on ``stream``; with ``grad``, its gradient as well.
+
+    logits [..., V] bf16/fp32 of R rows, tokens [...] int32 (-1: no token), row_offsets [2P + 1] int32: sequence 2i, rows
+    row_offsets[2i] to row_offsets[2i + 1] - 1, is the chosen one of pair i, sequence 2i + 1 the rejected one;
+    ref_logprobs [...] fp32 or None, weights [P] fp32 or None; loss [P] fp32, saved [..., 8] fp32 (for
+    dspark_preference_loss_backward too), row_status [...] int32, pair_status [P] int32, rewards [P, 2] fp32 or None,
+    logprobs [...] fp32 or None, grad like logits (may be logits) or None -- all CUDA tensors.  With ``mean`` the log ratios
+    are averaged over a sequence's tokens instead of summed.
+    """
+    if row_status is None:
+        raise ValueError("row_status is missing")
+    dev, R, p = _token_args(logits, tokens, temperature, row_status, grad, stream)
+    i32, f32 = _torch.i32, _torch.f32
+    P = loss.numel()
+    o = _preference(P, _flat("row_offsets", row_offsets, i32, 2 * P + 1, dev),
+                    0 if ref_logprobs is None else _flat("ref_logprobs", ref_logprobs, f32, R, dev),
+                    0 if weights is None else _flat("weights", weights, f32, P, dev), beta, margin, label_smoothing, bool(mean))
+    _launch(_calls().dspark_preference_loss, dev, logits.data_ptr(), o, p, _flat("loss", loss, f32, P, dev),
+            None if rewards is None else _flat("rewards", rewards, f32, 2 * P, dev),
+            _flat("pair_status", pair_status, i32, P, dev), None if logprobs is None else _flat("logprobs", logprobs, f32, R, dev),
+            _saved(saved, R, dev), None if grad is None else grad.data_ptr())
+
+
+def dspark_preference_loss_backward(logits, tokens, *, saved, grad, grad_loss, temperature=1.0, stream=None):
+    """The gradient of sum(grad_loss * loss) by the logits, from the inputs and the ``saved`` of a
+    dspark_preference_loss call; grad_loss [P] fp32."""
+    if grad is None:
+        raise ValueError("grad is missing")
+    dev, R, p = _token_args(logits, tokens, temperature, None, grad, stream)
+    P = grad_loss.numel()
+    _launch(_calls().dspark_preference_loss_backward, dev, logits.data_ptr(), p, P, _saved(saved, R, dev),
+            _flat("grad_loss", grad_loss, _torch.f32, P, dev), grad.data_ptr())
+
+
+class GradTable:
+    """A list of gradients as dspark_clip_grads takes it, made once for gradients that stay where they are.
+
+    grads: contiguous bf16/fp32 CUDA tensors of one device, None entries left out; out: None (the gradients are clipped
+    in place) or a tensor for each, of its shape and its dtype or fp32, that overlaps no gradient.  The table holds the
+    tensors; it knows nothing of a ``.grad`` that is replaced later.
+    """
+
+    def __init__(self, grads, out=None):
+        T = _t()
+        grads = list(grads)
+        out = grads if out is None else list(out)
+        if len(out) != len(grads):
+            raise ValueError(f"{len(grads)} gradients, {len(out)} outputs")
+        pairs = [(g, o) for g, o in zip(grads, out) if g is not None]
+        if not pairs:
+            raise ValueError("no gradients")
+        self.device = _device_of("a gradient", pairs[0][0])
+        self.tensors, fields, seen = pairs, [], set()
+        for g, o in pairs:
+            if g.get_device() != self.device or not g.is_contiguous():
+                raise ValueError("the gradients must be contiguous CUDA tensors of one device")
+            if g.numel() and g.data_ptr() in seen:
+                raise ValueError("a gradient appears twice")
+            seen.add(g.data_ptr())
+            if o is not g and (o is None or o.shape != g.shape or o.get_device() != self.device or not o.is_contiguous() or
+                               (o.dtype is not g.dtype and o.dtype is not T.f32)):
+                raise ValueError("an output must be contiguous, of its gradient's shape and device, and of its dtype or fp32")
+            fields.append(_grad(g.data_ptr(), o.data_ptr(), g.numel(), _dtype_of(g), _dtype_of(o)))
+        if len(fields) > DSPARK_MAX_GRADS:
+            raise ValueError(f"more than {DSPARK_MAX_GRADS} gradients")
+        self.packed = b"".join(fields)
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def dspark_clip_workspace_bytes(table) -> int:
+    return load_library().dspark_clip_workspace_bytes(len(table))
+
+
+def dspark_clip_grads(table, max_norm, *, norm, status, workspace, stream=None):
+    """The norm of the gradients of ``table`` (a GradTable, or a list to make one of) taken together, and the gradients
+    scaled by max_norm / norm where the norm is larger than max_norm, on ``stream``.
+
+    norm [1] fp32: before clipping; status [1] int32: 0, or ROW_NONFINITE when the norm is not finite (the gradients are
+    then as they were); workspace: uint8 CUDA tensor of at least dspark_clip_workspace_bytes(table) bytes.
+    """
+    if not isinstance(table, GradTable):
+        table = GradTable(table)
+    T = _t()
+    dev = table.device
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the gradients' device")
+    _launch(_calls().dspark_clip_grads, dev, table.packed, len(table), max_norm, _flat("norm", norm, T.f32, 1, dev),
+            _flat("status", status, T.i32, 1, dev), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            T.stream(dev) if stream is None else stream)
