@@ -277,9 +277,8 @@ def _own_preference(s):
     two = c["form"] == "two_call"
     b.dspark_preference_loss(s["logits"], s["tokens"], s["offsets"], loss=s["loss"], logprobs=s["logprobs"],
                              row_status=s["status"], pair_status=s["pair_status"], rewards=s["rewards"],
-                             saved=None if c["form"] == "forward" else s["saved"],
-                             grad=s["grad"] if c["form"] == "fused" else None, ref_logprobs=s["ref"], weights=s["weights"],
-                             beta=_BETA, margin=_MARGIN, label_smoothing=c["smoothing"], mean=c["mean"],
+                             saved=s["saved"], grad=s["grad"] if c["form"] == "fused" else None, ref_logprobs=s["ref"],
+                             weights=s["weights"], beta=_BETA, margin=_MARGIN, label_smoothing=c["smoothing"], mean=c["mean"],
                              temperature=c["temperature"])
     if two:
         b.dspark_preference_loss_backward(s["logits"], s["tokens"], saved=s["saved"], grad=s["grad"], grad_loss=s["up"],
