@@ -10,7 +10,9 @@
 //   dL/dx_v = -p_v (a + h (log p_v + H)) / T,   dL/dx_y = (a q - h p_y (log p_y + H)) / T
 //
 // stats_kernel streams a row and leaves what the gradient needs (32 bytes a row), grad_kernel streams it again.
+#include <algorithm>
 #include <cmath>
+#include <limits>
 
 #include "vocab_rows.cuh"
 
@@ -18,9 +20,12 @@ namespace dspark {
 
 namespace {
 
-constexpr int kTokVec = 4;                                   // vectors a thread holds at a time
+constexpr int kTokVec = 2;                                   // vectors a thread takes at a time
 constexpr int kGradVecs = 2048;                              // vectors of a row that a CTA of the gradient takes
 constexpr float kLn2 = 0.693147180559945f;
+// what the exponential unit's results lack on average, relative (2^20 arguments between whole exponents: 5.06e-8, from
+// 9e-8 too large to 1.4e-7 too small): added to the logarithm of a sum of them
+constexpr float kEx2Lacks = 5.06e-8f;
 
 enum TokenOp : int { kScore, kPolicy, kPreference };
 
@@ -36,7 +41,7 @@ static_assert(sizeof(RowSaved) == 4 * DSPARK_SAVED_FLOATS, "the header's size");
 
 struct TokArgs {
     int V, op;
-    float c, inv_t;                                          // log2(e) / T, 1 / T
+    float c, c_low, inv_c, inv_t;                            // log2(e) / T in two parts, 1 / c, 1 / T
     long long x_stride, g_stride;
     const void* x;
     void* g;
@@ -55,10 +60,13 @@ struct TokArgs {
     const float* up;                                         // upstream gradients, null: 1
     const float* up_entropy;                                 // (score) null: 0
     int n_up;                                                // (preference) entries of up
-    int log_c, splits;                                       // stats: log2 of the CTAs of a row; gradient: CTAs of a row
+    int log_c, splits;                                       // log2 of the CTAs of a row (stats); CTAs of a row (gradient, fused)
+    int span;                                                // vectors of each (fused)
+    unsigned zero;                                           // 0
 };
 
-// A sum of exponentials e by ExpRef(m), and the sum w of e times its exponent (base 2).
+// A sum of exponentials e by ExpRef(m), and the sum w of e times its exponent (base 2).  m is a logit of about the
+// largest ones' size; no e is larger than 2^16.
 struct EntSum {
     float m, sum, w;
 };
@@ -76,66 +84,144 @@ __device__ __forceinline__ void rebase_to(EntSum& a, float to, float c) {
     }
     a.m = to;
 }
-// The sum over groups of `lanes` lanes, in each of them.
-template <bool ENT>
-__device__ __forceinline__ EntSum lanes_join(EntSum a, int lanes, float c) {
+// The sum over groups of N lanes, in each of them.
+template <bool ENT, int N>
+__device__ __forceinline__ EntSum lanes_join(EntSum a, float c) {
     float m = a.m;
-    for (int o = lanes / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (N == 32) m = key_to_f(__reduce_max_sync(0xffffffffu, fkey(m)));
+    else
+#pragma unroll
+        for (int o = N / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (m > -INFINITY) rebase_to<ENT>(a, m, c);
-    for (int o = lanes / 2; o; o >>= 1) {
+#pragma unroll
+    for (int o = N / 2; o; o >>= 1) {
         a.sum += __shfl_xor_sync(0xffffffffu, a.sum, o);
         if (ENT) a.w += __shfl_xor_sync(0xffffffffu, a.w, o);
     }
     return a;
 }
 
-// Add U vectors whose maximum is bm.
-template <int SX, bool ENT, int U>
-__device__ __forceinline__ void add_vecs(RunSum& es, float& w, const uint4 (&v)[U], float bm, float c) {
-    constexpr int VE = 16 / SX;
-    if (!ENT) {
-        add_exps<SX>(es, v, bm, c);
-        return;
+// A thread's sum while it streams.
+//
+// Vectors are added by the reference that is there, whatever their maximum: where that makes a sum of 2^16 or more (the
+// first vectors, a maximum far above those before) they are added again by the maximum of both.  The reference's whole
+// exponent r makes the exponent's one rounding that of the fma; -inf stands for none.
+//
+// A row's log-probability may be off by 1e-7 at random, but not to one side: sums of a thousand log ratios follow.  So
+// the vectors' sum joins the rest in a pair of floats (added one by one, small terms are lost more often than gained:
+// 2e-8 of a row of 151936), and log2(e) / T is taken in two parts (rounded to one it is off by up to 2^-24 of the distance
+// between logits): here, or with the entropy, whose sum gives the mean logit, in row_end.
+template <int SX, bool ENT>
+struct RunEnt {
+    static constexpr int VE = 16 / SX;
+    float m = -INFINITY, r = -INFINITY, sum = 0.f, low = 0.f, w = 0.f;
+    uint32_t least = 0u;                                     // (bf16, entropy) logits below have e = 0: a pair of it
+
+    __device__ __forceinline__ EntSum get() const { return EntSum{m, sum + low, w}; }
+
+    __device__ __forceinline__ void rebase(float to, const ExpRef& ref, float c) {
+        EntSum was = get();
+        rebase_to<ENT>(was, to, c);
+        m = to;
+        r = ref.whole ? ref.r : -INFINITY;
+        sum = was.sum;
+        low = 0.f;
+        w = was.w;
     }
-    const float m = fmaxf(es.m, bm), t = m * c, r = ceilf(t);
-    EntSum was{es.m, es.sum, w};
-    if (m > -INFINITY) rebase_to<true>(was, m, c);
-    if (fabsf(t) < 4194304.f) {
-        const unsigned long long c2 = pack2(c, c), r2 = pack2(-r, -r);
-        unsigned long long acc = pack2(was.sum, 0.f), accw = pack2(was.w, 0.f);
+
+    template <int U>
+    __device__ __forceinline__ void add(uint4 (&v)[U], const TokArgs& a) {
+        float ws, s = sum_of(v, a, ws);
+        if (!(s < 65536.f)) {
+            // (a zero that the compiler does not know: else it keeps the first sum's conversions for the second, in registers
+            // that are not there)
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = make_uint4(v[u].x ^ a.zero, v[u].y ^ a.zero, v[u].z ^ a.zero, v[u].w ^ a.zero);
+            const float to = fmaxf(m, vecs_max<SX>(v));
+            const ExpRef ref(to, a.c);
+            if (!ref.whole) {
+#pragma unroll 1
+                for (int u = 0; u < U; ++u) {
+                    uint4 one = v[0];
+#pragma unroll
+                    for (int k = 1; k < U; ++k)
+                        if (k == u) one = v[k];
+                    add_far(one, a);
+                }
+                return;
+            }
+            rebase(to, ref, a.c);
+            if (ENT && SX == 2) least = least_pair(ref, a.inv_c);
+            s = sum_of(v, a, ws);                            // (NaN stays)
+        }
+        const TwoFloat t = two_sum(sum, s);
+        sum = t.hi;
+        low += t.lo;
+        if (ENT) w += ws;
+    }
+
+    template <int U>
+    __device__ __forceinline__ float sum_of(const uint4 (&v)[U], const TokArgs& a, float& ws) const {
+        const unsigned long long c2 = pack2(a.c, a.c), l2 = pack2(a.c_low, a.c_low), r2 = pack2(-r, -r);
+        unsigned long long acc[2] = {0ull, 0ull}, accw = 0ull;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int k = 0; k < VE / 2; ++k) {
+            for (int h = 0; h < VE / 2; ++h) {
+                unsigned long long x;
                 float lo, hi;
-                unpack2(fma2(pair_of<SX>(v[u], k), c2, r2), lo, hi);
+                if (ENT && SX == 2) {                        // (0 times -inf)
+                    const __nv_bfloat162 b = __hmax2_nan(reinterpret_cast<const __nv_bfloat162*>(&v[u])[h], *reinterpret_cast<const __nv_bfloat162*>(&least));
+                    const uint32_t bits = *reinterpret_cast<const uint32_t*>(&b);
+                    x = pack2(bf16_lo(bits), bf16_hi(bits));
+                } else {
+                    x = pair_of<SX>(v[u], h);
+                }
+                unsigned long long z = fma2(x, c2, r2);
+                if (!ENT) z = fma2(x, l2, z);
+                unpack2(z, lo, hi);
                 const unsigned long long e = pack2(ex2_approx(lo), ex2_approx(hi));
-                acc = add2(acc, e);
-                accw = fma2(e, pack2(fmaxf(lo, -16384.f), fmaxf(hi, -16384.f)), accw);   // (0 times -inf)
+                acc[h & 1] = add2(acc[h & 1], e);
+                if (ENT) accw = fma2(e, SX == 2 ? z : pack2(fmaxf(lo, -16384.f), fmaxf(hi, -16384.f)), accw);
             }
         float lo, hi;
-        unpack2(acc, lo, hi);
-        es.sum = lo + hi;
-        unpack2(accw, lo, hi);
-        w = lo + hi;
-    } else {
-        const float ref = m > -INFINITY ? m : 0.f;
-        es.sum = was.sum;
-        w = was.w;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int q = 0; q < VE; ++q) {
-                const float z = (elem<SX>(v[u], q) - ref) * c, e = ex2_approx(z);
-                es.sum += e;
-                w = fmaf(e, fmaxf(z, -16384.f), w);
-            }
+        if (ENT) {
+            unpack2(accw, lo, hi);
+            ws = lo + hi;
+        }
+        unpack2(add2(acc[0], acc[1]), lo, hi);
+        return lo + hi;
     }
-    es.m = m;
-    es.r = r;
-}
 
-// Replace logit i of a vector whose first is i0.
+    // Vectors of infinities, of the type's lowest values.
+    __device__ __forceinline__ void add_far(const uint4& v, const TokArgs& a) {
+        const float to = fmaxf(m, vec_max<SX>(v));
+        if (!(to > -INFINITY)) {                             // nothing yet; a NaN among it counts
+            float t = 0.f;
+#pragma unroll
+            for (int q = 0; q < VE; ++q) t += elem<SX>(v, q);
+            if (t != t) sum = t;
+            return;
+        }
+        const ExpRef ref(to, a.c);
+        rebase(to, ref, a.c);
+#pragma unroll
+        for (int q = 0; q < VE; ++q) {
+            const float x = elem<SX>(v, q), z = ref.whole ? fmaf(x, a.c, -ref.r) : (x - ref.m) * a.c, e = ex2_approx(z);
+            sum += e;
+            if (ENT) w = fmaf(e, fmaxf(z, -16384.f), w);
+        }
+        if (ENT && SX == 2 && ref.whole) least = least_pair(ref, a.inv_c);
+    }
+
+    // a logit whose exponential by the reference is 0, not below the type's lowest value
+    static __device__ __forceinline__ uint32_t least_pair(const ExpRef& ref, float inv_c) {
+        const float x = fmaxf((ref.r - 4096.f) * inv_c, -3.38e38f);
+        return pack_bf16(x, x);
+    }
+};
+
+// Replace logit `lane` of a vector.
 template <int SX>
 __device__ __forceinline__ void patch(uint4& v, int lane, uint32_t bits) {
 #pragma unroll
@@ -143,22 +229,9 @@ __device__ __forceinline__ void patch(uint4& v, int lane, uint32_t bits) {
         if (q == lane) put_bits<SX>(v, q, bits);
 }
 
-// log(1 + e^d) and 1 / (1 + e^-d)
-__device__ __forceinline__ TwoFloat softplus(const TwoFloat& d) {
-    if (!(d.hi > -INFINITY)) return TwoFloat{d.hi == d.hi ? 0.f : NAN, 0.f};
-    if (d.hi > 0.f) {
-        const float t = log1pf(expf(-d.hi));
-        if (!(d.hi < INFINITY)) return TwoFloat{d.hi, 0.f};
-        const TwoFloat s = two_sum(d.hi, t);
-        return TwoFloat{s.hi, s.lo + d.lo * (1.f - t)};
-    }
-    const float e = expf(d.hi);
-    return TwoFloat{log1pf(fmaf(e, d.lo, e)), 0.f};
-}
-__device__ __forceinline__ float sigmoid(float d) { return d > 0.f ? 1.f / (1.f + expf(-d)) : expf(d) / (1.f + expf(d)); }
-
-// e^D - D - 1 without the difference of near ones: its series where D is small (relative remainder below 2^-24)
-__device__ __forceinline__ float k3_of(float D) {
+// e^D - D - 1 without the difference of near ones: its series where D is small (relative remainder below 2^-24);
+// em1 is expm1f(D)
+__device__ __forceinline__ float k3_of(float D, float em1) {
     if (fabsf(D) < 0.25f) {
         float s = 1.f + D * (1.f / 9.f);
         s = fmaf(D * s, 1.f / 8.f, 1.f);
@@ -169,116 +242,173 @@ __device__ __forceinline__ float k3_of(float D) {
         s = fmaf(D * s, 1.f / 3.f, 1.f);
         return 0.5f * D * D * s;
     }
-    return expm1f(D) - D;
+    return em1 - D;
 }
 
 struct PolicyRow {
     float w, old, ref, adv;
 };
 
-// One row's results from its sum over the other tokens and its token's logit, by one thread.
+// A row's results, of which `saved` goes to its gradient.
+struct RowEnd {
+    RowSaved saved;
+    float logp, entropy, loss, kl;
+    int status;
+};
+
+// What log R - s_y is made of: log(1 + e^d) and log(1 + e^-d), 1 / (1 + e^-d) and 1 / (1 + e^d).
+struct Odds {
+    TwoFloat sp;
+    float sm, q, p;
+    __device__ __forceinline__ explicit Odds(const TwoFloat& d) {
+        const float t = expf(-fabsf(d.hi)), l = log1pf(t), inv = 1.f / (1.f + t), small = t * inv;
+        const bool up = d.hi > 0.f;
+        q = up ? inv : small;
+        p = up ? small : inv;
+        sm = up ? l : l - d.hi;
+        sp = up ? two_sum(d.hi, l) : TwoFloat{l, 0.f};
+        if (d.hi < INFINITY) sp.lo += d.lo * q;              // (the sum with an infinity has no error term)
+        else sp.lo = 0.f;
+    }
+};
+
+// From a row's sum over the other tokens and its token's logit, by one thread: on the way between the sum and the gradient,
+// so its steps are few and share what they can (1400 cycles in a first form: 45 of 500 us of policy_batch's rows).
 template <bool ENT>
-__device__ __forceinline__ RowSaved row_end(const TokArgs& a, long long row, const EntSum& es, float xy, const PolicyRow& pr) {
-    RowSaved s{0.f, -1.f, 0.f, 0.f, 0.f, 0.f, 0.f, -1};
-    int status = 0;
+__device__ __forceinline__ RowEnd row_end(const TokArgs& a, const EntSum& es, float xy, const PolicyRow& pr) {
+    RowEnd o{RowSaved{0.f, -1.f, 0.f, 0.f, 0.f, 0.f, 0.f, -1}, NAN, NAN, NAN, NAN, DSPARK_ROW_NONFINITE};
     const bool none = !(es.m > -INFINITY) && es.sum == es.sum;   // no other token has any mass
-    TwoFloat d{-INFINITY, 0.f};
-    if (!(xy < INFINITY) || es.sum != es.sum || !(es.m < INFINITY) || (none && !(xy > -INFINITY))) {
-        status = DSPARK_ROW_NONFINITE;
-    } else if (!none) {
+    if (!(xy < INFINITY) || es.sum != es.sum || !(es.m < INFINITY) || (none && !(xy > -INFINITY))) return o;
+    o.status = 0;
+    RowSaved& s = o.saved;
+    TwoFloat d{-INFINITY, 0.f}, lr{0.f, 0.f};
+    float mean = 0.f;                                        // of the others' exponents
+    if (!none) {
         const ExpRef ref(es.m, a.c);
+        lr = log_two(es.sum);
+        lr.lo += kEx2Lacks;
+        if (ENT) {
+            mean = es.w / es.sum;
+            if (ref.whole) lr.lo = fmaf(a.c_low * a.inv_c * kLn2, mean + ref.r, lr.lo);
+        }
         if (!(xy > -INFINITY)) {
             d.hi = INFINITY;
         } else if (ref.whole) {
             const TwoFloat p = two_prod(xy, a.c), by = two_sum(ref.r, -p.hi);
-            d = fabsf(p.hi) < INFINITY ? TwoFloat{by.hi, by.lo - p.lo} * ln2_two() + log_two(es.sum)
+            d = fabsf(p.hi) < INFINITY ? TwoFloat{by.hi, by.lo - fmaf(xy, a.c_low, p.lo)} * ln2_two() + lr
                                        : TwoFloat{xy > 0.f ? -INFINITY : INFINITY, 0.f};
         } else {
             const float by = (es.m - xy) * a.c;
-            d = fabsf(by) < INFINITY ? TwoFloat{by, 0.f} * ln2_two() + log_two(es.sum) : TwoFloat{by, 0.f};
+            d = fabsf(by) < INFINITY ? TwoFloat{by, 0.f} * ln2_two() + lr : TwoFloat{by, 0.f};
         }
+        s.m = es.m;
     }
-    TwoFloat lp{NAN, 0.f};
-    float H = NAN;
-    if (!status) {
-        const TwoFloat sp = softplus(d);
-        lp = -sp;
-        const float py = sigmoid(-d.hi), q = sigmoid(d.hi), sm = softplus(-d).hi;   // -log q
-        const float lr = none ? 0.f : logf(es.sum);
-        H = 0.f;
-        if (ENT) H = (py > 0.f ? py * sp.hi : 0.f) + (none || q == 0.f ? 0.f : q * (sm + (lr - kLn2 * (es.w / es.sum))));
-        s.m = none ? 0.f : es.m;
-        s.f = none ? 0.f : q / es.sum * a.inv_t;
-        s.level = none || !(sm < INFINITY) ? 0.f : H - lr - sm;
-        s.q = q * a.inv_t;
-        s.py = py > 0.f ? py * (lp.hi + H) * a.inv_t : 0.f;
-    }
-    const float logp = lp.hi + lp.lo;
+    const Odds k(d);
+    const TwoFloat lp = -k.sp;
+    float H = 0.f;
+    if (ENT) H = (k.p > 0.f ? k.p * k.sp.hi : 0.f) + (none || k.q == 0.f ? 0.f : k.q * (k.sm + fmaf(-kLn2, mean, lr.hi + lr.lo)));
+    s.f = none ? 0.f : k.q / es.sum * a.inv_t;
+    s.level = none || !(k.sm < INFINITY) ? 0.f : H - lr.hi - k.sm;
+    s.q = k.q * a.inv_t;
+    s.py = k.p > 0.f ? k.p * (lp.hi + H) * a.inv_t : 0.f;
+    o.logp = lp.hi + lp.lo;
+    o.entropy = H;
     if (a.op == kPolicy) {
-        float loss = NAN, kl = 0.f;
-        if (!status) {
-            const float rho = expf((lp.hi - pr.old) + lp.lo);
-            // the smaller of rho A and the clipped rho times A; clipping binds above for a gain, below for a loss
-            float gain = 0.f, by_lp = 0.f;
-            if (pr.adv != 0.f) {
-                const bool binds = pr.adv > 0.f ? rho > a.high : rho < a.low;
-                gain = (binds ? (pr.adv > 0.f ? a.high : a.low) : rho) * pr.adv;
-                by_lp = binds ? 0.f : -gain;
-            }
-            loss = -gain;
-            if (a.ref_lp) {
-                const float D = (pr.ref - lp.hi) - lp.lo;
-                kl = k3_of(D);
-                if (a.kl_coef != 0.f) {
-                    loss = fmaf(a.kl_coef, kl, loss);
-                    by_lp = fmaf(-a.kl_coef, expm1f(D), by_lp);
-                }
-            }
-            if (a.ent_coef != 0.f) loss = fmaf(-a.ent_coef, H, loss);
-            loss *= pr.w;
-            s.a = pr.w * by_lp;
-            s.h = -pr.w * a.ent_coef;
-            if (!(fabsf(loss) < INFINITY) || !(fabsf(s.a) < INFINITY)) {
-                status = DSPARK_ROW_NONFINITE;
-                loss = NAN;
-                s.f = -1.f;
+        // the smaller of rho A and the clipped rho times A; clipping binds above for a gain, below for a loss
+        const float rho = expf((lp.hi - pr.old) + lp.lo);
+        float gain = 0.f, by_lp = 0.f;
+        if (pr.adv != 0.f) {
+            const bool binds = pr.adv > 0.f ? rho > a.high : rho < a.low;
+            gain = (binds ? (pr.adv > 0.f ? a.high : a.low) : rho) * pr.adv;
+            by_lp = binds ? 0.f : -gain;
+        }
+        float loss = -gain;
+        o.kl = 0.f;
+        if (a.ref_lp) {
+            const float D = (pr.ref - lp.hi) - lp.lo, em1 = expm1f(D);
+            o.kl = k3_of(D, em1);
+            if (a.kl_coef != 0.f) {
+                loss = fmaf(a.kl_coef, o.kl, loss);
+                by_lp = fmaf(-a.kl_coef, em1, by_lp);
             }
         }
-        a.loss[row] = loss;
-        if (a.kl) a.kl[row] = status ? NAN : kl;
+        if (a.ent_coef != 0.f) loss = fmaf(-a.ent_coef, H, loss);
+        o.loss = loss * pr.w;
+        s.a = pr.w * by_lp;
+        s.h = -pr.w * a.ent_coef;
+        if (!(fabsf(o.loss) < INFINITY) || !(fabsf(s.a) < INFINITY)) {
+            o = RowEnd{s, NAN, NAN, NAN, NAN, DSPARK_ROW_NONFINITE};
+            o.saved.f = -1.f;
+        }
     } else if (a.op == kScore) {
         s.a = 1.f;
         s.h = ENT ? 1.f : NAN;                               // an entropy's gradient needs a call that asked for the entropy
-    } else if (!status) {
+    } else {
         s.level = lp.hi;                                     // a sequence's log ratios cancel: the sum takes both parts
         s.py = lp.lo;
     }
-    if (status && a.op != kPolicy) s.f = -1.f;
-    if (a.logp) a.logp[row] = status ? NAN : logp;
-    if (ENT && a.entropy) a.entropy[row] = status ? NAN : H;
-    a.row_status[row] = status;
-    return s;
+    return o;
+}
+__device__ __forceinline__ void row_write(const TokArgs& a, long long row, const RowEnd& o, bool entropy) {
+    if (a.logp) a.logp[row] = o.logp;
+    if (entropy && a.entropy) a.entropy[row] = o.entropy;
+    if (a.loss) a.loss[row] = o.loss;
+    if (a.kl) a.kl[row] = o.kl;
+    if (a.saved) a.saved[row] = o.saved;
+    a.row_status[row] = o.status;
 }
 
 // A row that is not read: without a token, of weight 0, or (status) with a token out of range.
 __device__ __forceinline__ void row_skipped(const TokArgs& a, long long row, int status) {
     const float v = status ? NAN : 0.f;
-    if (a.logp) a.logp[row] = v;
-    if (a.entropy) a.entropy[row] = v;
-    if (a.loss) a.loss[row] = v;
-    if (a.kl) a.kl[row] = v;
-    if (a.saved) a.saved[row] = RowSaved{0.f, -1.f, 0.f, 0.f, 0.f, 0.f, 0.f, -1};
-    a.row_status[row] = status;
+    row_write(a, row, RowEnd{RowSaved{0.f, -1.f, 0.f, 0.f, 0.f, 0.f, 0.f, -1}, v, v, v, v, status}, true);
 }
 
+// The place of logit i of a row among its vectors.
+template <int SX>
+struct Place {
+    int k, lane;
+    __device__ __forceinline__ Place(const VocabRow<SX>& x, int i) : k((i + x.a0) / VocabRow<SX>::VE), lane((i + x.a0) % VocabRow<SX>::VE) {}
+};
+
+__device__ __forceinline__ RowEnd row_bad(int status) {
+    return RowEnd{RowSaved{0.f, -1.f, 0.f, 0.f, 0.f, 0.f, 0.f, -1}, NAN, NAN, NAN, NAN, status};
+}
+
+// Sums between the CTAs of a row: each pushes its own to those that want it, where an mbarrier counts the bytes.
+struct __align__(16) PeerSum {
+    EntSum es;
+    float after;
+};
+__device__ __forceinline__ void expect_peers(uint64_t* bar, int n) {
+    if (threadIdx.x == 0) {
+        mbar_init(bar, 1);
+        fence_mbar_init();
+        mbar_arrive_expect_tx(bar, sizeof(PeerSum) * n);
+    }
+    cluster_arrive_relaxed();                                // before a peer can push here (the fence above orders it)
+}
+// after: something whose load has to be done before a peer may write
+__device__ __forceinline__ void push_sum(PeerSum* slot, uint64_t* bar, int to, const EntSum& es, float after) {
+    peer_push128(peer_addr(slot, to), peer_addr(bar, to), __float_as_uint(es.m), __float_as_uint(es.sum), __float_as_uint(es.w),
+                 __float_as_uint(after));
+}
+template <bool ENT>
+__device__ __forceinline__ EntSum peers_join(const PeerSum* s, int C, float c) {
+    const int k = threadIdx.x & (kMaxCluster - 1);
+    return lanes_join<ENT, kMaxCluster>(k < C ? s[k].es : EntSum{-INFINITY, 0.f, 0.f}, c);
+}
+
+constexpr int kStatsVec = 4;                                 // vectors a thread has on their way
 template <int SX, bool ENT>
-__global__ void __launch_bounds__(kRowThreads) stats_kernel(TokArgs a) {
+__global__ void __launch_bounds__(kRowThreads, 5) stats_kernel(TokArgs a) {
     __shared__ EntSum s_warp[kRowWarps];
-    __shared__ EntSum s_peer[kMaxCluster];                   // (in the row's first CTA) written by the cluster's
+    __shared__ PeerSum s_peer[kMaxCluster];                  // (in the row's first CTA) written by the cluster's
+    __shared__ uint64_t s_bar;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = 1 << a.log_c, rank = blockIdx.x & (C - 1);
     const long long row = blockIdx.x >> a.log_c;
-    if (C > 1) cluster_arrive_relaxed();
+    if (C > 1) expect_peers(&s_bar, C - 1);
     pdl_wait();
     const int y = a.tokens[row];
     PolicyRow pr{1.f, 0.f, 0.f, 0.f};
@@ -292,8 +422,6 @@ __global__ void __launch_bounds__(kRowThreads) stats_kernel(TokArgs a) {
     const VocabRow<SX> x(a.x, row, a.x_stride, a.V);
     const int k0 = static_cast<int>(static_cast<long long>(x.nvec) * rank >> a.log_c);
     const int k1 = static_cast<int>(static_cast<long long>(x.nvec) * (rank + 1) >> a.log_c);
-    constexpr int VE = VocabRow<SX>::VE;
-    const int ky = (y + x.a0) / VE, qy = (y + x.a0) % VE;    // the token's vector and lane
     float xy = 0.f;
     if (rank == 0 && tid == 0) {
         xy = load_logit<SX>(x, y);
@@ -303,45 +431,55 @@ __global__ void __launch_bounds__(kRowThreads) stats_kernel(TokArgs a) {
             if (a.ref_lp) pr.ref = a.ref_lp[row];
         }
     }
-    RunSum run;
-    float w = 0.f;
-    int k = k0 + tid;
-    for (; k + (kTokVec - 1) * kRowThreads < k1; k += kTokVec * kRowThreads) {
-        uint4 v[kTokVec];
+    // whole vectors [w0, w1) go straight through; the token's is its owner's business
+    const int w0 = k0 + (k0 < k1 && !x.whole(k0)), w1 = k1 - (k1 > w0 && !x.whole(k1 - 1));
+    const Place<SX> at(x, y);
+    const int own = (at.k - w0) % kRowThreads == tid ? at.k : -1;
+    RunEnt<SX, ENT> run;
+    int k = w0 + tid;
+    const uint4* p = reinterpret_cast<const uint4*>(x.p + static_cast<long long>(x.first(k)) * SX);
+    for (; k + (kStatsVec - 1) * kRowThreads < w1; k += kStatsVec * kRowThreads, p += kStatsVec * kRowThreads) {
+        uint4 v[kStatsVec];
 #pragma unroll
-        for (int u = 0; u < kTokVec; ++u) v[u] = load_vec<SX>(x, k + u * kRowThreads, k1);
+        for (int u = 0; u < kStatsVec; ++u) v[u] = ld_vec16(p + u * kRowThreads);
+        if (own >= k && own < k + kStatsVec * kRowThreads) {
 #pragma unroll
-        for (int u = 0; u < kTokVec; ++u)
-            if (k + u * kRowThreads == ky) patch<SX>(v[u], qy, ninf_bits<SX>());
-        add_vecs<SX, ENT>(run, w, v, vecs_max<SX>(v), a.c);
+            for (int u = 0; u < kStatsVec; ++u)
+                if (k + u * kRowThreads == own) patch<SX>(v[u], at.lane, ninf_bits<SX>());
+        }
+        run.add(v, a);
     }
-    for (; k < k1; k += kRowThreads) {
-        uint4 v[1] = {load_vec<SX>(x, k, k1)};
-        if (k == ky) patch<SX>(v[0], qy, ninf_bits<SX>());
-        add_vecs<SX, ENT>(run, w, v, vecs_max<SX>(v), a.c);
+    for (; k < w1; k += kRowThreads, p += kRowThreads) {
+        uint4 v[1] = {ld_vec16(p)};
+        if (k == own) patch<SX>(v[0], at.lane, ninf_bits<SX>());
+        run.add(v, a);
     }
-    EntSum es = lanes_join<ENT>(EntSum{run.m, run.sum, w}, 32, a.c);
+    if (tid < 2) {                                           // the ragged ends
+        const int e = tid ? w1 : k0;
+        if (tid ? w1 < k1 : k0 < w0) {
+            uint4 v[1] = {load_vec<SX>(x, e, k1)};
+            if (e == at.k) patch<SX>(v[0], at.lane, ninf_bits<SX>());
+            run.add(v, a);
+        }
+    }
+    EntSum es = lanes_join<ENT, 32>(run.get(), a.c);
     if (lane == 0) s_warp[warp] = es;
     __syncthreads();
-    if (warp == 0) es = lanes_join<ENT>(s_warp[lane & (kRowWarps - 1)], kRowWarps, a.c);
+    if (C > 1) cluster_wait();
+    if (warp != 0) return;
+    es = lanes_join<ENT, kRowWarps>(s_warp[lane & (kRowWarps - 1)], a.c);
+    bool late = false;
     if (C > 1) {
-        cluster_wait();                                      // the row's first CTA is there
-        if (tid == 0) {
-            const unsigned at = peer_addr(&s_peer[rank], 0);
-            asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(at), "f"(es.m) : "memory");
-            asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(at + 4), "f"(es.sum) : "memory");
-            asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(at + 8), "f"(es.w) : "memory");
+        if (rank != 0) {                                     // to the row's first CTA, which is there and waits
+            if (lane == 0) push_sum(&s_peer[rank], &s_bar, 0, es, 0.f);
+            return;
         }
-        cluster_arrive();
-        cluster_wait();
-        if (rank == 0 && warp == 0)
-            es = lanes_join<ENT>((lane & (kMaxCluster - 1)) < C ? s_peer[lane & (kMaxCluster - 1)] : EntSum{-INFINITY, 0.f, 0.f},
-                                 kMaxCluster, a.c);
+        if (lane == 0) s_peer[0].es = es;
+        __syncwarp();
+        late = !bar_wait(&s_bar, 0, kPeerMs);
+        es = peers_join<ENT>(s_peer, C, a.c);
     }
-    if (rank == 0 && tid == 0) {
-        const RowSaved s = row_end<ENT>(a, row, es, xy, pr);
-        if (a.saved) a.saved[row] = s;
-    }
+    if (lane == 0) row_write(a, row, late ? row_bad(DSPARK_ROW_INTERNAL) : row_end<ENT>(a, es, xy, pr), ENT);
 }
 
 template <int SX>
@@ -360,84 +498,295 @@ __device__ __forceinline__ void store_vec(const VocabRow<SX>& g, int i0, const u
         else reinterpret_cast<unsigned*>(p)[i] = word_of(w, q);
     }
 }
-
-// What a row's gradient is made with: e_v (a0 + a1 z_v) for exponentials e_v = 2^z_v, and the token's own.
-struct RowGrad {
-    float a0, a1, at_y;
-};
-__device__ __forceinline__ RowGrad row_grad(const RowSaved& s, float a, float h) {
-    return RowGrad{-s.f * fmaf(h, s.level, a), -s.f * h * kLn2, a * s.q - h * s.py};
+template <int SX>
+__device__ __forceinline__ void store_one(const VocabRow<SX>& g, int i, float v) {
+    unsigned char* p = const_cast<unsigned char*>(g.p);
+    if (SX == 2) reinterpret_cast<unsigned short*>(p)[i] = static_cast<unsigned short>(to_bits<SX>(v));
+    else reinterpret_cast<float*>(p)[i] = v;
 }
 
+// What a row's gradient is made with: e_v (a0 + a1 z_v) for exponentials e_v = 2^z_v, and the token's own.
 template <int SX, bool ENT>
-__device__ __forceinline__ uint4 grad_vec(const uint4& v, const ExpRef& ref, const RowGrad& rg) {
-    constexpr int VE = 16 / SX;
-    float f[VE];
-    const unsigned long long c2 = pack2(ref.c, ref.c), r2 = pack2(-ref.r, -ref.r);
-#pragma unroll
-    for (int h = 0; h < VE / 2; ++h) {
-        float lo, hi;
-        if (ref.whole) {
-            unpack2(fma2(pair_of<SX>(v, h), c2, r2), lo, hi);
-        } else {
-            lo = (elem<SX>(v, 2 * h) - ref.m) * ref.c;
-            hi = (elem<SX>(v, 2 * h + 1) - ref.m) * ref.c;
+struct RowGrad {
+    static constexpr int VE = 16 / SX;
+    ExpRef ref;
+    float c_low, a0, a1, at_y;
+    uint32_t least;
+
+    __device__ __forceinline__ RowGrad(const TokArgs& a, const RowSaved& s, float da, float dh)
+        : ref(s.m, a.c), c_low(a.c_low), a0(-s.f * fmaf(dh, s.level, da)), a1(-s.f * dh * kLn2), at_y(da * s.q - dh * s.py) {
+        if (!ENT) {
+            a0 = -s.f * da;
+            at_y = da * s.q;
         }
-        const unsigned long long e = pack2(ex2_approx(lo), ex2_approx(hi));
-        unsigned long long k = pack2(rg.a0, rg.a0);
-        if (ENT) k = fma2(pack2(fmaxf(lo, -16384.f), fmaxf(hi, -16384.f)), pack2(rg.a1, rg.a1), k);
-        unpack2(mul2(e, k), f[2 * h], f[2 * h + 1]);
+        least = ENT && SX == 2 ? RunEnt<SX, ENT>::least_pair(ref, a.inv_c) : 0u;
     }
-    if (SX == 2) return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4 % VE], f[5 % VE]), pack_bf16(f[6 % VE], f[7 % VE]));
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    __device__ __forceinline__ static uint4 pack(const float (&f)[VE]) {
+        if (SX == 2) return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4 % VE], f[5 % VE]), pack_bf16(f[6 % VE], f[7 % VE]));
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+    // by a reference with a whole exponent
+    __device__ __forceinline__ uint4 of(const uint4& v) const {
+        float f[VE];
+        const unsigned long long c2 = pack2(ref.c, ref.c), l2 = pack2(c_low, c_low), r2 = pack2(-ref.r, -ref.r);
+#pragma unroll
+        for (int h = 0; h < VE / 2; ++h) {
+            unsigned long long x;
+            if (ENT && SX == 2) {
+                const __nv_bfloat162 b = __hmax2(reinterpret_cast<const __nv_bfloat162*>(&v)[h], *reinterpret_cast<const __nv_bfloat162*>(&least));
+                const uint32_t bits = *reinterpret_cast<const uint32_t*>(&b);
+                x = pack2(bf16_lo(bits), bf16_hi(bits));
+            } else {
+                x = pair_of<SX>(v, h);
+            }
+            unsigned long long z = fma2(x, c2, r2);
+            if (SX == 4) z = fma2(x, l2, z);                 // (bf16 holds nothing that the second part would change)
+            float lo, hi;
+            unpack2(z, lo, hi);
+            unsigned long long k = pack2(a0, a0);
+            if (ENT) k = fma2(SX == 2 ? z : pack2(fmaxf(lo, -16384.f), fmaxf(hi, -16384.f)), pack2(a1, a1), k);
+            unpack2(mul2(pack2(ex2_approx(lo), ex2_approx(hi)), k), f[2 * h], f[2 * h + 1]);
+        }
+        return pack(f);
+    }
+    // by the types' lowest values
+    __device__ __forceinline__ uint4 far_of(const uint4& v) const {
+        float f[VE];
+#pragma unroll
+        for (int q = 0; q < VE; ++q) {
+            const float z = (elem<SX>(v, q) - ref.m) * ref.c;
+            f[q] = ex2_approx(z) * (ENT ? fmaf(fmaxf(z, -16384.f), a1, a0) : a0);
+        }
+        return pack(f);
+    }
+};
+
+// The gradient of vectors [k0, k1) of a row (or zeros), by the CTA's threads in turn, from get(k), which gives vector k to
+// the thread that asks for it; the token's entry by the thread that has its vector.
+template <int SX, bool ENT, int U, typename Get>
+__device__ __forceinline__ void write_grad(const VocabRow<SX>& x, const VocabRow<SX>& g, int k0, int k1, int y, bool zero,
+                                           const RowGrad<SX, ENT>& rg, Get get) {
+    const int tid = threadIdx.x;
+    const bool same_phase = x.a0 == g.a0;
+    int k = k0 + tid;
+    if (zero) {
+        for (; k < k1; k += kRowThreads) store_vec<SX>(g, x.first(k), make_uint4(0, 0, 0, 0), same_phase);
+        return;
+    }
+    if (same_phase && rg.ref.whole) {
+        // whole vectors go straight through, by the threads that have them
+        const int w0 = k0 + (k0 < k1 && !x.whole(k0)), w1 = k1 - (k1 > w0 && !x.whole(k1 - 1));
+        if (k < w0) k += kRowThreads;
+        unsigned char* p = const_cast<unsigned char*>(g.p) + static_cast<long long>(x.first(k)) * SX;
+        for (; k + (U - 1) * kRowThreads < w1; k += U * kRowThreads, p += 16 * U * kRowThreads) {
+            uint4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = get(k + u * kRowThreads);
+#pragma unroll
+            for (int u = 0; u < U; ++u) st_vec16(p + 16 * u * kRowThreads, rg.of(v[u]));
+        }
+        for (; k < w1; k += kRowThreads, p += 16 * kRowThreads) st_vec16(p, rg.of(get(k)));
+        if (tid == 0 && k0 < w0) store_vec<SX>(g, x.first(k0), rg.of(get(k0)), false);
+        if (w1 < k1 && (k1 - 1 - k0) % kRowThreads == tid) store_vec<SX>(g, x.first(k1 - 1), rg.of(get(k1 - 1)), false);
+    } else {
+        for (; k < k1; k += kRowThreads) {
+            const uint4 v = get(k);
+            store_vec<SX>(g, x.first(k), rg.ref.whole ? rg.of(v) : rg.far_of(v), same_phase);
+        }
+    }
+    const Place<SX> at(x, y);
+    if (at.k >= k0 && at.k < k1 && (at.k - k0) % kRowThreads == tid) store_one<SX>(g, y, rg.at_y);
 }
 
 template <int SX, bool ENT>
 __global__ void __launch_bounds__(kRowThreads) grad_kernel(TokArgs a) {
-    constexpr int VE = VocabRow<SX>::VE;
     const long long row = blockIdx.x / a.splits;
     const int part = blockIdx.x % a.splits;
     pdl_wait();
     const VocabRow<SX> x(a.x, row, a.x_stride, a.V), g(a.g, row, a.g_stride, a.V);
-    const bool same_phase = x.a0 == g.a0;
     const int k0 = part * kGradVecs, k1 = min(x.nvec, k0 + kGradVecs);
     RowSaved s = a.saved[row];
     const int y = a.tokens[row];
     if (a.op == kPreference) s.level = s.py = 0.f;
-    float ga = s.a, gh = s.h;
+    float da = s.a, dh = s.h;
     if (a.op == kScore) {
-        ga = a.up ? a.up[row] : 0.f;
-        gh = ENT && a.up_entropy ? s.h * a.up_entropy[row] : 0.f;
+        da = a.up ? a.up[row] : 0.f;
+        dh = ENT && a.up_entropy ? s.h * a.up_entropy[row] : 0.f;
     } else if (a.op == kPolicy) {
         const float u = a.up ? a.up[row] : 1.f;
-        ga *= u;
-        gh *= u;
+        da *= u;
+        dh *= u;
     } else if (a.up) {
-        ga = s.pair >= 0 && s.pair < a.n_up ? ga * a.up[s.pair] : 0.f;
+        da = s.pair >= 0 && s.pair < a.n_up ? da * a.up[s.pair] : 0.f;
     }
-    if (s.f < 0.f || (ga == 0.f && gh == 0.f)) {
-        for (int k = k0 + threadIdx.x; k < k1; k += kRowThreads) store_vec<SX>(g, x.first(k), make_uint4(0, 0, 0, 0), same_phase);
+    const RowGrad<SX, ENT> rg(a, s, da, dh);
+    write_grad<SX, ENT, kTokVec>(x, g, k0, k1, y, s.f < 0.f || (da == 0.f && dh == 0.f), rg, [&](int k) { return load_vec<SX>(x, k, k1); });
+}
+
+// ---------------------------------------------------------------- loss and gradient in one
+// What a policy row's gradient is made with, on the way between its sum and its gradient, where the whole CTA waits: base 2
+// and the hardware's functions, a third of row_end's steps (its chain of dependent instructions, run by one warp
+// among forty, took 42 of 434 us of policy_batch's rows).  Logarithms are split from their exponents, so that their
+// 2^-22 is absolute; what cancels has two parts.  Off by some 4e-7 relative where row_end is by 2e-7.
+struct QuickRow {
+    TwoFloat old2, ref2;                                     // log-probabilities by log2(e)
+    float w, adv;
+};
+__device__ __forceinline__ TwoFloat base2(float v) {
+    const TwoFloat p = two_prod(v, kLog2E);
+    return TwoFloat{p.hi, fabsf(p.hi) < INFINITY ? fmaf(v, 1.9259629e-8f, p.lo) : 0.f};
+}
+__device__ __forceinline__ float lg2_approx(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Whether quick_end takes the row: the others have a whole exponent and a sum, the token a logit among them.
+__device__ __forceinline__ bool is_quick(const EntSum& es, float xy, float c) {
+    return fabsf(es.m * c) < 4194304.f && es.sum > 0x1p-60f && es.sum < 0x1p60f && fabsf(xy * c) < 4194304.f;
+}
+template <bool ENT>
+__device__ __forceinline__ RowSaved quick_end(const TokArgs& a, const EntSum& es, float xy, const QuickRow& pr) {
+    RowSaved s{es.m, -1.f, 0.f, 0.f, 0.f, 0.f, 0.f, -1};
+    const float r = ceilf(es.m * a.c), by_sum = rcp_approx(es.sum), mean = ENT ? es.w * by_sum : 0.f;
+    const int e = (__float_as_int(es.sum) - 0x3F400000) >> 23;
+    float l = lg2_approx(__int_as_float(__float_as_int(es.sum) - (e << 23))) + kEx2Lacks * kLog2E;
+    if (ENT) l = fmaf(a.c_low * a.inv_c, mean + r, l);
+    const TwoFloat p = two_prod(xy, a.c), top = two_sum(r + static_cast<float>(e), -p.hi);
+    const float rest = top.lo + (l - fmaf(xy, a.c_low, p.lo)), d = top.hi + rest;   // log2 of R / e^s_y
+    const float t = ex2_approx(-fabsf(d)), u = 1.f + t, inv = rcp_approx(u), small = t * inv;
+    const bool up = d > 0.f;
+    const float q = up ? inv : small, py = up ? small : inv;
+    // log2(1 + t): its series where the logarithm of 1 + t would lose t
+    const float lu = t < 0.03125f ? t * kLog2E * fmaf(t, fmaf(t, fmaf(t, -0.25f, 1.f / 3.f), -0.5f), 1.f) : lg2_approx(u);
+    const TwoFloat lp{up ? -top.hi : 0.f, up ? -(rest + lu) : -lu};   // log2 of p
+    float H = 0.f;
+    if (ENT) {
+        const float sm = kLn2 * (up ? lu : lu - d), lr = kLn2 * (static_cast<float>(e) + l);
+        H = fmaf(q, sm + fmaf(-kLn2, mean, lr), -py * kLn2 * (lp.hi + lp.lo));
+        s.level = H - lr - sm;
+        s.py = py * fmaf(kLn2, lp.hi + lp.lo, H) * a.inv_t;
+    }
+    s.q = q * a.inv_t;
+    const float rho = ex2_approx((lp.hi - pr.old2.hi) + (lp.lo - pr.old2.lo));
+    float gain = 0.f, by_lp = 0.f;
+    if (pr.adv != 0.f) {
+        const bool binds = pr.adv > 0.f ? rho > a.high : rho < a.low;
+        gain = (binds ? (pr.adv > 0.f ? a.high : a.low) : rho) * pr.adv;
+        by_lp = binds ? 0.f : -gain;
+    }
+    float loss = -gain;
+    if (a.ref_lp) {
+        const float D2 = (pr.ref2.hi - lp.hi) + (pr.ref2.lo - lp.lo), D = kLn2 * D2;
+        const float em1 = fabsf(D) < 0.0625f ? D * fmaf(D, fmaf(D, fmaf(D, fmaf(D, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f), 1.f) : ex2_approx(D2) - 1.f;
+        loss += a.kl_coef != 0.f ? a.kl_coef * (em1 - D) : 0.f * (em1 - D);
+        if (a.kl_coef != 0.f) by_lp = fmaf(-a.kl_coef, em1, by_lp);
+    }
+    s.a = pr.w * by_lp;
+    s.h = -pr.w * a.ent_coef;
+    if (fabsf(loss * pr.w) < INFINITY && fabsf(s.a) < INFINITY) s.f = q * by_sum * a.inv_t;
+    return s;
+}
+
+// A policy row's loss and gradient without reading it twice: a cluster of C CTAs keeps the row in shared memory, a span
+// each, between the sum and the gradient.  A thread copies the vectors that it will read, so that nothing but the joins
+// of the sums has to wait for anyone.
+constexpr int kFusedSpan = 4608;                             // vectors of a span at most
+constexpr int kFusedCtas = 5;                                // CTAs to an SM at most
+
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_here() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+template <int SX, bool ENT>
+__global__ void __launch_bounds__(kRowThreads, kFusedCtas) fused_kernel(TokArgs a) {
+    __shared__ EntSum s_warp[kRowWarps];
+    __shared__ PeerSum s_peer[kMaxCluster];                  // written by the row's CTAs
+    __shared__ RowSaved s_row;
+    __shared__ uint64_t s_bar;
+    extern __shared__ uint4 s_x[];                           // [span]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int C = a.splits, rank = static_cast<int>(cluster_rank());
+    const long long row = cluster_id();
+    if (C > 1) expect_peers(&s_bar, C);
+    pdl_wait();
+    const int y = a.tokens[row];
+    PolicyRow pr{1.f, 0.f, 0.f, 0.f};
+    if (a.weights) pr.w = a.weights[row];
+    const bool bad = y < -1 || y >= a.V, dead = bad || y < 0 || pr.w == 0.f;   // the same in every CTA of the row
+    const VocabRow<SX> x(a.x, row, a.x_stride, a.V), g(a.g, row, a.g_stride, a.V);
+    const int k0 = min(x.nvec, rank * a.span), cnt = min(x.nvec, k0 + a.span) - k0;
+    if (dead) {
+        if (rank == 0 && tid == 0) row_skipped(a, row, bad ? DSPARK_ROW_BAD_TOKEN : 0);
+        for (int k = tid; k < cnt; k += kRowThreads) store_vec<SX>(g, x.first(k0 + k), make_uint4(0, 0, 0, 0), x.a0 == g.a0);
+        if (C > 1) cluster_wait();
         return;
     }
-    const RowGrad rg = row_grad(s, ga, gh);
-    const ExpRef ref(s.m, a.c);
-    const int ky = (y + x.a0) / VE, qy = (y + x.a0) % VE;
-    int k = k0 + threadIdx.x;
-    for (; k + (kTokVec - 1) * kRowThreads < k1; k += kTokVec * kRowThreads) {
-        uint4 v[kTokVec];
+    const unsigned char* const src = x.p + static_cast<long long>(x.first(k0)) * SX;   // of vector 0, which may lack some
+    for (int k = tid; k < cnt; k += kRowThreads) {
+        if ((k == 0 || k == cnt - 1) && !x.whole(k0 + k)) s_x[k] = load_vec<SX>(x, k0 + k, k0 + cnt);
+        else copy_async16(s_x + k, src + 16LL * k);
+    }
+    copy_commit();
+    float xy = 0.f;
+    if (warp == 0) {
+        xy = load_logit<SX>(x, y);
+        pr.old = a.old_lp[row];
+        pr.adv = a.adv[row];
+        if (a.ref_lp) pr.ref = a.ref_lp[row];
+    }
+    const Place<SX> at(x, y);
+    RunEnt<SX, ENT> run;
+    copies_here();
+    // the token leaves the sum (and the gradient's loop) here
+    if (at.k >= k0 && at.k < k0 + cnt && (at.k - k0) % kRowThreads == tid) patch<SX>(s_x[at.k - k0], at.lane, ninf_bits<SX>());
+    {
+        int k = tid;
+        for (; k + (kTokVec - 1) * kRowThreads < cnt; k += kTokVec * kRowThreads) {
+            uint4 v[kTokVec];
 #pragma unroll
-        for (int u = 0; u < kTokVec; ++u) v[u] = load_vec<SX>(x, k + u * kRowThreads, k1);
-#pragma unroll
-        for (int u = 0; u < kTokVec; ++u) {
-            uint4 o = grad_vec<SX, ENT>(v[u], ref, rg);
-            if (k + u * kRowThreads == ky) patch<SX>(o, qy, to_bits<SX>(rg.at_y));
-            store_vec<SX>(g, x.first(k + u * kRowThreads), o, same_phase);
+            for (int u = 0; u < kTokVec; ++u) v[u] = s_x[k + u * kRowThreads];
+            run.add(v, a);
+        }
+        for (; k < cnt; k += kRowThreads) {
+            uint4 v[1] = {s_x[k]};
+            run.add(v, a);
         }
     }
-    for (; k < k1; k += kRowThreads) {
-        uint4 o = grad_vec<SX, ENT>(load_vec<SX>(x, k, k1), ref, rg);
-        if (k == ky) patch<SX>(o, qy, to_bits<SX>(rg.at_y));
-        store_vec<SX>(g, x.first(k), o, same_phase);
+    EntSum es = lanes_join<ENT, 32>(run.get(), a.c);
+    if (lane == 0) s_warp[warp] = es;
+    __syncthreads();
+    if (C > 1) cluster_wait();                               // the row's CTAs are there
+    bool late = false;
+    if (warp == 0) {
+        es = lanes_join<ENT, kRowWarps>(s_warp[lane & (kRowWarps - 1)], a.c);
+        if (C > 1) {
+            // the token's logit has been read: its place may be written, where the gradient takes the logits' place
+            if (lane < C) push_sum(&s_peer[rank], &s_bar, lane, es, xy);
+            late = !bar_wait(&s_bar, 0, kPeerMs);
+            es = peers_join<ENT>(s_peer, C, a.c);
+        }
+        if (lane == 0) {
+            if (late) s_row = row_bad(DSPARK_ROW_INTERNAL).saved;
+            else s_row = is_quick(es, xy, a.c) ? quick_end<ENT>(a, es, xy, QuickRow{base2(pr.old), base2(pr.ref), pr.w, pr.adv})
+                                               : row_end<ENT>(a, es, xy, pr).saved;
+        }
+    }
+    __syncthreads();
+    const RowGrad<SX, ENT> rg(a, s_row, s_row.a, s_row.h);
+    const bool zero = s_row.f < 0.f;
+    write_grad<SX, ENT, 1>(x, g, k0, k0 + cnt, y, zero, rg, [&](int k) { return s_x[k - k0]; });
+    if (rank == 0 && tid == 0) {
+        RowEnd o = late ? row_bad(DSPARK_ROW_INTERNAL) : row_end<ENT>(a, es, xy, pr);
+        if (zero && !o.status) o = row_bad(DSPARK_ROW_NONFINITE);   // (a loss next to fp32's largest number)
+        row_write(a, row, o, ENT);
     }
 }
 
@@ -524,13 +873,13 @@ __global__ void __launch_bounds__(kRowThreads) pair_kernel(PairArgs a) {
         if (fabsf(z.hi) < INFINITY) z = reward[0] + -reward[1] + TwoFloat{-a.margin, 0.f};
         if (!st && z.hi != z.hi) st = DSPARK_ROW_NONFINITE;
         const float w = a.weights ? a.weights[p] : 1.f, e = a.smoothing;
-        const TwoFloat down = softplus(-z), up = softplus(z);   // -log sigma(z), -log sigma(-z)
+        const Odds of(z);                                    // -log sigma(z) = log(1 + e^-z), -log sigma(-z) = log(1 + e^z)
         float loss = 0.f, by_z = 0.f;
         if (w != 0.f) {
-            loss = (1.f - e) * (down.hi + down.lo);
-            if (e > 0.f) loss += e * (up.hi + up.lo);
+            loss = (1.f - e) * (of.sm - (z.lo * of.p));
+            if (e > 0.f) loss += e * (of.sp.hi + of.sp.lo);
             loss *= w;
-            by_z = w * (e * sigmoid(z.hi) - (1.f - e) * sigmoid(-z.hi));
+            by_z = w * (e * of.q - (1.f - e) * of.p);
         }
         a.loss[p] = st ? NAN : loss;
         if (a.rewards)
@@ -551,7 +900,10 @@ dspark_status_t token_args(const void* logits, const dspark_token_params_t* p, c
     if (!logits || !p || !p->tokens) return DSPARK_ERR_INVALID_ARG;
     if (p->n_rows < 1 || p->n_rows > DSPARK_MAX_ROWS || p->V < 1 || p->V > DSPARK_MAX_V) return DSPARK_ERR_INVALID_ARG;
     if (p->logits_dtype != DSPARK_BF16 && p->logits_dtype != DSPARK_FP32) return DSPARK_ERR_INVALID_ARG;
-    const float c = kLog2E / p->temperature, inv_t = 1.f / p->temperature;
+    const double exact = 1.44269504088896340736 / p->temperature;
+    float c = static_cast<float>(exact);
+    if (c > exact) c = std::nextafter(c, 0.f);               // below, so that c_low > 0 and -inf times both is -inf
+    const float inv_t = 1.f / p->temperature;
     if (!(p->temperature > 0.f) || !(c > 0.f) || !(c < INFINITY) || !(inv_t < INFINITY)) return DSPARK_ERR_INVALID_ARG;
     *sx = p->logits_dtype == DSPARK_BF16 ? 2 : 4;
     if (p->logits_stride < p->V || reinterpret_cast<uintptr_t>(logits) % *sx) return DSPARK_ERR_INVALID_ARG;
@@ -559,7 +911,9 @@ dspark_status_t token_args(const void* logits, const dspark_token_params_t* p, c
     if (grad == logits && p->grad_stride != p->logits_stride) return DSPARK_ERR_INVALID_ARG;
     a->V = p->V;
     a->c = c;
+    a->c_low = std::max(static_cast<float>(exact - c), std::numeric_limits<float>::denorm_min());
     a->inv_t = inv_t;
+    a->inv_c = std::min(1.f / c, std::numeric_limits<float>::max());
     a->x = logits;
     a->x_stride = p->logits_stride;
     a->g = const_cast<void*>(grad);
@@ -593,6 +947,38 @@ dspark_status_t launch_grad(TokArgs& a, int sx, bool entropy, const dspark_token
     auto kern = sx == 2 ? (entropy ? grad_kernel<2, true> : grad_kernel<2, false>)
                         : (entropy ? grad_kernel<4, true> : grad_kernel<4, false>);
     const cudaError_t e = launch_cluster(kern, static_cast<unsigned>(grid), kRowThreads, 1, 0, static_cast<cudaStream_t>(p->stream), a);
+    return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+// CTAs of a row whose span stays in shared memory; 0 when the row is too long for eight of them.
+int fused_split(int nvec, long long rows) {
+    int C = 1;
+    while (C < kMaxCluster && nvec >= C * 512 && rows * 2 * C <= 320) C *= 2;
+    int best = 0;
+    for (int c = C, most = 0; c <= kMaxCluster; ++c) {
+        const int span = (nvec + c - 1) / c;
+        if (c > C && span < 512) break;
+        if (span > kFusedSpan) continue;
+        const int held = span * std::min(kFusedCtas, 228 * 1024 / (16 * span + 2 * 1024));
+        if (held >= most) {
+            most = held;
+            best = c;
+        }
+    }
+    return best;
+}
+
+dspark_status_t launch_fused(TokArgs& a, int sx, bool entropy, const dspark_token_params_t* p, int C) {
+    a.splits = C;
+    a.span = (max_vectors(p->V, sx) + C - 1) / C;
+    auto kern = sx == 2 ? (entropy ? fused_kernel<2, true> : fused_kernel<2, false>)
+                        : (entropy ? fused_kernel<4, true> : fused_kernel<4, false>);
+    const size_t smem = static_cast<size_t>(a.span) * 16;
+    // beyond what a launch gets unasked; the same for every call, as another thread's may come between
+    if (smem > 32 * 1024 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 16 * kFusedSpan) != cudaSuccess)
+        return DSPARK_ERR_CUDA;
+    const cudaError_t e = launch_cluster(kern, static_cast<unsigned>(p->n_rows) * C, kRowThreads, C, smem,
+                                         static_cast<cudaStream_t>(p->stream), a);
     return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
@@ -660,7 +1046,10 @@ dspark_status_t dspark_policy_loss(const void* logits, const dspark_policy_t* po
     a.entropy = out_entropy;
     a.kl = out_kl;
     a.saved = reinterpret_cast<RowSaved*>(out_saved);
-    const dspark_status_t st = launch_stats(a, sx, out_entropy || policy->entropy_coef != 0.f, params);
+    const bool entropy = out_entropy || policy->entropy_coef != 0.f;
+    if (out_grad)
+        if (const int C = fused_split(max_vectors(params->V, sx), params->n_rows); C > 0) return launch_fused(a, sx, entropy, params, C);
+    const dspark_status_t st = launch_stats(a, sx, entropy, params);
     if (st != DSPARK_OK || !out_grad) return st;
     return launch_grad(a, sx, policy->entropy_coef != 0.f, params);
 }
