@@ -378,7 +378,7 @@ __device__ __forceinline__ RowEnd row_bad(int status) {
 // Sums between the CTAs of a row: each pushes its own to those that want it, where an mbarrier counts the bytes.
 struct __align__(16) PeerSum {
     EntSum es;
-    float after;
+    uint32_t after;
 };
 __device__ __forceinline__ void expect_peers(uint64_t* bar, int n) {
     if (threadIdx.x == 0) {
@@ -389,9 +389,9 @@ __device__ __forceinline__ void expect_peers(uint64_t* bar, int n) {
     cluster_arrive_relaxed();                                // before a peer can push here (the fence above orders it)
 }
 // after: something whose load has to be done before a peer may write
-__device__ __forceinline__ void push_sum(PeerSum* slot, uint64_t* bar, int to, const EntSum& es, float after) {
+__device__ __forceinline__ void push_sum(PeerSum* slot, uint64_t* bar, int to, const EntSum& es, uint32_t after) {
     peer_push128(peer_addr(slot, to), peer_addr(bar, to), __float_as_uint(es.m), __float_as_uint(es.sum), __float_as_uint(es.w),
-                 __float_as_uint(after));
+                 after);
 }
 template <bool ENT>
 __device__ __forceinline__ EntSum peers_join(const PeerSum* s, int C, float c) {
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kRowThreads, 5) stats_kernel(TokArgs a) {
     bool late = false;
     if (C > 1) {
         if (rank != 0) {                                     // to the row's first CTA, which is there and waits
-            if (lane == 0) push_sum(&s_peer[rank], &s_bar, 0, es, 0.f);
+            if (lane == 0) push_sum(&s_peer[rank], &s_bar, 0, es, 0u);
             return;
         }
         if (lane == 0) s_peer[0].es = es;
@@ -699,52 +699,52 @@ __device__ __forceinline__ RowSaved quick_end(const TokArgs& a, const EntSum& es
 constexpr int kFusedSpan = 4608;                             // vectors of a span at most
 constexpr int kFusedCtas = 5;                                // CTAs to an SM at most
 
-__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copies_here() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
-
-template <int SX, bool ENT>
-__global__ void __launch_bounds__(kRowThreads, kFusedCtas) fused_kernel(TokArgs a) {
+template <int SX, bool ENT, bool GRAD>
+__global__ void __launch_bounds__(kRowThreads, kFusedCtas) kept_kernel(TokArgs a) {
     __shared__ EntSum s_warp[kRowWarps];
     __shared__ PeerSum s_peer[kMaxCluster];                  // written by the row's CTAs
     __shared__ RowSaved s_row;
-    __shared__ uint64_t s_bar;
+    __shared__ uint64_t s_bar, s_copy;
     extern __shared__ uint4 s_x[];                           // [span]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = a.splits, rank = static_cast<int>(cluster_rank());
     const long long row = cluster_id();
-    if (C > 1) expect_peers(&s_bar, C);
+    if (tid == 0) {
+        mbar_init(&s_copy, 1);
+        fence_mbar_init();
+    }
+    if (C > 1) expect_peers(&s_bar, GRAD ? C : C - 1);
+    __syncthreads();
     pdl_wait();
     const int y = a.tokens[row];
     PolicyRow pr{1.f, 0.f, 0.f, 0.f};
-    if (a.weights) pr.w = a.weights[row];
+    if ((GRAD || a.op == kPolicy) && a.weights) pr.w = a.weights[row];
     const bool bad = y < -1 || y >= a.V, dead = bad || y < 0 || pr.w == 0.f;   // the same in every CTA of the row
-    const VocabRow<SX> x(a.x, row, a.x_stride, a.V), g(a.g, row, a.g_stride, a.V);
+    const VocabRow<SX> x(a.x, row, a.x_stride, a.V);
     const int k0 = min(x.nvec, rank * a.span), cnt = min(x.nvec, k0 + a.span) - k0;
     if (dead) {
         if (rank == 0 && tid == 0) row_skipped(a, row, bad ? DSPARK_ROW_BAD_TOKEN : 0);
-        for (int k = tid; k < cnt; k += kRowThreads) store_vec<SX>(g, x.first(k0 + k), make_uint4(0, 0, 0, 0), x.a0 == g.a0);
+        if (GRAD) {
+            const VocabRow<SX> g(a.g, row, a.g_stride, a.V);
+            for (int k = tid; k < cnt; k += kRowThreads) store_vec<SX>(g, x.first(k0 + k), make_uint4(0, 0, 0, 0), x.a0 == g.a0);
+        }
         if (C > 1) cluster_wait();
         return;
     }
-    const unsigned char* const src = x.p + static_cast<long long>(x.first(k0)) * SX;   // of vector 0, which may lack some
-    for (int k = tid; k < cnt; k += kRowThreads) {
-        if ((k == 0 || k == cnt - 1) && !x.whole(k0 + k)) s_x[k] = load_vec<SX>(x, k0 + k, k0 + cnt);
-        else copy_async16(s_x + k, src + 16LL * k);
-    }
-    copy_commit();
+    if (warp == 0) fetch_piece<SX>(x, k0, k0 + cnt, s_x, &s_copy);
     float xy = 0.f;
     if (warp == 0) {
         xy = load_logit<SX>(x, y);
-        pr.old = a.old_lp[row];
-        pr.adv = a.adv[row];
-        if (a.ref_lp) pr.ref = a.ref_lp[row];
+        if (GRAD || a.op == kPolicy) {
+            pr.old = a.old_lp[row];
+            pr.adv = a.adv[row];
+            if (a.ref_lp) pr.ref = a.ref_lp[row];
+        }
     }
     const Place<SX> at(x, y);
     RunEnt<SX, ENT> run;
-    copies_here();
+    bool late = !copy_wait(&s_copy, 0);
+    if (late) bar_wait(&s_copy, 0);                          // once more: it is in flight
     // the token leaves the sum (and the gradient's loop) here
     if (at.k >= k0 && at.k < k0 + cnt && (at.k - k0) % kRowThreads == tid) patch<SX>(s_x[at.k - k0], at.lane, ninf_bits<SX>());
     {
@@ -762,27 +762,35 @@ __global__ void __launch_bounds__(kRowThreads, kFusedCtas) fused_kernel(TokArgs 
     }
     EntSum es = lanes_join<ENT, 32>(run.get(), a.c);
     if (lane == 0) s_warp[warp] = es;
-    __syncthreads();
+    late = __syncthreads_or(late);
     if (C > 1) cluster_wait();                               // the row's CTAs are there
-    bool late = false;
     if (warp == 0) {
         es = lanes_join<ENT, kRowWarps>(s_warp[lane & (kRowWarps - 1)], a.c);
         if (C > 1) {
             // the token's logit has been read: its place may be written, where the gradient takes the logits' place
-            if (lane < C) push_sum(&s_peer[rank], &s_bar, lane, es, xy);
-            late = !bar_wait(&s_bar, 0, kPeerMs);
+            const uint32_t after = (__float_as_uint(xy) & ~1u) | late;
+            if (GRAD ? lane < C : lane == 0 && rank != 0) push_sum(&s_peer[rank], &s_bar, lane, es, after);
+            if (!GRAD && rank != 0) return;
+            if (!GRAD && lane == 0) s_peer[0] = PeerSum{es, after};
+            __syncwarp();
+            late = !bar_wait(&s_bar, 0, kPeerMs) || late;
+            late = __any_sync(0xffffffffu, lane < C && (s_peer[lane & (kMaxCluster - 1)].after & 1u)) || late;
             es = peers_join<ENT>(s_peer, C, a.c);
         }
-        if (lane == 0) {
+        if (GRAD && lane == 0) {
             if (late) s_row = row_bad(DSPARK_ROW_INTERNAL).saved;
             else s_row = is_quick(es, xy, a.c) ? quick_end<ENT>(a, es, xy, QuickRow{base2(pr.old), base2(pr.ref), pr.w, pr.adv})
                                                : row_end<ENT>(a, es, xy, pr).saved;
         }
     }
-    __syncthreads();
-    const RowGrad<SX, ENT> rg(a, s_row, s_row.a, s_row.h);
-    const bool zero = s_row.f < 0.f;
-    write_grad<SX, ENT, 1>(x, g, k0, k0 + cnt, y, zero, rg, [&](int k) { return s_x[k - k0]; });
+    bool zero = false;
+    if (GRAD) {
+        __syncthreads();
+        const VocabRow<SX> g(a.g, row, a.g_stride, a.V);
+        const RowGrad<SX, ENT> rg(a, s_row, s_row.a, s_row.h);
+        zero = s_row.f < 0.f;
+        write_grad<SX, ENT, 1>(x, g, k0, k0 + cnt, y, zero, rg, [&](int k) { return s_x[k - k0]; });
+    }
     if (rank == 0 && tid == 0) {
         RowEnd o = late ? row_bad(DSPARK_ROW_INTERNAL) : row_end<ENT>(a, es, xy, pr);
         if (zero && !o.status) o = row_bad(DSPARK_ROW_NONFINITE);   // (a loss next to fp32's largest number)
@@ -968,11 +976,12 @@ int fused_split(int nvec, long long rows) {
     return best;
 }
 
-dspark_status_t launch_fused(TokArgs& a, int sx, bool entropy, const dspark_token_params_t* p, int C) {
+template <bool GRAD>
+dspark_status_t launch_kept(TokArgs& a, int sx, bool entropy, const dspark_token_params_t* p, int C) {
     a.splits = C;
     a.span = (max_vectors(p->V, sx) + C - 1) / C;
-    auto kern = sx == 2 ? (entropy ? fused_kernel<2, true> : fused_kernel<2, false>)
-                        : (entropy ? fused_kernel<4, true> : fused_kernel<4, false>);
+    auto kern = sx == 2 ? (entropy ? kept_kernel<2, true, GRAD> : kept_kernel<2, false, GRAD>)
+                        : (entropy ? kept_kernel<4, true, GRAD> : kept_kernel<4, false, GRAD>);
     const size_t smem = static_cast<size_t>(a.span) * 16;
     // beyond what a launch gets unasked; the same for every call, as another thread's may come between
     if (smem > 32 * 1024 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 16 * kFusedSpan) != cudaSuccess)
@@ -1048,7 +1057,7 @@ dspark_status_t dspark_policy_loss(const void* logits, const dspark_policy_t* po
     a.saved = reinterpret_cast<RowSaved*>(out_saved);
     const bool entropy = out_entropy || policy->entropy_coef != 0.f;
     if (out_grad)
-        if (const int C = fused_split(max_vectors(params->V, sx), params->n_rows); C > 0) return launch_fused(a, sx, entropy, params, C);
+        if (const int C = fused_split(max_vectors(params->V, sx), params->n_rows); C > 0) return launch_kept<true>(a, sx, entropy, params, C);
     const dspark_status_t st = launch_stats(a, sx, entropy, params);
     if (st != DSPARK_OK || !out_grad) return st;
     return launch_grad(a, sx, policy->entropy_coef != 0.f, params);
