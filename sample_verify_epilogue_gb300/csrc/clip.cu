@@ -1,10 +1,10 @@
 // The norm of many gradients together, and the gradients scaled to a largest norm.
 //
-// norm_kernel: every CTA takes an equal share of the list's 16 KB chunks, whatever tensors they belong to, and leaves
-// one sum of squares; scale_kernel adds the shares up in a fixed order, in every CTA, and scales.  The list travels in
+// norm_kernel: every CTA takes an equal share of the list, whatever tensors it belongs to, and leaves one sum of squares;
+// scale_kernel adds the shares up in a fixed order, in every CTA, and scales.  The list travels in
 // the launches' parameters, so that a call needs no copy to the device and can be captured as it is.
 //
-// A thread's squares of one chunk are added in fp32, the chunks' sums in pairs of floats.  Squares leave fp32's range
+// A thread's squares of a few vectors are added in fp32, those sums in pairs of floats.  Squares leave fp32's range
 // for elements beyond 2^64 or below 2^-63: a share whose sum is infinite, or next to nothing though not all of it is 0,
 // is summed again by a power of two.
 #include <algorithm>
@@ -17,9 +17,9 @@ namespace dspark {
 namespace {
 
 constexpr int kClipThreads = 256, kClipWarps = kClipThreads / 32;
-constexpr int kClipVec = 4;                                  // vectors a thread holds at a time
-constexpr int kChunk = kClipThreads * kClipVec;              // vectors of a chunk: 16 KB of the gradient
-constexpr int kClipCtas = 8;                                 // CTAs to an SM
+constexpr int kNormVec = 8, kScaleVec = 4;                   // vectors a thread has on their way
+constexpr int kNormCtas = 4, kScaleCtas = 5;                 // CTAs to an SM
+constexpr int kUnit = kClipThreads;                          // vectors that go to one CTA together
 constexpr int kMaxShares = 2048;                             // shares of a group of tensors
 constexpr int kLargeList = 1000, kSmallList = 100;           // tensors of a launch: 32,000 bytes of parameters hold 1000
 
@@ -27,7 +27,7 @@ struct ClipItem {
     const unsigned char* grad;
     unsigned char* out;
     long long numel;
-    int first;                                               // its first chunk
+    int first;                                               // its first unit
     unsigned short bf16, wide;                               // the gradient is bf16; out is fp32 all the same
 };
 
@@ -37,7 +37,7 @@ struct ClipList {
     float* norm;
     int* status;
     float max_norm;
-    int n, chunks, n_shares, write_norm;                     // of this group; of all groups (scale); the first group's launch
+    int n, units, n_shares, write_norm;                      // of this group; of all groups (scale); the first group's launch
     ClipItem item[N];
 };
 
@@ -46,14 +46,17 @@ template <int SX>
 struct Flat {
     static constexpr int VE = 16 / SX;
     const unsigned char* p;
-    long long numel;
+    long long numel, nvec;
     int a0;
     __device__ __forceinline__ Flat(const void* base, long long n)
-        : p(static_cast<const unsigned char*>(base)), numel(n), a0(static_cast<int>((reinterpret_cast<uintptr_t>(base) & 15u) / SX)) {}
+        : p(static_cast<const unsigned char*>(base)), numel(n), a0(static_cast<int>((reinterpret_cast<uintptr_t>(base) & 15u) / SX)) {
+        nvec = (a0 + n + VE - 1) / VE;
+    }
     __device__ __forceinline__ long long first(long long k) const { return k * VE - a0; }
+    __device__ __forceinline__ bool whole(long long k) const { return first(k) >= 0 && first(k) + VE <= numel; }
     __device__ __forceinline__ uint4 load(long long k) const {   // elements it lacks read as 0
         const long long i0 = first(k);
-        if (i0 >= 0 && i0 + VE <= numel) return ld_vec16(p + i0 * SX);
+        if (whole(k)) return ld_vec16(p + i0 * SX);
         uint4 w = make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int q = 0; q < VE; ++q)
@@ -63,140 +66,198 @@ struct Flat {
     }
 };
 
-// The item that chunk j belongs to.
-template <int N>
-__device__ __forceinline__ int item_of(const ClipList<N>& a, int j) {
-    int lo = 0, hi = a.n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.item[mid].first <= j) lo = mid;
+// Calls part(item, first vector, last vector) for what units [j0, j1) of the list hold of each tensor.
+template <int N, typename Part>
+__device__ __forceinline__ void for_parts(const ClipList<N>& a, Part part) {
+    int j = static_cast<int>(static_cast<long long>(a.units) * blockIdx.x / gridDim.x);
+    const int j1 = static_cast<int>(static_cast<long long>(a.units) * (blockIdx.x + 1) / gridDim.x);
+    if (j >= j1) return;
+    int i = 0, hi = a.n - 1;
+    while (i < hi) {
+        const int mid = (i + hi + 1) >> 1;
+        if (a.item[mid].first <= j) i = mid;
         else hi = mid - 1;
     }
-    return lo;
-}
-
-template <int SX>
-__device__ __forceinline__ void add_squares(const ClipItem& it, int j, float scale, TwoFloat& sum, unsigned& any) {
-    const Flat<SX> g(it.grad, it.numel);
-    uint4 v[kClipVec];
-#pragma unroll
-    for (int u = 0; u < kClipVec; ++u) v[u] = g.load(static_cast<long long>(j) * kChunk + u * kClipThreads + threadIdx.x);
-    unsigned long long acc[2] = {0ull, 0ull};
-    const unsigned long long s2 = pack2(scale, scale);
-#pragma unroll
-    for (int u = 0; u < kClipVec; ++u) {
-        any |= (v[u].x | v[u].y | v[u].z | v[u].w) & (SX == 2 ? 0x7fff7fffu : 0x7fffffffu);
-#pragma unroll
-        for (int k = 0; k < 16 / SX / 2; ++k) {
-            const unsigned long long x = mul2(pair_of<SX>(v[u], k), s2);
-            acc[k & 1] = fma2(x, x, acc[k & 1]);
-        }
+    for (; j < j1; ++i) {
+        const int next = i + 1 < a.n ? min(a.item[i + 1].first, j1) : j1;
+        part(a.item[i], static_cast<long long>(j - a.item[i].first) * kUnit, static_cast<long long>(next - a.item[i].first) * kUnit);
+        j = next;
     }
-    float lo, hi;
-    unpack2(add2(acc[0], acc[1]), lo, hi);
-    const TwoFloat d = two_sum(sum.hi, lo + hi);
-    sum = TwoFloat{d.hi, sum.lo + d.lo};
 }
 
-// Sum of the CTA's share by scale, in thread 0; *any: something in it is not 0.
-template <int N>
-__device__ __forceinline__ TwoFloat share_sum(const ClipList<N>& a, int j0, int j1, float scale, TwoFloat* s_sum, bool* any) {
+struct Squares {
     TwoFloat sum{0.f, 0.f};
-    unsigned bits = 0u;
-    if (j0 < j1) {
-        int i = item_of(a, j0);
-        for (int j = j0; j < j1; ++j) {
-            while (i + 1 < a.n && a.item[i + 1].first <= j) ++i;
-            const ClipItem& it = a.item[i];
-            if (it.bf16) add_squares<2>(it, j - it.first, scale, sum, bits);
-            else add_squares<4>(it, j - it.first, scale, sum, bits);
+    unsigned any = 0u;                                       // not 0: something is not 0
+
+    template <int SX, int U>
+    __device__ __forceinline__ void add(const uint4 (&v)[U], float scale) {
+        unsigned long long acc[2] = {0ull, 0ull};
+        const unsigned long long s2 = pack2(scale, scale);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            any |= (v[u].x | v[u].y | v[u].z | v[u].w) & (SX == 2 ? 0x7fff7fffu : 0x7fffffffu);
+#pragma unroll
+            for (int k = 0; k < 16 / SX / 2; ++k) {
+                unsigned long long x = pair_of<SX>(v[u], k);
+                if (scale != 1.f) x = mul2(x, s2);
+                acc[k & 1] = fma2(x, x, acc[k & 1]);
+            }
+        }
+        float lo, hi;
+        unpack2(add2(acc[0], acc[1]), lo, hi);
+        const TwoFloat d = two_sum(sum.hi, lo + hi);
+        sum = TwoFloat{d.hi, sum.lo + d.lo};
+    }
+    template <int SX>
+    __device__ __forceinline__ void add_part(const ClipItem& it, long long b, long long e, float scale) {
+        const Flat<SX> g(it.grad, it.numel);
+        e = min(e, g.nvec);
+        // whole vectors go straight through
+        const long long w0 = b + (b < e && !g.whole(b)), w1 = e - (e > w0 && !g.whole(e - 1));
+        const unsigned char* p = g.p + g.first(w0 + threadIdx.x) * SX;
+        const int n = static_cast<int>(w1 - w0);             // a CTA's share of fewer than 2^31 units
+        int k = threadIdx.x;
+        for (; k + (kNormVec - 1) * kClipThreads < n; k += kNormVec * kClipThreads, p += 16 * kNormVec * kClipThreads) {
+            uint4 v[kNormVec];
+#pragma unroll
+            for (int u = 0; u < kNormVec; ++u) v[u] = ld_vec16(p + 16 * u * kClipThreads);
+            add<SX>(v, scale);
+        }
+        for (; k < n; k += kClipThreads, p += 16 * kClipThreads) {
+            const uint4 v[1] = {ld_vec16(p)};
+            add<SX>(v, scale);
+        }
+        if (threadIdx.x < 2) {                               // the ragged ends
+            if (threadIdx.x ? w1 < e : b < w0) {
+                const uint4 v[1] = {g.load(threadIdx.x ? w1 : b)};
+                add<SX>(v, scale);
+            }
         }
     }
-    auto join = [&](const TwoFloat& o) {
+    __device__ __forceinline__ void join(const TwoFloat& o) {
         const TwoFloat d = two_sum(sum.hi, o.hi);
         sum = TwoFloat{d.hi, d.lo + (sum.lo + o.lo)};
-    };
+    }
+};
+
+// Sum of the CTA's share by scale, in every thread; *any: something in it is not 0.
+template <int N>
+__device__ __forceinline__ TwoFloat share_sum(const ClipList<N>& a, float scale, TwoFloat* s_sum, bool* any) {
+    Squares q;
+    for_parts(a, [&](const ClipItem& it, long long b, long long e) {
+        if (it.bf16) q.add_part<2>(it, b, e, scale);
+        else q.add_part<4>(it, b, e, scale);
+    });
 #pragma unroll
-    for (int o = 16; o; o >>= 1) join(TwoFloat{__shfl_xor_sync(0xffffffffu, sum.hi, o), __shfl_xor_sync(0xffffffffu, sum.lo, o)});
-    if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = sum;
-    *any = __syncthreads_or(bits != 0u);
-    sum = s_sum[0];
-    for (int w = 1; w < kClipWarps; ++w) join(s_sum[w]);
+    for (int o = 16; o; o >>= 1)
+        q.join(TwoFloat{__shfl_xor_sync(0xffffffffu, q.sum.hi, o), __shfl_xor_sync(0xffffffffu, q.sum.lo, o)});
+    if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = q.sum;
+    *any = __syncthreads_or(q.any != 0u);
+    q.sum = s_sum[0];
+    for (int w = 1; w < kClipWarps; ++w) q.join(s_sum[w]);
     __syncthreads();
-    return sum;
+    return q.sum;
 }
 
 template <int N>
-__global__ void __launch_bounds__(kClipThreads, kClipCtas) norm_kernel(const __grid_constant__ ClipList<N> a) {
+__global__ void __launch_bounds__(kClipThreads, kNormCtas) norm_kernel(const __grid_constant__ ClipList<N> a) {
     __shared__ TwoFloat s_sum[kClipWarps];
     pdl_wait();
-    const int j0 = static_cast<int>(static_cast<long long>(a.chunks) * blockIdx.x / gridDim.x);
-    const int j1 = static_cast<int>(static_cast<long long>(a.chunks) * (blockIdx.x + 1) / gridDim.x);
-    bool any;
-    TwoFloat sum = share_sum(a, j0, j1, 1.f, s_sum, &any);
-    double scale = 1.0;
-    if (!(sum.hi < INFINITY)) {                              // the same in every thread
-        sum = share_sum(a, j0, j1, 0x1p-90f, s_sum, &any);
-        scale = 0x1p180;
-    } else if (any && sum.hi < 0x1p-90f) {
-        sum = share_sum(a, j0, j1, 0x1p80f, s_sum, &any);
-        scale = 0x1p-160;
+    TwoFloat sum{0.f, 0.f};
+    double back = 1.0;
+    float scale = 1.f;
+#pragma unroll 1
+    for (;;) {
+        bool any;
+        sum = share_sum(a, scale, s_sum, &any);              // the same in every thread
+        if (scale != 1.f) break;
+        if (!(sum.hi < INFINITY)) {
+            scale = 0x1p-90f;
+            back = 0x1p180;
+        } else if (any && sum.hi < 0x1p-90f) {
+            scale = 0x1p80f;
+            back = 0x1p-160;
+        } else {
+            break;
+        }
     }
-    if (threadIdx.x == 0) a.shares[blockIdx.x] = (static_cast<double>(sum.hi) + static_cast<double>(sum.hi < INFINITY ? sum.lo : 0.f)) * scale;
+    if (threadIdx.x == 0) a.shares[blockIdx.x] = (static_cast<double>(sum.hi) + static_cast<double>(sum.hi < INFINITY ? sum.lo : 0.f)) * back;
 }
 
-template <int SX>
-__device__ __forceinline__ void scale_chunk(const ClipItem& it, int j, float c) {
+// sqrt(sum) by a float and a step of Newton's (a thread's 64-bit root and quotient take 2 us): relative 2^-24
+__device__ __forceinline__ float norm_of(double sum) {
+    if (!(sum > 0.0 && sum < static_cast<double>(INFINITY))) return static_cast<float>(sum);
+    const int e = (((__double2hiint(sum) >> 20) & 0x7ff) - 1023) & ~1;
+    const double m = sum * __hiloint2double((1023 - e) << 20, 0);   // in [1, 4)
+    const float hi = static_cast<float>(m), lo = static_cast<float>(m - static_cast<double>(hi)), r = sqrtf(hi);
+    return ldexpf(fmaf(0.5f / r, fmaf(-r, r, hi) + lo, r), e / 2);
+}
+
+__device__ __forceinline__ void st_vec32(void* p, const float (&f)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :: "l"(p), "r"(__float_as_uint(f[0])), "r"(__float_as_uint(f[1])), "r"(__float_as_uint(f[2])), "r"(__float_as_uint(f[3])),
+                    "r"(__float_as_uint(f[4])), "r"(__float_as_uint(f[5])), "r"(__float_as_uint(f[6])), "r"(__float_as_uint(f[7])) : "memory");
+}
+
+template <int SX, bool WIDE>
+__device__ __forceinline__ void scale_one(const Flat<SX>& g, unsigned char* out, long long k, const uint4& v, float c, bool alike) {
     constexpr int VE = 16 / SX;
-    const Flat<SX> g(it.grad, it.numel);
-    const long long k0 = static_cast<long long>(j) * kChunk + threadIdx.x;
-    uint4 v[kClipVec];
+    const long long i0 = g.first(k);
+    float f[VE];
+    uint4 w = v;                                             // c = 1: as they are (a NaN keeps its bits)
+    if (c == 1.f) {
 #pragma unroll
-    for (int u = 0; u < kClipVec; ++u) v[u] = g.load(k0 + u * kClipThreads);
-    const bool wide = SX == 2 && it.wide;
-    // the output's vectors lie as the gradient's do
-    const bool alike = ((reinterpret_cast<uintptr_t>(it.out) - static_cast<uintptr_t>(g.a0) * (wide ? 4 : SX)) & 15u) == 0;
-    const unsigned long long c2 = pack2(c, c);
+        for (int q = 0; q < VE; ++q) f[q] = elem<SX>(v, q);
+    } else {
+        const unsigned long long c2 = pack2(c, c);
 #pragma unroll
-    for (int u = 0; u < kClipVec; ++u) {
-        const long long i0 = g.first(k0 + u * kClipThreads);
-        if (i0 >= it.numel) break;
-        float f[VE];
-        if (c == 1.f) {                                      // as they are (a NaN keeps its bits)
+        for (int h = 0; h < VE / 2; ++h) unpack2(mul2(pair_of<SX>(v, h), c2), f[2 * h], f[2 * h + 1]);
+        if (SX == 2) w = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4 % VE], f[5 % VE]), pack_bf16(f[6 % VE], f[7 % VE]));
+        else w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+    const bool whole = alike && g.whole(k);
+    if (WIDE) {
+        float* o = reinterpret_cast<float*>(out);
+        if (whole) {
+            float f8[8];
 #pragma unroll
-            for (int q = 0; q < VE; ++q) f[q] = elem<SX>(v[u], q);
+            for (int q = 0; q < 8; ++q) f8[q] = f[q % VE];
+            st_vec32(o + i0, f8);                            // whole sectors: 16 bytes each to every other half took 427 us, not 3xx
         } else {
 #pragma unroll
-            for (int h = 0; h < VE / 2; ++h) unpack2(mul2(pair_of<SX>(v[u], h), c2), f[2 * h], f[2 * h + 1]);
-            if (SX == 2 && !wide) v[u] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4 % VE], f[5 % VE]), pack_bf16(f[6 % VE], f[7 % VE]));
-            if (SX == 4) v[u] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+            for (int q = 0; q < VE; ++q)
+                if (i0 + q >= 0 && i0 + q < g.numel) o[i0 + q] = f[q];
         }
-        const bool whole = alike && i0 >= 0 && i0 + VE <= it.numel;
-        if (wide) {
-            float* o = reinterpret_cast<float*>(it.out);
-            if (whole) {
-                st_vec16(o + i0, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
-                st_vec16(o + i0 + 4, make_uint4(__float_as_uint(f[4 % VE]), __float_as_uint(f[5 % VE]), __float_as_uint(f[6 % VE]), __float_as_uint(f[7 % VE])));
-            } else {
+    } else if (whole) {
+        st_vec16(out + i0 * SX, w);
+    } else {
 #pragma unroll
-                for (int q = 0; q < VE; ++q)
-                    if (i0 + q >= 0 && i0 + q < it.numel) o[i0 + q] = f[q];
-            }
-        } else if (whole) {
-            st_vec16(it.out + i0 * SX, v[u]);
-        } else {
-#pragma unroll
-            for (int q = 0; q < VE; ++q) {
-                if (i0 + q < 0 || i0 + q >= it.numel) continue;
-                if (SX == 2) reinterpret_cast<unsigned short*>(it.out)[i0 + q] = static_cast<unsigned short>(word_of(v[u], q >> 1) >> (16 * (q & 1)));
-                else reinterpret_cast<unsigned*>(it.out)[i0 + q] = word_of(v[u], q);
-            }
+        for (int q = 0; q < VE; ++q) {
+            if (i0 + q < 0 || i0 + q >= g.numel) continue;
+            if (SX == 2) reinterpret_cast<unsigned short*>(out)[i0 + q] = static_cast<unsigned short>(word_of(w, q >> 1) >> (16 * (q & 1)));
+            else reinterpret_cast<unsigned*>(out)[i0 + q] = word_of(w, q);
         }
     }
+}
+template <int SX, bool WIDE>
+__device__ __forceinline__ void scale_part(const ClipItem& it, long long b, long long e, float c) {
+    const Flat<SX> g(it.grad, it.numel);
+    e = min(e, g.nvec);
+    // the output's vectors lie as the gradient's do
+    const bool alike = ((reinterpret_cast<uintptr_t>(it.out) - static_cast<uintptr_t>(g.a0) * (WIDE ? 4 : SX)) & (WIDE ? 31u : 15u)) == 0;
+    long long k = b + threadIdx.x;
+    for (; k + (kScaleVec - 1) * kClipThreads < e; k += kScaleVec * kClipThreads) {
+        uint4 v[kScaleVec];
+#pragma unroll
+        for (int u = 0; u < kScaleVec; ++u) v[u] = g.load(k + u * kClipThreads);
+#pragma unroll
+        for (int u = 0; u < kScaleVec; ++u) scale_one<SX, WIDE>(g, it.out, k + u * kClipThreads, v[u], c, alike);
+    }
+    for (; k < e; k += kClipThreads) scale_one<SX, WIDE>(g, it.out, k, g.load(k), c, alike);
 }
 
 template <int N>
-__global__ void __launch_bounds__(kClipThreads, kClipCtas) scale_kernel(const __grid_constant__ ClipList<N> a) {
+__global__ void __launch_bounds__(kClipThreads, kScaleCtas) scale_kernel(const __grid_constant__ ClipList<N> a) {
     __shared__ double s_part[kClipWarps];
     __shared__ float s_c;
     const int tid = threadIdx.x;
@@ -208,10 +269,9 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtas) scale_kernel(const __
     __syncthreads();
     if (tid == 0) {
         for (int w = 1; w < kClipWarps; ++w) sum += s_part[w];
-        const double n = sqrt(sum);
-        const float norm = static_cast<float>(n);
+        const float norm = norm_of(sum);
         const bool finite = norm < INFINITY;
-        s_c = finite && n > static_cast<double>(a.max_norm) ? static_cast<float>(static_cast<double>(a.max_norm) / n) : 1.f;
+        s_c = finite && norm > a.max_norm ? a.max_norm / norm : 1.f;
         if (a.write_norm && blockIdx.x == 0) {
             *a.norm = norm;
             *a.status = finite ? 0 : DSPARK_ROW_NONFINITE;
@@ -219,17 +279,12 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtas) scale_kernel(const __
     }
     __syncthreads();
     const float c = s_c;
-    const int j0 = static_cast<int>(static_cast<long long>(a.chunks) * blockIdx.x / gridDim.x);
-    const int j1 = static_cast<int>(static_cast<long long>(a.chunks) * (blockIdx.x + 1) / gridDim.x);
-    if (j0 >= j1) return;
-    int i = item_of(a, j0);
-    for (int j = j0; j < j1; ++j) {
-        while (i + 1 < a.n && a.item[i + 1].first <= j) ++i;
-        const ClipItem& it = a.item[i];
-        if (c == 1.f && it.out == it.grad) continue;
-        if (it.bf16) scale_chunk<2>(it, j - it.first, c);
-        else scale_chunk<4>(it, j - it.first, c);
-    }
+    for_parts(a, [&](const ClipItem& it, long long b, long long e) {
+        if (c == 1.f && it.out == it.grad) return;
+        if (!it.bf16) scale_part<4, false>(it, b, e, c);
+        else if (it.wide) scale_part<2, true>(it, b, e, c);
+        else scale_part<2, false>(it, b, e, c);
+    });
 }
 
 int groups_of(int n) { return (n + kLargeList - 1) / kLargeList; }
@@ -240,7 +295,7 @@ dspark_status_t check_list(const dspark_grad_t* grads, int n) {
         if (g.numel < 0 || (g.dtype != DSPARK_BF16 && g.dtype != DSPARK_FP32)) return DSPARK_ERR_INVALID_ARG;
         if (g.out_dtype != g.dtype && g.out_dtype != DSPARK_FP32) return DSPARK_ERR_INVALID_ARG;
         if (g.numel == 0) continue;
-        if (g.numel > (1LL << 43)) return DSPARK_ERR_UNSUPPORTED;   // 2^31 chunks of an fp32 list
+        if (g.numel > (1LL << 43)) return DSPARK_ERR_UNSUPPORTED;   // 2^31 units of an fp32 list
         const size_t sx = g.dtype == DSPARK_BF16 ? 2 : 4, so = g.out_dtype == DSPARK_BF16 ? 2 : 4;
         if (!g.grad || !g.out || reinterpret_cast<uintptr_t>(g.grad) % sx || reinterpret_cast<uintptr_t>(g.out) % so)
             return DSPARK_ERR_INVALID_ARG;
@@ -249,10 +304,10 @@ dspark_status_t check_list(const dspark_grad_t* grads, int n) {
     return DSPARK_OK;
 }
 
-// Fill the list with the group's tensors; false when it has too many chunks.
+// Fill the list with the group's tensors; false when it has too many units.
 template <int N>
 bool fill(ClipList<N>& a, const dspark_grad_t* grads, int n) {
-    long long chunks = 0;
+    long long units = 0;
     a.n = 0;
     for (int i = 0; i < n; ++i) {
         const dspark_grad_t& g = grads[i];
@@ -261,16 +316,16 @@ bool fill(ClipList<N>& a, const dspark_grad_t* grads, int n) {
         const long long a0 = static_cast<long long>(reinterpret_cast<uintptr_t>(g.grad) & 15u) / sx;
         const long long nvec = (a0 + g.numel + 16 / sx - 1) / (16 / sx);
         a.item[a.n++] = ClipItem{static_cast<const unsigned char*>(g.grad), static_cast<unsigned char*>(g.out), g.numel,
-                                 static_cast<int>(chunks), g.dtype == DSPARK_BF16, g.out_dtype != g.dtype};
-        chunks += (nvec + kChunk - 1) / kChunk;
-        if (chunks > 0x7fffffffLL) return false;
+                                 static_cast<int>(units), g.dtype == DSPARK_BF16, g.out_dtype != g.dtype};
+        units += (nvec + kUnit - 1) / kUnit;
+        if (units > 0x7fffffffLL) return false;
     }
-    a.chunks = static_cast<int>(chunks);
+    a.units = static_cast<int>(units);
     return true;
 }
 
 template <int N>
-dspark_status_t clip(const dspark_grad_t* grads, int n, float max_norm, float* norm, int* status, double* shares, int most, cudaStream_t s) {
+dspark_status_t clip(const dspark_grad_t* grads, int n, float max_norm, float* norm, int* status, double* shares, int sms, cudaStream_t s) {
     ClipList<N> a;
     a.max_norm = max_norm;
     a.norm = norm;
@@ -281,17 +336,17 @@ dspark_status_t clip(const dspark_grad_t* grads, int n, float max_norm, float* n
         int done = 0;
         for (int k = 0; k < groups; ++k) {
             if (!fill(a, grads + k * kLargeList, std::min(kLargeList, n - k * kLargeList))) return DSPARK_ERR_UNSUPPORTED;
-            const int grid = std::max(1, std::min(a.chunks, most));
+            const int grid = std::max(1, std::min({a.units, kMaxShares, sms * (pass == 0 ? kNormCtas : kScaleCtas)}));
             a.shares = pass == 0 ? shares + done : shares;
             a.n_shares = total;
             a.write_norm = k == 0;
-            done += grid;
-            const bool skip = pass == 1 && k > 0 && a.chunks == 0;
+            if (pass == 0) done += grid;
+            const bool skip = pass == 1 && k > 0 && a.units == 0;
             if (!skip && launch_k(pass == 0 ? norm_kernel<N> : scale_kernel<N>, dim3(static_cast<unsigned>(grid)), dim3(kClipThreads), 0, s,
                                   true, a) != cudaSuccess)
                 return DSPARK_ERR_CUDA;
         }
-        total = done;
+        if (pass == 0) total = done;
     }
     return DSPARK_OK;
 }
@@ -316,11 +371,10 @@ dspark_status_t dspark_clip_grads(const dspark_grad_t* grads, int32_t n_grads, f
         return DSPARK_ERR_WORKSPACE;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return DSPARK_ERR_CUDA;
-    const int most = std::min(kMaxShares, sms * kClipCtas);
     double* const shares = static_cast<double*>(workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return n_grads <= kSmallList ? clip<kSmallList>(grads, n_grads, max_norm, out_norm, out_status, shares, most, s)
-                                 : clip<kLargeList>(grads, n_grads, max_norm, out_norm, out_status, shares, most, s);
+    return n_grads <= kSmallList ? clip<kSmallList>(grads, n_grads, max_norm, out_norm, out_status, shares, sms, s)
+                                 : clip<kLargeList>(grads, n_grads, max_norm, out_norm, out_status, shares, sms, s);
 }
 
 }  // extern "C"
