@@ -400,9 +400,9 @@ __device__ __forceinline__ EntSum peers_join(const PeerSum* s, int C, float c) {
 }
 
 constexpr int kStatsVec = 4;                                 // vectors a thread has on their way
-template <int SX, bool ENT>
-__global__ void __launch_bounds__(kRowThreads, 5) stats_kernel(TokArgs a) {
-    __shared__ EntSum s_warp[kRowWarps];
+template <int SX, bool ENT, int NT>
+__global__ void __launch_bounds__(NT, NT == 256 ? 6 : 3) stats_kernel(TokArgs a) {
+    __shared__ EntSum s_warp[(NT / 32)];
     __shared__ PeerSum s_peer[kMaxCluster];                  // (in the row's first CTA) written by the cluster's
     __shared__ uint64_t s_bar;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -434,22 +434,22 @@ __global__ void __launch_bounds__(kRowThreads, 5) stats_kernel(TokArgs a) {
     // whole vectors [w0, w1) go straight through; the token's is its owner's business
     const int w0 = k0 + (k0 < k1 && !x.whole(k0)), w1 = k1 - (k1 > w0 && !x.whole(k1 - 1));
     const Place<SX> at(x, y);
-    const int own = (at.k - w0) % kRowThreads == tid ? at.k : -1;
+    const int own = (at.k - w0) % NT == tid ? at.k : -1;
     RunEnt<SX, ENT> run;
     int k = w0 + tid;
     const uint4* p = reinterpret_cast<const uint4*>(x.p + static_cast<long long>(x.first(k)) * SX);
-    for (; k + (kStatsVec - 1) * kRowThreads < w1; k += kStatsVec * kRowThreads, p += kStatsVec * kRowThreads) {
+    for (; k + (kStatsVec - 1) * NT < w1; k += kStatsVec * NT, p += kStatsVec * NT) {
         uint4 v[kStatsVec];
 #pragma unroll
-        for (int u = 0; u < kStatsVec; ++u) v[u] = ld_vec16(p + u * kRowThreads);
-        if (own >= k && own < k + kStatsVec * kRowThreads) {
+        for (int u = 0; u < kStatsVec; ++u) v[u] = ld_vec16(p + u * NT);
+        if (own >= k && own < k + kStatsVec * NT) {
 #pragma unroll
             for (int u = 0; u < kStatsVec; ++u)
-                if (k + u * kRowThreads == own) patch<SX>(v[u], at.lane, ninf_bits<SX>());
+                if (k + u * NT == own) patch<SX>(v[u], at.lane, ninf_bits<SX>());
         }
         run.add(v, a);
     }
-    for (; k < w1; k += kRowThreads, p += kRowThreads) {
+    for (; k < w1; k += NT, p += NT) {
         uint4 v[1] = {ld_vec16(p)};
         if (k == own) patch<SX>(v[0], at.lane, ninf_bits<SX>());
         run.add(v, a);
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kRowThreads, 5) stats_kernel(TokArgs a) {
     __syncthreads();
     if (C > 1) cluster_wait();
     if (warp != 0) return;
-    es = lanes_join<ENT, kRowWarps>(s_warp[lane & (kRowWarps - 1)], a.c);
+    es = lanes_join<ENT, (NT / 32)>(s_warp[lane & ((NT / 32) - 1)], a.c);
     bool late = false;
     if (C > 1) {
         if (rank != 0) {                                     // to the row's first CTA, which is there and waits
@@ -933,18 +933,28 @@ dspark_status_t token_args(const void* logits, const dspark_token_params_t* p, c
 
 bool misplaced(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 
+// A row is a CTA's work where there are rows enough; an SM holds six CTAs of 256 threads (five: 2% less for 4096 rows of
+// 151936, 5 to 20% more where that leaves a few rows to a second wave: 900 of them 58 us, 46 with six) or three of
+// 512, which have a row done in half the time: as many rows as they are in one wave are theirs (400 rows of 151936: 23 us,
+// 27 by 256; 509 of 50001 fp32: 22 and 20).  Fewer still are split over clusters (9 rows of 151936 in 1, 2, 4, 8 CTAs of
+// 256: 11.4, 7.9, 5.8, 4.5 us; 8 of 512: 3.9; short rows lose by it: 100 of 32000 4.1 us whole, 4.9 in halves).
 dspark_status_t launch_stats(TokArgs& a, int sx, bool entropy, const dspark_token_params_t* p) {
     const int nvec = max_vectors(p->V, sx);
+    const long long rows = p->n_rows;
+    const bool wide = rows <= 456 && nvec >= 4096;
     int C = 1;
     a.log_c = 0;
-    while (C < kMaxCluster && nvec >= C * 512 && static_cast<long long>(p->n_rows) * 2 * C <= 640) {
+    while (C < kMaxCluster && nvec >= C * 4096 && rows * 2 * C <= (wide ? 456 : 640)) {
         C *= 2;
         ++a.log_c;
     }
-    auto kern = sx == 2 ? (entropy ? stats_kernel<2, true> : stats_kernel<2, false>)
-                        : (entropy ? stats_kernel<4, true> : stats_kernel<4, false>);
-    const cudaError_t e = launch_cluster(kern, static_cast<unsigned>(p->n_rows) * C, kRowThreads, C, 0,
-                                         static_cast<cudaStream_t>(p->stream), a);
+    const unsigned grid = static_cast<unsigned>(p->n_rows) * C;
+    const cudaStream_t s = static_cast<cudaStream_t>(p->stream);
+    auto narrow_kern = sx == 2 ? (entropy ? stats_kernel<2, true, 256> : stats_kernel<2, false, 256>)
+                               : (entropy ? stats_kernel<4, true, 256> : stats_kernel<4, false, 256>);
+    auto wide_kern = sx == 2 ? (entropy ? stats_kernel<2, true, 512> : stats_kernel<2, false, 512>)
+                             : (entropy ? stats_kernel<4, true, 512> : stats_kernel<4, false, 512>);
+    const cudaError_t e = wide ? launch_cluster(wide_kern, grid, 512, C, 0, s, a) : launch_cluster(narrow_kern, grid, 256, C, 0, s, a);
     return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
