@@ -8,7 +8,8 @@ Each round, for B requests and K drafted tokens:
      position;
   3. dspark_verify_sample accepts drafts and draws the next token;
   4. dspark_top_logits records the target's largest logits at the verified positions;
-  5. the drafter takes a step on the distillation loss of that record.
+  5. the drafter takes a step on the distillation loss of that record, its gradient clipped by
+     dspark_clip_grads.
 
 The "models" are one linear head each over given hidden states: there is no network to load.
 
@@ -27,6 +28,7 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 from sample_verify_epilogue_gb300 import binding  # noqa: E402
 from sample_verify_epilogue_gb300.distill import distill_loss  # noqa: E402
+from sample_verify_epilogue_gb300.training import clip_grads_  # noqa: E402
 
 
 def run(rounds=30, B=32, K=4, V=32000, draft_V=8000, hidden=16, n=64, seed=0, say=print):
@@ -97,6 +99,7 @@ def run(rounds=30, B=32, K=4, V=32000, draft_V=8000, hidden=16, n=64, seed=0, sa
         loss, _ = distill_loss(student, *record, t2d=t2d)
         optimizer.zero_grad()
         loss.mean().backward()
+        clip_grads_([head], 1.0)
         optimizer.step()
 
         losses.append(float(loss.detach().mean()))

@@ -66,7 +66,7 @@ struct TokArgs {
 };
 
 // A sum of exponentials e by ExpRef(m), and the sum w of e times its exponent (base 2).  m is a logit of about the
-// largest ones' size; no e is larger than 2^16.
+// largest ones' size; no e is larger than 64.
 struct EntSum {
     float m, sum, w;
 };
@@ -103,8 +103,9 @@ __device__ __forceinline__ EntSum lanes_join(EntSum a, float c) {
 
 // A thread's sum while it streams.
 //
-// Vectors are added by the reference that is there, whatever their maximum: where that makes a sum of 2^16 or more (the
-// first vectors, a maximum far above those before) they are added again by the maximum of both.  The reference's whole
+// Vectors are added by the reference that is there, whatever their maximum: where that makes a sum of 64 or more (the
+// first vectors, a maximum far above those before) they are added again by the maximum of both.  (64: an entropy is a
+// difference of what the exponents weigh and the sum's logarithm, which should not be far from 0 themselves.)  The reference's whole
 // exponent r makes the exponent's one rounding that of the fma; -inf stands for none.
 //
 // A row's log-probability may be off by 1e-7 at random, but not to one side: sums of a thousand log ratios follow.  So
@@ -129,10 +130,22 @@ struct RunEnt {
         w = was.w;
     }
 
+    // Before the first vectors, by a whole warp: the largest of them all is a reference that hardly ever has to be raised
+    // (a thread's own: policy_batch 389 -> 435 us).
+    template <int U>
+    __device__ __forceinline__ void seed(const uint4 (&v)[U], const TokArgs& a) {
+        const float to = key_to_f(__reduce_max_sync(0xffffffffu, fkey(vecs_max<SX>(v))));
+        const ExpRef ref(to, a.c);
+        if (!ref.whole) return;
+        m = to;
+        r = ref.r;
+        if (ENT && SX == 2) least = least_pair(ref, a.inv_c);
+    }
+
     template <int U>
     __device__ __forceinline__ void add(uint4 (&v)[U], const TokArgs& a) {
         float ws, s = sum_of(v, a, ws);
-        if (!(s < 65536.f)) {
+        if (!(s < 64.f)) {
             // (a zero that the compiler does not know: else it keeps the first sum's conversions for the second, in registers
             // that are not there)
 #pragma unroll
@@ -274,7 +287,7 @@ struct Odds {
 
 // From a row's sum over the other tokens and its token's logit, by one thread: on the way between the sum and the gradient,
 // so its steps are few and share what they can (1400 cycles in a first form: 45 of 500 us of policy_batch's rows).
-template <bool ENT>
+template <int SX, bool ENT>
 __device__ __forceinline__ RowEnd row_end(const TokArgs& a, const EntSum& es, float xy, const PolicyRow& pr) {
     RowEnd o{RowSaved{0.f, -1.f, 0.f, 0.f, 0.f, 0.f, 0.f, -1}, NAN, NAN, NAN, NAN, DSPARK_ROW_NONFINITE};
     const bool none = !(es.m > -INFINITY) && es.sum == es.sum;   // no other token has any mass
@@ -282,24 +295,24 @@ __device__ __forceinline__ RowEnd row_end(const TokArgs& a, const EntSum& es, fl
     o.status = 0;
     RowSaved& s = o.saved;
     TwoFloat d{-INFINITY, 0.f}, lr{0.f, 0.f};
-    float mean = 0.f;                                        // of the others' exponents
+    float mean = 0.f, by_low = 0.f;                          // of the others' exponents; what c_low adds to log R
     if (!none) {
         const ExpRef ref(es.m, a.c);
         lr = log_two(es.sum);
         lr.lo += kEx2Lacks;
         if (ENT) {
             mean = es.w / es.sum;
-            if (ref.whole) lr.lo = fmaf(a.c_low * a.inv_c * kLn2, mean + ref.r, lr.lo);
+            if (ref.whole) by_low = a.c_low * a.inv_c * kLn2 * (mean + ref.r);
         }
         if (!(xy > -INFINITY)) {
             d.hi = INFINITY;
         } else if (ref.whole) {
             const TwoFloat p = two_prod(xy, a.c), by = two_sum(ref.r, -p.hi);
-            d = fabsf(p.hi) < INFINITY ? TwoFloat{by.hi, by.lo - fmaf(xy, a.c_low, p.lo)} * ln2_two() + lr
-                                       : TwoFloat{xy > 0.f ? -INFINITY : INFINITY, 0.f};
+            d = fabsf(p.hi) < INFINITY ? TwoFloat{by.hi, by.lo - fmaf(xy, a.c_low, p.lo)} * ln2_two() + TwoFloat{lr.hi, lr.lo + by_low}
+                                       : TwoFloat{fmaf(-xy, a.inv_t, ref.r * kLn2), 0.f};   // the types' lowest values
         } else {
-            const float by = (es.m - xy) * a.c;
-            d = fabsf(by) < INFINITY ? TwoFloat{by, 0.f} * ln2_two() + lr : TwoFloat{by, 0.f};
+            const float by = (es.m - xy) * a.inv_t;
+            d = fabsf(by) < INFINITY ? TwoFloat{by, 0.f} + lr : TwoFloat{by, 0.f};
         }
         s.m = es.m;
     }
@@ -307,8 +320,10 @@ __device__ __forceinline__ RowEnd row_end(const TokArgs& a, const EntSum& es, fl
     const TwoFloat lp = -k.sp;
     float H = 0.f;
     if (ENT) H = (k.p > 0.f ? k.p * k.sp.hi : 0.f) + (none || k.q == 0.f ? 0.f : k.q * (k.sm + fmaf(-kLn2, mean, lr.hi + lr.lo)));
-    s.f = none ? 0.f : k.q / es.sum * a.inv_t;
-    s.level = none || !(k.sm < INFINITY) ? 0.f : H - lr.hi - k.sm;
+    // (the gradient of fp32 takes c_low into its exponents, that of bf16 does not; H, a difference of two that have it or
+    // have it not, is the same)
+    s.f = none ? 0.f : k.q / es.sum * a.inv_t * (SX == 4 ? 1.f - by_low : 1.f);
+    s.level = none || !(k.sm < INFINITY) ? 0.f : H - (SX == 4 ? lr.hi + by_low : lr.hi) - k.sm;
     s.q = k.q * a.inv_t;
     s.py = k.p > 0.f ? k.p * (lp.hi + H) * a.inv_t : 0.f;
     o.logp = lp.hi + lp.lo;
@@ -447,6 +462,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 3) stats_kernel(TokArgs a)
             for (int u = 0; u < kStatsVec; ++u)
                 if (k + u * NT == own) patch<SX>(v[u], at.lane, ninf_bits<SX>());
         }
+        if (k == w0 + tid && w0 + (tid | 31) + (kStatsVec - 1) * NT < w1) run.seed(v, a);
         run.add(v, a);
     }
     for (; k < w1; k += NT, p += NT) {
@@ -479,7 +495,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 3) stats_kernel(TokArgs a)
         late = !bar_wait(&s_bar, 0, kPeerMs);
         es = peers_join<ENT>(s_peer, C, a.c);
     }
-    if (lane == 0) row_write(a, row, late ? row_bad(DSPARK_ROW_INTERNAL) : row_end<ENT>(a, es, xy, pr), ENT);
+    if (lane == 0) row_write(a, row, late ? row_bad(DSPARK_ROW_INTERNAL) : row_end<SX, ENT>(a, es, xy, pr), ENT);
 }
 
 template <int SX>
@@ -650,15 +666,15 @@ __device__ __forceinline__ float rcp_approx(float x) {
 __device__ __forceinline__ bool is_quick(const EntSum& es, float xy, float c) {
     return fabsf(es.m * c) < 4194304.f && es.sum > 0x1p-60f && es.sum < 0x1p60f && fabsf(xy * c) < 4194304.f;
 }
-template <bool ENT>
+template <int SX, bool ENT>
 __device__ __forceinline__ RowSaved quick_end(const TokArgs& a, const EntSum& es, float xy, const QuickRow& pr) {
     RowSaved s{es.m, -1.f, 0.f, 0.f, 0.f, 0.f, 0.f, -1};
     const float r = ceilf(es.m * a.c), by_sum = rcp_approx(es.sum), mean = ENT ? es.w * by_sum : 0.f;
     const int e = (__float_as_int(es.sum) - 0x3F400000) >> 23;
-    float l = lg2_approx(__int_as_float(__float_as_int(es.sum) - (e << 23))) + kEx2Lacks * kLog2E;
-    if (ENT) l = fmaf(a.c_low * a.inv_c, mean + r, l);
+    const float l = lg2_approx(__int_as_float(__float_as_int(es.sum) - (e << 23))) + kEx2Lacks * kLog2E;
+    const float by_low = ENT ? a.c_low * a.inv_c * (mean + r) : 0.f;
     const TwoFloat p = two_prod(xy, a.c), top = two_sum(r + static_cast<float>(e), -p.hi);
-    const float rest = top.lo + (l - fmaf(xy, a.c_low, p.lo)), d = top.hi + rest;   // log2 of R / e^s_y
+    const float rest = top.lo + (l + by_low - fmaf(xy, a.c_low, p.lo)), d = top.hi + rest;   // log2 of R / e^s_y
     const float t = ex2_approx(-fabsf(d)), u = 1.f + t, inv = rcp_approx(u), small = t * inv;
     const bool up = d > 0.f;
     const float q = up ? inv : small, py = up ? small : inv;
@@ -669,7 +685,7 @@ __device__ __forceinline__ RowSaved quick_end(const TokArgs& a, const EntSum& es
     if (ENT) {
         const float sm = kLn2 * (up ? lu : lu - d), lr = kLn2 * (static_cast<float>(e) + l);
         H = fmaf(q, sm + fmaf(-kLn2, mean, lr), -py * kLn2 * (lp.hi + lp.lo));
-        s.level = H - lr - sm;
+        s.level = H - (SX == 4 ? fmaf(kLn2, by_low, lr) : lr) - sm;
         s.py = py * fmaf(kLn2, lp.hi + lp.lo, H) * a.inv_t;
     }
     s.q = q * a.inv_t;
@@ -689,7 +705,7 @@ __device__ __forceinline__ RowSaved quick_end(const TokArgs& a, const EntSum& es
     }
     s.a = pr.w * by_lp;
     s.h = -pr.w * a.ent_coef;
-    if (fabsf(loss * pr.w) < INFINITY && fabsf(s.a) < INFINITY) s.f = q * by_sum * a.inv_t;
+    if (fabsf(loss * pr.w) < INFINITY && fabsf(s.a) < INFINITY) s.f = q * by_sum * a.inv_t * (SX == 4 ? 1.f - kLn2 * by_low : 1.f);
     return s;
 }
 
@@ -753,6 +769,7 @@ __global__ void __launch_bounds__(kRowThreads, kFusedCtas) kept_kernel(TokArgs a
             uint4 v[kTokVec];
 #pragma unroll
             for (int u = 0; u < kTokVec; ++u) v[u] = s_x[k + u * kRowThreads];
+            if (k == tid && (tid | 31) + (kTokVec - 1) * kRowThreads < cnt) run.seed(v, a);
             run.add(v, a);
         }
         for (; k < cnt; k += kRowThreads) {
@@ -779,8 +796,8 @@ __global__ void __launch_bounds__(kRowThreads, kFusedCtas) kept_kernel(TokArgs a
         }
         if (GRAD && lane == 0) {
             if (late) s_row = row_bad(DSPARK_ROW_INTERNAL).saved;
-            else s_row = is_quick(es, xy, a.c) ? quick_end<ENT>(a, es, xy, QuickRow{base2(pr.old), base2(pr.ref), pr.w, pr.adv})
-                                               : row_end<ENT>(a, es, xy, pr).saved;
+            else s_row = is_quick(es, xy, a.c) ? quick_end<SX, ENT>(a, es, xy, QuickRow{base2(pr.old), base2(pr.ref), pr.w, pr.adv})
+                                               : row_end<SX, ENT>(a, es, xy, pr).saved;
         }
     }
     bool zero = false;
@@ -792,7 +809,7 @@ __global__ void __launch_bounds__(kRowThreads, kFusedCtas) kept_kernel(TokArgs a
         write_grad<SX, ENT, 1>(x, g, k0, k0 + cnt, y, zero, rg, [&](int k) { return s_x[k - k0]; });
     }
     if (rank == 0 && tid == 0) {
-        RowEnd o = late ? row_bad(DSPARK_ROW_INTERNAL) : row_end<ENT>(a, es, xy, pr);
+        RowEnd o = late ? row_bad(DSPARK_ROW_INTERNAL) : row_end<SX, ENT>(a, es, xy, pr);
         if (zero && !o.status) o = row_bad(DSPARK_ROW_NONFINITE);   // (a loss next to fp32's largest number)
         row_write(a, row, o, ENT);
     }
