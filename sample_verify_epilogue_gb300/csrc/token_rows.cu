@@ -21,6 +21,7 @@ namespace dspark {
 namespace {
 
 constexpr int kTokVec = 2;                                   // vectors a thread takes at a time
+constexpr int kGradVec = 4;                                  // vectors a thread of the gradient has on their way
 constexpr int kGradVecs = 2048;                              // vectors of a row that a CTA of the gradient takes
 constexpr float kLn2 = 0.693147180559945f;
 // what the exponential unit's results lack on average, relative (2^20 arguments between whole exponents: 5.06e-8, from
@@ -65,8 +66,9 @@ struct TokArgs {
     unsigned zero;                                           // 0
 };
 
-// A sum of exponentials e by ExpRef(m), and the sum w of e times its exponent (base 2).  m is a logit of about the
-// largest ones' size; no e is larger than 64.
+// A sum of exponentials e by ExpRef(m), and the sum w of e times its exponent (base 2).  m is about the largest logits'
+// size, a power of two above those it was taken from: exponents between -1 and 1 lose their last bits in the exponential
+// unit (its results are 2e-8 larger there).  No e is larger than 64.
 struct EntSum {
     float m, sum, w;
 };
@@ -134,12 +136,39 @@ struct RunEnt {
     // (a thread's own: policy_batch 389 -> 435 us).
     template <int U>
     __device__ __forceinline__ void seed(const uint4 (&v)[U], const TokArgs& a) {
-        const float to = key_to_f(__reduce_max_sync(0xffffffffu, fkey(vecs_max<SX>(v))));
+        const float to = key_to_f(__reduce_max_sync(0xffffffffu, fkey(vecs_max<SX>(v)))) + a.inv_c;
         const ExpRef ref(to, a.c);
         if (!ref.whole) return;
         m = to;
         r = ref.r;
         if (ENT && SX == 2) least = least_pair(ref, a.inv_c);
+    }
+
+    // U vectors from shared memory, `stride` apart: read again where the reference has to be raised.
+    template <int U>
+    __device__ __forceinline__ void add_from(const uint4* p, int stride, const TokArgs& a) {
+        float ws, s;
+        {
+            uint4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = p[u * stride];
+            s = sum_of(v, a, ws);
+        }
+        if (!(s < 64.f)) {
+#pragma unroll 1
+            for (int u = 0; u < U; ++u) {
+                uint4 v[1] = {p[u * stride]};
+                add(v, a);
+            }
+            return;
+        }
+        take(s, ws);
+    }
+    __device__ __forceinline__ void take(float s, float ws) {
+        const TwoFloat t = two_sum(sum, s);
+        sum = t.hi;
+        low += t.lo;
+        if (ENT) w += ws;
     }
 
     template <int U>
@@ -150,7 +179,7 @@ struct RunEnt {
             // that are not there)
 #pragma unroll
             for (int u = 0; u < U; ++u) v[u] = make_uint4(v[u].x ^ a.zero, v[u].y ^ a.zero, v[u].z ^ a.zero, v[u].w ^ a.zero);
-            const float to = fmaxf(m, vecs_max<SX>(v));
+            const float to = fmaxf(m, vecs_max<SX>(v) + a.inv_c);
             const ExpRef ref(to, a.c);
             if (!ref.whole) {
 #pragma unroll 1
@@ -167,10 +196,7 @@ struct RunEnt {
             if (ENT && SX == 2) least = least_pair(ref, a.inv_c);
             s = sum_of(v, a, ws);                            // (NaN stays)
         }
-        const TwoFloat t = two_sum(sum, s);
-        sum = t.hi;
-        low += t.lo;
-        if (ENT) w += ws;
+        take(s, ws);
     }
 
     template <int U>
@@ -233,6 +259,23 @@ struct RunEnt {
         return pack_bf16(x, x);
     }
 };
+
+// log(v), v > 0 normal, to some 2^-31: the exponent's part, and 2 atanh((m - 1) / (m + 1)) of what is left in [0.75, 1.5).
+// (logf's error there, 2^-25, would be the same for every row whose sum is about as large: a sequence's sum has it
+// hundreds of times.)
+__device__ __forceinline__ TwoFloat log_fine(float v) {
+    const int e = (__float_as_int(v) - 0x3F400000) >> 23;
+    const float m = __int_as_float(__float_as_int(v) - (e << 23)), num = m - 1.f;
+    const TwoFloat den = two_sum(m, 1.f);
+    const float f = num / den.hi, low = (fmaf(-f, den.hi, num) - f * den.lo) / den.hi, s = f * f;
+    float p = fmaf(s, 1.f / 13.f, 1.f / 11.f);
+    p = fmaf(s, p, 1.f / 9.f);
+    p = fmaf(s, p, 1.f / 7.f);
+    p = fmaf(s, p, 1.f / 5.f);
+    p = fmaf(s, p, 1.f / 3.f);
+    const TwoFloat l = TwoFloat{static_cast<float>(e), 0.f} * ln2_two() + TwoFloat{2.f * f, 2.f * fmaf(f * s, p, low)};
+    return two_sum(l.hi, l.lo);
+}
 
 // Replace logit `lane` of a vector.
 template <int SX>
@@ -298,7 +341,7 @@ __device__ __forceinline__ RowEnd row_end(const TokArgs& a, const EntSum& es, fl
     float mean = 0.f, by_low = 0.f;                          // of the others' exponents; what c_low adds to log R
     if (!none) {
         const ExpRef ref(es.m, a.c);
-        lr = log_two(es.sum);
+        lr = log_fine(es.sum);
         lr.lo += kEx2Lacks;
         if (ENT) {
             mean = es.w / es.sum;
@@ -577,11 +620,11 @@ struct RowGrad {
     }
 };
 
-// The gradient of vectors [k0, k1) of a row (or zeros), by the CTA's threads in turn, from get(k), which gives vector k to
-// the thread that asks for it; the token's entry by the thread that has its vector.
-template <int SX, bool ENT, int U, typename Get>
+// The gradient of vectors [k0, k1) of a row (or zeros), by the CTA's threads in turn; src is where vector k0 lies, in global
+// or shared memory (kept: whole there, ragged ones too); the token's entry by the thread that has its vector.
+template <int SX, bool ENT, bool KEPT, int U>
 __device__ __forceinline__ void write_grad(const VocabRow<SX>& x, const VocabRow<SX>& g, int k0, int k1, int y, bool zero,
-                                           const RowGrad<SX, ENT>& rg, Get get) {
+                                           const RowGrad<SX, ENT>& rg, const uint4* src) {
     const int tid = threadIdx.x;
     const bool same_phase = x.a0 == g.a0;
     int k = k0 + tid;
@@ -589,19 +632,23 @@ __device__ __forceinline__ void write_grad(const VocabRow<SX>& x, const VocabRow
         for (; k < k1; k += kRowThreads) store_vec<SX>(g, x.first(k), make_uint4(0, 0, 0, 0), same_phase);
         return;
     }
+    auto get = [&](int k) { return KEPT ? src[k - k0] : load_vec<SX>(x, k, k1); };
     if (same_phase && rg.ref.whole) {
         // whole vectors go straight through, by the threads that have them
         const int w0 = k0 + (k0 < k1 && !x.whole(k0)), w1 = k1 - (k1 > w0 && !x.whole(k1 - 1));
         if (k < w0) k += kRowThreads;
         unsigned char* p = const_cast<unsigned char*>(g.p) + static_cast<long long>(x.first(k)) * SX;
-        for (; k + (U - 1) * kRowThreads < w1; k += U * kRowThreads, p += 16 * U * kRowThreads) {
+        const uint4* q = src + (k - k0);
+        const uint4* const end = src + (w1 - k0);
+        for (; q + (U - 1) * kRowThreads < end; q += U * kRowThreads, p += 16 * U * kRowThreads) {
             uint4 v[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) v[u] = get(k + u * kRowThreads);
+            for (int u = 0; u < U; ++u) v[u] = KEPT ? q[u * kRowThreads] : ld_vec16(q + u * kRowThreads);
 #pragma unroll
             for (int u = 0; u < U; ++u) st_vec16(p + 16 * u * kRowThreads, rg.of(v[u]));
         }
-        for (; k < w1; k += kRowThreads, p += 16 * kRowThreads) st_vec16(p, rg.of(get(k)));
+        if (U > 1)
+            for (; q < end; q += kRowThreads, p += 16 * kRowThreads) st_vec16(p, rg.of(KEPT ? *q : ld_vec16(q)));
         if (tid == 0 && k0 < w0) store_vec<SX>(g, x.first(k0), rg.of(get(k0)), false);
         if (w1 < k1 && (k1 - 1 - k0) % kRowThreads == tid) store_vec<SX>(g, x.first(k1 - 1), rg.of(get(k1 - 1)), false);
     } else {
@@ -636,7 +683,8 @@ __global__ void __launch_bounds__(kRowThreads) grad_kernel(TokArgs a) {
         da = s.pair >= 0 && s.pair < a.n_up ? da * a.up[s.pair] : 0.f;
     }
     const RowGrad<SX, ENT> rg(a, s, da, dh);
-    write_grad<SX, ENT, kTokVec>(x, g, k0, k1, y, s.f < 0.f || (da == 0.f && dh == 0.f), rg, [&](int k) { return load_vec<SX>(x, k, k1); });
+    write_grad<SX, ENT, false, kGradVec>(x, g, k0, k1, y, s.f < 0.f || (da == 0.f && dh == 0.f), rg,
+                                         reinterpret_cast<const uint4*>(x.p + static_cast<long long>(x.first(k0)) * SX));
 }
 
 // ---------------------------------------------------------------- loss and gradient in one
@@ -763,20 +811,14 @@ __global__ void __launch_bounds__(kRowThreads, kFusedCtas) kept_kernel(TokArgs a
     if (late) bar_wait(&s_copy, 0);                          // once more: it is in flight
     // the token leaves the sum (and the gradient's loop) here
     if (at.k >= k0 && at.k < k0 + cnt && (at.k - k0) % kRowThreads == tid) patch<SX>(s_x[at.k - k0], at.lane, ninf_bits<SX>());
-    {
-        int k = tid;
-        for (; k + (kTokVec - 1) * kRowThreads < cnt; k += kTokVec * kRowThreads) {
-            uint4 v[kTokVec];
-#pragma unroll
-            for (int u = 0; u < kTokVec; ++u) v[u] = s_x[k + u * kRowThreads];
-            if (k == tid && (tid | 31) + (kTokVec - 1) * kRowThreads < cnt) run.seed(v, a);
-            run.add(v, a);
-        }
-        for (; k < cnt; k += kRowThreads) {
-            uint4 v[1] = {s_x[k]};
-            run.add(v, a);
-        }
+    const uint4* const end = s_x + cnt;
+    const uint4* q = s_x + tid;
+    if ((tid | 31) < cnt) {
+        const uint4 v[1] = {*q};
+        run.seed(v, a);
     }
+    for (; q + (kTokVec - 1) * kRowThreads < end; q += kTokVec * kRowThreads) run.template add_from<kTokVec>(q, kRowThreads, a);
+    for (; q < end; q += kRowThreads) run.template add_from<1>(q, kRowThreads, a);
     EntSum es = lanes_join<ENT, 32>(run.get(), a.c);
     if (lane == 0) s_warp[warp] = es;
     late = __syncthreads_or(late);
@@ -806,7 +848,7 @@ __global__ void __launch_bounds__(kRowThreads, kFusedCtas) kept_kernel(TokArgs a
         const VocabRow<SX> g(a.g, row, a.g_stride, a.V);
         const RowGrad<SX, ENT> rg(a, s_row, s_row.a, s_row.h);
         zero = s_row.f < 0.f;
-        write_grad<SX, ENT, 1>(x, g, k0, k0 + cnt, y, zero, rg, [&](int k) { return s_x[k - k0]; });
+        write_grad<SX, ENT, true, 1>(x, g, k0, k0 + cnt, y, zero, rg, s_x);
     }
     if (rank == 0 && tid == 0) {
         RowEnd o = late ? row_bad(DSPARK_ROW_INTERNAL) : row_end<SX, ENT>(a, es, xy, pr);
