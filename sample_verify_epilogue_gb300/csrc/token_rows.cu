@@ -24,9 +24,10 @@ constexpr int kTokVec = 2;                                   // vectors a thread
 constexpr int kGradVec = 4;                                  // vectors a thread of the gradient has on their way
 constexpr int kGradVecs = 2048;                              // vectors of a row that a CTA of the gradient takes
 constexpr float kLn2 = 0.693147180559945f;
-// what the exponential unit's results lack on average, relative (2^20 arguments between whole exponents: 5.06e-8, from
-// 9e-8 too large to 1.4e-7 too small): added to the logarithm of a sum of them
-constexpr float kEx2Lacks = 5.06e-8f;
+// what a sum of the exponential unit's results lacks on average, relative: added to its logarithm.  Single results lack
+// 5.06e-8 (2^20 arguments between whole exponents: from 9e-8 too large to 1.4e-7 too small); rows of 32000 and 151936
+// normal logits at temperatures of 1 and 0.7 lacked 2.2e-8 to 5.5e-8.
+constexpr float kEx2Lacks = 3.5e-8f;
 
 enum TokenOp : int { kScore, kPolicy, kPreference };
 
