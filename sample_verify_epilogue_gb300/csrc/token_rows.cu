@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kTokVec = 2;                                   // vectors a thread takes at a time
 constexpr int kGradVec = 4;                                  // vectors a thread of the gradient has on their way
+constexpr int kShortRow = 2048;                              // vectors of a row that 128 threads take, where rows are many
 constexpr int kGradVecs = 2048;                              // vectors of a row that a CTA of the gradient takes
 constexpr float kLn2 = 0.693147180559945f;
 // what a sum of the exponential unit's results lacks on average, relative: added to its logarithm.  Single results lack
@@ -460,7 +461,7 @@ __device__ __forceinline__ EntSum peers_join(const PeerSum* s, int C, float c) {
 
 constexpr int kStatsVec = 4;                                 // vectors a thread has on their way
 template <int SX, bool ENT, int NT>
-__global__ void __launch_bounds__(NT, NT == 256 ? 6 : 3) stats_kernel(TokArgs a) {
+__global__ void __launch_bounds__(NT, 1536 / NT) stats_kernel(TokArgs a) {
     __shared__ EntSum s_warp[(NT / 32)];
     __shared__ PeerSum s_peer[kMaxCluster];                  // (in the row's first CTA) written by the cluster's
     __shared__ uint64_t s_bar;
@@ -469,6 +470,7 @@ __global__ void __launch_bounds__(NT, NT == 256 ? 6 : 3) stats_kernel(TokArgs a)
     const long long row = blockIdx.x >> a.log_c;
     if (C > 1) expect_peers(&s_bar, C - 1);
     pdl_wait();
+    if (a.op == kPreference) pdl_trigger();                  // the pairs' few CTAs may come while the last rows are read
     const int y = a.tokens[row];
     PolicyRow pr{1.f, 0.f, 0.f, 0.f};
     if (a.op == kPolicy && a.weights) pr.w = a.weights[row];
@@ -623,43 +625,43 @@ struct RowGrad {
 
 // The gradient of vectors [k0, k1) of a row (or zeros), by the CTA's threads in turn; src is where vector k0 lies, in global
 // or shared memory (kept: whole there, ragged ones too); the token's entry by the thread that has its vector.
-template <int SX, bool ENT, bool KEPT, int U>
+template <int SX, bool ENT, bool KEPT, int U, int NT>
 __device__ __forceinline__ void write_grad(const VocabRow<SX>& x, const VocabRow<SX>& g, int k0, int k1, int y, bool zero,
                                            const RowGrad<SX, ENT>& rg, const uint4* src) {
     const int tid = threadIdx.x;
     const bool same_phase = x.a0 == g.a0;
     int k = k0 + tid;
     if (zero) {
-        for (; k < k1; k += kRowThreads) store_vec<SX>(g, x.first(k), make_uint4(0, 0, 0, 0), same_phase);
+        for (; k < k1; k += NT) store_vec<SX>(g, x.first(k), make_uint4(0, 0, 0, 0), same_phase);
         return;
     }
     auto get = [&](int k) { return KEPT ? src[k - k0] : load_vec<SX>(x, k, k1); };
     if (same_phase && rg.ref.whole) {
         // whole vectors go straight through, by the threads that have them
         const int w0 = k0 + (k0 < k1 && !x.whole(k0)), w1 = k1 - (k1 > w0 && !x.whole(k1 - 1));
-        if (k < w0) k += kRowThreads;
+        if (k < w0) k += NT;
         unsigned char* p = const_cast<unsigned char*>(g.p) + static_cast<long long>(x.first(k)) * SX;
         const uint4* q = src + (k - k0);
         const uint4* const end = src + (w1 - k0);
-        for (; q + (U - 1) * kRowThreads < end; q += U * kRowThreads, p += 16 * U * kRowThreads) {
+        for (; q + (U - 1) * NT < end; q += U * NT, p += 16 * U * NT) {
             uint4 v[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) v[u] = KEPT ? q[u * kRowThreads] : ld_vec16(q + u * kRowThreads);
+            for (int u = 0; u < U; ++u) v[u] = KEPT ? q[u * NT] : ld_vec16(q + u * NT);
 #pragma unroll
-            for (int u = 0; u < U; ++u) st_vec16(p + 16 * u * kRowThreads, rg.of(v[u]));
+            for (int u = 0; u < U; ++u) st_vec16(p + 16 * u * NT, rg.of(v[u]));
         }
         if (U > 1)
-            for (; q < end; q += kRowThreads, p += 16 * kRowThreads) st_vec16(p, rg.of(KEPT ? *q : ld_vec16(q)));
+            for (; q < end; q += NT, p += 16 * NT) st_vec16(p, rg.of(KEPT ? *q : ld_vec16(q)));
         if (tid == 0 && k0 < w0) store_vec<SX>(g, x.first(k0), rg.of(get(k0)), false);
-        if (w1 < k1 && (k1 - 1 - k0) % kRowThreads == tid) store_vec<SX>(g, x.first(k1 - 1), rg.of(get(k1 - 1)), false);
+        if (w1 < k1 && (k1 - 1 - k0) % NT == tid) store_vec<SX>(g, x.first(k1 - 1), rg.of(get(k1 - 1)), false);
     } else {
-        for (; k < k1; k += kRowThreads) {
+        for (; k < k1; k += NT) {
             const uint4 v = get(k);
             store_vec<SX>(g, x.first(k), rg.ref.whole ? rg.of(v) : rg.far_of(v), same_phase);
         }
     }
     const Place<SX> at(x, y);
-    if (at.k >= k0 && at.k < k1 && (at.k - k0) % kRowThreads == tid) store_one<SX>(g, y, rg.at_y);
+    if (at.k >= k0 && at.k < k1 && (at.k - k0) % NT == tid) store_one<SX>(g, y, rg.at_y);
 }
 
 template <int SX, bool ENT>
@@ -684,7 +686,7 @@ __global__ void __launch_bounds__(kRowThreads) grad_kernel(TokArgs a) {
         da = s.pair >= 0 && s.pair < a.n_up ? da * a.up[s.pair] : 0.f;
     }
     const RowGrad<SX, ENT> rg(a, s, da, dh);
-    write_grad<SX, ENT, false, kGradVec>(x, g, k0, k1, y, s.f < 0.f || (da == 0.f && dh == 0.f), rg,
+    write_grad<SX, ENT, false, kGradVec, kRowThreads>(x, g, k0, k1, y, s.f < 0.f || (da == 0.f && dh == 0.f), rg,
                                          reinterpret_cast<const uint4*>(x.p + static_cast<long long>(x.first(k0)) * SX));
 }
 
@@ -761,12 +763,12 @@ __device__ __forceinline__ RowSaved quick_end(const TokArgs& a, const EntSum& es
 // A policy row's loss and gradient without reading it twice: a cluster of C CTAs keeps the row in shared memory, a span
 // each, between the sum and the gradient.  A thread copies the vectors that it will read, so that nothing but the joins
 // of the sums has to wait for anyone.
-constexpr int kFusedSpan = 4608;                             // vectors of a span at most
-constexpr int kFusedCtas = 5;                                // CTAs to an SM at most
+constexpr int kFusedSpan = 14000;                            // vectors of a span at most: 224,000 bytes
+constexpr int kFusedCtas = 5;                                // CTAs of 256 threads to an SM at most
 
-template <int SX, bool ENT, bool GRAD>
-__global__ void __launch_bounds__(kRowThreads, kFusedCtas) kept_kernel(TokArgs a) {
-    __shared__ EntSum s_warp[kRowWarps];
+template <int SX, bool ENT, int NT>
+__global__ void __launch_bounds__(NT, kFusedCtas * 256 / NT) kept_kernel(TokArgs a) {
+    __shared__ EntSum s_warp[(NT / 32)];
     __shared__ PeerSum s_peer[kMaxCluster];                  // written by the row's CTAs
     __shared__ RowSaved s_row;
     __shared__ uint64_t s_bar, s_copy;
@@ -778,21 +780,18 @@ __global__ void __launch_bounds__(kRowThreads, kFusedCtas) kept_kernel(TokArgs a
         mbar_init(&s_copy, 1);
         fence_mbar_init();
     }
-    if (C > 1) expect_peers(&s_bar, GRAD ? C : C - 1);
+    if (C > 1) expect_peers(&s_bar, C);
     __syncthreads();
     pdl_wait();
     const int y = a.tokens[row];
     PolicyRow pr{1.f, 0.f, 0.f, 0.f};
-    if ((GRAD || a.op == kPolicy) && a.weights) pr.w = a.weights[row];
+    if (a.weights) pr.w = a.weights[row];
     const bool bad = y < -1 || y >= a.V, dead = bad || y < 0 || pr.w == 0.f;   // the same in every CTA of the row
-    const VocabRow<SX> x(a.x, row, a.x_stride, a.V);
+    const VocabRow<SX> x(a.x, row, a.x_stride, a.V), g(a.g, row, a.g_stride, a.V);
     const int k0 = min(x.nvec, rank * a.span), cnt = min(x.nvec, k0 + a.span) - k0;
     if (dead) {
         if (rank == 0 && tid == 0) row_skipped(a, row, bad ? DSPARK_ROW_BAD_TOKEN : 0);
-        if (GRAD) {
-            const VocabRow<SX> g(a.g, row, a.g_stride, a.V);
-            for (int k = tid; k < cnt; k += kRowThreads) store_vec<SX>(g, x.first(k0 + k), make_uint4(0, 0, 0, 0), x.a0 == g.a0);
-        }
+        for (int k = tid; k < cnt; k += NT) store_vec<SX>(g, x.first(k0 + k), make_uint4(0, 0, 0, 0), x.a0 == g.a0);
         if (C > 1) cluster_wait();
         return;
     }
@@ -800,57 +799,48 @@ __global__ void __launch_bounds__(kRowThreads, kFusedCtas) kept_kernel(TokArgs a
     float xy = 0.f;
     if (warp == 0) {
         xy = load_logit<SX>(x, y);
-        if (GRAD || a.op == kPolicy) {
-            pr.old = a.old_lp[row];
-            pr.adv = a.adv[row];
-            if (a.ref_lp) pr.ref = a.ref_lp[row];
-        }
+        pr.old = a.old_lp[row];
+        pr.adv = a.adv[row];
+        if (a.ref_lp) pr.ref = a.ref_lp[row];
     }
     const Place<SX> at(x, y);
     RunEnt<SX, ENT> run;
     bool late = !copy_wait(&s_copy, 0);
     if (late) bar_wait(&s_copy, 0);                          // once more: it is in flight
     // the token leaves the sum (and the gradient's loop) here
-    if (at.k >= k0 && at.k < k0 + cnt && (at.k - k0) % kRowThreads == tid) patch<SX>(s_x[at.k - k0], at.lane, ninf_bits<SX>());
+    if (at.k >= k0 && at.k < k0 + cnt && (at.k - k0) % NT == tid) patch<SX>(s_x[at.k - k0], at.lane, ninf_bits<SX>());
     const uint4* const end = s_x + cnt;
     const uint4* q = s_x + tid;
     if ((tid | 31) < cnt) {
         const uint4 v[1] = {*q};
         run.seed(v, a);
     }
-    for (; q + (kTokVec - 1) * kRowThreads < end; q += kTokVec * kRowThreads) run.template add_from<kTokVec>(q, kRowThreads, a);
-    for (; q < end; q += kRowThreads) run.template add_from<1>(q, kRowThreads, a);
+    for (; q + (kTokVec - 1) * NT < end; q += kTokVec * NT) run.template add_from<kTokVec>(q, NT, a);
+    for (; q < end; q += NT) run.template add_from<1>(q, NT, a);
     EntSum es = lanes_join<ENT, 32>(run.get(), a.c);
     if (lane == 0) s_warp[warp] = es;
     late = __syncthreads_or(late);
     if (C > 1) cluster_wait();                               // the row's CTAs are there
     if (warp == 0) {
-        es = lanes_join<ENT, kRowWarps>(s_warp[lane & (kRowWarps - 1)], a.c);
+        es = lanes_join<ENT, (NT / 32)>(s_warp[lane & ((NT / 32) - 1)], a.c);
         if (C > 1) {
             // the token's logit has been read: its place may be written, where the gradient takes the logits' place
             const uint32_t after = (__float_as_uint(xy) & ~1u) | late;
-            if (GRAD ? lane < C : lane == 0 && rank != 0) push_sum(&s_peer[rank], &s_bar, lane, es, after);
-            if (!GRAD && rank != 0) return;
-            if (!GRAD && lane == 0) s_peer[0] = PeerSum{es, after};
-            __syncwarp();
+            if (lane < C) push_sum(&s_peer[rank], &s_bar, lane, es, after);
             late = !bar_wait(&s_bar, 0, kPeerMs) || late;
             late = __any_sync(0xffffffffu, lane < C && (s_peer[lane & (kMaxCluster - 1)].after & 1u)) || late;
             es = peers_join<ENT>(s_peer, C, a.c);
         }
-        if (GRAD && lane == 0) {
+        if (lane == 0) {
             if (late) s_row = row_bad(DSPARK_ROW_INTERNAL).saved;
             else s_row = is_quick(es, xy, a.c) ? quick_end<SX, ENT>(a, es, xy, QuickRow{base2(pr.old), base2(pr.ref), pr.w, pr.adv})
                                                : row_end<SX, ENT>(a, es, xy, pr).saved;
         }
     }
-    bool zero = false;
-    if (GRAD) {
-        __syncthreads();
-        const VocabRow<SX> g(a.g, row, a.g_stride, a.V);
-        const RowGrad<SX, ENT> rg(a, s_row, s_row.a, s_row.h);
-        zero = s_row.f < 0.f;
-        write_grad<SX, ENT, true, 1>(x, g, k0, k0 + cnt, y, zero, rg, s_x);
-    }
+    __syncthreads();
+    const RowGrad<SX, ENT> rg(a, s_row, s_row.a, s_row.h);
+    const bool zero = s_row.f < 0.f;
+    write_grad<SX, ENT, true, 1, NT>(x, g, k0, k0 + cnt, y, zero, rg, s_x);
     if (rank == 0 && tid == 0) {
         RowEnd o = late ? row_bad(DSPARK_ROW_INTERNAL) : row_end<SX, ENT>(a, es, xy, pr);
         if (zero && !o.status) o = row_bad(DSPARK_ROW_NONFINITE);   // (a loss next to fp32's largest number)
@@ -873,18 +863,27 @@ struct PairArgs {
     RowSaved* saved;
 };
 
-// A CTA to a pair: the two sequences' sums in pairs of floats (they cancel), the loss, and each row's dL/dlog p.
+// A CTA to a pair, half of its warps to a sequence: the sums in pairs of floats (they cancel), the loss, and each row's
+// dL/dlog p.  4 us, most of it its launch and three trips to L2 in a row.
+struct __align__(16) SeqSum {
+    TwoFloat sum;
+    int count, status;
+};
+__device__ __forceinline__ TwoFloat add_finite(const TwoFloat& a, const TwoFloat& b) {   // infinities and NaN have no low part
+    return fabsf(a.hi) < INFINITY && fabsf(b.hi) < INFINITY ? a + b : TwoFloat{a.hi + b.hi, 0.f};
+}
 __global__ void __launch_bounds__(kRowThreads) pair_kernel(PairArgs a) {
-    __shared__ TwoFloat s_sum[2][kRowWarps];
-    __shared__ int s_count[2][kRowWarps];
+    __shared__ SeqSum s_part[kRowWarps];
     __shared__ float s_coef[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, p = blockIdx.x;
+    constexpr int kHalf = kRowThreads / 2;
     pdl_wait();
     // the offsets up to this pair's last ascend and stay inside the rows
-    bool bad = false;
-    for (int k = tid; k < 2 * p + 2; k += kRowThreads) bad = bad || a.offsets[k] > a.offsets[k + 1];
     const int lo = a.offsets[2 * p], mid = a.offsets[2 * p + 1], hi = a.offsets[2 * p + 2];
-    if (__syncthreads_or(bad || a.offsets[0] < 0 || hi > a.R)) {
+    const int first = a.offsets[0];
+    bool bad = first < 0 || hi > a.R;
+    for (int k = tid; k < 2 * p + 2; k += kRowThreads) bad = bad || a.offsets[k] > a.offsets[k + 1];
+    if (__syncthreads_or(bad)) {
         if (tid == 0) {
             a.loss[p] = NAN;
             if (a.rewards) a.rewards[2 * p] = a.rewards[2 * p + 1] = NAN;
@@ -892,50 +891,41 @@ __global__ void __launch_bounds__(kRowThreads) pair_kernel(PairArgs a) {
         }
         return;
     }
-    int status = 0;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        TwoFloat sum{0.f, 0.f};
-        int count = 0;
-        for (int r = (k ? mid : lo) + tid; r < (k ? hi : mid); r += kRowThreads) {
-            status |= a.row_status[r];
-            if (a.tokens[r] < 0) continue;
-            ++count;
-            const float lp = a.saved[r].level;
-            TwoFloat gain = a.ref_lp ? two_sum(lp, -a.ref_lp[r]) : TwoFloat{lp, 0.f};
-            gain.lo += a.saved[r].py;
-            sum = fabsf(gain.hi) < INFINITY && fabsf(sum.hi) < INFINITY ? sum + gain : TwoFloat{sum.hi + gain.hi, 0.f};
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            const TwoFloat other{__shfl_xor_sync(0xffffffffu, sum.hi, o), __shfl_xor_sync(0xffffffffu, sum.lo, o)};
-            sum = fabsf(other.hi) < INFINITY && fabsf(sum.hi) < INFINITY ? sum + other : TwoFloat{sum.hi + other.hi, 0.f};
-            count += __shfl_xor_sync(0xffffffffu, count, o);
-        }
-        if (lane == 0) {
-            s_sum[k][warp] = sum;
-            s_count[k][warp] = count;
-        }
+    SeqSum q{TwoFloat{0.f, 0.f}, 0, 0};
+    const int half = tid / kHalf;
+    for (int r = (half ? mid : lo) + tid % kHalf; r < (half ? hi : mid); r += kHalf) {
+        q.status |= a.row_status[r];
+        const float lp = a.saved[r].level, low = a.saved[r].py, ref = a.ref_lp ? a.ref_lp[r] : 0.f;
+        if (a.tokens[r] < 0) continue;
+        ++q.count;
+        TwoFloat gain = a.ref_lp ? two_sum(lp, -ref) : TwoFloat{lp, 0.f};
+        gain.lo += low;
+        q.sum = add_finite(q.sum, gain);
     }
-    status = __reduce_or_sync(0xffffffffu, status);
-    __shared__ int s_status[kRowWarps];
-    if (lane == 0) s_status[warp] = status;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        q.sum = add_finite(q.sum, TwoFloat{__shfl_xor_sync(0xffffffffu, q.sum.hi, o), __shfl_xor_sync(0xffffffffu, q.sum.lo, o)});
+    }
+    q.count = __reduce_add_sync(0xffffffffu, q.count);
+    q.status = __reduce_or_sync(0xffffffffu, q.status);
+    if (lane == 0) s_part[warp] = q;
     __syncthreads();
     if (tid == 0) {
         TwoFloat reward[2];
         float norm[2];
         int st = 0;
-        for (int w = 0; w < kRowWarps; ++w) st |= s_status[w];
+#pragma unroll
         for (int k = 0; k < 2; ++k) {
-            TwoFloat sum{0.f, 0.f};
-            int count = 0;
-            for (int w = 0; w < kRowWarps; ++w) {
-                const TwoFloat other = s_sum[k][w];
-                sum = fabsf(other.hi) < INFINITY && fabsf(sum.hi) < INFINITY ? sum + other : TwoFloat{sum.hi + other.hi, 0.f};
-                count += s_count[k][w];
+            SeqSum s = s_part[k * kRowWarps / 2];
+#pragma unroll
+            for (int w = 1; w < kRowWarps / 2; ++w) {
+                const SeqSum& o = s_part[k * kRowWarps / 2 + w];
+                s = SeqSum{add_finite(s.sum, o.sum), s.count + o.count, s.status | o.status};
             }
-            norm[k] = a.mean ? static_cast<float>(max(count, 1)) : 1.f;
-            reward[k] = fabsf(sum.hi) < INFINITY ? sum * TwoFloat{a.beta, 0.f} / TwoFloat{norm[k], 0.f} : TwoFloat{sum.hi, 0.f};
+            st |= s.status;
+            norm[k] = a.mean ? static_cast<float>(max(s.count, 1)) : 1.f;
+            reward[k] = fabsf(s.sum.hi) < INFINITY ? s.sum * TwoFloat{a.beta, 0.f} : TwoFloat{s.sum.hi, 0.f};
+            if (a.mean && fabsf(reward[k].hi) < INFINITY) reward[k] = reward[k] / TwoFloat{norm[k], 0.f};
         }
         TwoFloat z{(reward[0].hi - reward[1].hi) - a.margin, 0.f};
         if (fabsf(z.hi) < INFINITY) z = reward[0] + -reward[1] + TwoFloat{-a.margin, 0.f};
@@ -949,12 +939,12 @@ __global__ void __launch_bounds__(kRowThreads) pair_kernel(PairArgs a) {
             loss *= w;
             by_z = w * (e * of.q - (1.f - e) * of.p);
         }
+        s_coef[0] = st ? 0.f : by_z * a.beta / norm[0];
+        s_coef[1] = st ? 0.f : -by_z * a.beta / norm[1];
         a.loss[p] = st ? NAN : loss;
         if (a.rewards)
             for (int k = 0; k < 2; ++k) a.rewards[2 * p + k] = st ? NAN : reward[k].hi + reward[k].lo;
         a.pair_status[p] = st;
-        s_coef[0] = st ? 0.f : by_z * a.beta / norm[0];
-        s_coef[1] = st ? 0.f : -by_z * a.beta / norm[1];
     }
     __syncthreads();
     for (int r = lo + tid; r < hi; r += kRowThreads) {
@@ -998,6 +988,12 @@ bool misplaced(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) 
 // 512, which have a row done in half the time: as many rows as they are in one wave are theirs (400 rows of 151936: 23 us,
 // 27 by 256; 509 of 50001 fp32: 22 and 20).  Fewer still are split over clusters (9 rows of 151936 in 1, 2, 4, 8 CTAs of
 // 256: 11.4, 7.9, 5.8, 4.5 us; 8 of 512: 3.9; short rows lose by it: 100 of 32000 4.1 us whole, 4.9 in halves).
+template <int NT>
+cudaError_t launch_stats_by(const TokArgs& a, int sx, bool entropy, unsigned grid, int C, cudaStream_t s) {
+    auto kern = sx == 2 ? (entropy ? stats_kernel<2, true, NT> : stats_kernel<2, false, NT>)
+                        : (entropy ? stats_kernel<4, true, NT> : stats_kernel<4, false, NT>);
+    return launch_cluster(kern, grid, NT, C, 0, s, a);
+}
 dspark_status_t launch_stats(TokArgs& a, int sx, bool entropy, const dspark_token_params_t* p) {
     const int nvec = max_vectors(p->V, sx);
     const long long rows = p->n_rows;
@@ -1010,11 +1006,8 @@ dspark_status_t launch_stats(TokArgs& a, int sx, bool entropy, const dspark_toke
     }
     const unsigned grid = static_cast<unsigned>(p->n_rows) * C;
     const cudaStream_t s = static_cast<cudaStream_t>(p->stream);
-    auto narrow_kern = sx == 2 ? (entropy ? stats_kernel<2, true, 256> : stats_kernel<2, false, 256>)
-                               : (entropy ? stats_kernel<4, true, 256> : stats_kernel<4, false, 256>);
-    auto wide_kern = sx == 2 ? (entropy ? stats_kernel<2, true, 512> : stats_kernel<2, false, 512>)
-                             : (entropy ? stats_kernel<4, true, 512> : stats_kernel<4, false, 512>);
-    const cudaError_t e = wide ? launch_cluster(wide_kern, grid, 512, C, 0, s, a) : launch_cluster(narrow_kern, grid, 256, C, 0, s, a);
+    const cudaError_t e = wide ? launch_stats_by<512>(a, sx, entropy, grid, C, s)
+                          : rows > 456 && nvec <= kShortRow ? launch_stats_by<128>(a, sx, entropy, grid, C, s) : launch_stats_by<256>(a, sx, entropy, grid, C, s);
     return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
@@ -1046,18 +1039,20 @@ int fused_split(int nvec, long long rows) {
     return best;
 }
 
-template <bool GRAD>
+template <int NT>
+cudaError_t launch_kept_by(TokArgs& a, int sx, bool entropy, const dspark_token_params_t* p) {
+    auto kern = sx == 2 ? (entropy ? kept_kernel<2, true, NT> : kept_kernel<2, false, NT>)
+                        : (entropy ? kept_kernel<4, true, NT> : kept_kernel<4, false, NT>);
+    const size_t smem = static_cast<size_t>(a.span) * 16;
+    // beyond what a launch gets unasked; the same for every call, as another thread's may come between
+    if (smem > 32 * 1024)
+        if (const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 16 * kFusedSpan); e != cudaSuccess) return e;
+    return launch_cluster(kern, static_cast<unsigned>(p->n_rows) * a.splits, NT, a.splits, smem, static_cast<cudaStream_t>(p->stream), a);
+}
 dspark_status_t launch_kept(TokArgs& a, int sx, bool entropy, const dspark_token_params_t* p, int C) {
     a.splits = C;
     a.span = (max_vectors(p->V, sx) + C - 1) / C;
-    auto kern = sx == 2 ? (entropy ? kept_kernel<2, true, GRAD> : kept_kernel<2, false, GRAD>)
-                        : (entropy ? kept_kernel<4, true, GRAD> : kept_kernel<4, false, GRAD>);
-    const size_t smem = static_cast<size_t>(a.span) * 16;
-    // beyond what a launch gets unasked; the same for every call, as another thread's may come between
-    if (smem > 32 * 1024 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 16 * kFusedSpan) != cudaSuccess)
-        return DSPARK_ERR_CUDA;
-    const cudaError_t e = launch_cluster(kern, static_cast<unsigned>(p->n_rows) * C, kRowThreads, C, smem,
-                                         static_cast<cudaStream_t>(p->stream), a);
+    const cudaError_t e = C == 1 && a.span <= kShortRow ? launch_kept_by<128>(a, sx, entropy, p) : launch_kept_by<256>(a, sx, entropy, p);
     return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
@@ -1127,7 +1122,7 @@ dspark_status_t dspark_policy_loss(const void* logits, const dspark_policy_t* po
     a.saved = reinterpret_cast<RowSaved*>(out_saved);
     const bool entropy = out_entropy || policy->entropy_coef != 0.f;
     if (out_grad)
-        if (const int C = fused_split(max_vectors(params->V, sx), params->n_rows); C > 0) return launch_kept<true>(a, sx, entropy, params, C);
+        if (const int C = fused_split(max_vectors(params->V, sx), params->n_rows); C > 0) return launch_kept(a, sx, entropy, params, C);
     const dspark_status_t st = launch_stats(a, sx, entropy, params);
     if (st != DSPARK_OK || !out_grad) return st;
     return launch_grad(a, sx, policy->entropy_coef != 0.f, params);

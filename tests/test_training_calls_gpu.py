@@ -242,7 +242,8 @@ def test_calls_from_two_threads(bd):  # noqa: F811
                              status=t[12].cpu().numpy(), grad=host(t[11])), "fp32", 1.0, 0.1, 0.01)
 
 
-@pytest.mark.parametrize("dtype,V", [("bf16", 294912), ("bf16", 300001), ("fp32", 147456), ("fp32", 150001)])
+@pytest.mark.parametrize("dtype,V", [("bf16", 294912), ("bf16", 300001), ("fp32", 150001), ("bf16", 896000), ("bf16", 900001),
+                                     ("fp32", 448000), ("fp32", 450001)])
 def test_rows_around_the_longest_kept_ones(bd, dtype, V):  # noqa: F811
     """Rows that eight spans just hold, and rows that they do not, which are read twice; also unaligned."""
     rng = np.random.default_rng(V)
