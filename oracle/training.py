@@ -11,15 +11,13 @@ def token_row(x, y, temperature):
     if np.isnan(x).any() or np.isposinf(x).any() or not np.isfinite(x).any():
         return None
     s = x / temperature
-    lse = s.max() + np.log(np.exp(s - s.max()).sum())
     others = np.delete(s, y)
+    m = d = -np.inf                                          # d: log of the others' mass over the token's
     if len(others) and np.isfinite(others).any():
         m = others.max()
-        log_rest = m + np.log(np.exp(others - m).sum())
-    else:
-        m = log_rest = -np.inf
-    d = log_rest - s[y]
-    logp = s - lse
+        d = (m - s[y]) + np.log(np.exp(others - m).sum())
+    # from the largest logit, which may be far larger than what the logarithm adds
+    logp = (s - s.max()) - np.log(np.exp(s - s.max()).sum())
     logp[y] = -np.logaddexp(0, d)                            # to its last bits for a token that has nearly all the mass
     with np.errstate(over="ignore"):
         q = 1 / (1 + np.exp(-d))
@@ -27,7 +25,7 @@ def token_row(x, y, temperature):
         logp[y], q = -np.inf, 1.0
     p = np.exp(logp)
     entropy = -(p[p > 0] * logp[p > 0]).sum()
-    return dict(s=s, y=y, p=p, logp=logp, q=q, d=d, entropy=entropy, m=m, log_rest=log_rest)
+    return dict(s=s, y=y, p=p, logp=logp, q=q, d=d, entropy=entropy, m=m)
 
 
 def token_grad(r, a, h, temperature):

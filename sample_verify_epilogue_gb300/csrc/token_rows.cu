@@ -9,7 +9,11 @@
 // dL/dH = h:
 //   dL/dx_v = -p_v (a + h (log p_v + H)) / T,   dL/dx_y = (a q - h p_y (log p_y + H)) / T
 //
-// stats_kernel streams a row and leaves what the gradient needs (32 bytes a row), grad_kernel streams it again.
+// stats_kernel streams a row and leaves what the gradient needs (32 bytes a row), grad_kernel streams it again, kept_kernel
+// does both with the row in shared memory, pair_kernel makes the pairs of a preference from their rows.  All but the last are
+// bound by bandwidth where there is enough to read: of the copy bandwidth stats 0.92 to 0.98 (4096 rows of 151936 bf16 with the
+// entropy 182 us, a tenth of them without a token), the gradient 0.93, both in one 0.98 (353 us; 0.93, 376 us, with an entropy
+// bonus).  Where a CTA has little to read its latencies bound it: token, first vectors, joins, the row's end.
 #include <algorithm>
 #include <cmath>
 #include <limits>
@@ -20,7 +24,7 @@ namespace dspark {
 
 namespace {
 
-constexpr int kTokVec = 2;                                   // vectors a thread takes at a time
+constexpr int kTokVec = 2;                                   // vectors a thread takes at a time from shared memory
 constexpr int kGradVec = 4;                                  // vectors a thread of the gradient has on their way
 constexpr int kShortRow = 2048;                              // vectors of a row that 128 threads take, where rows are many
 constexpr int kGradVecs = 2048;                              // vectors of a row that a CTA of the gradient takes
@@ -109,8 +113,9 @@ __device__ __forceinline__ EntSum lanes_join(EntSum a, float c) {
 //
 // Vectors are added by the reference that is there, whatever their maximum: where that makes a sum of 64 or more (the
 // first vectors, a maximum far above those before) they are added again by the maximum of both.  (64: an entropy is a
-// difference of what the exponents weigh and the sum's logarithm, which should not be far from 0 themselves.)  The reference's whole
-// exponent r makes the exponent's one rounding that of the fma; -inf stands for none.
+// difference of what the exponents weigh and the sum's logarithm, which should not be far from 0 themselves.)  The
+// reference's whole exponent r makes the exponent's one rounding that of the fma; -inf stands for none.  (With the running
+// maximum of every batch of vectors in the way: 191 us where this takes 177, 4096 rows of 151936 with the entropy.)
 //
 // A row's log-probability may be off by 1e-7 at random, but not to one side: sums of a thousand log ratios follow.  So
 // the vectors' sum joins the rest in a pair of floats (added one by one, small terms are lost more often than gained:
@@ -135,7 +140,7 @@ struct RunEnt {
     }
 
     // Before the first vectors, by a whole warp: the largest of them all is a reference that hardly ever has to be raised
-    // (a thread's own: policy_batch 389 -> 435 us).
+    // (a thread's own: 4096 policy rows of 151936 389 -> 435 us).
     template <int U>
     __device__ __forceinline__ void seed(const uint4 (&v)[U], const TokArgs& a) {
         const float to = key_to_f(__reduce_max_sync(0xffffffffu, fkey(vecs_max<SX>(v)))) + a.inv_c;
@@ -255,10 +260,11 @@ struct RunEnt {
         if (ENT && SX == 2 && ref.whole) least = least_pair(ref, a.inv_c);
     }
 
-    // a logit whose exponential by the reference is 0, not below the type's lowest value
+    // a logit whose exponential by the reference is 0, not below the type's lowest value (rounded down: of logits of a million
+    // the next one above may be the largest)
     static __device__ __forceinline__ uint32_t least_pair(const ExpRef& ref, float inv_c) {
-        const float x = fmaxf((ref.r - 4096.f) * inv_c, -3.38e38f);
-        return pack_bf16(x, x);
+        const uint32_t x = __bfloat16_as_ushort(__float2bfloat16_rd(fmaxf((ref.r - 4096.f) * inv_c, -3.38e38f)));
+        return x | x << 16;
     }
 };
 
@@ -300,7 +306,7 @@ __device__ __forceinline__ float k3_of(float D, float em1) {
         s = fmaf(D * s, 1.f / 3.f, 1.f);
         return 0.5f * D * D * s;
     }
-    return em1 - D;
+    return D > 64.f ? em1 : em1 - D;                         // (an infinite D has an infinite e^D)
 }
 
 struct PolicyRow {
@@ -330,8 +336,17 @@ struct Odds {
     }
 };
 
-// From a row's sum over the other tokens and its token's logit, by one thread: on the way between the sum and the gradient,
-// so its steps are few and share what they can (1400 cycles in a first form: 45 of 500 us of policy_batch's rows).
+// What the gradient's exponentials, relative to those of the sum, have to be multiplied with for c_low (as much as 2% for
+// logits of a million T): fp32's gradient takes it into its exponents, bf16's does not; a sum with the entropy does not.
+// by_low is what it adds to the sum's logarithm; without the entropy the largest logit stands for all that count.  (H, a
+// difference of two that have it or have it not, is the same.)
+template <int SX, bool ENT>
+__device__ __forceinline__ float by_low_of(const TokArgs& a, float m, float by_low) {
+    if (ENT) return SX == 4 ? ex2_approx(-kLog2E * by_low) : 1.f;
+    return SX == 4 ? 1.f : fabsf(m * a.c) < 4194304.f ? ex2_approx(m * a.c_low) : 1.f;
+}
+
+// From a row's sum over the other tokens and its token's logit, by one thread.
 template <int SX, bool ENT>
 __device__ __forceinline__ RowEnd row_end(const TokArgs& a, const EntSum& es, float xy, const PolicyRow& pr) {
     RowEnd o{RowSaved{0.f, -1.f, 0.f, 0.f, 0.f, 0.f, 0.f, -1}, NAN, NAN, NAN, NAN, DSPARK_ROW_NONFINITE};
@@ -359,15 +374,14 @@ __device__ __forceinline__ RowEnd row_end(const TokArgs& a, const EntSum& es, fl
             const float by = (es.m - xy) * a.inv_t;
             d = fabsf(by) < INFINITY ? TwoFloat{by, 0.f} + lr : TwoFloat{by, 0.f};
         }
+        if (fabsf(d.hi) < INFINITY) d = two_sum(d.hi, d.lo);   // (what c_low adds is not small beside logits of thousands)
         s.m = es.m;
     }
     const Odds k(d);
     const TwoFloat lp = -k.sp;
     float H = 0.f;
     if (ENT) H = (k.p > 0.f ? k.p * k.sp.hi : 0.f) + (none || k.q == 0.f ? 0.f : k.q * (k.sm + fmaf(-kLn2, mean, lr.hi + lr.lo)));
-    // (the gradient of fp32 takes c_low into its exponents, that of bf16 does not; H, a difference of two that have it or
-    // have it not, is the same)
-    s.f = none ? 0.f : k.q / es.sum * a.inv_t * (SX == 4 ? 1.f - by_low : 1.f);
+    s.f = none ? 0.f : k.q / es.sum * a.inv_t * by_low_of<SX, ENT>(a, es.m, by_low);
     s.level = none || !(k.sm < INFINITY) ? 0.f : H - (SX == 4 ? lr.hi + by_low : lr.hi) - k.sm;
     s.q = k.q * a.inv_t;
     s.py = k.p > 0.f ? k.p * (lp.hi + H) * a.inv_t : 0.f;
@@ -459,9 +473,8 @@ __device__ __forceinline__ EntSum peers_join(const PeerSum* s, int C, float c) {
     return lanes_join<ENT, kMaxCluster>(k < C ? s[k].es : EntSum{-INFINITY, 0.f, 0.f}, c);
 }
 
-constexpr int kStatsVec = 4;                                 // vectors a thread has on their way
-template <int SX, bool ENT, int NT>
-__global__ void __launch_bounds__(NT, 1536 / NT) stats_kernel(TokArgs a) {
+template <int SX, bool ENT, int NT, int U>
+__global__ void __launch_bounds__(NT, U == 4 ? 1536 / NT : 1024 / NT) stats_kernel(TokArgs a) {
     __shared__ EntSum s_warp[(NT / 32)];
     __shared__ PeerSum s_peer[kMaxCluster];                  // (in the row's first CTA) written by the cluster's
     __shared__ uint64_t s_bar;
@@ -499,16 +512,16 @@ __global__ void __launch_bounds__(NT, 1536 / NT) stats_kernel(TokArgs a) {
     RunEnt<SX, ENT> run;
     int k = w0 + tid;
     const uint4* p = reinterpret_cast<const uint4*>(x.p + static_cast<long long>(x.first(k)) * SX);
-    for (; k + (kStatsVec - 1) * NT < w1; k += kStatsVec * NT, p += kStatsVec * NT) {
-        uint4 v[kStatsVec];
+    for (; k + (U - 1) * NT < w1; k += U * NT, p += U * NT) {
+        uint4 v[U];
 #pragma unroll
-        for (int u = 0; u < kStatsVec; ++u) v[u] = ld_vec16(p + u * NT);
-        if (own >= k && own < k + kStatsVec * NT) {
+        for (int u = 0; u < U; ++u) v[u] = ld_vec16(p + u * NT);
+        if (own >= k && own < k + U * NT) {
 #pragma unroll
-            for (int u = 0; u < kStatsVec; ++u)
+            for (int u = 0; u < U; ++u)
                 if (k + u * NT == own) patch<SX>(v[u], at.lane, ninf_bits<SX>());
         }
-        if (k == w0 + tid && w0 + (tid | 31) + (kStatsVec - 1) * NT < w1) run.seed(v, a);
+        if (k == w0 + tid && w0 + (tid | 31) + (U - 1) * NT < w1) run.seed(v, a);
         run.add(v, a);
     }
     for (; k < w1; k += NT, p += NT) {
@@ -664,6 +677,8 @@ __device__ __forceinline__ void write_grad(const VocabRow<SX>& x, const VocabRow
     if (at.k >= k0 && at.k < k1 && (at.k - k0) % NT == tid) store_one<SX>(g, y, rg.at_y);
 }
 
+// The gradient alone, 32 KB of a row to a CTA (16 KB: 3% slower for 509 fp32 rows of 50001, 8 KB: 34%).  Rows whose gradient is
+// 0 are not read.
 template <int SX, bool ENT>
 __global__ void __launch_bounds__(kRowThreads) grad_kernel(TokArgs a) {
     const long long row = blockIdx.x / a.splits;
@@ -687,13 +702,13 @@ __global__ void __launch_bounds__(kRowThreads) grad_kernel(TokArgs a) {
     }
     const RowGrad<SX, ENT> rg(a, s, da, dh);
     write_grad<SX, ENT, false, kGradVec, kRowThreads>(x, g, k0, k1, y, s.f < 0.f || (da == 0.f && dh == 0.f), rg,
-                                         reinterpret_cast<const uint4*>(x.p + static_cast<long long>(x.first(k0)) * SX));
+                                                      reinterpret_cast<const uint4*>(x.p + static_cast<long long>(x.first(k0)) * SX));
 }
 
 // ---------------------------------------------------------------- loss and gradient in one
 // What a policy row's gradient is made with, on the way between its sum and its gradient, where the whole CTA waits: base 2
 // and the hardware's functions, a third of row_end's steps (its chain of dependent instructions, run by one warp
-// among forty, took 42 of 434 us of policy_batch's rows).  Logarithms are split from their exponents, so that their
+// among forty, took 42 of 434 us of 4096 rows of 151936).  Logarithms are split from their exponents, so that their
 // 2^-22 is absolute; what cancels has two parts.  Off by some 4e-7 relative where row_end is by 2e-7.
 struct QuickRow {
     TwoFloat old2, ref2;                                     // log-probabilities by log2(e)
@@ -748,21 +763,23 @@ __device__ __forceinline__ RowSaved quick_end(const TokArgs& a, const EntSum& es
         by_lp = binds ? 0.f : -gain;
     }
     float loss = -gain;
-    if (a.ref_lp) {
+    if (a.kl_coef != 0.f) {
         const float D2 = (pr.ref2.hi - lp.hi) + (pr.ref2.lo - lp.lo), D = kLn2 * D2;
         const float em1 = fabsf(D) < 0.0625f ? D * fmaf(D, fmaf(D, fmaf(D, fmaf(D, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f), 1.f) : ex2_approx(D2) - 1.f;
-        loss += a.kl_coef != 0.f ? a.kl_coef * (em1 - D) : 0.f * (em1 - D);
-        if (a.kl_coef != 0.f) by_lp = fmaf(-a.kl_coef, em1, by_lp);
+        loss = fmaf(a.kl_coef, em1 - D, loss);
+        by_lp = fmaf(-a.kl_coef, em1, by_lp);
     }
     s.a = pr.w * by_lp;
     s.h = -pr.w * a.ent_coef;
-    if (fabsf(loss * pr.w) < INFINITY && fabsf(s.a) < INFINITY) s.f = q * by_sum * a.inv_t * (SX == 4 ? 1.f - kLn2 * by_low : 1.f);
+    if (fabsf(loss * pr.w) < INFINITY && fabsf(s.a) < INFINITY) s.f = q * by_sum * a.inv_t * by_low_of<SX, ENT>(a, es.m, kLn2 * by_low);
     return s;
 }
 
 // A policy row's loss and gradient without reading it twice: a cluster of C CTAs keeps the row in shared memory, a span
-// each, between the sum and the gradient.  A thread copies the vectors that it will read, so that nothing but the joins
-// of the sums has to wait for anyone.
+// each, between the sum and the gradient.  A span comes by one bulk copy (copies of 16 bytes by the threads that read them:
+// 381 us where this takes 357, 4096 rows of 151936; the row read twice: 532); a thread reads the same vectors for both, so
+// that only the joins of the sums wait for others.  An SM moves as many bytes as it holds over how long it holds them: some
+// 200 KB for 9.5 us at the copy bandwidth, so what stands between copy and gradient is kept short.
 constexpr int kFusedSpan = 14000;                            // vectors of a span at most: 224,000 bytes
 constexpr int kFusedCtas = 5;                                // CTAs of 256 threads to an SM at most
 
@@ -983,31 +1000,40 @@ dspark_status_t token_args(const void* logits, const dspark_token_params_t* p, c
 
 bool misplaced(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 
-// A row is a CTA's work where there are rows enough; an SM holds six CTAs of 256 threads (five: 2% less for 4096 rows of
-// 151936, 5 to 20% more where that leaves a few rows to a second wave: 900 of them 58 us, 46 with six) or three of
-// 512, which have a row done in half the time: as many rows as they are in one wave are theirs (400 rows of 151936: 23 us,
-// 27 by 256; 509 of 50001 fp32: 22 and 20).  Fewer still are split over clusters (9 rows of 151936 in 1, 2, 4, 8 CTAs of
-// 256: 11.4, 7.9, 5.8, 4.5 us; 8 of 512: 3.9; short rows lose by it: 100 of 32000 4.1 us whole, 4.9 in halves).
-template <int NT>
+// A row is a CTA's work where there are rows enough: 456, 912 or 1824 of them are on the GPU at a time, by CTAs of 512, 256 or
+// 128 threads, and take the longer the more they are.
+//   - rows for one wave of 512 threads are theirs (400 rows of 151936: 23 us, 27 by 256 threads; 509 of 50001 fp32: 22 and 20);
+//   - rows whose last wave of 256 threads makes them an even number of waves take half as many of 128 (1024 rows of
+//     151936: 54 us, 63 by 256; 3000: 139 and 144; 2048, three waves of 256: 115 and 104; more than four: 195 and 188);
+//     up to eight of these to an SM have six vectors on their way in place of four (1024 rows: 52 us, and of 50001 fp32 34, 36, 41);
+//   - short rows too (4096 rows of 4096: 15.3 and 20.1 us; 200 of 16000: 4.8 and 4.1);
+//   - the others are by 256, six to an SM (five: 2% less for 4096 rows of 151936, 900 rows 58 us instead of 46).
+// Fewer rows still are split over clusters (9 rows of 151936 in 1, 2, 4, 8 CTAs of 256: 11.4, 7.9, 5.8, 4.5 us; 8 of 512:
+// 3.9; short rows lose by it: 100 of 32000 4.1 us whole, 4.9 in halves).
+constexpr int kWave = 152 * 6;                               // rows by 256 threads
+template <int NT, int U = 4>
 cudaError_t launch_stats_by(const TokArgs& a, int sx, bool entropy, unsigned grid, int C, cudaStream_t s) {
-    auto kern = sx == 2 ? (entropy ? stats_kernel<2, true, NT> : stats_kernel<2, false, NT>)
-                        : (entropy ? stats_kernel<4, true, NT> : stats_kernel<4, false, NT>);
+    auto kern = sx == 2 ? (entropy ? stats_kernel<2, true, NT, U> : stats_kernel<2, false, NT, U>)
+                        : (entropy ? stats_kernel<4, true, NT, U> : stats_kernel<4, false, NT, U>);
     return launch_cluster(kern, grid, NT, C, 0, s, a);
 }
 dspark_status_t launch_stats(TokArgs& a, int sx, bool entropy, const dspark_token_params_t* p) {
     const int nvec = max_vectors(p->V, sx);
     const long long rows = p->n_rows;
-    const bool wide = rows <= 456 && nvec >= 4096;
+    const bool wide = rows <= kWave / 2 && nvec >= 4096;
+    const bool thin = rows > kWave / 2 && (nvec <= kShortRow || (rows <= 4 * kWave && (rows + kWave - 1) / kWave % 2 == 0));
     int C = 1;
     a.log_c = 0;
-    while (C < kMaxCluster && nvec >= C * 4096 && rows * 2 * C <= (wide ? 456 : 640)) {
+    while (C < kMaxCluster && nvec >= C * 4096 && rows * 2 * C <= (wide ? kWave / 2 : 640)) {
         C *= 2;
         ++a.log_c;
     }
     const unsigned grid = static_cast<unsigned>(p->n_rows) * C;
     const cudaStream_t s = static_cast<cudaStream_t>(p->stream);
     const cudaError_t e = wide ? launch_stats_by<512>(a, sx, entropy, grid, C, s)
-                          : rows > 456 && nvec <= kShortRow ? launch_stats_by<128>(a, sx, entropy, grid, C, s) : launch_stats_by<256>(a, sx, entropy, grid, C, s);
+                          : thin ? (rows > kWave && rows <= 1216 ? launch_stats_by<128, 6>(a, sx, entropy, grid, C, s)
+                                                                 : launch_stats_by<128>(a, sx, entropy, grid, C, s))
+                                 : launch_stats_by<256>(a, sx, entropy, grid, C, s);
     return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
@@ -1021,7 +1047,9 @@ dspark_status_t launch_grad(TokArgs& a, int sx, bool entropy, const dspark_token
     return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
-// CTAs of a row whose span stays in shared memory; 0 when the row is too long for eight of them.
+// CTAs of a row whose span stays in shared memory; 0 when the row is too long for eight of them.  Of the splits that fit, the
+// one by which an SM holds the most bytes (4096 rows of 151936 bf16 in 4, 5, 6, 7, 8: 407, 443, 411, 392, 409 us for 152,
+// 182, 203, 217, 190 KB; 2048 fp32 rows of it in eighths of 76 KB: 412 us, read twice 525); few rows in more.
 int fused_split(int nvec, long long rows) {
     int C = 1;
     while (C < kMaxCluster && nvec >= C * 512 && rows * 2 * C <= 320) C *= 2;

@@ -163,6 +163,24 @@ def test_clip_shapes_and_missing_gradients(bd):  # noqa: F811
     assert abs(float(g[3][0, 0]) - 28 ** -0.5) < 1e-6
 
 
+def test_clip_refuses_tables(bd):  # noqa: F811
+    a, b = torch.ones(4, device="cuda"), torch.ones(4, device="cuda")
+    for grads, out in (([a, a], None), ([a, b], [b, a]), ([a], [torch.ones(5, device="cuda")]), ([a], [torch.ones(4)]), ([a], [None]),
+                       ([a], [torch.ones(4, device="cuda", dtype=torch.bfloat16)]), ([torch.ones(4, 4, device="cuda").t()[:2]], None),
+                       ([torch.ones(8, device="cuda")[::2]], None), ([a, torch.ones(4)], None)):
+        with pytest.raises(ValueError):
+            bd.GradTable(grads, out)
+    with pytest.raises(TypeError):
+        bd.GradTable([a.half()])
+    t = bd.GradTable([a])
+    norm, status = torch.zeros(1, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(bd.dspark_clip_workspace_bytes(t), dtype=torch.uint8, device="cuda")
+    for bad in (dict(workspace=ws[1:]), dict(workspace=ws[:-1]), dict(norm=torch.zeros(2, device="cuda")), dict(status=norm), dict(max_norm=-1.0)):
+        given = dict(max_norm=1.0, norm=norm, status=status, workspace=ws) | bad
+        with pytest.raises((ValueError, RuntimeError)):
+            bd.dspark_clip_grads(t, given.pop("max_norm"), **given)
+
+
 def test_clip_grads_of_parameters(bd):  # noqa: F811
     from sample_verify_epilogue_gb300.training import clip_grads_
     p = [torch.nn.Parameter(torch.zeros(4, 4, device="cuda")) for _ in range(3)]

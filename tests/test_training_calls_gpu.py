@@ -279,6 +279,23 @@ def test_rows_that_begin_with_a_mask(bd, value, dtype):  # noqa: F811
             check_policy(c, policy_call(bd, c, dtype, 1.0, 0.0, ent, form, use_ref=False), dtype, 1.0, 0.0, ent, use_ref=False)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("size", [300.0, 3e4, 1e6, 1e8, 1e30])
+def test_large_logits(bd, size, dtype):  # noqa: F811
+    """Logits whose neighbours in the type are far apart: a few of them have all the mass, or one; at exponents around and
+    past four million, where no whole one is taken, too."""
+    rng = np.random.default_rng(int(np.log10(size)))
+    rows, V = 8, 5003
+    x = R.rounded(size * (1 + rng.uniform(-0.01, 0.01, (rows, V))) * rng.choice([-1, 1], rows)[:, None], dtype)
+    x[4:, ::7] = x[4:].max(1, keepdims=True)                 # many ties for the largest
+    y = rng.integers(0, V, rows)
+    y[5] = 7
+    y[6:] = np.argmax(x[6:], 1)
+    up = rng.normal(0, 1, (2, rows))
+    check_logprobs(x, y, dtype, 1.0, logprobs_call(bd, x, y, dtype, up=up), up)
+    check_logprobs(x, y, dtype, 1.0, logprobs_call(bd, x, y, dtype, entropy=False, up=(up[0], None)), (up[0], None))
+
+
 @pytest.mark.parametrize("T", [1e-3, 0.05, 30.0, 1e4])
 def test_temperatures(bd, T):  # noqa: F811
     rng = np.random.default_rng(7)

@@ -280,6 +280,19 @@ def test_policy_loss_status(bd, form):  # noqa: F811
                  bad={part.index(r): s for r, s in bad.items()})
 
 
+@pytest.mark.parametrize("form", ["fused", "two_call"])
+def test_policy_reference_without_a_term(bd, form):  # noqa: F811
+    """A reference that is asked about but has no weight in the loss: what it holds changes nothing but the KL."""
+    c = policy_batch(np.random.default_rng(4), 6, 2003, "fp32", 1.0, special=False)
+    plain = policy_call(bd, c, "fp32", 1.0, 0.0, 0.0, form)
+    c["ref"][:3] = np.inf, -np.inf, np.nan
+    got = policy_call(bd, c, "fp32", 1.0, 0.0, 0.0, form)
+    assert not got["status"].any()
+    for k in ("loss", "logprobs", "grad"):
+        assert np.array_equal(got[k], plain[k])
+    assert np.isposinf(got["kl"][:2]).all() and np.array_equal(got["kl"][3:], plain["kl"][3:])
+
+
 def test_policy_ratio_at_a_border_is_not_clipped(bd):  # noqa: F811
     """rho = 1 with clip 0 on both sides: the gradient of rho A, as at the first step on a rollout."""
     x = np.zeros((2, 4))
