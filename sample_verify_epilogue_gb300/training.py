@@ -5,6 +5,10 @@ its backward call in their backward pass, each on torch's current stream at that
 alone: old and reference log-probabilities, advantages and weights are constants.  A training loop that knows its
 weights beforehand gets loss and gradient together from ``binding.dspark_policy_loss(..., grad=...)`` and
 ``binding.dspark_preference_loss(..., grad=...)`` instead.
+
+Rows have to be evenly spaced: for logits [B, T, V] whose position t predicts token t + 1, pass all of them with the tokens
+moved up by one and -1 at the last position, rather than ``logits[:, :-1]``.  A step is captured into a CUDA graph with
+``torch.autograd.grad``, or ``backward`` while no eager graph of the same leaves is alive.
 """
 from __future__ import annotations
 
