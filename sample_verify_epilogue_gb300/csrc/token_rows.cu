@@ -16,6 +16,7 @@
 // bonus).  Where a CTA has little to read its latencies bound it: token, first vectors, joins, the row's end.
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 #include <limits>
 
 #include "vocab_rows.cuh"
@@ -29,10 +30,12 @@ constexpr int kGradVec = 4;                                  // vectors a thread
 constexpr int kShortRow = 2048;                              // vectors of a row that 128 threads take, where rows are many
 constexpr int kGradVecs = 2048;                              // vectors of a row that a CTA of the gradient takes
 constexpr float kLn2 = 0.693147180559945f;
-// what a sum of the exponential unit's results lacks on average, relative: added to its logarithm.  Single results lack
-// 5.06e-8 (2^20 arguments between whole exponents: from 9e-8 too large to 1.4e-7 too small); rows of 32000 and 151936
-// normal logits at temperatures of 1 and 0.7 lacked 2.2e-8 to 5.5e-8.
-constexpr float kEx2Lacks = 3.5e-8f;
+// what a sum of the exponential unit's results lacks on average, relative: added to its logarithm.  (2^20 arguments between whole
+// exponents: 5.06e-8, from 9e-8 too large to 1.4e-7 too small; sums of 262144 normal logits over 0.7, 1 and 1.3, by a
+// reference above them: 4.6e-8 to 5.1e-8.)
+constexpr float kEx2Lacks = 5.06e-8f;
+
+constexpr float kAbove = 5.f;
 
 enum TokenOp : int { kScore, kPolicy, kPreference };
 
@@ -48,7 +51,9 @@ static_assert(sizeof(RowSaved) == 4 * DSPARK_SAVED_FLOATS, "the header's size");
 
 struct TokArgs {
     int V, op;
-    float c, c_low, inv_c, inv_t;                            // log2(e) / T in two parts, 1 / c, 1 / T
+    float c, c_low, inv_c, inv_t;                            // log2(e) / T and what it lacks of it, 1 / c, 1 / T
+    float above;                                             // kAbove / c, a distance of logits
+    float c_head, c_tail;                                    // log2(e) / T in two positive parts, 16 bits and the rest
     long long x_stride, g_stride;
     const void* x;
     void* g;
@@ -69,12 +74,14 @@ struct TokArgs {
     int n_up;                                                // (preference) entries of up
     int log_c, splits;                                       // log2 of the CTAs of a row (stats); CTAs of a row (gradient, fused)
     int span;                                                // vectors of each (fused)
+    float most;                                              // a sum of vectors from which on the reference is raised
     unsigned zero;                                           // 0
 };
 
 // A sum of exponentials e by ExpRef(m), and the sum w of e times its exponent (base 2).  m is about the largest logits'
-// size, a power of two above those it was taken from: exponents between -1 and 1 lose their last bits in the exponential
-// unit (its results are 2e-8 larger there).  No e is larger than 64.
+// size, kAbove powers of two above those it was taken from, so that few that come later are larger: exponents above -1 lose their
+// last bits in the exponential unit (sums by the largest of a thousand logits lacked 5e-9 to 4e-8 of what is below, by one
+// above all of them 5e-8).
 struct EntSum {
     float m, sum, w;
 };
@@ -111,16 +118,17 @@ __device__ __forceinline__ EntSum lanes_join(EntSum a, float c) {
 
 // A thread's sum while it streams.
 //
-// Vectors are added by the reference that is there, whatever their maximum: where that makes a sum of 64 or more (the
-// first vectors, a maximum far above those before) they are added again by the maximum of both.  (64: an entropy is a
-// difference of what the exponents weigh and the sum's logarithm, which should not be far from 0 themselves.)  The
-// reference's whole exponent r makes the exponent's one rounding that of the fma; -inf stands for none.  (With the running
+// Vectors are added by the reference that is there, whatever their maximum: where that makes a sum of a.most or more
+// (the first vectors, a maximum above the reference) they are added again by a reference above it.  The reference's whole exponent r
+// makes the exponent's one rounding that of the fma; -inf stands for none.  (With the running
 // maximum of every batch of vectors in the way: 191 us where this takes 177, 4096 rows of 151936 with the entropy.)
 //
 // A row's log-probability may be off by 1e-7 at random, but not to one side: sums of a thousand log ratios follow.  So
 // the vectors' sum joins the rest in a pair of floats (added one by one, small terms are lost more often than gained:
-// 2e-8 of a row of 151936), and log2(e) / T is taken in two parts (rounded to one it is off by up to 2^-24 of the distance
-// between logits): here, or with the entropy, whose sum gives the mean logit, in row_end.
+// 2e-8 of a row of 151936), and log2(e) / T is not rounded to one float (which makes every log-probability off by up to
+// 2^-24 of the distance between logits): it has a head of 16 bits, whose product with a bf16 is exact, and a tail whose product is
+// large beside an exponent's last bit (of 24 bits and the rest the rest would be rounded away, the same way in every row); with
+// the entropy, whose sum gives the mean logit, what the one float lacks is made up for in row_end.
 template <int SX, bool ENT>
 struct RunEnt {
     static constexpr int VE = 16 / SX;
@@ -143,7 +151,7 @@ struct RunEnt {
     // (a thread's own: 4096 policy rows of 151936 389 -> 435 us).
     template <int U>
     __device__ __forceinline__ void seed(const uint4 (&v)[U], const TokArgs& a) {
-        const float to = key_to_f(__reduce_max_sync(0xffffffffu, fkey(vecs_max<SX>(v)))) + a.inv_c;
+        const float to = key_to_f(__reduce_max_sync(0xffffffffu, fkey(vecs_max<SX>(v)))) + a.above;
         const ExpRef ref(to, a.c);
         if (!ref.whole) return;
         m = to;
@@ -161,7 +169,7 @@ struct RunEnt {
             for (int u = 0; u < U; ++u) v[u] = p[u * stride];
             s = sum_of(v, a, ws);
         }
-        if (!(s < 64.f)) {
+        if (!(s < a.most)) {
 #pragma unroll 1
             for (int u = 0; u < U; ++u) {
                 uint4 v[1] = {p[u * stride]};
@@ -181,12 +189,12 @@ struct RunEnt {
     template <int U>
     __device__ __forceinline__ void add(uint4 (&v)[U], const TokArgs& a) {
         float ws, s = sum_of(v, a, ws);
-        if (!(s < 64.f)) {
+        if (!(s < a.most)) {
             // (a zero that the compiler does not know: else it keeps the first sum's conversions for the second, in registers
             // that are not there)
 #pragma unroll
             for (int u = 0; u < U; ++u) v[u] = make_uint4(v[u].x ^ a.zero, v[u].y ^ a.zero, v[u].z ^ a.zero, v[u].w ^ a.zero);
-            const float to = fmaxf(m, vecs_max<SX>(v) + a.inv_c);
+            const float to = fmaxf(m, vecs_max<SX>(v) + a.above);
             const ExpRef ref(to, a.c);
             if (!ref.whole) {
 #pragma unroll 1
@@ -208,7 +216,8 @@ struct RunEnt {
 
     template <int U>
     __device__ __forceinline__ float sum_of(const uint4 (&v)[U], const TokArgs& a, float& ws) const {
-        const unsigned long long c2 = pack2(a.c, a.c), l2 = pack2(a.c_low, a.c_low), r2 = pack2(-r, -r);
+        const float c = ENT ? a.c : a.c_head;
+        const unsigned long long c2 = pack2(c, c), l2 = pack2(a.c_tail, a.c_tail), r2 = pack2(-r, -r);
         unsigned long long acc[2] = {0ull, 0ull}, accw = 0ull;
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -337,7 +346,7 @@ struct Odds {
 };
 
 // What the gradient's exponentials, relative to those of the sum, have to be multiplied with for c_low (as much as 2% for
-// logits of a million T): fp32's gradient takes it into its exponents, bf16's does not; a sum with the entropy does not.
+// logits of a million T): fp32's gradient has all of log2(e) / T in its exponents, bf16's does not; a sum with the entropy does not.
 // by_low is what it adds to the sum's logarithm; without the entropy the largest logit stands for all that count.  (H, a
 // difference of two that have it or have it not, is the same.)
 template <int SX, bool ENT>
@@ -585,11 +594,11 @@ template <int SX, bool ENT>
 struct RowGrad {
     static constexpr int VE = 16 / SX;
     ExpRef ref;
-    float c_low, a0, a1, at_y;
+    float head, tail, a0, a1, at_y;                          // of log2(e) / T
     uint32_t least;
 
     __device__ __forceinline__ RowGrad(const TokArgs& a, const RowSaved& s, float da, float dh)
-        : ref(s.m, a.c), c_low(a.c_low), a0(-s.f * fmaf(dh, s.level, da)), a1(-s.f * dh * kLn2), at_y(da * s.q - dh * s.py) {
+        : ref(s.m, a.c), head(SX == 4 ? a.c_head : a.c), tail(a.c_tail), a0(-s.f * fmaf(dh, s.level, da)), a1(-s.f * dh * kLn2), at_y(da * s.q - dh * s.py) {
         if (!ENT) {
             a0 = -s.f * da;
             at_y = da * s.q;
@@ -603,7 +612,7 @@ struct RowGrad {
     // by a reference with a whole exponent
     __device__ __forceinline__ uint4 of(const uint4& v) const {
         float f[VE];
-        const unsigned long long c2 = pack2(ref.c, ref.c), l2 = pack2(c_low, c_low), r2 = pack2(-ref.r, -ref.r);
+        const unsigned long long c2 = pack2(head, head), l2 = pack2(tail, tail), r2 = pack2(-ref.r, -ref.r);
 #pragma unroll
         for (int h = 0; h < VE / 2; ++h) {
             unsigned long long x;
@@ -976,8 +985,7 @@ dspark_status_t token_args(const void* logits, const dspark_token_params_t* p, c
     if (p->n_rows < 1 || p->n_rows > DSPARK_MAX_ROWS || p->V < 1 || p->V > DSPARK_MAX_V) return DSPARK_ERR_INVALID_ARG;
     if (p->logits_dtype != DSPARK_BF16 && p->logits_dtype != DSPARK_FP32) return DSPARK_ERR_INVALID_ARG;
     const double exact = 1.44269504088896340736 / p->temperature;
-    float c = static_cast<float>(exact);
-    if (c > exact) c = std::nextafter(c, 0.f);               // below, so that c_low > 0 and -inf times both is -inf
+    const float c = static_cast<float>(exact);
     const float inv_t = 1.f / p->temperature;
     if (!(p->temperature > 0.f) || !(c > 0.f) || !(c < INFINITY) || !(inv_t < INFINITY)) return DSPARK_ERR_INVALID_ARG;
     *sx = p->logits_dtype == DSPARK_BF16 ? 2 : 4;
@@ -986,9 +994,17 @@ dspark_status_t token_args(const void* logits, const dspark_token_params_t* p, c
     if (grad == logits && p->grad_stride != p->logits_stride) return DSPARK_ERR_INVALID_ARG;
     a->V = p->V;
     a->c = c;
-    a->c_low = std::max(static_cast<float>(exact - c), std::numeric_limits<float>::denorm_min());
+    a->c_low = static_cast<float>(exact - c);
+    float head = c > exact ? std::nextafter(c, 0.f) : c;
+    uint32_t bits;
+    std::memcpy(&bits, &head, sizeof bits);
+    bits &= 0xFFFFFF00u;
+    std::memcpy(&head, &bits, sizeof bits);
+    a->c_head = head;                                        // the tail is not 0, so that -inf times both is -inf
+    a->c_tail = std::max(static_cast<float>(exact - head), std::numeric_limits<float>::denorm_min());
     a->inv_t = inv_t;
     a->inv_c = std::min(1.f / c, std::numeric_limits<float>::max());
+    a->above = std::min(kAbove / c, std::numeric_limits<float>::max());
     a->x = logits;
     a->x_stride = p->logits_stride;
     a->g = const_cast<void*>(grad);
@@ -1028,6 +1044,7 @@ dspark_status_t launch_stats(TokArgs& a, int sx, bool entropy, const dspark_toke
         C *= 2;
         ++a.log_c;
     }
+    a.most = 1.f;
     const unsigned grid = static_cast<unsigned>(p->n_rows) * C;
     const cudaStream_t s = static_cast<cudaStream_t>(p->stream);
     const cudaError_t e = wide ? launch_stats_by<512>(a, sx, entropy, grid, C, s)
@@ -1080,6 +1097,7 @@ cudaError_t launch_kept_by(TokArgs& a, int sx, bool entropy, const dspark_token_
 dspark_status_t launch_kept(TokArgs& a, int sx, bool entropy, const dspark_token_params_t* p, int C) {
     a.splits = C;
     a.span = (max_vectors(p->V, sx) + C - 1) / C;
+    a.most = 64.f;                                           // (1: 387 us for 377, 4096 rows of 151936; no row's loss is a long sum)
     const cudaError_t e = C == 1 && a.span <= kShortRow ? launch_kept_by<128>(a, sx, entropy, p) : launch_kept_by<256>(a, sx, entropy, p);
     return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }

@@ -9,15 +9,15 @@ exponential's; a row's sum of exponentials R has tests/_rows.sum_bound relative 
   q, p_y              relative p_y ed + 8 u, q ed + 8 u
   H                   the sum of its terms' errors (see entropy_bound)
   p_v                 relative es + EX2 + 3 u |s_v - m| + q's + 8 u
-  flushing            exponentials below 2^-126 are 0.  They are by a whole exponent r = ceil(m c + 1) < m c + 2, m the
-                      largest logit: what is below 2^-124 of the largest may be 0
+  flushing            exponentials below 2^-126 are 0.  They are by a whole exponent r = ceil(m c + 5) < m c + 6, m the
+                      largest logit: what is below 2^-120 of the largest may be 0
 """
 import numpy as np
 
 from tests import _rows as R
 
 U, EX2 = R.U, R.EX2
-FLUSH = 2.0 ** -124
+FLUSH = 2.0 ** -120
 
 
 def row_errors(r, V):
