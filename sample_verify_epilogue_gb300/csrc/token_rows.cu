@@ -683,7 +683,8 @@ __device__ __forceinline__ void write_grad(const VocabRow<SX>& x, const VocabRow
         }
     }
     const Place<SX> at(x, y);
-    if (at.k >= k0 && at.k < k1 && (at.k - k0) % NT == tid) store_one<SX>(g, y, rg.at_y);
+    // (a token that changed after the call that saved the row may be out of range)
+    if (y >= 0 && y < x.V && at.k >= k0 && at.k < k1 && (at.k - k0) % NT == tid) store_one<SX>(g, y, rg.at_y);
 }
 
 // The gradient alone, 32 KB of a row to a CTA (16 KB: 3% slower for 509 fp32 rows of 50001, 8 KB: 34%).  Rows whose gradient is

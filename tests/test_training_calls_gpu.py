@@ -412,3 +412,27 @@ def test_results_come_again(bd):  # noqa: F811
         again = policy_call(bd, c, "bf16", 1.0, 0.1, 0.01, "fused"), preference_call(bd, p, "bf16", "fused")
         for a, b in zip(first, again):
             assert all(np.array_equal(a[k], b[k]) for k in a)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_tokens_that_change_before_the_backward_call(bd, dtype):  # noqa: F811
+    """A backward call whose tokens are out of range by then writes nothing beside its rows."""
+    V, kind = 1003, torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(6, V, generator=g, device="cuda").to(kind)
+    tokens = torch.tensor([5, 1, 2, 3, 4, 5], dtype=torch.int32, device="cuda")
+    saved, ones = torch.empty(6, 8, device="cuda"), full(6, 1.0)
+    bd.dspark_token_logprobs(x, tokens, logprobs=full(6, 9.0), entropy=full(6, 9.0), row_status=full(6, -1, torch.int32), saved=saved)
+    late = torch.tensor([5, V, -1, V + 3, -7, 5], dtype=torch.int32, device="cuda")
+
+    def run(t):
+        held = torch.full((8, V + 9), 77.0, dtype=kind, device="cuda")
+        grad = held[1:7, 3:3 + V]                            # another alignment than the logits'
+        bd.dspark_token_logprobs_backward(x, t, saved=saved, grad=grad, grad_logprobs=ones, grad_entropy=ones)
+        rest = held.clone()
+        rest[1:7, 3:3 + V] = 77.0
+        assert bool((rest == 77.0).all())
+        return grad
+
+    first, then = run(tokens), run(late)
+    assert torch.equal(first[0], then[0]) and torch.equal(first[5], then[5]) and bool(torch.isfinite(then).all())
