@@ -891,7 +891,9 @@ struct PairArgs {
 };
 
 // A CTA to a pair, half of its warps to a sequence: the sums in pairs of floats (they cancel), the loss, and each row's
-// dL/dlog p.  4 us, most of it its launch and three trips to L2 in a row.
+// dL/dlog p.  4 us, most of it its launch and three trips to L2 in a row.  More pairs than fit the GPU at once go to its CTAs in
+// runs, so that the offsets before a pair are looked through once for a run (for each pair: 2040 us for 65536, 160 in runs).
+constexpr int kPairCtas = 152 * 8;
 struct __align__(16) SeqSum {
     TwoFloat sum;
     int count, status;
@@ -899,25 +901,9 @@ struct __align__(16) SeqSum {
 __device__ __forceinline__ TwoFloat add_finite(const TwoFloat& a, const TwoFloat& b) {   // infinities and NaN have no low part
     return fabsf(a.hi) < INFINITY && fabsf(b.hi) < INFINITY ? a + b : TwoFloat{a.hi + b.hi, 0.f};
 }
-__global__ void __launch_bounds__(kRowThreads) pair_kernel(PairArgs a) {
-    __shared__ SeqSum s_part[kRowWarps];
-    __shared__ float s_coef[2];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, p = blockIdx.x;
+__device__ __forceinline__ void one_pair(const PairArgs& a, int p, int lo, int mid, int hi, SeqSum* s_part, float* s_coef) {
     constexpr int kHalf = kRowThreads / 2;
-    pdl_wait();
-    // the offsets up to this pair's last ascend and stay inside the rows
-    const int lo = a.offsets[2 * p], mid = a.offsets[2 * p + 1], hi = a.offsets[2 * p + 2];
-    const int first = a.offsets[0];
-    bool bad = first < 0 || hi > a.R;
-    for (int k = tid; k < 2 * p + 2; k += kRowThreads) bad = bad || a.offsets[k] > a.offsets[k + 1];
-    if (__syncthreads_or(bad)) {
-        if (tid == 0) {
-            a.loss[p] = NAN;
-            if (a.rewards) a.rewards[2 * p] = a.rewards[2 * p + 1] = NAN;
-            a.pair_status[p] = DSPARK_ROW_BAD_PARAMS;
-        }
-        return;
-    }
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     SeqSum q{TwoFloat{0.f, 0.f}, 0, 0};
     const int half = tid / kHalf;
     for (int r = (half ? mid : lo) + tid % kHalf; r < (half ? hi : mid); r += kHalf) {
@@ -977,6 +963,35 @@ __global__ void __launch_bounds__(kRowThreads) pair_kernel(PairArgs a) {
     for (int r = lo + tid; r < hi; r += kRowThreads) {
         a.saved[r].a = s_coef[r >= mid];
         a.saved[r].pair = p;
+    }
+}
+__global__ void __launch_bounds__(kRowThreads) pair_kernel(PairArgs a) {
+    __shared__ SeqSum s_part[kRowWarps];
+    __shared__ float s_coef[2];
+    const int tid = threadIdx.x;
+    pdl_wait();
+    const int p0 = static_cast<int>(static_cast<long long>(a.P) * blockIdx.x / gridDim.x);
+    const int p1 = static_cast<int>(static_cast<long long>(a.P) * (blockIdx.x + 1) / gridDim.x);
+    // the offsets up to a pair's last ascend and stay inside the rows
+    int lo = a.offsets[2 * p0], mid = a.offsets[2 * p0 + 1], hi = a.offsets[2 * p0 + 2];
+    bool bad = a.offsets[0] < 0;
+#pragma unroll 4
+    for (int k = tid; k < 2 * p0; k += kRowThreads) bad |= a.offsets[k] > a.offsets[k + 1];
+    bad = __syncthreads_or(bad);
+    for (int p = p0; p < p1; ++p) {
+        if (p > p0) {
+            lo = hi;
+            mid = a.offsets[2 * p + 1];
+            hi = a.offsets[2 * p + 2];
+        }
+        bad = bad || lo > mid || mid > hi || hi > a.R;
+        if (!bad) {
+            one_pair(a, p, lo, mid, hi, s_part, s_coef);
+        } else if (tid == 0) {
+            a.loss[p] = NAN;
+            if (a.rewards) a.rewards[2 * p] = a.rewards[2 * p + 1] = NAN;
+            a.pair_status[p] = DSPARK_ROW_BAD_PARAMS;
+        }
     }
 }
 
@@ -1204,7 +1219,7 @@ dspark_status_t dspark_preference_loss(const void* logits, const dspark_preferen
     PairArgs b{params->n_rows, pref->n_pairs, pref->mean, pref->beta, pref->margin, pref->label_smoothing, pref->row_offsets,
                params->tokens, pref->ref_logprobs, pref->weights, params->row_status, out_loss, out_rewards,
                pair_status, a.saved};
-    if (launch_cluster(pair_kernel, static_cast<unsigned>(pref->n_pairs), kRowThreads, 1, 0,
+    if (launch_cluster(pair_kernel, static_cast<unsigned>(std::min(pref->n_pairs, kPairCtas)), kRowThreads, 1, 0,
                        static_cast<cudaStream_t>(params->stream), b) != cudaSuccess)
         return DSPARK_ERR_CUDA;
     return out_grad ? launch_grad(a, sx, false, params) : DSPARK_OK;

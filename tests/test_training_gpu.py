@@ -419,6 +419,19 @@ def test_preference_loss_many_pairs(bd):  # noqa: F811
     check_preference(c, preference_call(bd, c, "fp32", "fused"), "fp32")
 
 
+@pytest.mark.parametrize("at", [None, 1, 2900, 2901, 5999, 6000])
+def test_preference_loss_runs_of_pairs(bd, at):  # noqa: F811
+    """More pairs than CTAs, which take them in runs; an offset that descends ends a run's good pairs and all later ones."""
+    P = 3000
+    c = preference_batch(np.random.default_rng(13), tuple(i % 3 for i in range(2 * P)), 11, "fp32")
+    bad = {}
+    if at is not None:
+        c["off"][at] = -1 if at < 2 else c["off"][at - 1] - 1
+        bad = {p: bd.ROW_BAD_PARAMS for p in range(P) if (np.diff(c["off"][:2 * p + 3]) < 0).any()}
+        assert len(bad) == P - (at - 1) // 2
+    check_preference(c, preference_call(bd, c, "fp32", "fused"), "fp32", bad_pairs=bad)
+
+
 def test_preference_loss_status(bd):  # noqa: F811
     """Bad rows spoil their own pair; a margin that is no number too."""
     c = preference_batch(np.random.default_rng(11), (4,) * 12, 1003, "fp32", tail=3)
