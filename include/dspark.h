@@ -421,8 +421,9 @@ dspark_status_t dspark_distill_backward(const void* student, const dspark_teache
  * Training on decoded tokens: the log-probability of one token of every row, the losses made of it
  * (of a policy from the advantages of its own tokens, of a preference between two answers) and the
  * clipping of the gradients that come of them.  As above: no allocation, no state between calls, safe to
- * capture and to call from several host threads.  Each call is one launch, the gradient of a loss one
- * more, dspark_preference_loss one more, dspark_clip_grads two.
+ * capture and to call from several host threads.  Each call is one launch; dspark_preference_loss is two, and
+ * one more with a gradient; dspark_policy_loss is two with a gradient of rows too long for eight SMs' shared memory;
+ * dspark_clip_grads is two, for every 1000 gradients.
  * ------------------------------------------------------------------------------------------ */
 
 typedef struct {

@@ -736,21 +736,25 @@ class GradTable:
         if not pairs:
             raise ValueError("no gradients")
         self.device = _device_of("a gradient", pairs[0][0])
-        self.tensors, fields, seen, written = pairs, [], set(), set()
+        self.tensors, fields, held = pairs, [], []
         for g, o in pairs:
             if g.get_device() != self.device or not g.is_contiguous():
                 raise ValueError("the gradients must be contiguous CUDA tensors of one device")
-            if g.numel() and g.data_ptr() in seen:
-                raise ValueError("a gradient appears twice")
-            seen.add(g.data_ptr())
             if o is not g and (o is None or o.shape != g.shape or o.get_device() != self.device or not o.is_contiguous() or
                                (o.dtype is not g.dtype and o.dtype is not T.f32)):
                 raise ValueError("an output must be contiguous, of its gradient's shape and device, and of its dtype or fp32")
-            if o is not g and o.numel():
-                written.add(o.data_ptr())
-            fields.append(_grad(g.data_ptr(), o.data_ptr(), g.numel(), _dtype_of(g), _dtype_of(o)))
-        if written & seen:
-            raise ValueError("an output is a gradient of the list")
+            n = g.numel()
+            if n:
+                held.append((g.data_ptr(), n * g.element_size()))
+                if o is not g:
+                    held.append((o.data_ptr(), n * o.element_size()))
+            fields.append(_grad(g.data_ptr(), o.data_ptr(), n, _dtype_of(g), _dtype_of(o)))
+        held.sort()
+        end = 0
+        for at, size in held:
+            if at < end:
+                raise ValueError("gradients or outputs overlap, or one appears twice")
+            end = at + size
         if len(fields) > DSPARK_MAX_GRADS:
             raise ValueError(f"more than {DSPARK_MAX_GRADS} gradients")
         self.packed = b"".join(fields)

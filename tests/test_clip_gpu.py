@@ -243,3 +243,19 @@ def test_clip_beyond_32_bits(bd):  # noqa: F811
     norm, status = clip_call(bd, [g], 8.5)
     assert status == 0 and abs(norm - 85) < 1e-4
     assert [float(g[k]) for k in (-1, -2, 0, (1 << 31) + 1)] == [float(torch.tensor(v / 10).bfloat16()) for v in (3, 4, 12, 84)]
+
+
+def test_clip_refuses_overlaps(bd):  # noqa: F811
+    """Memory that two entries share is refused, whole or in part; neighbours and empty gradients are not."""
+    flat, wide = torch.ones(64, device="cuda"), torch.zeros(64, device="cuda")
+    half = torch.ones(16, device="cuda", dtype=torch.bfloat16)
+    for grads, out in (([flat[:8], flat[7:9]], None), ([flat, flat[63:]], None), ([flat[8:16], flat[:32]], None),
+                       ([flat[:8], flat[8:16]], [wide[:8], wide[7:15]]), ([flat[:8], flat[8:16]], [wide[:8], wide[:8]]),
+                       ([flat[:8]], [flat[4:12]]), ([half, flat[:8]], [flat[4:20], wide[:8]])):
+        with pytest.raises(ValueError, match="overlap"):
+            bd.GradTable(grads, out)
+    for grads, out in (([flat[8:16], flat[:8], flat[8:8], flat[16:]], None), ([flat[8:8], flat[8:16]], None),
+                       ([half, flat[:8]], [wide[:16], wide[16:24]])):
+        assert len(bd.GradTable(grads, out)) == len(grads)
+    norm, status = clip_call(bd, [flat[8:16], flat[:8], flat[8:8], flat[16:]], 2.0)
+    assert status == 0 and norm == 8.0 and bool((flat == 0.25).all())
