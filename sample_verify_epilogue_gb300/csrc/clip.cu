@@ -35,9 +35,15 @@ struct ClipItem {
     unsigned short bf16, wide;                               // the gradient is bf16; out is fp32 all the same
 };
 
+// A share's sum of squares: (hi + lo) 2^(180 kind) for kind 0 and 1, 2^-160 for -1.
+struct __align__(16) Share {
+    float hi, lo;
+    int kind, pad;
+};
+
 template <int N>
 struct ClipList {
-    double* shares;                                          // [all shares]
+    Share* shares;                                           // [all shares]
     float* norm;
     int* status;
     float max_norm;
@@ -168,33 +174,74 @@ __global__ void __launch_bounds__(kClipThreads, kNormCtas) norm_kernel(const __g
     __shared__ TwoFloat s_sum[kClipWarps];
     pdl_wait();
     TwoFloat sum{0.f, 0.f};
-    double back = 1.0;
+    int kind = 0;
     float scale = 1.f;
 #pragma unroll 1
     for (;;) {
         bool any;
         sum = share_sum(a, scale, s_sum, &any);              // the same in every thread
-        if (scale != 1.f) break;
+        if (kind != 0) break;
         if (!(sum.hi < INFINITY)) {
             scale = 0x1p-90f;
-            back = 0x1p180;
+            kind = 1;
         } else if (any && sum.hi < 0x1p-90f) {
             scale = 0x1p80f;
-            back = 0x1p-160;
+            kind = -1;
         } else {
             break;
         }
     }
-    if (threadIdx.x == 0) a.shares[blockIdx.x] = (static_cast<double>(sum.hi) + static_cast<double>(sum.hi < INFINITY ? sum.lo : 0.f)) * back;
+    if (threadIdx.x == 0) a.shares[blockIdx.x] = Share{sum.hi, sum.hi < INFINITY ? sum.lo : 0.f, kind, 0};
 }
 
-// sqrt(sum) by a float and a step of Newton's (a thread's 64-bit root and quotient take 2 us): relative 2^-24
-__device__ __forceinline__ float norm_of(double sum) {
-    if (!(sum > 0.0 && sum < static_cast<double>(INFINITY))) return static_cast<float>(sum);
-    const int e = (((__double2hiint(sum) >> 20) & 0x7ff) - 1023) & ~1;
-    const double m = sum * __hiloint2double((1023 - e) << 20, 0);   // in [1, 4)
-    const float hi = static_cast<float>(m), lo = static_cast<float>(m - static_cast<double>(hi)), r = sqrtf(hi);
-    return ldexpf(fmaf(0.5f / r, fmaf(-r, r, hi) + lo, r), e / 2);
+// sqrt(sum 2^e), e even, by a float's root and a step of Newton's: relative 2^-24
+__device__ __forceinline__ float norm_of(TwoFloat sum, int e) {
+    if (!(sum.hi > 0.f && sum.hi < INFINITY)) return sum.hi;
+    if (sum.hi < 0x1p-64f) {
+        sum = TwoFloat{sum.hi * 0x1p64f, sum.lo * 0x1p64f};
+        e -= 64;
+    }
+    const int x = ((__float_as_int(sum.hi) >> 23) - 127) & ~1;
+    const float by = __int_as_float((127 - x) << 23), hi = sum.hi * by, lo = sum.lo * by, r = sqrtf(hi);   // hi in [1, 4)
+    return ldexpf(fmaf(0.5f / r, fmaf(-r, r, hi) + lo, r), (x + e) / 2);
+}
+
+// The norm from all shares, the same in every thread of every CTA.  In pairs of floats: the 64-bit sums of 760 CTAs, two
+// lanes a cycle, took SUMS us.
+struct ShareSum {
+    TwoFloat sum;
+    unsigned kinds;                                          // bits: some are of kind 1, -1, 0 and not 0
+};
+__device__ __forceinline__ float norm_of_shares(const Share* shares, int n, ShareSum* s_part) {
+    const int tid = threadIdx.x;
+    for (int unit = 0;;) {                                   // the sum by this kind's power of two
+        Squares q;
+        unsigned kinds = 0u;
+        for (int k = tid; k < n; k += kClipThreads) {
+            const Share s = shares[k];
+            kinds |= s.kind > 0 ? 1u : s.kind < 0 ? 2u : s.hi > 0.f ? 4u : 0u;
+            // (a share far below the unit's: its root twice, as a float holds no 2^-160)
+            const float f = s.kind >= unit ? 1.f : unit == 0 ? 0x1p-80f : s.kind == 0 ? 0x1p-90f : 0.f;
+            q.join(TwoFloat{s.hi * f * f, s.lo * f * f});
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            q.join(TwoFloat{__shfl_xor_sync(0xffffffffu, q.sum.hi, o), __shfl_xor_sync(0xffffffffu, q.sum.lo, o)});
+        kinds = __reduce_or_sync(0xffffffffu, kinds);
+        if ((tid & 31) == 0) s_part[tid >> 5] = ShareSum{q.sum, kinds};
+        __syncthreads();
+        q.sum = s_part[0].sum;
+        kinds = s_part[0].kinds;
+#pragma unroll
+        for (int w = 1; w < kClipWarps; ++w) {
+            q.join(s_part[w].sum);
+            kinds |= s_part[w].kinds;
+        }
+        const bool large = (kinds & 1u) || !(q.sum.hi < INFINITY), small = kinds == 2u;
+        if (unit != 0 || !(large || small)) return norm_of(q.sum, unit > 0 ? 180 : unit < 0 ? -160 : 0);
+        unit = large ? 1 : -1;
+        __syncthreads();
+    }
 }
 
 __device__ __forceinline__ void st_vec32(void* p, const float (&f)[8]) {
@@ -262,27 +309,15 @@ __device__ __forceinline__ void scale_part(const ClipItem& it, long long b, long
 
 template <int N>
 __global__ void __launch_bounds__(kClipThreads, kScaleCtas) scale_kernel(const __grid_constant__ ClipList<N> a) {
-    __shared__ double s_part[kClipWarps];
-    __shared__ float s_c;
-    const int tid = threadIdx.x;
+    __shared__ ShareSum s_part[kClipWarps];
     pdl_wait();
-    double sum = 0.0;
-    for (int k = tid; k < a.n_shares; k += kClipThreads) sum += a.shares[k];
-    sum = warp_sum_d(sum);
-    if ((tid & 31) == 0) s_part[tid >> 5] = sum;
-    __syncthreads();
-    if (tid == 0) {
-        for (int w = 1; w < kClipWarps; ++w) sum += s_part[w];
-        const float norm = norm_of(sum);
-        const bool finite = norm < INFINITY;
-        s_c = finite && norm > a.max_norm ? a.max_norm / norm : 1.f;
-        if (a.write_norm && blockIdx.x == 0) {
-            *a.norm = norm;
-            *a.status = finite ? 0 : DSPARK_ROW_NONFINITE;
-        }
+    const float norm = norm_of_shares(a.shares, a.n_shares, s_part);
+    const bool finite = norm < INFINITY;
+    const float c = finite && norm > a.max_norm ? a.max_norm / norm : 1.f;
+    if (a.write_norm && blockIdx.x == 0 && threadIdx.x == 0) {
+        *a.norm = norm;
+        *a.status = finite ? 0 : DSPARK_ROW_NONFINITE;
     }
-    __syncthreads();
-    const float c = s_c;
     for_parts(a, [&](const ClipItem& it, long long b, long long e) {
         if (c == 1.f && it.out == it.grad) return;
         if (!it.bf16) scale_part<4, false>(it, b, e, c);
@@ -329,7 +364,7 @@ bool fill(ClipList<N>& a, const dspark_grad_t* grads, int n) {
 }
 
 template <int N>
-dspark_status_t clip(const dspark_grad_t* grads, int n, float max_norm, float* norm, int* status, double* shares, int sms, cudaStream_t s) {
+dspark_status_t clip(const dspark_grad_t* grads, int n, float max_norm, float* norm, int* status, Share* shares, int sms, cudaStream_t s) {
     ClipList<N> a;
     a.max_norm = max_norm;
     a.norm = norm;
@@ -364,7 +399,7 @@ extern "C" {
 
 size_t dspark_clip_workspace_bytes(int32_t n_grads) {
     if (n_grads < 1 || n_grads > DSPARK_MAX_GRADS) return 0;
-    return static_cast<size_t>(groups_of(n_grads)) * kMaxShares * sizeof(double);
+    return static_cast<size_t>(groups_of(n_grads)) * kMaxShares * sizeof(Share);
 }
 
 dspark_status_t dspark_clip_grads(const dspark_grad_t* grads, int32_t n_grads, float max_norm, float* out_norm, int32_t* out_status,
@@ -375,7 +410,7 @@ dspark_status_t dspark_clip_grads(const dspark_grad_t* grads, int32_t n_grads, f
         return DSPARK_ERR_WORKSPACE;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return DSPARK_ERR_CUDA;
-    double* const shares = static_cast<double*>(workspace);
+    Share* const shares = static_cast<Share*>(workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return n_grads <= kSmallList ? clip<kSmallList>(grads, n_grads, max_norm, out_norm, out_status, shares, sms, s)
                                  : clip<kLargeList>(grads, n_grads, max_norm, out_norm, out_status, shares, sms, s);
