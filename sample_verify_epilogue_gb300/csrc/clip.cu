@@ -10,7 +10,7 @@
 //
 // Bound by bandwidth: 374 M bf16 into fp32 take 112 us for the norm (6.7 TB/s) and 368 for the scaling (6.1 TB/s of reads and
 // writes).  The gradients are read twice, since the factor needs them all; of lists that fit L2 the second read is from there.
-// A short list (4 tensors of 1 MB) takes 5.6 us: two launches, and the shares' way through L2.
+// A short list (4 tensors of 1 MB) takes 5.0 us: two launches, and the shares' way through L2.
 #include <algorithm>
 #include <cmath>
 
@@ -21,8 +21,8 @@ namespace dspark {
 namespace {
 
 constexpr int kClipThreads = 256, kClipWarps = kClipThreads / 32;
-constexpr int kNormVec = 8, kScaleVec = 4;                   // vectors a thread has on their way
-constexpr int kNormCtas = 4, kScaleCtas = 5;                 // CTAs to an SM
+constexpr int kClipVec = 4;                                  // vectors a thread has on their way (8 in the norm: lists of 5 to 80 MB 1 to 15% slower)
+constexpr int kClipCtas = 4;                                 // CTAs to an SM (five in the scaling: lists of 1 to 20 MB 1 to 10% slower)
 constexpr int kUnit = kClipThreads;                          // vectors that go to one CTA together
 constexpr int kMaxShares = 2048;                             // shares of a group of tensors
 constexpr int kLargeList = 1000, kSmallList = 100;           // tensors of a launch: 32,000 bytes of parameters hold 1000
@@ -127,10 +127,10 @@ struct Squares {
         const unsigned char* p = g.p + g.first(w0 + threadIdx.x) * SX;
         const int n = static_cast<int>(w1 - w0);             // a CTA's share of fewer than 2^31 units
         int k = threadIdx.x;
-        for (; k + (kNormVec - 1) * kClipThreads < n; k += kNormVec * kClipThreads, p += 16 * kNormVec * kClipThreads) {
-            uint4 v[kNormVec];
+        for (; k + (kClipVec - 1) * kClipThreads < n; k += kClipVec * kClipThreads, p += 16 * kClipVec * kClipThreads) {
+            uint4 v[kClipVec];
 #pragma unroll
-            for (int u = 0; u < kNormVec; ++u) v[u] = ld_vec16(p + 16 * u * kClipThreads);
+            for (int u = 0; u < kClipVec; ++u) v[u] = ld_vec16(p + 16 * u * kClipThreads);
             add<SX>(v, scale);
         }
         for (; k < n; k += kClipThreads, p += 16 * kClipThreads) {
@@ -170,7 +170,7 @@ __device__ __forceinline__ TwoFloat share_sum(const ClipList<N>& a, float scale,
 }
 
 template <int N>
-__global__ void __launch_bounds__(kClipThreads, kNormCtas) norm_kernel(const __grid_constant__ ClipList<N> a) {
+__global__ void __launch_bounds__(kClipThreads, kClipCtas) norm_kernel(const __grid_constant__ ClipList<N> a) {
     __shared__ TwoFloat s_sum[kClipWarps];
     pdl_wait();
     TwoFloat sum{0.f, 0.f};
@@ -206,8 +206,8 @@ __device__ __forceinline__ float norm_of(TwoFloat sum, int e) {
     return ldexpf(fmaf(0.5f / r, fmaf(-r, r, hi) + lo, r), (x + e) / 2);
 }
 
-// The norm from all shares, the same in every thread of every CTA.  In pairs of floats: the 64-bit sums of 760 CTAs, two
-// lanes a cycle, took SUMS us.
+// The norm from all shares, the same in every thread of every CTA.  In pairs of floats: 64-bit sums, of which an SM adds some
+// two a cycle, took 0.7 us of a list of 1 MB and 2 us of one of 12 MB.
 struct ShareSum {
     TwoFloat sum;
     unsigned kinds;                                          // bits: some are of kind 1, -1, 0 and not 0
@@ -297,18 +297,18 @@ __device__ __forceinline__ void scale_part(const ClipItem& it, long long b, long
     // the output's vectors lie as the gradient's do
     const bool alike = ((reinterpret_cast<uintptr_t>(it.out) - static_cast<uintptr_t>(g.a0) * (WIDE ? 4 : SX)) & (WIDE ? 31u : 15u)) == 0;
     long long k = b + threadIdx.x;
-    for (; k + (kScaleVec - 1) * kClipThreads < e; k += kScaleVec * kClipThreads) {
-        uint4 v[kScaleVec];
+    for (; k + (kClipVec - 1) * kClipThreads < e; k += kClipVec * kClipThreads) {
+        uint4 v[kClipVec];
 #pragma unroll
-        for (int u = 0; u < kScaleVec; ++u) v[u] = g.load(k + u * kClipThreads);
+        for (int u = 0; u < kClipVec; ++u) v[u] = g.load(k + u * kClipThreads);
 #pragma unroll
-        for (int u = 0; u < kScaleVec; ++u) scale_one<SX, WIDE>(g, it.out, k + u * kClipThreads, v[u], c, alike);
+        for (int u = 0; u < kClipVec; ++u) scale_one<SX, WIDE>(g, it.out, k + u * kClipThreads, v[u], c, alike);
     }
     for (; k < e; k += kClipThreads) scale_one<SX, WIDE>(g, it.out, k, g.load(k), c, alike);
 }
 
 template <int N>
-__global__ void __launch_bounds__(kClipThreads, kScaleCtas) scale_kernel(const __grid_constant__ ClipList<N> a) {
+__global__ void __launch_bounds__(kClipThreads, kClipCtas) scale_kernel(const __grid_constant__ ClipList<N> a) {
     __shared__ ShareSum s_part[kClipWarps];
     pdl_wait();
     const float norm = norm_of_shares(a.shares, a.n_shares, s_part);
@@ -375,7 +375,9 @@ dspark_status_t clip(const dspark_grad_t* grads, int n, float max_norm, float* n
         int done = 0;
         for (int k = 0; k < groups; ++k) {
             if (!fill(a, grads + k * kLargeList, std::min(kLargeList, n - k * kLargeList))) return DSPARK_ERR_UNSUPPORTED;
-            const int grid = std::max(1, std::min({a.units, kMaxShares, sms * (pass == 0 ? kNormCtas : kScaleCtas)}));
+            // a unit to a CTA, or two where there are more than two for every SM (a list of 3 MB by one and two: 7.3 and 6.5 us;
+            // one of 1 MB by two: 5.8 for 5.2)
+            const int grid = std::max(1, std::min({a.units <= 2 * sms ? a.units : a.units / 2, kMaxShares, sms * kClipCtas}));
             a.shares = pass == 0 ? shares + done : shares;
             a.n_shares = total;
             a.write_norm = k == 0;

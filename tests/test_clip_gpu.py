@@ -259,3 +259,16 @@ def test_clip_refuses_overlaps(bd):  # noqa: F811
         assert len(bd.GradTable(grads, out)) == len(grads)
     norm, status = clip_call(bd, [flat[8:16], flat[:8], flat[8:8], flat[16:]], 2.0)
     assert status == 0 and norm == 8.0 and bool((flat == 0.25).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("scales", [(1e30, 1.0, 1e-30), (1.0, 1e-30), (1e-30, 1e-20, 0.0), (2e-14, 1e-25), (2e17, 2e17), (1e19, 2e17), (1e25, 1e-12),
+                                    (3e-41, 1e-38), (1.0, 3e19)])
+def test_clip_shares_of_every_size(bd, scales, dtype):  # noqa: F811
+    """Tensors of many shares each, whose sums lie on either side of fp32's range, or leave it together."""
+    rng = np.random.default_rng(7)
+    values = [rng.uniform(0.5, 1, 900001) * s for s in scales]
+    held = [torch.from_numpy(v.astype(np.float32)).to(R.TORCH[dtype]).double() for v in values]
+    norm = float(sum((h * h).sum() for h in held)) ** 0.5
+    for max_norm in (norm / 3, norm * 2):
+        check(bd, values, [dtype] * len(values), float(np.float32(max_norm)))
