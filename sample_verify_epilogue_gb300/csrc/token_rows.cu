@@ -28,6 +28,7 @@ namespace {
 constexpr int kTokVec = 2;                                   // vectors a thread takes at a time from shared memory
 constexpr int kGradVec = 4;                                  // vectors a thread of the gradient has on their way
 constexpr int kShortRow = 2048;                              // vectors of a row that 128 threads take, where rows are many
+constexpr int kSlimRow = 1024;                               // those that 64 take
 constexpr int kGradVecs = 2048;                              // vectors of a row that a CTA of the gradient takes
 constexpr float kLn2 = 0.693147180559945f;
 // what a sum of the exponential unit's results lacks on average, relative: added to its logarithm.  (2^20 arguments between whole
@@ -1032,13 +1033,17 @@ dspark_status_t token_args(const void* logits, const dspark_token_params_t* p, c
 
 bool misplaced(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; }
 
-// A row is a CTA's work where there are rows enough: 456, 912 or 1824 of them are on the GPU at a time, by CTAs of 512, 256 or
-// 128 threads, and take the longer the more they are.
+// A row is a CTA's work where there are rows enough: 456, 912, 1824 or 3648 of them are on the GPU at a time, by CTAs of 512, 256,
+// 128 or 64 threads, and take the longer the more they are.
 //   - rows for one wave of 512 threads are theirs (400 rows of 151936: 23 us, 27 by 256 threads; 509 of 50001 fp32: 22 and 20);
 //   - rows whose last wave of 256 threads makes them an even number of waves take half as many of 128 (1024 rows of
-//     151936: 54 us, 63 by 256; 3000: 139 and 144; 2048, three waves of 256: 115 and 104; more than four: 195 and 188);
+//     151936: 54 us, 63 by 256; 3600: 167 and 170; more than four: 195 and 188);
 //     up to eight of these to an SM have six vectors on their way in place of four (1024 rows: 52 us, and of 50001 fp32 34, 36, 41);
-//   - short rows too (4096 rows of 4096: 15.3 and 20.1 us; 200 of 16000: 4.8 and 4.1);
+//   - short rows too (700 rows of 12470: 6.1 and 6.5 us; 200 of 16000: 4.8 and 4.1);
+//   - what takes more than one wave of 128 threads and one of 64 is theirs (1900 rows of 12470 fp32: 24.1 us by 128, 20.6 by 64;
+//     2100 of 151936: 123 and 108, by 256 111), of the long rows up to three quarters of it (3600 of 151936: 167 by 128, 172 by
+//     64), and rows so short that their latencies are most of their time (9000 rows of 7200: 37.4 and 31.6; of 10000 39.1 and 38.7,
+//     4096 of them 21.4 and 22.8);
 //   - the others are by 256, six to an SM (five: 2% less for 4096 rows of 151936, 900 rows 58 us instead of 46).
 // Fewer rows still are split over clusters (9 rows of 151936 in 1, 2, 4, 8 CTAs of 256: 11.4, 7.9, 5.8, 4.5 us; 8 of 512:
 // 3.9; short rows lose by it: 100 of 32000 4.1 us whole, 4.9 in halves).
@@ -1054,6 +1059,7 @@ dspark_status_t launch_stats(TokArgs& a, int sx, bool entropy, const dspark_toke
     const long long rows = p->n_rows;
     const bool wide = rows <= kWave / 2 && nvec >= 4096;
     const bool thin = rows > kWave / 2 && (nvec <= kShortRow || (rows <= 4 * kWave && (rows + kWave - 1) / kWave % 2 == 0));
+    const bool slim = rows > 2 * kWave && (nvec <= kSlimRow || rows <= (nvec <= 8192 ? 4 : 3) * kWave);
     int C = 1;
     a.log_c = 0;
     while (C < kMaxCluster && nvec >= C * 4096 && rows * 2 * C <= (wide ? kWave / 2 : 640)) {
@@ -1064,6 +1070,7 @@ dspark_status_t launch_stats(TokArgs& a, int sx, bool entropy, const dspark_toke
     const unsigned grid = static_cast<unsigned>(p->n_rows) * C;
     const cudaStream_t s = static_cast<cudaStream_t>(p->stream);
     const cudaError_t e = wide ? launch_stats_by<512>(a, sx, entropy, grid, C, s)
+                          : slim ? launch_stats_by<64>(a, sx, entropy, grid, C, s)
                           : thin ? (rows > kWave && rows <= 1216 ? launch_stats_by<128, 6>(a, sx, entropy, grid, C, s)
                                                                  : launch_stats_by<128>(a, sx, entropy, grid, C, s))
                                  : launch_stats_by<256>(a, sx, entropy, grid, C, s);

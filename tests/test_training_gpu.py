@@ -463,3 +463,12 @@ def test_preference_loss_bad_offsets(bd, at, value):  # noqa: F811
     assert bad
     for form in ("fused", "two_call"):
         check_preference(c, preference_call(bd, c, "fp32", form), "fp32", bad_pairs=bad)
+
+
+@pytest.mark.parametrize("rows,V,dtype", [(1825, 4003, "fp32"), (3649, 301, "bf16"), (1900, 16411, "bf16")])
+def test_token_logprobs_of_many_rows(bd, rows, V, dtype):  # noqa: F811
+    """Rows that CTAs of 64 threads take."""
+    rng = np.random.default_rng(rows)
+    x, y = T_.token_rows(rng, rows, V, dtype)
+    up = rng.normal(0, 1, (2, rows)).astype(np.float32)
+    check_logprobs(x, y, dtype, 1.0, logprobs_call(bd, x, y, dtype, up=up), up)
