@@ -29,7 +29,6 @@ constexpr int kTokVec = 2;                                   // vectors a thread
 constexpr int kGradVec = 4;                                  // vectors a thread of the gradient has on their way
 constexpr int kShortRow = 2048;                              // vectors of a row that 128 threads take, where rows are many
 constexpr int kSlimRow = 1024;                               // those that 64 take
-constexpr int kGradVecs = 2048;                              // vectors of a row that a CTA of the gradient takes
 constexpr float kLn2 = 0.693147180559945f;
 // what a sum of the exponential unit's results lacks on average, relative: added to its logarithm.  (2^20 arguments between whole
 // exponents: 5.06e-8, from 9e-8 too large to 1.4e-7 too small; sums of 262144 normal logits over 0.7, 1 and 1.3, by a
@@ -666,15 +665,26 @@ __device__ __forceinline__ void write_grad(const VocabRow<SX>& x, const VocabRow
         unsigned char* p = const_cast<unsigned char*>(g.p) + static_cast<long long>(x.first(k)) * SX;
         const uint4* q = src + (k - k0);
         const uint4* const end = src + (w1 - k0);
-        for (; q + (U - 1) * NT < end; q += U * NT, p += 16 * U * NT) {
-            uint4 v[U];
+        if (U == 1 || SX == 4)
+            for (; q + (U - 1) * NT < end; q += U * NT, p += 16 * U * NT) {
+                uint4 v[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) v[u] = KEPT ? q[u * NT] : ld_vec16(q + u * NT);
+                for (int u = 0; u < U; ++u) v[u] = KEPT ? q[u * NT] : ld_vec16(q + u * NT);
 #pragma unroll
-            for (int u = 0; u < U; ++u) st_vec16(p + 16 * u * NT, rg.of(v[u]));
-        }
+                for (int u = 0; u < U; ++u) st_vec16(p + 16 * u * NT, rg.of(v[u]));
+            }
+        // the last ones on their way together too (one by one: 16000 rows of 5000 bf16 83 us, 60 so); of bf16, whose registers are
+        // short, all of them here
         if (U > 1)
-            for (; q < end; q += NT, p += 16 * NT) st_vec16(p, rg.of(KEPT ? *q : ld_vec16(q)));
+            for (; q < end; q += U * NT, p += 16 * U * NT) {
+                uint4 v[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (q + u * NT < end) v[u] = KEPT ? q[u * NT] : ld_vec16(q + u * NT);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (q + u * NT < end) st_vec16(p + 16 * u * NT, rg.of(v[u]));
+            }
         if (tid == 0 && k0 < w0) store_vec<SX>(g, x.first(k0), rg.of(get(k0)), false);
         if (w1 < k1 && (k1 - 1 - k0) % NT == tid) store_vec<SX>(g, x.first(k1 - 1), rg.of(get(k1 - 1)), false);
     } else {
@@ -688,15 +698,14 @@ __device__ __forceinline__ void write_grad(const VocabRow<SX>& x, const VocabRow
     if (y >= 0 && y < x.V && at.k >= k0 && at.k < k1 && (at.k - k0) % NT == tid) store_one<SX>(g, y, rg.at_y);
 }
 
-// The gradient alone, 32 KB of a row to a CTA (16 KB: 3% slower for 509 fp32 rows of 50001, 8 KB: 34%).  Rows whose gradient is
-// 0 are not read.
-template <int SX, bool ENT>
-__global__ void __launch_bounds__(kRowThreads) grad_kernel(TokArgs a) {
+// The gradient alone, VECS vectors of a row to a CTA.  Rows whose gradient is 0 are not read.
+template <int SX, bool ENT, int NT, int VECS>
+__global__ void __launch_bounds__(NT) grad_kernel(TokArgs a) {
     const long long row = blockIdx.x / a.splits;
     const int part = blockIdx.x % a.splits;
     pdl_wait();
     const VocabRow<SX> x(a.x, row, a.x_stride, a.V), g(a.g, row, a.g_stride, a.V);
-    const int k0 = part * kGradVecs, k1 = min(x.nvec, k0 + kGradVecs);
+    const int k0 = part * VECS, k1 = min(x.nvec, k0 + VECS);
     RowSaved s = a.saved[row];
     const int y = a.tokens[row];
     if (a.op == kPreference) s.level = s.py = 0.f;
@@ -712,7 +721,7 @@ __global__ void __launch_bounds__(kRowThreads) grad_kernel(TokArgs a) {
         da = s.pair >= 0 && s.pair < a.n_up ? da * a.up[s.pair] : 0.f;
     }
     const RowGrad<SX, ENT> rg(a, s, da, dh);
-    write_grad<SX, ENT, false, kGradVec, kRowThreads>(x, g, k0, k1, y, s.f < 0.f || (da == 0.f && dh == 0.f), rg,
+    write_grad<SX, ENT, false, kGradVec, NT>(x, g, k0, k1, y, s.f < 0.f || (da == 0.f && dh == 0.f), rg,
                                                       reinterpret_cast<const uint4*>(x.p + static_cast<long long>(x.first(k0)) * SX));
 }
 
@@ -1077,13 +1086,21 @@ dspark_status_t launch_stats(TokArgs& a, int sx, bool entropy, const dspark_toke
     return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
+// Of fp32 32 KB of a row to a CTA of 256 threads (16 KB: 3% slower for 509 rows of 50001, 8 KB: 34%); of bf16, with twice the
+// instructions to a byte, 16 KB to one of 128 (2000 rows of 151936 with the entropy 177 us, 32 KB to 256 threads 200; without
+// it 335 and 332 for 3843); of many short rows 16 KB to one of 64 (16000 rows of 5000 bf16: 51 us, 57 by 128; 500 of them 3.0, 2.7).
+template <int SX, int NT, int VECS>
+cudaError_t launch_grad_by(TokArgs& a, bool entropy, const dspark_token_params_t* p) {
+    a.splits = (max_vectors(p->V, SX) + VECS - 1) / VECS;
+    auto kern = entropy ? grad_kernel<SX, true, NT, VECS> : grad_kernel<SX, false, NT, VECS>;
+    return launch_cluster(kern, static_cast<unsigned>(p->n_rows) * a.splits, NT, 1, 0, static_cast<cudaStream_t>(p->stream), a);
+}
 dspark_status_t launch_grad(TokArgs& a, int sx, bool entropy, const dspark_token_params_t* p) {
-    a.splits = (max_vectors(p->V, sx) + kGradVecs - 1) / kGradVecs;
-    const long long grid = static_cast<long long>(p->n_rows) * a.splits;
-    if (grid > 0x7fffffffLL) return DSPARK_ERR_UNSUPPORTED;
-    auto kern = sx == 2 ? (entropy ? grad_kernel<2, true> : grad_kernel<2, false>)
-                        : (entropy ? grad_kernel<4, true> : grad_kernel<4, false>);
-    const cudaError_t e = launch_cluster(kern, static_cast<unsigned>(grid), kRowThreads, 1, 0, static_cast<cudaStream_t>(p->stream), a);
+    const int nvec = max_vectors(p->V, sx);
+    if (static_cast<long long>(p->n_rows) * ((nvec + 1023) / 1024) > 0x7fffffffLL) return DSPARK_ERR_UNSUPPORTED;
+    const bool slim = nvec <= kShortRow && p->n_rows > kWave;
+    const cudaError_t e = sx == 2 ? (slim ? launch_grad_by<2, 64, 1024>(a, entropy, p) : launch_grad_by<2, 128, 1024>(a, entropy, p))
+                                  : (slim ? launch_grad_by<4, 64, 1024>(a, entropy, p) : launch_grad_by<4, 256, 2048>(a, entropy, p));
     return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
