@@ -533,10 +533,17 @@ __global__ void __launch_bounds__(NT, U == 4 ? 1536 / NT : 1024 / NT) stats_kern
         if (k == w0 + tid && w0 + (tid | 31) + (U - 1) * NT < w1) run.seed(v, a);
         run.add(v, a);
     }
-    for (; k < w1; k += NT, p += NT) {
-        uint4 v[1] = {ld_vec16(p)};
-        if (k == own) patch<SX>(v[0], at.lane, ninf_bits<SX>());
-        run.add(v, a);
+    if (k < w1) {                                            // what is left, on its way together too (1 to 8% of rows of 5000 to 32000)
+        uint4 v[U - 1][1];
+#pragma unroll
+        for (int u = 0; u < U - 1; ++u)
+            if (k + u * NT < w1) v[u][0] = ld_vec16(p + u * NT);
+#pragma unroll
+        for (int u = 0; u < U - 1; ++u)
+            if (k + u * NT < w1) {
+                if (k + u * NT == own) patch<SX>(v[u][0], at.lane, ninf_bits<SX>());
+                run.add(v[u], a);
+            }
     }
     if (tid < 2) {                                           // the ragged ends
         const int e = tid ? w1 : k0;
@@ -1044,7 +1051,8 @@ bool misplaced(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) 
 
 // A row is a CTA's work where there are rows enough: 456, 912, 1824 or 3648 of them are on the GPU at a time, by CTAs of 512, 256,
 // 128 or 64 threads, and take the longer the more they are.
-//   - rows for one wave of 512 threads are theirs (400 rows of 151936: 23 us, 27 by 256 threads; 509 of 50001 fp32: 22 and 20);
+//   - rows for one wave of 512 threads are theirs (400 rows of 151936: 23 us, 27 by 256 threads; 150 of 32000: 4.0 and 4.7; but
+//     509 of 50001 fp32: 22 and 20);
 //   - rows whose last wave of 256 threads makes them an even number of waves take half as many of 128 (1024 rows of
 //     151936: 54 us, 63 by 256; 3600: 167 and 170; more than four: 195 and 188);
 //     up to eight of these to an SM have six vectors on their way in place of four (1024 rows: 52 us, and of 50001 fp32 34, 36, 41);
@@ -1055,7 +1063,7 @@ bool misplaced(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) 
 //     4096 of them 21.4 and 22.8);
 //   - the others are by 256, six to an SM (five: 2% less for 4096 rows of 151936, 900 rows 58 us instead of 46).
 // Fewer rows still are split over clusters (9 rows of 151936 in 1, 2, 4, 8 CTAs of 256: 11.4, 7.9, 5.8, 4.5 us; 8 of 512:
-// 3.9; short rows lose by it: 100 of 32000 4.1 us whole, 4.9 in halves).
+// 3.9; shorter rows only where they are a handful: 9 of 32000 whole, in 2, 4, 8 3.7, 4.4, 3.6, 3.2 us, 40 of them 3.9, 4.4, 4.1, 4.2).
 constexpr int kWave = 152 * 6;                               // rows by 256 threads
 template <int NT, int U = 4>
 cudaError_t launch_stats_by(const TokArgs& a, int sx, bool entropy, unsigned grid, int C, cudaStream_t s) {
@@ -1066,12 +1074,13 @@ cudaError_t launch_stats_by(const TokArgs& a, int sx, bool entropy, unsigned gri
 dspark_status_t launch_stats(TokArgs& a, int sx, bool entropy, const dspark_token_params_t* p) {
     const int nvec = max_vectors(p->V, sx);
     const long long rows = p->n_rows;
-    const bool wide = rows <= kWave / 2 && nvec >= 4096;
+    const bool wide = rows <= kWave / 2 && nvec >= 2048;
     const bool thin = rows > kWave / 2 && (nvec <= kShortRow || (rows <= 4 * kWave && (rows + kWave - 1) / kWave % 2 == 0));
     const bool slim = rows > 2 * kWave && (nvec <= kSlimRow || rows <= (nvec <= 8192 ? 4 : 3) * kWave);
     int C = 1;
     a.log_c = 0;
-    while (C < kMaxCluster && nvec >= C * 4096 && rows * 2 * C <= (wide ? kWave / 2 : 640)) {
+    const int least = wide && rows <= 16 && nvec <= 8192 ? 512 : 4096;   // vectors that are worth one more CTA
+    while (C < kMaxCluster && nvec >= C * least && rows * 2 * C <= (wide ? kWave / 2 : 640)) {
         C *= 2;
         ++a.log_c;
     }
