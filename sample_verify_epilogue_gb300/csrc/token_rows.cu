@@ -12,8 +12,8 @@
 // stats_kernel streams a row and leaves what the gradient needs (32 bytes a row), grad_kernel streams it again, kept_kernel
 // does both with the row in shared memory, pair_kernel makes the pairs of a preference from their rows.  All but the last are
 // bound by bandwidth where there is enough to read: of the copy bandwidth stats 0.92 to 0.98 (4096 rows of 151936 bf16 with the
-// entropy 182 us, a tenth of them without a token), the gradient 0.93, both in one 0.98 (353 us; 0.93, 376 us, with an entropy
-// bonus).  Where a CTA has little to read its latencies bound it: token, first vectors, joins, the row's end.
+// entropy 180 us, a tenth of them without a token), the gradient 0.93 to 1, both in one 0.98 (353 us; 0.93, 376 us, with an
+// entropy bonus).  Where a CTA has little to read its latencies bound it: token, first vectors, joins, the row's end.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -1117,10 +1117,11 @@ dspark_status_t launch_grad(TokArgs& a, int sx, bool entropy, const dspark_token
 
 // CTAs of a row whose span stays in shared memory; 0 when the row is too long for eight of them.  Of the splits that fit, the
 // one by which an SM holds the most bytes (4096 rows of 151936 bf16 in 4, 5, 6, 7, 8: 407, 443, 411, 392, 409 us for 152,
-// 182, 203, 217, 190 KB; 2048 fp32 rows of it in eighths of 76 KB: 412 us, read twice 525); few rows in more.
+// 182, 203, 217, 190 KB; 2048 fp32 rows of it in eighths of 76 KB: 412 us, read twice 525); few rows in more
+// (100 of 32000 in 1, 2, 4, 8: 6.2, 6.3, 5.7, 8.3 us, 37 of them 6.1, 5.3, 5.0, 4.8).
 int fused_split(int nvec, long long rows) {
     int C = 1;
-    while (C < kMaxCluster && nvec >= C * 512 && rows * 2 * C <= 320) C *= 2;
+    while (C < kMaxCluster && nvec >= C * 512 && rows * 2 * C <= 400) C *= 2;
     int best = 0;
     for (int c = C, most = 0; c <= kMaxCluster; ++c) {
         const int span = (nvec + c - 1) / c;
