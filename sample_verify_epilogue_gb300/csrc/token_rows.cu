@@ -1059,10 +1059,10 @@ bool misplaced(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) 
 //     151936: 54 us, 63 by 256; 3600: 167 and 170; more than four: 195 and 188);
 //     up to eight of these to an SM have six vectors on their way in place of four (1024 rows: 52 us, and of 50001 fp32 34, 36, 41);
 //   - short rows too (700 rows of 12470: 6.1 and 6.5 us; 200 of 16000: 4.8 and 4.1);
-//   - what takes more than one wave of 128 threads and one of 64 is theirs (1900 rows of 12470 fp32: 24.1 us by 128, 20.6 by 64;
-//     2100 of 151936: 123 and 108, by 256 111), of the long rows up to three quarters of it (3600 of 151936: 167 by 128, 172 by
-//     64), and rows so short that their latencies are most of their time (9000 rows of 7200: 37.4 and 31.6; of 10000 39.1 and 38.7,
-//     4096 of them 21.4 and 22.8);
+//   - what takes little more than one wave of 128 threads is a wave by 64 (1900 rows of 12470 fp32: 24.1 us by 128, 20.6 by 64;
+//     2100 of 151936: 123 and 108, by 256 111; 2700 of 20000 fp32 37.1, 37.1, 37.4, 3600 46.0, 46.6, 48.5; of long rows 2400 of
+//     60000 fp32 93.8, 89.9, 86.4), and rows so short that their latencies are most of their time are theirs too (9000 rows of
+//     7200: 37.4 and 31.6; of 10000 39.1 and 38.7, 4096 of them 21.4 and 22.8);
 //   - the others are by 256, six to an SM (five: 2% less for 4096 rows of 151936, 900 rows 58 us instead of 46).
 // Fewer rows still are split over clusters (9 rows of 151936 in 1, 2, 4, 8 CTAs of 256: 11.4, 7.9, 5.8, 4.5 us; 8 of 512:
 // 3.9; shorter rows only where they are a handful: 9 of 32000 whole, in 2, 4, 8 3.7, 4.4, 3.6, 3.2 us, 40 of them 3.9, 4.4, 4.1, 4.2).
@@ -1078,7 +1078,7 @@ dspark_status_t launch_stats(TokArgs& a, int sx, bool entropy, const dspark_toke
     const long long rows = p->n_rows;
     const bool wide = rows <= kWave / 2 && nvec >= 2048;
     const bool thin = rows > kWave / 2 && (nvec <= kShortRow || (rows <= 4 * kWave && (rows + kWave - 1) / kWave % 2 == 0));
-    const bool slim = rows > 2 * kWave && (nvec <= kSlimRow || rows <= (nvec <= 8192 ? 4 : 3) * kWave);
+    const bool slim = rows > 2 * kWave && (nvec <= kSlimRow || rows <= (nvec <= 8192 ? 3 * kWave : 5 * kWave / 2));
     int C = 1;
     a.log_c = 0;
     const int least = wide && rows <= 16 && nvec <= 8192 ? 512 : 4096;   // vectors that are worth one more CTA
