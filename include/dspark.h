@@ -513,7 +513,7 @@ typedef struct {
  *   out_rewards   [P, 2] fp32 or NULL: beta S_2i, beta S_2i+1
  *   pair_status   [P] int32: 0, the bits of its rows' statuses, DSPARK_ROW_NONFINITE (z is NaN), or
  *                 DSPARK_ROW_BAD_PARAMS (row_offsets up to the pair's last descend somewhere or leave [0, R]); such a pair
- *                 has a loss and rewards of NaN and gradients of 0
+ *                 has a loss and rewards of NaN and gradients of 0, whatever comes from upstream (of weight 0 too)
  *   out_logprobs  [R] fp32 or NULL
  *   out_saved     [R, DSPARK_SAVED_FLOATS] fp32, 16-byte aligned, required: the rows' results on their way to the pairs
  *   out_grad      [R, V] or NULL: gradient of the sum of out_loss; may be logits itself (same pointer and

@@ -920,7 +920,7 @@ struct __align__(16) SeqSum {
 __device__ __forceinline__ TwoFloat add_finite(const TwoFloat& a, const TwoFloat& b) {   // infinities and NaN have no low part
     return fabsf(a.hi) < INFINITY && fabsf(b.hi) < INFINITY ? a + b : TwoFloat{a.hi + b.hi, 0.f};
 }
-__device__ __forceinline__ void one_pair(const PairArgs& a, int p, int lo, int mid, int hi, SeqSum* s_part, float* s_coef) {
+__device__ __forceinline__ void one_pair(const PairArgs& a, int p, int lo, int mid, int hi, SeqSum* s_part, float* s_coef, bool* s_none) {
     constexpr int kHalf = kRowThreads / 2;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     SeqSum q{TwoFloat{0.f, 0.f}, 0, 0};
@@ -971,22 +971,27 @@ __device__ __forceinline__ void one_pair(const PairArgs& a, int p, int lo, int m
             loss *= w;
             by_z = w * (e * of.q - (1.f - e) * of.p);
         }
-        s_coef[0] = st ? 0.f : by_z * a.beta / norm[0];
-        s_coef[1] = st ? 0.f : -by_z * a.beta / norm[1];
+        s_coef[0] = by_z * a.beta / norm[0];
+        s_coef[1] = -by_z * a.beta / norm[1];
+        *s_none = st != 0 || w == 0.f;
         a.loss[p] = st ? NAN : loss;
         if (a.rewards)
             for (int k = 0; k < 2; ++k) a.rewards[2 * p + k] = st ? NAN : reward[k].hi + reward[k].lo;
         a.pair_status[p] = st;
     }
     __syncthreads();
+    // (a pair without a gradient, of weight 0 too, has none whatever comes from upstream: its NaN loss comes back as NaN)
+    const bool none = *s_none;
     for (int r = lo + tid; r < hi; r += kRowThreads) {
         a.saved[r].a = s_coef[r >= mid];
         a.saved[r].pair = p;
+        if (none) a.saved[r].f = -1.f;
     }
 }
 __global__ void __launch_bounds__(kRowThreads) pair_kernel(PairArgs a) {
     __shared__ SeqSum s_part[kRowWarps];
     __shared__ float s_coef[2];
+    __shared__ bool s_none;
     const int tid = threadIdx.x;
     pdl_wait();
     const int p0 = static_cast<int>(static_cast<long long>(a.P) * blockIdx.x / gridDim.x);
@@ -1005,7 +1010,7 @@ __global__ void __launch_bounds__(kRowThreads) pair_kernel(PairArgs a) {
         }
         bad = bad || lo > mid || mid > hi || hi > a.R;
         if (!bad) {
-            one_pair(a, p, lo, mid, hi, s_part, s_coef);
+            one_pair(a, p, lo, mid, hi, s_part, s_coef, &s_none);
         } else if (tid == 0) {
             a.loss[p] = NAN;
             if (a.rewards) a.rewards[2 * p] = a.rewards[2 * p + 1] = NAN;
