@@ -479,8 +479,9 @@ typedef struct {
  *   out_saved   [R, DSPARK_SAVED_FLOATS] fp32, 16-byte aligned, or NULL
  *   out_grad    [R, V] or NULL: gradient of the sum of out_loss; may be logits itself (same pointer and
  *               stride).  It needs out_saved.
- * Where clipping binds, rho A gives no gradient; at its border rho counts as not clipped.  A = 0 leaves the
- * first term out, whatever rho is.  Rows without a token or of weight 0 are not read and have 0 everywhere.
+ * Where clipping binds, rho A gives no gradient; at its border, and past it by what the rounding of two log-probabilities makes
+ * (relative 2^-20 + 2^-22 |l|), rho counts as not clipped.  A = 0 leaves the first term out, whatever rho is.
+ * Rows without a token or of weight 0 are not read and have 0 everywhere.
  * row_status[r] as above, and DSPARK_ROW_NONFINITE for a row whose loss or derivative is not finite as well (a
  * masked token under a KL term, log-probabilities that are NaN): loss NaN, gradient 0.
  */

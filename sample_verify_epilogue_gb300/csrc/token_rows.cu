@@ -322,6 +322,20 @@ struct PolicyRow {
     float w, old, ref, adv;
 };
 
+// The smaller gain of rho A and the clipped rho times A: clipping binds above for A > 0, below for A < 0.  A ratio at
+// the border, or past it by what two fp32 log-probabilities' rounding makes of it, keeps its gradient (2^-24 |log p| for each of them and
+// 2e-7 of the sums: with clip 0 half of a rollout's rows would have none on the policy that drew them).
+struct Clipped {
+    float ratio, edge;                                       // clipped; from where clipping binds
+    bool binds;
+    __device__ __forceinline__ Clipped(const TokArgs& a, float rho, float logp, float adv) {
+        const float border = adv > 0.f ? a.high : a.low, slack = fmaf(fabsf(logp), 0x1p-22f, 0x1p-20f);
+        edge = fmaf(border, adv > 0.f ? slack : -slack, border);
+        binds = adv > 0.f ? rho > edge : rho < edge;
+        ratio = (adv > 0.f ? rho > border : rho < border) ? border : rho;
+    }
+};
+
 // A row's results, of which `saved` goes to its gradient.
 struct RowEnd {
     RowSaved saved;
@@ -397,13 +411,12 @@ __device__ __forceinline__ RowEnd row_end(const TokArgs& a, const EntSum& es, fl
     o.logp = lp.hi + lp.lo;
     o.entropy = H;
     if (a.op == kPolicy) {
-        // the smaller of rho A and the clipped rho times A; clipping binds above for a gain, below for a loss
         const float rho = expf((lp.hi - pr.old) + lp.lo);
         float gain = 0.f, by_lp = 0.f;
         if (pr.adv != 0.f) {
-            const bool binds = pr.adv > 0.f ? rho > a.high : rho < a.low;
-            gain = (binds ? (pr.adv > 0.f ? a.high : a.low) : rho) * pr.adv;
-            by_lp = binds ? 0.f : -gain;
+            const Clipped k(a, rho, lp.hi, pr.adv);
+            gain = k.ratio * pr.adv;
+            by_lp = k.binds ? 0.f : -rho * pr.adv;
         }
         float loss = -gain;
         o.kl = 0.f;
@@ -787,9 +800,9 @@ __device__ __forceinline__ RowSaved quick_end(const TokArgs& a, const EntSum& es
     const float rho = ex2_approx((lp.hi - pr.old2.hi) + (lp.lo - pr.old2.lo));
     float gain = 0.f, by_lp = 0.f;
     if (pr.adv != 0.f) {
-        const bool binds = pr.adv > 0.f ? rho > a.high : rho < a.low;
-        gain = (binds ? (pr.adv > 0.f ? a.high : a.low) : rho) * pr.adv;
-        by_lp = binds ? 0.f : -gain;
+        const Clipped k(a, rho, kLn2 * (lp.hi + lp.lo), pr.adv);
+        gain = k.ratio * pr.adv;
+        by_lp = k.binds ? 0.f : -rho * pr.adv;
     }
     float loss = -gain;
     if (a.kl_coef != 0.f) {

@@ -41,3 +41,51 @@ def test_upstream_of_pairs_without_a_gradient(bd, up, dtype):  # noqa: F811
     c["off"][4] = 0
     got = preference_call(bd, c, dtype, "two_call", up=np.full(4, up))
     assert list(got["pair_status"][1:]) == [bd.ROW_BAD_PARAMS] * 3 and not got["grad"].any()
+
+
+def own_logprobs(bd, x, y, dtype, T=1.0):  # noqa: F811
+    return logprobs_call(bd, x, y, dtype, T, entropy=False)[0]
+
+
+def clipped_call(bd, x, y, dtype, old, adv, form, low, high, w=None, T=1.0, ref=None, kl=0.0):  # noqa: F811
+    """(loss, status, gradient) of a policy loss with these borders."""
+    logits, tokens, rows = R.on_gpu(x, dtype), R.i32(y), len(x)
+    loss, st, saved = full(rows, 9.0), full(rows, -1, torch.int32), torch.full((rows, 8), 9.0, device="cuda")
+    grad = torch.full_like(logits, 77.0)
+    given = dict(clip_low=low, clip_high=high, weights=None if w is None else R.f32(w), ref_logprobs=None if ref is None else R.f32(ref),
+                 kl_coef=kl, temperature=T)
+    bd.dspark_policy_loss(logits, tokens, R.f32(old), R.f32(adv), loss=loss, row_status=st, saved=saved,
+                          grad=grad if form == "fused" else None, **given)
+    if form == "two_call":
+        bd.dspark_policy_loss_backward(logits, tokens, R.f32(old), R.f32(adv), saved=saved, grad=grad, **given)
+    return loss.double().cpu().numpy(), st.cpu().numpy(), grad.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("form", ["fused", "two_call"])
+def test_ratio_at_a_border_has_its_gradient(bd, form, dtype):  # noqa: F811
+    """A row's own log-probability as its old one, clip 0 on both sides: rho is 1 to the rounding of two log-probabilities and counts
+    as not clipped, so every row has the gradient of rho A.  The same where the border is elsewhere, and none a little beyond it."""
+    rng = np.random.default_rng(15)
+    rows, V = 200, 1003
+    x, y = T_.token_rows(rng, rows, V, dtype, special=False)
+    lp = own_logprobs(bd, x, y, dtype)
+    adv = (rng.uniform(0.5, 2, rows) * rng.choice([-1, 1], rows)).astype(np.float32)
+    for low, high in ((0.0, 0.0), (0.25, 0.5)):
+        edge = np.where(adv > 0, np.log1p(high), np.log1p(-low))
+        for beyond in (False, True):
+            # (beyond: by 1e-4, where the largest log-probability's rounding is 2^-20 of it)
+            old = (lp - edge - (np.sign(adv) * 1e-4 if beyond else 0)).astype(np.float32)
+            loss, st, grad = clipped_call(bd, x, y, dtype, old, adv, form, low, high)
+            assert not st.any()
+            for r in range(rows):
+                if beyond:
+                    assert not grad[r].any(), r
+                    continue
+                row = O.token_row(x[r], y[r], 1.0)
+                rho = np.exp(row["logp"][y[r]] - float(old[r]))
+                slack = 2.0 ** -20 + 2.0 ** -22 * abs(row["logp"][y[r]]) + T_.row_errors(row, V)[2]
+                want = O.token_grad(row, -float(adv[r]) * rho, 0.0, 1.0)
+                tol = T_.grad_bound(row, float(adv[r]) * rho, 0.0, V, 1.0, dtype, want, abs(float(adv[r])) * rho * slack)
+                assert (np.abs(grad[r] - want) <= tol).all(), (r, np.abs(grad[r] - want).max())
+                assert abs(loss[r] + float(adv[r]) * rho) <= abs(float(adv[r])) * rho * 2 * slack, r
