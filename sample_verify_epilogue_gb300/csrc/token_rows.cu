@@ -432,7 +432,7 @@ __device__ __forceinline__ RowEnd row_end(const TokArgs& a, const EntSum& es, fl
         o.loss = loss * pr.w;
         s.a = pr.w * by_lp;
         s.h = -pr.w * a.ent_coef;
-        if (!(fabsf(o.loss) < INFINITY) || !(fabsf(s.a) < INFINITY)) {
+        if (!(fabsf(o.loss) < INFINITY) || !(fabsf(s.a) < INFINITY) || !(fabsf(s.h) < INFINITY)) {
             o = RowEnd{s, NAN, NAN, NAN, NAN, DSPARK_ROW_NONFINITE};
             o.saved.f = -1.f;
         }
@@ -770,12 +770,15 @@ __device__ __forceinline__ float rcp_approx(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// Whether quick_end takes the row: the others have a whole exponent and a sum, the token a logit among them.
+// Whether quick_end takes the row: the others have a whole exponent and a sum, the token a logit among them.  What is a matter of
+// the last bits it leaves to row_end (sure = false), whose loss and status the row reports: a ratio within 2^-20 of where
+// clipping binds, of which its own is off by less, and what may leave fp32's range.
+constexpr float kSureRange = 0x1p120f;
 __device__ __forceinline__ bool is_quick(const EntSum& es, float xy, float c) {
     return fabsf(es.m * c) < 4194304.f && es.sum > 0x1p-60f && es.sum < 0x1p60f && fabsf(xy * c) < 4194304.f;
 }
 template <int SX, bool ENT>
-__device__ __forceinline__ RowSaved quick_end(const TokArgs& a, const EntSum& es, float xy, const QuickRow& pr) {
+__device__ __forceinline__ RowSaved quick_end(const TokArgs& a, const EntSum& es, float xy, const QuickRow& pr, bool& sure) {
     RowSaved s{es.m, -1.f, 0.f, 0.f, 0.f, 0.f, 0.f, -1};
     const float r = ceilf(es.m * a.c), by_sum = rcp_approx(es.sum), mean = ENT ? es.w * by_sum : 0.f;
     const int e = (__float_as_int(es.sum) - 0x3F400000) >> 23;
@@ -803,6 +806,7 @@ __device__ __forceinline__ RowSaved quick_end(const TokArgs& a, const EntSum& es
         const Clipped k(a, rho, kLn2 * (lp.hi + lp.lo), pr.adv);
         gain = k.ratio * pr.adv;
         by_lp = k.binds ? 0.f : -rho * pr.adv;
+        sure = fabsf(gain) < kSureRange && !(fabsf(rho - k.edge) <= 0x1p-20f * k.edge);
     }
     float loss = -gain;
     if (a.kl_coef != 0.f) {
@@ -811,9 +815,11 @@ __device__ __forceinline__ RowSaved quick_end(const TokArgs& a, const EntSum& es
         loss = fmaf(a.kl_coef, em1 - D, loss);
         by_lp = fmaf(-a.kl_coef, em1, by_lp);
     }
+    if (ENT) loss = fmaf(-a.ent_coef, H, loss);
     s.a = pr.w * by_lp;
     s.h = -pr.w * a.ent_coef;
-    if (fabsf(loss * pr.w) < INFINITY && fabsf(s.a) < INFINITY) s.f = q * by_sum * a.inv_t * by_low_of<SX, ENT>(a, es.m, kLn2 * by_low);
+    sure = sure && fabsf(loss * pr.w) < kSureRange && fabsf(s.a) < kSureRange && fabsf(s.h) < kSureRange;
+    s.f = q * by_sum * a.inv_t * by_low_of<SX, ENT>(a, es.m, kLn2 * by_low);
     return s;
 }
 
@@ -891,9 +897,10 @@ __global__ void __launch_bounds__(NT, kFusedCtas * 256 / NT) kept_kernel(TokArgs
             es = peers_join<ENT>(s_peer, C, a.c);
         }
         if (lane == 0) {
+            bool sure = late || is_quick(es, xy, a.c);
             if (late) s_row = row_bad(DSPARK_ROW_INTERNAL).saved;
-            else s_row = is_quick(es, xy, a.c) ? quick_end<SX, ENT>(a, es, xy, QuickRow{base2(pr.old), base2(pr.ref), pr.w, pr.adv})
-                                               : row_end<SX, ENT>(a, es, xy, pr).saved;
+            else if (sure) s_row = quick_end<SX, ENT>(a, es, xy, QuickRow{base2(pr.old), base2(pr.ref), pr.w, pr.adv}, sure);
+            if (!sure) s_row = row_end<SX, ENT>(a, es, xy, pr).saved;
         }
     }
     __syncthreads();
@@ -901,9 +908,7 @@ __global__ void __launch_bounds__(NT, kFusedCtas * 256 / NT) kept_kernel(TokArgs
     const bool zero = s_row.f < 0.f;
     write_grad<SX, ENT, true, 1, NT>(x, g, k0, k0 + cnt, y, zero, rg, s_x);
     if (rank == 0 && tid == 0) {
-        RowEnd o = late ? row_bad(DSPARK_ROW_INTERNAL) : row_end<SX, ENT>(a, es, xy, pr);
-        if (zero && !o.status) o = row_bad(DSPARK_ROW_NONFINITE);   // (a loss next to fp32's largest number)
-        row_write(a, row, o, ENT);
+        row_write(a, row, late ? row_bad(DSPARK_ROW_INTERNAL) : row_end<SX, ENT>(a, es, xy, pr), ENT);
     }
 }
 

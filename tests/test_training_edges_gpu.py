@@ -89,3 +89,45 @@ def test_ratio_at_a_border_has_its_gradient(bd, form, dtype):  # noqa: F811
                 tol = T_.grad_bound(row, float(adv[r]) * rho, 0.0, V, 1.0, dtype, want, abs(float(adv[r])) * rho * slack)
                 assert (np.abs(grad[r] - want) <= tol).all(), (r, np.abs(grad[r] - want).max())
                 assert abs(loss[r] + float(adv[r]) * rho) <= abs(float(adv[r])) * rho * 2 * slack, r
+
+
+@pytest.mark.parametrize("high", [0.0, 0.25])
+def test_both_forms_clip_the_same_rows(bd, high):  # noqa: F811
+    """Ratios within some 1e-6 of where clipping begins: the gradient in one call and the one from what that call has saved are of the
+    same rows, all or nothing."""
+    rng = np.random.default_rng(16)
+    rows, V = 2000, 67
+    x, y = T_.token_rows(rng, rows, V, "fp32", special=False)
+    lp = own_logprobs(bd, x, y, "fp32")
+    adv = np.ones(rows, np.float32)
+    seen = set()
+    for at in (0.0, 2.0 ** -20):                             # of the border itself, and of what counts as at it
+        slack = at + (2.0 ** -22 * np.abs(lp) if at else 0)
+        old = (lp - np.log1p(high) - slack + rng.uniform(-1e-6, 1e-6, rows)).astype(np.float32)
+        logits, tokens = R.on_gpu(x, "fp32"), R.i32(y)
+        loss, st, saved = full(rows, 9.0), full(rows, -1, torch.int32), torch.zeros(rows, 8, device="cuda")
+        fused, then = torch.full_like(logits, 77.0), torch.full_like(logits, 77.0)
+        args = (logits, tokens, R.f32(old), R.f32(adv))
+        bd.dspark_policy_loss(*args, loss=loss, row_status=st, saved=saved, grad=fused, clip_low=0.0, clip_high=high)
+        bd.dspark_policy_loss_backward(*args, saved=saved, grad=then, clip_low=0.0, clip_high=high)
+        a, b = (t.ne(0).any(1).cpu().numpy() for t in (fused, then))
+        assert np.array_equal(a, b), (at, int((a != b).sum()))
+        seen |= set(a.tolist())
+    assert seen == {True, False}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_losses_next_to_the_largest_number(bd, dtype):  # noqa: F811
+    """Advantages of fp32's largest number: a row whose loss is not finite has a status, a NaN loss and a gradient of 0, the others
+    have none of these."""
+    rng = np.random.default_rng(17)
+    rows, V = 2000, 67
+    x, y = T_.token_rows(rng, rows, V, dtype, special=False)
+    lp = own_logprobs(bd, x, y, dtype)
+    old = (lp + rng.uniform(-1e-6, 1e-6, rows)).astype(np.float32)
+    for adv, w in ((np.float32(3.4028235e38), None), (np.float32(2.0 ** 127), np.full(rows, 2, np.float32))):
+        loss, st, grad = clipped_call(bd, x, y, dtype, old, np.full(rows, -adv, np.float32), "fused", 0.2, 0.2, w=w)
+        bad = st != 0
+        assert bad.any() and not bad.all() and set(st[bad].tolist()) == {bd.ROW_NONFINITE}
+        assert np.isnan(loss[bad]).all() and np.isfinite(loss[~bad]).all()
+        assert not grad[bad].any() and (grad[~bad] != 0).any(1).all()
