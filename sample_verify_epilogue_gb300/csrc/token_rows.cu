@@ -831,6 +831,12 @@ __device__ __forceinline__ RowSaved quick_end(const TokArgs& a, const EntSum& es
 constexpr int kFusedSpan = 14000;                            // vectors of a span at most: 224,000 bytes
 constexpr int kFusedCtas = 5;                                // CTAs of 256 threads to an SM at most
 
+#ifdef DSPARK_TEST_EXPIRED_PEERS
+constexpr unsigned kExpirePeerMs = 50;                       // test build: a second wait of the row's second CTA, for what nobody sends
+#else
+constexpr unsigned kExpirePeerMs = 0;
+#endif
+
 template <int SX, bool ENT, int NT>
 __global__ void __launch_bounds__(NT, kFusedCtas * 256 / NT) kept_kernel(TokArgs a) {
     __shared__ EntSum s_warp[(NT / 32)];
@@ -892,7 +898,7 @@ __global__ void __launch_bounds__(NT, kFusedCtas * 256 / NT) kept_kernel(TokArgs
             // the token's logit has been read: its place may be written, where the gradient takes the logits' place
             const uint32_t after = (__float_as_uint(xy) & ~1u) | late;
             if (lane < C) push_sum(&s_peer[rank], &s_bar, lane, es, after);
-            late = !bar_wait(&s_bar, 0, kPeerMs) || late;
+            late = !bar_wait(&s_bar, 0, kPeerMs) || (kExpirePeerMs && rank == 1 && !bar_wait(&s_bar, 1, kExpirePeerMs)) || late;
             late = __any_sync(0xffffffffu, lane < C && (s_peer[lane & (kMaxCluster - 1)].after & 1u)) || late;
             es = peers_join<ENT>(s_peer, C, a.c);
         }
@@ -907,7 +913,8 @@ __global__ void __launch_bounds__(NT, kFusedCtas * 256 / NT) kept_kernel(TokArgs
     const RowGrad<SX, ENT> rg(a, s_row, s_row.a, s_row.h);
     const bool zero = s_row.f < 0.f;
     write_grad<SX, ENT, true, 1, NT>(x, g, k0, k0 + cnt, y, zero, rg, s_x);
-    if (rank == 0 && tid == 0) {
+    // the first CTA's business, but one whose wait for the others ran out has written zeros: it says so, seconds after it
+    if (tid == 0 && (rank == 0 || late)) {
         row_write(a, row, late ? row_bad(DSPARK_ROW_INTERNAL) : row_end<SX, ENT>(a, es, xy, pr), ENT);
     }
 }

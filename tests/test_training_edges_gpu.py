@@ -131,3 +131,27 @@ def test_losses_next_to_the_largest_number(bd, dtype):  # noqa: F811
         assert bad.any() and not bad.all() and set(st[bad].tolist()) == {bd.ROW_NONFINITE}
         assert np.isnan(loss[bad]).all() and np.isfinite(loss[~bad]).all()
         assert not grad[bad].any() and (grad[~bad] != 0).any(1).all()
+
+
+def test_one_cta_waits_in_vain(bd, monkeypatch):  # noqa: F811
+    """A test build in which the second CTA of every row that is split waits, 50 ms long, for what nobody sends: its part of the
+    gradient is 0, and though the first CTA has all it needs, the row reports DSPARK_ROW_INTERNAL and a NaN loss.  Rows of one CTA,
+    rows that are not read, and the calls after it are as ever."""
+    from sample_verify_epilogue_gb300 import binding as b_
+    from sample_verify_epilogue_gb300.build import build_variant
+    lib = b_.open_library(build_variant("expired_token_peers", ["-DDSPARK_TEST_EXPIRED_PEERS"], ["token_rows.cu"]))
+    expired = b_._Calls(lib)
+    rng = np.random.default_rng(24)
+    c = policy_batch(rng, 5, 140001, "bf16", 1.0, special=False)
+    c["y"][1], c["y"][3] = -1, 140001
+    one = policy_batch(rng, 6, 1003, "bf16", 1.0, special=False)
+    with monkeypatch.context() as m:
+        m.setattr(b_, "_calls_of", expired)
+        got = policy_call(bd, c, "bf16", 1.0, 0.1, 0.01, "fused", pad=1, shift=1)
+        check_policy(one, policy_call(bd, one, "bf16", 1.0, 0.1, 0.01, "fused"), "bf16", 1.0, 0.1, 0.01)
+    read = [0, 4]                                            # (2 has weight 0)
+    assert (got["status"][read] == b_.ROW_INTERNAL).all() and np.isnan(got["loss"][read]).all()
+    assert (got["grad"][read] == 0).any(1).all()
+    assert got["status"][1] == 0 and got["status"][2] == 0 and got["status"][3] == b_.ROW_BAD_TOKEN
+    good = policy_call(bd, c, "bf16", 1.0, 0.1, 0.01, "fused", pad=1, shift=1)
+    check_policy(c, good, "bf16", 1.0, 0.1, 0.01, bad={3: b_.ROW_BAD_TOKEN})
