@@ -348,8 +348,10 @@ struct Odds {
     TwoFloat sp;
     float sm, q, p;
     __device__ __forceinline__ explicit Odds(const TwoFloat& d) {
-        const float t = expf(-fabsf(d.hi)), l = log1pf(t), inv = 1.f / (1.f + t), small = t * inv;
+        // (d.lo is up to 2^-24 d: of a sure token's q 16 u)
         const bool up = d.hi > 0.f;
+        const float t = expf(-fabsf(d.hi)), l = log1pf(t), by = fabsf(d.hi) < INFINITY ? fmaf(t, up ? -d.lo : d.lo, t) : t;
+        const float inv = 1.f / (1.f + by), small = by * inv;
         q = up ? inv : small;
         p = up ? small : inv;
         sm = up ? l : l - d.hi;

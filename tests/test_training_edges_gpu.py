@@ -155,3 +155,55 @@ def test_one_cta_waits_in_vain(bd, monkeypatch):  # noqa: F811
     assert got["status"][1] == 0 and got["status"][2] == 0 and got["status"][3] == b_.ROW_BAD_TOKEN
     good = policy_call(bd, c, "bf16", 1.0, 0.1, 0.01, "fused", pad=1, shift=1)
     check_policy(c, good, "bf16", 1.0, 0.1, 0.01, bad={3: b_.ROW_BAD_TOKEN})
+
+
+LOG2E = float(np.float32(np.log2(np.e)))                     # a temperature by which logits are their own exponents of two
+
+
+def sure_rows(rng, rows, T):
+    """Two logits a row, 0 and the token's, whose odds are e^-23 to e^-24: the sum over the others is a power of two, without
+    rounding, so that what is off comes of the row's end."""
+    y = rng.integers(0, 2, rows)
+    x = np.zeros((rows, 2))
+    x[np.arange(rows), y] = R.rounded(rng.uniform(23, 24, rows) * T, "fp32")
+    return x, y, x[np.arange(rows), y] / T
+
+
+@pytest.mark.parametrize("T", [1.0, LOG2E])
+@pytest.mark.parametrize("form", ["logprobs", "two_call"])
+def test_gradients_of_sure_tokens(bd, form, T):  # noqa: F811
+    """The gradient of a token with nearly all the mass is q = 1 - p to fp32's last bits.  Roundings: the logarithm of the
+    sum and the unit's mean error in it u each, the exponential 4 u (ex2 too), its correction, 1 + t, the division and the product u each,
+    1 / T and two products by it u each, and rho for the policy (exp of next to nothing) 2 u: 14 u.  d in one float would add up to
+    16 u at odds of e^-23."""
+    rng = np.random.default_rng(18)
+    rows = 1000
+    x, y, d = sure_rows(rng, rows, T)
+    want = 1 / (1 + np.exp(d)) / T
+    if form == "logprobs":
+        grad = logprobs_call(bd, x, y, "fp32", T, entropy=False, up=(np.ones(rows), None))[3]
+    else:
+        grad = clipped_call(bd, x, y, "fp32", np.zeros(rows), np.full(rows, -1.0), form, 0.2, 0.2, T=T)[2]
+        want = want * np.exp(-1 / (1 + np.exp(d)))
+    at = grad[np.arange(rows), y]
+    assert (np.abs(at - want) <= 14 * U * want).all(), np.abs(at / want - 1).max() / U
+
+
+def test_slopes_of_settled_pairs(bd):  # noqa: F811
+    """A pair whose answers are far apart: the slope sigma(-z) keeps fp32's bits where z is no float.  Both rows have the same log p,
+    so z is beta times the references' difference, in pairs of floats: sigma(-z) 8 u with its correction, two products by beta and 1 / n u
+    each; the token's q, a half, 4 u, its product u: 15 u."""
+    rng = np.random.default_rng(20)
+    P = 300
+    x = np.zeros((2 * P, 2))
+    y = np.zeros(2 * P, np.int64)
+    ref = np.zeros(2 * P)
+    beta = float(np.float32(0.1))
+    ref[0::2] = R.rounded(rng.uniform(-240, -170, P), "fp32")
+    ref[1::2] = R.rounded(rng.uniform(-1, 1, P), "fp32")
+    c = dict(x=x, y=y, off=np.arange(2 * P + 1), ref=ref.astype(np.float32), w=None)
+    got = preference_call(bd, c, "fp32", "fused", beta=beta)
+    z = beta * (-ref[0::2] + ref[1::2])
+    want = -beta * np.exp(-np.logaddexp(0, z)) * 0.5         # at the chosen token
+    at = got["grad"][0::2, 0]
+    assert (np.abs(at - want) <= 15 * U * np.abs(want)).all(), np.abs(at / want - 1).max() / U
