@@ -752,8 +752,10 @@ __global__ void __launch_bounds__(NT, (ENT ? 0 : SX == 2 ? 1152 : NT == 64 ? 128
 // ---------------------------------------------------------------- loss and gradient in one
 // What a policy row's gradient is made with, on the way between its sum and its gradient, where the whole CTA waits: base 2
 // and the hardware's functions, a third of row_end's steps (its chain of dependent instructions, run by one warp
-// among forty, took 42 of 434 us of 4096 rows of 151936).  Logarithms are split from their exponents, so that their
-// 2^-22 is absolute; what cancels has two parts.  Off by some 4e-7 relative where row_end is by 2e-7.
+// among forty, took 42 of 434 us of 4096 rows of 151936).  Logarithms are split from their exponents, what cancels has two parts.
+// For fp32 logarithms and e^D - 1 by series, corrected reciprocals: the gradient at the token is off by 9e-8 relative (5e-7 at most), as by
+// row_end (1000 rows, V of 2 to 32003), for 0.4 to 1% of the time.  For bf16 the units' own: 1.7e-7 (7e-7, and 2e-6 of a KL
+// term's e^D - 1), where the result's rounding is 2e-3.
 struct QuickRow {
     TwoFloat old2, ref2;                                     // log-probabilities by log2(e)
     float w, adv;
@@ -762,15 +764,44 @@ __device__ __forceinline__ TwoFloat base2(float v) {
     const TwoFloat p = two_prod(v, kLog2E);
     return TwoFloat{p.hi, fabsf(p.hi) < INFINITY ? fmaf(v, 1.9259629e-8f, p.lo) : 0.f};
 }
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ float lg2_approx(float x) {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ float rcp_approx(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
+// 1 / x and 2^x without what the units lack: a step of Newton's; the exponential's mean error
+__device__ __forceinline__ float rcp_fine(float x) {
+    const float r = rcp_approx(x);
+    return fmaf(r, fmaf(-x, r, 1.f), r);
+}
+__device__ __forceinline__ float ex2_fine(float x, float more = 0.f) {   // times 1 + more
+    const float e = ex2_approx(x);
+    return fmaf(e, more + kEx2Lacks, e);
+}
+// log2((den + num) / (den - num)) = 2 / ln 2 atanh(num / den), by K terms of atanh's series
+template <int K>
+__device__ __forceinline__ float lg2_ratio(float num, float den) {
+    const float r = rcp_approx(den), g = num * r, f = fmaf(r, fmaf(-g, den, num), g), s = f * f, c = 2.f * kLog2E * f;
+    float p = 1.f / (2 * K - 1);
+#pragma unroll
+    for (int k = K - 1; k > 1; --k) p = fmaf(s, p, 1.f / (2 * k - 1));
+    return fmaf(c * s, p, c);
+}
+// log2 of m in [0.75, 1.5) and of 1 + t, t up to 1, the series' remainders 1e-8 relative; for bf16 2^-22 absolute (4096 rows of
+// 32000 81.7 us, by the series 82.9)
+template <int SX>
+__device__ __forceinline__ float lg2_near1(float m) {
+    return SX == 4 ? lg2_ratio<5>(m - 1.f, m + 1.f) : lg2_approx(m);
+}
+template <int SX>
+__device__ __forceinline__ float lg2_1p(float t) {
+    if (SX == 4) return lg2_ratio<7>(t, 2.f + t);
+    return t < 0.03125f ? t * kLog2E * fmaf(t, fmaf(t, fmaf(t, -0.25f, 1.f / 3.f), -0.5f), 1.f) : lg2_approx(1.f + t);
 }
 // Whether quick_end takes the row: the others have a whole exponent and a sum, the token a logit among them.  What is a matter of
 // the last bits it leaves to row_end (sure = false), whose loss and status the row reports: a ratio within 2^-20 of where
@@ -782,17 +813,17 @@ __device__ __forceinline__ bool is_quick(const EntSum& es, float xy, float c) {
 template <int SX, bool ENT>
 __device__ __forceinline__ RowSaved quick_end(const TokArgs& a, const EntSum& es, float xy, const QuickRow& pr, bool& sure) {
     RowSaved s{es.m, -1.f, 0.f, 0.f, 0.f, 0.f, 0.f, -1};
-    const float r = ceilf(es.m * a.c), by_sum = rcp_approx(es.sum), mean = ENT ? es.w * by_sum : 0.f;
+    const float r = ceilf(es.m * a.c), by_sum = rcp_fine(es.sum), mean = ENT ? es.w * by_sum : 0.f;
     const int e = (__float_as_int(es.sum) - 0x3F400000) >> 23;
-    const float l = lg2_approx(__int_as_float(__float_as_int(es.sum) - (e << 23))) + kEx2Lacks * kLog2E;
+    const float l = lg2_near1<SX>(__int_as_float(__float_as_int(es.sum) - (e << 23))) + kEx2Lacks * kLog2E;
     const float by_low = ENT ? a.c_low * a.inv_c * (mean + r) : 0.f;
     const TwoFloat p = two_prod(xy, a.c), top = two_sum(r + static_cast<float>(e), -p.hi);
     const float rest = top.lo + (l + by_low - fmaf(xy, a.c_low, p.lo)), d = top.hi + rest;   // log2 of R / e^s_y
-    const float t = ex2_approx(-fabsf(d)), u = 1.f + t, inv = rcp_approx(u), small = t * inv;
     const bool up = d > 0.f;
+    const float d_low = kLn2 * ((top.hi - d) + rest);
+    const float t = ex2_fine(-fabsf(d), up ? -d_low : d_low), inv = rcp_fine(1.f + t), small = t * inv;
     const float q = up ? inv : small, py = up ? small : inv;
-    // log2(1 + t): its series where the logarithm of 1 + t would lose t
-    const float lu = t < 0.03125f ? t * kLog2E * fmaf(t, fmaf(t, fmaf(t, -0.25f, 1.f / 3.f), -0.5f), 1.f) : lg2_approx(u);
+    const float lu = lg2_1p<SX>(t);
     const TwoFloat lp{up ? -top.hi : 0.f, up ? -(rest + lu) : -lu};   // log2 of p
     float H = 0.f;
     if (ENT) {
@@ -802,7 +833,7 @@ __device__ __forceinline__ RowSaved quick_end(const TokArgs& a, const EntSum& es
         s.py = py * fmaf(kLn2, lp.hi + lp.lo, H) * a.inv_t;
     }
     s.q = q * a.inv_t;
-    const float rho = ex2_approx((lp.hi - pr.old2.hi) + (lp.lo - pr.old2.lo));
+    const float rho = ex2_fine((lp.hi - pr.old2.hi) + (lp.lo - pr.old2.lo));
     float gain = 0.f, by_lp = 0.f;
     if (pr.adv != 0.f) {
         const Clipped k(a, rho, kLn2 * (lp.hi + lp.lo), pr.adv);
@@ -813,7 +844,8 @@ __device__ __forceinline__ RowSaved quick_end(const TokArgs& a, const EntSum& es
     float loss = -gain;
     if (a.kl_coef != 0.f) {
         const float D2 = (pr.ref2.hi - lp.hi) + (pr.ref2.lo - lp.lo), D = kLn2 * D2;
-        const float em1 = fabsf(D) < 0.0625f ? D * fmaf(D, fmaf(D, fmaf(D, fmaf(D, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f), 1.f) : ex2_approx(D2) - 1.f;
+        const float em1 = SX == 4 ? expm1f(D)
+                          : fabsf(D) < 0.0625f ? D * fmaf(D, fmaf(D, fmaf(D, fmaf(D, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f), 0.5f), 1.f) : ex2_approx(D2) - 1.f;
         loss = fmaf(a.kl_coef, em1 - D, loss);
         by_lp = fmaf(-a.kl_coef, em1, by_lp);
     }

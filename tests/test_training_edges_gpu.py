@@ -170,7 +170,7 @@ def sure_rows(rng, rows, T):
 
 
 @pytest.mark.parametrize("T", [1.0, LOG2E])
-@pytest.mark.parametrize("form", ["logprobs", "two_call"])
+@pytest.mark.parametrize("form", ["logprobs", "fused", "two_call"])
 def test_gradients_of_sure_tokens(bd, form, T):  # noqa: F811
     """The gradient of a token with nearly all the mass is q = 1 - p to fp32's last bits.  Roundings: the logarithm of the
     sum and the unit's mean error in it u each, the exponential 4 u (ex2 too), its correction, 1 + t, the division and the product u each,
@@ -207,3 +207,19 @@ def test_slopes_of_settled_pairs(bd):  # noqa: F811
     want = -beta * np.exp(-np.logaddexp(0, z)) * 0.5         # at the chosen token
     at = got["grad"][0::2, 0]
     assert (np.abs(at - want) <= 15 * U * np.abs(want)).all(), np.abs(at / want - 1).max() / U
+
+
+@pytest.mark.parametrize("form", ["fused", "two_call"])
+def test_gradients_of_a_small_kl_term(bd, form):  # noqa: F811
+    """Rows whose gradient is the KL term's alone (A = 0): e^D - 1 for log-ratios that are small but not next to nothing, at tokens
+    whose log-probability is next to 0, so that D is the reference's.  expm1 2 u more than above, D's own rounding u |D e^D / (e^D - 1)|
+    < 2 u, the product u: 19 u."""
+    rng = np.random.default_rng(19)
+    rows = 2000
+    x, y, d = sure_rows(rng, rows, LOG2E)
+    ref = (rng.uniform(0.01, 0.3, rows) * rng.choice([-1, 1], rows)).astype(np.float32)
+    grad = clipped_call(bd, x, y, "fp32", np.zeros(rows), np.zeros(rows), form, 0.2, 0.2, T=LOG2E, ref=ref, kl=1.0)[2]
+    q = 1 / (1 + np.exp(d))
+    want = -np.expm1(ref.astype(np.float64) + np.log1p(np.exp(-d))) * q / LOG2E
+    at = grad[np.arange(rows), y]
+    assert (np.abs(at - want) <= 19 * U * np.abs(want)).all(), np.abs(at / want - 1).max() / U
