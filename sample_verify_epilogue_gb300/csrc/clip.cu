@@ -194,16 +194,27 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtas) norm_kernel(const __g
     if (threadIdx.x == 0) a.shares[blockIdx.x] = Share{sum.hi, sum.hi < INFINITY ? sum.lo : 0.f, kind, 0};
 }
 
-// sqrt(sum 2^e), e even, by a float's root and a step of Newton's: relative 2^-24
-__device__ __forceinline__ float norm_of(TwoFloat sum, int e) {
-    if (!(sum.hi > 0.f && sum.hi < INFINITY)) return sum.hi;
+// m 2^e, m in [1, 2] as a pair of floats, or what is 0 or not finite with e = 0.
+struct Norm {
+    TwoFloat m;
+    int e;
+    __device__ __forceinline__ float value() const { return ldexpf(m.hi, e); }
+};
+// sqrt(sum 2^e), e even, by a float's root and a step of Newton's: relative 2^-46
+__device__ __forceinline__ Norm norm_of(TwoFloat sum, int e) {
+    if (!(sum.hi > 0.f && sum.hi < INFINITY)) return Norm{TwoFloat{sum.hi, 0.f}, 0};
     if (sum.hi < 0x1p-64f) {
         sum = TwoFloat{sum.hi * 0x1p64f, sum.lo * 0x1p64f};
         e -= 64;
     }
     const int x = ((__float_as_int(sum.hi) >> 23) - 127) & ~1;
     const float by = __int_as_float((127 - x) << 23), hi = sum.hi * by, lo = sum.lo * by, r = sqrtf(hi);   // hi in [1, 4)
-    return ldexpf(fmaf(0.5f / r, fmaf(-r, r, hi) + lo, r), (x + e) / 2);
+    return Norm{two_sum(r, 0.5f / r * (fmaf(-r, r, hi) + lo)), (x + e) / 2};
+}
+// v / m, rounded once (and a hundredth of that)
+__device__ __forceinline__ float over(float v, const TwoFloat& m) {
+    const float inv = __fdividef(1.f, m.hi), q = v * inv;
+    return fmaf(fmaf(-q, m.hi, v) - q * m.lo, inv, q);
 }
 
 // The norm from all shares, the same in every thread of every CTA.  In pairs of floats: 64-bit sums, of which an SM adds some
@@ -212,7 +223,7 @@ struct ShareSum {
     TwoFloat sum;
     unsigned kinds;                                          // bits: some are of kind 1, -1, 0 and not 0
 };
-__device__ __forceinline__ float norm_of_shares(const Share* shares, int n, ShareSum* s_part) {
+__device__ __forceinline__ Norm norm_of_shares(const Share* shares, int n, ShareSum* s_part) {
     const int tid = threadIdx.x;
     for (int unit = 0;;) {                                   // the sum by this kind's power of two
         Squares q;
@@ -311,9 +322,11 @@ template <int N>
 __global__ void __launch_bounds__(kClipThreads, kClipCtas) scale_kernel(const __grid_constant__ ClipList<N> a) {
     __shared__ ShareSum s_part[kClipWarps];
     pdl_wait();
-    const float norm = norm_of_shares(a.shares, a.n_shares, s_part);
+    const Norm n = norm_of_shares(a.shares, a.n_shares, s_part);
+    const float norm = n.value();
     const bool finite = norm < INFINITY;
-    const float c = finite && norm > a.max_norm ? a.max_norm / norm : 1.f;
+    // by the norm before its rounding (by the rounded one up to 1.7 u off for 1)
+    const float c = finite && norm > a.max_norm ? ldexpf(over(a.max_norm, n.m), -n.e) : 1.f;
     if (a.write_norm && blockIdx.x == 0 && threadIdx.x == 0) {
         *a.norm = norm;
         *a.status = finite ? 0 : DSPARK_ROW_NONFINITE;

@@ -223,3 +223,17 @@ def test_gradients_of_a_small_kl_term(bd, form):  # noqa: F811
     want = -np.expm1(ref.astype(np.float64) + np.log1p(np.exp(-d))) * q / LOG2E
     at = grad[np.arange(rows), y]
     assert (np.abs(at - want) <= 19 * U * np.abs(want)).all(), np.abs(at / want - 1).max() / U
+
+
+def test_clip_factor_to_the_last_bit(bd):  # noqa: F811
+    """n ones, whose sum of squares has no rounding: each comes out as max_norm / sqrt(n), rounded once.  (u, and 2^-40 for the
+    root in a pair of floats; from a norm rounded to a float it is 2 u.)"""
+    worst = 0.0
+    for n in range(2, 300, 7):
+        for max_norm in (1.0, float(np.float32(0.7))):
+            g = torch.ones(n, device="cuda")
+            norm, status = clip_call(bd, [g], max_norm)
+            want = max_norm / n ** 0.5
+            assert status == 0 and abs(norm - n ** 0.5) <= U * n ** 0.5 * (1 + 2.0 ** -20)
+            worst = max(worst, float((g.double() / want - 1).abs().max()))
+    assert worst <= U * (1 + 2.0 ** -12), worst / U
