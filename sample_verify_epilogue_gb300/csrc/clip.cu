@@ -194,11 +194,16 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtas) norm_kernel(const __g
     if (threadIdx.x == 0) a.shares[blockIdx.x] = Share{sum.hi, sum.hi < INFINITY ? sum.lo : 0.f, kind, 0};
 }
 
+// v 2^e, |e| below 250, rounded once
+__device__ __forceinline__ float times_2(float v, int e) {
+    const int half = e >> 1;
+    return v * __int_as_float((127 + half) << 23) * __int_as_float((127 + e - half) << 23);
+}
 // m 2^e, m in [1, 2] as a pair of floats, or what is 0 or not finite with e = 0.
 struct Norm {
     TwoFloat m;
     int e;
-    __device__ __forceinline__ float value() const { return ldexpf(m.hi, e); }
+    __device__ __forceinline__ float value() const { return times_2(m.hi, e); }
 };
 // sqrt(sum 2^e), e even, by a float's root and a step of Newton's: relative 2^-46
 __device__ __forceinline__ Norm norm_of(TwoFloat sum, int e) {
@@ -209,7 +214,7 @@ __device__ __forceinline__ Norm norm_of(TwoFloat sum, int e) {
     }
     const int x = ((__float_as_int(sum.hi) >> 23) - 127) & ~1;
     const float by = __int_as_float((127 - x) << 23), hi = sum.hi * by, lo = sum.lo * by, r = sqrtf(hi);   // hi in [1, 4)
-    return Norm{two_sum(r, 0.5f / r * (fmaf(-r, r, hi) + lo)), (x + e) / 2};
+    return Norm{two_sum(r, __fdividef(0.5f, r) * (fmaf(-r, r, hi) + lo)), (x + e) / 2};
 }
 // v / m, rounded once (and a hundredth of that)
 __device__ __forceinline__ float over(float v, const TwoFloat& m) {
@@ -318,6 +323,24 @@ __device__ __forceinline__ void scale_part(const ClipItem& it, long long b, long
     for (; k < e; k += kClipThreads) scale_one<SX, WIDE>(g, it.out, k, g.load(k), c, alike);
 }
 
+// The same by a factor below 2^-126, which fp32 holds with fewer bits or as 0: first by a power of two that brings the norm
+// into [0.5, 1], then by the rest.  Element by element, as the other calls share its registers and code (by vectors: a list of 12 MB
+// 9.9 us for 9.6).
+template <int N>
+__device__ __forceinline__ void scale_tiny(const ClipList<N>& a, float first, float c) {
+    for_parts(a, [&](const ClipItem& it, long long b, long long e) {
+        const int sx = it.bf16 ? 2 : 4, ve = 16 / sx, a0 = static_cast<int>((reinterpret_cast<uintptr_t>(it.grad) & 15u) / sx);
+        const long long i1 = min(it.numel, e * ve - a0);
+#pragma unroll 1
+        for (long long i = max(0LL, b * ve - a0) + threadIdx.x; i < i1; i += kClipThreads) {
+            const float g = it.bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(it.grad)[i]) : reinterpret_cast<const float*>(it.grad)[i];
+            const float v = g * first * c;
+            if (it.bf16 && !it.wide) reinterpret_cast<__nv_bfloat16*>(it.out)[i] = __float2bfloat16_rn(v);
+            else reinterpret_cast<float*>(it.out)[i] = v;
+        }
+    });
+}
+
 template <int N>
 __global__ void __launch_bounds__(kClipThreads, kClipCtas) scale_kernel(const __grid_constant__ ClipList<N> a) {
     __shared__ ShareSum s_part[kClipWarps];
@@ -326,17 +349,21 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtas) scale_kernel(const __
     const float norm = n.value();
     const bool finite = norm < INFINITY;
     // by the norm before its rounding (by the rounded one up to 1.7 u off for 1)
-    const float c = finite && norm > a.max_norm ? ldexpf(over(a.max_norm, n.m), -n.e) : 1.f;
+    const float c = finite && norm > a.max_norm ? times_2(over(a.max_norm, n.m), -n.e) : 1.f;
     if (a.write_norm && blockIdx.x == 0 && threadIdx.x == 0) {
         *a.norm = norm;
         *a.status = finite ? 0 : DSPARK_ROW_NONFINITE;
     }
-    for_parts(a, [&](const ClipItem& it, long long b, long long e) {
-        if (c == 1.f && it.out == it.grad) return;
-        if (!it.bf16) scale_part<4, false>(it, b, e, c);
-        else if (it.wide) scale_part<2, true>(it, b, e, c);
-        else scale_part<2, false>(it, b, e, c);
-    });
+    if (__builtin_expect(!(c < 0x1p-126f), 1)) {
+        for_parts(a, [&](const ClipItem& it, long long b, long long e) {
+            if (c == 1.f && it.out == it.grad) return;
+            if (!it.bf16) scale_part<4, false>(it, b, e, c);
+            else if (it.wide) scale_part<2, true>(it, b, e, c);
+            else scale_part<2, false>(it, b, e, c);
+        });
+    } else {
+        scale_tiny(a, ldexpf(1.f, -n.e - 1), over(2.f * a.max_norm, n.m));
+    }
 }
 
 int groups_of(int n) { return (n + kLargeList - 1) / kLargeList; }

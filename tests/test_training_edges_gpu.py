@@ -237,3 +237,24 @@ def test_clip_factor_to_the_last_bit(bd):  # noqa: F811
             assert status == 0 and abs(norm - n ** 0.5) <= U * n ** 0.5 * (1 + 2.0 ** -20)
             worst = max(worst, float((g.double() / want - 1).abs().max()))
     assert worst <= U * (1 + 2.0 ** -12), worst / U
+
+
+@pytest.mark.parametrize("out", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("size,max_norm", [(1e38, 1e-3), (3e38, 1e-8), (1e38, 1e-30), (2e37, 1.2e-38), (1e30, 1e-20), (1.5, 2e-38), (1e20, 1e-40), (3e38, 1e-44)])
+def test_clip_factors_below_the_smallest_number(bd, size, max_norm, dtype, out):  # noqa: F811
+    """Gradients near fp32's largest number, clipped to small norms: the factor lies below fp32's numbers, what it makes does not."""
+    rng = np.random.default_rng(21)
+    v = np.concatenate([rng.uniform(-0.2, 0.2, 30) * size, rng.normal(0, 1e-3, 4000) * size, rng.normal(0, 1e-9, 40) * size])
+    g = torch.from_numpy(v.astype(np.float32)).to(R.TORCH[dtype]).cuda()
+    held = g.double().cpu().numpy()
+    m = float(np.float32(max_norm))
+    outs = [torch.full(v.shape, 7.0, device="cuda")] if out else None
+    norm, status = clip_call(bd, [g], m, outs)
+    want_norm, want = O.clip([held], m)
+    assert status == 0 and abs(norm - want_norm) <= 14 * U * want_norm
+    got = (outs[0] if out else g).double().cpu().numpy()
+    kind = "fp32" if out else dtype
+    # the norm's sum 12 u (squares of a chunk), the factor and the products u each; a step of the smallest numbers
+    tol = (16 * U + R.HALF[kind]) * np.abs(want[0]) + (2.0 ** -133 if kind == "bf16" else 2.0 ** -149)
+    assert (np.abs(got - want[0]) <= tol).all(), (np.abs(got - want[0]) - tol).max()
