@@ -258,3 +258,28 @@ def test_clip_factors_below_the_smallest_number(bd, size, max_norm, dtype, out):
     # the norm's sum 12 u (squares of a chunk), the factor and the products u each; a step of the smallest numbers
     tol = (16 * U + R.HALF[kind]) * np.abs(want[0]) + (2.0 ** -133 if kind == "bf16" else 2.0 ** -149)
     assert (np.abs(got - want[0]) <= tol).all(), (np.abs(got - want[0]) - tol).max()
+
+
+@pytest.mark.parametrize("rows,V,dtype", [(500, 16411, "bf16"), (600, 5003, "fp32"), (913, 16411, "bf16"), (1000, 8209, "fp32"),
+                                          (1216, 16400, "bf16"), (1217, 16411, "bf16"), (1300, 8203, "fp32"), (300, 8209, "fp32")])
+def test_loops_of_every_launch_shape(bd, rows, V, dtype):  # noqa: F811
+    """Rows by 256, 128 and 512 threads, by four and by six vectors at a time, long enough for the loop over whole batches, the last
+    vectors and both ragged ends, with tokens in each of them."""
+    rng = np.random.default_rng(rows)
+    x, y = T_.token_rows(rng, rows, V, dtype)
+    for r in range(20, 60):                                  # the first and the last vectors' logits
+        y[r] = r - 20 if r < 40 else V - 60 + r
+    x = R.rounded(x, dtype)
+    up = rng.normal(0, 1, (2, rows)).astype(np.float32)
+    check_logprobs(x, y, dtype, 1.0, logprobs_call(bd, x, y, dtype, pad=2, shift=3, up=up), up)
+    check_logprobs(x, y, dtype, 1.0, logprobs_call(bd, x, y, dtype, entropy=False, up=(up[0], None)), (up[0], None))
+
+
+@pytest.mark.parametrize("rows,V,dtype", [(450, 5003, "fp32"), (900, 8003, "bf16"), (450, 8209, "fp32"), (201, 16411, "bf16")])
+def test_loops_of_kept_rows(bd, rows, V, dtype):  # noqa: F811
+    """Policy losses whose rows are one CTA's, of 128 threads and of 256."""
+    rng = np.random.default_rng(rows)
+    c = policy_batch(rng, rows, V, dtype, 1.0, special=False)
+    for ent in (0.0, 0.02):
+        got = policy_call(bd, c, dtype, 1.0, 0.05, ent, "fused", pad=2, shift=3)
+        check_policy(c, got, dtype, 1.0, 0.05, ent)
