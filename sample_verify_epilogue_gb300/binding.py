@@ -718,12 +718,28 @@ def dspark_preference_loss_backward(logits, tokens, *, saved, grad, grad_loss, t
             _flat("grad_loss", grad_loss, _torch.f32, P, dev), grad.data_ptr())
 
 
+def _dense(t):
+    """Whether the elements of ``t`` fill its memory, each once, whatever the order of its dimensions."""
+    n = 1
+    for stride, size in sorted(zip(t.stride(), t.shape)):
+        if size != 1:
+            if stride != n:
+                return False
+            n *= size
+    return True
+
+
+def _ordered_as(o, t):
+    return all(n == 1 or a == b for n, a, b in zip(t.shape, o.stride(), t.stride()))
+
+
 class GradTable:
     """A list of gradients as dspark_clip_grads takes it, made once for gradients that stay where they are.
 
-    grads: contiguous bf16/fp32 CUDA tensors of one device, None entries left out; out: None (the gradients are clipped
-    in place) or a tensor for each, of its shape and its dtype or fp32, that overlaps no gradient.  The table holds the
-    tensors; it knows nothing of a ``.grad`` that is replaced later.
+    grads: bf16/fp32 CUDA tensors of one device whose elements fill their memory, in any order of dimensions (contiguous,
+    transposed, channels-last), None entries left out; out: None (the gradients are clipped in place) or a tensor for each,
+    of its shape and order and its dtype or fp32, that overlaps no gradient.  The table holds the tensors; it knows nothing
+    of a ``.grad`` that is replaced later.
     """
 
     def __init__(self, grads, out=None):
@@ -738,11 +754,13 @@ class GradTable:
         self.device = _device_of("a gradient", pairs[0][0])
         self.tensors, fields, held = pairs, [], []
         for g, o in pairs:
-            if g.get_device() != self.device or not g.is_contiguous():
-                raise ValueError("the gradients must be contiguous CUDA tensors of one device")
-            if o is not g and (o is None or o.shape != g.shape or o.get_device() != self.device or not o.is_contiguous() or
+            plain = g.is_contiguous()
+            if g.get_device() != self.device or not (plain or _dense(g)):
+                raise ValueError("the gradients must be dense CUDA tensors of one device")
+            if o is not g and (o is None or o.shape != g.shape or o.get_device() != self.device or
+                               not (o.is_contiguous() if plain else _ordered_as(o, g)) or
                                (o.dtype is not g.dtype and o.dtype is not T.f32)):
-                raise ValueError("an output must be contiguous, of its gradient's shape and device, and of its dtype or fp32")
+                raise ValueError("an output must be of its gradient's shape, order and device, and of its dtype or fp32")
             n = g.numel()
             if n:
                 held.append((g.data_ptr(), n * g.element_size()))

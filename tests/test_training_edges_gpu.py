@@ -283,3 +283,32 @@ def test_loops_of_kept_rows(bd, rows, V, dtype):  # noqa: F811
     for ent in (0.0, 0.02):
         got = policy_call(bd, c, dtype, 1.0, 0.05, ent, "fused", pad=2, shift=3)
         check_policy(c, got, dtype, 1.0, 0.05, ent)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_clip_dense_gradients_of_other_orders(bd, dtype):  # noqa: F811
+    """Gradients of transposed and channels-last parameters, whose elements fill their memory in another order; into outputs of the
+    same order too.  What has gaps or shares memory is refused."""
+    rng = np.random.default_rng(22)
+
+    def make():
+        a = torch.from_numpy(rng.normal(0, 1, (33, 70)).astype(np.float32)).to(R.TORCH[dtype]).cuda().t()
+        b = torch.from_numpy(rng.normal(0, 1, (2, 3, 5, 7)).astype(np.float32)).to(R.TORCH[dtype]).cuda().to(memory_format=torch.channels_last)
+        return [a, b, torch.ones(1, 9, device="cuda").t()]
+
+    for out in (None, "same", "fp32"):
+        g = make()
+        held = [t.double().cpu().numpy() for t in g]
+        outs = None if out is None else [torch.empty_like(t, dtype=torch.float32 if out == "fp32" else t.dtype) for t in g]
+        assert outs is None or all(o.stride() == t.stride() for o, t in zip(outs, g))
+        norm, status = clip_call(bd, g, 2.0, outs)
+        want, scaled = O.clip(held, 2.0)
+        assert status == 0 and abs(norm - want) <= 14 * U * want
+        for t, w in zip(g if out is None else outs, scaled):
+            half = R.HALF["bf16" if t.dtype is torch.bfloat16 else "fp32"]
+            assert (np.abs(t.double().cpu().numpy() - w) <= (16 * U + half) * np.abs(w) + 2.0 ** -133).all()
+    a = torch.ones(4, 6, device="cuda")
+    for grads, outs in (([a[:, ::2]], None), ([a[:, :3]], None), ([a[0].expand(4, 6)], None), ([a.t()], [torch.ones(6, 4, device="cuda")]),
+                        ([a], [torch.ones(6, 4, device="cuda").t()]), ([a, a.t()], None)):
+        with pytest.raises(ValueError):
+            bd.GradTable(grads, outs)
