@@ -130,10 +130,15 @@ def preference_loss(logits, tokens, row_offsets, *, ref_logprobs=None, weights=N
 
 
 def clip_grads_(parameters, max_norm):
-    """Scale the gradients of ``parameters`` in place so that their norm taken together is at most max_norm; (norm before,
-    status) on the GPU, each [1]: see dspark_clip_grads.  Parameters without a gradient are left out.  A loop whose gradients
-    stay where they are makes a ``binding.GradTable`` and its buffers once and calls ``binding.dspark_clip_grads``."""
-    table = binding.GradTable([p.grad for p in parameters])
+    """Scale the gradients of ``parameters`` (or of one) in place so that their norm taken together is at most max_norm; (norm
+    before, status) on the GPU, each [1]: see dspark_clip_grads.  Parameters without a gradient are left out; where none has one
+    the norm is 0.  A loop whose gradients stay where they are makes a ``binding.GradTable`` and its buffers once and calls
+    ``binding.dspark_clip_grads``."""
+    parameters = [parameters] if isinstance(parameters, torch.Tensor) else list(parameters)
+    grads = [p.grad for p in parameters]
+    if parameters and all(g is None for g in grads):
+        return torch.zeros(1, device=parameters[0].device), torch.zeros(1, dtype=torch.int32, device=parameters[0].device)
+    table = binding.GradTable(grads)
     first = table.tensors[0][0]
     norm, status = _like(first, 1), _like(first, 1, dtype=torch.int32)
     workspace = _like(first, binding.dspark_clip_workspace_bytes(table), dtype=torch.uint8)

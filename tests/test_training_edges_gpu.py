@@ -312,3 +312,17 @@ def test_clip_dense_gradients_of_other_orders(bd, dtype):  # noqa: F811
                         ([a], [torch.ones(6, 4, device="cuda").t()]), ([a, a.t()], None)):
         with pytest.raises(ValueError):
             bd.GradTable(grads, outs)
+
+
+def test_clip_grads_of_a_parameter_and_of_none(bd):  # noqa: F811
+    """A single parameter in place of a list; parameters of which none has a gradient: the norm of nothing is 0."""
+    from sample_verify_epilogue_gb300.training import clip_grads_
+    p = torch.nn.Parameter(torch.zeros(4, 4, device="cuda"))
+    q = torch.nn.Parameter(torch.zeros(3, device="cuda"))
+    norm, status = clip_grads_(iter([p, q]), 1.0)
+    assert norm.shape == (1,) and float(norm) == 0.0 and int(status) == 0 and norm.is_cuda
+    p.grad = torch.full((4, 4), 2.0, device="cuda")
+    norm, status = clip_grads_(p, 4.0)
+    assert float(norm) == 8.0 and int(status) == 0 and bool((p.grad == 1.0).all())
+    with pytest.raises(ValueError):
+        clip_grads_([], 1.0)
