@@ -85,15 +85,26 @@ struct TokArgs {
 struct EntSum {
     float m, sum, w;
 };
-// what a sum by `from` scales by to be by `to`, and what its exponents gain
-__device__ __forceinline__ float shift_of(float from, float to, float c) {
-    const ExpRef a(from, c), b(to, c);
-    return fmaxf(a.whole && b.whole ? a.r - b.r : (from - to) * c, -16384.f);
+// What a sum by `from` scales by to be by `to`, a power of two, and what its exponents gain: the difference of what was taken from
+// the exponents, a whole number or (logits of 2.9 million T) m log2(e) / T itself, as a pair of floats, with the constant's second
+// part where the exponents have it.
+struct RefExp {
+    float hi, lo;
+    __device__ __forceinline__ RefExp(float m, float c, float low) {
+        const float t = m * c;
+        const bool whole = fabsf(t) < 4194304.f;
+        hi = whole ? ceilf(t) : t;
+        lo = whole ? 0.f : fmaf(m, low, fmaf(m, c, -t));
+    }
+};
+__device__ __forceinline__ float shift_of(float from, float to, float c, float low) {
+    const RefExp a(from, c, low), b(to, c, low);
+    return from == to ? 0.f : fmaxf((a.hi - b.hi) + (a.lo - b.lo), -16384.f);   // (NaN, of the types' lowest values: nothing is left)
 }
 template <bool ENT>
-__device__ __forceinline__ void rebase_to(EntSum& a, float to, float c) {
+__device__ __forceinline__ void rebase_to(EntSum& a, float to, float c, float low) {
     if (a.m > -INFINITY) {
-        const float by = shift_of(a.m, to, c), k = ex2_approx(by);
+        const float by = shift_of(a.m, to, c, ENT ? 0.f : low), k = ex2_approx(by);
         if (ENT) a.w = fmaf(a.sum, by, a.w) * k;
         a.sum *= k;
     }
@@ -101,13 +112,13 @@ __device__ __forceinline__ void rebase_to(EntSum& a, float to, float c) {
 }
 // The sum over groups of N lanes, in each of them.
 template <bool ENT, int N>
-__device__ __forceinline__ EntSum lanes_join(EntSum a, float c) {
+__device__ __forceinline__ EntSum lanes_join(EntSum a, const TokArgs& args) {
     float m = a.m;
     if (N == 32) m = key_to_f(__reduce_max_sync(0xffffffffu, fkey(m)));
     else
 #pragma unroll
         for (int o = N / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (m > -INFINITY) rebase_to<ENT>(a, m, c);
+    if (m > -INFINITY) rebase_to<ENT>(a, m, args.c, args.c_low);
 #pragma unroll
     for (int o = N / 2; o; o >>= 1) {
         a.sum += __shfl_xor_sync(0xffffffffu, a.sum, o);
@@ -137,9 +148,9 @@ struct RunEnt {
 
     __device__ __forceinline__ EntSum get() const { return EntSum{m, sum + low, w}; }
 
-    __device__ __forceinline__ void rebase(float to, const ExpRef& ref, float c) {
+    __device__ __forceinline__ void rebase(float to, const ExpRef& ref, const TokArgs& a) {
         EntSum was = get();
-        rebase_to<ENT>(was, to, c);
+        rebase_to<ENT>(was, to, a.c, a.c_low);
         m = to;
         r = ref.whole ? ref.r : -INFINITY;
         sum = was.sum;
@@ -207,7 +218,7 @@ struct RunEnt {
                 }
                 return;
             }
-            rebase(to, ref, a.c);
+            rebase(to, ref, a);
             if (ENT && SX == 2) least = least_pair(ref, a.inv_c);
             s = sum_of(v, a, ws);                            // (NaN stays)
         }
@@ -259,10 +270,11 @@ struct RunEnt {
             return;
         }
         const ExpRef ref(to, a.c);
-        rebase(to, ref, a.c);
+        rebase(to, ref, a);
 #pragma unroll
         for (int q = 0; q < VE; ++q) {
-            const float x = elem<SX>(v, q), z = ref.whole ? fmaf(x, a.c, -ref.r) : (x - ref.m) * a.c, e = ex2_approx(z);
+            const float x = elem<SX>(v, q), z = !ref.whole ? (x - ref.m) * a.c : ENT ? fmaf(x, a.c, -ref.r) : fmaf(x, a.c_tail, fmaf(x, a.c_head, -ref.r));
+            const float e = ex2_approx(z);
             sum += e;
             if (ENT) w = fmaf(e, fmaxf(z, -16384.f), w);
         }
@@ -492,9 +504,9 @@ __device__ __forceinline__ void push_sum(PeerSum* slot, uint64_t* bar, int to, c
                  after);
 }
 template <bool ENT>
-__device__ __forceinline__ EntSum peers_join(const PeerSum* s, int C, float c) {
+__device__ __forceinline__ EntSum peers_join(const PeerSum* s, int C, const TokArgs& args) {
     const int k = threadIdx.x & (kMaxCluster - 1);
-    return lanes_join<ENT, kMaxCluster>(k < C ? s[k].es : EntSum{-INFINITY, 0.f, 0.f}, c);
+    return lanes_join<ENT, kMaxCluster>(k < C ? s[k].es : EntSum{-INFINITY, 0.f, 0.f}, args);
 }
 
 template <int SX, bool ENT, int NT, int U>
@@ -568,12 +580,12 @@ __global__ void __launch_bounds__(NT, U == 4 ? 1536 / NT : 1024 / NT) stats_kern
             run.add(v, a);
         }
     }
-    EntSum es = lanes_join<ENT, 32>(run.get(), a.c);
+    EntSum es = lanes_join<ENT, 32>(run.get(), a);
     if (lane == 0) s_warp[warp] = es;
     __syncthreads();
     if (C > 1) cluster_wait();
     if (warp != 0) return;
-    es = lanes_join<ENT, (NT / 32)>(s_warp[lane & ((NT / 32) - 1)], a.c);
+    es = lanes_join<ENT, (NT / 32)>(s_warp[lane & ((NT / 32) - 1)], a);
     bool late = false;
     if (C > 1) {
         if (rank != 0) {                                     // to the row's first CTA, which is there and waits
@@ -583,7 +595,7 @@ __global__ void __launch_bounds__(NT, U == 4 ? 1536 / NT : 1024 / NT) stats_kern
         if (lane == 0) s_peer[0].es = es;
         __syncwarp();
         late = !bar_wait(&s_bar, 0, kPeerMs);
-        es = peers_join<ENT>(s_peer, C, a.c);
+        es = peers_join<ENT>(s_peer, C, a);
     }
     if (lane == 0) row_write(a, row, late ? row_bad(DSPARK_ROW_INTERNAL) : row_end<SX, ENT>(a, es, xy, pr), ENT);
 }
@@ -922,19 +934,19 @@ __global__ void __launch_bounds__(NT, kFusedCtas * 256 / NT) kept_kernel(TokArgs
     }
     for (; q + (kTokVec - 1) * NT < end; q += kTokVec * NT) run.template add_from<kTokVec>(q, NT, a);
     for (; q < end; q += NT) run.template add_from<1>(q, NT, a);
-    EntSum es = lanes_join<ENT, 32>(run.get(), a.c);
+    EntSum es = lanes_join<ENT, 32>(run.get(), a);
     if (lane == 0) s_warp[warp] = es;
     late = __syncthreads_or(late);
     if (C > 1) cluster_wait();                               // the row's CTAs are there
     if (warp == 0) {
-        es = lanes_join<ENT, (NT / 32)>(s_warp[lane & ((NT / 32) - 1)], a.c);
+        es = lanes_join<ENT, (NT / 32)>(s_warp[lane & ((NT / 32) - 1)], a);
         if (C > 1) {
             // the token's logit has been read: its place may be written, where the gradient takes the logits' place
             const uint32_t after = (__float_as_uint(xy) & ~1u) | late;
             if (lane < C) push_sum(&s_peer[rank], &s_bar, lane, es, after);
             late = !bar_wait(&s_bar, 0, kPeerMs) || (kExpirePeerMs && rank == 1 && !bar_wait(&s_bar, 1, kExpirePeerMs)) || late;
             late = __any_sync(0xffffffffu, lane < C && (s_peer[lane & (kMaxCluster - 1)].after & 1u)) || late;
-            es = peers_join<ENT>(s_peer, C, a.c);
+            es = peers_join<ENT>(s_peer, C, a);
         }
         if (lane == 0) {
             bool sure = late || is_quick(es, xy, a.c);

@@ -326,3 +326,24 @@ def test_clip_grads_of_a_parameter_and_of_none(bd):  # noqa: F811
     assert float(norm) == 8.0 and int(status) == 0 and bool((p.grad == 1.0).all())
     with pytest.raises(ValueError):
         clip_grads_([], 1.0)
+
+
+@pytest.mark.parametrize("entropy", [False, True])
+@pytest.mark.parametrize("rows", [4, 1000])
+def test_logits_next_to_the_last_whole_exponent(bd, rows, entropy):  # noqa: F811
+    """Logits of some 2.9 million, where one thread's reference has a whole exponent and another's has none (they begin at 2^22):
+    their sums join without a jump.  Exponents by whole references lose 2^-24 of some 64 powers of two, a batch of them as often as not
+    the same way, others 2^-24 of their own: 64 u log 2 < 3e-6, and as much again for the token's; 2e-5 with margin."""
+    rng = np.random.default_rng(23)
+    V = 9001
+    x = R.rounded(2.0 ** 22 * np.log(2) + rng.integers(-60, 20, (rows, 1)) * 0.25 + rng.integers(-12, 13, (rows, V)) * 0.25, "fp32")
+    x[1::2] *= -1
+    y = rng.integers(0, V, rows)
+    lp, H, st, grad = logprobs_call(bd, x, y, "fp32", entropy=entropy, up=(np.ones(rows), np.ones(rows) if entropy else None))
+    assert not st.any()
+    for r in range(rows):
+        row = O.token_row(x[r], y[r], 1.0)
+        assert abs(lp[r] - row["logp"][y[r]]) < 2e-5, r
+        assert H is None or abs(H[r] - row["entropy"]) < 4e-5, r
+        want = O.token_grad(row, 1.0, 1.0 if entropy else 0.0, 1.0)
+        assert (np.abs(grad[r] - want) <= 2e-5 * row["p"] * (1 + 10 * entropy) + 1e-6 * np.abs(want) + (4e-5 if entropy else 2e-5) * (np.arange(V) == y[r])).all(), r
