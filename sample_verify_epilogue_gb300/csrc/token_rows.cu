@@ -1027,8 +1027,10 @@ __device__ __forceinline__ void one_pair(const PairArgs& a, int p, int lo, int m
             }
             st |= s.status;
             norm[k] = a.mean ? static_cast<float>(max(s.count, 1)) : 1.f;
+            // the mean before beta, which may leave fp32's range; what has left it has no low part
+            if (a.mean && fabsf(s.sum.hi) < INFINITY) s.sum = s.sum / TwoFloat{norm[k], 0.f};
             reward[k] = fabsf(s.sum.hi) < INFINITY ? s.sum * TwoFloat{a.beta, 0.f} : TwoFloat{s.sum.hi, 0.f};
-            if (a.mean && fabsf(reward[k].hi) < INFINITY) reward[k] = reward[k] / TwoFloat{norm[k], 0.f};
+            if (!(fabsf(reward[k].hi) < INFINITY)) reward[k].lo = 0.f;
         }
         TwoFloat z{(reward[0].hi - reward[1].hi) - a.margin, 0.f};
         if (fabsf(z.hi) < INFINITY) z = reward[0] + -reward[1] + TwoFloat{-a.margin, 0.f};

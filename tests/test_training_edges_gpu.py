@@ -347,3 +347,16 @@ def test_logits_next_to_the_last_whole_exponent(bd, rows, entropy):  # noqa: F81
         assert H is None or abs(H[r] - row["entropy"]) < 4e-5, r
         want = O.token_grad(row, 1.0, 1.0 if entropy else 0.0, 1.0)
         assert (np.abs(grad[r] - want) <= 2e-5 * row["p"] * (1 + 10 * entropy) + 1e-6 * np.abs(want) + (4e-5 if entropy else 2e-5) * (np.arange(V) == y[r])).all(), r
+
+
+@pytest.mark.parametrize("mean", [False, True])
+def test_rewards_beyond_the_largest_number(bd, mean):  # noqa: F811
+    """beta times a log ratio that fp32 does not hold: rewards are infinite, not NaN, and so is the loss of the pair that has
+    the smaller one chosen."""
+    x = np.zeros((4, 8))
+    c = dict(x=x, y=np.zeros(4, np.int64), off=np.arange(5), ref=np.array([5, -5, -5, 5], np.float32), w=None)
+    got = preference_call(bd, c, "fp32", "fused", beta=2e38, mean=mean)
+    assert not got["pair_status"].any()
+    assert got["rewards"][0, 0] == -np.inf and got["rewards"][1, 1] == -np.inf
+    assert got["rewards"][0, 1] == np.inf and got["rewards"][1, 0] == np.inf
+    assert list(got["loss"]) == [np.inf, 0.0]
