@@ -454,7 +454,7 @@ dspark_status_t dspark_token_logprobs(const void* logits, const dspark_token_par
  * The gradient of sum_r (grad_logprobs[r] log p_r(y_r) + grad_entropy[r] H_r) by the logits, from the logits and
  * params of a dspark_token_logprobs call and its out_saved.  Either may be NULL (all 0), not both; grad_entropy needs
  * a call that asked for the entropy (else the gradient is NaN).
- *   out_grad  [R, V] of logits_dtype; may be logits itself (same pointer and stride)
+ *   out_grad  [R, V] of logits_dtype; may be logits itself (same pointer and stride), but not overlap it otherwise
  *   out_grad[r][v] = (g (1[v = y] - p_v) - e p_v (log p_v + H)) / T, g and e the upstream gradients
  */
 dspark_status_t dspark_token_logprobs_backward(const void* logits, const dspark_token_params_t* params, const float* saved,

@@ -1093,6 +1093,16 @@ __global__ void __launch_bounds__(kRowThreads) pair_kernel(PairArgs a) {
 }
 
 // ---------------------------------------------------------------- host
+// Whether a gradient that does not take the logits' place shares elements with them: a row's gradient would be made of another's.
+bool overlaps(const void* logits, const void* grad, const dspark_token_params_t* p, int sx) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(logits), g = reinterpret_cast<uintptr_t>(grad);
+    const auto bytes = [&](int64_t stride) { return (static_cast<uintptr_t>(p->n_rows - 1) * stride + p->V) * sx; };
+    if (g >= x ? g - x >= bytes(p->logits_stride) : x - g >= bytes(p->grad_stride)) return false;
+    if (p->logits_stride != p->grad_stride) return true;     // (rows among each other: not looked into)
+    const uintptr_t stride = static_cast<uintptr_t>(p->logits_stride) * sx, row = static_cast<uintptr_t>(p->V) * sx;
+    const uintptr_t on = g >= x ? (g - x) % stride : (x - g) % stride;
+    return on < row || stride - on < row;
+}
 dspark_status_t token_args(const void* logits, const dspark_token_params_t* p, const void* grad, TokArgs* a, int* sx) {
     if (!logits || !p || !p->tokens) return DSPARK_ERR_INVALID_ARG;
     if (p->n_rows < 1 || p->n_rows > DSPARK_MAX_ROWS || p->V < 1 || p->V > DSPARK_MAX_V) return DSPARK_ERR_INVALID_ARG;
@@ -1104,7 +1114,7 @@ dspark_status_t token_args(const void* logits, const dspark_token_params_t* p, c
     *sx = p->logits_dtype == DSPARK_BF16 ? 2 : 4;
     if (p->logits_stride < p->V || reinterpret_cast<uintptr_t>(logits) % *sx) return DSPARK_ERR_INVALID_ARG;
     if (grad && (p->grad_stride < p->V || reinterpret_cast<uintptr_t>(grad) % *sx)) return DSPARK_ERR_INVALID_ARG;
-    if (grad == logits && p->grad_stride != p->logits_stride) return DSPARK_ERR_INVALID_ARG;
+    if (grad && (grad != logits ? overlaps(logits, grad, p, *sx) : p->grad_stride != p->logits_stride)) return DSPARK_ERR_INVALID_ARG;
     a->V = p->V;
     a->c = c;
     a->c_low = static_cast<float>(exact - c);
