@@ -462,8 +462,10 @@ dspark_status_t dspark_token_logprobs_backward(const void* logits, const dspark_
 
 /* What a row's policy loss is made with (device arrays). */
 typedef struct {
-    const float* old_logprobs;    /* [R] of the policy that drew the tokens (dspark_verify_sample's out_logprobs)  */
-    const float* ref_logprobs;    /* [R] of the reference policy, or NULL                                          */
+    const float* old_logprobs;    /* [R] of the tokens under the policy that drew them, at this call's temperature: at 1
+                                     dspark_verify_sample's raw out_logprobs, whatever temperature and truncation its requests
+                                     have; else dspark_token_logprobs of the rollout's logits                      */
+    const float* ref_logprobs;    /* [R] of the reference policy at this call's temperature, or NULL               */
     const float* advantages;      /* [R]                                                                           */
     const float* weights;         /* [R] or NULL (all 1); a row of weight 0 is not read                            */
     float clip_low, clip_high;    /* in [0, 1]; >= 0: the ratio is clipped to [1 - clip_low, 1 + clip_high]         */
@@ -498,7 +500,7 @@ dspark_status_t dspark_policy_loss_backward(const void* logits, const dspark_pol
 typedef struct {
     int32_t n_pairs;              /* P, 1..DSPARK_MAX_PAIRS                                                  */
     const int32_t* row_offsets;   /* device [2P + 1]: sequence k is rows row_offsets[k] .. row_offsets[k+1] - 1 */
-    const float* ref_logprobs;    /* device [R] of the reference policy, or NULL: no reference                */
+    const float* ref_logprobs;    /* device [R] of the reference policy at this call's temperature, or NULL: none */
     const float* weights;         /* device [P] or NULL (all 1)                                              */
     float beta;                   /* > 0                                                                     */
     float margin;

@@ -650,8 +650,9 @@ def dspark_policy_loss(logits, tokens, old_logprobs, advantages, *, loss, row_st
     gradient as well.
 
     logits [..., V] bf16/fp32 of R rows, tokens [...] int32 (-1: no token), old_logprobs, advantages, ref_logprobs (or
-    None), weights (or None) [...] fp32; loss [...] fp32, row_status [...] int32, logprobs, entropy, kl [...] fp32 or None,
-    saved [..., 8] fp32 (needed with grad and for dspark_policy_loss_backward) or None, grad like logits (may be
+    None), weights (or None) [...] fp32, the log-probabilities at this call's temperature (a verify call's raw ones are
+    at 1); loss [...] fp32, row_status [...] int32, logprobs, entropy, kl [...] fp32 or None, saved [..., 8] fp32 (needed
+    with grad and for dspark_policy_loss_backward) or None, grad like logits (may be
     logits) or None -- all CUDA tensors.
     """
     if row_status is None:

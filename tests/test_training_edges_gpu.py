@@ -360,3 +360,27 @@ def test_rewards_beyond_the_largest_number(bd, mean):  # noqa: F811
     assert got["rewards"][0, 0] == -np.inf and got["rewards"][1, 1] == -np.inf
     assert got["rewards"][0, 1] == np.inf and got["rewards"][1, 0] == np.inf
     assert list(got["loss"]) == [np.inf, 0.0]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_old_logprobs_are_of_the_losses_temperature(bd, dtype):  # noqa: F811
+    """Tokens drawn at a temperature of 0.7 from a truncated distribution: the verify call's log-probabilities are those of the whole
+    distribution at 1, and the ratios of a loss at temperature 1 are 1; dspark_token_logprobs at 0.7 goes with a loss at 0.7."""
+    from sample_verify_epilogue_gb300.runner import EpilogueCall
+    from workloads.generate import make_batch, row_params
+    B, K, V = 5, 3, 5001
+    batch = make_batch(B=B, K_max=K, V=V, logits_dtype=dtype, rows=[row_params(0.7, 0, 0.9, 0.0, 0.0, K)] * B, seed=5, philox_seed=5,
+                       history_len=0, want_logprobs=True)
+    call = EpilogueCall(batch)
+    call.run()
+    tokens, raw, n = call.out["tokens"], call.out["logprobs"], B * (K + 1)
+    live = (tokens >= 0).view(-1)
+    assert int(live.sum()) >= B
+    lp, st, loss = full(n, 9.0), full(n, -1, torch.int32), full(n, 9.0)
+    adv = torch.ones(n, device="cuda")
+    for T, old in ((1.0, raw.contiguous().view(-1)), (0.7, lp)):
+        if T != 1.0:
+            bd.dspark_token_logprobs(call.x, tokens, logprobs=lp, row_status=st, temperature=T)
+        bd.dspark_policy_loss(call.x, tokens, old, adv, loss=loss, row_status=st, temperature=T)
+        # the verify call's log-probabilities are within 1e-4
+        assert not st.any() and float((loss[live] + 1).abs().max()) < 2e-4 and not loss[~live].any()
