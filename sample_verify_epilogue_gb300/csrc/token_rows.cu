@@ -816,8 +816,8 @@ __device__ __forceinline__ float lg2_1p(float t) {
     return t < 0.03125f ? t * kLog2E * fmaf(t, fmaf(t, fmaf(t, -0.25f, 1.f / 3.f), -0.5f), 1.f) : lg2_approx(1.f + t);
 }
 // Whether quick_end takes the row: the others have a whole exponent and a sum, the token a logit among them.  What is a matter of
-// the last bits it leaves to row_end (sure = false), whose loss and status the row reports: a ratio within 2^-20 of where
-// clipping binds, of which its own is off by less, and what may leave fp32's range.
+// the last bits it leaves to row_end (sure = false), whose loss and status the row reports: a ratio within 2^-19 of where
+// clipping binds (its own is off by 6e-7 at most, row_end's by 3e-7), and what may leave fp32's range.
 constexpr float kSureRange = 0x1p120f;
 __device__ __forceinline__ bool is_quick(const EntSum& es, float xy, float c) {
     return fabsf(es.m * c) < 4194304.f && es.sum > 0x1p-60f && es.sum < 0x1p60f && fabsf(xy * c) < 4194304.f;
@@ -851,7 +851,7 @@ __device__ __forceinline__ RowSaved quick_end(const TokArgs& a, const EntSum& es
         const Clipped k(a, rho, kLn2 * (lp.hi + lp.lo), pr.adv);
         gain = k.ratio * pr.adv;
         by_lp = k.binds ? 0.f : -rho * pr.adv;
-        sure = fabsf(gain) < kSureRange && !(fabsf(rho - k.edge) <= 0x1p-20f * k.edge);
+        sure = fabsf(gain) < kSureRange && !(fabsf(rho - k.edge) <= 0x1p-19f * k.edge);
     }
     float loss = -gain;
     if (a.kl_coef != 0.f) {
