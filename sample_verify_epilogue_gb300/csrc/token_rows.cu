@@ -86,20 +86,15 @@ struct EntSum {
     float m, sum, w;
 };
 // What a sum by `from` scales by to be by `to`, a power of two, and what its exponents gain: the difference of what was taken from
-// the exponents, a whole number or (logits of 2.9 million T) m log2(e) / T itself, as a pair of floats, with the constant's second
-// part where the exponents have it.
-struct RefExp {
-    float hi, lo;
-    __device__ __forceinline__ RefExp(float m, float c, float low) {
-        const float t = m * c;
-        const bool whole = fabsf(t) < 4194304.f;
-        hi = whole ? ceilf(t) : t;
-        lo = whole ? 0.f : fmaf(m, low, fmaf(m, c, -t));
-    }
-};
+// the exponents, a whole number or (logits of 2.9 million T) m log2(e) / T itself, to its low part, with the constant's second part where
+// the exponents have it.
 __device__ __forceinline__ float shift_of(float from, float to, float c, float low) {
-    const RefExp a(from, c, low), b(to, c, low);
-    return from == to ? 0.f : fmaxf((a.hi - b.hi) + (a.lo - b.lo), -16384.f);   // (NaN, of the types' lowest values: nothing is left)
+    const float t = from * c, u = to * c;
+    const bool t_whole = fabsf(t) < 4194304.f, u_whole = fabsf(u) < 4194304.f;
+    float by = (t_whole ? ceilf(t) : t) - (u_whole ? ceilf(u) : u);
+    if (!t_whole) by += fmaf(from, low, fmaf(from, c, -t));
+    if (!u_whole) by -= fmaf(to, low, fmaf(to, c, -u));
+    return from == to ? 0.f : fmaxf(by, -16384.f);           // (NaN, of the types' lowest values: nothing is left)
 }
 template <bool ENT>
 __device__ __forceinline__ void rebase_to(EntSum& a, float to, float c, float low) {
@@ -1147,10 +1142,11 @@ bool misplaced(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) 
 //     151936: 54 us, 63 by 256; 3600: 167 and 170; more than four: 195 and 188);
 //     up to eight of these to an SM have six vectors on their way in place of four (1024 rows: 52 us, and of 50001 fp32 34, 36, 41);
 //   - short rows too (700 rows of 12470: 6.1 and 6.5 us; 200 of 16000: 4.8 and 4.1);
-//   - what takes little more than one wave of 128 threads is a wave by 64 (1900 rows of 12470 fp32: 24.1 us by 128, 20.6 by 64;
-//     2100 of 151936: 123 and 108, by 256 111; 2700 of 20000 fp32 37.1, 37.1, 37.4, 3600 46.0, 46.6, 48.5; of long rows 2400 of
-//     60000 fp32 93.8, 89.9, 86.4), and rows so short that their latencies are most of their time are theirs too (9000 rows of
-//     7200: 37.4 and 31.6; of 10000 39.1 and 38.7, 4096 of them 21.4 and 22.8);
+//   - what takes little more than one wave of 128 threads is a wave by 64, up to three waves of 256 (by 64, 128, 256: 1900 rows of 12470
+//     fp32 19.6, 22.6, 22.5; 2100 of 151936 104, 118, 105; of 20000 fp32 2300 32.7, 34.9, 33.7, 2500 34.6, 36.0, 35.6, 2700 36.9, 37.5,
+//     37.8; beyond, as fast or slower: 2828 of 32347 fp32 with the entropy 64.6, 63.1, 66.2, 3600 of 20000 51.0, 49.6, 51.1), of long rows up to
+//     two and a half (2300 of 60000 fp32 87.0, 92.9, 85.0), and rows so short that their latencies are most of their time are
+//     theirs too (9000 rows of 7200: 37.4 and 31.6 us by 128 and 64; of 10000 39.1 and 38.7, 4096 of them 21.4 and 22.8);
 //   - the others are by 256, six to an SM (five: 2% less for 4096 rows of 151936, 900 rows 58 us instead of 46).
 // Fewer rows still are split over clusters (9 rows of 151936 in 1, 2, 4, 8 CTAs of 256: 11.4, 7.9, 5.8, 4.5 us; 8 of 512:
 // 3.9; shorter rows only where they are a handful: 9 of 32000 whole, in 2, 4, 8 3.7, 4.4, 3.6, 3.2 us, 40 of them 3.9, 4.4, 4.1, 4.2).
