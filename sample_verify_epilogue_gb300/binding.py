@@ -731,7 +731,8 @@ def _dense(t):
 
 
 def _ordered_as(o, t):
-    return all(n == 1 or a == b for n, a, b in zip(t.shape, o.stride(), t.stride()))
+    """Whether the dimensions of ``o`` lie in memory as those of ``t``."""
+    return o is not None and all(n == 1 or a == b for n, a, b in zip(t.shape, o.stride(), t.stride()))
 
 
 class GradTable:
@@ -755,11 +756,10 @@ class GradTable:
         self.device = _device_of("a gradient", pairs[0][0])
         self.tensors, fields, held = pairs, [], []
         for g, o in pairs:
-            plain = g.is_contiguous()
-            if g.get_device() != self.device or not (plain or _dense(g)):
-                raise ValueError("the gradients must be dense CUDA tensors of one device")
+            if g.get_device() != self.device or not (g.is_contiguous() or _dense(g) and (o is g or _ordered_as(o, g))):
+                raise ValueError("the gradients must be dense CUDA tensors of one device, their outputs of the same order")
             if o is not g and (o is None or o.shape != g.shape or o.get_device() != self.device or
-                               not (o.is_contiguous() if plain else _ordered_as(o, g)) or
+                               (not o.is_contiguous() and not _ordered_as(o, g)) or
                                (o.dtype is not g.dtype and o.dtype is not T.f32)):
                 raise ValueError("an output must be of its gradient's shape, order and device, and of its dtype or fp32")
             n = g.numel()
