@@ -11,8 +11,8 @@
 //
 // stats_kernel streams a row and leaves what the gradient needs (32 bytes a row), grad_kernel streams it again, kept_kernel
 // does both with the row in shared memory, pair_kernel makes the pairs of a preference from their rows.  All but the last are
-// bound by bandwidth where there is enough to read: of the copy bandwidth stats 0.92 to 0.98 (4096 rows of 151936 bf16 with the
-// entropy 180 us, a tenth of them without a token), the gradient 0.93 to 1, both in one 0.98 (353 us; 0.93, 376 us, with an
+// bound by bandwidth where there is enough to read: of the copy bandwidth stats 0.91 to 0.98 (4096 rows of 151936 bf16 with the
+// entropy 181 us, a tenth of them without a token), the gradient 0.93 to 1, both in one 0.98 (351 us; 0.93, 375 us, with an
 // entropy bonus).  Where a CTA has little to read its latencies bound it: token, first vectors, joins, the row's end.
 #include <algorithm>
 #include <cmath>
@@ -127,7 +127,7 @@ __device__ __forceinline__ EntSum lanes_join(EntSum a, const TokArgs& args) {
 // Vectors are added by the reference that is there, whatever their maximum: where that makes a sum of a.most or more
 // (the first vectors, a maximum above the reference) they are added again by a reference above it.  The reference's whole exponent r
 // makes the exponent's one rounding that of the fma; -inf stands for none.  (With the running
-// maximum of every batch of vectors in the way: 191 us where this takes 177, 4096 rows of 151936 with the entropy.)
+// maximum of every batch of vectors in the way: 191 us where this takes 181, 4096 rows of 151936 with the entropy.)
 //
 // A row's log-probability may be off by 1e-7 at random, but not to one side: sums of a thousand log ratios follow.  So
 // the vectors' sum joins the rest in a pair of floats (added one by one, small terms are lost more often than gained:
@@ -866,7 +866,7 @@ __device__ __forceinline__ RowSaved quick_end(const TokArgs& a, const EntSum& es
 
 // A policy row's loss and gradient without reading it twice: a cluster of C CTAs keeps the row in shared memory, a span
 // each, between the sum and the gradient.  A span comes by one bulk copy (copies of 16 bytes by the threads that read them:
-// 381 us where this takes 357, 4096 rows of 151936; the row read twice: 532); a thread reads the same vectors for both, so
+// 8% slower, 4096 rows of 151936; the row read twice: half as long again); a thread reads the same vectors for both, so
 // that only the joins of the sums wait for others.  An SM moves as many bytes as it holds over how long it holds them: some
 // 200 KB for 9.5 us at the copy bandwidth, so what stands between copy and gradient is kept short.
 constexpr int kFusedSpan = 14000;                            // vectors of a span at most: 224,000 bytes
