@@ -349,7 +349,9 @@ __global__ void __launch_bounds__(kClipThreads, kClipCtas) scale_kernel(const __
     const float norm = n.value();
     const bool finite = norm < INFINITY;
     // by the norm before its rounding (by the rounded one up to 1.7 u off for 1)
-    const float c = finite && norm > a.max_norm ? times_2(over(a.max_norm, n.m), -n.e) : 1.f;
+    // (a small max_norm by 2^64: what its quotient leaves would lie below fp32's numbers)
+    const bool small = a.max_norm < 0x1p-64f;
+    const float c = finite && norm > a.max_norm ? times_2(over(small ? a.max_norm * 0x1p64f : a.max_norm, n.m), small ? -n.e - 64 : -n.e) : 1.f;
     if (a.write_norm && blockIdx.x == 0 && threadIdx.x == 0) {
         *a.norm = norm;
         *a.status = finite ? 0 : DSPARK_ROW_NONFINITE;

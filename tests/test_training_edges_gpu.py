@@ -260,6 +260,19 @@ def test_clip_factors_below_the_smallest_number(bd, size, max_norm, dtype, out):
     assert (np.abs(got - want[0]) <= tol).all(), (np.abs(got - want[0]) - tol).max()
 
 
+@pytest.mark.parametrize("size,max_norm", [(2.0 ** -100, 2.0 ** -101), (2.0 ** -60, 3e-38), (2.0 ** -130, 1e-40), (2.0 ** -128, 3e-41), (2.0 ** -140, 1e-43)])
+def test_clip_small_gradients_to_smaller_norms(bd, size, max_norm):  # noqa: F811
+    """The factor to its last bit where max_norm, its quotient's remainder or the gradients lie near or below the smallest normal
+    number: u of what comes out, and half a step of the smallest numbers (once more where the norm's is one)."""
+    m = float(np.float32(max_norm))
+    for n in range(2, 300, 7):
+        g = torch.full((n,), size, device="cuda")
+        norm, status = clip_call(bd, [g], m)
+        want = min(m / n ** 0.5, size)
+        assert status == 0 and abs(norm - n ** 0.5 * size) <= U * n ** 0.5 * size * (1 + 2.0 ** -12) + 2.0 ** -150
+        assert float((g.double() - want).abs().max()) <= 2 * U * want + 2.0 ** -150, n
+
+
 @pytest.mark.parametrize("rows,V,dtype", [(500, 16411, "bf16"), (600, 5003, "fp32"), (913, 16411, "bf16"), (1000, 8209, "fp32"),
                                           (1216, 16400, "bf16"), (1217, 16411, "bf16"), (1300, 8203, "fp32"), (300, 8209, "fp32")])
 def test_loops_of_every_launch_shape(bd, rows, V, dtype):  # noqa: F811
